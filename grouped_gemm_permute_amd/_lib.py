@@ -28,7 +28,8 @@ EXPORTS = (
     "moe_ffn_backward", "moe_ffn_backward_timed", "moe_router_topk", "moe_ffn_forward_routed",
     "moe_ffn_forward_routed_timed", "moe_device_clock_sample", "moe_ffn_forward_noalloc",
     "moe_stream_read", "moe_ffn_forward_save_gu", "moe_ffn_backward_cached",
-    "moe_ffn_backward_cached_timed",
+    "moe_ffn_backward_cached_timed", "moe_layer_norm_forward",
+    "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward",
 )
 
 # Bytes of the per-device workspace array behind moe_ffn_forward_noalloc.
@@ -120,6 +121,12 @@ def lib():
         L.moe_device_clock_sample.argtypes = [P, ci, P]
         L.moe_stream_read.restype = ci
         L.moe_stream_read.argtypes = [P, ctypes.c_size_t, P, ci, P]
+        L.moe_layer_norm_forward.restype = ci
+        L.moe_layer_norm_forward.argtypes = [P] * 8 + [i64, ci, ci, ctypes.c_float, ci, P]
+        L.moe_layer_norm_backward_workspace_size.restype = sz
+        L.moe_layer_norm_backward_workspace_size.argtypes = [i64, ci, ci]
+        L.moe_layer_norm_backward.restype = ci
+        L.moe_layer_norm_backward.argtypes = [P] * 9 + [i64, ci, ci, P, sz, P]
         L.moe_ffn_get_device_error.restype = ci
         L.moe_ffn_get_device_error.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
         _lib = L
@@ -493,3 +500,109 @@ def forward_routed(x, gate_w, W1, W3, W2, shared=None, k=2, y=None, variant="unf
     else:
         _check(lib().moe_ffn_forward_routed_timed(*args, events), "moe_ffn_forward_routed_timed")
     return y, idx, w
+
+
+def _on_current_device(ref):
+    """Kernels launch on the current device: a tensor of another one is refused."""
+    if ref.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {ref.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty from the pool of the stream the kernels run on, so that
+    the allocator does not hand the memory on, or over, while another
+    stream's work is still using it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _check_rows(name, x):
+    _dtype_enum(x.dtype)
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [T,D]")
+    _expect(name, x, x.shape, x.dtype)
+    return x.shape
+
+
+def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False, out=None, stats=True,
+               stream=None) -> dict:
+    """moe_layer_norm_forward: y = (h - mean) rstd weight + bias over the rows
+    of h = x (+ residual), x and residual [T,D], weight and bias [D] of x's
+    dtype (None: 1, 0); with rms the mean is not taken off.  Returns y, h (x
+    itself without a residual, else the rounded sum), and the fp32 [T] mean
+    (None with rms) and rstd that layer_norm_backward takes (both None
+    with stats=False).  ``out`` may supply y and h."""
+    T, D = _check_rows("x", x)
+    for name, t, shape in (("weight", weight, (D,)), ("bias", bias, (D,)), ("residual", residual, (T, D))):
+        if t is not None:
+            _expect(name, t, shape, x.dtype)
+    o = dict(out or {})
+    for name in o:
+        if name not in ("y", "h") or (name == "h" and residual is None):
+            raise ValueError(f"out has no place for {name}")
+        _expect(name, o[name], (T, D), x.dtype)
+    _same_device(x, dict(weight=weight, bias=bias, residual=residual, **o))
+    _on_current_device(x)
+    if "y" not in o:
+        o["y"] = _empty((T, D), x.dtype, x.device, stream)
+    if residual is not None and "h" not in o:
+        o["h"] = _empty((T, D), x.dtype, x.device, stream)
+    o["mean"] = _empty((T,), torch.float32, x.device, stream) if stats and not rms else None
+    o["rstd"] = _empty((T,), torch.float32, x.device, stream) if stats else None
+    _check(lib().moe_layer_norm_forward(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(o["y"]),
+                                        _ptr(o.get("h")), _ptr(o["mean"]), _ptr(o["rstd"]), T, D,
+                                        int(rms), eps, _dtype_enum(x.dtype), _stream(stream)),
+           "moe_layer_norm_forward")
+    if residual is None:
+        o["h"] = x
+    return o
+
+
+def layer_norm_backward(h, dy, rstd, mean=None, weight=None, dh=None, bias_grad=False, out=None,
+                        workspace=None, stream=None) -> dict:
+    """moe_layer_norm_backward: gradients of layer_norm for the incoming dy
+    [T,D], from its h, rstd and mean (None: rms).  Returns dx (x's and the
+    residual's gradient, dh added when given), dweight (fp32 [D]; None
+    without weight) and dbias (fp32 [D]; None without bias_grad).  ``out`` may
+    supply any of these."""
+    T, D = _check_rows("h", h)
+    _expect("dy", dy, (T, D), h.dtype)
+    _expect("rstd", rstd, (T,), torch.float32)
+    if mean is not None:
+        _expect("mean", mean, (T,), torch.float32)
+    if weight is not None:
+        _expect("weight", weight, (D,), h.dtype)
+    if dh is not None:
+        _expect("dh", dh, (T, D), h.dtype)
+    shapes = dict(dx=((T, D), h.dtype))
+    if weight is not None:
+        shapes["dweight"] = ((D,), torch.float32)
+    if bias_grad:
+        shapes["dbias"] = ((D,), torch.float32)
+    o = dict(out or {})
+    for name, t in o.items():
+        if name not in shapes:
+            raise ValueError(f"out has no place for {name}")
+        _expect(name, t, *shapes[name])
+    _same_device(h, dict(dy=dy, rstd=rstd, mean=mean, weight=weight, dh=dh, **o))
+    _on_current_device(h)
+    for name, (shape, dtype) in shapes.items():
+        if name not in o:
+            o[name] = _empty(shape, dtype, h.device, stream)
+    n = 0
+    if weight is not None or bias_grad:
+        n = lib().moe_layer_norm_backward_workspace_size(T, D, _dtype_enum(h.dtype))
+        if workspace is None:
+            workspace = _empty((max(n, 256),), torch.uint8, h.device, stream)
+        _check_workspace(h, workspace, n)
+    o.setdefault("dweight", None)
+    o.setdefault("dbias", None)
+    _check(lib().moe_layer_norm_backward(_ptr(h), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dy), _ptr(dh),
+                                         _ptr(o["dx"]), _ptr(o["dweight"]), _ptr(o["dbias"]), T, D,
+                                         _dtype_enum(h.dtype), _ptr(workspace) if n else None, n,
+                                         _stream(stream)),
+           "moe_layer_norm_backward")
+    return o

@@ -504,6 +504,77 @@ moe_status moe_ffn_backward_cached_timed(const void *x, const int32_t *topk_idx,
                                          void *workspace, size_t ws_bytes, hipStream_t stream,
                                          hipEvent_t events[9]);
 
+/* ------------------------------------------------------------------------
+ * Layer norm in front of the layer (and, in a pre-norm block, the residual
+ * sum in front of the norm).  Per row:
+ *
+ *   h = x (+ residual),  mean = sum(h) / D,  var = sum((h - mean)^2) / D
+ *   rstd = 1 / sqrt(var + eps),  y = (h - mean) * rstd * weight + bias
+ *
+ * With rms != 0 the mean is not taken off (mean = 0 above): the root mean
+ * square norm.
+ * ------------------------------------------------------------------------ */
+
+/*
+ *   x         [T, D]  dtype
+ *   residual  [T, D]  dtype, or NULL; added to x, the sum rounded once to
+ *             dtype and written to h; the norm is that of the rounded sum
+ *   weight, bias [D]  dtype; NULL: 1, 0
+ *   y         [T, D]  dtype; out
+ *   h         [T, D]  dtype; out, given exactly when residual is
+ *   mean, rstd [T]    fp32; out, for the backward; NULL: not written.  mean
+ *             must be NULL with rms
+ *
+ * Arithmetic is fp32: the row is held in registers, the variance is the sum
+ * of squared deviations from its mean, y is rounded once.  A row that holds
+ * an infinity or NaN gives NaN in its own outputs alone.  h may be x or
+ * residual and y may be x (the same buffer, not a shifted one).
+ *
+ * D may be any size up to 16384; rows are dense.  x, residual, weight,
+ * bias, y, h are 16-byte aligned, mean and rstd 4-byte aligned.
+ *
+ * Returns MOE_OK; MOE_ERR_INVALID_ARG (null or misaligned pointer, T < 0,
+ * T >= 2^31, D <= 0, eps negative or not finite, unknown dtype, only one of
+ * residual and h, mean with rms); MOE_ERR_UNSUPPORTED (D > 16384);
+ * MOE_ERR_HIP.  T == 0 launches nothing.
+ */
+moe_status moe_layer_norm_forward(const void *x, const void *residual, const void *weight,
+                                  const void *bias, void *y, void *h, float *mean, float *rstd,
+                                  int64_t T, int D, int rms, float eps, moe_dtype dtype,
+                                  hipStream_t stream);
+
+/* Workspace bytes moe_layer_norm_backward needs for dweight or dbias (at
+ * most 512 rows of 2 D floats); 0 if the sizes are invalid or unsupported. */
+size_t moe_layer_norm_backward_workspace_size(int64_t T, int D, moe_dtype dtype);
+
+/*
+ * Backward of moe_layer_norm_forward: with z = (h - mean) * rstd and
+ * g = dy * weight,
+ *
+ *   dx = rstd * (g - sum(g) / D - z * sum(g * z) / D) (+ dh)
+ *   dweight = sum over rows of dy * z,  dbias = sum over rows of dy
+ *
+ *   h         [T, D]  dtype; the row the norm was taken of (x without residual)
+ *   mean, rstd [T]    fp32; the forward's.  mean NULL: rms (no sum(g) term)
+ *   weight    [D]     dtype; NULL: 1
+ *   dy        [T, D]  dtype
+ *   dh        [T, D]  dtype, or NULL: the gradient that reaches h by itself
+ *             (the residual stream's), added to dx
+ *   dx        [T, D]  dtype; out: the gradient of x, and of residual alike
+ *   dweight, dbias [D] fp32; out, fully overwritten (zeros with T == 0);
+ *             NULL: not wanted
+ *   workspace >= moe_layer_norm_backward_workspace_size() bytes, 256-byte
+ *             aligned; read only when dweight or dbias is wanted
+ *
+ * fp32 arithmetic; dx is rounded once; the sums over rows have a fixed
+ * order, so repeated calls give equal bits.  dx may be dy, dh or h.
+ * Alignment, errors and D as in the forward, and MOE_ERR_WORKSPACE.
+ */
+moe_status moe_layer_norm_backward(const void *h, const float *mean, const float *rstd,
+                                   const void *weight, const void *dy, const void *dh, void *dx,
+                                   float *dweight, float *dbias, int64_t T, int D, moe_dtype dtype,
+                                   void *workspace, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
