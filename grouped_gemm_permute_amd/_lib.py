@@ -30,6 +30,7 @@ EXPORTS = (
     "moe_stream_read", "moe_ffn_forward_save_gu", "moe_ffn_backward_cached",
     "moe_ffn_backward_cached_timed", "moe_layer_norm_forward",
     "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward",
+    "moe_newton_schulz_workspace_size", "moe_newton_schulz", "moe_muon_step",
 )
 
 # Bytes of the per-device workspace array behind moe_ffn_forward_noalloc.
@@ -127,6 +128,13 @@ def lib():
         L.moe_layer_norm_backward_workspace_size.argtypes = [i64, ci, ci]
         L.moe_layer_norm_backward.restype = ci
         L.moe_layer_norm_backward.argtypes = [P] * 9 + [i64, ci, ci, P, sz, P]
+        cf, cd = ctypes.c_float, ctypes.c_double
+        L.moe_newton_schulz_workspace_size.restype = sz
+        L.moe_newton_schulz_workspace_size.argtypes = [ci, ci, ci]
+        L.moe_newton_schulz.restype = ci
+        L.moe_newton_schulz.argtypes = [P, P, ci, ci, ci, ci, cd, cd, cd, cd, ci, P, sz, P]
+        L.moe_muon_step.restype = ci
+        L.moe_muon_step.argtypes = [P, P, P, P, ci, ci, ci, cf, cf, cf, cf, ci, ci, cd, cd, cd, cd, ci, P, sz, P]
         L.moe_ffn_get_device_error.restype = ci
         L.moe_ffn_get_device_error.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
         _lib = L
@@ -606,3 +614,76 @@ def layer_norm_backward(h, dy, rstd, mean=None, weight=None, dh=None, bias_grad=
                                          _stream(stream)),
            "moe_layer_norm_backward")
     return o
+
+
+# Coefficients of the Newton-Schulz step that newton_schulz and muon_step take by default.
+NS_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def _check_matrices(name, x, dtypes):
+    """(B, M, N) of a [M,N] or [B,M,N] tensor."""
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {x.dtype}")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [M,N] or [B,M,N]")
+    _expect(name, x, x.shape, x.dtype)
+    return (1, *x.shape) if x.dim() == 2 else tuple(x.shape)
+
+
+def newton_schulz_workspace_size(B, M, N) -> int:
+    return lib().moe_newton_schulz_workspace_size(B, M, N)
+
+
+def _ns_workspace(x, B, M, N, workspace, stream):
+    n = newton_schulz_workspace_size(B, M, N)
+    if workspace is None and n:
+        workspace = _empty((n,), torch.uint8, x.device, stream)
+    if workspace is not None:
+        _check_workspace(x, workspace, n)
+    return workspace, n
+
+
+def newton_schulz(G, steps=5, coeffs=NS_COEFFS, eps=1e-7, out=None, workspace=None, stream=None):
+    """moe_newton_schulz: the orthogonalised G ([M,N] or [B,M,N], bf16 or
+    fp32): X = G / (|G| + eps), then ``steps`` times
+    X <- a X + (b A + c A A) X with A = X X^T on the shorter side and
+    (a, b, c) = ``coeffs``.  ``out`` may be G."""
+    B, M, N = _check_matrices("G", G, (torch.float32, torch.bfloat16))
+    if out is not None:
+        _expect("out", out, G.shape, G.dtype)
+    _same_device(G, dict(out=out))
+    _on_current_device(G)
+    if out is None:
+        out = _empty(G.shape, G.dtype, G.device, stream)
+    workspace, n = _ns_workspace(G, B, M, N, workspace, stream)
+    a, b, c = coeffs
+    _check(lib().moe_newton_schulz(_ptr(G), _ptr(out), B, M, N, steps, a, b, c, eps, _dtype_enum(G.dtype),
+                                   _ptr(workspace), n, _stream(stream)), "moe_newton_schulz")
+    return out
+
+
+def muon_step(W, dW, momentum, lr, beta=0.95, weight_decay=0.0, scale=None, nesterov=True, steps=5,
+              coeffs=NS_COEFFS, eps=1e-7, W_bf16=None, workspace=None, stream=None):
+    """moe_muon_step, in place on W ([M,N] or [B,M,N], bf16 or fp32) and
+    momentum (fp32): momentum <- beta momentum + dW, U = dW + beta momentum
+    (``nesterov``) or momentum, W <- (1 - lr weight_decay) W - lr scale X with
+    X = newton_schulz(U).  ``scale`` defaults to sqrt(max(1, N / M)) (weights
+    are [in, out] here).  ``W_bf16`` (beside an fp32 W): receives the new W in
+    bf16, for the layer's calls.  Returns W."""
+    B, M, N = _check_matrices("W", W, (torch.float32, torch.bfloat16))
+    _expect("dW", dW, W.shape, torch.float32)
+    _expect("momentum", momentum, W.shape, torch.float32)
+    if W_bf16 is not None:
+        if W.dtype != torch.float32:
+            raise ValueError("W_bf16 goes with an fp32 W")
+        _expect("W_bf16", W_bf16, W.shape, torch.bfloat16)
+    _same_device(W, dict(dW=dW, momentum=momentum, W_bf16=W_bf16))
+    _on_current_device(W)
+    if scale is None:
+        scale = max(1.0, N / M) ** 0.5
+    workspace, n = _ns_workspace(W, B, M, N, workspace, stream)
+    a, b, c = coeffs
+    _check(lib().moe_muon_step(_ptr(W), _ptr(W_bf16), _ptr(dW), _ptr(momentum), B, M, N, lr, beta,
+                               weight_decay, scale, int(nesterov), steps, a, b, c, eps,
+                               _dtype_enum(W.dtype), _ptr(workspace), n, _stream(stream)), "moe_muon_step")
+    return W

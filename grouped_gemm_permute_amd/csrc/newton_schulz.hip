@@ -1,0 +1,865 @@
+// newton_schulz.hip -- orthogonalisation of a batch of matrices by
+// Newton-Schulz products, and the Muon step around it; the C entry points
+// moe_newton_schulz and moe_muon_step.
+//
+//   X_0 = U / (|U| + eps),  |U| the Frobenius norm
+//   A = X X^T on the shorter side m,  X <- a X + (b A + c A A) X,  `steps` times
+//   newton_schulz: U = G, out = X
+//   muon:          momentum <- beta momentum + dW,  U = dW + beta momentum
+//                  (or momentum),  W <- (1 - lr decay) W - lr scale X
+//
+// Every product is a matrix product on the matrix cores with fp32 accuracy.
+// An operand is held as two fp16 planes, hi = f16(v s) and lo = f16(v s - hi)
+// with a power of two s, 22 bits of v together, and a product takes the
+// three terms hi hi + hi lo + lo hi, summed in fp32: 3 of the fast fp16
+// instructions (16x the fp32 ones' rate) keep the iteration within 1.1x of
+// fp32's own error, where one fp16 or bf16 plane leaves 2e-3 to 2e-2, since
+// small singular values grow by a factor a in each step and their rounding
+// with them.  s comes from a bound on the singular values: the host follows
+// the largest value of |x (a + b x^2 + c x^4)| from [0, 1] through the steps, an
+// entry is never larger than the largest singular value, and s puts the bound
+// at 2^15 at most (fp16 ends at 65504).
+//
+// Layout: a plane matrix has rows of K values in groups of 32, a group's 64
+// bytes of hi followed by its 64 bytes of lo, so one 128-byte line feeds both
+// planes of a K step.  Sizes are padded with zeros to multiples of 64 (they
+// stay zero through the iteration), so only the first and the last kernel
+// know the matrix's own sizes.
+//
+// Each product is C = P Q^T over row-major operands: A = X X^T takes X's rows
+// twice, A A = A A^T takes A's (A is symmetric), and B X takes B's rows and
+// those of X^T; so X is kept in both orders, and an epilogue writes its tile in
+// both.  For the symmetric results only tiles on and below the diagonal are
+// computed, and their transposed tile is written beside them.
+#include "mfma_common.h"
+#include "moe_ffn.h"
+
+#include <math.h>
+
+namespace moe {
+namespace {
+
+using namespace mfma;
+
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
+
+// ---------------------------------------------------------------- elements
+
+struct __attribute__((packed, aligned(4))) Raw4f {
+    float v[4];
+};
+struct __attribute__((packed, aligned(2))) Raw8h {
+    uint32_t w[4];
+};
+
+// Eight consecutive fp32 or bf16 elements, `left` of which exist.
+__device__ __forceinline__ void load8(const void* base, int64_t at, int left, bool bf16, float* v) {
+    if (bf16) {
+        const uint16_t* p = (const uint16_t*)base + at;
+        if (left >= 8) {
+            const Raw8h r = *(const Raw8h*)p;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(r.w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < left ? __uint_as_float((uint32_t)p[i] << 16) : 0.f;
+        }
+    } else {
+        const float* p = (const float*)base + at;
+        if (left >= 8) {
+            const Raw4f r0 = *(const Raw4f*)p, r1 = *(const Raw4f*)(p + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = r0.v[i], v[4 + i] = r1.v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.f;
+        }
+    }
+}
+__device__ __forceinline__ void store8(void* base, int64_t at, int left, bool bf16, const float* v) {
+    if (bf16) {
+        uint16_t* p = (uint16_t*)base + at;
+        if (left >= 8) {
+            Raw8h r;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+            *(Raw8h*)p = r;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left) p[i] = (uint16_t)pack_bf16(v[i], 0.f);
+        }
+    } else {
+        float* p = (float*)base + at;
+        if (left >= 8) {
+            Raw4f r0, r1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r0.v[i] = v[i], r1.v[i] = v[4 + i];
+            *(Raw4f*)p = r0;
+            *(Raw4f*)(p + 4) = r1;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left) p[i] = v[i];
+        }
+    }
+}
+
+// Where U comes from and the result goes.
+struct Source {
+    const void* g;      // G (newton_schulz, fp32 or bf16) or dW (muon, fp32)
+    float* mom;         // muon: momentum; null: newton_schulz
+    float beta;
+    int nesterov;
+    int g_bf16;
+};
+struct Target {
+    void* out;          // newton_schulz: X; muon: W, read and written
+    uint16_t* copy;     // muon: bf16 copy of W, or null
+    float keep, rate;   // muon: W <- keep W - rate X
+    int muon;
+    int out_bf16;
+};
+
+// U of the muon step from dW and the momentum already moved on.
+__device__ __forceinline__ void source8(const Source& s, int64_t at, int left, float* u) {
+    load8(s.g, at, left, s.g_bf16, u);
+    if (s.mom) {
+        float m[8];
+        load8(s.mom, at, left, false, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = s.nesterov ? fmaf(s.beta, m[i], u[i]) : m[i];
+    }
+}
+// The same for the first pass, which moves the momentum on.
+__device__ __forceinline__ void source8_first(const Source& s, int64_t at, int left, float* u) {
+    load8(s.g, at, left, s.g_bf16, u);
+    if (s.mom) {
+        float m[8];
+        load8(s.mom, at, left, false, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = fmaf(s.beta, m[i], u[i]);
+        store8(s.mom, at, left, false, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = s.nesterov ? fmaf(s.beta, m[i], u[i]) : m[i];
+    }
+}
+__device__ __forceinline__ void target8(const Target& t, int64_t at, int left, float* v) {
+    if (t.muon) {
+        float w[8];
+        load8(t.out, at, left, t.out_bf16, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(-t.rate, v[i], t.keep * w[i]);
+        if (t.copy) store8(t.copy, at, left, true, v);
+    }
+    store8(t.out, at, left, t.out_bf16, v);
+}
+
+// ------------------------------------------------------- norm and planes
+
+// Sum of squares of one matrix's U, by norm_blocks(size) workgroups, in fp64
+// (fp32 squares would overflow or vanish for gradients of 1e20 or 1e-20).
+constexpr int kNormChunk = 256 * 8 * 4;      // elements a workgroup takes at least
+constexpr int kNormMaxBlocks = 256;
+int norm_blocks(int64_t size) {
+    const int64_t n = (size + kNormChunk - 1) / kNormChunk;
+    return (int)(n < kNormMaxBlocks ? n : kNormMaxBlocks);
+}
+
+__device__ __forceinline__ double block_sum(double v, double* red, int waves) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.;
+    for (int i = 0; i < waves; ++i) v += red[i];
+    return v;
+}
+
+__global__ __launch_bounds__(256) void ns_norm_kernel(const Source s, int64_t size, double* part) {
+    __shared__ double red[4];
+    const int64_t base = (int64_t)blockIdx.y * size;
+    double sum = 0.;
+    for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; at < size;
+         at += (int64_t)gridDim.x * 256 * 8) {
+        float u[8];
+        source8_first(s, base + at, (int)min((int64_t)8, size - at), u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fma((double)u[i], (double)u[i], sum);
+    }
+    sum = block_sum(sum, red, 4);
+    if (threadIdx.x == 0) part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = sum;
+}
+
+// hi and lo of eight scaled values.
+__device__ __forceinline__ void split8(const float* v, u32x4_t& hi, u32x4_t& lo) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f16x2_t h = {(_Float16)v[2 * i], (_Float16)v[2 * i + 1]};
+        const f16x2_t l = {(_Float16)(v[2 * i] - (float)h[0]), (_Float16)(v[2 * i + 1] - (float)h[1])};
+        hi[i] = __builtin_bit_cast(uint32_t, h);
+        lo[i] = __builtin_bit_cast(uint32_t, l);
+    }
+}
+// Byte offset of column c (a multiple of 8) of a plane row; lo is 64 bytes on.
+__device__ __forceinline__ int64_t plane_at(int64_t row, int64_t ld, int c) {
+    return row * ld * 4 + (c >> 5) * 128 + (c & 31) * 2;
+}
+__device__ __forceinline__ void store_planes(char* base, int64_t at, const float* v) {
+    u32x4_t hi, lo;
+    split8(v, hi, lo);
+    *(u32x4_t*)(base + at) = hi;
+    *(u32x4_t*)(base + at + 64) = lo;
+}
+__device__ __forceinline__ void add_planes(const char* base, int64_t at, float f, float* v) {
+    const u32x4_t hi = *(const u32x4_t*)(base + at), lo = *(const u32x4_t*)(base + at + 64);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t hw = hi[i], lw = lo[i];
+        const f16x2_t h = __builtin_bit_cast(f16x2_t, hw), l = __builtin_bit_cast(f16x2_t, lw);
+        v[2 * i] = fmaf(f, (float)h[0] + (float)l[0], v[2 * i]);
+        v[2 * i + 1] = fmaf(f, (float)h[1] + (float)l[1], v[2 * i + 1]);
+    }
+}
+
+struct SplitArgs {
+    Source s;
+    const double* part;     // [B][nb]
+    int nb;
+    int M, N;               // U's own sizes
+    int Mp, Np;             // padded
+    double eps;
+    float scale;
+    char *rows, *cols;      // planes [B][Mp][Np] (U's rows) and [B][Np][Mp] (its columns)
+};
+constexpr int ST = 64;
+__global__ __launch_bounds__(256) void ns_split_kernel(const SplitArgs a) {
+    __shared__ float tile[ST][ST + 1];
+    __shared__ double red[4];
+    const int b = blockIdx.z, i0 = blockIdx.y * ST, j0 = blockIdx.x * ST, tid = threadIdx.x;
+    const double sq = block_sum(tid < a.nb ? a.part[(int64_t)b * a.nb + tid] : 0., red, 4);
+    const double inv = (double)a.scale / (sqrt(sq) + a.eps);
+    const int64_t base = (int64_t)b * a.M * a.N;
+    char* rows = a.rows + (int64_t)b * a.Mp * a.Np * 4;
+    char* cols = a.cols + (int64_t)b * a.Mp * a.Np * 4;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int r = (tid >> 3) + 32 * k, c = (tid & 7) * 8;
+        float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const int left = a.N - (j0 + c);
+        if (i0 + r < a.M && left > 0) {
+            source8(a.s, base + (int64_t)(i0 + r) * a.N + j0 + c, left, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = e < left ? (float)((double)u[e] * inv) : 0.f;
+        }
+        store_planes(rows, plane_at(i0 + r, a.Np, j0 + c), u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) tile[r][c + e] = u[e];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int c = (tid >> 3) + 32 * k, r = (tid & 7) * 8;
+        float u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = tile[r + e][c];
+        store_planes(cols, plane_at(j0 + c, a.Mp, i0 + r), u);
+    }
+}
+
+// ---------------------------------------------------------------- products
+
+enum : int { GRAM = 0, SQUARE = 1, APPLY = 2, FINAL = 3 };
+
+constexpr int BT = 128;                       // tile rows and columns
+constexpr int KB = 32;                        // K step
+constexpr int ROW = 128;                      // bytes of a staged row: 32 hi, 32 lo
+constexpr int OPB = BT * ROW;                 // one operand of a stage
+
+struct MulArgs {
+    const char *p, *q;          // planes [B][pr][K], [B][qr][K]
+    int64_t p_stride, q_stride; // bytes per matrix
+    int pr, qr, K;              // padded rows of each side, reduction length
+    int ti, tj;                 // tiles of each side
+    float f;                    // factor of the product
+    const char* add;            // SQUARE: A; APPLY, FINAL: X (FINAL, swapped: X^T)
+    int64_t add_stride;
+    float fa;                   // factor of the addend
+    float so;                   // scale of the stored planes
+    char *c, *ct;               // planes out, as computed and transposed
+    int64_t c_stride;
+    int swap;                   // FINAL: the target is the transposed tile
+    int M, N;                   // FINAL: the target's sizes
+    Target t;
+};
+
+// Index of element (r, c) of the fp32 tile in LDS.  Writes of a wavefront
+// (32 columns of two rows), reads of 8 columns by 16 lanes of four rows and
+// reads of 8 rows by 16 lanes of four columns all spread over the banks.
+__device__ __forceinline__ int tile_at(int r, int c) {
+    return r * BT + (c ^ ((((r >> 3) ^ (r & 1)) & 7) << 2) ^ ((c >> 5) & 3));
+}
+
+template <int MODE>
+__global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
+    constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
+    // separate objects, so that a read of one buffer does not wait for the
+    // transfers into the other; the epilogue holds rows 0..63 of the fp32 tile
+    // in the first, 64..127 in the second
+    __shared__ __attribute__((aligned(1024))) char st0[2 * OPB];
+    __shared__ __attribute__((aligned(1024))) char st1[2 * OPB];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    const int per = SYM ? a.ti * (a.ti + 1) / 2 : a.ti * a.tj;
+    const int id = xcd_remap(blockIdx.x, gridDim.x);
+    const int b = id / per;
+    int t = id - b * per, ti, tj;
+    if constexpr (SYM) {
+        ti = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
+        while (ti * (ti + 1) / 2 > t) --ti;
+        while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
+        tj = t - ti * (ti + 1) / 2;
+    } else {
+        ti = t % a.ti;
+        tj = t / a.ti;
+    }
+    const int i0 = ti * BT, j0 = tj * BT;
+
+    // stage sources: transfer j of wavefront w fills rows 32 w + 8 j .. +7 of an
+    // operand; a lane brings the chunk that its place holds under the swizzle.
+    // Rows past the padded end (half tiles) read the last row and are not stored.
+    const char *ps[4], *qs[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = 32 * wave + 8 * j + (lane >> 3);
+        const int ch = ((lane & 7) ^ swz8(r)) * 16;
+        ps[j] = a.p + b * a.p_stride + (int64_t)min(i0 + r, a.pr - 1) * a.K * 4 + ch;
+        qs[j] = a.q + b * a.q_stride + (int64_t)min(j0 + r, a.qr - 1) * a.K * 4 + ch;
+    }
+    auto issue = [&](int kt, char* st) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            load_lds16(ps[j] + (int64_t)kt * ROW, st + (32 * wave + 8 * j) * ROW);
+            load_lds16(qs[j] + (int64_t)kt * ROW, st + OPB + (32 * wave + 8 * j) * ROW);
+        }
+    };
+
+    const int wi = wave >> 1, wj = wave & 1, rl = lane & 31, kh = lane >> 5;
+    f32x16_t acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
+
+    auto compute = [&](const char* st) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            f16x8_t ph[2], pl[2], qh[2], ql[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int pr = 64 * wi + 32 * i + rl, qr = 64 * wj + 32 * i + rl;
+                const char* pb = st + pr * ROW;
+                const char* qb = st + OPB + qr * ROW;
+                const int ch = 2 * ks + kh;
+                ph[i] = __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(pb + ((ch ^ swz8(pr)) << 4)));
+                pl[i] = __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(pb + (((ch + 4) ^ swz8(pr)) << 4)));
+                qh[i] = __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(qb + ((ch ^ swz8(qr)) << 4)));
+                ql[i] = __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(qb + (((ch + 4) ^ swz8(qr)) << 4)));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], qh[j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], ql[j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[i], qh[j], acc[i][j], 0, 0, 0);
+                }
+        }
+    };
+    // Step kt: wait for stage kt, then (all wavefronts being past their reads
+    // of the other buffer) send stage kt + 1 there and compute on stage kt.
+    const int KT = a.K / KB;     // even: K is a multiple of 64
+    auto step = [&](int kt, char* cur, char* nxt) {
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (kt + 1 < KT) issue(kt + 1, nxt);
+        compute(cur);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    issue(0, st0);
+    for (int kt = 0; kt < KT; kt += 2) {
+        step(kt, st0, st1);
+        step(kt + 1, st1, st0);
+    }
+    __syncthreads();
+
+    // ---- epilogue: the fp32 tile through LDS, then 8 values a thread along
+    // the rows, and along the columns for the transposed result
+    auto at = [&](int r, int c) -> float& {
+        return ((float*)(r < 64 ? st0 : st1))[tile_at(r & 63, c)];
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int g = 0; g < 16; ++g) {
+                const int r = 64 * wi + 32 * i + 8 * (g >> 2) + (g & 3) + 4 * kh;
+                at(r, 64 * wj + 32 * j + rl) = acc[i][j][g] * a.f;
+            }
+    __syncthreads();
+    const int seg = tid & 15;
+    if constexpr (MODE == FINAL) {
+        const int rows = a.swap ? j0 : i0, cols = a.swap ? i0 : j0;
+        const int ld = a.swap ? a.pr : a.qr;
+        const char* add = a.add + b * a.add_stride;
+        for (int k = 0; k < 8; ++k) {
+            const int r = (tid >> 4) + 16 * k, c = 8 * seg;
+            const int left = a.N - (cols + c);
+            if (rows + r >= a.M || left <= 0) continue;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = a.swap ? at(c + e, r) : at(r, c + e);
+            add_planes(add, plane_at(rows + r, ld, cols + c), a.fa, v);
+            target8(a.t, ((int64_t)b * a.M + rows + r) * a.N + cols + c, left, v);
+        }
+    } else {
+        char* out = a.c + b * a.c_stride;
+        char* outt = a.ct + b * a.c_stride;
+        const bool both = !SYM || ti != tj;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = (tid >> 4) + 16 * k, c = 8 * seg;
+            if (i0 + r >= a.pr || j0 + c >= a.qr) continue;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = at(r, c + e);
+            const int64_t to = plane_at(i0 + r, a.qr, j0 + c);
+            if constexpr (MODE != GRAM) add_planes(a.add + b * a.add_stride, to, a.fa, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= a.so;
+            store_planes(out, to, v);
+            if (both) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) at(r, c + e) = v[e];
+            }
+        }
+        if (!both) return;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int c = (tid >> 4) + 16 * k, r = 8 * seg;
+            if (i0 + r >= a.pr || j0 + c >= a.qr) continue;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = at(r + e, c);
+            store_planes(outt, plane_at(j0 + c, a.pr, i0 + r), v);
+        }
+    }
+}
+
+// ------------------------------------------------- short sides of up to 32
+
+// One workgroup takes a whole matrix when its short side m is at most 32: A is
+// summed in fp64 straight from U, and since every step multiplies X by a
+// polynomial of A, and those commute, the steps run on the m x m side alone
+// (A <- P A P, Q <- Q P with P = a I + b A + c A A, in fp64, whose rounding the
+// growth of small singular values leaves far below fp32's), and U is read a
+// second time for X = Q U / (|U| + eps).  One launch where the general path
+// takes two and three for each step.
+constexpr int SM = 32, SNT = 512, SL = 128, SPS = SM + 4;
+struct SmallArgs {
+    Source s;
+    Target t;
+    int M, N, steps;
+    double a, b, c, eps;
+};
+
+// C = P Q for symmetric m x m factors of one another's polynomials (so C is
+// symmetric), 2 x 2 entries a thread.
+__device__ __forceinline__ void small_product(const double* P, const double* Q, double* C, int m) {
+    const int nb = (m + 1) >> 1;
+    if ((int)threadIdx.x < nb * nb) {
+        const int p = 2 * (threadIdx.x / nb), q = 2 * (threadIdx.x % nb);
+        double c00 = 0., c01 = 0., c10 = 0., c11 = 0.;
+        for (int k = 0; k < m; ++k) {
+            const double p0 = P[k * SM + p], p1 = P[k * SM + p + 1];
+            const double q0 = Q[k * SM + q], q1 = Q[k * SM + q + 1];
+            c00 = fma(p0, q0, c00);
+            c01 = fma(p0, q1, c01);
+            c10 = fma(p1, q0, c10);
+            c11 = fma(p1, q1, c11);
+        }
+        C[p * SM + q] = c00;
+        C[p * SM + q + 1] = c01;
+        C[(p + 1) * SM + q] = c10;
+        C[(p + 1) * SM + q + 1] = c11;
+    }
+    __syncthreads();
+}
+
+__global__ __launch_bounds__(SNT) void ns_small_kernel(const SmallArgs a) {
+    __shared__ __attribute__((aligned(16))) float tile[SL * SPS];       // [l][p], p along the short side
+    __shared__ __attribute__((aligned(16))) double part[SNT * 16];      // partial A, then A, P, Q and a product
+    __shared__ double norm;
+    const int tid = threadIdx.x;
+    const bool tall = a.M > a.N;
+    const int m = tall ? a.N : a.M, n = tall ? a.M : a.N;
+    const int64_t base = (int64_t)blockIdx.x * a.M * a.N;
+
+    // columns l0 .. of the long side into the tile, zeros where there is nothing
+    auto load_tile = [&](int l0, auto&& src) {
+        for (int i = tid; i < SL * SM / 8; i += SNT) {
+            if (tall) {                       // eight along the short side
+                const int l = i / (SM / 8), p = 8 * (i % (SM / 8));
+                float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (l0 + l < n && p < m) src(base + (int64_t)(l0 + l) * m + p, m - p, u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) tile[l * SPS + p + e] = p + e < m ? u[e] : 0.f;
+            } else {
+                const int p = i / (SL / 8), l = 8 * (i % (SL / 8));
+                float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (l0 + l < n && p < m) src(base + (int64_t)p * n + l0 + l, n - (l0 + l), u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) tile[(l + e) * SPS + p] = l0 + l + e < n ? u[e] : 0.f;
+            }
+        }
+        __syncthreads();
+    };
+
+    // A = U U^T: 4 x 4 entries a thread, nb^2 threads cover the matrix, and the
+    // SNT / nb^2 groups of threads share out the long side
+    const int nb = (m + 3) >> 2, per = nb * nb, groups = SNT / per;
+    const int grp = tid / per, bp = 4 * ((tid % per) / nb), bq = 4 * ((tid % per) % nb);
+    double acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.;
+    for (int l0 = 0; l0 < n; l0 += SL) {
+        load_tile(l0, [&](int64_t at, int left, float* u) { source8_first(a.s, at, left, u); });
+        if (grp < groups)
+            for (int l = grp; l < SL; l += groups) {
+                const float4 p = *(const float4*)&tile[l * SPS + bp], q = *(const float4*)&tile[l * SPS + bq];
+                const double pd[4] = {p.x, p.y, p.z, p.w}, qd[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fma(pd[i], qd[j], acc[i][j]);
+            }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (grp < groups) part[(grp * 16 + 4 * i + j) * per + tid % per] = acc[i][j];
+    __syncthreads();
+    // entry (i, j) of block k: the groups' partial sums in order
+    double sum[2] = {0., 0.};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int e = tid + k * SNT;
+        if (e < 16 * per)
+            for (int g = 0; g < groups; ++g) sum[k] += part[g * 16 * per + e];
+    }
+    __syncthreads();
+    double *A = part, *P = part + SM * SM, *Q = part + 2 * SM * SM, *S = part + 3 * SM * SM;
+    for (int i = tid; i < 4 * SM * SM; i += SNT) part[i] = 0.;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int e = tid + k * SNT;
+        if (e < 16 * per) {
+            const int ij = e / per, blk = e % per;
+            A[(4 * (blk / nb) + (ij >> 2)) * SM + 4 * (blk % nb) + (ij & 3)] = sum[k];
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        double t = 0.;
+        for (int i = 0; i < m; ++i) t += A[i * SM + i];
+        norm = sqrt(t) + a.eps;
+    }
+    __syncthreads();
+    const double inv = 1. / norm;
+    for (int i = tid; i < SM * SM; i += SNT) A[i] = A[i] * inv * inv;
+    __syncthreads();
+    for (int k = 0; k < a.steps; ++k) {
+        small_product(A, A, S, m);
+        for (int i = tid; i < SM * SM; i += SNT) {
+            const double d = (i / SM == i % SM && i / SM < m) ? a.a : 0.;
+            P[i] = d + a.b * A[i] + a.c * S[i];
+            if (k == 0) Q[i] = P[i];
+        }
+        __syncthreads();
+        if (k > 0) {
+            small_product(Q, P, S, m);
+            double* x = Q;
+            Q = S;
+            S = x;
+        }
+        if (k + 1 < a.steps) {
+            small_product(A, P, S, m);
+            small_product(S, P, A, m);
+        }
+    }
+    // X = Q U / norm: a thread takes one column of the long side and every fourth
+    // group of four rows
+    for (int l0 = 0; l0 < n; l0 += SL) {
+        load_tile(l0, [&](int64_t at, int left, float* u) { source8(a.s, at, left, u); });
+        const int l = tid % SL;
+        for (int pb = tid / SL; pb < nb; pb += SNT / SL) {
+            double o[4] = {0., 0., 0., 0.};
+            for (int q = 0; q < 4 * nb; q += 4) {
+                const float4 u = *(const float4*)&tile[l * SPS + q];
+                const double ud[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = fma(Q[(q + j) * SM + 4 * pb + i], ud[j], o[i]);
+            }
+            if (l0 + l >= n) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int p = 4 * pb + i;
+                if (p >= m) continue;
+                const int64_t at = base + (tall ? (int64_t)(l0 + l) * m + p : (int64_t)p * n + l0 + l);
+                float v[8] = {(float)(o[i] * inv)};
+                target8(a.t, at, 1, v);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+constexpr size_t kAlign = 256;
+constexpr int kMaxSide = 32768, kMaxSteps = 64;
+size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+int pad64(int v) { return (v + 63) / 64 * 64; }
+
+bool is_small(int M, int N) { return (M < N ? M : N) <= SM; }
+
+struct Layout {
+    size_t part, x, xt[2], A, B, total;
+};
+
+moe_status check_sizes(int B, int M, int N) {
+    if (B < 0 || M <= 0 || N <= 0) return MOE_ERR_INVALID_ARG;
+    if (M > kMaxSide || N > kMaxSide || B > 65535) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+Layout layout_of(int B, int M, int N) {
+    Layout L = {};
+    if (is_small(M, N)) return L;
+    const size_t m = pad64(M < N ? M : N), n = pad64(M < N ? N : M);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align_up(off + bytes);
+        return at;
+    };
+    L.part = take((size_t)B * norm_blocks((int64_t)M * N) * sizeof(double));
+    L.x = take((size_t)B * m * n * 4);
+    L.xt[0] = take((size_t)B * m * n * 4);
+    L.xt[1] = take((size_t)B * m * n * 4);
+    L.A = take((size_t)B * m * m * 4);
+    L.B = take((size_t)B * m * m * 4);
+    L.total = off;
+    return L;
+}
+
+// Largest |v(x)| over [0, s] for v's values at the ends and at the points given.
+struct Bound {
+    double best = 0.;
+    bool fine = true;
+    void at(double v) {
+        if (!(fabs(v) <= 1e4)) fine = false;
+        if (fabs(v) > best) best = fabs(v);
+    }
+};
+// Bounds of a step that starts with singular values in [0, s]: of b A + c A A
+// and of the singular values after it.
+bool step_bounds(double a, double b, double c, double s, double* mid, double* next) {
+    Bound p, q;
+    const double y = s * s;
+    auto poly = [&](double t) { return t >= 0. && t <= y; };
+    p.at(b * y + c * y * y);
+    if (c != 0. && poly(-b / (2. * c))) p.at(-b * b / (4. * c));
+    auto f = [&](double t) { return sqrt(t) * (a + b * t + c * t * t); };
+    q.at(f(y));
+    if (c != 0.) {
+        const double d = 9. * b * b - 20. * a * c;
+        if (d >= 0.)
+            for (int k = -1; k <= 1; k += 2) {
+                const double t = (-3. * b + k * sqrt(d)) / (10. * c);
+                if (poly(t)) q.at(f(t));
+            }
+    } else if (b != 0. && poly(-a / (3. * b))) {
+        q.at(f(-a / (3. * b)));
+    }
+    *mid = p.best * (1. + 1e-3);
+    *next = q.best * (1. + 1e-3);
+    return p.fine && q.fine;
+}
+// The largest power of two that keeps `bound` at 2^15 at most.
+double scale_for(double bound) {
+    double s = 1.;
+    while (s * bound > 32768.) s *= 0.5;
+    while (s < 1099511627776. && 2. * s * bound <= 32768.) s *= 2.;
+    return s;
+}
+
+moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int steps, double a, double b,
+               double c, double eps, void* workspace, size_t ws_bytes, hipStream_t stream) {
+    if (steps < 1 || steps > kMaxSteps) return MOE_ERR_INVALID_ARG;
+    if (!(eps >= 0.) || !isfinite(eps) || !isfinite(a) || !isfinite(b) || !isfinite(c))
+        return MOE_ERR_INVALID_ARG;
+    double mid[kMaxSteps], top[kMaxSteps + 1];
+    top[0] = 1.;
+    for (int k = 0; k < steps; ++k)
+        if (!step_bounds(a, b, c, top[k], &mid[k], &top[k + 1])) return MOE_ERR_UNSUPPORTED;
+    if (B == 0) return MOE_OK;
+    (void)hipGetLastError();
+    auto ok = [] { return hipGetLastError() == hipSuccess; };
+    if (is_small(M, N)) {
+        const SmallArgs s = {src, tgt, M, N, steps, a, b, c, eps};
+        ns_small_kernel<<<B, SNT, 0, stream>>>(s);
+        return ok() ? MOE_OK : MOE_ERR_HIP;
+    }
+    const Layout L = layout_of(B, M, N);
+    if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    char* ws = (char*)workspace;
+    const bool tall = M > N;
+    const int m = pad64(tall ? N : M), n = pad64(tall ? M : N);
+    const int ti = (m + BT - 1) / BT, tj = (n + BT - 1) / BT;
+    const int64_t wide_grid = (int64_t)B * ti * tj, sym_grid = (int64_t)B * ti * (ti + 1) / 2;
+    if (wide_grid * 256 >= ((int64_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
+    const int nb = norm_blocks((int64_t)M * N);
+    ns_norm_kernel<<<dim3(nb, B), 256, 0, stream>>>(src, (int64_t)M * N, (double*)(ws + L.part));
+    if (!ok()) return MOE_ERR_HIP;
+
+    char *x = ws + L.x, *A = ws + L.A, *Bm = ws + L.B;
+    char* xt[2] = {ws + L.xt[0], ws + L.xt[1]};
+    double sx = scale_for(top[0]);
+    const int Mp = pad64(M), Np = pad64(N);
+    const SplitArgs sp = {src, (const double*)(ws + L.part), nb, M, N, Mp, Np, eps, (float)sx,
+                          tall ? xt[0] : x, tall ? x : xt[0]};
+    ns_split_kernel<<<dim3(Np / ST, Mp / ST, B), 256, 0, stream>>>(sp);
+    if (!ok()) return MOE_ERR_HIP;
+
+    const int64_t xs = (int64_t)m * n * 4, as = (int64_t)m * m * 4;
+    for (int k = 0; k < steps; ++k) {
+        const double sa = scale_for(top[k] * top[k]), sb = scale_for(mid[k]), sn = scale_for(top[k + 1]);
+        char *xc = xt[k & 1], *xn = xt[(k + 1) & 1];
+        MulArgs g = {};
+        g.p = g.q = x;
+        g.p_stride = g.q_stride = xs;
+        g.pr = g.qr = m;
+        g.K = n;
+        g.ti = g.tj = ti;
+        g.f = (float)(1. / (sx * sx));
+        g.so = (float)sa;
+        g.c = g.ct = A;
+        g.c_stride = as;
+        ns_product_kernel<GRAM><<<(unsigned)sym_grid, 256, 0, stream>>>(g);
+        if (!ok()) return MOE_ERR_HIP;
+        MulArgs q = g;
+        q.p = q.q = q.add = A;
+        q.p_stride = q.q_stride = q.add_stride = as;
+        q.K = m;
+        q.f = (float)(c / (sa * sa));
+        q.fa = (float)(b / sa);
+        q.so = (float)sb;
+        q.c = q.ct = Bm;
+        ns_product_kernel<SQUARE><<<(unsigned)sym_grid, 256, 0, stream>>>(q);
+        if (!ok()) return MOE_ERR_HIP;
+        MulArgs y = {};
+        y.p = Bm;
+        y.p_stride = as;
+        y.pr = m;
+        y.q = xc;
+        y.q_stride = xs;
+        y.qr = n;
+        y.K = m;
+        y.ti = ti;
+        y.tj = tj;
+        y.f = (float)(1. / (sb * sx));
+        y.fa = (float)(a / sx);
+        y.add = x;
+        y.add_stride = y.c_stride = xs;
+        if (k + 1 < steps) {
+            y.so = (float)sn;
+            y.c = x;
+            y.ct = xn;
+            ns_product_kernel<APPLY><<<(unsigned)wide_grid, 256, 0, stream>>>(y);
+        } else {
+            y.swap = tall;
+            if (tall) y.add = xc;
+            y.M = M;
+            y.N = N;
+            y.t = tgt;
+            ns_product_kernel<FINAL><<<(unsigned)wide_grid, 256, 0, stream>>>(y);
+        }
+        if (!ok()) return MOE_ERR_HIP;
+        sx = sn;
+    }
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+size_t moe_newton_schulz_workspace_size(int B, int M, int N) {
+    if (moe::check_sizes(B, M, N) != MOE_OK) return 0;
+    return moe::layout_of(B, M, N).total;
+}
+
+moe_status moe_newton_schulz(const void* G, void* out, int B, int M, int N, int steps, double a, double b,
+                             double c, double eps, moe_dtype dtype, void* workspace, size_t ws_bytes,
+                             hipStream_t stream) {
+    const moe_status st = moe::check_sizes(B, M, N);
+    if (st != MOE_OK) return st;
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (B > 0 && (!G || !out)) return MOE_ERR_INVALID_ARG;
+    if (!moe::aligned(G, 16) || !moe::aligned(out, 16)) return MOE_ERR_INVALID_ARG;
+    const int bf16 = dtype == MOE_BF16;
+    const moe::Source src = {G, nullptr, 0.f, 0, bf16};
+    const moe::Target tgt = {out, nullptr, 0.f, 0.f, 0, bf16};
+    return moe::run(src, tgt, B, M, N, steps, a, b, c, eps, workspace, ws_bytes, stream);
+}
+
+moe_status moe_muon_step(void* W, void* W_bf16, const float* dW, float* momentum, int B, int M, int N,
+                         float lr, float beta, float weight_decay, float scale, int nesterov, int steps,
+                         double a, double b, double c, double eps, moe_dtype dtype, void* workspace,
+                         size_t ws_bytes, hipStream_t stream) {
+    const moe_status st = moe::check_sizes(B, M, N);
+    if (st != MOE_OK) return st;
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (W_bf16 && dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
+    if (!isfinite(lr) || !isfinite(beta) || !isfinite(weight_decay) || !isfinite(scale))
+        return MOE_ERR_INVALID_ARG;
+    if (B > 0 && (!W || !dW || !momentum)) return MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {W, W_bf16, dW, momentum};
+    for (const void* p : ptrs)
+        if (!moe::aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+    const moe::Source src = {dW, momentum, beta, nesterov ? 1 : 0, 0};
+    const moe::Target tgt = {W, (uint16_t*)W_bf16, (float)(1. - (double)lr * weight_decay),
+                             (float)((double)lr * scale), 1, dtype == MOE_BF16};
+    return moe::run(src, tgt, B, M, N, steps, a, b, c, eps, workspace, ws_bytes, stream);
+}
+
+}  // extern "C"

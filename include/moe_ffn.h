@@ -575,6 +575,75 @@ moe_status moe_layer_norm_backward(const void *h, const float *mean, const float
                                    float *dweight, float *dbias, int64_t T, int D, moe_dtype dtype,
                                    void *workspace, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Orthogonalised updates of the weights from their gradients: the
+ * Newton-Schulz iteration and the Muon step around it, for a batch of B
+ * matrices [M, N] (the experts' dW1, dW3 [E, D, F] and dW2 [E, F, D] as
+ * moe_ffn_backward writes them, B = E).  Per matrix:
+ *
+ *   X = U / (|U| + eps),  |U| the Frobenius norm
+ *   `steps` times:  X <- a X + (b A + c A A) X,  A = X X^T
+ *   (X^T X on the right when M > N: the products run on the shorter side)
+ *
+ * With (a, b, c) = (3.4445, -4.7750, 2.0315) and five steps the singular
+ * values of U end near 1 (between about 0.7 and 1.2, those too small to get
+ * there multiplied by at most a^5); (1.5, -0.5, 0) is the classical
+ * iteration, which needs more steps and converges to 1.
+ * ------------------------------------------------------------------------ */
+
+/* Workspace bytes moe_newton_schulz and moe_muon_step need (16 bytes an
+ * element and 8 an entry of A, sizes padded to multiples of 64, and a little;
+ * 0 when the shorter side is at most 32, which needs none); 0 if the sizes
+ * are invalid or unsupported. */
+size_t moe_newton_schulz_workspace_size(int B, int M, int N);
+
+/*
+ *   G    [B, M, N]  dtype; U = G
+ *   out  [B, M, N]  dtype; X after `steps` steps; may be G
+ *   workspace >= moe_newton_schulz_workspace_size() bytes, 256-byte aligned
+ *
+ * Results are those of fp32 arithmetic (fp16 pairs of 22 bits on the matrix
+ * cores, fp32 sums; shorter sides of at most 32: fp64), rounded once to
+ * dtype; the norm is summed in fp64, so gradients of any magnitude will do.
+ * Summation orders are fixed: repeated calls give equal bits.  A zero
+ * matrix gives zeros (eps > 0); one that holds an infinity or NaN gives NaN,
+ * the others of the batch are untouched by it.
+ *
+ * Returns MOE_OK; MOE_ERR_INVALID_ARG (null or misaligned pointer, B < 0, M
+ * or N < 1, steps outside [1, 64], eps negative, eps or a coefficient not
+ * finite, unknown dtype); MOE_ERR_UNSUPPORTED (M or N > 32768, B > 65535,
+ * 2^24 or more 128 x 128 tiles in all, coefficients that let a singular value
+ * in [0, 1] or the polynomial b A + c A A grow beyond 10^4 within the steps);
+ * MOE_ERR_WORKSPACE; MOE_ERR_HIP.  G and out are 16-byte aligned.  B == 0
+ * launches nothing.
+ */
+moe_status moe_newton_schulz(const void *G, void *out, int B, int M, int N, int steps, double a,
+                             double b, double c, double eps, moe_dtype dtype, void *workspace,
+                             size_t ws_bytes, hipStream_t stream);
+
+/*
+ * One Muon step:
+ *
+ *   momentum <- beta * momentum + dW
+ *   U = dW + beta * momentum (nesterov != 0), momentum otherwise
+ *   W <- (1 - lr * weight_decay) * W - lr * scale * X,  X as above from U
+ *
+ *   W        [B, M, N]  dtype; in and out
+ *   W_bf16   [B, M, N]  bf16 or NULL; out: the new W rounded to bf16 (dtype
+ *            MOE_F32 only: 32-bit weights beside the copy the layer reads)
+ *   dW       [B, M, N]  fp32
+ *   momentum [B, M, N]  fp32; in and out
+ *
+ * W is rounded once to dtype.  The buffers must not overlap.  Workspace,
+ * precision, errors and sizes as moe_newton_schulz, and
+ * MOE_ERR_INVALID_ARG for lr, beta, weight_decay or scale that is not
+ * finite, or W_bf16 beside a bf16 W.  A refused call changes nothing.
+ */
+moe_status moe_muon_step(void *W, void *W_bf16, const float *dW, float *momentum, int B, int M, int N,
+                         float lr, float beta, float weight_decay, float scale, int nesterov,
+                         int steps, double a, double b, double c, double eps, moe_dtype dtype,
+                         void *workspace, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
