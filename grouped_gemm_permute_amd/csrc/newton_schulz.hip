@@ -20,11 +20,13 @@
 // entry is never larger than the largest singular value, and s puts the bound
 // at 2^15 at most (fp16 ends at 65504).
 //
-// Layout: a plane matrix has rows of K values in groups of 32, a group's 64
-// bytes of hi followed by its 64 bytes of lo, so one 128-byte line feeds both
-// planes of a K step.  Sizes are padded with zeros to multiples of 64 (they
-// stay zero through the iteration), so only the first and the last kernel
-// know the matrix's own sizes.
+// Layout: a matrix of planes is cut into blocks of 32 rows by 32 columns of
+// 4 KiB, each in the order in which the matrix instruction's lanes take it (plane,
+// half of the columns, then 16 bytes for each of the 64 lanes), so a fragment
+// is 1 KiB of consecutive memory for its wavefront, whether it goes to LDS or
+// to registers, and needs no swizzle there.  Sizes are padded with zeros to multiples of
+// 64 (they stay zero through the iteration), so only the first and the last
+// kernel know the matrix's own sizes.
 //
 // Each product is C = P Q^T over row-major operands: A = X X^T takes X's rows
 // twice, A A = A A^T takes A's (A is symmetric), and B X takes B's rows and
@@ -205,18 +207,23 @@ __device__ __forceinline__ void split8(const float* v, u32x4_t& hi, u32x4_t& lo)
         lo[i] = __builtin_bit_cast(uint32_t, l);
     }
 }
-// Byte offset of column c (a multiple of 8) of a plane row; lo is 64 bytes on.
-__device__ __forceinline__ int64_t plane_at(int64_t row, int64_t ld, int c) {
-    return row * ld * 4 + (c >> 5) * 128 + (c & 31) * 2;
+// Planes of a 32 x 32 block: [hi, lo][columns 0..15, 16..31][lane][8 values],
+// lane = row % 32 + 32 for the second eight columns of a half.
+constexpr int BLOCK = 4096, LO = 2048, HALF = 1024;
+// Byte offset of the hi values of columns c .. c + 7 (c a multiple of 8) of a
+// row; ld is the padded row length.  The lo values are LO bytes on.
+__device__ __forceinline__ int64_t plane_at(int row, int ld, int c) {
+    return ((int64_t)(row >> 5) * (ld >> 5) + (c >> 5)) * BLOCK + ((c >> 4) & 1) * HALF + ((c >> 3) & 1) * 512 +
+           (row & 31) * 16;
 }
 __device__ __forceinline__ void store_planes(char* base, int64_t at, const float* v) {
     u32x4_t hi, lo;
     split8(v, hi, lo);
     *(u32x4_t*)(base + at) = hi;
-    *(u32x4_t*)(base + at + 64) = lo;
+    *(u32x4_t*)(base + at + LO) = lo;
 }
 __device__ __forceinline__ void add_planes(const char* base, int64_t at, float f, float* v) {
-    const u32x4_t hi = *(const u32x4_t*)(base + at), lo = *(const u32x4_t*)(base + at + 64);
+    const u32x4_t hi = *(const u32x4_t*)(base + at), lo = *(const u32x4_t*)(base + at + LO);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t hw = hi[i], lw = lo[i];
@@ -256,18 +263,21 @@ __global__ __launch_bounds__(256) void ns_split_kernel(const SplitArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) u[e] = e < left ? (float)((double)u[e] * inv) : 0.f;
         }
-        store_planes(rows, plane_at(i0 + r, a.Np, j0 + c), u);
 #pragma unroll
         for (int e = 0; e < 8; ++e) tile[r][c + e] = u[e];
     }
     __syncthreads();
+    // consecutive lanes take consecutive rows of the planes written
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int c = (tid >> 3) + 32 * k, r = (tid & 7) * 8;
+        const int r = tid & 63, c = ((tid >> 6) + 4 * k) * 8;
         float u[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = tile[r + e][c];
-        store_planes(cols, plane_at(j0 + c, a.Mp, i0 + r), u);
+        for (int e = 0; e < 8; ++e) u[e] = tile[r][c + e];
+        store_planes(rows, plane_at(i0 + r, a.Np, j0 + c), u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = tile[c + e][r];
+        store_planes(cols, plane_at(j0 + r, a.Mp, i0 + c), u);
     }
 }
 
@@ -277,8 +287,8 @@ enum : int { GRAM = 0, SQUARE = 1, APPLY = 2, FINAL = 3 };
 
 constexpr int BT = 128;                       // tile rows and columns
 constexpr int KB = 32;                        // K step
-constexpr int ROW = 128;                      // bytes of a staged row: 32 hi, 32 lo
-constexpr int OPB = BT * ROW;                 // one operand of a stage
+constexpr int OPB = BT / 32 * BLOCK;          // one operand of a stage
+constexpr int TLD = BT + 1;                   // row of the fp32 tile in LDS
 
 struct MulArgs {
     const char *p, *q;          // planes [B][pr][K], [B][qr][K]
@@ -286,7 +296,7 @@ struct MulArgs {
     int pr, qr, K;              // padded rows of each side, reduction length
     int ti, tj;                 // tiles of each side
     float f;                    // factor of the product
-    const char* add;            // SQUARE: A; APPLY, FINAL: X (FINAL, swapped: X^T)
+    const char* add;            // SQUARE: A; APPLY, FINAL: X
     int64_t add_stride;
     float fa;                   // factor of the addend
     float so;                   // scale of the stored planes
@@ -297,28 +307,25 @@ struct MulArgs {
     Target t;
 };
 
-// Index of element (r, c) of the fp32 tile in LDS.  Writes of a wavefront
-// (32 columns of two rows), reads of 8 columns by 16 lanes of four rows and
-// reads of 8 rows by 16 lanes of four columns all spread over the banks.
-__device__ __forceinline__ int tile_at(int r, int c) {
-    return r * BT + (c ^ ((((r >> 3) ^ (r & 1)) & 7) << 2) ^ ((c >> 5) & 3));
+// Row of accumulator register g within its 32 x 32 block (the column is lane % 32).
+__device__ __forceinline__ int acc_row(int g, int kh) { return 8 * (g >> 2) + (g & 3) + 4 * kh; }
+
+// acc += (ph + pl)(qh + ql)^T without the product of the two low parts.
+__device__ __forceinline__ void mul3(f32x16_t& acc, f16x8_t ph, f16x8_t pl, f16x8_t qh, f16x8_t ql) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, acc, 0, 0, 0);
 }
 
-template <int MODE>
-__global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
-    constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
-    // separate objects, so that a read of one buffer does not wait for the
-    // transfers into the other; the epilogue holds rows 0..63 of the fp32 tile
-    // in the first, 64..127 in the second
-    __shared__ __attribute__((aligned(1024))) char st0[2 * OPB];
-    __shared__ __attribute__((aligned(1024))) char st1[2 * OPB];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-
+// This workgroup's matrix and tile; of a symmetric result the tiles on and
+// below the diagonal.  Each XCD takes a contiguous range, so its L2 holds
+// one matrix's operands (or a band of rows).
+template <bool SYM>
+__device__ __forceinline__ void tile_of(const MulArgs& a, int& b, int& ti, int& tj) {
     const int per = SYM ? a.ti * (a.ti + 1) / 2 : a.ti * a.tj;
     const int id = xcd_remap(blockIdx.x, gridDim.x);
-    const int b = id / per;
-    int t = id - b * per, ti, tj;
+    b = id / per;
+    const int t = id - b * per;
     if constexpr (SYM) {
         ti = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);
         while (ti * (ti + 1) / 2 > t) --ti;
@@ -328,24 +335,95 @@ __global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
         ti = t % a.ti;
         tj = t / a.ti;
     }
+}
+
+// From the sums of a TS x TS tile (sum8: eight of a row) to what the mode
+// writes: eight values a thread along the rows, and, through the fp32 tile
+// `at` in LDS, along the columns for the transposed order.
+template <int MODE, int TS, int NT, typename Sum8, typename At>
+__device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0, bool both, Sum8 sum8,
+                                         At at) {
+    constexpr int SEGS = TS / 8, PASSES = (TS * SEGS + NT - 1) / NT;
+    // consecutive lanes take consecutive rows (the planes' order), or, for the
+    // target, the segments of a row
+    auto place = [](int id, int& row, int& seg) {
+        row = MODE == FINAL ? id / SEGS : id % TS;
+        seg = 8 * (MODE == FINAL ? id % SEGS : id / TS);
+    };
+    if (MODE == FINAL) both = a.swap;
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+        int r, c;
+        place(threadIdx.x + k * NT, r, c);
+        if (r >= TS || c >= TS || i0 + r >= a.pr || j0 + c >= a.qr) continue;
+        float v[8];
+        sum8(r, c, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= a.f;
+        const int64_t to = plane_at(i0 + r, a.qr, j0 + c);
+        if constexpr (MODE != GRAM) add_planes(a.add + b * a.add_stride, to, a.fa, v);
+        if constexpr (MODE != FINAL) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= a.so;
+            store_planes(a.c + b * a.c_stride, to, v);
+        } else if (!a.swap) {
+            const int left = a.N - (j0 + c);
+            if (i0 + r < a.M && left > 0)
+                target8(a.t, ((int64_t)b * a.M + i0 + r) * a.N + j0 + c, left, v);
+        }
+        if (both) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) at(r, c + e) = v[e];
+        }
+    }
+    if (!both) return;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+        int c, r;
+        place(threadIdx.x + k * NT, c, r);
+        if (c >= TS || r >= TS || i0 + r >= a.pr || j0 + c >= a.qr) continue;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = at(r + e, c);
+        if constexpr (MODE != FINAL) {
+            store_planes(a.ct + b * a.c_stride, plane_at(j0 + c, a.pr, i0 + r), v);
+        } else {
+            const int left = a.N - (i0 + r);
+            if (j0 + c < a.M && left > 0)
+                target8(a.t, ((int64_t)b * a.M + j0 + c) * a.N + i0 + r, left, v);
+        }
+    }
+}
+
+template <int MODE>
+__global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
+    constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
+    // separate objects, so that a read of one buffer does not wait for the
+    // transfers into the other; the epilogue holds rows 0..63 of the fp32 tile
+    // in the first, 64..127 in the second
+    constexpr int TILE_BYTES = BT / 2 * TLD * 4;
+    static_assert(TILE_BYTES >= 2 * OPB, "a half of the fp32 tile covers a stage");
+    __shared__ __attribute__((aligned(1024))) char st0[TILE_BYTES];
+    __shared__ __attribute__((aligned(1024))) char st1[TILE_BYTES];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    int b, ti, tj;
+    tile_of<SYM>(a, b, ti, tj);
     const int i0 = ti * BT, j0 = tj * BT;
 
-    // stage sources: transfer j of wavefront w fills rows 32 w + 8 j .. +7 of an
-    // operand; a lane brings the chunk that its place holds under the swizzle.
-    // Rows past the padded end (half tiles) read the last row and are not stored.
-    const char *ps[4], *qs[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int r = 32 * wave + 8 * j + (lane >> 3);
-        const int ch = ((lane & 7) ^ swz8(r)) * 16;
-        ps[j] = a.p + b * a.p_stride + (int64_t)min(i0 + r, a.pr - 1) * a.K * 4 + ch;
-        qs[j] = a.q + b * a.q_stride + (int64_t)min(j0 + r, a.qr - 1) * a.K * 4 + ch;
-    }
+    // stage sources: wavefront w brings block row w of both operands, four
+    // transfers of 1 KiB each.  Block rows past the padded end (half tiles)
+    // read the last one and are not stored.
+    const int KT = a.K / KB;     // even: K is a multiple of 64
+    const char* ps = a.p + b * a.p_stride + (int64_t)min((i0 >> 5) + wave, (a.pr >> 5) - 1) * KT * BLOCK;
+    const char* qs = a.q + b * a.q_stride + (int64_t)min((j0 >> 5) + wave, (a.qr >> 5) - 1) * KT * BLOCK;
     auto issue = [&](int kt, char* st) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            load_lds16(ps[j] + (int64_t)kt * ROW, st + (32 * wave + 8 * j) * ROW);
-            load_lds16(qs[j] + (int64_t)kt * ROW, st + OPB + (32 * wave + 8 * j) * ROW);
+            load_lds16(ps + (int64_t)kt * BLOCK + j * 1024 + lane * 16, st + wave * BLOCK + j * 1024);
+            load_lds16(qs + (int64_t)kt * BLOCK + j * 1024 + lane * 16, st + OPB + wave * BLOCK + j * 1024);
         }
     };
 
@@ -356,34 +434,28 @@ __global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
 
+    auto frag = [&](const char* p) { return __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(p + lane * 16)); };
     auto compute = [&](const char* st) {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
             f16x8_t ph[2], pl[2], qh[2], ql[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int pr = 64 * wi + 32 * i + rl, qr = 64 * wj + 32 * i + rl;
-                const char* pb = st + pr * ROW;
-                const char* qb = st + OPB + qr * ROW;
-                const int ch = 2 * ks + kh;
-                ph[i] = __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(pb + ((ch ^ swz8(pr)) << 4)));
-                pl[i] = __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(pb + (((ch + 4) ^ swz8(pr)) << 4)));
-                qh[i] = __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(qb + ((ch ^ swz8(qr)) << 4)));
-                ql[i] = __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(qb + (((ch + 4) ^ swz8(qr)) << 4)));
+                const char* pb = st + (2 * wi + i) * BLOCK + ks * HALF;
+                const char* qb = st + OPB + (2 * wj + i) * BLOCK + ks * HALF;
+                ph[i] = frag(pb);
+                pl[i] = frag(pb + LO);
+                qh[i] = frag(qb);
+                ql[i] = frag(qb + LO);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], qh[j], acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], ql[j], acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[i], qh[j], acc[i][j], 0, 0, 0);
-                }
+                for (int j = 0; j < 2; ++j) mul3(acc[i][j], ph[i], pl[i], qh[j], ql[j]);
         }
     };
     // Step kt: wait for stage kt, then (all wavefronts being past their reads
     // of the other buffer) send stage kt + 1 there and compute on stage kt.
-    const int KT = a.K / KB;     // even: K is a multiple of 64
     auto step = [&](int kt, char* cur, char* nxt) {
         __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
         __builtin_amdgcn_s_barrier();
@@ -399,69 +471,113 @@ __global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
     }
     __syncthreads();
 
-    // ---- epilogue: the fp32 tile through LDS, then 8 values a thread along
-    // the rows, and along the columns for the transposed result
+    // ---- epilogue: the fp32 tile through LDS, rows 0..63 in the first buffer
     auto at = [&](int r, int c) -> float& {
-        return ((float*)(r < 64 ? st0 : st1))[tile_at(r & 63, c)];
+        return ((float*)(r < 64 ? st0 : st1))[(r & 63) * TLD + c];
     };
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int g = 0; g < 16; ++g) {
-                const int r = 64 * wi + 32 * i + 8 * (g >> 2) + (g & 3) + 4 * kh;
-                at(r, 64 * wj + 32 * j + rl) = acc[i][j][g] * a.f;
-            }
+            for (int g = 0; g < 16; ++g)
+                at(64 * wi + 32 * i + acc_row(g, kh), 64 * wj + 32 * j + rl) = acc[i][j][g];
     __syncthreads();
-    const int seg = tid & 15;
-    if constexpr (MODE == FINAL) {
-        const int rows = a.swap ? j0 : i0, cols = a.swap ? i0 : j0;
-        const int ld = a.swap ? a.pr : a.qr;
-        const char* add = a.add + b * a.add_stride;
-        for (int k = 0; k < 8; ++k) {
-            const int r = (tid >> 4) + 16 * k, c = 8 * seg;
-            const int left = a.N - (cols + c);
-            if (rows + r >= a.M || left <= 0) continue;
-            float v[8];
+    auto sum8 = [&](int r, int c, float* v) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = a.swap ? at(c + e, r) : at(r, c + e);
-            add_planes(add, plane_at(rows + r, ld, cols + c), a.fa, v);
-            target8(a.t, ((int64_t)b * a.M + rows + r) * a.N + cols + c, left, v);
-        }
-    } else {
-        char* out = a.c + b * a.c_stride;
-        char* outt = a.ct + b * a.c_stride;
-        const bool both = !SYM || ti != tj;
+        for (int e = 0; e < 8; ++e) v[e] = at(r, c + e);
+    };
+    epilogue<MODE, BT, 256>(a, b, i0, j0, !SYM || ti != tj, sum8, at);
+}
+
+// The same product for grids that would leave most of the GPU idle: tiles of
+// 32 TB rows and columns (TB = 1, 2), whose eight wavefronts share out the K
+// steps among them and add their sums through LDS, so that a product of a
+// few hundred rows runs on hundreds of compute units and each wavefront's
+// chain is an eighth as long.  Operands go from memory straight to registers:
+// nothing in a tile is read twice, so LDS would only add its latency.
+constexpr int DW = 8;
+template <int MODE, int TB>
+__global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulArgs a) {
+    constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
+    constexpr int TS = 32 * TB, LD = TS + 1;
+    __shared__ float part[DW][TS * LD];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int b, ti, tj;
+    tile_of<SYM>(a, b, ti, tj);
+    const int i0 = ti * TS, j0 = tj * TS;
+    const int rl = lane & 31, kh = lane >> 5;
+
+    const int KT = a.K / KB;
+    const char *pp[TB], *qp[TB];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int r = (tid >> 4) + 16 * k, c = 8 * seg;
-            if (i0 + r >= a.pr || j0 + c >= a.qr) continue;
-            float v[8];
+    for (int i = 0; i < TB; ++i) {
+        pp[i] = a.p + b * a.p_stride + (int64_t)((i0 >> 5) + i) * KT * BLOCK;
+        qp[i] = a.q + b * a.q_stride + (int64_t)((j0 >> 5) + i) * KT * BLOCK;
+    }
+    const uint32_t at16 = lane * 16;
+    struct Frags {
+        f16x8_t ph[2][TB], pl[2][TB], qh[2][TB], ql[2][TB];   // [k16 slice][block]
+    };
+    auto load = [&](int kt, Frags& f) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = at(r, c + e);
-            const int64_t to = plane_at(i0 + r, a.qr, j0 + c);
-            if constexpr (MODE != GRAM) add_planes(a.add + b * a.add_stride, to, a.fa, v);
+        for (int i = 0; i < TB; ++i) {
+            const char *pb = pp[i] + (int64_t)kt * BLOCK, *qb = qp[i] + (int64_t)kt * BLOCK;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= a.so;
-            store_planes(out, to, v);
-            if (both) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) at(r, c + e) = v[e];
+            for (int ks = 0; ks < 2; ++ks) {
+                f.ph[ks][i] = *(const f16x8_t*)(pb + at16 + ks * HALF);
+                f.pl[ks][i] = *(const f16x8_t*)(pb + at16 + ks * HALF + LO);
+                f.qh[ks][i] = *(const f16x8_t*)(qb + at16 + ks * HALF);
+                f.ql[ks][i] = *(const f16x8_t*)(qb + at16 + ks * HALF + LO);
             }
         }
-        if (!both) return;
-        __syncthreads();
+    };
+    f32x16_t acc[TB][TB];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int c = (tid >> 4) + 16 * k, r = 8 * seg;
-            if (i0 + r >= a.pr || j0 + c >= a.qr) continue;
-            float v[8];
+    for (int i = 0; i < TB; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = at(r + e, c);
-            store_planes(outt, plane_at(j0 + c, a.pr, i0 + r), v);
+        for (int j = 0; j < TB; ++j) acc[i][j] = f32x16_t{};
+    auto compute = [&](const Frags& f) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int i = 0; i < TB; ++i)
+#pragma unroll
+                for (int j = 0; j < TB; ++j)
+                    mul3(acc[i][j], f.ph[ks][i], f.pl[ks][i], f.qh[ks][j], f.ql[ks][j]);
+    };
+    Frags f0, f1;
+    if (wave < KT) {
+        load(wave, f0);
+#pragma unroll 1
+        for (int kt = wave; kt < KT; kt += 2 * DW) {
+            if (kt + DW < KT) load(kt + DW, f1);
+            compute(f0);
+            if (kt + DW >= KT) break;
+            if (kt + 2 * DW < KT) load(kt + 2 * DW, f0);
+            compute(f1);
         }
     }
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+#pragma unroll
+        for (int j = 0; j < TB; ++j)
+#pragma unroll
+            for (int g = 0; g < 16; ++g)
+                part[wave][(32 * i + acc_row(g, kh)) * LD + 32 * j + rl] = acc[i][j][g];
+    __syncthreads();
+    // a thread's results replace the first partial sums of its own entries
+    auto at = [&](int r, int c) -> float& { return part[0][r * LD + c]; };
+    auto sum8 = [&](int r, int c, float* v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = part[0][r * LD + c + e];
+#pragma unroll
+        for (int w = 1; w < DW; ++w)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += part[w][r * LD + c + e];
+    };
+    epilogue<MODE, TS, 64 * DW>(a, b, i0, j0, !SYM || ti != tj, sum8, at);
 }
 
 // ------------------------------------------------- short sides of up to 32
@@ -642,6 +758,9 @@ __global__ __launch_bounds__(SNT) void ns_small_kernel(const SmallArgs a) {
 // ---------------------------------------------------------------- host side
 
 constexpr size_t kAlign = 256;
+// Products of fewer 64-tiles than kSplit32 run on 32-tiles, of fewer 128-tiles
+// than kSplit64 on 64-tiles.
+constexpr int64_t kSplit32 = 128, kSplit64 = 128;
 constexpr int kMaxSide = 32768, kMaxSteps = 64;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -720,6 +839,29 @@ double scale_for(double bound) {
     return s;
 }
 
+// Tile of a product: 128 rows and columns, or the split kernel's 64 or 32.
+template <int MODE>
+bool launch_product(MulArgs& g, int B, hipStream_t stream) {
+    constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
+    auto grid = [&](int tile) {
+        g.ti = (g.pr + tile - 1) / tile;
+        g.tj = (g.qr + tile - 1) / tile;
+        return (int64_t)B * (SYM ? (int64_t)g.ti * (g.ti + 1) / 2 : (int64_t)g.ti * g.tj);
+    };
+    int64_t n;
+    if (grid(64) < kSplit32) {
+        n = grid(32);
+        ns_product_split_kernel<MODE, 1><<<(unsigned)n, 64 * DW, 0, stream>>>(g);
+    } else if (grid(BT) < kSplit64) {
+        n = grid(64);
+        ns_product_split_kernel<MODE, 2><<<(unsigned)n, 64 * DW, 0, stream>>>(g);
+    } else {
+        n = grid(BT);
+        ns_product_kernel<MODE><<<(unsigned)n, 256, 0, stream>>>(g);
+    }
+    return hipGetLastError() == hipSuccess;
+}
+
 moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int steps, double a, double b,
                double c, double eps, void* workspace, size_t ws_bytes, hipStream_t stream) {
     if (steps < 1 || steps > kMaxSteps) return MOE_ERR_INVALID_ARG;
@@ -743,9 +885,8 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     char* ws = (char*)workspace;
     const bool tall = M > N;
     const int m = pad64(tall ? N : M), n = pad64(tall ? M : N);
-    const int ti = (m + BT - 1) / BT, tj = (n + BT - 1) / BT;
-    const int64_t wide_grid = (int64_t)B * ti * tj, sym_grid = (int64_t)B * ti * (ti + 1) / 2;
-    if (wide_grid * 256 >= ((int64_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
+    // a grid's threads are fewer than 2^32
+    if ((int64_t)B * ((m + BT - 1) / BT) * ((n + BT - 1) / BT) >= 1 << 24) return MOE_ERR_UNSUPPORTED;
     const int nb = norm_blocks((int64_t)M * N);
     ns_norm_kernel<<<dim3(nb, B), 256, 0, stream>>>(src, (int64_t)M * N, (double*)(ws + L.part));
     if (!ok()) return MOE_ERR_HIP;
@@ -768,13 +909,11 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
         g.p_stride = g.q_stride = xs;
         g.pr = g.qr = m;
         g.K = n;
-        g.ti = g.tj = ti;
         g.f = (float)(1. / (sx * sx));
         g.so = (float)sa;
         g.c = g.ct = A;
         g.c_stride = as;
-        ns_product_kernel<GRAM><<<(unsigned)sym_grid, 256, 0, stream>>>(g);
-        if (!ok()) return MOE_ERR_HIP;
+        if (!launch_product<GRAM>(g, B, stream)) return MOE_ERR_HIP;
         MulArgs q = g;
         q.p = q.q = q.add = A;
         q.p_stride = q.q_stride = q.add_stride = as;
@@ -783,8 +922,7 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
         q.fa = (float)(b / sa);
         q.so = (float)sb;
         q.c = q.ct = Bm;
-        ns_product_kernel<SQUARE><<<(unsigned)sym_grid, 256, 0, stream>>>(q);
-        if (!ok()) return MOE_ERR_HIP;
+        if (!launch_product<SQUARE>(q, B, stream)) return MOE_ERR_HIP;
         MulArgs y = {};
         y.p = Bm;
         y.p_stride = as;
@@ -793,8 +931,6 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
         y.q_stride = xs;
         y.qr = n;
         y.K = m;
-        y.ti = ti;
-        y.tj = tj;
         y.f = (float)(1. / (sb * sx));
         y.fa = (float)(a / sx);
         y.add = x;
@@ -803,16 +939,14 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
             y.so = (float)sn;
             y.c = x;
             y.ct = xn;
-            ns_product_kernel<APPLY><<<(unsigned)wide_grid, 256, 0, stream>>>(y);
+            if (!launch_product<APPLY>(y, B, stream)) return MOE_ERR_HIP;
         } else {
             y.swap = tall;
-            if (tall) y.add = xc;
             y.M = M;
             y.N = N;
             y.t = tgt;
-            ns_product_kernel<FINAL><<<(unsigned)wide_grid, 256, 0, stream>>>(y);
+            if (!launch_product<FINAL>(y, B, stream)) return MOE_ERR_HIP;
         }
-        if (!ok()) return MOE_ERR_HIP;
         sx = sn;
     }
     return MOE_OK;
