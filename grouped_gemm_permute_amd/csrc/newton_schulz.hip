@@ -222,8 +222,7 @@ __device__ __forceinline__ void store_planes(char* base, int64_t at, const float
     *(u32x4_t*)(base + at) = hi;
     *(u32x4_t*)(base + at + LO) = lo;
 }
-__device__ __forceinline__ void add_planes(const char* base, int64_t at, float f, float* v) {
-    const u32x4_t hi = *(const u32x4_t*)(base + at), lo = *(const u32x4_t*)(base + at + LO);
+__device__ __forceinline__ void add_planes(const u32x4_t hi, const u32x4_t lo, float f, float* v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t hw = hi[i], lw = lo[i];
@@ -310,11 +309,20 @@ struct MulArgs {
 // Row of accumulator register g within its 32 x 32 block (the column is lane % 32).
 __device__ __forceinline__ int acc_row(int g, int kh) { return 8 * (g >> 2) + (g & 3) + 4 * kh; }
 
-// acc += (ph + pl)(qh + ql)^T without the product of the two low parts.
-__device__ __forceinline__ void mul3(f32x16_t& acc, f16x8_t ph, f16x8_t pl, f16x8_t qh, f16x8_t ql) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, acc, 0, 0, 0);
+// acc[i][j] += (ph[i] + pl[i])(qh[j] + ql[j])^T without the product of the two
+// low parts, term by term over the blocks, so that instructions in a row do not
+// wait for each other's sums.
+template <int NI, int NJ>
+__device__ __forceinline__ void mul3(f32x16_t (&acc)[NI][NJ], const f16x8_t* ph, const f16x8_t* pl,
+                                     const f16x8_t* qh, const f16x8_t* ql) {
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(t == 2 ? pl[i] : ph[i], t == 1 ? ql[j] : qh[j],
+                                                                   acc[i][j], 0, 0, 0);
 }
 
 // This workgroup's matrix and tile; of a symmetric result the tiles on and
@@ -351,21 +359,34 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
         seg = 8 * (MODE == FINAL ? id % SEGS : id / TS);
     };
     if (MODE == FINAL) both = a.swap;
+    auto here = [&](int r, int c) { return r < TS && c < TS && i0 + r < a.pr && j0 + c < a.qr; };
+    // all addends on their way before the first store
+    u32x4_t hi[PASSES], lo[PASSES];
+    if constexpr (MODE != GRAM) {
+#pragma unroll
+        for (int k = 0; k < PASSES; ++k) {
+            int r, c;
+            place(threadIdx.x + k * NT, r, c);
+            if (!here(r, c)) continue;
+            const char* p = a.add + b * a.add_stride + plane_at(i0 + r, a.qr, j0 + c);
+            hi[k] = *(const u32x4_t*)p;
+            lo[k] = *(const u32x4_t*)(p + LO);
+        }
+    }
 #pragma unroll
     for (int k = 0; k < PASSES; ++k) {
         int r, c;
         place(threadIdx.x + k * NT, r, c);
-        if (r >= TS || c >= TS || i0 + r >= a.pr || j0 + c >= a.qr) continue;
+        if (!here(r, c)) continue;
         float v[8];
         sum8(r, c, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= a.f;
-        const int64_t to = plane_at(i0 + r, a.qr, j0 + c);
-        if constexpr (MODE != GRAM) add_planes(a.add + b * a.add_stride, to, a.fa, v);
+        if constexpr (MODE != GRAM) add_planes(hi[k], lo[k], a.fa, v);
         if constexpr (MODE != FINAL) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= a.so;
-            store_planes(a.c + b * a.c_stride, to, v);
+            store_planes(a.c + b * a.c_stride, plane_at(i0 + r, a.qr, j0 + c), v);
         } else if (!a.swap) {
             const int left = a.N - (j0 + c);
             if (i0 + r < a.M && left > 0)
@@ -382,7 +403,7 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
     for (int k = 0; k < PASSES; ++k) {
         int c, r;
         place(threadIdx.x + k * NT, c, r);
-        if (c >= TS || r >= TS || i0 + r >= a.pr || j0 + c >= a.qr) continue;
+        if (!here(r, c)) continue;
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = at(r + e, c);
@@ -396,19 +417,115 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
     }
 }
 
-template <int MODE>
-__global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
+// The same from accumulators, for the modes that write planes, a wavefront's
+// 32 x 32 blocks by themselves.  A lane holds four rows in a row of one column, half
+// of a 16-byte piece of the transposed block, which goes out as it is (64 lanes,
+// 512 consecutive bytes); for the other order the block's planes pass through 4 KiB of
+// LDS of the wavefront's own, written in the transposed order and read back with
+// the transposing read.  The addend is the second operand's block at the
+// transposed place (A is symmetric; X^T holds X's entries), in the order of
+// the accumulators.  Through an fp32 tile and two passes of 8 values a thread the
+// same took about 7 us of a 128-tile; this takes 2.
+template <int MODE, int NI, int NJ>
+__device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0, int jb0, bool both,
+                                                const f32x16_t (&acc)[NI][NJ], char* lds) {
+    const int lane = threadIdx.x & 63, rl = lane & 31, kh = lane >> 5;
+    const int pb = a.pr >> 5, qb = a.qr >> 5;
+    // piece q (rows 8 q .. + 7) of the transposed block; + LO for the low plane
+    auto piece = [&](int q) { return (q >> 1) * HALF + (q & 1) * 512 + rl * 16 + kh * 8; };
+    auto one = [&](int i, int j, const uint2 (&hi)[4], const uint2 (&lo)[4]) {
+        const int ib = ib0 + i, jb = jb0 + j;
+        if (ib >= pb || jb >= qb) return;
+        char* ct = a.ct + b * a.c_stride + ((int64_t)jb * pb + ib) * BLOCK;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * a.f;
+            if constexpr (MODE != GRAM) {
+                const uint32_t hw[2] = {hi[q].x, hi[q].y}, lw[2] = {lo[q].x, lo[q].y};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const f16x2_t h = __builtin_bit_cast(f16x2_t, hw[e >> 1]);
+                    const f16x2_t l = __builtin_bit_cast(f16x2_t, lw[e >> 1]);
+                    v[e] = fmaf(a.fa, (float)h[e & 1] + (float)l[e & 1], v[e]);
+                }
+            }
+            uint32_t oh[2], ol[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float x = v[2 * e] * a.so, y = v[2 * e + 1] * a.so;
+                const f16x2_t h = {(_Float16)x, (_Float16)y};
+                const f16x2_t l = {(_Float16)(x - (float)h[0]), (_Float16)(y - (float)h[1])};
+                oh[e] = __builtin_bit_cast(uint32_t, h);
+                ol[e] = __builtin_bit_cast(uint32_t, l);
+            }
+            *(uint2*)(ct + piece(q)) = make_uint2(oh[0], oh[1]);
+            *(uint2*)(ct + piece(q) + LO) = make_uint2(ol[0], ol[1]);
+            if (both) {
+                *(uint2*)(lds + piece(q)) = make_uint2(oh[0], oh[1]);
+                *(uint2*)(lds + piece(q) + LO) = make_uint2(ol[0], ol[1]);
+            }
+        }
+        if (!both) return;
+        // the other lanes' writes: LDS serves a wavefront in order
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        char* c = a.c + b * a.c_stride + ((int64_t)ib * qb + jb) * BLOCK;
+        // a read gives lane s of 16 row 16 (G & 1) + s of the block, four columns;
+        // group G = lane / 16 takes the eight columns 8 (G >> 1) of each half
+        const int G = lane >> 4, sl = lane & 15;
+        const int src = (G & 1) * HALF + ((sl >> 1) & 1) * 512 + (8 * (G >> 1) + (sl >> 2)) * 16 + (sl & 1) * 8;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const char* at = lds + p * LO + src + 256 * h;
+                const s16x4_t x = read_tr(at), y = read_tr(at + 64);
+                const s16x8_t w = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+                *(s16x8_t*)(c + p * LO + h * HALF + lane * 16) = w;
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        uint2 hi[NJ][4], lo[NJ][4];
+        if constexpr (MODE != GRAM) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int ib = min(ib0 + i, pb - 1), jb = min(jb0 + j, qb - 1);
+                const char* add = a.q + b * a.q_stride + ((int64_t)jb * pb + ib) * BLOCK;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    hi[j][q] = *(const uint2*)(add + piece(q));
+                    lo[j][q] = *(const uint2*)(add + piece(q) + LO);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) one(i, j, hi[j], lo[j]);
+    }
+}
+
+// 128 x 128 tiles, four wavefronts of 64 x 64 each, a ring of NS stages of
+// 32 KiB.  NS = 2: two workgroups share a compute unit, one's epilogue under
+// the other's matrix instructions.  NS = 4, for grids of at most one workgroup a
+// compute unit: a stage has three steps to arrive.
+template <int MODE, int NS>
+__global__ __launch_bounds__(256, NS == 2 ? 2 : 1) void ns_product_kernel(const MulArgs a) {
     constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
-    // separate objects, so that a read of one buffer does not wait for the
-    // transfers into the other; the epilogue holds rows 0..63 of the fp32 tile
-    // in the first, 64..127 in the second
     constexpr int TILE_BYTES = BT / 2 * TLD * 4;
     static_assert(TILE_BYTES >= 2 * OPB, "a half of the fp32 tile covers a stage");
+    // separate objects, so that a read of one buffer does not wait for the
+    // transfers into the others; the epilogue holds rows 0..63 of the fp32 tile
+    // in the first, 64..127 in the second
     __shared__ __attribute__((aligned(1024))) char st0[TILE_BYTES];
     __shared__ __attribute__((aligned(1024))) char st1[TILE_BYTES];
+    __shared__ __attribute__((aligned(1024))) char st2[NS == 4 ? 2 * OPB : 16];
+    __shared__ __attribute__((aligned(1024))) char st3[NS == 4 ? 2 * OPB : 16];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-
     int b, ti, tj;
     tile_of<SYM>(a, b, ti, tj);
     const int i0 = ti * BT, j0 = tj * BT;
@@ -416,14 +533,16 @@ __global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
     // stage sources: wavefront w brings block row w of both operands, four
     // transfers of 1 KiB each.  Block rows past the padded end (half tiles)
     // read the last one and are not stored.
-    const int KT = a.K / KB;     // even: K is a multiple of 64
+    const int KT = a.K / KB;
     const char* ps = a.p + b * a.p_stride + (int64_t)min((i0 >> 5) + wave, (a.pr >> 5) - 1) * KT * BLOCK;
     const char* qs = a.q + b * a.q_stride + (int64_t)min((j0 >> 5) + wave, (a.qr >> 5) - 1) * KT * BLOCK;
-    auto issue = [&](int kt, char* st) {
+    constexpr int PER_STAGE = 8;
+    auto issue = [&](int n, char* st) {
+        const int64_t o = (int64_t)n * BLOCK + lane * 16;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            load_lds16(ps + (int64_t)kt * BLOCK + j * 1024 + lane * 16, st + wave * BLOCK + j * 1024);
-            load_lds16(qs + (int64_t)kt * BLOCK + j * 1024 + lane * 16, st + OPB + wave * BLOCK + j * 1024);
+            load_lds16(ps + o + j * 1024, st + wave * BLOCK + j * 1024);
+            load_lds16(qs + o + j * 1024, st + OPB + wave * BLOCK + j * 1024);
         }
     };
 
@@ -434,47 +553,81 @@ __global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
 
-    auto frag = [&](const char* p) { return __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(p + lane * 16)); };
-    auto compute = [&](const char* st) {
+    struct Frags {
+        f16x8_t ph[2][2], pl[2][2], qh[2][2], ql[2][2];   // [k16 slice][block]
+    };
+    auto read = [&](const char* st, Frags& f) {
+        auto frag = [&](const char* p) { return __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(p + lane * 16)); };
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            f16x8_t ph[2], pl[2], qh[2], ql[2];
+        for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const char* pb = st + (2 * wi + i) * BLOCK + ks * HALF;
                 const char* qb = st + OPB + (2 * wj + i) * BLOCK + ks * HALF;
-                ph[i] = frag(pb);
-                pl[i] = frag(pb + LO);
-                qh[i] = frag(qb);
-                ql[i] = frag(qb + LO);
+                f.ph[ks][i] = frag(pb);
+                f.pl[ks][i] = frag(pb + LO);
+                f.qh[ks][i] = frag(qb);
+                f.ql[ks][i] = frag(qb + LO);
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) mul3(acc[i][j], ph[i], pl[i], qh[j], ql[j]);
-        }
     };
-    // Step kt: wait for stage kt, then (all wavefronts being past their reads
-    // of the other buffer) send stage kt + 1 there and compute on stage kt.
-    auto step = [&](int kt, char* cur, char* nxt) {
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+    auto compute = [&](const Frags& f) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) mul3(acc, f.ph[ks], f.pl[ks], f.qh[ks], f.ql[ks]);
+    };
+    // Step n, its operands already in registers: wait until stage n + 1 has
+    // landed and this wavefront's reads of stage n are done; after the barrier
+    // stage n's buffer is free, so stage n + NS is sent there, stage n + 1 is
+    // read into the other registers and the matrix instructions of stage n run
+    // over both.  Past the last stage the last one is sent and read again, so
+    // that every step is alike.
+    auto step = [&](int n, const Frags& fc, Frags& fn, char* cur, const char* nxt) {
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 2) * PER_STAGE, 0));
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        if (kt + 1 < KT) issue(kt + 1, nxt);
-        compute(cur);
+        issue(min(n + NS, KT - 1), cur);
+        read(nxt, fn);
+        compute(fc);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // matrix instruction
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // transfer
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
         __builtin_amdgcn_sched_barrier(0);
     };
+    Frags f0, f1;
     issue(0, st0);
-    for (int kt = 0; kt < KT; kt += 2) {
-        step(kt, st0, st1);
-        step(kt + 1, st1, st0);
+    issue(min(1, KT - 1), st1);
+    if constexpr (NS == 4) {
+        issue(min(2, KT - 1), st2);
+        issue(min(3, KT - 1), st3);
     }
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 1) * PER_STAGE, 15));   // stage 0 has landed
+    __builtin_amdgcn_s_barrier();
+    read(st0, f0);
+    for (int n = 0; n < KT; n += NS) {       // KT is even
+        step(n, f0, f1, st0, st1);
+        if constexpr (NS == 2) {
+            step(n + 1, f1, f0, st1, st0);
+        } else {
+            step(n + 1, f1, f0, st1, st2);
+            if (n + 2 >= KT) break;
+            step(n + 2, f0, f1, st2, st3);
+            step(n + 3, f1, f0, st3, st0);
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));           // before the buffers are used anew
     __syncthreads();
 
-    // ---- epilogue: the fp32 tile through LDS, rows 0..63 in the first buffer
-    auto at = [&](int r, int c) -> float& {
-        return ((float*)(r < 64 ? st0 : st1))[(r & 63) * TLD + c];
-    };
+    if constexpr (MODE != FINAL) {
+        epilogue_blocks<MODE>(a, b, (i0 >> 5) + 2 * wi, (j0 >> 5) + 2 * wj, !SYM || ti != tj, acc, st0 + wave * BLOCK);
+        return;
+    }
+    // ---- the target: the fp32 tile through LDS
+    auto at = [&](int r, int c) -> float& { return ((float*)(r < 64 ? st0 : st1))[(r & 63) * TLD + c]; };
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -487,7 +640,135 @@ __global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = at(r, c + e);
     };
-    epilogue<MODE, BT, 256>(a, b, i0, j0, !SYM || ti != tj, sum8, at);
+    epilogue<MODE, BT, 256>(a, b, i0, j0, true, sum8, at);
+}
+
+// 256 x 256 tiles for long grids: eight wavefronts of 128 x 64, two stages of
+// 64 KiB, one workgroup a compute unit.  A byte from memory feeds twice the
+// products of a 128-tile, and an LDS byte 1.5 times.  Operands are held in
+// registers for one half of the columns of a K step: one half is read while the
+// other is multiplied, so the buffer of a stage is free in the middle of its
+// step and the next but one has a whole step to arrive.
+constexpr int LT = 256, LOPB = LT / 32 * BLOCK;
+template <int MODE>
+__global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs a) {
+    constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
+    constexpr int QUAD = BT * TLD * 4;       // a quadrant of the fp32 tile
+    static_assert(QUAD >= 2 * LOPB, "a quadrant covers a stage");
+    __shared__ __attribute__((aligned(1024))) char st0[QUAD];
+    __shared__ __attribute__((aligned(1024))) char st1[QUAD];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int b, ti, tj;
+    tile_of<SYM>(a, b, ti, tj);
+    const int i0 = ti * LT, j0 = tj * LT;
+    const int KT = a.K / KB;     // even
+    const char* ps = a.p + b * a.p_stride + (int64_t)min((i0 >> 5) + wave, (a.pr >> 5) - 1) * KT * BLOCK;
+    const char* qs = a.q + b * a.q_stride + (int64_t)min((j0 >> 5) + wave, (a.qr >> 5) - 1) * KT * BLOCK;
+    auto issue = [&](int n, char* st) {
+        const int64_t o = (int64_t)n * BLOCK + lane * 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            load_lds16(ps + o + j * 1024, st + wave * BLOCK + j * 1024);
+            load_lds16(qs + o + j * 1024, st + LOPB + wave * BLOCK + j * 1024);
+        }
+    };
+    const int wi = wave >> 2, wj = wave & 3, rl = lane & 31, kh = lane >> 5;
+    f32x16_t acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
+    struct Frags {
+        f16x8_t ph[4], pl[4], qh[2], ql[2];
+    };
+    auto read = [&](const char* st, int ks, Frags& f) {
+        auto frag = [&](const char* p) { return __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(p + lane * 16)); };
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const char* qb = st + LOPB + (2 * wj + j) * BLOCK + ks * HALF;
+            f.qh[j] = frag(qb);
+            f.ql[j] = frag(qb + LO);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const char* pb = st + (4 * wi + i) * BLOCK + ks * HALF;
+            f.ph[i] = frag(pb);
+            f.pl[i] = frag(pb + LO);
+        }
+    };
+    auto compute = [&](const Frags& f) { mul3(acc, f.ph, f.pl, f.qh, f.ql); };
+    auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+    // stage n in `cur`, its first half in f0
+    Frags f0, f1;
+    auto step = [&](int n, char* cur, const char* nxt) {
+        read(cur, 1, f1);
+        compute(f0);
+#pragma unroll
+        for (int i = 0; i < 12; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        fence();
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));   // stage n + 1 has landed, stage n is read
+        __builtin_amdgcn_s_barrier();
+        fence();
+        issue(min(n + 2, KT - 1), cur);
+        read(nxt, 0, f0);
+        compute(f1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        fence();
+    };
+    issue(0, st0);
+    issue(min(1, KT - 1), st1);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 15));
+    __builtin_amdgcn_s_barrier();
+    read(st0, 0, f0);
+    fence();
+    for (int n = 0; n < KT; n += 2) {
+        step(n, st0, st1);
+        step(n + 1, st1, st0);
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+    __syncthreads();
+
+    if constexpr (MODE != FINAL) {
+        epilogue_blocks<MODE>(a, b, (i0 >> 5) + 4 * wi, (j0 >> 5) + 2 * wj, !SYM || ti != tj, acc, st0 + wave * BLOCK);
+        return;
+    }
+    // ---- the target by quadrants, a row of two at a time
+    for (int qi = 0; qi < 2; ++qi) {
+        if (i0 + BT * qi >= a.pr) break;
+        if (wi == qi) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int g = 0; g < 16; ++g)
+                        ((float*)(wj < 2 ? st0 : st1))[(32 * i + acc_row(g, kh)) * TLD + 64 * (wj & 1) + 32 * j + rl] =
+                            acc[i][j][g];
+        }
+        __syncthreads();
+        auto quadrant = [&](char* st, int qj) {
+            if (j0 + BT * qj >= a.qr) return;
+            auto at = [&](int r, int c) -> float& { return ((float*)st)[r * TLD + c]; };
+            auto sum8 = [&](int r, int c, float* v) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = at(r, c + e);
+            };
+            epilogue<MODE, BT, 512>(a, b, i0 + BT * qi, j0 + BT * qj, true, sum8, at);
+        };
+        quadrant(st0, 0);
+        quadrant(st1, 1);
+        __syncthreads();
+    }
 }
 
 // The same product for grids that would leave most of the GPU idle: tiles of
@@ -496,11 +777,14 @@ __global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
 // few hundred rows runs on hundreds of compute units and each wavefront's
 // chain is an eighth as long.  Operands go from memory straight to registers:
 // nothing in a tile is read twice, so LDS would only add its latency.
-constexpr int DW = 8;
+template <int TB>
+constexpr int split_waves() {
+    return TB == 1 ? 8 : 4;
+}
 template <int MODE, int TB>
-__global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulArgs a) {
+__global__ __launch_bounds__((64 * split_waves<TB>()), 2) void ns_product_split_kernel(const MulArgs a) {
     constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
-    constexpr int TS = 32 * TB, LD = TS + 1;
+    constexpr int TS = 32 * TB, LD = TS + 1, DW = split_waves<TB>();
     __shared__ float part[DW][TS * LD];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -540,12 +824,7 @@ __global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulA
         for (int j = 0; j < TB; ++j) acc[i][j] = f32x16_t{};
     auto compute = [&](const Frags& f) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int i = 0; i < TB; ++i)
-#pragma unroll
-                for (int j = 0; j < TB; ++j)
-                    mul3(acc[i][j], f.ph[ks][i], f.pl[ks][i], f.qh[ks][j], f.ql[ks][j]);
+        for (int ks = 0; ks < 2; ++ks) mul3(acc, f.ph[ks], f.pl[ks], f.qh[ks], f.ql[ks]);
     };
     Frags f0, f1;
     if (wave < KT) {
@@ -760,7 +1039,7 @@ __global__ __launch_bounds__(SNT) void ns_small_kernel(const SmallArgs a) {
 constexpr size_t kAlign = 256;
 // Products of fewer 64-tiles than kSplit32 run on 32-tiles, of fewer 128-tiles
 // than kSplit64 on 64-tiles.
-constexpr int64_t kSplit32 = 128, kSplit64 = 128;
+constexpr int64_t kSplit32 = 128, kSplit64 = 128, kOneRound = 256, kLarge = 512;
 constexpr int kMaxSide = 32768, kMaxSteps = 64;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -848,16 +1127,21 @@ bool launch_product(MulArgs& g, int B, hipStream_t stream) {
         g.tj = (g.qr + tile - 1) / tile;
         return (int64_t)B * (SYM ? (int64_t)g.ti * (g.ti + 1) / 2 : (int64_t)g.ti * g.tj);
     };
-    int64_t n;
-    if (grid(64) < kSplit32) {
-        n = grid(32);
-        ns_product_split_kernel<MODE, 1><<<(unsigned)n, 64 * DW, 0, stream>>>(g);
-    } else if (grid(BT) < kSplit64) {
-        n = grid(64);
-        ns_product_split_kernel<MODE, 2><<<(unsigned)n, 64 * DW, 0, stream>>>(g);
+    const int64_t n32 = grid(32), n64 = grid(64), n128 = grid(BT), n256 = grid(LT);
+    if (n64 < kSplit32) {
+        grid(32);
+        ns_product_split_kernel<MODE, 1><<<(unsigned)n32, 64 * split_waves<1>(), 0, stream>>>(g);
+    } else if (n128 < kSplit64) {
+        grid(64);
+        ns_product_split_kernel<MODE, 2><<<(unsigned)n64, 64 * split_waves<2>(), 0, stream>>>(g);
+    } else if (n256 >= kLarge) {
+        ns_product_large_kernel<MODE><<<(unsigned)n256, 512, 0, stream>>>(g);
     } else {
-        n = grid(BT);
-        ns_product_kernel<MODE><<<(unsigned)n, 256, 0, stream>>>(g);
+        grid(BT);
+        if (n128 <= kOneRound)
+            ns_product_kernel<MODE, 4><<<(unsigned)n128, 256, 0, stream>>>(g);
+        else
+            ns_product_kernel<MODE, 2><<<(unsigned)n128, 256, 0, stream>>>(g);
     }
     return hipGetLastError() == hipSuccess;
 }
