@@ -9,6 +9,7 @@ There is no fallback: if the library is missing, loading raises ImportError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -510,29 +511,64 @@ def forward_routed(x, gate_w, W1, W3, W2, shared=None, k=2, y=None, variant="unf
     return y, idx, w
 
 
-def _on_current_device(ref):
-    """Kernels launch on the current device: a tensor of another one is refused."""
-    if ref.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {ref.device}, the current device is "
+def _fits(t, shape, dtype, device):
+    return t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == device
+
+
+def _refuse(ref, **named):
+    """Raise what is wrong with one of named = {name: (tensor, shape, dtype)}:
+    the slow side of _fits."""
+    for name, (t, shape, dtype) in named.items():
+        _expect(name, t, shape, dtype)
+        _same_device(ref, {name: t})
+
+
+def _on_current_device(ref, device):
+    """Kernels launch on the current device: a tensor of the host or of
+    another device is refused."""
+    if device < 0:
+        _same_device(ref, {})
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
 
 
-def _empty(shape, dtype, device, stream):
-    """torch.empty from the pool of the stream the kernels run on, so that
-    the allocator does not hand the memory on, or over, while another
-    stream's work is still using it."""
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _empty(n, dtype, device, stream):
+    """n elements from the pool of the stream the kernels run on, so that the
+    allocator does not hand the memory on, or over, while another stream's
+    work is still using it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(n, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(n, dtype=dtype, device=device)
 
 
-def _check_rows(name, x):
-    _dtype_enum(x.dtype)
-    if x.dim() != 2:
-        raise ValueError(f"{name} must be [T,D]")
-    _expect(name, x, x.shape, x.dtype)
-    return x.shape
+def _empty_like(t, stream):
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
+def _workspace_for(ref, device, n, workspace, stream):
+    """The caller's workspace once it holds n bytes on ref's device, or a new one (n > 0)."""
+    if workspace is None:
+        return _empty(n, torch.uint8, ref.device, stream) if n else None
+    _check_workspace(ref, workspace, n)
+    return workspace
+
+
+def _outputs(out, names):
+    """A copy of ``out``, whose names must be among ``names``."""
+    o = dict(out) if out else {}
+    for name in o:
+        if name not in names:
+            raise ValueError(f"out has no place for {name}")
+    return o
 
 
 def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False, out=None, stats=True,
@@ -543,30 +579,46 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False, ou
     itself without a residual, else the rounded sum), and the fp32 [T] mean
     (None with rms) and rstd that layer_norm_backward takes (both None
     with stats=False).  ``out`` may supply y and h."""
-    T, D = _check_rows("x", x)
-    for name, t, shape in (("weight", weight, (D,)), ("bias", bias, (D,)), ("residual", residual, (T, D))):
-        if t is not None:
-            _expect(name, t, shape, x.dtype)
-    o = dict(out or {})
-    for name in o:
-        if name not in ("y", "h") or (name == "h" and residual is None):
-            raise ValueError(f"out has no place for {name}")
-        _expect(name, o[name], (T, D), x.dtype)
-    _same_device(x, dict(weight=weight, bias=bias, residual=residual, **o))
-    _on_current_device(x)
+    dt, shape, dev, dtype = x.dtype, x.shape, x.get_device(), _dtype_enum(x.dtype)
+    if len(shape) != 2:
+        raise ValueError("x must be [T,D]")
+    T, D = shape
+    o = _outputs(out, ("y",) if residual is None else ("y", "h"))
+    if not x.is_contiguous():
+        _refuse(x, x=(x, shape, dt))
+    if weight is not None and not _fits(weight, (D,), dt, dev):
+        _refuse(x, weight=(weight, (D,), dt))
+    if bias is not None and not _fits(bias, (D,), dt, dev):
+        _refuse(x, bias=(bias, (D,), dt))
+    if residual is not None and not _fits(residual, shape, dt, dev):
+        _refuse(x, residual=(residual, shape, dt))
+    for name, t in o.items():
+        if not _fits(t, shape, dt, dev):
+            _refuse(x, **{name: (t, shape, dt)})
+    _on_current_device(x, dev)
+    h = None
     if "y" not in o:
-        o["y"] = _empty((T, D), x.dtype, x.device, stream)
-    if residual is not None and "h" not in o:
-        o["h"] = _empty((T, D), x.dtype, x.device, stream)
-    o["mean"] = _empty((T,), torch.float32, x.device, stream) if stats and not rms else None
-    o["rstd"] = _empty((T,), torch.float32, x.device, stream) if stats else None
-    _check(lib().moe_layer_norm_forward(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(o["y"]),
-                                        _ptr(o.get("h")), _ptr(o["mean"]), _ptr(o["rstd"]), T, D,
-                                        int(rms), eps, _dtype_enum(x.dtype), _stream(stream)),
-           "moe_layer_norm_forward")
-    if residual is None:
+        o["y"] = _empty_like(x, stream)
+    if residual is not None:
+        if "h" not in o:
+            o["h"] = _empty_like(x, stream)
+        h = o["h"].data_ptr()
+    mean = _empty(T, torch.float32, x.device, stream) if stats and not rms else None
+    rstd = _empty(T, torch.float32, x.device, stream) if stats else None
+    st = lib().moe_layer_norm_forward(x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(bias),
+                                      o["y"].data_ptr(), h, _ptr(mean), _ptr(rstd), T, D, int(rms), eps,
+                                      dtype, _raw_stream(stream, dev))
+    if st:
+        raise MoeError(st, "moe_layer_norm_forward")
+    if h is None:
         o["h"] = x
+    o["mean"], o["rstd"] = mean, rstd
     return o
+
+
+@functools.lru_cache(maxsize=1024)
+def _layer_norm_backward_bytes(T, D, dtype):
+    return lib().moe_layer_norm_backward_workspace_size(T, D, dtype)
 
 
 def layer_norm_backward(h, dy, rstd, mean=None, weight=None, dh=None, bias_grad=False, out=None,
@@ -576,43 +628,45 @@ def layer_norm_backward(h, dy, rstd, mean=None, weight=None, dh=None, bias_grad=
     residual's gradient, dh added when given), dweight (fp32 [D]; None
     without weight) and dbias (fp32 [D]; None without bias_grad).  ``out`` may
     supply any of these."""
-    T, D = _check_rows("h", h)
-    _expect("dy", dy, (T, D), h.dtype)
-    _expect("rstd", rstd, (T,), torch.float32)
-    if mean is not None:
-        _expect("mean", mean, (T,), torch.float32)
+    dt, shape, dev, dtype = h.dtype, h.shape, h.get_device(), _dtype_enum(h.dtype)
+    if len(shape) != 2:
+        raise ValueError("h must be [T,D]")
+    T, D = shape
+    f32 = torch.float32
+    if not h.is_contiguous():
+        _refuse(h, h=(h, shape, dt))
+    if not _fits(dy, shape, dt, dev):
+        _refuse(h, dy=(dy, shape, dt))
+    if not _fits(rstd, (T,), f32, dev):
+        _refuse(h, rstd=(rstd, (T,), f32))
+    if mean is not None and not _fits(mean, (T,), f32, dev):
+        _refuse(h, mean=(mean, (T,), f32))
+    if weight is not None and not _fits(weight, (D,), dt, dev):
+        _refuse(h, weight=(weight, (D,), dt))
+    if dh is not None and not _fits(dh, shape, dt, dev):
+        _refuse(h, dh=(dh, shape, dt))
+    wanted = ["dx"]
     if weight is not None:
-        _expect("weight", weight, (D,), h.dtype)
-    if dh is not None:
-        _expect("dh", dh, (T, D), h.dtype)
-    shapes = dict(dx=((T, D), h.dtype))
-    if weight is not None:
-        shapes["dweight"] = ((D,), torch.float32)
+        wanted.append("dweight")
     if bias_grad:
-        shapes["dbias"] = ((D,), torch.float32)
-    o = dict(out or {})
+        wanted.append("dbias")
+    o = _outputs(out, wanted)
     for name, t in o.items():
-        if name not in shapes:
-            raise ValueError(f"out has no place for {name}")
-        _expect(name, t, *shapes[name])
-    _same_device(h, dict(dy=dy, rstd=rstd, mean=mean, weight=weight, dh=dh, **o))
-    _on_current_device(h)
-    for name, (shape, dtype) in shapes.items():
+        like = (shape, dt) if name == "dx" else ((D,), f32)
+        if not _fits(t, *like, dev):
+            _refuse(h, **{name: (t, *like)})
+    _on_current_device(h, dev)
+    for name in wanted:
         if name not in o:
-            o[name] = _empty(shape, dtype, h.device, stream)
-    n = 0
-    if weight is not None or bias_grad:
-        n = lib().moe_layer_norm_backward_workspace_size(T, D, _dtype_enum(h.dtype))
-        if workspace is None:
-            workspace = _empty((max(n, 256),), torch.uint8, h.device, stream)
-        _check_workspace(h, workspace, n)
-    o.setdefault("dweight", None)
-    o.setdefault("dbias", None)
-    _check(lib().moe_layer_norm_backward(_ptr(h), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dy), _ptr(dh),
-                                         _ptr(o["dx"]), _ptr(o["dweight"]), _ptr(o["dbias"]), T, D,
-                                         _dtype_enum(h.dtype), _ptr(workspace) if n else None, n,
-                                         _stream(stream)),
-           "moe_layer_norm_backward")
+            o[name] = _empty_like(h, stream) if name == "dx" else _empty(D, f32, h.device, stream)
+    n = _layer_norm_backward_bytes(T, D, dtype) if len(wanted) > 1 else 0
+    workspace = _workspace_for(h, dev, n, workspace, stream)
+    dweight, dbias = o.setdefault("dweight", None), o.setdefault("dbias", None)
+    st = lib().moe_layer_norm_backward(h.data_ptr(), _ptr(mean), rstd.data_ptr(), _ptr(weight), dy.data_ptr(),
+                                       _ptr(dh), o["dx"].data_ptr(), _ptr(dweight), _ptr(dbias), T, D, dtype,
+                                       _ptr(workspace), n, _raw_stream(stream, dev))
+    if st:
+        raise MoeError(st, "moe_layer_norm_backward")
     return o
 
 
@@ -620,27 +674,19 @@ def layer_norm_backward(h, dy, rstd, mean=None, weight=None, dh=None, bias_grad=
 NS_COEFFS = (3.4445, -4.7750, 2.0315)
 
 
-def _check_matrices(name, x, dtypes):
-    """(B, M, N) of a [M,N] or [B,M,N] tensor."""
-    if x.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {x.dtype}")
+def _check_matrices(name, x):
+    """(B, M, N) of a dense [M,N] or [B,M,N] tensor of a library dtype."""
+    _dtype_enum(x.dtype)
     if x.dim() not in (2, 3):
         raise ValueError(f"{name} must be [M,N] or [B,M,N]")
-    _expect(name, x, x.shape, x.dtype)
+    if not x.is_contiguous():
+        _refuse(x, **{name: (x, x.shape, x.dtype)})
     return (1, *x.shape) if x.dim() == 2 else tuple(x.shape)
 
 
+@functools.lru_cache(maxsize=1024)
 def newton_schulz_workspace_size(B, M, N) -> int:
     return lib().moe_newton_schulz_workspace_size(B, M, N)
-
-
-def _ns_workspace(x, B, M, N, workspace, stream):
-    n = newton_schulz_workspace_size(B, M, N)
-    if workspace is None and n:
-        workspace = _empty((n,), torch.uint8, x.device, stream)
-    if workspace is not None:
-        _check_workspace(x, workspace, n)
-    return workspace, n
 
 
 def newton_schulz(G, steps=5, coeffs=NS_COEFFS, eps=1e-7, out=None, workspace=None, stream=None):
@@ -648,17 +694,20 @@ def newton_schulz(G, steps=5, coeffs=NS_COEFFS, eps=1e-7, out=None, workspace=No
     fp32): X = G / (|G| + eps), then ``steps`` times
     X <- a X + (b A + c A A) X with A = X X^T on the shorter side and
     (a, b, c) = ``coeffs``.  ``out`` may be G."""
-    B, M, N = _check_matrices("G", G, (torch.float32, torch.bfloat16))
-    if out is not None:
-        _expect("out", out, G.shape, G.dtype)
-    _same_device(G, dict(out=out))
-    _on_current_device(G)
+    B, M, N = _check_matrices("G", G)
+    dev = G.get_device()
+    if out is not None and not _fits(out, G.shape, G.dtype, dev):
+        _refuse(G, out=(out, G.shape, G.dtype))
+    _on_current_device(G, dev)
     if out is None:
-        out = _empty(G.shape, G.dtype, G.device, stream)
-    workspace, n = _ns_workspace(G, B, M, N, workspace, stream)
+        out = _empty_like(G, stream)
+    n = newton_schulz_workspace_size(B, M, N)
+    workspace = _workspace_for(G, dev, n, workspace, stream)
     a, b, c = coeffs
-    _check(lib().moe_newton_schulz(_ptr(G), _ptr(out), B, M, N, steps, a, b, c, eps, _dtype_enum(G.dtype),
-                                   _ptr(workspace), n, _stream(stream)), "moe_newton_schulz")
+    st = lib().moe_newton_schulz(G.data_ptr(), out.data_ptr(), B, M, N, steps, a, b, c, eps,
+                                 _dtype_enum(G.dtype), _ptr(workspace), n, _raw_stream(stream, dev))
+    if st:
+        raise MoeError(st, "moe_newton_schulz")
     return out
 
 
@@ -670,20 +719,26 @@ def muon_step(W, dW, momentum, lr, beta=0.95, weight_decay=0.0, scale=None, nest
     X = newton_schulz(U).  ``scale`` defaults to sqrt(max(1, N / M)) (weights
     are [in, out] here).  ``W_bf16`` (beside an fp32 W): receives the new W in
     bf16, for the layer's calls.  Returns W."""
-    B, M, N = _check_matrices("W", W, (torch.float32, torch.bfloat16))
-    _expect("dW", dW, W.shape, torch.float32)
-    _expect("momentum", momentum, W.shape, torch.float32)
+    B, M, N = _check_matrices("W", W)
+    dev, f32 = W.get_device(), torch.float32
+    if not _fits(dW, W.shape, f32, dev):
+        _refuse(W, dW=(dW, W.shape, f32))
+    if not _fits(momentum, W.shape, f32, dev):
+        _refuse(W, momentum=(momentum, W.shape, f32))
     if W_bf16 is not None:
-        if W.dtype != torch.float32:
+        if W.dtype != f32:
             raise ValueError("W_bf16 goes with an fp32 W")
-        _expect("W_bf16", W_bf16, W.shape, torch.bfloat16)
-    _same_device(W, dict(dW=dW, momentum=momentum, W_bf16=W_bf16))
-    _on_current_device(W)
+        if not _fits(W_bf16, W.shape, torch.bfloat16, dev):
+            _refuse(W, W_bf16=(W_bf16, W.shape, torch.bfloat16))
+    _on_current_device(W, dev)
     if scale is None:
         scale = max(1.0, N / M) ** 0.5
-    workspace, n = _ns_workspace(W, B, M, N, workspace, stream)
+    n = newton_schulz_workspace_size(B, M, N)
+    workspace = _workspace_for(W, dev, n, workspace, stream)
     a, b, c = coeffs
-    _check(lib().moe_muon_step(_ptr(W), _ptr(W_bf16), _ptr(dW), _ptr(momentum), B, M, N, lr, beta,
-                               weight_decay, scale, int(nesterov), steps, a, b, c, eps,
-                               _dtype_enum(W.dtype), _ptr(workspace), n, _stream(stream)), "moe_muon_step")
+    st = lib().moe_muon_step(W.data_ptr(), _ptr(W_bf16), dW.data_ptr(), momentum.data_ptr(), B, M, N, lr, beta,
+                             weight_decay, scale, int(nesterov), steps, a, b, c, eps, _dtype_enum(W.dtype),
+                             _ptr(workspace), n, _raw_stream(stream, dev))
+    if st:
+        raise MoeError(st, "moe_muon_step")
     return W

@@ -56,8 +56,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(bf16_t v) { return __uint_as_float((uint32_t)v.bits << 16); }
-__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_one(bf16_t* p, float v) { p->bits = (uint16_t)pack_bf16(v, 0.f); }
 
 __device__ __forceinline__ void unpack(const Raw<float>& r, float* v) {
 #pragma unroll
@@ -79,33 +77,75 @@ __device__ __forceinline__ void pack(const float* v, Raw<bf16_t>& r) {
     for (int i = 0; i < 4; ++i) r.w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
 }
 
-// `left` elements remain from p: a whole vector, the tail's elements, or
-// nothing (left <= 0); what is not there reads as zero.
 template <typename T>
-__device__ __forceinline__ Raw<T> load_raw(const T* p, int left) {
+struct __attribute__((packed, aligned(sizeof(T)))) Raw2 {
+    uint32_t w[2];
+};
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Raw1 {
+    uint32_t w;
+};
+
+// `left` elements of the row remain from p: a whole vector, its tail (TAIL:
+// rows that have one), or nothing (left <= 0); what is not there reads as zero.
+// A tail is taken from the row's last 16 bytes and shifted down, one load like
+// any other; only a row shorter than a vector (SHORT: rows that may be) has no
+// such 16 bytes and reads its elements, each at a place that exists.
+template <bool TAIL, bool SHORT, typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p, int left, int D) {
     constexpr int VEC = vec_of<T>();
     Raw<T> r = {{0, 0, 0, 0}};
-    if (left >= VEC) {
-        r = *(const Raw<T>*)p;
-    } else if (left > 0) {
-        float v[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = i < left ? to_float(p[i]) : 0.f;
-        pack(v, r);
+    if constexpr (!TAIL) {
+        if (left > 0) r = *(const Raw<T>*)p;
+        return r;
     }
+    if (left <= 0) return r;
+    if constexpr (SHORT) {
+        if (D < VEC) {
+            float v[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = to_float(p[i < left ? i : 0]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = i < left ? v[i] : 0.f;
+            pack(v, r);
+            return r;
+        }
+    }
+    const int over = left < VEC ? VEC - left : 0, bits = over * (int)sizeof(T) * 8;
+    r = *(const Raw<T>*)(p - over);
+    uint64_t lo = r.w[0] | (uint64_t)r.w[1] << 32, hi = r.w[2] | (uint64_t)r.w[3] << 32;
+    if (bits >= 64) {
+        lo = hi;
+        hi = 0;
+    }
+    const int b = bits & 63;
+    lo = lo >> b | (hi << 1) << (63 - b);
+    hi >>= b;
+    r.w[0] = (uint32_t)lo;
+    r.w[1] = (uint32_t)(lo >> 32);
+    r.w[2] = (uint32_t)hi;
+    r.w[3] = (uint32_t)(hi >> 32);
     return r;
 }
-template <typename T>
+// Four elements, two and one for the tail.
+template <bool TAIL, typename T>
 __device__ __forceinline__ void store_vec(T* p, int left, const float* v) {
     constexpr int VEC = vec_of<T>();
-    if (left >= VEC) {
-        Raw<T> r;
-        pack(v, r);
+    Raw<T> r;
+    pack(v, r);
+    if (TAIL ? left >= VEC : left > 0) {
         *(Raw<T>*)p = r;
+        return;
+    }
+    if (!TAIL || left <= 0) return;
+    if constexpr (sizeof(T) == 4) {
+        if (left & 2) *(Raw2<T>*)p = {{r.w[0], r.w[1]}};
+        if (left & 1) *(uint32_t*)(p + (left & 2)) = left & 2 ? r.w[2] : r.w[0];
     } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            if (i < left) store_one(p + i, v[i]);
+        if (left & 4) *(Raw2<T>*)p = {{r.w[0], r.w[1]}};
+        const uint32_t w0 = left & 4 ? r.w[2] : r.w[0], w1 = left & 4 ? r.w[3] : r.w[1];
+        if (left & 2) *(Raw1<T>*)(p + (left & 4)) = {w0};
+        if (left & 1) p[left & 6].bits = (uint16_t)(left & 2 ? w1 : w0);
     }
 }
 
@@ -142,7 +182,7 @@ struct FwdArgs {
     float eps;
 };
 
-template <typename T, int LANES, int NV>
+template <typename T, int LANES, int NV, bool TAIL>
 __global__ __launch_bounds__(threads_of<LANES>()) void norm_forward_kernel(const FwdArgs a) {
     constexpr int VEC = vec_of<T>(), NT = threads_of<LANES>(), ROWS = NT / LANES;
     __shared__ float red[2][LANES > 64 ? LANES / 64 : 1];
@@ -152,12 +192,17 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_forward_kernel(const
     // vectors before a lane's last are whole: the last, partial or absent
     // vector of a row falls to the last one of some lanes
     auto left = [&](int i) { return i < NV - 1 ? VEC : a.D - col[i]; };
+    auto load = [&](const void* base, int64_t at, int i) {
+        const T* p = (const T*)base + at + col[i];
+        if (i < NV - 1) return *(const Raw<T>*)p;
+        return load_raw<TAIL, LANES == 8 && NV == 1>(p, left(i), a.D);
+    };
     Raw<T> w[NV], b[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         col[i] = (lane + i * LANES) * VEC;
-        if (a.w) w[i] = load_raw((const T*)a.w + col[i], left(i));
-        if (a.b) b[i] = load_raw((const T*)a.b + col[i], left(i));
+        if (a.w) w[i] = load(a.w, 0, i);
+        if (a.b) b[i] = load(a.b, 0, i);
     }
     // rows of a workgroup-wide LANES advance together (one row per workgroup),
     // so every thread reaches the barriers of row_sum
@@ -167,10 +212,10 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_forward_kernel(const
         float v[NV][VEC];
         Raw<T> rx[NV], rr[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) rx[i] = load_raw((const T*)a.x + at + col[i], left(i));
+        for (int i = 0; i < NV; ++i) rx[i] = load(a.x, at, i);
         if (a.r) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) rr[i] = load_raw((const T*)a.r + at + col[i], left(i));
+            for (int i = 0; i < NV; ++i) rr[i] = load(a.r, at, i);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -184,7 +229,7 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_forward_kernel(const
                 Raw<T> s;
                 pack(v[i], s);
                 unpack(s, v[i]);
-                store_vec((T*)a.h + at + col[i], left(i), v[i]);
+                store_vec<TAIL>((T*)a.h + at + col[i], left(i), v[i]);
             }
         }
         float mean = 0.f;
@@ -226,7 +271,7 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_forward_kernel(const
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) v[i][e] += u[e];
             }
-            store_vec((T*)a.y + at + col[i], left(i), v[i]);
+            store_vec<TAIL>((T*)a.y + at + col[i], left(i), v[i]);
         }
     }
 }
@@ -240,7 +285,7 @@ struct BwdArgs {
     int D;
 };
 
-template <typename T, int LANES, int NV>
+template <typename T, int LANES, int NV, bool TAIL>
 __global__ __launch_bounds__(threads_of<LANES>()) void norm_backward_kernel(const BwdArgs a) {
     constexpr int VEC = vec_of<T>(), NT = threads_of<LANES>(), ROWS = NT / LANES;
     constexpr int WAVES = NT / 64, COLS = LANES * NV * VEC;
@@ -252,61 +297,85 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_backward_kernel(cons
     // vectors before a lane's last are whole: the last, partial or absent
     // vector of a row falls to the last one of some lanes
     auto left = [&](int i) { return i < NV - 1 ? VEC : a.D - col[i]; };
+    auto load = [&](const void* base, int64_t at, int i) {
+        const T* p = (const T*)base + at + col[i];
+        if (i < NV - 1) return *(const Raw<T>*)p;
+        return load_raw<TAIL, LANES == 8 && NV == 1>(p, left(i), a.D);
+    };
     Raw<T> w[NV];
     float dw[NV][VEC], db[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         col[i] = (lane + i * LANES) * VEC;
-        if (a.w) w[i] = load_raw((const T*)a.w + col[i], left(i));
+        w[i] = a.w ? load(a.w, 0, i) : Raw<T>{};
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dw[i][e] = db[i][e] = 0.f;
     }
+    // z and g stay in fp32 between the sums and their use; rows wider than 256
+    // lanes hold form them twice from the packed row, in half the registers
+    constexpr bool KEEP = LANES <= 256;
     for (int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES; t < a.T;
          t += (int64_t)gridDim.x * ROWS) {
         const int64_t at = t * a.D;
         Raw<T> rh[NV], ry[NV], rd[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            rh[i] = load_raw((const T*)a.h + at + col[i], left(i));
-            ry[i] = load_raw((const T*)a.dy + at + col[i], left(i));
+            rh[i] = load(a.h, at, i);
+            ry[i] = load(a.dy, at, i);
         }
         if (a.dh) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) rd[i] = load_raw((const T*)a.dh + at + col[i], left(i));
+            for (int i = 0; i < NV; ++i) rd[i] = load(a.dh, at, i);
         }
         const float mean = a.mean ? a.mean[t] : 0.f, rstd = a.rstd[t];
-        float z[NV][VEC], g[NV][VEC];
+        auto values = [&](int i, float* dy, float* z, float* g) {
+            unpack(rh[i], z);
+            unpack(ry[i], dy);
+            unpack(w[i], g);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                z[e] = (z[e] - mean) * rstd;
+                g[e] = a.w ? g[e] * dy[e] : dy[e];
+            }
+        };
+        float z[KEEP ? NV : 1][VEC], g[KEEP ? NV : 1][VEC];
         float sg = 0.f, sgz = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            unpack(rh[i], z[i]);
-            unpack(ry[i], g[i]);
-            float u[VEC];
-            if (a.w) unpack(w[i], u);
+            constexpr int one = KEEP ? 1 : 0;
+            float dy[VEC], *zi = z[i * one], *gi = g[i * one];
+            values(i, dy, zi, gi);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 // past the row's end dy is zero, and so is every sum's share
-                z[i][e] = (z[i][e] - mean) * rstd;
-                dw[i][e] = fmaf(g[i][e], z[i][e], dw[i][e]);
-                db[i][e] += g[i][e];
-                if (a.w) g[i][e] *= u[e];
-                sg += g[i][e];
-                sgz = fmaf(g[i][e], z[i][e], sgz);
+                dw[i][e] = fmaf(dy[e], zi[e], dw[i][e]);
+                db[i][e] += dy[e];
+                sg += gi[e];
+                sgz = fmaf(gi[e], zi[e], sgz);
             }
         }
         sg = row_sum<LANES>(sg, red[0]);
         sgz = row_sum<LANES>(sgz, red[1]);
+        if constexpr (!KEEP) {
+            // the packed values stand for new ones: nothing unpacked is carried over
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) asm volatile("" : "+v"(rh[i].w[k]), "+v"(ry[i].w[k]), "+v"(w[i].w[k]));
+        }
         const float mg = a.mean ? sg * inv_d : 0.f, mgz = sgz * inv_d;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float u[VEC];
+            constexpr int one = KEEP ? 1 : 0;
+            float dy[VEC], u[VEC], *zi = z[i * one], *gi = g[i * one];
+            if constexpr (!KEEP) values(i, dy, zi, gi);
             if (a.dh) unpack(rd[i], u);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float t0 = fmaf(-z[i][e], mgz, g[i][e] - mg);
-                g[i][e] = a.dh ? fmaf(rstd, t0, u[e]) : rstd * t0;
+                const float t0 = fmaf(-zi[e], mgz, gi[e] - mg);
+                gi[e] = a.dh ? fmaf(rstd, t0, u[e]) : rstd * t0;
             }
-            store_vec((T*)a.dx + at + col[i], left(i), g[i]);
+            store_vec<TAIL>((T*)a.dx + at + col[i], left(i), gi);
         }
     }
     if (!a.part) return;
@@ -348,7 +417,7 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_backward_kernel(cons
 
 // dweight / dbias: column sums of the [rows, D] partials, one workgroup per
 // SUM_COLS columns of one of the two, SUM_SLICES threads per column.
-constexpr int SUM_COLS = 32, SUM_SLICES = 16;
+constexpr int SUM_COLS = 32, SUM_SLICES = 32;
 __global__ __launch_bounds__(SUM_COLS * SUM_SLICES) void norm_partial_sum_kernel(
     const float* __restrict__ part, int rows, int D, float* __restrict__ dw, float* __restrict__ db) {
     __shared__ float s[SUM_SLICES][SUM_COLS];
@@ -359,7 +428,7 @@ __global__ __launch_bounds__(SUM_COLS * SUM_SLICES) void norm_partial_sum_kernel
     const int c = blockIdx.x * SUM_COLS + cl;
     float v = 0.f;
     if (c < D) {
-#pragma unroll 8
+#pragma unroll 16
         for (int r = sl; r < rows; r += SUM_SLICES) v += p[(int64_t)r * D + c];
     }
     s[sl][cl] = v;
@@ -380,12 +449,15 @@ constexpr size_t kAlign = 256;
 struct Shape {
     int lanes, nv;
 };
-// Lanes per row and 16-byte vectors per lane: at most four vectors a lane
-// (their fp32 copies and, in the backward, their gradient sums stay in
-// registers), the fewest lanes that hold the row.
+// Lanes per row and 16-byte vectors per lane: the fewest lanes that hold the
+// row in 24 bf16 or 16 fp32 elements each.  Their fp32 copies and, in the
+// backward, their gradient sums stay in registers; with a fourth bf16 vector
+// the backward has one wavefront a SIMD (4096 x 777: 24 us instead of 16).
 Shape shape_of(int D, moe_dtype dt) {
-    const int vec = dt == MOE_BF16 ? 8 : 4, nvec = (D + vec - 1) / vec;
-    const int lanes = nvec <= 32 ? 8 : nvec <= 128 ? 32 : nvec <= 256 ? 64 : nvec <= 1024 ? 256 : 1024;
+    const int vec = dt == MOE_BF16 ? 8 : 4, most = dt == MOE_BF16 ? 3 : 4, nvec = (D + vec - 1) / vec;
+    int lanes = 1024;
+    for (int l : {256, 64, 32, 8})
+        if (nvec <= l * most) lanes = l;
     return {lanes, (nvec + lanes - 1) / lanes};
 }
 int threads_for(int lanes) { return lanes > 256 ? lanes : 256; }
@@ -406,43 +478,47 @@ moe_status check_sizes(int64_t T, int D, moe_dtype dt) {
     return MOE_OK;
 }
 
-// Calls f<LANES, NV>() for the shape; only the pairs that shape_of gives.
-template <typename F>
-void dispatch(Shape p, F&& f) {
-    auto nv = [&](auto lanes, auto least) {
-        constexpr int N = decltype(least)::value;
-        if constexpr (N <= 1)
-            if (p.nv == 1) return f(lanes, std::integral_constant<int, 1>{});
-        if constexpr (N <= 2)
-            if (p.nv == 2) return f(lanes, std::integral_constant<int, 2>{});
-        if (p.nv == 3) return f(lanes, std::integral_constant<int, 3>{});
-        f(lanes, std::integral_constant<int, 4>{});
+// Calls f(LANES, NV, TAIL) for the shape, of the values that shape_of gives.
+template <typename T, typename F>
+void dispatch(Shape p, int D, F&& f) {
+    using std::integral_constant;
+    constexpr int most = sizeof(T) == 2 ? 3 : 4;
+    // NV from the least that the next fewer lanes leave to `most` (of kMaxD
+    // elements, where that is less)
+    auto nv = [&](auto lanes, auto low) {
+        constexpr int longest = kMaxD / vec_of<T>() / decltype(lanes)::value;
+        constexpr int top = longest < most ? longest : most;
+        auto at = [&](auto self, auto n) -> void {
+            if (p.nv == n.value) {
+                if (D % vec_of<T>()) return f(lanes, n, std::true_type{});
+                return f(lanes, n, std::false_type{});
+            }
+            if constexpr (n.value < top) self(self, integral_constant<int, n.value + 1>{});
+        };
+        at(at, low);
     };
     switch (p.lanes) {
-        case 8: return nv(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-        case 32: return nv(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
-        case 64: return nv(std::integral_constant<int, 64>{}, std::integral_constant<int, 3>{});
-        case 256: return nv(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-        default: return nv(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+        case 8: return nv(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+        case 32: return nv(integral_constant<int, 32>{}, integral_constant<int, most * 8 / 32 + 1>{});
+        case 64: return nv(integral_constant<int, 64>{}, integral_constant<int, most * 32 / 64 + 1>{});
+        case 256: return nv(integral_constant<int, 256>{}, integral_constant<int, most * 64 / 256 + 1>{});
+        default: return nv(integral_constant<int, 1024>{}, integral_constant<int, most * 256 / 1024 + 1>{});
     }
 }
 
 template <typename T>
 hipError_t launch_forward(const FwdArgs& a, Shape p, unsigned grid, hipStream_t s) {
-    dispatch(p, [&](auto lanes, auto nv) {
-        constexpr int L = decltype(lanes)::value, N = decltype(nv)::value;
-        // a row of kMaxD elements of two bytes has two vectors a thread at most
-        if constexpr (sizeof(T) == 4 || L < 1024 || N <= 2)
-            norm_forward_kernel<T, L, N><<<grid, threads_of<L>(), 0, s>>>(a);
+    dispatch<T>(p, a.D, [&](auto lanes, auto nv, auto tail) {
+        constexpr int L = decltype(lanes)::value;
+        norm_forward_kernel<T, L, decltype(nv)::value, decltype(tail)::value><<<grid, threads_of<L>(), 0, s>>>(a);
     });
     return hipGetLastError();
 }
 template <typename T>
 hipError_t launch_backward(const BwdArgs& a, Shape p, unsigned grid, hipStream_t s) {
-    dispatch(p, [&](auto lanes, auto nv) {
-        constexpr int L = decltype(lanes)::value, N = decltype(nv)::value;
-        if constexpr (sizeof(T) == 4 || L < 1024 || N <= 2)
-            norm_backward_kernel<T, L, N><<<grid, threads_of<L>(), 0, s>>>(a);
+    dispatch<T>(p, a.D, [&](auto lanes, auto nv, auto tail) {
+        constexpr int L = decltype(lanes)::value;
+        norm_backward_kernel<T, L, decltype(nv)::value, decltype(tail)::value><<<grid, threads_of<L>(), 0, s>>>(a);
     });
     return hipGetLastError();
 }

@@ -67,7 +67,7 @@ def test_binding_refusals():
     G = torch.zeros(2, 64, 48)
     with pytest.raises(ValueError, match="GPU"):
         gg.newton_schulz(G)
-    with pytest.raises(TypeError, match="G must be"):
+    with pytest.raises(TypeError, match="dtype"):
         gg.newton_schulz(G.half())
     with pytest.raises(ValueError, match="M,N"):
         gg.newton_schulz(G[None])
