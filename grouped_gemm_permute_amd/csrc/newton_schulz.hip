@@ -282,7 +282,12 @@ __global__ __launch_bounds__(256) void ns_split_kernel(const SplitArgs a) {
 
 // ---------------------------------------------------------------- products
 
-enum : int { GRAM = 0, SQUARE = 1, APPLY = 2, FINAL = 3 };
+// GRAM:  C = f P P^T
+// SYMM:  C = f P Q + fa P + fq Q for symmetric P and Q that commute (polynomials
+//        of one matrix), so that C is symmetric
+// APPLY: C = f P Q^T + fa X, P on the short side, Q = X^T
+// FINAL: the same into the target
+enum : int { GRAM = 0, SYMM = 1, APPLY = 2, FINAL = 3 };
 
 constexpr int BT = 128;                       // tile rows and columns
 constexpr int KB = 32;                        // K step
@@ -295,9 +300,10 @@ struct MulArgs {
     int pr, qr, K;              // padded rows of each side, reduction length
     int ti, tj;                 // tiles of each side
     float f;                    // factor of the product
-    const char* add;            // SQUARE: A; APPLY, FINAL: X
+    const char* add;            // SYMM: P; APPLY, FINAL: X
     int64_t add_stride;
     float fa;                   // factor of the addend
+    float fq;                   // SYMM: factor of Q, added too (0: not)
     float so;                   // scale of the stored planes
     char *c, *ct;               // planes out, as computed and transposed
     int64_t c_stride;
@@ -361,16 +367,22 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
     if (MODE == FINAL) both = a.swap;
     auto here = [&](int r, int c) { return r < TS && c < TS && i0 + r < a.pr && j0 + c < a.qr; };
     // all addends on their way before the first store
-    u32x4_t hi[PASSES], lo[PASSES];
+    u32x4_t hi[PASSES], lo[PASSES], qhi[PASSES], qlo[PASSES];
     if constexpr (MODE != GRAM) {
 #pragma unroll
         for (int k = 0; k < PASSES; ++k) {
             int r, c;
             place(threadIdx.x + k * NT, r, c);
             if (!here(r, c)) continue;
-            const char* p = a.add + b * a.add_stride + plane_at(i0 + r, a.qr, j0 + c);
+            const int64_t from = plane_at(i0 + r, a.qr, j0 + c);
+            const char* p = a.add + b * a.add_stride + from;
             hi[k] = *(const u32x4_t*)p;
             lo[k] = *(const u32x4_t*)(p + LO);
+            if (MODE == SYMM && a.fq != 0.f) {
+                p = a.q + b * a.q_stride + from;
+                qhi[k] = *(const u32x4_t*)p;
+                qlo[k] = *(const u32x4_t*)(p + LO);
+            }
         }
     }
 #pragma unroll
@@ -383,6 +395,7 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= a.f;
         if constexpr (MODE != GRAM) add_planes(hi[k], lo[k], a.fa, v);
+        if (MODE == SYMM && a.fq != 0.f) add_planes(qhi[k], qlo[k], a.fq, v);
         if constexpr (MODE != FINAL) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= a.so;
@@ -422,9 +435,8 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
 // of a 16-byte piece of the transposed block, which goes out as it is (64 lanes,
 // 512 consecutive bytes); for the other order the block's planes pass through 4 KiB of
 // LDS of the wavefront's own, written in the transposed order and read back with
-// the transposing read.  The addend is the second operand's block at the
-// transposed place (A is symmetric; X^T holds X's entries), in the order of
-// the accumulators.  Through an fp32 tile and two passes of 8 values a thread the
+// the transposing read.  The addends are blocks at the transposed place, of the
+// symmetric operands or of X^T, in the order of the accumulators.  Through an fp32 tile and two passes of 8 values a thread the
 // same took about 7 us of a 128-tile; this takes 2.
 template <int MODE, int NI, int NJ>
 __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0, int jb0, bool both,
@@ -433,7 +445,28 @@ __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0
     const int pb = a.pr >> 5, qb = a.qr >> 5;
     // piece q (rows 8 q .. + 7) of the transposed block; + LO for the low plane
     auto piece = [&](int q) { return (q >> 1) * HALF + (q & 1) * 512 + rl * 16 + kh * 8; };
-    auto one = [&](int i, int j, const uint2 (&hi)[4], const uint2 (&lo)[4]) {
+    struct Addend {
+        uint2 hi[4], lo[4];
+    };
+    auto fetch = [&](const char* base, int64_t stride, int i, int j, Addend& d) {
+        const int ib = min(ib0 + i, pb - 1), jb = min(jb0 + j, qb - 1);
+        const char* p = base + b * stride + ((int64_t)jb * pb + ib) * BLOCK;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            d.hi[q] = *(const uint2*)(p + piece(q));
+            d.lo[q] = *(const uint2*)(p + piece(q) + LO);
+        }
+    };
+    auto add4 = [&](const Addend& d, int q, float f, float* v) {
+        const uint32_t hw[2] = {d.hi[q].x, d.hi[q].y}, lw[2] = {d.lo[q].x, d.lo[q].y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f16x2_t h = __builtin_bit_cast(f16x2_t, hw[e >> 1]), l = __builtin_bit_cast(f16x2_t, lw[e >> 1]);
+            v[e] = fmaf(f, (float)h[e & 1] + (float)l[e & 1], v[e]);
+        }
+    };
+    const bool second = MODE == SYMM && a.fq != 0.f;
+    auto one = [&](int i, int j, const Addend& d, const Addend& dq) {
         const int ib = ib0 + i, jb = jb0 + j;
         if (ib >= pb || jb >= qb) return;
         char* ct = a.ct + b * a.c_stride + ((int64_t)jb * pb + ib) * BLOCK;
@@ -442,15 +475,8 @@ __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * a.f;
-            if constexpr (MODE != GRAM) {
-                const uint32_t hw[2] = {hi[q].x, hi[q].y}, lw[2] = {lo[q].x, lo[q].y};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const f16x2_t h = __builtin_bit_cast(f16x2_t, hw[e >> 1]);
-                    const f16x2_t l = __builtin_bit_cast(f16x2_t, lw[e >> 1]);
-                    v[e] = fmaf(a.fa, (float)h[e & 1] + (float)l[e & 1], v[e]);
-                }
-            }
+            if constexpr (MODE != GRAM) add4(d, q, a.fa, v);
+            if (second) add4(dq, q, a.fq, v);
             uint32_t oh[2], ol[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -490,21 +516,15 @@ __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0
     };
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        uint2 hi[NJ][4], lo[NJ][4];
-        if constexpr (MODE != GRAM) {
+        Addend d[NJ], dq[NJ];
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int ib = min(ib0 + i, pb - 1), jb = min(jb0 + j, qb - 1);
-                const char* add = a.q + b * a.q_stride + ((int64_t)jb * pb + ib) * BLOCK;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    hi[j][q] = *(const uint2*)(add + piece(q));
-                    lo[j][q] = *(const uint2*)(add + piece(q) + LO);
-                }
-            }
+        for (int j = 0; j < NJ; ++j) {
+            if constexpr (MODE == SYMM) fetch(a.p, a.p_stride, i, j, d[j]);
+            if constexpr (MODE == APPLY) fetch(a.q, a.q_stride, i, j, d[j]);
+            if (second) fetch(a.q, a.q_stride, i, j, dq[j]);
         }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) one(i, j, hi[j], lo[j]);
+        for (int j = 0; j < NJ; ++j) one(i, j, d[j], dq[j]);
     }
 }
 
@@ -514,7 +534,7 @@ __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0
 // compute unit: a stage has three steps to arrive.
 template <int MODE, int NS>
 __global__ __launch_bounds__(256, NS == 2 ? 2 : 1) void ns_product_kernel(const MulArgs a) {
-    constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
+    constexpr bool SYM = MODE == GRAM || MODE == SYMM;
     constexpr int TILE_BYTES = BT / 2 * TLD * 4;
     static_assert(TILE_BYTES >= 2 * OPB, "a half of the fp32 tile covers a stage");
     // separate objects, so that a read of one buffer does not wait for the
@@ -652,7 +672,7 @@ __global__ __launch_bounds__(256, NS == 2 ? 2 : 1) void ns_product_kernel(const 
 constexpr int LT = 256, LOPB = LT / 32 * BLOCK;
 template <int MODE>
 __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs a) {
-    constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
+    constexpr bool SYM = MODE == GRAM || MODE == SYMM;
     constexpr int QUAD = BT * TLD * 4;       // a quadrant of the fp32 tile
     static_assert(QUAD >= 2 * LOPB, "a quadrant covers a stage");
     __shared__ __attribute__((aligned(1024))) char st0[QUAD];
@@ -783,7 +803,7 @@ constexpr int split_waves() {
 }
 template <int MODE, int TB>
 __global__ __launch_bounds__((64 * split_waves<TB>()), 2) void ns_product_split_kernel(const MulArgs a) {
-    constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
+    constexpr bool SYM = MODE == GRAM || MODE == SYMM;
     constexpr int TS = 32 * TB, LD = TS + 1, DW = split_waves<TB>();
     __shared__ float part[DW][TS * LD];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -1039,8 +1059,9 @@ __global__ __launch_bounds__(SNT) void ns_small_kernel(const SmallArgs a) {
 constexpr size_t kAlign = 256;
 // Products of fewer 64-tiles than kSplit32 run on 32-tiles, of fewer 128-tiles
 // than kSplit64 on 64-tiles.
-constexpr int64_t kSplit32 = 128, kSplit64 = 128, kOneRound = 256, kLarge = 512;
+constexpr int64_t kSplit32 = 128, kSplit64 = 128, kOneRound = 256, kLarge = 512, kGrouped = 1;
 constexpr int kMaxSide = 32768, kMaxSteps = 64;
+constexpr int kSyms = 5;      // symmetric matrices of a call: A, A P and three of S and R
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 int pad64(int v) { return (v + 63) / 64 * 64; }
@@ -1048,7 +1069,7 @@ int pad64(int v) { return (v + 63) / 64 * 64; }
 bool is_small(int M, int N) { return (M < N ? M : N) <= SM; }
 
 struct Layout {
-    size_t part, x, xt[2], A, B, total;
+    size_t part, x, xt[2], sym[kSyms], total;
 };
 
 moe_status check_sizes(int B, int M, int N) {
@@ -1071,8 +1092,7 @@ Layout layout_of(int B, int M, int N) {
     L.x = take((size_t)B * m * n * 4);
     L.xt[0] = take((size_t)B * m * n * 4);
     L.xt[1] = take((size_t)B * m * n * 4);
-    L.A = take((size_t)B * m * m * 4);
-    L.B = take((size_t)B * m * m * 4);
+    for (size_t& at : L.sym) at = take((size_t)B * m * m * 4);
     L.total = off;
     return L;
 }
@@ -1086,14 +1106,19 @@ struct Bound {
         if (fabs(v) > best) best = fabs(v);
     }
 };
-// Bounds of a step that starts with singular values in [0, s]: of b A + c A A
-// and of the singular values after it.
-bool step_bounds(double a, double b, double c, double s, double* mid, double* next) {
-    Bound p, q;
+// Bounds of a step that starts with singular values in [0, s]: of S = b A + c A A,
+// of P = a I + S, and of the singular values after it.
+bool step_bounds(double a, double b, double c, double s, double* mid, double* whole, double* next) {
+    Bound p, w, q;
     const double y = s * s;
-    auto poly = [&](double t) { return t >= 0. && t <= y; };
-    p.at(b * y + c * y * y);
-    if (c != 0. && poly(-b / (2. * c))) p.at(-b * b / (4. * c));
+    auto inside = [&](double t) { return t >= 0. && t <= y; };
+    auto both = [&](double t) {
+        p.at(b * t + c * t * t);
+        w.at(a + b * t + c * t * t);
+    };
+    both(0.);
+    both(y);
+    if (c != 0. && inside(-b / (2. * c))) both(-b / (2. * c));
     auto f = [&](double t) { return sqrt(t) * (a + b * t + c * t * t); };
     q.at(f(y));
     if (c != 0.) {
@@ -1101,14 +1126,15 @@ bool step_bounds(double a, double b, double c, double s, double* mid, double* ne
         if (d >= 0.)
             for (int k = -1; k <= 1; k += 2) {
                 const double t = (-3. * b + k * sqrt(d)) / (10. * c);
-                if (poly(t)) q.at(f(t));
+                if (inside(t)) q.at(f(t));
             }
-    } else if (b != 0. && poly(-a / (3. * b))) {
+    } else if (b != 0. && inside(-a / (3. * b))) {
         q.at(f(-a / (3. * b)));
     }
     *mid = p.best * (1. + 1e-3);
+    *whole = w.best * (1. + 1e-3);
     *next = q.best * (1. + 1e-3);
-    return p.fine && q.fine;
+    return p.fine && w.fine && q.fine;
 }
 // The largest power of two that keeps `bound` at 2^15 at most.
 double scale_for(double bound) {
@@ -1121,7 +1147,7 @@ double scale_for(double bound) {
 // Tile of a product: 128 rows and columns, or the split kernel's 64 or 32.
 template <int MODE>
 bool launch_product(MulArgs& g, int B, hipStream_t stream) {
-    constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
+    constexpr bool SYM = MODE == GRAM || MODE == SYMM;
     auto grid = [&](int tile) {
         g.ti = (g.pr + tile - 1) / tile;
         g.tj = (g.qr + tile - 1) / tile;
@@ -1151,10 +1177,10 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     if (steps < 1 || steps > kMaxSteps) return MOE_ERR_INVALID_ARG;
     if (!(eps >= 0.) || !isfinite(eps) || !isfinite(a) || !isfinite(b) || !isfinite(c))
         return MOE_ERR_INVALID_ARG;
-    double mid[kMaxSteps], top[kMaxSteps + 1];
+    double mid[kMaxSteps], whole[kMaxSteps], top[kMaxSteps + 1];
     top[0] = 1.;
     for (int k = 0; k < steps; ++k)
-        if (!step_bounds(a, b, c, top[k], &mid[k], &top[k + 1])) return MOE_ERR_UNSUPPORTED;
+        if (!step_bounds(a, b, c, top[k], &mid[k], &whole[k], &top[k + 1])) return MOE_ERR_UNSUPPORTED;
     if (B == 0) return MOE_OK;
     (void)hipGetLastError();
     auto ok = [] { return hipGetLastError() == hipSuccess; };
@@ -1171,11 +1197,13 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     const int m = pad64(tall ? N : M), n = pad64(tall ? M : N);
     // a grid's threads are fewer than 2^32
     if ((int64_t)B * ((m + BT - 1) / BT) * ((n + BT - 1) / BT) >= 1 << 24) return MOE_ERR_UNSUPPORTED;
+    const bool grouped = (tgt.muon || tgt.out_bf16) && kGrouped && 2 * n >= 3 * m &&
+                         (int64_t)B * ((m + BT - 1) / BT) * ((n + BT - 1) / BT) >= kSplit64;
     const int nb = norm_blocks((int64_t)M * N);
     ns_norm_kernel<<<dim3(nb, B), 256, 0, stream>>>(src, (int64_t)M * N, (double*)(ws + L.part));
     if (!ok()) return MOE_ERR_HIP;
 
-    char *x = ws + L.x, *A = ws + L.A, *Bm = ws + L.B;
+    char* x = ws + L.x;
     char* xt[2] = {ws + L.xt[0], ws + L.xt[1]};
     double sx = scale_for(top[0]);
     const int Mp = pad64(M), Np = pad64(N);
@@ -1184,54 +1212,97 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     ns_split_kernel<<<dim3(Np / ST, Mp / ST, B), 256, 0, stream>>>(sp);
     if (!ok()) return MOE_ERR_HIP;
 
+    // ---- the steps, in groups of one, two or three.  A group takes X's Gram
+    // matrix A once and X once more in its end; between them
+    //   S_j = b A_j + c A_j A_j,  P_j = a I + S_j,
+    //   A_{j+1} = P_j A_j P_j = a U + U S_j with U = a A_j + A_j S_j,
+    //   P_0 .. P_j = alpha I + R_j,  R_j = a R_{j-1} + alpha' S_j + R_{j-1} S_j,
+    // all on the short side, where a I stays out of the stored planes.
+    struct Plane {
+        char* p;
+        double scale;
+    };
     const int64_t xs = (int64_t)m * n * 4, as = (int64_t)m * m * 4;
-    for (int k = 0; k < steps; ++k) {
-        const double sa = scale_for(top[k] * top[k]), sb = scale_for(mid[k]), sn = scale_for(top[k + 1]);
-        char *xc = xt[k & 1], *xn = xt[(k + 1) & 1];
-        MulArgs g = {};
+    MulArgs y = {};      // a product on the short side
+    y.p_stride = y.q_stride = y.add_stride = y.c_stride = as;
+    y.pr = y.qr = y.K = m;
+    auto symm = [&](Plane P, Plane Q, double f, double fp, double fq, Plane out) {
+        MulArgs g = y;
+        g.p = g.add = P.p;
+        g.q = Q.p;
+        g.f = (float)(f / (P.scale * Q.scale));
+        g.fa = (float)(fp / P.scale);
+        g.fq = (float)(fq / Q.scale);
+        g.so = (float)out.scale;
+        g.c = g.ct = out.p;
+        return launch_product<SYMM>(g, B, stream);
+    };
+    int turn = 0;
+    for (int k = 0; k < steps;) {
+        const int group = grouped ? ((steps - k) % 2 && steps - k > 1 ? 3 : (steps - k > 1 ? 2 : 1)) : 1;
+        Plane A = {ws + L.sym[0], scale_for(top[k] * top[k])}, U = {ws + L.sym[1], 0.};
+        // where S and R are by turns: an S may be the R of the next step
+        Plane S = {}, R = {};
+        int free_at = 0;
+        auto fresh = [&](double scale) {
+            for (;; free_at = (free_at + 1) % 3) {
+                char* p = ws + L.sym[2 + free_at];
+                if (p != S.p && p != R.p) return Plane{p, scale};
+            }
+        };
+        MulArgs g = y;
         g.p = g.q = x;
         g.p_stride = g.q_stride = xs;
-        g.pr = g.qr = m;
         g.K = n;
         g.f = (float)(1. / (sx * sx));
-        g.so = (float)sa;
-        g.c = g.ct = A;
-        g.c_stride = as;
+        g.so = (float)A.scale;
+        g.c = g.ct = A.p;
         if (!launch_product<GRAM>(g, B, stream)) return MOE_ERR_HIP;
-        MulArgs q = g;
-        q.p = q.q = q.add = A;
-        q.p_stride = q.q_stride = q.add_stride = as;
-        q.K = m;
-        q.f = (float)(c / (sa * sa));
-        q.fa = (float)(b / sa);
-        q.so = (float)sb;
-        q.c = q.ct = Bm;
-        if (!launch_product<SQUARE>(q, B, stream)) return MOE_ERR_HIP;
-        MulArgs y = {};
-        y.p = Bm;
-        y.p_stride = as;
-        y.pr = m;
-        y.q = xc;
-        y.q_stride = xs;
-        y.qr = n;
-        y.K = m;
-        y.f = (float)(1. / (sb * sx));
-        y.fa = (float)(a / sx);
-        y.add = x;
-        y.add_stride = y.c_stride = xs;
-        if (k + 1 < steps) {
-            y.so = (float)sn;
-            y.c = x;
-            y.ct = xn;
-            if (!launch_product<APPLY>(y, B, stream)) return MOE_ERR_HIP;
-        } else {
-            y.swap = tall;
-            y.M = M;
-            y.N = N;
-            y.t = tgt;
-            if (!launch_product<FINAL>(y, B, stream)) return MOE_ERR_HIP;
+        double alpha = 1., bound = 1.;
+        for (int j = 0; j < group; ++j) {
+            const int at = k + j;
+            S = Plane{};
+            S = fresh(scale_for(mid[at]));
+            if (!symm(A, A, c, b, 0., S)) return MOE_ERR_HIP;
+            bound *= whole[at];
+            if (j == 0) {
+                R = S;
+            } else {
+                const Plane next = fresh(scale_for(bound + fabs(alpha * a)));
+                if (!symm(R, S, 1., a, alpha, next)) return MOE_ERR_HIP;
+                R = next;
+            }
+            alpha *= a;
+            if (j + 1 < group) {
+                U.scale = scale_for(top[at] * top[at + 1]);
+                const Plane next = {A.p, scale_for(top[at + 1] * top[at + 1])};
+                if (!symm(A, S, 1., a, 0., U) || !symm(U, S, 1., a, 0., next)) return MOE_ERR_HIP;
+                A = next;
+            }
         }
-        sx = sn;
+        k += group;
+        MulArgs z = y;
+        z.p = R.p;
+        z.q = xt[turn];
+        z.q_stride = z.add_stride = z.c_stride = xs;
+        z.qr = n;
+        z.add = x;
+        z.f = (float)(1. / (R.scale * sx));
+        z.fa = (float)(alpha / sx);
+        if (k < steps) {
+            sx = scale_for(top[k]);
+            turn ^= 1;
+            z.so = (float)sx;
+            z.c = x;
+            z.ct = xt[turn];
+            if (!launch_product<APPLY>(z, B, stream)) return MOE_ERR_HIP;
+        } else {
+            z.swap = tall;
+            z.M = M;
+            z.N = N;
+            z.t = tgt;
+            if (!launch_product<FINAL>(z, B, stream)) return MOE_ERR_HIP;
+        }
     }
     return MOE_OK;
 }

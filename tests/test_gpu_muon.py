@@ -25,6 +25,12 @@ LARGE = [(1, 33, 33), (2, 40, 100), (1, 64, 64), (1, 65, 127), (1, 129, 128), (2
          (3, 128, 256), (1, 300, 1000), (1, 1000, 333), (2, 192, 192), (1, 257, 2050), (5, 768, 96)]
 
 
+# Batches that reach every tile of the products: 64 (split), 128 in one round and more, 256 (also with
+# tiles that end past the padded matrix), and, for bf16, steps in groups (long sides of 1.5 times the short).
+BATCHES = [(3, 500, 700), (6, 700, 500), (8, 256, 1024), (9, 600, 1300), (24, 520, 330), (150, 300, 300),
+           (150, 180, 460), (16, 1024, 1024)]
+
+
 def gradient(B, M, N, seed, size=1e-3):
     g = torch.Generator().manual_seed(seed)
     r = max(1, min(M, N) // 16)
@@ -73,6 +79,60 @@ def test_newton_schulz(B, M, N, dtype):
     out = gg.newton_schulz(G.cuda())
     torch.cuda.synchronize()
     check(out, G, dtype, what=f"{B}x{M}x{N}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,M,N", BATCHES)
+def test_newton_schulz_batches(B, M, N, dtype):
+    """The reference of all matrices in 64 bits on the GPU, and the fp32 error too."""
+    g = torch.Generator(device="cuda").manual_seed(B + M)
+    G = 1e-3 * torch.randn(B, M, N, generator=g, device="cuda")
+    G[:, : M // 8] *= 5
+    G = G.to(dtype)
+    for steps in (5, 4):
+        say(f"newton_schulz {B}x{M}x{N} {dtype} steps{steps}")
+        out = gg.newton_schulz(G, steps=steps).double()
+        torch.cuda.synchronize()
+        want = iterate(G, steps, MUON, 1e-7, torch.float64)
+        f32 = iterate(G.cpu(), steps, MUON, 1e-7, torch.float32).double().cuda() if B * M * N < 3e6 else None
+        norm = lambda t: t.square().sum((-1, -2)).sqrt()  # noqa: E731
+        # where the fp32 run on the CPU takes too long: its error is at least 2 u |X| (X's last rounding and a product's)
+        most = 8 * (norm(f32 - want) if f32 is not None else 30 * U * norm(want)) + 16 * U * norm(want)
+        if dtype == torch.bfloat16:
+            most = most + 2.0 ** -8 * norm(want)
+        assert (norm(out - want) <= most).all(), f"{(norm(out - want) / norm(want)).max()}"
+        worst = (out - want).abs().amax((-1, -2)) / want.abs().amax((-1, -2))
+        assert float(worst.max()) < (2.0 ** -8 * 1.01 if dtype == torch.bfloat16 else 0) + 1e-4
+
+
+@pytest.mark.parametrize("B,M,N,dtype", [(16, 256, 512, torch.float32), (16, 520, 256, torch.bfloat16),
+                                         (3, 512, 1500, torch.float32)])
+def test_muon_step_batches(B, M, N, dtype):
+    """Steps in groups (long sides of 1.5 times the short, enough tiles): the update against 64 bits."""
+    lr, beta, scale = 0.02, 0.95, 1.3
+    g = torch.Generator(device="cuda").manual_seed(M)
+    W0 = (torch.randn(B, M, N, generator=g, device="cuda") / M ** 0.5).to(dtype)
+    dW = 1e-3 * torch.randn(B, M, N, generator=g, device="cuda")
+    mom = 5e-3 * torch.randn(B, M, N, generator=g, device="cuda")
+    W = torch.zeros_like(W0)                  # the update alone, without W's own rounding above it
+    say(f"muon_step {B}x{M}x{N} {dtype}")
+    m0 = mom.clone()
+    gg.muon_step(W, dW, mom, lr, beta=beta, scale=scale)
+    torch.cuda.synchronize()
+    f = lambda v: torch.tensor(v, dtype=torch.float32).double().item()  # noqa: E731
+    u = dW.double() + f(beta) * mom.double()
+    X = iterate(u, 5, MUON, 1e-7, torch.float64)
+    x32 = iterate(u[:2].float().cpu(), 5, MUON, 1e-7, torch.float32).double().cuda()
+    off = 8 * (x32 - X[:2]).square().mean().sqrt() + 16 * U * X.square().mean().sqrt()
+    want = -f(lr) * f(scale) * X
+    rms = (W.double() - want).square().mean().sqrt()
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else U
+    assert rms <= lr * scale * off + (half + 4 * U) * want.square().mean().sqrt()
+    W = W0.clone()
+    gg.muon_step(W, dW, m0, lr, beta=beta, scale=scale)
+    assert torch.equal(m0, mom)
+    assert ((W.double() - (W0.double() + want)).abs() <= half * (W0.double() + want).abs() * 1.01 + 4 * U * W0.double().abs()
+            + 1e-4 * want.abs().max()).all()
 
 
 @pytest.mark.parametrize("M,N", [(24, 90), (90, 24), (96, 160), (160, 96)])
