@@ -791,57 +791,41 @@ __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs 
     }
 }
 
-// The same product for grids that would leave most of the GPU idle: tiles of
-// 32 TB rows and columns (TB = 1, 2), whose eight wavefronts share out the K
-// steps among them and add their sums through LDS, so that a product of a
-// few hundred rows runs on hundreds of compute units and each wavefront's
-// chain is an eighth as long.  Operands go from memory straight to registers:
-// nothing in a tile is read twice, so LDS would only add its latency.
-template <int TB>
-constexpr int split_waves() {
-    return TB == 1 ? 8 : 4;
-}
-template <int MODE, int TB>
-__global__ __launch_bounds__((64 * split_waves<TB>()), 2) void ns_product_split_kernel(const MulArgs a) {
+// The same product for grids that would leave most of the GPU idle: 32 x 32
+// tiles whose eight wavefronts share out the K steps among them and add their
+// sums through LDS, so that a product of a few hundred rows runs on hundreds of
+// compute units and a wavefront's chain of loads is an eighth as long.  Operands go
+// from memory straight to registers: nothing in a tile is read twice, so LDS
+// would only add its latency.
+constexpr int DT = 32, DW = 8;
+template <int MODE>
+__global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulArgs a) {
     constexpr bool SYM = MODE == GRAM || MODE == SYMM;
-    constexpr int TS = 32 * TB, LD = TS + 1, DW = split_waves<TB>();
-    __shared__ float part[DW][TS * LD];
+    constexpr int LD = DT + 1;
+    __shared__ float part[DW][DT * LD];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int b, ti, tj;
     tile_of<SYM>(a, b, ti, tj);
-    const int i0 = ti * TS, j0 = tj * TS;
     const int rl = lane & 31, kh = lane >> 5;
-
     const int KT = a.K / KB;
-    const char *pp[TB], *qp[TB];
-#pragma unroll
-    for (int i = 0; i < TB; ++i) {
-        pp[i] = a.p + b * a.p_stride + (int64_t)((i0 >> 5) + i) * KT * BLOCK;
-        qp[i] = a.q + b * a.q_stride + (int64_t)((j0 >> 5) + i) * KT * BLOCK;
-    }
+    const char* pp = a.p + b * a.p_stride + (int64_t)ti * KT * BLOCK;
+    const char* qp = a.q + b * a.q_stride + (int64_t)tj * KT * BLOCK;
     const uint32_t at16 = lane * 16;
     struct Frags {
-        f16x8_t ph[2][TB], pl[2][TB], qh[2][TB], ql[2][TB];   // [k16 slice][block]
+        f16x8_t ph[2][1], pl[2][1], qh[2][1], ql[2][1];   // [k16 slice]
     };
     auto load = [&](int kt, Frags& f) {
+        const char *pb = pp + (int64_t)kt * BLOCK, *qb = qp + (int64_t)kt * BLOCK;
 #pragma unroll
-        for (int i = 0; i < TB; ++i) {
-            const char *pb = pp[i] + (int64_t)kt * BLOCK, *qb = qp[i] + (int64_t)kt * BLOCK;
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                f.ph[ks][i] = *(const f16x8_t*)(pb + at16 + ks * HALF);
-                f.pl[ks][i] = *(const f16x8_t*)(pb + at16 + ks * HALF + LO);
-                f.qh[ks][i] = *(const f16x8_t*)(qb + at16 + ks * HALF);
-                f.ql[ks][i] = *(const f16x8_t*)(qb + at16 + ks * HALF + LO);
-            }
+        for (int ks = 0; ks < 2; ++ks) {
+            f.ph[ks][0] = *(const f16x8_t*)(pb + at16 + ks * HALF);
+            f.pl[ks][0] = *(const f16x8_t*)(pb + at16 + ks * HALF + LO);
+            f.qh[ks][0] = *(const f16x8_t*)(qb + at16 + ks * HALF);
+            f.ql[ks][0] = *(const f16x8_t*)(qb + at16 + ks * HALF + LO);
         }
     };
-    f32x16_t acc[TB][TB];
-#pragma unroll
-    for (int i = 0; i < TB; ++i)
-#pragma unroll
-        for (int j = 0; j < TB; ++j) acc[i][j] = f32x16_t{};
+    f32x16_t acc[1][1] = {{f32x16_t{}}};
     auto compute = [&](const Frags& f) {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) mul3(acc, f.ph[ks], f.pl[ks], f.qh[ks], f.ql[ks]);
@@ -859,12 +843,7 @@ __global__ __launch_bounds__((64 * split_waves<TB>()), 2) void ns_product_split_
         }
     }
 #pragma unroll
-    for (int i = 0; i < TB; ++i)
-#pragma unroll
-        for (int j = 0; j < TB; ++j)
-#pragma unroll
-            for (int g = 0; g < 16; ++g)
-                part[wave][(32 * i + acc_row(g, kh)) * LD + 32 * j + rl] = acc[i][j][g];
+    for (int g = 0; g < 16; ++g) part[wave][acc_row(g, kh) * LD + rl] = acc[0][0][g];
     __syncthreads();
     // a thread's results replace the first partial sums of its own entries
     auto at = [&](int r, int c) -> float& { return part[0][r * LD + c]; };
@@ -876,7 +855,7 @@ __global__ __launch_bounds__((64 * split_waves<TB>()), 2) void ns_product_split_
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += part[w][r * LD + c + e];
     };
-    epilogue<MODE, TS, 64 * DW>(a, b, i0, j0, !SYM || ti != tj, sum8, at);
+    epilogue<MODE, DT, 64 * DW>(a, b, ti * DT, tj * DT, !SYM || ti != tj, sum8, at);
 }
 
 // ------------------------------------------------- short sides of up to 32
@@ -1057,9 +1036,6 @@ __global__ __launch_bounds__(SNT) void ns_small_kernel(const SmallArgs a) {
 // ---------------------------------------------------------------- host side
 
 constexpr size_t kAlign = 256;
-// Products of fewer 64-tiles than kSplit32 run on 32-tiles, of fewer 128-tiles
-// than kSplit64 on 64-tiles.
-constexpr int64_t kSplit32 = 128, kSplit64 = 128, kOneRound = 256, kLarge = 512, kGrouped = 1;
 constexpr int kMaxSide = 32768, kMaxSteps = 64;
 constexpr int kSyms = 5;      // symmetric matrices of a call: A, A P and three of S and R
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
@@ -1144,7 +1120,19 @@ double scale_for(double bound) {
     return s;
 }
 
-// Tile of a product: 128 rows and columns, or the split kernel's 64 or 32.
+// Which tile a product runs on, from the number of tiles n and of K steps k
+// (256 compute units; times in us of one launch, measured over 40 products of
+// 1 to 64 matrices, short sides 128 to 4096, k 4 to 128):
+//  * 256: one workgroup a unit, 2.0 to 2.6 a step.  It wins where its rounds of 256
+//    are well filled: full, or 160 of 256 with k >= 48, or 128 with k >= 96
+//    (k = 128: 254 us against 286 with 160 tiles, 231 against 247 with 136;
+//    k = 32: 77 against 72 with 160; k = 24: 135 against 119 with 288).
+//  * 32 split over K: about 4 + n (0.0022 + 0.0003 k) (k = 24: 10.7 with 600 tiles, 49
+//    with 4800), against 8 + k (0.45 + 0.0009 n) for up to 256 tiles of 128
+//    (k = 24: 19 with 21 tiles, 23 with 168): the smaller of the two.
+//  * 128: the ring of four stages in one round of 256 with k >= 32 (84 us
+//    against 92 with 144 tiles, k = 128), else two stages and two workgroups
+//    a unit (12 against 13 with 192 tiles, k = 8; 74 against 88 with 272, k = 64).
 template <int MODE>
 bool launch_product(MulArgs& g, int B, hipStream_t stream) {
     constexpr bool SYM = MODE == GRAM || MODE == SYMM;
@@ -1153,18 +1141,17 @@ bool launch_product(MulArgs& g, int B, hipStream_t stream) {
         g.tj = (g.qr + tile - 1) / tile;
         return (int64_t)B * (SYM ? (int64_t)g.ti * (g.ti + 1) / 2 : (int64_t)g.ti * g.tj);
     };
-    const int64_t n32 = grid(32), n64 = grid(64), n128 = grid(BT), n256 = grid(LT);
-    if (n64 < kSplit32) {
-        grid(32);
-        ns_product_split_kernel<MODE, 1><<<(unsigned)n32, 64 * split_waves<1>(), 0, stream>>>(g);
-    } else if (n128 < kSplit64) {
-        grid(64);
-        ns_product_split_kernel<MODE, 2><<<(unsigned)n64, 64 * split_waves<2>(), 0, stream>>>(g);
-    } else if (n256 >= kLarge) {
+    const int64_t n32 = grid(DT), n128 = grid(BT), n256 = grid(LT);
+    const int k = g.K / KB;
+    const int64_t round = n256 / ((n256 + 255) / 256);
+    if (round >= 240 || (round >= 160 && k >= 48) || (round >= 128 && k >= 96)) {
         ns_product_large_kernel<MODE><<<(unsigned)n256, 512, 0, stream>>>(g);
+    } else if (n128 <= 256 && 4. + n32 * (0.0022 + 0.0003 * k) < 8. + k * (0.45 + 0.0009 * n128)) {
+        grid(DT);
+        ns_product_split_kernel<MODE><<<(unsigned)n32, 64 * DW, 0, stream>>>(g);
     } else {
         grid(BT);
-        if (n128 <= kOneRound)
+        if (n128 <= 256 && k >= 32)
             ns_product_kernel<MODE, 4><<<(unsigned)n128, 256, 0, stream>>>(g);
         else
             ns_product_kernel<MODE, 2><<<(unsigned)n128, 256, 0, stream>>>(g);
@@ -1197,8 +1184,8 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     const int m = pad64(tall ? N : M), n = pad64(tall ? M : N);
     // a grid's threads are fewer than 2^32
     if ((int64_t)B * ((m + BT - 1) / BT) * ((n + BT - 1) / BT) >= 1 << 24) return MOE_ERR_UNSUPPORTED;
-    const bool grouped = (tgt.muon || tgt.out_bf16) && kGrouped && 2 * n >= 3 * m &&
-                         (int64_t)B * ((m + BT - 1) / BT) * ((n + BT - 1) / BT) >= kSplit64;
+    const bool grouped = (tgt.muon || tgt.out_bf16) && 2 * n >= 3 * m &&
+                         (int64_t)B * ((m + BT - 1) / BT) * ((n + BT - 1) / BT) >= 128;
     const int nb = norm_blocks((int64_t)M * N);
     ns_norm_kernel<<<dim3(nb, B), 256, 0, stream>>>(src, (int64_t)M * N, (double*)(ws + L.part));
     if (!ok()) return MOE_ERR_HIP;
