@@ -38,6 +38,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -860,176 +862,253 @@ __global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulA
 
 // ------------------------------------------------- short sides of up to 32
 
-// One workgroup takes a whole matrix when its short side m is at most 32: A is
-// summed in fp64 straight from U, and since every step multiplies X by a
-// polynomial of A, and those commute, the steps run on the m x m side alone
-// (A <- P A P, Q <- Q P with P = a I + b A + c A A, in fp64, whose rounding the
-// growth of small singular values leaves far below fp32's), and U is read a
-// second time for X = Q U / (|U| + eps).  One launch where the general path
-// takes two and three for each step.
-constexpr int SM = 32, SNT = 512, SL = 128, SPS = SM + 4;
+// With a short side m of at most 32 nothing is worth planes or tiles: since every
+// step multiplies X by a polynomial of A, and those commute, the steps run on
+// the m x m side alone,
+//   A <- P A P,  Q <- Q P  with P = a I + b A + c A A,
+// in fp64 (whose rounding the growth of small singular values leaves far below
+// fp32's), and X = Q U / (|U| + eps), |U|^2 = trace(U U^T), takes U once more.
+// One workgroup sums A for a chunk of the long side; each workgroup of the second
+// launch adds the chunks' sums, runs the steps by itself and multiplies its
+// own chunk.  A matrix of one chunk takes a single launch.
+//
+// All products are fp64 matrix instructions of 16 x 16 x 4: a lane (g = lane / 16,
+// c = lane % 16) holds A[c][k] and B[k][c] and receives rows 4 v + g, column c of the
+// result in its value v.  The four instructions of a 16-block take k = 4 v + g, so
+// a result block is an operand as it stands: mfma4(X, Y) = X^T Y.  768 x 8 took
+// 23 us with fp64 vector products and a barrier for each; this takes 17.
+typedef __attribute__((ext_vector_type(4))) double f64x4_t;
+constexpr int SM = 32;
+// Columns of the long side a workgroup takes: all of up to 768 (short sides of
+// up to 16) or 256, in turns of 256 by 16 wavefronts in one launch (768 x 8:
+// 17 us a call, 19 in two launches; 1024 x 16: 24 and 20; 32 x 256: 21 and 23,
+// 32 x 512: 29 and 24); otherwise 128, one turn of 8 wavefronts, or more where that
+// would be over 64 chunks, whose sums each workgroup adds (32 x 4096: 27 us, 331
+// by one workgroup).
+int small_chunk(int M, int N) {
+    const int m = M < N ? M : N, n = M < N ? N : M;
+    if (n <= (m <= 16 ? 768 : 256)) return n;
+    return n <= 64 * 128 ? 128 : ((n + 63) / 64 + 127) / 128 * 128;
+}
+int small_chunks(int M, int N) {
+    const int n = M < N ? N : M, chunk = small_chunk(M, N);
+    return (n + chunk - 1) / chunk;
+}
+
 struct SmallArgs {
     Source s;
     Target t;
-    int M, N, steps;
+    int M, N, steps, chunk;      // chunk: columns of the long side a workgroup takes
     double a, b, c, eps;
+    double* part;                // [B][chunks][blocks][256] sums of A, blocks (0,0), (1,0), (1,1)
 };
 
-// C = P Q for symmetric m x m factors of one another's polynomials (so C is
-// symmetric), 2 x 2 entries a thread.
-__device__ __forceinline__ void small_product(const double* P, const double* Q, double* C, int m) {
-    const int nb = (m + 1) >> 1;
-    if ((int)threadIdx.x < nb * nb) {
-        const int p = 2 * (threadIdx.x / nb), q = 2 * (threadIdx.x % nb);
-        double c00 = 0., c01 = 0., c10 = 0., c11 = 0.;
-        for (int k = 0; k < m; ++k) {
-            const double p0 = P[k * SM + p], p1 = P[k * SM + p + 1];
-            const double q0 = Q[k * SM + q], q1 = Q[k * SM + q + 1];
-            c00 = fma(p0, q0, c00);
-            c01 = fma(p0, q1, c01);
-            c10 = fma(p1, q0, c10);
-            c11 = fma(p1, q1, c11);
+__device__ __forceinline__ f64x4_t mfma4(f64x4_t x, f64x4_t y, f64x4_t acc) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc = __builtin_amdgcn_mfma_f64_16x16x4f64(x[v], y[v], acc, 0, 0, 0);
+    return acc;
+}
+__device__ __forceinline__ float load1(const void* base, int64_t at, int bf16) {
+    return bf16 ? __uint_as_float((uint32_t)((const uint16_t*)base)[at] << 16) : ((const float*)base)[at];
+}
+__device__ __forceinline__ float source1(const Source& s, int64_t at, bool first) {
+    const float g = load1(s.g, at, s.g_bf16);
+    if (!s.mom) return g;
+    float m = s.mom[at];
+    if (first) s.mom[at] = m = fmaf(s.beta, m, g);
+    return s.nesterov ? fmaf(s.beta, m, g) : m;
+}
+__device__ __forceinline__ void target1(const Target& t, int64_t at, float v) {
+    if (t.muon) {
+        v = fmaf(-t.rate, v, t.keep * load1(t.out, at, t.out_bf16));
+        if (t.copy) t.copy[at] = (uint16_t)pack_bf16(v, 0.f);
+    }
+    if (t.out_bf16)
+        ((uint16_t*)t.out)[at] = (uint16_t)pack_bf16(v, 0.f);
+    else
+        ((float*)t.out)[at] = v;
+}
+
+// Block index of (i, j), i >= j.
+__device__ __forceinline__ int low_block(int i, int j) { return i + j; }
+
+// This workgroup's sum of U U^T over columns lo .. hi - 1 of the long side, NB x NB
+// blocks of 16: blocks (0,0), (1,0), (1,1) of `sum` ([blocks][256], in LDS).
+// A wavefront takes 16 columns at a time.
+template <int NB, int NT>
+__device__ __forceinline__ void small_gram(const SmallArgs& a, int lo, int hi, double* sum) {
+    constexpr int BLOCKS = NB == 1 ? 1 : 3, WAVES = NT / 64;
+    __shared__ double part[WAVES][BLOCKS][256];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
+    const bool tall = a.M > a.N;
+    const int m = tall ? a.N : a.M, n = tall ? a.M : a.N;
+    const int64_t base = (int64_t)blockIdx.y * a.M * a.N;
+    f64x4_t acc[BLOCKS];
+#pragma unroll
+    for (int k = 0; k < BLOCKS; ++k) acc[k] = f64x4_t{0., 0., 0., 0.};
+#pragma unroll 2
+    for (int l0 = lo + 16 * wave; l0 < hi; l0 += 16 * WAVES) {
+        f64x4_t u[NB];
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                // four consecutive columns a lane, so that a wide row's are one line's
+                const int p = 16 * k + c, l = l0 + 4 * g + v;
+                u[k][v] = p < m && l < hi
+                              ? (double)source1(a.s, base + (tall ? (int64_t)l * m + p : (int64_t)p * n + l), true)
+                              : 0.;
+            }
+        acc[0] = mfma4(u[0], u[0], acc[0]);
+        if constexpr (NB == 2) {
+            acc[1] = mfma4(u[1], u[0], acc[1]);
+            acc[2] = mfma4(u[1], u[1], acc[2]);
         }
-        C[p * SM + q] = c00;
-        C[p * SM + q + 1] = c01;
-        C[(p + 1) * SM + q] = c10;
-        C[(p + 1) * SM + q + 1] = c11;
+    }
+#pragma unroll
+    for (int k = 0; k < BLOCKS; ++k)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) part[wave][k][(4 * v + g) * 16 + c] = acc[k][v];
+    __syncthreads();
+    for (int e = tid; e < BLOCKS * 256; e += NT) {
+        double t = 0.;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) t += part[w][e >> 8][e & 255];
+        sum[e] = t;
     }
     __syncthreads();
 }
 
-__global__ __launch_bounds__(SNT) void ns_small_kernel(const SmallArgs a) {
-    __shared__ __attribute__((aligned(16))) float tile[SL * SPS];       // [l][p], p along the short side
-    __shared__ __attribute__((aligned(16))) double part[SNT * 16];      // partial A, then A, P, Q and a product
-    __shared__ double norm;
-    const int tid = threadIdx.x;
+constexpr int kChunkThreads = 512, kOneThreads = 1024;
+template <int NB>
+__global__ __launch_bounds__(kChunkThreads) void ns_small_gram_kernel(const SmallArgs a) {
+    constexpr int BLOCKS = NB == 1 ? 1 : 3, NT = kChunkThreads;
+    __shared__ double sum[BLOCKS * 256];
+    const int n = a.M > a.N ? a.M : a.N, lo = blockIdx.x * a.chunk;
+    small_gram<NB, NT>(a, lo, min(lo + a.chunk, n), sum);
+    double* out = a.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (BLOCKS * 256);
+    for (int e = threadIdx.x; e < BLOCKS * 256; e += NT) out[e] = sum[e];
+}
+
+// ONE: the whole matrix is this workgroup's chunk, and its sums are taken here.
+template <int NB, bool ONE>
+__global__ __launch_bounds__(ONE ? kOneThreads : kChunkThreads) void ns_small_kernel(const SmallArgs a) {
+    constexpr int BLOCKS = NB == 1 ? 1 : 3, NT = ONE ? kOneThreads : kChunkThreads;
+    __shared__ double sum[BLOCKS * 256];
+    // whole matrices, blocks [i][j] of 16 x 16 in result order: value v of a lane at 64 v + lane
+    __shared__ double A[NB][NB][256], P[NB][NB][256], U[NB][NB][256], Q[2][NB][NB][256];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
     const bool tall = a.M > a.N;
     const int m = tall ? a.N : a.M, n = tall ? a.M : a.N;
-    const int64_t base = (int64_t)blockIdx.x * a.M * a.N;
-
-    // columns l0 .. of the long side into the tile, zeros where there is nothing
-    auto load_tile = [&](int l0, auto&& src) {
-        for (int i = tid; i < SL * SM / 8; i += SNT) {
-            if (tall) {                       // eight along the short side
-                const int l = i / (SM / 8), p = 8 * (i % (SM / 8));
-                float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (l0 + l < n && p < m) src(base + (int64_t)(l0 + l) * m + p, m - p, u);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) tile[l * SPS + p + e] = p + e < m ? u[e] : 0.f;
-            } else {
-                const int p = i / (SL / 8), l = 8 * (i % (SL / 8));
-                float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (l0 + l < n && p < m) src(base + (int64_t)p * n + l0 + l, n - (l0 + l), u);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) tile[(l + e) * SPS + p] = l0 + l + e < n ? u[e] : 0.f;
-            }
+    const int lo = blockIdx.x * a.chunk, hi = min(lo + a.chunk, n);
+    if constexpr (ONE) {
+        small_gram<NB, NT>(a, lo, hi, sum);
+    } else {
+        for (int e = tid; e < BLOCKS * 256; e += NT) {
+            double t = 0.;
+#pragma unroll 8
+            for (unsigned k = 0; k < gridDim.x; ++k)
+                t += a.part[((int64_t)blockIdx.y * gridDim.x + k) * (BLOCKS * 256) + e];
+            sum[e] = t;
         }
         __syncthreads();
+    }
+    double trace = lane < m ? sum[low_block(lane >> 4, lane >> 4) * 256 + (lane & 15) * 17] : 0.;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) trace += __shfl_xor(trace, o, 64);
+    trace = __shfl(trace, 0, 64);
+    const double inv = 1. / (sqrt(trace) + a.eps);
+
+    // ---- the steps: wavefront w < NB^2 owns block (bi, bj) of every matrix
+    const bool works = wave < NB * NB;
+    const int bi = NB == 1 ? 0 : wave >> 1 & 1, bj = NB == 1 ? 0 : wave & 1;
+    auto product = [&](double (*x)[NB][256], double (*y)[NB][256]) {
+        f64x4_t acc = {0., 0., 0., 0.};
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            f64x4_t p, q;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) p[v] = x[k][bi][64 * v + lane], q[v] = y[k][bj][64 * v + lane];
+            acc = mfma4(p, q, acc);          // block (k, bi)^T = block (bi, k)
+        }
+        return acc;
     };
-
-    // A = U U^T: 4 x 4 entries a thread, nb^2 threads cover the matrix, and the
-    // SNT / nb^2 groups of threads share out the long side
-    const int nb = (m + 3) >> 2, per = nb * nb, groups = SNT / per;
-    const int grp = tid / per, bp = 4 * ((tid % per) / nb), bq = 4 * ((tid % per) % nb);
-    double acc[4][4];
+    auto put = [&](double (*x)[NB][256], f64x4_t r) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int v = 0; v < 4; ++v) x[bi][bj][64 * v + lane] = r[v];
+    };
+    f64x4_t own;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.;
-    for (int l0 = 0; l0 < n; l0 += SL) {
-        load_tile(l0, [&](int64_t at, int left, float* u) { source8_first(a.s, at, left, u); });
-        if (grp < groups)
-            for (int l = grp; l < SL; l += groups) {
-                const float4 p = *(const float4*)&tile[l * SPS + bp], q = *(const float4*)&tile[l * SPS + bq];
-                const double pd[4] = {p.x, p.y, p.z, p.w}, qd[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fma(pd[i], qd[j], acc[i][j]);
-            }
-        __syncthreads();
+    for (int v = 0; v < 4; ++v) {
+        const int i = 4 * v + g;
+        const double* blk = sum + low_block(max(bi, bj), min(bi, bj)) * 256;
+        own[v] = (bi >= bj ? blk[i * 16 + c] : blk[c * 16 + i]) * inv * inv;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (grp < groups) part[(grp * 16 + 4 * i + j) * per + tid % per] = acc[i][j];
+    if (works) put(A, own);
     __syncthreads();
-    // entry (i, j) of block k: the groups' partial sums in order
-    double sum[2] = {0., 0.};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int e = tid + k * SNT;
-        if (e < 16 * per)
-            for (int g = 0; g < groups; ++g) sum[k] += part[g * 16 * per + e];
-    }
-    __syncthreads();
-    double *A = part, *P = part + SM * SM, *Q = part + 2 * SM * SM, *S = part + 3 * SM * SM;
-    for (int i = tid; i < 4 * SM * SM; i += SNT) part[i] = 0.;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int e = tid + k * SNT;
-        if (e < 16 * per) {
-            const int ij = e / per, blk = e % per;
-            A[(4 * (blk / nb) + (ij >> 2)) * SM + 4 * (blk % nb) + (ij & 3)] = sum[k];
-        }
-    }
-    __syncthreads();
-    if (tid == 0) {
-        double t = 0.;
-        for (int i = 0; i < m; ++i) t += A[i * SM + i];
-        norm = sqrt(t) + a.eps;
-    }
-    __syncthreads();
-    const double inv = 1. / norm;
-    for (int i = tid; i < SM * SM; i += SNT) A[i] = A[i] * inv * inv;
-    __syncthreads();
+    int q = 0;
     for (int k = 0; k < a.steps; ++k) {
-        small_product(A, A, S, m);
-        for (int i = tid; i < SM * SM; i += SNT) {
-            const double d = (i / SM == i % SM && i / SM < m) ? a.a : 0.;
-            P[i] = d + a.b * A[i] + a.c * S[i];
-            if (k == 0) Q[i] = P[i];
+        if (works) {
+            const f64x4_t sq = product(A, A);
+            f64x4_t r;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int i = 16 * bi + 4 * v + g;
+                r[v] = (i == 16 * bj + c && i < m ? a.a : 0.) + a.b * own[v] + a.c * sq[v];
+            }
+            put(P, r);
+            if (k == 0) put(Q[0], r);
         }
         __syncthreads();
-        if (k > 0) {
-            small_product(Q, P, S, m);
-            double* x = Q;
-            Q = S;
-            S = x;
+        if (works) {
+            if (k > 0) put(Q[q ^ 1], product(Q[q], P));
+            if (k + 1 < a.steps) put(U, product(A, P));
         }
+        if (k > 0) q ^= 1;
+        __syncthreads();
         if (k + 1 < a.steps) {
-            small_product(A, P, S, m);
-            small_product(S, P, A, m);
+            if (works) {
+                own = product(U, P);
+                put(A, own);
+            }
+            __syncthreads();
         }
     }
-    // X = Q U / norm: a thread takes one column of the long side and every fourth
-    // group of four rows
-    for (int l0 = 0; l0 < n; l0 += SL) {
-        load_tile(l0, [&](int64_t at, int left, float* u) { source8(a.s, at, left, u); });
-        const int l = tid % SL;
-        for (int pb = tid / SL; pb < nb; pb += SNT / SL) {
-            double o[4] = {0., 0., 0., 0.};
-            for (int q = 0; q < 4 * nb; q += 4) {
-                const float4 u = *(const float4*)&tile[l * SPS + q];
-                const double ud[4] = {u.x, u.y, u.z, u.w};
+
+    // ---- X = Q U / (|U| + eps) for columns lo .. hi - 1, 16 a wavefront at a time
+    f64x4_t qb[NB][NB];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+    for (int i = 0; i < NB; ++i)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = fma(Q[(q + j) * SM + 4 * pb + i], ud[j], o[i]);
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) qb[i][j][v] = Q[q][i][j][64 * v + lane];
+    const int64_t base = (int64_t)blockIdx.y * a.M * a.N;
+#pragma unroll 2
+    for (int l0 = lo + 16 * wave; l0 < hi; l0 += NT / 4) {
+        f64x4_t u[NB];
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int p = 16 * k + 4 * v + g, l = l0 + c;
+                u[k][v] = p < m && l < hi
+                              ? (double)source1(a.s, base + (tall ? (int64_t)l * m + p : (int64_t)p * n + l), false)
+                              : 0.;
             }
-            if (l0 + l >= n) continue;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int p = 4 * pb + i;
-                if (p >= m) continue;
-                const int64_t at = base + (tall ? (int64_t)(l0 + l) * m + p : (int64_t)p * n + l0 + l);
-                float v[8] = {(float)(o[i] * inv)};
-                target8(a.t, at, 1, v);
+        for (int i = 0; i < NB; ++i) {
+            f64x4_t r = {0., 0., 0., 0.};
+#pragma unroll
+            for (int k = 0; k < NB; ++k) r = tall ? mfma4(u[k], qb[k][i], r) : mfma4(qb[k][i], u[k], r);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                // the result's rows are columns of the long side when tall, of the short otherwise
+                const int p = 16 * i + (tall ? c : 4 * v + g), l = l0 + (tall ? 4 * v + g : c);
+                if (p < m && l < hi)
+                    target1(a.t, base + (tall ? (int64_t)l * m + p : (int64_t)p * n + l), (float)(r[v] * inv));
             }
         }
-        __syncthreads();
     }
 }
 
@@ -1056,7 +1135,11 @@ moe_status check_sizes(int B, int M, int N) {
 
 Layout layout_of(int B, int M, int N) {
     Layout L = {};
-    if (is_small(M, N)) return L;
+    if (is_small(M, N)) {
+        const size_t chunks = small_chunks(M, N), blocks = (M < N ? M : N) <= 16 ? 1 : 3;
+        L.total = chunks > 1 ? (size_t)B * chunks * blocks * 256 * sizeof(double) : 0;
+        return L;
+    }
     const size_t m = pad64(M < N ? M : N), n = pad64(M < N ? N : M);
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -1171,14 +1254,30 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     if (B == 0) return MOE_OK;
     (void)hipGetLastError();
     auto ok = [] { return hipGetLastError() == hipSuccess; };
-    if (is_small(M, N)) {
-        const SmallArgs s = {src, tgt, M, N, steps, a, b, c, eps};
-        ns_small_kernel<<<B, SNT, 0, stream>>>(s);
-        return ok() ? MOE_OK : MOE_ERR_HIP;
-    }
     const Layout L = layout_of(B, M, N);
-    if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
-    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    if (L.total) {
+        if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
+        if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    }
+    if (is_small(M, N)) {
+        const int chunks = small_chunks(M, N);
+        const SmallArgs s = {src, tgt, M, N, steps, small_chunk(M, N), a, b, c, eps, (double*)workspace};
+        const dim3 grid(chunks, B);
+        auto launch = [&](auto blocks) {
+            constexpr int NB = decltype(blocks)::value;
+            if (chunks == 1) {
+                ns_small_kernel<NB, true><<<grid, kOneThreads, 0, stream>>>(s);
+                return ok();
+            }
+            ns_small_gram_kernel<NB><<<grid, kChunkThreads, 0, stream>>>(s);
+            if (!ok()) return false;
+            ns_small_kernel<NB, false><<<grid, kChunkThreads, 0, stream>>>(s);
+            return ok();
+        };
+        const bool done = (M < N ? M : N) <= 16 ? launch(std::integral_constant<int, 1>{})
+                                                : launch(std::integral_constant<int, 2>{});
+        return done ? MOE_OK : MOE_ERR_HIP;
+    }
     char* ws = (char*)workspace;
     const bool tall = M > N;
     const int m = pad64(tall ? N : M), n = pad64(tall ? M : N);

@@ -591,10 +591,10 @@ moe_status moe_layer_norm_backward(const void *h, const float *mean, const float
  * iteration, which needs more steps and converges to 1.
  * ------------------------------------------------------------------------ */
 
-/* Workspace bytes moe_newton_schulz and moe_muon_step need (16 bytes an
- * element and 8 an entry of A, sizes padded to multiples of 64, and a little;
- * 0 when the shorter side is at most 32, which needs none); 0 if the sizes
- * are invalid or unsupported. */
+/* Workspace bytes moe_newton_schulz and moe_muon_step need (12 bytes an
+ * element and 20 an entry of A, sizes padded to multiples of 64, and a
+ * little; with a shorter side of at most 32 at most 384 KiB a matrix, and none when
+ * the longer is at most 256); 0 if the sizes are invalid or unsupported. */
 size_t moe_newton_schulz_workspace_size(int B, int M, int N);
 
 /*
