@@ -293,7 +293,6 @@ enum : int { GRAM = 0, SYMM = 1, APPLY = 2, FINAL = 3 };
 
 constexpr int BT = 128;                       // tile rows and columns
 constexpr int KB = 32;                        // K step
-constexpr int OPB = BT / 32 * BLOCK;          // one operand of a stage
 constexpr int TLD = BT + 1;                   // row of the fp32 tile in LDS
 
 struct MulArgs {
@@ -530,18 +529,19 @@ __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0
     }
 }
 
-// 128 x 128 tiles, four wavefronts of 64 x 64 each, a ring of NS stages of
-// 32 KiB.  NS = 2: two workgroups share a compute unit, one's epilogue under
-// the other's matrix instructions.  NS = 4, for grids of at most one workgroup a
-// compute unit: a stage has three steps to arrive.
-template <int MODE, int NS>
-__global__ __launch_bounds__(256, NS == 2 ? 2 : 1) void ns_product_kernel(const MulArgs a) {
+// Tiles of T = 64 NI rows and columns, four wavefronts of 32 NI x 32 NI each, a
+// ring of NS stages of 16 NI KiB.  NS = 2: as many workgroups as fit share a
+// compute unit, one's epilogue under the others' matrix instructions.  NS = 4, for
+// grids of about one workgroup a compute unit: a stage has three steps to
+// arrive.  NI = 1 for grids that 128-tiles would leave half empty.
+template <int MODE, int NI, int NS>
+__global__ __launch_bounds__(256, NI == 2 && NS == 4 ? 1 : 2) void ns_product_kernel(const MulArgs a) {
     constexpr bool SYM = MODE == GRAM || MODE == SYMM;
-    constexpr int TILE_BYTES = BT / 2 * TLD * 4;
-    static_assert(TILE_BYTES >= 2 * OPB, "a half of the fp32 tile covers a stage");
+    constexpr int T = 64 * NI, NB = T / 32, LD = T + 1, OPB = NB * BLOCK;
+    constexpr int TILE_BYTES = T / 2 * LD * 4 > 2 * OPB ? T / 2 * LD * 4 : 2 * OPB;
     // separate objects, so that a read of one buffer does not wait for the
-    // transfers into the others; the epilogue holds rows 0..63 of the fp32 tile
-    // in the first, 64..127 in the second
+    // transfers into the others; the first two hold a half of the fp32 tile each
+    // in the epilogue
     __shared__ __attribute__((aligned(1024))) char st0[TILE_BYTES];
     __shared__ __attribute__((aligned(1024))) char st1[TILE_BYTES];
     __shared__ __attribute__((aligned(1024))) char st2[NS == 4 ? 2 * OPB : 16];
@@ -550,42 +550,48 @@ __global__ __launch_bounds__(256, NS == 2 ? 2 : 1) void ns_product_kernel(const 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int b, ti, tj;
     tile_of<SYM>(a, b, ti, tj);
-    const int i0 = ti * BT, j0 = tj * BT;
+    const int i0 = ti * T, j0 = tj * T;
 
-    // stage sources: wavefront w brings block row w of both operands, four
-    // transfers of 1 KiB each.  Block rows past the padded end (half tiles)
-    // read the last one and are not stored.
+    // stage sources: wavefront w brings blocks w NB / 2 .. of the P then Q block
+    // rows, four transfers of 1 KiB each.  Block rows past the padded end (tiles
+    // that end outside) read the last one and are not stored.
     const int KT = a.K / KB;
-    const char* ps = a.p + b * a.p_stride + (int64_t)min((i0 >> 5) + wave, (a.pr >> 5) - 1) * KT * BLOCK;
-    const char* qs = a.q + b * a.q_stride + (int64_t)min((j0 >> 5) + wave, (a.qr >> 5) - 1) * KT * BLOCK;
-    constexpr int PER_STAGE = 8;
+    constexpr int MINE = NB / 2, PER_STAGE = 4 * MINE;
+    const char* src[MINE];
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        const int blk = wave * MINE + i;
+        const bool second = blk >= NB;
+        const int row = second ? min((j0 >> 5) + blk - NB, (a.qr >> 5) - 1) : min((i0 >> 5) + blk, (a.pr >> 5) - 1);
+        src[i] = (second ? a.q + b * a.q_stride : a.p + b * a.p_stride) + (int64_t)row * KT * BLOCK;
+    }
     auto issue = [&](int n, char* st) {
         const int64_t o = (int64_t)n * BLOCK + lane * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            load_lds16(ps + o + j * 1024, st + wave * BLOCK + j * 1024);
-            load_lds16(qs + o + j * 1024, st + OPB + wave * BLOCK + j * 1024);
-        }
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < MINE; ++i)
+                load_lds16(src[i] + o + j * 1024, st + (wave * MINE + i) * BLOCK + j * 1024);
     };
 
     const int wi = wave >> 1, wj = wave & 1, rl = lane & 31, kh = lane >> 5;
-    f32x16_t acc[2][2];
+    f32x16_t acc[NI][NI];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
+        for (int j = 0; j < NI; ++j) acc[i][j] = f32x16_t{};
 
     struct Frags {
-        f16x8_t ph[2][2], pl[2][2], qh[2][2], ql[2][2];   // [k16 slice][block]
+        f16x8_t ph[2][NI], pl[2][NI], qh[2][NI], ql[2][NI];   // [k16 slice][block]
     };
     auto read = [&](const char* st, Frags& f) {
         auto frag = [&](const char* p) { return __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(p + lane * 16)); };
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const char* pb = st + (2 * wi + i) * BLOCK + ks * HALF;
-                const char* qb = st + OPB + (2 * wj + i) * BLOCK + ks * HALF;
+            for (int i = 0; i < NI; ++i) {
+                const char* pb = st + (NI * wi + i) * BLOCK + ks * HALF;
+                const char* qb = st + OPB + (NI * wj + i) * BLOCK + ks * HALF;
                 f.ph[ks][i] = frag(pb);
                 f.pl[ks][i] = frag(pb + LO);
                 f.qh[ks][i] = frag(qb);
@@ -609,14 +615,16 @@ __global__ __launch_bounds__(256, NS == 2 ? 2 : 1) void ns_product_kernel(const 
         issue(min(n + NS, KT - 1), cur);
         read(nxt, fn);
         compute(fc);
+        if constexpr (NI == 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // matrix instruction
-            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // transfer
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            for (int i = 0; i < 8; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // matrix instruction
+                __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // transfer
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -645,24 +653,24 @@ __global__ __launch_bounds__(256, NS == 2 ? 2 : 1) void ns_product_kernel(const 
     __syncthreads();
 
     if constexpr (MODE != FINAL) {
-        epilogue_blocks<MODE>(a, b, (i0 >> 5) + 2 * wi, (j0 >> 5) + 2 * wj, !SYM || ti != tj, acc, st0 + wave * BLOCK);
+        epilogue_blocks<MODE>(a, b, (i0 >> 5) + NI * wi, (j0 >> 5) + NI * wj, !SYM || ti != tj, acc, st0 + wave * BLOCK);
         return;
     }
     // ---- the target: the fp32 tile through LDS
-    auto at = [&](int r, int c) -> float& { return ((float*)(r < 64 ? st0 : st1))[(r & 63) * TLD + c]; };
+    auto at = [&](int r, int c) -> float& { return ((float*)(r < T / 2 ? st0 : st1))[(r & (T / 2 - 1)) * LD + c]; };
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NI; ++j)
 #pragma unroll
             for (int g = 0; g < 16; ++g)
-                at(64 * wi + 32 * i + acc_row(g, kh), 64 * wj + 32 * j + rl) = acc[i][j][g];
+                at(32 * (NI * wi + i) + acc_row(g, kh), 32 * (NI * wj + j) + rl) = acc[i][j][g];
     __syncthreads();
     auto sum8 = [&](int r, int c, float* v) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = at(r, c + e);
     };
-    epilogue<MODE, BT, 256>(a, b, i0, j0, true, sum8, at);
+    epilogue<MODE, T, 256>(a, b, i0, j0, true, sum8, at);
 }
 
 // 256 x 256 tiles for long grids: eight wavefronts of 128 x 64, two stages of
@@ -1203,19 +1211,44 @@ double scale_for(double bound) {
     return s;
 }
 
-// Which tile a product runs on, from the number of tiles n and of K steps k
-// (256 compute units; times in us of one launch, measured over 40 products of
-// 1 to 64 matrices, short sides 128 to 4096, k 4 to 128):
-//  * 256: one workgroup a unit, 2.0 to 2.6 a step.  It wins where its rounds of 256
-//    are well filled: full, or 160 of 256 with k >= 48, or 128 with k >= 96
-//    (k = 128: 254 us against 286 with 160 tiles, 231 against 247 with 136;
-//    k = 32: 77 against 72 with 160; k = 24: 135 against 119 with 288).
-//  * 32 split over K: about 4 + n (0.0022 + 0.0003 k) (k = 24: 10.7 with 600 tiles, 49
-//    with 4800), against 8 + k (0.45 + 0.0009 n) for up to 256 tiles of 128
-//    (k = 24: 19 with 21 tiles, 23 with 168): the smaller of the two.
-//  * 128: the ring of four stages in one round of 256 with k >= 32 (84 us
-//    against 92 with 144 tiles, k = 128), else two stages and two workgroups
-//    a unit (12 against 13 with 192 tiles, k = 8; 74 against 88 with 272, k = 64).
+// The tile a product runs on: the one whose estimate is the least.  The estimates
+// are fits (us of one launch; n tiles, k steps of 32; 256 compute units) to 130
+// launches of 1 to 64 matrices with short sides of 128 to 4096 and k of 4 to 128,
+// most within 15%:
+//  * 32, split over K:  4 + n (0.0022 + 0.0003 k), 0.0005 k where an operand
+//    outgrows an XCD's 4 MiB of L2
+//  * 64, four stages:   4 + k max(0.235, 0.00102 n)
+//    64, two stages:    4 + k max(0.385, 0.00092 n), 0.0011 n beyond 1000 tiles
+//  * 128, four stages:  8 + k max(0.5, 0.003 n), n <= 256
+//    128, two stages:   8 + k max(0.57, 0.0032 n); beyond 512 tiles 0.0034 n, 0.0038 n
+//    with an outgrown operand
+//  * 256:               24 r - 12 + k (1.1 r + 0.0048 n) in r rounds of 256
+// Measured on both sides of the borders: k = 24, one 768 x 1536 matrix's A A 7.8 us
+// on 32-tiles, 10.8 on 64; eight of them 25.6, 18.6 on 64, 21.1 on 128; their B X
+// 84, 55.7, 55.9 and 55.7 on 256; sixteen 1024 x 4096 matrices' B X (k = 32) 586
+// on 64, 453 on 128, 408 on 256.
+struct Choice {
+    int tile, stages;
+};
+Choice choose(int64_t n32, int64_t n64, int64_t n128, int64_t n256, int k, bool outgrown) {
+    const int64_t r = (n256 + 255) / 256;
+    const struct {
+        Choice c;
+        double us;
+    } all[] = {
+        {{32, 0}, 4. + n32 * (0.0022 + (outgrown ? 0.0005 : 0.0003) * k)},
+        {{64, 4}, 4. + k * fmax(0.235, 0.00102 * n64)},
+        {{64, 2}, 4. + k * fmax(0.385, (n64 <= 1000 ? 0.00092 : 0.0011) * n64)},
+        {{128, 4}, n128 <= 256 ? 8. + k * fmax(0.5, 0.003 * n128) : 1e30},
+        {{128, 2}, 8. + k * fmax(0.57, (n128 <= 512 ? 0.0032 : outgrown ? 0.0038 : 0.0034) * n128)},
+        {{256, 2}, 24. * r - 12. + k * (1.1 * r + 0.0048 * n256)},
+    };
+    int best = 0;
+    for (int i = 1; i < 6; ++i)
+        if (all[i].us < all[best].us) best = i;
+    return all[best].c;
+}
+
 template <int MODE>
 bool launch_product(MulArgs& g, int B, hipStream_t stream) {
     constexpr bool SYM = MODE == GRAM || MODE == SYMM;
@@ -1224,21 +1257,21 @@ bool launch_product(MulArgs& g, int B, hipStream_t stream) {
         g.tj = (g.qr + tile - 1) / tile;
         return (int64_t)B * (SYM ? (int64_t)g.ti * (g.ti + 1) / 2 : (int64_t)g.ti * g.tj);
     };
-    const int64_t n32 = grid(DT), n128 = grid(BT), n256 = grid(LT);
-    const int k = g.K / KB;
-    const int64_t round = n256 / ((n256 + 255) / 256);
-    if (round >= 240 || (round >= 160 && k >= 48) || (round >= 128 && k >= 96)) {
-        ns_product_large_kernel<MODE><<<(unsigned)n256, 512, 0, stream>>>(g);
-    } else if (n128 <= 256 && 4. + n32 * (0.0022 + 0.0003 * k) < 8. + k * (0.45 + 0.0009 * n128)) {
-        grid(DT);
-        ns_product_split_kernel<MODE><<<(unsigned)n32, 64 * DW, 0, stream>>>(g);
-    } else {
-        grid(BT);
-        if (n128 <= 256 && k >= 32)
-            ns_product_kernel<MODE, 4><<<(unsigned)n128, 256, 0, stream>>>(g);
-        else
-            ns_product_kernel<MODE, 2><<<(unsigned)n128, 256, 0, stream>>>(g);
-    }
+    const bool outgrown = (int64_t)g.qr * g.K * 4 > 4 << 20;
+    const Choice c = choose(grid(DT), grid(64), grid(128), grid(LT), g.K / KB, outgrown);
+    const unsigned n = (unsigned)grid(c.tile);
+    if (c.tile == 32)
+        ns_product_split_kernel<MODE><<<n, 64 * DW, 0, stream>>>(g);
+    else if (c.tile == 64 && c.stages == 4)
+        ns_product_kernel<MODE, 1, 4><<<n, 256, 0, stream>>>(g);
+    else if (c.tile == 64)
+        ns_product_kernel<MODE, 1, 2><<<n, 256, 0, stream>>>(g);
+    else if (c.tile == 128 && c.stages == 4)
+        ns_product_kernel<MODE, 2, 4><<<n, 256, 0, stream>>>(g);
+    else if (c.tile == 128)
+        ns_product_kernel<MODE, 2, 2><<<n, 256, 0, stream>>>(g);
+    else
+        ns_product_large_kernel<MODE><<<n, 512, 0, stream>>>(g);
     return hipGetLastError() == hipSuccess;
 }
 
