@@ -437,6 +437,83 @@ def run_train_step(args):
           flush=True)
 
 
+def block_step_record(workload, steps, warmup):
+    """A pre-norm block's training step on one workload, its operators one
+    after the other: residual sum and layer norm, router, layer (gate and up
+    products kept), the layer's backward, the norm's backward, and a Muon step
+    on each expert matrix (fp32 weights beside the bf16 ones the layer reads).
+    Each call is timed alone and the step as a whole (host clock between two
+    synchronisations); one JSON line."""
+    import torch
+
+    import grouped_gemm_permute_amd as gg
+    import moe_inputs
+
+    w = moe_inputs.WORKLOADS[workload]
+    if w.dtype != "bf16":
+        raise SystemExit("--block-step: the kept gate/up products exist on the bf16 path only")
+    torch.cuda.set_device(0)
+    gen = torch.Generator(device="cuda").manual_seed(workload)
+
+    def n(*shape, by=1.0):
+        return (torch.randn(shape, generator=gen, device="cuda") * by).to(torch.bfloat16)
+
+    x, r, dout = n(w.T, w.D), n(w.T, w.D), n(w.T, w.D)
+    ln_w, ln_b, gate = 1 + n(w.D, by=0.1), n(w.D, by=0.1), n(w.D, w.E, by=w.D ** -0.5)
+    W1, W3 = n(w.E, w.D, w.F, by=w.D ** -0.5), n(w.E, w.D, w.F, by=w.D ** -0.5)
+    W2 = n(w.E, w.F, w.D, by=w.F ** -0.5)
+    shared = (n(w.D, w.F, by=w.D ** -0.5), n(w.D, w.F, by=w.D ** -0.5), n(w.F, w.D, by=w.F ** -0.5)) if w.shared else None
+    state = {name: (t, t.float(), torch.zeros(t.shape, device="cuda"))
+             for name, t in (("dW1", W1), ("dW3", W3), ("dW2", W2))}
+    log(f"block-step workload {w.name}")
+    keep = {}
+
+    def norm():
+        keep["f"] = gg.layer_norm(x, ln_w, ln_b, residual=r)
+
+    def router():
+        keep["idx"], keep["w"] = gg.router_topk(keep["f"]["y"], gate, w.k)
+
+    def layer():
+        return (keep["f"]["y"], keep["idx"], keep["w"], W1, W3, W2, shared)
+
+    def forward():
+        keep["y"], keep["gu"] = gg.forward_save_gu(*layer(), gu=keep.get("gu"))
+
+    def backward():
+        keep["g"] = gg.backward(*layer(), dout, out=keep.get("g"), gu=keep["gu"])
+
+    def norm_backward():
+        f = keep["f"]
+        keep["b"] = gg.layer_norm_backward(f["h"], keep["g"]["dx"], f["rstd"], f["mean"], ln_w, dh=dout, bias_grad=True)
+
+    def muon():
+        for name, (t, master, mom) in state.items():
+            gg.muon_step(master, keep["g"][name], mom, 1e-3, W_bf16=t)
+
+    calls = {"layer_norm": norm, "router_topk": router, "forward_save_gu": forward, "backward_cached": backward,
+             "layer_norm_backward": norm_backward, "muon_step_x3": muon}
+    calls["step"] = lambda fs=tuple(calls.values()): [f() for f in fs]
+    ms = {}
+    for name, f in calls.items():
+        for _ in range(warmup + 1):
+            f()
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        for _ in range(steps):
+            f()
+        torch.cuda.synchronize()
+        ms[name] = (time.perf_counter() - t0) * 1e3 / steps
+        log(f"{name}: {ms[name]:.4f} ms per call")
+    return {
+        "metric": "pre-norm MoE block training step ms (norm, router, layer, backward, Muon)", "unit": "ms",
+        "value": round(ms["step"], 5), "higher_is_better": False, "n_gpus": 1, "steps": steps, "warmup": warmup,
+        "dtype": w.dtype, "data": "synthetic",
+        "config": {"workload": w.name, "T": w.T, "D": w.D, "F": w.F, "E": w.E, "k": w.k, "shared_expert": w.shared},
+        "ms_per_call": {k: round(v, 5) for k, v in ms.items()},
+    }
+
+
 def time_forward(w, variant, steps, warmup, rotate_bytes=512e6):
     """Wall time per forward call of workload w (inputs rotated as in the
     main bench), in ms."""
@@ -856,6 +933,9 @@ def main():
     ap.add_argument("--train-step", action="store_true",
                     help="time a training step's forward and backward with the gate/up products "
                          "recomputed by the backward or kept from the forward (bf16 workloads)")
+    ap.add_argument("--block-step", action="store_true",
+                    help="time a pre-norm block's training step: layer norm, router, layer, its "
+                         "backward, the norm's backward and a Muon step on the expert matrices")
     ap.add_argument("--routed", action="store_true",
                     help="time moe_ffn_forward_routed: the top-k router (x @ gate_w, top-k, softmax) "
                          "feeding the permute, then the same forward")
@@ -884,6 +964,9 @@ def main():
         return
     if args.train_step:
         run_train_step(args)
+        return
+    if args.block_step:
+        print(json.dumps(block_step_record(args.workload, args.steps, args.warmup)), flush=True)
         return
     if args.sweep:
         run_sweep(args)
