@@ -152,10 +152,13 @@ __device__ __forceinline__ void source8_first(const Source& s, int64_t at, int l
         for (int i = 0; i < 8; ++i) u[i] = s.nesterov ? fmaf(s.beta, m[i], u[i]) : m[i];
     }
 }
-__device__ __forceinline__ void target8(const Target& t, int64_t at, int left, float* v) {
+// The weights that eight results will change (muon), and the change: apart, so
+// that a thread's loads are all on their way before its first store.
+__device__ __forceinline__ void target8_load(const Target& t, int64_t at, int left, float* w) {
+    if (t.muon) load8(t.out, at, left, t.out_bf16, w);
+}
+__device__ __forceinline__ void target8_store(const Target& t, int64_t at, int left, float* v, const float* w) {
     if (t.muon) {
-        float w[8];
-        load8(t.out, at, left, t.out_bf16, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = fmaf(-t.rate, v[i], t.keep * w[i]);
         if (t.copy) store8(t.copy, at, left, true, v);
@@ -367,7 +370,25 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
     };
     if (MODE == FINAL) both = a.swap;
     auto here = [&](int r, int c) { return r < TS && c < TS && i0 + r < a.pr && j0 + c < a.qr; };
-    // all addends on their way before the first store
+    // FINAL: where a piece of the target's row `row` begins
+    auto target_at = [&](int row, int seg) {
+        return a.swap ? ((int64_t)b * a.M + j0 + row) * a.N + i0 + seg : ((int64_t)b * a.M + i0 + row) * a.N + j0 + seg;
+    };
+    auto target_left = [&](int row, int seg) {
+        if ((a.swap ? j0 : i0) + row >= a.M) return 0;
+        return a.N - (a.swap ? i0 : j0) - seg;
+    };
+    // all addends, and the weights of the target, on their way before the first store
+    float w[MODE == FINAL ? PASSES : 1][8];
+    if constexpr (MODE == FINAL) {
+#pragma unroll
+        for (int k = 0; k < PASSES; ++k) {
+            int row, seg;
+            place(threadIdx.x + k * NT, row, seg);
+            const int left = row < TS && seg < TS ? target_left(row, seg) : 0;
+            if (left > 0) target8_load(a.t, target_at(row, seg), left, w[k]);
+        }
+    }
     u32x4_t hi[PASSES], lo[PASSES], qhi[PASSES], qlo[PASSES];
     if constexpr (MODE != GRAM) {
 #pragma unroll
@@ -402,9 +423,8 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
             for (int e = 0; e < 8; ++e) v[e] *= a.so;
             store_planes(a.c + b * a.c_stride, plane_at(i0 + r, a.qr, j0 + c), v);
         } else if (!a.swap) {
-            const int left = a.N - (j0 + c);
-            if (i0 + r < a.M && left > 0)
-                target8(a.t, ((int64_t)b * a.M + i0 + r) * a.N + j0 + c, left, v);
+            const int left = target_left(r, c);
+            if (left > 0) target8_store(a.t, target_at(r, c), left, v, w[k]);
         }
         if (both) {
 #pragma unroll
@@ -424,9 +444,8 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
         if constexpr (MODE != FINAL) {
             store_planes(a.ct + b * a.c_stride, plane_at(j0 + c, a.pr, i0 + r), v);
         } else {
-            const int left = a.N - (i0 + r);
-            if (j0 + c < a.M && left > 0)
-                target8(a.t, ((int64_t)b * a.M + j0 + c) * a.N + i0 + r, left, v);
+            const int left = target_left(c, r);
+            if (left > 0) target8_store(a.t, target_at(c, r), left, v, w[k]);
         }
     }
 }
