@@ -550,9 +550,11 @@ __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0
 
 // Tiles of T = 64 NI rows and columns, four wavefronts of 32 NI x 32 NI each, a
 // ring of NS stages of 16 NI KiB.  NS = 2: as many workgroups as fit share a
-// compute unit, one's epilogue under the others' matrix instructions.  NS = 4, for
-// grids of about one workgroup a compute unit: a stage has three steps to
-// arrive.  NI = 1 for grids that 128-tiles would leave half empty.
+// compute unit, one's epilogue under the others' matrix instructions.  NS = 3 (NI =
+// 1) or 4 (NI = 2), for grids of about one workgroup a compute unit: a stage has
+// two or three steps to arrive (k = 48, 156 tiles of 64: 16.4 us, 22.3 with two
+// stages; four were no faster).  NI = 1 for grids that 128-tiles would leave half
+// empty.
 template <int MODE, int NI, int NS>
 __global__ __launch_bounds__(256, NI == 2 && NS == 4 ? 1 : 2) void ns_product_kernel(const MulArgs a) {
     constexpr bool SYM = MODE == GRAM || MODE == SYMM;
@@ -563,7 +565,7 @@ __global__ __launch_bounds__(256, NI == 2 && NS == 4 ? 1 : 2) void ns_product_ke
     // in the epilogue
     __shared__ __attribute__((aligned(1024))) char st0[TILE_BYTES];
     __shared__ __attribute__((aligned(1024))) char st1[TILE_BYTES];
-    __shared__ __attribute__((aligned(1024))) char st2[NS == 4 ? 2 * OPB : 16];
+    __shared__ __attribute__((aligned(1024))) char st2[NS >= 3 ? 2 * OPB : 16];
     __shared__ __attribute__((aligned(1024))) char st3[NS == 4 ? 2 * OPB : 16];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -650,22 +652,36 @@ __global__ __launch_bounds__(256, NI == 2 && NS == 4 ? 1 : 2) void ns_product_ke
     Frags f0, f1;
     issue(0, st0);
     issue(min(1, KT - 1), st1);
-    if constexpr (NS == 4) {
-        issue(min(2, KT - 1), st2);
-        issue(min(3, KT - 1), st3);
-    }
+    if constexpr (NS >= 3) issue(min(2, KT - 1), st2);
+    if constexpr (NS == 4) issue(min(3, KT - 1), st3);
     __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 1) * PER_STAGE, 15));   // stage 0 has landed
     __builtin_amdgcn_s_barrier();
     read(st0, f0);
-    for (int n = 0; n < KT; n += NS) {       // KT is even
-        step(n, f0, f1, st0, st1);
-        if constexpr (NS == 2) {
+    if constexpr (NS == 2) {
+        for (int n = 0; n < KT; n += 2) {        // KT is even
+            step(n, f0, f1, st0, st1);
             step(n + 1, f1, f0, st1, st0);
-        } else {
+        }
+    } else if constexpr (NS == 3) {
+        for (int n = 0;; n += 6) {
+            step(n, f0, f1, st0, st1);
+            step(n + 1, f1, f0, st1, st2);
+            if (n + 2 >= KT) break;
+            step(n + 2, f0, f1, st2, st0);
+            step(n + 3, f1, f0, st0, st1);
+            if (n + 4 >= KT) break;
+            step(n + 4, f0, f1, st1, st2);
+            step(n + 5, f1, f0, st2, st0);
+            if (n + 6 >= KT) break;
+        }
+    } else {
+        for (int n = 0;; n += 4) {
+            step(n, f0, f1, st0, st1);
             step(n + 1, f1, f0, st1, st2);
             if (n + 2 >= KT) break;
             step(n + 2, f0, f1, st2, st3);
             step(n + 3, f1, f0, st3, st0);
+            if (n + 4 >= KT) break;
         }
     }
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));           // before the buffers are used anew
@@ -1236,7 +1252,7 @@ double scale_for(double bound) {
 // most within 15%:
 //  * 32, split over K:  4 + n (0.0022 + 0.0003 k), 0.0005 k where an operand
 //    outgrows an XCD's 4 MiB of L2
-//  * 64, four stages:   4 + k max(0.235, 0.00102 n)
+//  * 64, three stages:  4 + k max(0.235, 0.00096 n)
 //    64, two stages:    4 + k max(0.385, 0.00092 n), 0.0011 n beyond 1000 tiles
 //  * 128, four stages:  8 + k max(0.5, 0.003 n), n <= 256
 //    128, two stages:   8 + k max(0.57, 0.0032 n); beyond 512 tiles 0.0034 n, 0.0038 n
@@ -1244,7 +1260,7 @@ double scale_for(double bound) {
 //  * 256:               24 r - 12 + k (1.1 r + 0.0048 n) in r rounds of 256
 // Measured on both sides of the borders: k = 24, one 768 x 1536 matrix's A A 7.8 us
 // on 32-tiles, 10.8 on 64; eight of them 25.6, 18.6 on 64, 21.1 on 128; their B X
-// 84, 55.7, 55.9 and 55.7 on 256; sixteen 1024 x 4096 matrices' B X (k = 32) 586
+// 84, 55.7, 55.9 and 55.7 on 256-tiles; sixteen 1024 x 4096 matrices' B X (k = 32) 586
 // on 64, 453 on 128, 408 on 256.
 struct Choice {
     int tile, stages;
@@ -1256,7 +1272,7 @@ Choice choose(int64_t n32, int64_t n64, int64_t n128, int64_t n256, int k, bool 
         double us;
     } all[] = {
         {{32, 0}, 4. + n32 * (0.0022 + (outgrown ? 0.0005 : 0.0003) * k)},
-        {{64, 4}, 4. + k * fmax(0.235, 0.00102 * n64)},
+        {{64, 3}, 4. + k * fmax(0.235, 0.00096 * n64)},
         {{64, 2}, 4. + k * fmax(0.385, (n64 <= 1000 ? 0.00092 : 0.0011) * n64)},
         {{128, 4}, n128 <= 256 ? 8. + k * fmax(0.5, 0.003 * n128) : 1e30},
         {{128, 2}, 8. + k * fmax(0.57, (n128 <= 512 ? 0.0032 : outgrown ? 0.0038 : 0.0034) * n128)},
@@ -1281,8 +1297,8 @@ bool launch_product(MulArgs& g, int B, hipStream_t stream) {
     const unsigned n = (unsigned)grid(c.tile);
     if (c.tile == 32)
         ns_product_split_kernel<MODE><<<n, 64 * DW, 0, stream>>>(g);
-    else if (c.tile == 64 && c.stages == 4)
-        ns_product_kernel<MODE, 1, 4><<<n, 256, 0, stream>>>(g);
+    else if (c.tile == 64 && c.stages == 3)
+        ns_product_kernel<MODE, 1, 3><<<n, 256, 0, stream>>>(g);
     else if (c.tile == 64)
         ns_product_kernel<MODE, 1, 2><<<n, 256, 0, stream>>>(g);
     else if (c.tile == 128 && c.stages == 4)
