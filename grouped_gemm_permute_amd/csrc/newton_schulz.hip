@@ -303,6 +303,7 @@ struct MulArgs {
     int64_t p_stride, q_stride; // bytes per matrix
     int pr, qr, K;              // padded rows of each side, reduction length
     int ti, tj;                 // tiles of each side
+    int whole;                  // mixed tiles: how many of 128
     float f;                    // factor of the product
     const char* add;            // SYMM: P; APPLY, FINAL: X
     int64_t add_stride;
@@ -335,13 +336,12 @@ __device__ __forceinline__ void mul3(f32x16_t (&acc)[NI][NJ], const f16x8_t* ph,
                                                                    acc[i][j], 0, 0, 0);
 }
 
-// This workgroup's matrix and tile; of a symmetric result the tiles on and
-// below the diagonal.  Each XCD takes a contiguous range, so its L2 holds
-// one matrix's operands (or a band of rows).
+// The matrix and tile of number id; of a symmetric result the tiles on and
+// below the diagonal.  Each XCD takes a contiguous range (xcd_remap), so its L2
+// holds one matrix's operands (or a band of rows).
 template <bool SYM>
-__device__ __forceinline__ void tile_of(const MulArgs& a, int& b, int& ti, int& tj) {
+__device__ __forceinline__ void tile_of(const MulArgs& a, int id, int& b, int& ti, int& tj) {
     const int per = SYM ? a.ti * (a.ti + 1) / 2 : a.ti * a.tj;
-    const int id = xcd_remap(blockIdx.x, gridDim.x);
     b = id / per;
     const int t = id - b * per;
     if constexpr (SYM) {
@@ -555,23 +555,24 @@ __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0
 // two or three steps to arrive (k = 48, 156 tiles of 64: 16.4 us, 22.3 with two
 // stages; four were no faster).  NI = 1 for grids that 128-tiles would leave half
 // empty.
+template <int NI>
+constexpr int stage_bytes() {
+    return 2 * 2 * NI * BLOCK;
+}
+// Bytes of the first two stages, which hold a half of the fp32 tile each in the end.
+template <int NI>
+constexpr int tile_bytes() {
+    constexpr int T = 64 * NI, half = T / 2 * (T + 1) * 4;
+    return half > stage_bytes<NI>() ? half : stage_bytes<NI>();
+}
+// The tile at rows i0, columns j0 of matrix b.  The stages are separate objects, so
+// that a read of one does not wait for the transfers into the others.
 template <int MODE, int NI, int NS>
-__global__ __launch_bounds__(256, NI == 2 && NS == 4 ? 1 : 2) void ns_product_kernel(const MulArgs a) {
-    constexpr bool SYM = MODE == GRAM || MODE == SYMM;
+__device__ __forceinline__ void product_tile(const MulArgs& a, int b, int i0, int j0, bool both, char* st0,
+                                             char* st1, char* st2, char* st3) {
     constexpr int T = 64 * NI, NB = T / 32, LD = T + 1, OPB = NB * BLOCK;
-    constexpr int TILE_BYTES = T / 2 * LD * 4 > 2 * OPB ? T / 2 * LD * 4 : 2 * OPB;
-    // separate objects, so that a read of one buffer does not wait for the
-    // transfers into the others; the first two hold a half of the fp32 tile each
-    // in the epilogue
-    __shared__ __attribute__((aligned(1024))) char st0[TILE_BYTES];
-    __shared__ __attribute__((aligned(1024))) char st1[TILE_BYTES];
-    __shared__ __attribute__((aligned(1024))) char st2[NS >= 3 ? 2 * OPB : 16];
-    __shared__ __attribute__((aligned(1024))) char st3[NS == 4 ? 2 * OPB : 16];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int b, ti, tj;
-    tile_of<SYM>(a, b, ti, tj);
-    const int i0 = ti * T, j0 = tj * T;
 
     // stage sources: wavefront w brings blocks w NB / 2 .. of the P then Q block
     // rows, four transfers of 1 KiB each.  Block rows past the padded end (tiles
@@ -688,7 +689,7 @@ __global__ __launch_bounds__(256, NI == 2 && NS == 4 ? 1 : 2) void ns_product_ke
     __syncthreads();
 
     if constexpr (MODE != FINAL) {
-        epilogue_blocks<MODE>(a, b, (i0 >> 5) + NI * wi, (j0 >> 5) + NI * wj, !SYM || ti != tj, acc, st0 + wave * BLOCK);
+        epilogue_blocks<MODE>(a, b, (i0 >> 5) + NI * wi, (j0 >> 5) + NI * wj, both, acc, st0 + wave * BLOCK);
         return;
     }
     // ---- the target: the fp32 tile through LDS
@@ -708,6 +709,41 @@ __global__ __launch_bounds__(256, NI == 2 && NS == 4 ? 1 : 2) void ns_product_ke
     epilogue<MODE, T, 256>(a, b, i0, j0, true, sum8, at);
 }
 
+template <int MODE, int NI, int NS>
+__global__ __launch_bounds__(256, NI == 2 && NS == 4 ? 1 : 2) void ns_product_kernel(const MulArgs a) {
+    constexpr bool SYM = MODE == GRAM || MODE == SYMM;
+    __shared__ __attribute__((aligned(1024))) char st0[tile_bytes<NI>()];
+    __shared__ __attribute__((aligned(1024))) char st1[tile_bytes<NI>()];
+    __shared__ __attribute__((aligned(1024))) char st2[NS >= 3 ? stage_bytes<NI>() : 16];
+    __shared__ __attribute__((aligned(1024))) char st3[NS == 4 ? stage_bytes<NI>() : 16];
+    int b, ti, tj;
+    tile_of<SYM>(a, xcd_remap(blockIdx.x, gridDim.x), b, ti, tj);
+    product_tile<MODE, NI, NS>(a, b, 64 * NI * ti, 64 * NI * tj, !SYM || ti != tj, st0, st1, st2, st3);
+}
+
+// 128-tiles in full rounds of 256 and the few that remain as four 64-tiles each,
+// so that they end sooner than a round of their own: a.whole tiles of 128,
+// then 4 (all - whole) workgroups of 64.  k = 32 steps, 576 tiles: 61 us, 69.5
+// with every tile of 128; k = 64, 272 tiles: 58 and 73.
+template <int MODE>
+__global__ __launch_bounds__(256, 2) void ns_product_mixed_kernel(const MulArgs a) {
+    constexpr bool SYM = MODE == GRAM || MODE == SYMM;
+    __shared__ __attribute__((aligned(1024))) char st0[tile_bytes<2>()];
+    __shared__ __attribute__((aligned(1024))) char st1[tile_bytes<2>()];
+    __shared__ __attribute__((aligned(1024))) char none[16];
+    int b, ti, tj;
+    if ((int)blockIdx.x < a.whole) {
+        tile_of<SYM>(a, xcd_remap(blockIdx.x, a.whole), b, ti, tj);
+        product_tile<MODE, 2, 2>(a, b, BT * ti, BT * tj, !SYM || ti != tj, st0, st1, none, none);
+        return;
+    }
+    const int id = xcd_remap(blockIdx.x - a.whole, gridDim.x - a.whole);
+    tile_of<SYM>(a, a.whole + (id >> 2), b, ti, tj);
+    const int i0 = BT * ti + 64 * ((id >> 1) & 1), j0 = BT * tj + 64 * (id & 1);
+    if (i0 >= a.pr || j0 >= a.qr || (SYM && i0 < j0)) return;
+    product_tile<MODE, 1, 2>(a, b, i0, j0, !SYM || i0 != j0, st0, st1, none, none);
+}
+
 // 256 x 256 tiles for long grids: eight wavefronts of 128 x 64, two stages of
 // 64 KiB, one workgroup a compute unit.  A byte from memory feeds twice the
 // products of a 128-tile, and an LDS byte 1.5 times.  Operands are held in
@@ -725,7 +761,7 @@ __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int b, ti, tj;
-    tile_of<SYM>(a, b, ti, tj);
+    tile_of<SYM>(a, xcd_remap(blockIdx.x, gridDim.x), b, ti, tj);
     const int i0 = ti * LT, j0 = tj * LT;
     const int KT = a.K / KB;     // even
     const char* ps = a.p + b * a.p_stride + (int64_t)min((i0 >> 5) + wave, (a.pr >> 5) - 1) * KT * BLOCK;
@@ -851,7 +887,7 @@ __global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulA
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int b, ti, tj;
-    tile_of<SYM>(a, b, ti, tj);
+    tile_of<SYM>(a, xcd_remap(blockIdx.x, gridDim.x), b, ti, tj);
     const int rl = lane & 31, kh = lane >> 5;
     const int KT = a.K / KB;
     const char* pp = a.p + b * a.p_stride + (int64_t)ti * KT * BLOCK;
@@ -1256,27 +1292,31 @@ double scale_for(double bound) {
 //    64, two stages:    4 + k max(0.385, 0.00092 n), 0.0011 n beyond 1000 tiles
 //  * 128, four stages:  8 + k max(0.5, 0.003 n), n <= 256
 //    128, two stages:   8 + k max(0.57, 0.0032 n); beyond 512 tiles 0.0034 n, 0.0038 n
-//    with an outgrown operand
+//    with an outgrown operand; mixed with 64 where at most 64 are over a
+//    multiple of 256 (336 tiles: 59, mixed 62): 12 + the same for the multiple
 //  * 256:               24 r - 12 + k (1.1 r + 0.0048 n) in r rounds of 256
 // Measured on both sides of the borders: k = 24, one 768 x 1536 matrix's A A 7.8 us
 // on 32-tiles, 10.8 on 64; eight of them 25.6, 18.6 on 64, 21.1 on 128; their B X
 // 84, 55.7, 55.9 and 55.7 on 256-tiles; sixteen 1024 x 4096 matrices' B X (k = 32) 586
 // on 64, 453 on 128, 408 on 256.
 struct Choice {
-    int tile, stages;
+    int tile, stages, whole;     // whole: mixed, how many of 128
 };
 Choice choose(int64_t n32, int64_t n64, int64_t n128, int64_t n256, int k, bool outgrown) {
-    const int64_t r = (n256 + 255) / 256;
+    const int64_t r = (n256 + 255) / 256, over = n128 % 256;
+    const bool mixed = n128 > 256 && over > 0 && over <= 64;
+    const int64_t n = mixed ? n128 - over : n128;
     const struct {
         Choice c;
         double us;
     } all[] = {
-        {{32, 0}, 4. + n32 * (0.0022 + (outgrown ? 0.0005 : 0.0003) * k)},
-        {{64, 3}, 4. + k * fmax(0.235, 0.00096 * n64)},
-        {{64, 2}, 4. + k * fmax(0.385, (n64 <= 1000 ? 0.00092 : 0.0011) * n64)},
-        {{128, 4}, n128 <= 256 ? 8. + k * fmax(0.5, 0.003 * n128) : 1e30},
-        {{128, 2}, 8. + k * fmax(0.57, (n128 <= 512 ? 0.0032 : outgrown ? 0.0038 : 0.0034) * n128)},
-        {{256, 2}, 24. * r - 12. + k * (1.1 * r + 0.0048 * n256)},
+        {{32, 0, 0}, 4. + n32 * (0.0022 + (outgrown ? 0.0005 : 0.0003) * k)},
+        {{64, 3, 0}, 4. + k * fmax(0.235, 0.00096 * n64)},
+        {{64, 2, 0}, 4. + k * fmax(0.385, (n64 <= 1000 ? 0.00092 : 0.0011) * n64)},
+        {{128, 4, 0}, n128 <= 256 ? 8. + k * fmax(0.5, 0.003 * n128) : 1e30},
+        {{128, 2, mixed ? (int)n : 0},
+         (mixed ? 12. : 8.) + k * fmax(0.57, (n <= 512 ? 0.0032 : outgrown ? 0.0038 : 0.0034) * n)},
+        {{256, 2, 0}, 24. * r - 12. + k * (1.1 * r + 0.0048 * n256)},
     };
     int best = 0;
     for (int i = 1; i < 6; ++i)
@@ -1303,7 +1343,10 @@ bool launch_product(MulArgs& g, int B, hipStream_t stream) {
         ns_product_kernel<MODE, 1, 2><<<n, 256, 0, stream>>>(g);
     else if (c.tile == 128 && c.stages == 4)
         ns_product_kernel<MODE, 2, 4><<<n, 256, 0, stream>>>(g);
-    else if (c.tile == 128)
+    else if (c.whole) {
+        g.whole = c.whole;
+        ns_product_mixed_kernel<MODE><<<c.whole + 4 * (n - c.whole), 256, 0, stream>>>(g);
+    } else if (c.tile == 128)
         ns_product_kernel<MODE, 2, 2><<<n, 256, 0, stream>>>(g);
     else
         ns_product_large_kernel<MODE><<<n, 512, 0, stream>>>(g);

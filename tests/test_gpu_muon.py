@@ -28,7 +28,7 @@ LARGE = [(1, 33, 33), (2, 40, 100), (1, 64, 64), (1, 65, 127), (1, 129, 128), (2
 # Batches that reach every tile of the products: 64 (split), 128 in one round and more, 256 (also with
 # tiles that end past the padded matrix), and, for bf16, steps in groups (long sides of 1.5 times the short).
 BATCHES = [(3, 500, 700), (6, 700, 500), (8, 256, 1024), (9, 600, 1300), (24, 520, 330), (150, 300, 300),
-           (150, 180, 460), (16, 1024, 1024)]
+           (150, 180, 460), (16, 1024, 1024), (90, 256, 256), (17, 500, 1000), (1, 2100, 2100)]
 
 
 def gradient(B, M, N, seed, size=1e-3):
