@@ -744,20 +744,22 @@ __global__ __launch_bounds__(256, 2) void ns_product_mixed_kernel(const MulArgs 
     product_tile<MODE, 1, 2>(a, b, i0, j0, !SYM || i0 != j0, st0, st1, none, none);
 }
 
-// 256 x 256 tiles for long grids: eight wavefronts of 128 x 64, two stages of
-// 64 KiB, one workgroup a compute unit.  A byte from memory feeds twice the
-// products of a 128-tile, and an LDS byte 1.5 times.  Operands are held in
-// registers for one half of the columns of a K step: one half is read while the
-// other is multiplied, so the buffer of a stage is free in the middle of its
-// step and the next but one has a whole step to arrive.
-constexpr int LT = 256, LOPB = LT / 32 * BLOCK;
+// 256 x 256 tiles for long grids: eight wavefronts of 128 x 64, one workgroup a
+// compute unit.  A byte from memory feeds twice the products of a 128-tile,
+// and an LDS byte 1.5 times.  A stage is one half of the columns of a K step
+// (32 KiB), in a ring of four, held in registers for the one that is multiplied
+// and the one that is read: a stage has three half steps to arrive.
+constexpr int LT = 256;
 template <int MODE>
 __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs a) {
     constexpr bool SYM = MODE == GRAM || MODE == SYMM;
-    constexpr int QUAD = BT * TLD * 4;       // a quadrant of the fp32 tile
-    static_assert(QUAD >= 2 * LOPB, "a quadrant covers a stage");
-    __shared__ __attribute__((aligned(1024))) char st0[QUAD];
-    __shared__ __attribute__((aligned(1024))) char st1[QUAD];
+    constexpr int NB = LT / 32, PIECE = 1024, OPB = NB * 2 * PIECE;      // a block's hi and lo halves
+    // in the end two of them hold a quadrant of the fp32 tile
+    __shared__ __attribute__((aligned(1024))) char st0[tile_bytes<2>()];
+    __shared__ __attribute__((aligned(1024))) char st1[tile_bytes<2>()];
+    __shared__ __attribute__((aligned(1024))) char st2[tile_bytes<2>()];
+    __shared__ __attribute__((aligned(1024))) char st3[tile_bytes<2>()];
+    static_assert(tile_bytes<2>() >= 2 * OPB, "a stage fits");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int b, ti, tj;
@@ -766,12 +768,13 @@ __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs 
     const int KT = a.K / KB;     // even
     const char* ps = a.p + b * a.p_stride + (int64_t)min((i0 >> 5) + wave, (a.pr >> 5) - 1) * KT * BLOCK;
     const char* qs = a.q + b * a.q_stride + (int64_t)min((j0 >> 5) + wave, (a.qr >> 5) - 1) * KT * BLOCK;
-    auto issue = [&](int n, char* st) {
-        const int64_t o = (int64_t)n * BLOCK + lane * 16;
+    // half step h: columns 16 (h & 1) .. of block h / 2
+    auto issue = [&](int h, char* st) {
+        const int64_t o = (int64_t)(h >> 1) * BLOCK + (h & 1) * HALF + lane * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            load_lds16(ps + o + j * 1024, st + wave * BLOCK + j * 1024);
-            load_lds16(qs + o + j * 1024, st + LOPB + wave * BLOCK + j * 1024);
+        for (int j = 0; j < 2; ++j) {
+            load_lds16(ps + o + j * LO, st + (2 * wave + j) * PIECE);
+            load_lds16(qs + o + j * LO, st + OPB + (2 * wave + j) * PIECE);
         }
     };
     const int wi = wave >> 2, wj = wave & 3, rl = lane & 31, kh = lane >> 5;
@@ -783,58 +786,59 @@ __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs 
     struct Frags {
         f16x8_t ph[4], pl[4], qh[2], ql[2];
     };
-    auto read = [&](const char* st, int ks, Frags& f) {
+    auto read = [&](const char* st, Frags& f) {
         auto frag = [&](const char* p) { return __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(p + lane * 16)); };
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const char* qb = st + LOPB + (2 * wj + j) * BLOCK + ks * HALF;
+            const char* qb = st + OPB + (2 * wj + j) * 2 * PIECE;
             f.qh[j] = frag(qb);
-            f.ql[j] = frag(qb + LO);
+            f.ql[j] = frag(qb + PIECE);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const char* pb = st + (4 * wi + i) * BLOCK + ks * HALF;
+            const char* pb = st + (4 * wi + i) * 2 * PIECE;
             f.ph[i] = frag(pb);
-            f.pl[i] = frag(pb + LO);
+            f.pl[i] = frag(pb + PIECE);
         }
     };
-    auto compute = [&](const Frags& f) { mul3(acc, f.ph, f.pl, f.qh, f.ql); };
-    auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
-    // stage n in `cur`, its first half in f0
-    Frags f0, f1;
-    auto step = [&](int n, char* cur, const char* nxt) {
-        read(cur, 1, f1);
-        compute(f0);
-#pragma unroll
-        for (int i = 0; i < 12; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-        fence();
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));   // stage n + 1 has landed, stage n is read
+    // Half step h, its operands already in registers: wait until stage h + 1 has
+    // landed (the two after it may be on their way) and this wavefront's reads
+    // of stage h are done; after the barrier its buffer takes stage h + 4.
+    const int last = 2 * KT - 1;
+    auto step = [&](int h, const Frags& fc, Frags& fn, char* cur, const char* nxt) {
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 0));
         __builtin_amdgcn_s_barrier();
-        fence();
-        issue(min(n + 2, KT - 1), cur);
-        read(nxt, 0, f0);
-        compute(f1);
+        __builtin_amdgcn_sched_barrier(0);
+        issue(min(h + 4, last), cur);
+        read(nxt, fn);
+        mul3(acc, fc.ph, fc.pl, fc.qh, fc.ql);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // matrix instruction
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // transfer
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
-        fence();
+        __builtin_amdgcn_sched_barrier(0);
     };
+    Frags f0, f1;
     issue(0, st0);
-    issue(min(1, KT - 1), st1);
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 15));
+    issue(1, st1);
+    issue(2, st2);               // 2 KT >= 4
+    issue(3, st3);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(12, 15));
     __builtin_amdgcn_s_barrier();
-    read(st0, 0, f0);
-    fence();
-    for (int n = 0; n < KT; n += 2) {
-        step(n, st0, st1);
-        step(n + 1, st1, st0);
+    read(st0, f0);
+    __builtin_amdgcn_sched_barrier(0);
+    for (int h = 0; h <= last; h += 4) {
+        step(h, f0, f1, st0, st1);
+        step(h + 1, f1, f0, st1, st2);
+        step(h + 2, f0, f1, st2, st3);
+        step(h + 3, f1, f0, st3, st0);
     }
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
     __syncthreads();
@@ -853,21 +857,21 @@ __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs 
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int g = 0; g < 16; ++g)
-                        ((float*)(wj < 2 ? st0 : st1))[(32 * i + acc_row(g, kh)) * TLD + 64 * (wj & 1) + 32 * j + rl] =
-                            acc[i][j][g];
+                        ((float*)(wj < 2 ? (i < 2 ? st0 : st1) : (i < 2 ? st2 : st3)))[(32 * (i & 1) + acc_row(g, kh)) * TLD +
+                                                                                    64 * (wj & 1) + 32 * j + rl] = acc[i][j][g];
         }
         __syncthreads();
-        auto quadrant = [&](char* st, int qj) {
+        auto quadrant = [&](char* top, char* bottom, int qj) {
             if (j0 + BT * qj >= a.qr) return;
-            auto at = [&](int r, int c) -> float& { return ((float*)st)[r * TLD + c]; };
+            auto at = [&](int r, int c) -> float& { return ((float*)(r < 64 ? top : bottom))[(r & 63) * TLD + c]; };
             auto sum8 = [&](int r, int c, float* v) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = at(r, c + e);
             };
             epilogue<MODE, BT, 512>(a, b, i0 + BT * qi, j0 + BT * qj, true, sum8, at);
         };
-        quadrant(st0, 0);
-        quadrant(st1, 1);
+        quadrant(st0, st1, 0);
+        quadrant(st2, st3, 1);
         __syncthreads();
     }
 }
