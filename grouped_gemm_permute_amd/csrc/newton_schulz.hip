@@ -45,6 +45,7 @@ namespace {
 
 using namespace mfma;
 
+typedef __attribute__((address_space(3))) float lds_float_t;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
 
@@ -548,37 +549,43 @@ __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0
     }
 }
 
-// Tiles of T = 64 NI rows and columns, four wavefronts of 32 NI x 32 NI each, a
-// ring of NS stages of 16 NI KiB.  NS = 2: as many workgroups as fit share a
-// compute unit, one's epilogue under the others' matrix instructions.  NS = 3 (NI =
-// 1) or 4 (NI = 2), for grids of about one workgroup a compute unit: a stage has
-// two or three steps to arrive (k = 48, 156 tiles of 64: 16.4 us, 22.3 with two
-// stages; four were no faster).  NI = 1 for grids that 128-tiles would leave half
-// empty.
-template <int NI>
+// Tiles of T = 64 NI rows and columns, four wavefronts of 32 NI x 32 NI each.  A
+// stage holds KS halves of a K step (16 columns each), in a ring of NS stages;
+// operands are in registers for the stage that is multiplied and the one that is
+// read.  As many workgroups as fit share a compute unit, one's epilogue under
+// the others' matrix instructions.
+//  * KS = 1, NS = 4: a stage has three half steps to arrive, in the LDS of two
+//    whole ones (against a ring of two whole steps: 576 128-tiles, k = 128: 253 ->
+//    213 us; 4096 tiles, k = 32: 451 -> 429; 78 64-tiles, k = 48: 21.8 -> 14.5)
+//  * KS = 2, NS = 2: half the barriers, for 64-tiles with two or three workgroups a
+//    unit (528 tiles, k = 256: 158 -> 134 us; 640, k = 32: 25.8 -> 23.8; at 408,
+//    k = 64, it loses: 25.7 -> 32.4)
+template <int NI, int KS>
 constexpr int stage_bytes() {
-    return 2 * 2 * NI * BLOCK;
+    return 4 * NI * KS * (BLOCK / 2);
 }
-// Bytes of the first two stages, which hold a half of the fp32 tile each in the end.
-template <int NI>
-constexpr int tile_bytes() {
-    constexpr int T = 64 * NI, half = T / 2 * (T + 1) * 4;
-    return half > stage_bytes<NI>() ? half : stage_bytes<NI>();
+// Bytes of a stage's buffer; in the end each holds rows of the fp32 tile, T / NS of them.
+template <int NI, int KS, int NS>
+constexpr int buffer_bytes() {
+    constexpr int T = 64 * NI, rows = T / NS * (T + 1) * 4;
+    return rows > stage_bytes<NI, KS>() ? rows : stage_bytes<NI, KS>();
 }
 // The tile at rows i0, columns j0 of matrix b.  The stages are separate objects, so
-// that a read of one does not wait for the transfers into the others.
-template <int MODE, int NI, int NS>
+// that a read of one does not wait for the transfers into the others (st2 and
+// st3 with NS = 4 only).
+template <int MODE, int NI, int KS, int NS>
 __device__ __forceinline__ void product_tile(const MulArgs& a, int b, int i0, int j0, bool both, char* st0,
                                              char* st1, char* st2, char* st3) {
-    constexpr int T = 64 * NI, NB = T / 32, LD = T + 1, OPB = NB * BLOCK;
+    constexpr int T = 64 * NI, NB = T / 32, LD = T + 1;
+    constexpr int PIECE = 1024, ENTRY = 2 * KS * PIECE;      // a block's share of a stage: [plane][half]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     // stage sources: wavefront w brings blocks w NB / 2 .. of the P then Q block
-    // rows, four transfers of 1 KiB each.  Block rows past the padded end (tiles
+    // rows, 2 KS transfers of 1 KiB each.  Block rows past the padded end (tiles
     // that end outside) read the last one and are not stored.
-    const int KT = a.K / KB;
-    constexpr int MINE = NB / 2, PER_STAGE = 4 * MINE;
+    const int KT = a.K / KB;     // even
+    constexpr int MINE = NB / 2, PER_STAGE = 2 * KS * MINE;
     const char* src[MINE];
 #pragma unroll
     for (int i = 0; i < MINE; ++i) {
@@ -588,12 +595,13 @@ __device__ __forceinline__ void product_tile(const MulArgs& a, int b, int i0, in
         src[i] = (second ? a.q + b * a.q_stride : a.p + b * a.p_stride) + (int64_t)row * KT * BLOCK;
     }
     auto issue = [&](int n, char* st) {
-        const int64_t o = (int64_t)n * BLOCK + lane * 16;
+        const int64_t o = KS == 2 ? (int64_t)n * BLOCK : (int64_t)(n >> 1) * BLOCK + (n & 1) * HALF;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 2 * KS; ++j)
 #pragma unroll
             for (int i = 0; i < MINE; ++i)
-                load_lds16(src[i] + o + j * 1024, st + (wave * MINE + i) * BLOCK + j * 1024);
+                load_lds16(src[i] + o + (j / KS) * LO + (j % KS) * HALF + lane * 16,
+                           st + (wave * MINE + i) * ENTRY + j * PIECE);
     };
 
     const int wi = wave >> 1, wj = wave & 1, rl = lane & 31, kh = lane >> 5;
@@ -604,42 +612,40 @@ __device__ __forceinline__ void product_tile(const MulArgs& a, int b, int i0, in
         for (int j = 0; j < NI; ++j) acc[i][j] = f32x16_t{};
 
     struct Frags {
-        f16x8_t ph[2][NI], pl[2][NI], qh[2][NI], ql[2][NI];   // [k16 slice][block]
+        f16x8_t ph[KS][NI], pl[KS][NI], qh[KS][NI], ql[KS][NI];
     };
     auto read = [&](const char* st, Frags& f) {
         auto frag = [&](const char* p) { return __builtin_bit_cast(f16x8_t, *(const u32x4_t*)(p + lane * 16)); };
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const char* pb = st + (NI * wi + i) * BLOCK + ks * HALF;
-                const char* qb = st + OPB + (NI * wj + i) * BLOCK + ks * HALF;
+                const char* pb = st + (NI * wi + i) * ENTRY + ks * PIECE;
+                const char* qb = st + (NB + NI * wj + i) * ENTRY + ks * PIECE;
                 f.ph[ks][i] = frag(pb);
-                f.pl[ks][i] = frag(pb + LO);
+                f.pl[ks][i] = frag(pb + KS * PIECE);
                 f.qh[ks][i] = frag(qb);
-                f.ql[ks][i] = frag(qb + LO);
+                f.ql[ks][i] = frag(qb + KS * PIECE);
             }
     };
-    auto compute = [&](const Frags& f) {
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) mul3(acc, f.ph[ks], f.pl[ks], f.qh[ks], f.ql[ks]);
-    };
-    // Step n, its operands already in registers: wait until stage n + 1 has
+    // Stage n, its operands already in registers: wait until stage n + 1 has
     // landed and this wavefront's reads of stage n are done; after the barrier
     // stage n's buffer is free, so stage n + NS is sent there, stage n + 1 is
     // read into the other registers and the matrix instructions of stage n run
     // over both.  Past the last stage the last one is sent and read again, so
     // that every step is alike.
+    const int last = 2 * KT / KS - 1;
     auto step = [&](int n, const Frags& fc, Frags& fn, char* cur, const char* nxt) {
         __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 2) * PER_STAGE, 0));
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        issue(min(n + NS, KT - 1), cur);
+        issue(min(n + NS, last), cur);
         read(nxt, fn);
-        compute(fc);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) mul3(acc, fc.ph[ks], fc.pl[ks], fc.qh[ks], fc.ql[ks]);
         if constexpr (NI == 2) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4 * KS; ++i) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // matrix instruction
                 __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // transfer
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
@@ -650,50 +656,45 @@ __device__ __forceinline__ void product_tile(const MulArgs& a, int b, int i0, in
         }
         __builtin_amdgcn_sched_barrier(0);
     };
+    static_assert(NS == 2 || (NS == 4 && KS == 1), "stages in fours: 2 KT is a multiple of 4");
     Frags f0, f1;
     issue(0, st0);
-    issue(min(1, KT - 1), st1);
-    if constexpr (NS >= 3) issue(min(2, KT - 1), st2);
-    if constexpr (NS == 4) issue(min(3, KT - 1), st3);
+    issue(1, st1);
+    if constexpr (NS == 4) {
+        issue(2, st2);
+        issue(3, st3);
+    }
     __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 1) * PER_STAGE, 15));   // stage 0 has landed
     __builtin_amdgcn_s_barrier();
     read(st0, f0);
-    if constexpr (NS == 2) {
-        for (int n = 0; n < KT; n += 2) {        // KT is even
-            step(n, f0, f1, st0, st1);
+    for (int n = 0; n <= last; n += NS) {
+        step(n, f0, f1, st0, st1);
+        if constexpr (NS == 2) {
             step(n + 1, f1, f0, st1, st0);
-        }
-    } else if constexpr (NS == 3) {
-        for (int n = 0;; n += 6) {
-            step(n, f0, f1, st0, st1);
+        } else {
             step(n + 1, f1, f0, st1, st2);
-            if (n + 2 >= KT) break;
-            step(n + 2, f0, f1, st2, st0);
-            step(n + 3, f1, f0, st0, st1);
-            if (n + 4 >= KT) break;
-            step(n + 4, f0, f1, st1, st2);
-            step(n + 5, f1, f0, st2, st0);
-            if (n + 6 >= KT) break;
-        }
-    } else {
-        for (int n = 0;; n += 4) {
-            step(n, f0, f1, st0, st1);
-            step(n + 1, f1, f0, st1, st2);
-            if (n + 2 >= KT) break;
             step(n + 2, f0, f1, st2, st3);
             step(n + 3, f1, f0, st3, st0);
-            if (n + 4 >= KT) break;
         }
     }
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));           // before the buffers are used anew
     __syncthreads();
 
     if constexpr (MODE != FINAL) {
-        epilogue_blocks<MODE>(a, b, (i0 >> 5) + NI * wi, (j0 >> 5) + NI * wj, both, acc, st0 + wave * BLOCK);
+        char* mine = NS == 2 ? st0 + wave * BLOCK : wave == 0 ? st0 : wave == 1 ? st1 : wave == 2 ? st2 : st3;
+        epilogue_blocks<MODE>(a, b, (i0 >> 5) + NI * wi, (j0 >> 5) + NI * wj, both, acc, mine);
         return;
     }
-    // ---- the target: the fp32 tile through LDS
-    auto at = [&](int r, int c) -> float& { return ((float*)(r < T / 2 ? st0 : st1))[(r & (T / 2 - 1)) * LD + c]; };
+    // ---- the target: the fp32 tile through LDS, T / NS rows a buffer
+    // (a sum of distances: choosing among four pointers kept them in scratch memory)
+    lds_float_t* const first = (lds_float_t*)st0;
+    const int d1 = (lds_float_t*)st1 - first, d2 = (lds_float_t*)st2 - (lds_float_t*)st1,
+              d3 = (lds_float_t*)st3 - (lds_float_t*)st2;
+    auto at = [=](int r, int c) -> lds_float_t& {
+        constexpr int rows = T / NS;
+        const int to = (r >= rows ? d1 : 0) + (NS == 4 && r >= 2 * rows ? d2 : 0) + (NS == 4 && r >= 3 * rows ? d3 : 0);
+        return first[to + (r & (rows - 1)) * LD + c];
+    };
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -709,16 +710,17 @@ __device__ __forceinline__ void product_tile(const MulArgs& a, int b, int i0, in
     epilogue<MODE, T, 256>(a, b, i0, j0, true, sum8, at);
 }
 
-template <int MODE, int NI, int NS>
-__global__ __launch_bounds__(256, NI == 2 && NS == 4 ? 1 : 2) void ns_product_kernel(const MulArgs a) {
+template <int MODE, int NI, int KS, int NS>
+__global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
     constexpr bool SYM = MODE == GRAM || MODE == SYMM;
-    __shared__ __attribute__((aligned(1024))) char st0[tile_bytes<NI>()];
-    __shared__ __attribute__((aligned(1024))) char st1[tile_bytes<NI>()];
-    __shared__ __attribute__((aligned(1024))) char st2[NS >= 3 ? stage_bytes<NI>() : 16];
-    __shared__ __attribute__((aligned(1024))) char st3[NS == 4 ? stage_bytes<NI>() : 16];
+    constexpr int BYTES = buffer_bytes<NI, KS, NS>(), MORE = NS == 4 ? BYTES : 16;
+    __shared__ __attribute__((aligned(1024))) char st0[BYTES];
+    __shared__ __attribute__((aligned(1024))) char st1[BYTES];
+    __shared__ __attribute__((aligned(1024))) char st2[MORE];
+    __shared__ __attribute__((aligned(1024))) char st3[MORE];
     int b, ti, tj;
     tile_of<SYM>(a, xcd_remap(blockIdx.x, gridDim.x), b, ti, tj);
-    product_tile<MODE, NI, NS>(a, b, 64 * NI * ti, 64 * NI * tj, !SYM || ti != tj, st0, st1, st2, st3);
+    product_tile<MODE, NI, KS, NS>(a, b, 64 * NI * ti, 64 * NI * tj, !SYM || ti != tj, st0, st1, st2, st3);
 }
 
 // 128-tiles in full rounds of 256 and the few that remain as four 64-tiles each,
@@ -728,20 +730,22 @@ __global__ __launch_bounds__(256, NI == 2 && NS == 4 ? 1 : 2) void ns_product_ke
 template <int MODE>
 __global__ __launch_bounds__(256, 2) void ns_product_mixed_kernel(const MulArgs a) {
     constexpr bool SYM = MODE == GRAM || MODE == SYMM;
-    __shared__ __attribute__((aligned(1024))) char st0[tile_bytes<2>()];
-    __shared__ __attribute__((aligned(1024))) char st1[tile_bytes<2>()];
-    __shared__ __attribute__((aligned(1024))) char none[16];
+    constexpr int BYTES = buffer_bytes<2, 1, 4>();
+    __shared__ __attribute__((aligned(1024))) char st0[BYTES];
+    __shared__ __attribute__((aligned(1024))) char st1[BYTES];
+    __shared__ __attribute__((aligned(1024))) char st2[BYTES];
+    __shared__ __attribute__((aligned(1024))) char st3[BYTES];
     int b, ti, tj;
     if ((int)blockIdx.x < a.whole) {
         tile_of<SYM>(a, xcd_remap(blockIdx.x, a.whole), b, ti, tj);
-        product_tile<MODE, 2, 2>(a, b, BT * ti, BT * tj, !SYM || ti != tj, st0, st1, none, none);
+        product_tile<MODE, 2, 1, 4>(a, b, BT * ti, BT * tj, !SYM || ti != tj, st0, st1, st2, st3);
         return;
     }
     const int id = xcd_remap(blockIdx.x - a.whole, gridDim.x - a.whole);
     tile_of<SYM>(a, a.whole + (id >> 2), b, ti, tj);
     const int i0 = BT * ti + 64 * ((id >> 1) & 1), j0 = BT * tj + 64 * (id & 1);
     if (i0 >= a.pr || j0 >= a.qr || (SYM && i0 < j0)) return;
-    product_tile<MODE, 1, 2>(a, b, i0, j0, !SYM || i0 != j0, st0, st1, none, none);
+    product_tile<MODE, 1, 1, 4>(a, b, i0, j0, !SYM || i0 != j0, st0, st1, st2, st3);
 }
 
 // 256 x 256 tiles for long grids: eight wavefronts of 128 x 64, one workgroup a
@@ -755,11 +759,12 @@ __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs 
     constexpr bool SYM = MODE == GRAM || MODE == SYMM;
     constexpr int NB = LT / 32, PIECE = 1024, OPB = NB * 2 * PIECE;      // a block's hi and lo halves
     // in the end two of them hold a quadrant of the fp32 tile
-    __shared__ __attribute__((aligned(1024))) char st0[tile_bytes<2>()];
-    __shared__ __attribute__((aligned(1024))) char st1[tile_bytes<2>()];
-    __shared__ __attribute__((aligned(1024))) char st2[tile_bytes<2>()];
-    __shared__ __attribute__((aligned(1024))) char st3[tile_bytes<2>()];
-    static_assert(tile_bytes<2>() >= 2 * OPB, "a stage fits");
+    constexpr int BYTES = BT / 2 * TLD * 4;
+    static_assert(BYTES >= 2 * OPB, "a stage fits");
+    __shared__ __attribute__((aligned(1024))) char st0[BYTES];
+    __shared__ __attribute__((aligned(1024))) char st1[BYTES];
+    __shared__ __attribute__((aligned(1024))) char st2[BYTES];
+    __shared__ __attribute__((aligned(1024))) char st3[BYTES];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int b, ti, tj;
@@ -863,7 +868,11 @@ __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs 
         __syncthreads();
         auto quadrant = [&](char* top, char* bottom, int qj) {
             if (j0 + BT * qj >= a.qr) return;
-            auto at = [&](int r, int c) -> float& { return ((float*)(r < 64 ? top : bottom))[(r & 63) * TLD + c]; };
+            lds_float_t* const first = (lds_float_t*)top;
+            const int down = (lds_float_t*)bottom - first;
+            auto at = [=](int r, int c) -> lds_float_t& {
+                return first[(r < 64 ? 0 : down) + (r & 63) * TLD + c];
+            };
             auto sum8 = [&](int r, int c, float* v) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = at(r, c + e);
@@ -1287,24 +1296,25 @@ double scale_for(double bound) {
 }
 
 // The tile a product runs on: the one whose estimate is the least.  The estimates
-// are fits (us of one launch; n tiles, k steps of 32; 256 compute units) to 130
-// launches of 1 to 64 matrices with short sides of 128 to 4096 and k of 4 to 128,
-// most within 15%:
-//  * 32, split over K:  4 + n (0.0022 + 0.0003 k), 0.0005 k where an operand
+// are fits (us of one launch; n tiles, k steps of 32; 256 compute units) to 40
+// products of 1 to 64 matrices with short sides of 256 to 4096 and k of 8 to 256, each
+// timed on every tile.  They are within 15% mostly, and their choice
+// is within 6% of the best of them, most often the best:
+//  * 32, split over K:  each tile costs by itself, and more where an operand
 //    outgrows an XCD's 4 MiB of L2
-//  * 64, three stages:  4 + k max(0.235, 0.00096 n)
-//    64, two stages:    4 + k max(0.385, 0.00092 n), 0.0011 n beyond 1000 tiles
-//  * 128, four stages:  8 + k max(0.5, 0.003 n), n <= 256
-//    128, two stages:   8 + k max(0.57, 0.0032 n); beyond 512 tiles 0.0034 n, 0.0038 n
-//    with an outgrown operand; mixed with 64 where at most 64 are over a
-//    multiple of 256 (336 tiles: 59, mixed 62): 12 + the same for the multiple
-//  * 256:               24 r - 12 + k (1.1 r + 0.0048 n) in r rounds of 256
-// Measured on both sides of the borders: k = 24, one 768 x 1536 matrix's A A 7.8 us
-// on 32-tiles, 10.8 on 64; eight of them 25.6, 18.6 on 64, 21.1 on 128; their B X
-// 84, 55.7, 55.9 and 55.7 on 256-tiles; sixteen 1024 x 4096 matrices' B X (k = 32) 586
-// on 64, 453 on 128, 408 on 256.
+//  * 64 and 128:        a floor by the waits of a K step while units are idle, then by
+//    the tiles; 128-tiles mixed with 64 where at most 64 are over a multiple of 256
+//    (336 tiles: 57, mixed 56; 528 tiles: 227, mixed 195)
+//  * 256:               by rounds of 256 workgroups, one a unit, and tiles
+// Measured on both sides of the borders, 32 / 64 (half steps, whole) / 128 (or mixed) /
+// 256: k = 48, one 768 x 1536 matrix's A 10.4 / 14.5, 21.8 / 25.7 / 78 us, two of them 14.2 /
+// 14.9, 21.9 / 26.0 / 77, eight 39.9 / 31.6, 31.5 / 32.2 / 78; k = 24, B X of two 24.7 /
+// 18.9, 18.5 / 18.9 / 50, of four 44.8 / 30.7, 34.2 / 27.5 / 51, of sixteen 208 / 139, 137 / 108 /
+// 131; k = 32, of sixteen 1024 x 4096 matrices - / 622, 584 / 429 / 406.
 struct Choice {
-    int tile, stages, whole;     // whole: mixed, how many of 128
+    int tile;
+    bool halves;     // 64: four half steps; else two whole ones
+    int whole;       // 128, mixed: how many of 128
 };
 Choice choose(int64_t n32, int64_t n64, int64_t n128, int64_t n256, int k, bool outgrown) {
     const int64_t r = (n256 + 255) / 256, over = n128 % 256;
@@ -1314,16 +1324,15 @@ Choice choose(int64_t n32, int64_t n64, int64_t n128, int64_t n256, int k, bool 
         Choice c;
         double us;
     } all[] = {
-        {{32, 0, 0}, 4. + n32 * (0.0022 + (outgrown ? 0.0005 : 0.0003) * k)},
-        {{64, 3, 0}, 4. + k * fmax(0.235, 0.00096 * n64)},
-        {{64, 2, 0}, 4. + k * fmax(0.385, (n64 <= 1000 ? 0.00092 : 0.0011) * n64)},
-        {{128, 4, 0}, n128 <= 256 ? 8. + k * fmax(0.5, 0.003 * n128) : 1e30},
-        {{128, 2, mixed ? (int)n : 0},
-         (mixed ? 12. : 8.) + k * fmax(0.57, (n <= 512 ? 0.0032 : outgrown ? 0.0038 : 0.0034) * n)},
-        {{256, 2, 0}, 24. * r - 12. + k * (1.1 * r + 0.0048 * n256)},
+        {{32, false, 0}, 4. + n32 * (0.0022 + (outgrown ? 0.0005 : 0.0003) * k)},
+        {{64, true, 0}, 4. + k * fmax(0.22, 0.00096 * n64)},
+        {{64, false, 0}, 4. + k * fmax(0.385, n64 <= 1000 ? 0.13 + 0.00072 * n64 : 0.0011 * n64)},
+        {{128, true, mixed ? (int)n : 0},
+         (mixed ? 12. : 8.) + k * fmax(0.48, (n <= 256 ? 0.0028 : n <= 512 ? 0.0032 : outgrown ? 0.0033 : 0.0031) * n)},
+        {{256, false, 0}, 24. * r - 12. + k * (1.1 * r + 0.0048 * n256)},
     };
     int best = 0;
-    for (int i = 1; i < 6; ++i)
+    for (int i = 1; i < 5; ++i)
         if (all[i].us < all[best].us) best = i;
     return all[best].c;
 }
@@ -1341,17 +1350,15 @@ bool launch_product(MulArgs& g, int B, hipStream_t stream) {
     const unsigned n = (unsigned)grid(c.tile);
     if (c.tile == 32)
         ns_product_split_kernel<MODE><<<n, 64 * DW, 0, stream>>>(g);
-    else if (c.tile == 64 && c.stages == 3)
-        ns_product_kernel<MODE, 1, 3><<<n, 256, 0, stream>>>(g);
+    else if (c.tile == 64 && c.halves)
+        ns_product_kernel<MODE, 1, 1, 4><<<n, 256, 0, stream>>>(g);
     else if (c.tile == 64)
-        ns_product_kernel<MODE, 1, 2><<<n, 256, 0, stream>>>(g);
-    else if (c.tile == 128 && c.stages == 4)
-        ns_product_kernel<MODE, 2, 4><<<n, 256, 0, stream>>>(g);
+        ns_product_kernel<MODE, 1, 2, 2><<<n, 256, 0, stream>>>(g);
     else if (c.whole) {
         g.whole = c.whole;
         ns_product_mixed_kernel<MODE><<<c.whole + 4 * (n - c.whole), 256, 0, stream>>>(g);
     } else if (c.tile == 128)
-        ns_product_kernel<MODE, 2, 2><<<n, 256, 0, stream>>>(g);
+        ns_product_kernel<MODE, 2, 1, 4><<<n, 256, 0, stream>>>(g);
     else
         ns_product_large_kernel<MODE><<<n, 512, 0, stream>>>(g);
     return hipGetLastError() == hipSuccess;
