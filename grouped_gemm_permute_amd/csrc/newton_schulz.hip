@@ -1371,8 +1371,13 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
         return MOE_ERR_INVALID_ARG;
     double mid[kMaxSteps], whole[kMaxSteps], top[kMaxSteps + 1];
     top[0] = 1.;
-    for (int k = 0; k < steps; ++k)
+    for (int k = 0; k < steps; ++k) {
         if (!step_bounds(a, b, c, top[k], &mid[k], &whole[k], &top[k + 1])) return MOE_ERR_UNSUPPORTED;
+        // what shrinks this far leaves fp16's range at the largest scale (all
+        // zero coefficients are exact)
+        if (top[k] != 0. && top[k] < 1e-9) return MOE_ERR_UNSUPPORTED;
+        if (whole[k] != 0. && whole[k] < (1. + fabs(b) + fabs(c)) * 1e-12) return MOE_ERR_UNSUPPORTED;
+    }
     if (B == 0) return MOE_OK;
     (void)hipGetLastError();
     auto ok = [] { return hipGetLastError() == hipSuccess; };
@@ -1447,7 +1452,15 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     };
     int turn = 0;
     for (int k = 0; k < steps;) {
-        const int group = grouped ? ((steps - k) % 2 && steps - k > 1 ? 3 : (steps - k > 1 ? 2 : 1)) : 1;
+        int group = grouped ? ((steps - k) % 2 && steps - k > 1 ? 3 : (steps - k > 1 ? 2 : 1)) : 1;
+        // alpha and R cancel where the steps bring a singular value near 1: what
+        // their 22 bits leave there is 2^-22 of the largest product of the P_j,
+        // which stays at 2^-16 (three steps of the usual coefficients: 41)
+        double product = 1.;
+        for (int j = 0; j < group; ++j) {
+            product *= whole[k + j];
+            if (product > 64.) group = j > 0 ? j : 1;
+        }
         Plane A = {ws + L.sym[0], scale_for(top[k] * top[k])}, U = {ws + L.sym[1], 0.};
         // where S and R are by turns: an S may be the R of the next step
         Plane S = {}, R = {};

@@ -527,7 +527,8 @@ moe_status moe_ffn_backward_cached_timed(const void *x, const int32_t *topk_idx,
  *
  * Arithmetic is fp32: the row is held in registers, the variance is the sum
  * of squared deviations from its mean, y is rounded once.  A row that holds
- * an infinity or NaN gives NaN in its own outputs alone.  h may be x or
+ * an infinity or NaN gives NaN in its own outputs alone (rms beside an
+ * infinity: 0).  h may be x or
  * residual and y may be x (the same buffer, not a shifted one).
  *
  * D may be any size up to 16384; rows are dense.  x, residual, weight,
@@ -613,7 +614,9 @@ size_t moe_newton_schulz_workspace_size(int B, int M, int N);
  * or N < 1, steps outside [1, 64], eps negative, eps or a coefficient not
  * finite, unknown dtype); MOE_ERR_UNSUPPORTED (M or N > 32768, B > 65535,
  * 2^24 or more 128 x 128 tiles in all, coefficients that let a singular value
- * in [0, 1] or the polynomial b A + c A A grow beyond 10^4 within the steps);
+ * in [0, 1] or the polynomial b A + c A A grow beyond 10^4 within the steps, or
+ * that shrink all of them below 10^-9 before the last step, or a + b A + c A A
+ * below 10^-12 (1 + |b| + |c|); all three zero will do);
  * MOE_ERR_WORKSPACE; MOE_ERR_HIP.  G and out are 16-byte aligned.  B == 0
  * launches nothing.
  */

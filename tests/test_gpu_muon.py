@@ -137,7 +137,8 @@ def test_muon_step_batches(B, M, N, dtype):
 
 @pytest.mark.parametrize("M,N", [(24, 90), (90, 24), (96, 160), (160, 96)])
 @pytest.mark.parametrize("steps,coeffs", [(1, MUON), (2, MUON), (6, MUON), (7, (1.5, -0.5, 0.0)), (3, (2.0, -1.5, 0.5)),
-                                          (2, (0.0, 0.0, 0.0)), (4, (1e-3, 0.0, 0.0))])
+                                          (2, (0.0, 0.0, 0.0)), (4, (1e-3, 0.0, 0.0)), (10, (0.1, 0.0, 0.0)),
+                                          (2, (0.0, 0.1, 0.0))])
 def test_steps_and_coefficients(M, N, steps, coeffs):
     G = gradient(2, M, N, 77)
     say(f"newton_schulz {M}x{N} steps{steps} {coeffs}")
@@ -273,3 +274,21 @@ def test_captured_and_replayed(M, N):
         gg.muon_step(W2, dW, mom2, 0.02)
         torch.cuda.synchronize()
         assert torch.equal(W, W2) and torch.equal(mom, mom2) and torch.equal(Wc, W2.bfloat16()), k
+
+
+@pytest.mark.parametrize("coeffs,steps", [(MUON, 6), ((1.5, -0.5, 0.0), 7), ((12.0, -30.0, 20.0), 2), ((4.0, -6.0, 3.0), 3)])
+def test_muon_step_batches_with_coefficients(coeffs, steps):
+    """Coefficients whose steps taken together would lose what each keeps are taken one by one."""
+    B, M, N = 16, 256, 512
+    g = torch.Generator(device="cuda").manual_seed(steps)
+    dW = 1e-3 * torch.randn(B, M, N, generator=g, device="cuda")
+    dW[:, :16] *= 8
+    W, mom = torch.zeros_like(dW), torch.zeros_like(dW)
+    say(f"muon_step {B}x{M}x{N} {coeffs} steps{steps}")
+    gg.muon_step(W, dW, mom, -1.0, beta=0.0, scale=1.0, steps=steps, coeffs=coeffs)
+    torch.cuda.synchronize()
+    X = iterate(dW, steps, coeffs, 1e-7, torch.float64)
+    norm = lambda t: t.square().sum((-1, -2)).sqrt()  # noqa: E731
+    x32 = iterate(dW.cpu(), steps, coeffs, 1e-7, torch.float32).double().cuda()
+    most = 8 * norm(x32 - X) + 16 * U * norm(X)
+    assert (norm(W.double() - X) <= most).all(), f"{(norm(W.double() - X) / norm(X)).max()} of {(most / norm(X)).max()}"

@@ -20,6 +20,8 @@ COMMON = [
     (dict(M=32769), UNS), (dict(B=65536), UNS),
     (dict(B=65535, M=4096, N=4096), UNS),                       # 2^24 tiles and more
     (dict(a=20.0), UNS), (dict(c=-500.0), UNS),                 # singular values would run away
+    (dict(a=0.1, b=0.0, c=0.0, steps=12), UNS), (dict(a=0.0, b=1e-13, c=0.0), UNS),     # or vanish
+    (dict(a=0.1, b=0.0, c=0.0, steps=9, B=0), L.MOE_OK), (dict(a=0.0, b=0.0, c=0.0, B=0), L.MOE_OK),
     (dict(B=0), L.MOE_OK),
 ]
 
