@@ -29,10 +29,18 @@
 // kernel know the matrix's own sizes.
 //
 // Each product is C = P Q^T over row-major operands: A = X X^T takes X's rows
-// twice, A A = A A^T takes A's (A is symmetric), and B X takes B's rows and
-// those of X^T; so X is kept in both orders, and an epilogue writes its tile in
-// both.  For the symmetric results only tiles on and below the diagonal are
-// computed, and their transposed tile is written beside them.
+// twice, S = b A + c A A takes A's (A is symmetric), and X <- a X + S X takes S's
+// rows and those of X^T; so X is kept in both orders, and an epilogue writes its
+// tile in both.  For the symmetric results only tiles on and below the diagonal
+// are computed, and their transposed tile is written beside them.
+//
+// What bounds the products: a compute unit draws about 36 bytes a clock from its
+// L2, whether through LDS or straight to registers.  A K step of 32 columns is
+// 16, 32 and 64 KiB of a 64-, 128- and 256-tile, so 450, 900 and 1800 clocks, against
+// 192, 768 and 3072 of matrix instructions: tiles of 64 are bound by it, those of
+// 128 by both, those of 256 by the matrix cores (52% of their cycles at sixteen
+// 1024 x 4096, the rest the epilogues of one workgroup a unit); a few matrices have
+// only small tiles enough for 256 units, and below that by the 4 us of a launch.
 #include "mfma_common.h"
 #include "moe_ffn.h"
 
@@ -457,8 +465,9 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
 // 512 consecutive bytes); for the other order the block's planes pass through 4 KiB of
 // LDS of the wavefront's own, written in the transposed order and read back with
 // the transposing read.  The addends are blocks at the transposed place, of the
-// symmetric operands or of X^T, in the order of the accumulators.  Through an fp32 tile and two passes of 8 values a thread the
-// same took about 7 us of a 128-tile; this takes 2.
+// symmetric operands or of X^T, in the order of the accumulators.  Through an
+// fp32 tile and two passes of 8 values a thread the same took about 7 us of a
+// 128-tile; this takes 2.
 template <int MODE, int NI, int NJ>
 __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0, int jb0, bool both,
                                                 const f32x16_t (&acc)[NI][NJ], char* lds) {
@@ -560,6 +569,9 @@ __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0
 //  * KS = 2, NS = 2: half the barriers, for 64-tiles with two or three workgroups a
 //    unit (528 tiles, k = 256: 158 -> 134 us; 640, k = 32: 25.8 -> 23.8; at 408,
 //    k = 64, it loses: 25.7 -> 32.4)
+// 64-tiles whose wavefronts hold the whole tile and share out the K steps,
+// straight from memory to registers, halve the LDS reads and gain nothing (624
+// tiles, k = 48: 33 us, 31.5 here): LDS is not what they wait for.
 template <int NI, int KS>
 constexpr int stage_bytes() {
     return 4 * NI * KS * (BLOCK / 2);
@@ -1308,7 +1320,7 @@ double scale_for(double bound) {
 //  * 256:               by rounds of 256 workgroups, one a unit, and tiles
 // Measured on both sides of the borders, 32 / 64 (half steps, whole) / 128 (or mixed) /
 // 256: k = 48, one 768 x 1536 matrix's A 10.4 / 14.5, 21.8 / 25.7 / 78 us, two of them 14.2 /
-// 14.9, 21.9 / 26.0 / 77, eight 39.9 / 31.6, 31.5 / 32.2 / 78; k = 24, B X of two 24.7 /
+// 14.9, 21.9 / 26.0 / 77, eight 39.9 / 31.6, 31.5 / 32.2 / 78; k = 24, S X of two 24.7 /
 // 18.9, 18.5 / 18.9 / 50, of four 44.8 / 30.7, 34.2 / 27.5 / 51, of sixteen 208 / 139, 137 / 108 /
 // 131; k = 32, of sixteen 1024 x 4096 matrices - / 622, 584 / 429 / 406.
 struct Choice {
@@ -1410,6 +1422,12 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     const int m = pad64(tall ? N : M), n = pad64(tall ? M : N);
     // a grid's threads are fewer than 2^32
     if ((int64_t)B * ((m + BT - 1) / BT) * ((n + BT - 1) / BT) >= 1 << 24) return MOE_ERR_UNSUPPORTED;
+    // Steps in groups trade 3 m^2 n products of a step for up to 4 m^3, and lose a
+    // little (all steps 3.5x fp32's error, 1.1x one by one, so not for fp32
+    // results), from long sides of 1.5 times the short on and enough tiles to
+    // share out: eight 768 x 1024 417 us one by one, 419 in groups, 768 x 1152 439,
+    // 432, 768 x 1536 537, 478; sixteen 1024 x 4096 3559, 2321; one 768 x 1536 (72
+    // tiles) 163, 167, two 231, 219.
     const bool grouped = (tgt.muon || tgt.out_bf16) && 2 * n >= 3 * m &&
                          (int64_t)B * ((m + BT - 1) / BT) * ((n + BT - 1) / BT) >= 128;
     const int nb = norm_blocks((int64_t)M * N);
