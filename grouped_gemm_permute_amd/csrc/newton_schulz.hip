@@ -737,8 +737,8 @@ __global__ __launch_bounds__(256, 2) void ns_product_kernel(const MulArgs a) {
 
 // 128-tiles in full rounds of 256 and the few that remain as four 64-tiles each,
 // so that they end sooner than a round of their own: a.whole tiles of 128,
-// then 4 (all - whole) workgroups of 64.  k = 32 steps, 576 tiles: 61 us, 69.5
-// with every tile of 128; k = 64, 272 tiles: 58 and 73.
+// then 4 (all - whole) workgroups of 64.  576 tiles, k = 32: 60 us, 68 with every
+// tile of 128; k = 128: 213 and 238; 288 tiles, k = 24: 27.5 and 33.9.
 template <int MODE>
 __global__ __launch_bounds__(256, 2) void ns_product_mixed_kernel(const MulArgs a) {
     constexpr bool SYM = MODE == GRAM || MODE == SYMM;
