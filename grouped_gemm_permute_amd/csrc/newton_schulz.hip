@@ -979,19 +979,21 @@ __global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulA
 // All products are fp64 matrix instructions of 16 x 16 x 4: a lane (g = lane / 16,
 // c = lane % 16) holds A[c][k] and B[k][c] and receives rows 4 v + g, column c of the
 // result in its value v.  The four instructions of a 16-block take k = 4 v + g, so
-// a result block is an operand as it stands: mfma4(X, Y) = X^T Y.  768 x 8 took
-// 23 us with fp64 vector products and a barrier for each; this takes 17.
+// a result block is an operand as it stands: mfma4(X, Y) = X^T Y.  Short sides of up
+// to 16 need one block, and the steps stay in one wavefront's registers (0.83 us a
+// step through LDS with a barrier for each product, 0.4 there, 0.2 up to 8 rows);
+// larger ones are four blocks, one a wavefront, and go through LDS (1.5 us a step).
 typedef __attribute__((ext_vector_type(4))) double f64x4_t;
 constexpr int SM = 32;
-// Columns of the long side a workgroup takes: all of up to 768 (short sides of
-// up to 16) or 256, in turns of 256 by 16 wavefronts in one launch (768 x 8:
-// 17 us a call, 19 in two launches; 1024 x 16: 24 and 20; 32 x 256: 21 and 23,
-// 32 x 512: 29 and 24); otherwise 128, one turn of 8 wavefronts, or more where that
-// would be over 64 chunks, whose sums each workgroup adds (32 x 4096: 27 us, 331
-// by one workgroup).
+// Columns of the long side a workgroup takes: all of up to 384 (short sides of
+// up to 16) or 256, in turns of 256 by 16 wavefronts in one launch (256 x 8: 6.9 us,
+// 9.3 in two launches; 384 x 8: 8.3, 9.3; 768 x 8: 11.7, 9.7; 768 x 16: 15.3, 10.5; 32 x 192:
+// 16.6, 17.2; 32 x 256: 18.7, 17.7); otherwise 128, one turn of 8 wavefronts, or more
+// where that would be over 64 chunks, whose sums each workgroup adds (32 x 4096:
+// 27 us, 331 by one workgroup).
 int small_chunk(int M, int N) {
     const int m = M < N ? M : N, n = M < N ? N : M;
-    if (n <= (m <= 16 ? 768 : 256)) return n;
+    if (n <= (m <= 16 ? 384 : 256)) return n;
     return n <= 64 * 128 ? 128 : ((n + 63) / 64 + 127) / 128 * 128;
 }
 int small_chunks(int M, int N) {
@@ -1123,63 +1125,115 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kChunkThreads) void ns_small_ke
     trace = __shfl(trace, 0, 64);
     const double inv = 1. / (sqrt(trace) + a.eps);
 
-    // ---- the steps: wavefront w < NB^2 owns block (bi, bj) of every matrix
-    const bool works = wave < NB * NB;
-    const int bi = NB == 1 ? 0 : wave >> 1 & 1, bj = NB == 1 ? 0 : wave & 1;
-    auto product = [&](double (*x)[NB][256], double (*y)[NB][256]) {
-        f64x4_t acc = {0., 0., 0., 0.};
+    // this wavefront's next columns of U for the end: the first on their way during the
+    // steps, where registers allow
+    const int64_t base = (int64_t)blockIdx.y * a.M * a.N;
+    float raw[NB][4];
+    auto load = [&](int l0) {
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
-            f64x4_t p, q;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) p[v] = x[k][bi][64 * v + lane], q[v] = y[k][bj][64 * v + lane];
-            acc = mfma4(p, q, acc);          // block (k, bi)^T = block (bi, k)
-        }
-        return acc;
-    };
-    auto put = [&](double (*x)[NB][256], f64x4_t r) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) x[bi][bj][64 * v + lane] = r[v];
-    };
-    f64x4_t own;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        const int i = 4 * v + g;
-        const double* blk = sum + low_block(max(bi, bj), min(bi, bj)) * 256;
-        own[v] = (bi >= bj ? blk[i * 16 + c] : blk[c * 16 + i]) * inv * inv;
-    }
-    if (works) put(A, own);
-    __syncthreads();
-    int q = 0;
-    for (int k = 0; k < a.steps; ++k) {
-        if (works) {
-            const f64x4_t sq = product(A, A);
-            f64x4_t r;
+        for (int k = 0; k < NB; ++k)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const int i = 16 * bi + 4 * v + g;
-                r[v] = (i == 16 * bj + c && i < m ? a.a : 0.) + a.b * own[v] + a.c * sq[v];
+                const int p = 16 * k + 4 * v + g, l = l0 + c;
+                raw[k][v] = p < m && l < hi
+                                ? source1(a.s, base + (tall ? (int64_t)l * m + p : (int64_t)p * n + l), false)
+                                : 0.f;
             }
-            put(P, r);
-            if (k == 0) put(Q[0], r);
+    };
+    int l0 = lo + 16 * wave;
+    if (NB == 1 && l0 < hi) load(l0);
+
+    int q = 0;
+    if constexpr (NB == 1) {
+        // ---- the steps, all in the registers of one wavefront.  Past m everything is
+        // zero, so that up to 8 half of the terms are left out
+        if (wave == 0) {
+            auto product = [&](f64x4_t x, f64x4_t y) {
+                f64x4_t r = {0., 0., 0., 0.};
+#pragma unroll
+                for (int v = 0; v < 2; ++v) r = __builtin_amdgcn_mfma_f64_16x16x4f64(x[v], y[v], r, 0, 0, 0);
+                if (m > 8) {
+#pragma unroll
+                    for (int v = 2; v < 4; ++v) r = __builtin_amdgcn_mfma_f64_16x16x4f64(x[v], y[v], r, 0, 0, 0);
+                }
+                return r;
+            };
+            f64x4_t A1, Q1;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) A1[v] = sum[(4 * v + g) * 16 + c] * inv * inv;
+            for (int k = 0; k < a.steps; ++k) {
+                f64x4_t P1 = product(A1, A1);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int i = 4 * v + g;
+                    P1[v] = (i == c && i < m ? a.a : 0.) + a.b * A1[v] + a.c * P1[v];
+                }
+                Q1 = k == 0 ? P1 : product(Q1, P1);
+                if (k + 1 < a.steps) A1 = product(product(A1, P1), P1);
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) Q[0][0][0][64 * v + lane] = Q1[v];
         }
         __syncthreads();
-        if (works) {
-            if (k > 0) put(Q[q ^ 1], product(Q[q], P));
-            if (k + 1 < a.steps) put(U, product(A, P));
+    } else {
+        // ---- the steps: wavefront w < NB^2 owns block (bi, bj) of every matrix
+        const bool works = wave < NB * NB;
+        const int bi = wave >> 1 & 1, bj = wave & 1;
+        auto product = [&](double (*x)[NB][256], double (*y)[NB][256]) {
+            f64x4_t acc = {0., 0., 0., 0.};
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                f64x4_t p, q;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) p[v] = x[k][bi][64 * v + lane], q[v] = y[k][bj][64 * v + lane];
+                acc = mfma4(p, q, acc);          // block (k, bi)^T = block (bi, k)
+            }
+            return acc;
+        };
+        auto put = [&](double (*x)[NB][256], f64x4_t r) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) x[bi][bj][64 * v + lane] = r[v];
+        };
+        f64x4_t own;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int i = 4 * v + g;
+            const double* blk = sum + low_block(max(bi, bj), min(bi, bj)) * 256;
+            own[v] = (bi >= bj ? blk[i * 16 + c] : blk[c * 16 + i]) * inv * inv;
         }
-        if (k > 0) q ^= 1;
+        if (works) put(A, own);
         __syncthreads();
-        if (k + 1 < a.steps) {
+        for (int k = 0; k < a.steps; ++k) {
             if (works) {
-                own = product(U, P);
-                put(A, own);
+                const f64x4_t sq = product(A, A);
+                f64x4_t r;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int i = 16 * bi + 4 * v + g;
+                    r[v] = (i == 16 * bj + c && i < m ? a.a : 0.) + a.b * own[v] + a.c * sq[v];
+                }
+                put(P, r);
+                if (k == 0) put(Q[0], r);
             }
             __syncthreads();
+            if (works) {
+                if (k > 0) put(Q[q ^ 1], product(Q[q], P));
+                if (k + 1 < a.steps) put(U, product(A, P));
+            }
+            if (k > 0) q ^= 1;
+            __syncthreads();
+            if (k + 1 < a.steps) {
+                if (works) {
+                    own = product(U, P);
+                    put(A, own);
+                }
+                __syncthreads();
+            }
         }
     }
 
     // ---- X = Q U / (|U| + eps) for columns lo .. hi - 1, 16 a wavefront at a time
+    if (NB == 2 && l0 < hi) load(l0);
     f64x4_t qb[NB][NB];
 #pragma unroll
     for (int i = 0; i < NB; ++i)
@@ -1187,19 +1241,14 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kChunkThreads) void ns_small_ke
         for (int j = 0; j < NB; ++j)
 #pragma unroll
             for (int v = 0; v < 4; ++v) qb[i][j][v] = Q[q][i][j][64 * v + lane];
-    const int64_t base = (int64_t)blockIdx.y * a.M * a.N;
-#pragma unroll 2
-    for (int l0 = lo + 16 * wave; l0 < hi; l0 += NT / 4) {
+#pragma unroll 1
+    for (; l0 < hi; l0 += NT / 4) {
         f64x4_t u[NB];
 #pragma unroll
         for (int k = 0; k < NB; ++k)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int p = 16 * k + 4 * v + g, l = l0 + c;
-                u[k][v] = p < m && l < hi
-                              ? (double)source1(a.s, base + (tall ? (int64_t)l * m + p : (int64_t)p * n + l), false)
-                              : 0.;
-            }
+            for (int v = 0; v < 4; ++v) u[k][v] = raw[k][v];
+        if (l0 + NT / 4 < hi) load(l0 + NT / 4);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             f64x4_t r = {0., 0., 0., 0.};

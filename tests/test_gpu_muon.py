@@ -20,7 +20,8 @@ pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 MUON = (3.4445, -4.7750, 2.0315)
 SMALL = [(1, 1, 1), (2, 1, 5), (3, 32, 7), (1, 8, 768), (1, 768, 8), (2, 32, 300), (1, 31, 129), (1, 5, 4100),
-         (2, 17, 17), (1, 4097, 3), (3, 16, 769), (2, 32, 256), (2, 257, 32), (1, 20, 9000)]
+         (2, 17, 17), (1, 4097, 3), (3, 16, 769), (2, 32, 256), (2, 257, 32), (1, 20, 9000), (2, 384, 16),
+         (1, 385, 9), (2, 5, 384), (3, 9, 40)]
 LARGE = [(1, 33, 33), (2, 40, 100), (1, 64, 64), (1, 65, 127), (1, 129, 128), (2, 200, 130), (1, 130, 200),
          (3, 128, 256), (1, 300, 1000), (1, 1000, 333), (2, 192, 192), (1, 257, 2050), (5, 768, 96)]
 

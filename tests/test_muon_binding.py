@@ -59,7 +59,7 @@ def test_muon_refusals(over, status):
 
 def test_workspace_size():
     size = gg.newton_schulz_workspace_size
-    assert size(4, 32, 256) == 0 and size(4, 768, 8) == 0            # one workgroup a matrix, no workspace
+    assert size(4, 32, 256) == 0 and size(4, 384, 8) == 0            # one workgroup a matrix, no workspace
     assert size(4, 5000, 8) == 4 * 40 * 2048 and size(2, 32, 257) == 2 * 3 * 3 * 2048    # chunks' sums of A
     assert size(1, 33, 33) > 0 and size(1, 0, 5) == 0 and size(0, 64, 64) == 0
     assert size(8, 768, 1536) == size(8, 1536, 768)
