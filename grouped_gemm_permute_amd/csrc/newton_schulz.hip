@@ -179,10 +179,11 @@ __device__ __forceinline__ void target8_store(const Target& t, int64_t at, int l
 
 // Sum of squares of one matrix's U, by norm_blocks(size) workgroups, in fp64
 // (fp32 squares would overflow or vanish for gradients of 1e20 or 1e-20).
-constexpr int kNormChunk = 256 * 8 * 4;      // elements a workgroup takes at least
+// Four turns of 8 elements a thread, or one while that makes at most 128 workgroups
+// (1000 x 333: 4.1 -> 3.2 us).
 constexpr int kNormMaxBlocks = 256;
 int norm_blocks(int64_t size) {
-    const int64_t n = (size + kNormChunk - 1) / kNormChunk;
+    const int64_t one = (size + 2047) / 2048, four = (size + 8191) / 8192, n = one < 128 ? one : four < 128 ? 128 : four;
     return (int)(n < kNormMaxBlocks ? n : kNormMaxBlocks);
 }
 
@@ -261,23 +262,22 @@ __global__ __launch_bounds__(256) void ns_split_kernel(const SplitArgs a) {
     __shared__ float tile[ST][ST + 1];
     __shared__ double red[4];
     const int b = blockIdx.z, i0 = blockIdx.y * ST, j0 = blockIdx.x * ST, tid = threadIdx.x;
-    const double sq = block_sum(tid < a.nb ? a.part[(int64_t)b * a.nb + tid] : 0., red, 4);
-    const double inv = (double)a.scale / (sqrt(sq) + a.eps);
     const int64_t base = (int64_t)b * a.M * a.N;
     char* rows = a.rows + (int64_t)b * a.Mp * a.Np * 4;
     char* cols = a.cols + (int64_t)b * a.Mp * a.Np * 4;
+    const double mine = tid < a.nb ? a.part[(int64_t)b * a.nb + tid] : 0.;
+    float in[2][8];              // on their way while the norm is added up
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int r = (tid >> 3) + 32 * k, c = (tid & 7) * 8;
-        float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        const int left = a.N - (j0 + c);
-        if (i0 + r < a.M && left > 0) {
-            source8(a.s, base + (int64_t)(i0 + r) * a.N + j0 + c, left, u);
+        const int r = (tid >> 3) + 32 * k, left = a.N - (j0 + (tid & 7) * 8);
+        if (i0 + r < a.M && left > 0) source8(a.s, base + (int64_t)(i0 + r) * a.N + j0 + (tid & 7) * 8, left, in[k]);
+    }
+    const double inv = (double)a.scale / (sqrt(block_sum(mine, red, 4)) + a.eps);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = e < left ? (float)((double)u[e] * inv) : 0.f;
-        }
+    for (int k = 0; k < 2; ++k) {
+        const int r = (tid >> 3) + 32 * k, c = (tid & 7) * 8, left = i0 + r < a.M ? a.N - (j0 + c) : 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) tile[r][c + e] = u[e];
+        for (int e = 0; e < 8; ++e) tile[r][c + e] = e < left ? (float)((double)in[k][e] * inv) : 0.f;
     }
     __syncthreads();
     // consecutive lanes take consecutive rows of the planes written
