@@ -34,13 +34,14 @@
 // tile in both.  For the symmetric results only tiles on and below the diagonal
 // are computed, and their transposed tile is written beside them.
 //
-// What bounds the products: a compute unit draws about 36 bytes a clock from its
+// What bounds the products: a compute unit draws 36 to 46 bytes a clock from its
 // L2, whether through LDS or straight to registers.  A K step of 32 columns is
-// 16, 32 and 64 KiB of a 64-, 128- and 256-tile, so 450, 900 and 1800 clocks, against
-// 192, 768 and 3072 of matrix instructions: tiles of 64 are bound by it, those of
-// 128 by both, those of 256 by the matrix cores (52% of their cycles at sixteen
-// 1024 x 4096, the rest the epilogues of one workgroup a unit); a few matrices have
-// only small tiles enough for 256 units, and below that by the 4 us of a launch.
+// 16, 32 and 64 KiB of a 64-, 128- and 256-tile, so at 36 bytes 450, 900 and 1800 clocks,
+// against 192, 768 and about 3000 of matrix instructions: tiles of 64 are bound
+// by it, those of 128 by both, those of 256 by the matrix cores (52% of their
+// cycles at sixteen 1024 x 4096, the rest the epilogues of one workgroup a unit).
+// Few or small matrices fill 256 units with small tiles only, and the smallest
+// products are bound by the 4 us of a launch.
 #include "mfma_common.h"
 #include "moe_ffn.h"
 
