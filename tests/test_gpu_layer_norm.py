@@ -233,3 +233,46 @@ def test_captured_and_replayed():
         got = [t.clone() for t in out]
         want = step()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), k
+
+
+@pytest.mark.parametrize("D,dtype", [(5, "bf16"), (777, "f32"), (5001, "bf16"), (8193, "bf16"), (16383, "f32"), (16384, "bf16")])
+def test_in_place_rows_of_every_width(D, dtype):
+    """y over x, h over the residual, dx over dy, dh or h: rows of one lane's group to a whole workgroup, with tails."""
+    import grouped_gemm_permute_amd as gg
+    x, r, w, b, dy, dh = [t.cuda() for t in inputs(37, D, dtype, 4)]
+    for rms in (False, True):
+        say(f"layer_norm in place D{D} {dtype} rms{rms}")
+        want = gg.layer_norm(x, w, b, residual=r, rms=rms)
+        x2, r2 = x.clone(), r.clone()
+        gg.layer_norm(x2, w, b, residual=r2, rms=rms, out={"y": x2, "h": r2})
+        assert torch.equal(x2, want["y"]) and torch.equal(r2, want["h"])
+        x2, r2 = x.clone(), r.clone()
+        gg.layer_norm(x2, w, b, residual=r2, rms=rms, out={"y": r2, "h": x2})
+        assert torch.equal(r2, want["y"]) and torch.equal(x2, want["h"])
+        back = gg.layer_norm_backward(want["h"], dy, want["rstd"], want["mean"], w, dh, bias_grad=True)
+        for which in range(3):
+            t = [want["h"].clone(), dy.clone(), dh.clone()]
+            got = gg.layer_norm_backward(t[0], t[1], want["rstd"], want["mean"], w, t[2], bias_grad=True,
+                                         out={"dx": t[which]})
+            assert all(torch.equal(got[k], back[k]) for k in ("dx", "dweight", "dbias")), which
+
+
+def test_offsets_beyond_32_bits():
+    """2.4e9 elements: the last rows as by themselves, and the weight's gradient as many times that of one part."""
+    import grouped_gemm_permute_amd as gg
+    T, D, part = 600000, 4096, 600
+    x, _, w, b, dy, _ = [t.cuda() for t in inputs(part, D, "bf16", 3)]
+    X, DY = x.repeat(T // part, 1), dy.repeat(T // part, 1)
+    say(f"layer_norm {T}x{D} bf16")
+    f = gg.layer_norm(X, w, b)
+    g = gg.layer_norm_backward(X, DY, f["rstd"], f["mean"], w, bias_grad=True)
+    torch.cuda.synchronize()
+    f1 = gg.layer_norm(x, w, b)
+    g1 = gg.layer_norm_backward(x, dy, f1["rstd"], f1["mean"], w, bias_grad=True)
+    for got, want in ((f["y"], f1["y"]), (g["dx"], g1["dx"])):
+        assert all(torch.equal(got[k:k + part], want) for k in range(0, T, part * 37)) and torch.equal(got[-part:], want)
+    z = (x.double() - f1["mean"].double()[:, None]) * f1["rstd"].double()[:, None]
+    for got, terms in ((g["dweight"], dy.double() * z), (g["dbias"], dy.double())):
+        # sums of at most T / 512 terms in a row, then 512 partial rows: u (T / 512 + 16 + 16) of the terms' sum
+        most = 2.0 ** -24 * (T / 512 + 32 + 4) * terms.abs().sum(0) * (T // part)
+        assert ((got.double() - terms.sum(0) * (T // part)).abs() <= most).all()

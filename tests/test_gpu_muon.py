@@ -192,7 +192,8 @@ def test_zero_infinite_and_nan_matrices(M, N):
 
 @pytest.mark.parametrize("nesterov", [True, False])
 @pytest.mark.parametrize("dtype,copy", [(torch.float32, False), (torch.float32, True), (torch.bfloat16, False)])
-@pytest.mark.parametrize("B,M,N", [(1, 1, 3), (2, 8, 70), (2, 70, 8), (2, 100, 150), (3, 150, 100), (1, 130, 131)])
+@pytest.mark.parametrize("B,M,N", [(1, 1, 3), (2, 8, 70), (2, 70, 8), (2, 100, 150), (3, 150, 100), (1, 130, 131),
+                                   (2, 768, 8), (3, 13, 500), (1, 300, 20), (2, 31, 600), (1, 384, 16)])
 def test_muon_step(B, M, N, dtype, copy, nesterov):
     lr, beta, decay, scale = 0.02, 0.9, 0.1, 1.4
     g = torch.Generator().manual_seed(M * N)
@@ -293,3 +294,18 @@ def test_muon_step_batches_with_coefficients(coeffs, steps):
     x32 = iterate(dW.cpu(), steps, coeffs, 1e-7, torch.float32).double().cuda()
     most = 8 * norm(x32 - X) + 16 * U * norm(X)
     assert (norm(W.double() - X) <= most).all(), f"{(norm(W.double() - X) / norm(X)).max()} of {(most / norm(X)).max()}"
+
+
+def test_offsets_beyond_32_bits():
+    """2.2e9 elements (8.7 GB a copy of X): the first matrix against 64 bits, the others, which are equal, against it."""
+    B, M, N = 130, 1024, 16384
+    g = torch.Generator(device="cuda").manual_seed(7)
+    one = (1e-3 * torch.randn(1, M, N, generator=g, device="cuda")).bfloat16()
+    G = one.expand(B, M, N).contiguous()
+    say(f"newton_schulz {B}x{M}x{N} bf16")
+    out = gg.newton_schulz(G)
+    torch.cuda.synchronize()
+    want = iterate(one, 5, MUON, 1e-7, torch.float64)
+    norm = lambda t: t.double().square().sum().sqrt()  # noqa: E731
+    assert norm(out[:1].double() - want) <= (2.0 ** -8 + 8 * 30 * U) * norm(want)
+    assert all(torch.equal(out[k], out[0]) for k in range(1, B))
