@@ -528,7 +528,7 @@ def _on_current_device(ref, device):
     another device is refused."""
     if device < 0:
         _same_device(ref, {})
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():
         raise ValueError(f"tensors are on cuda:{device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
 
@@ -564,7 +564,9 @@ def _workspace_for(ref, device, n, workspace, stream):
 
 def _outputs(out, names):
     """A copy of ``out``, whose names must be among ``names``."""
-    o = dict(out) if out else {}
+    if not out:
+        return {}
+    o = dict(out)
     for name in o:
         if name not in names:
             raise ValueError(f"out has no place for {name}")
@@ -603,8 +605,11 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False, ou
         if "h" not in o:
             o["h"] = _empty_like(x, stream)
         h = o["h"].data_ptr()
-    mean = _empty(T, torch.float32, x.device, stream) if stats and not rms else None
-    rstd = _empty(T, torch.float32, x.device, stream) if stats else None
+    mean = rstd = None
+    if stats:
+        rstd = _empty(T, torch.float32, x.device, stream)
+        if not rms:
+            mean = _empty_like(rstd, stream)
     st = lib().moe_layer_norm_forward(x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(bias),
                                       o["y"].data_ptr(), h, _ptr(mean), _ptr(rstd), T, D, int(rms), eps,
                                       dtype, _raw_stream(stream, dev))
