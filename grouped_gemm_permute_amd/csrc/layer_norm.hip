@@ -23,7 +23,8 @@
 // its own columns in registers over the rows its workgroup walks, the
 // workgroup adds its wavefronts' sums through LDS and writes one partial
 // row, and a second kernel adds the partial rows in a fixed order (no
-// atomics, so repeated calls give equal bits).
+// atomics, so repeated calls give equal bits).  With few rows further
+// workgroups of the same launch take it, each some columns of all rows.
 #include "moe_ffn.h"
 
 #include <hip/hip_runtime.h>
@@ -280,10 +281,64 @@ struct BwdArgs {
     const void *h, *dy, *w, *dh;
     const float *mean, *rstd;
     void* dx;
-    float* part;      // [2][gridDim.x][D] partial dweight, dbias; null: neither is wanted
+    float* part;      // [2][row_blocks][D] partial dweight, dbias; null: none
+    float *dw, *db;   // the workgroups past row_blocks: the sums themselves
     int64_t T;
-    int D;
+    int D, row_blocks;
 };
+
+// The weight's gradients of CV vectors of columns over all rows, for few rows: a
+// thread takes one vector and a slice of the rows, and the slices are added by
+// shuffles and through LDS.
+constexpr int CV = 4;
+template <typename T, int NT, bool TAIL>
+__device__ __forceinline__ void column_sums(const BwdArgs& a) {
+    constexpr int VEC = vec_of<T>(), SLICES = NT / CV, WAVES = NT / 64;
+    __shared__ float sums[WAVES][2][CV * VEC];
+    const int first = ((int)blockIdx.x - a.row_blocks) * CV * VEC;
+    const int vec = threadIdx.x % CV, col = first + vec * VEC, left = a.D - col;
+    auto load = [&](const void* base, int64_t at) {
+        const T* p = (const T*)base + at;
+        if (!TAIL || left >= VEC) return load_raw<false, false>(p, left, a.D);
+        return load_raw<TAIL, TAIL>(p, left, a.D);
+    };
+    float dw[VEC], db[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) dw[e] = db[e] = 0.f;
+#pragma unroll 4
+    for (int t = threadIdx.x / CV; t < (int)a.T; t += SLICES) {
+        const Raw<T> rh = load(a.h, (int64_t)t * a.D + col), ry = load(a.dy, (int64_t)t * a.D + col);
+        const float mean = a.mean ? a.mean[t] : 0.f, rstd = a.rstd[t];
+        float z[VEC], dy[VEC];
+        unpack(rh, z);
+        unpack(ry, dy);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            dw[e] = fmaf(dy[e], (z[e] - mean) * rstd, dw[e]);
+            db[e] += dy[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+        for (int o = CV; o < 64; o <<= 1) {
+            dw[e] += __shfl_xor(dw[e], o, 64);
+            db[e] += __shfl_xor(db[e], o, 64);
+        }
+        if ((threadIdx.x & 63) < CV) {
+            sums[threadIdx.x >> 6][0][vec * VEC + e] = dw[e];
+            sums[threadIdx.x >> 6][1][vec * VEC + e] = db[e];
+        }
+    }
+    __syncthreads();
+    const int which = threadIdx.x / (CV * VEC), c = threadIdx.x % (CV * VEC);
+    float* out = which ? a.db : a.dw;
+    if (which > 1 || !out || first + c >= a.D) return;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) v += sums[w][which][c];
+    out[first + c] = v;
+}
 
 template <typename T, int LANES, int NV, bool TAIL>
 __global__ __launch_bounds__(threads_of<LANES>()) void norm_backward_kernel(const BwdArgs a) {
@@ -291,6 +346,7 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_backward_kernel(cons
     constexpr int WAVES = NT / 64, COLS = LANES * NV * VEC;
     __shared__ float red[2][LANES > 64 ? LANES / 64 : 1];
     __shared__ float wsum[LANES > 64 ? 1 : WAVES * COLS];
+    if ((int)blockIdx.x >= a.row_blocks) return column_sums<T, NT, TAIL>(a);
     const int lane = threadIdx.x % LANES;
     const float inv_d = 1.f / (float)a.D;
     int col[NV];
@@ -315,7 +371,7 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_backward_kernel(cons
     // lanes hold form them twice from the packed row, in half the registers
     constexpr bool KEEP = LANES <= 256;
     for (int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES; t < a.T;
-         t += (int64_t)gridDim.x * ROWS) {
+         t += (int64_t)a.row_blocks * ROWS) {
         const int64_t at = t * a.D;
         Raw<T> rh[NV], ry[NV], rd[NV];
 #pragma unroll
@@ -380,7 +436,7 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_backward_kernel(cons
     }
     if (!a.part) return;
     float* out[2] = {a.part + (int64_t)blockIdx.x * a.D,
-                     a.part + ((int64_t)gridDim.x + blockIdx.x) * a.D};
+                     a.part + ((int64_t)a.row_blocks + blockIdx.x) * a.D};
     if constexpr (LANES > 64) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -471,6 +527,15 @@ unsigned grid_of(int64_t T, int lanes, int64_t most) {
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// Few rows: the weight's gradients come from workgroups of their own beside the rows'
+// (one launch, h and dy read twice) instead of partial rows and a second launch.
+// (512 x 768 bf16 9.6 -> 5.2 us, 1024 x 768 10.4 -> 8.0, 2048 x 768 would be 12.3 ->
+// 14.5; 512 x 4096 25 -> 8.6, 1024 x 4096 fp32 20.5 -> 18.9; with tails 512 x 1001 8.6 ->
+// 8.1, 1024 x 1001 would be 10.7 -> 18.3.)
+bool few_rows(int64_t T, int D, moe_dtype dt) {
+    return T > 0 && T <= (D % (dt == MOE_BF16 ? 8 : 4) ? 512 : 1024);
+}
+
 moe_status check_sizes(int64_t T, int D, moe_dtype dt) {
     if (T < 0 || T >= ((int64_t)1 << 31) || D <= 0) return MOE_ERR_INVALID_ARG;
     if (dt != MOE_F32 && dt != MOE_BF16) return MOE_ERR_INVALID_ARG;
@@ -552,7 +617,7 @@ moe_status moe_layer_norm_forward(const void* x, const void* residual, const voi
 }
 
 size_t moe_layer_norm_backward_workspace_size(int64_t T, int D, moe_dtype dtype) {
-    if (check_sizes(T, D, dtype) != MOE_OK) return 0;
+    if (check_sizes(T, D, dtype) != MOE_OK || few_rows(T, D, dtype)) return 0;
     const size_t rows = grid_of(T, shape_of(D, dtype).lanes, kBwdMaxBlocks);
     const size_t bytes = 2 * rows * (size_t)D * sizeof(float);
     return (bytes + kAlign - 1) / kAlign * kAlign;
@@ -571,21 +636,31 @@ moe_status moe_layer_norm_backward(const void* h, const float* mean, const float
     const void* floats[] = {mean, rstd, dweight, dbias};
     for (const void* p : floats)
         if (!aligned(p, 4)) return MOE_ERR_INVALID_ARG;
-    const bool sums = dweight || dbias;
-    if (sums && T > 0) {
+    const bool sums = dweight || dbias, apart = sums && !few_rows(T, D, dtype);
+    if (apart && T > 0) {
         if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
         if (ws_bytes < moe_layer_norm_backward_workspace_size(T, D, dtype)) return MOE_ERR_WORKSPACE;
     }
     const Shape p = shape_of(D, dtype);
     const unsigned grid = grid_of(T, p.lanes, kBwdMaxBlocks);
     (void)hipGetLastError();
+    BwdArgs a = {h, dy, weight, dh, mean, rstd, dx, apart ? (float*)workspace : nullptr, dweight, dbias, T, D, (int)grid};
+    auto launch = [&](unsigned blocks) {
+        return dtype == MOE_BF16 ? launch_backward<bf16_t>(a, p, blocks, stream) : launch_backward<float>(a, p, blocks, stream);
+    };
     if (T > 0) {
-        const BwdArgs a = {h, dy, weight, dh, mean, rstd, dx, sums ? (float*)workspace : nullptr, T, D};
-        const hipError_t e = dtype == MOE_BF16 ? launch_backward<bf16_t>(a, p, grid, stream)
-                                               : launch_backward<float>(a, p, grid, stream);
-        if (e != hipSuccess) return MOE_ERR_HIP;
+        const unsigned cols = sums && !apart ? (unsigned)((D * (dtype == MOE_BF16 ? 2 : 4) + 16 * CV - 1) / (16 * CV)) : 0;
+        if (cols && (dx == h || dx == dy)) {
+            // dx would be written over what the columns' workgroups read
+            a.row_blocks = 0;
+            if (launch(cols) != hipSuccess) return MOE_ERR_HIP;
+            a.row_blocks = (int)grid;
+            if (launch(grid) != hipSuccess) return MOE_ERR_HIP;
+        } else if (launch(grid + cols) != hipSuccess) {
+            return MOE_ERR_HIP;
+        }
     }
-    if (sums) {
+    if (apart) {
         // with T == 0 there are no partial rows, and the sums are written as zeros
         norm_partial_sum_kernel<<<dim3((D + SUM_COLS - 1) / SUM_COLS, 2), SUM_COLS * SUM_SLICES, 0,
                                   stream>>>((const float*)workspace, (int)grid, D, dweight, dbias);

@@ -545,7 +545,8 @@ moe_status moe_layer_norm_forward(const void *x, const void *residual, const voi
                                   hipStream_t stream);
 
 /* Workspace bytes moe_layer_norm_backward needs for dweight or dbias (at
- * most 512 rows of 2 D floats); 0 if the sizes are invalid or unsupported. */
+ * most 512 rows of 2 D floats); 0 if it needs none (few rows) or the sizes are
+ * invalid or unsupported. */
 size_t moe_layer_norm_backward_workspace_size(int64_t T, int D, moe_dtype dtype);
 
 /*
@@ -565,7 +566,7 @@ size_t moe_layer_norm_backward_workspace_size(int64_t T, int D, moe_dtype dtype)
  *   dweight, dbias [D] fp32; out, fully overwritten (zeros with T == 0);
  *             NULL: not wanted
  *   workspace >= moe_layer_norm_backward_workspace_size() bytes, 256-byte
- *             aligned; read only when dweight or dbias is wanted
+ *             aligned; used only when that is not 0 and dweight or dbias is wanted
  *
  * fp32 arithmetic; dx is rounded once; the sums over rows have a fixed
  * order, so repeated calls give equal bits.  dx may be dy, dh or h.

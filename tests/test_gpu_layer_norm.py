@@ -105,8 +105,14 @@ def test_forward(T, D, dtype):
         within(o["y"], y, slack, HALF[dtype], "y")
 
 
+# the weight's gradients by partial rows (more than 1024 rows, or 512 with tails), and on both sides of that
+TALL = [(1025, 1), (1026, 2), (1027, 7), (1025, 64), (1030, 257), (1026, 768), (1100, 1001), (1025, 1024), (1030, 1032),
+        (1040, 2047), (1025, 2056), (1030, 4100), (1025, 8200), (1026, 16384), (513, 16383), (512, 1001), (513, 1001),
+        (1024, 1000), (512, 12), (600, 20), (20000, 40)]
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("T,D", SHAPES + [(20000, 40)])
+@pytest.mark.parametrize("T,D", SHAPES + TALL)
 def test_backward(T, D, dtype):
     import grouped_gemm_permute_amd as gg
     x, _, w, _, dy, dh = inputs(T, D, dtype, 5 + T + D)
@@ -235,13 +241,14 @@ def test_captured_and_replayed():
         assert all(torch.equal(a, b) for a, b in zip(got, want)), k
 
 
+@pytest.mark.parametrize("T", [37, 1025])
 @pytest.mark.parametrize("D,dtype", [(5, "bf16"), (777, "f32"), (5001, "bf16"), (8193, "bf16"), (16383, "f32"), (16384, "bf16")])
-def test_in_place_rows_of_every_width(D, dtype):
+def test_in_place_rows_of_every_width(T, D, dtype):
     """y over x, h over the residual, dx over dy, dh or h: rows of one lane's group to a whole workgroup, with tails."""
     import grouped_gemm_permute_amd as gg
-    x, r, w, b, dy, dh = [t.cuda() for t in inputs(37, D, dtype, 4)]
+    x, r, w, b, dy, dh = [t.cuda() for t in inputs(T, D, dtype, 4)]
     for rms in (False, True):
-        say(f"layer_norm in place D{D} {dtype} rms{rms}")
+        say(f"layer_norm in place T{T} D{D} {dtype} rms{rms}")
         want = gg.layer_norm(x, w, b, residual=r, rms=rms)
         x2, r2 = x.clone(), r.clone()
         gg.layer_norm(x2, w, b, residual=r2, rms=rms, out={"y": x2, "h": r2})

@@ -41,7 +41,7 @@ def test_forward_refusals(over, status):
 
 
 def _bwd(**over):
-    a = dict(h=FAKE, mean=FAKE, rstd=FAKE, w=FAKE, dy=FAKE, dh=None, dx=FAKE, dw=FAKE, db=FAKE, T=16, D=64,
+    a = dict(h=FAKE, mean=FAKE, rstd=FAKE, w=FAKE, dy=FAKE, dh=None, dx=FAKE, dw=FAKE, db=FAKE, T=2000, D=64,
              dt=L.MOE_BF16, ws=FAKE, n=1 << 30)
     a.update(over)
     return L.lib().moe_layer_norm_backward(a["h"], a["mean"], a["rstd"], a["w"], a["dy"], a["dh"], a["dx"],
@@ -69,7 +69,9 @@ def test_backward_refusals(over, status):
 def test_workspace_size():
     size = L.lib().moe_layer_norm_backward_workspace_size
     assert size(0, 64, L.MOE_BF16) == 0
-    assert size(1, 64, L.MOE_BF16) == 2 * 64 * 4                     # one partial row of each sum
+    assert size(1025, 64, L.MOE_BF16) == 33 * 2 * 64 * 4             # partial rows of each sum, one of 32 rows
+    assert size(1, 64, L.MOE_BF16) == size(512, 1001, L.MOE_F32) == size(1024, 1000, L.MOE_F32) == 0   # few rows
+    assert size(513, 1001, L.MOE_F32) > 0
     assert size(1 << 20, 768, L.MOE_BF16) <= 512 * 2 * 768 * 4
     assert size(4, 20000, L.MOE_BF16) == 0 and size(-1, 64, L.MOE_BF16) == 0
 
