@@ -36,6 +36,7 @@ namespace {
 
 typedef __attribute__((ext_vector_type(2))) float f32x2_t;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 
 struct bf16_t {
     uint16_t bits;
@@ -345,7 +346,7 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_backward_kernel(cons
     constexpr int VEC = vec_of<T>(), NT = threads_of<LANES>(), ROWS = NT / LANES;
     constexpr int WAVES = NT / 64, COLS = LANES * NV * VEC;
     __shared__ float red[2][LANES > 64 ? LANES / 64 : 1];
-    __shared__ float wsum[LANES > 64 ? 1 : WAVES * COLS];
+    __shared__ __attribute__((aligned(16))) float wsum[LANES > 64 ? 1 : WAVES * COLS];
     if ((int)blockIdx.x >= a.row_blocks) return column_sums<T, NT, TAIL>(a);
     const int lane = threadIdx.x % LANES;
     const float inv_d = 1.f / (float)a.D;
@@ -451,15 +452,21 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_backward_kernel(cons
         for (int s = 0; s < 2; ++s) {
             if (s) __syncthreads();
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                float v[VEC];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    float v = s ? db[i][e] : dw[i][e];
+                    v[e] = s ? db[i][e] : dw[i][e];
 #pragma unroll
-                    for (int o = LANES; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-                    if ((threadIdx.x & 63) < LANES)
-                        wsum[(threadIdx.x >> 6) * COLS + col[i] + e] = v;
+                    for (int o = LANES; o < 64; o <<= 1) v[e] += __shfl_xor(v[e], o, 64);
                 }
+                // 16 bytes a store: element by element a lane's stride of VEC is
+                // as many bank conflicts
+                if ((threadIdx.x & 63) < LANES)
+#pragma unroll
+                    for (int e = 0; e < VEC; e += 4)
+                        *(f32x4_t*)&wsum[(threadIdx.x >> 6) * COLS + col[i] + e] = f32x4_t{v[e], v[e + 1], v[e + 2], v[e + 3]};
+            }
             __syncthreads();
             for (int c = threadIdx.x; c < a.D; c += NT) {
                 float v = 0.f;
