@@ -965,10 +965,10 @@ __global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulA
     epilogue<MODE, DT, 64 * DW>(a, b, ti * DT, tj * DT, !SYM || ti != tj, sum8, at);
 }
 
-// ------------------------------------------------- short sides of up to 32
+// ------------------------------------------------- short sides of up to 64
 
-// With a short side m of at most 32 nothing is worth planes or tiles: since every
-// step multiplies X by a polynomial of A, and those commute, the steps run on
+// With a short side m of at most 32, or 64 in few matrices, nothing is worth planes or
+// tiles: since every step multiplies X by a polynomial of A, and those commute, the steps run on
 // the m x m side alone,
 //   A <- P A P,  Q <- Q P  with P = a I + b A + c A A,
 // in fp64 (whose rounding the growth of small singular values leaves far below
@@ -983,9 +983,15 @@ __global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulA
 // a result block is an operand as it stands: mfma4(X, Y) = X^T Y.  Short sides of up
 // to 16 need one block, and the steps stay in one wavefront's registers (0.83 us a
 // step through LDS with a barrier for each product, 0.4 there, 0.2 up to 8 rows);
-// larger ones are four blocks, one a wavefront, and go through LDS (1.5 us a step).
+// larger ones are 4, 6 or 10 blocks, one a wavefront, and go through LDS (1.5, 4 and 8 us a
+// step, bound by the fp64 instructions).
 typedef __attribute__((ext_vector_type(4))) double f64x4_t;
-constexpr int SM = 32;
+
+// Short sides beyond 32 by the workgroups that would run, each of which takes the
+// steps by itself: up to 512 with short sides of up to 48 (512 of 48 x 48: 62 us, 107 in planes;
+// 8 of 48 x 768 39, 67), 256 up to 64 (64 x 64: 51, 62; 64 x 4096 69, 108; 256 of 64 x 64 54, 71, 300
+// would be 102, 85).
+constexpr int64_t small_most(int m) { return m <= 32 ? INT64_MAX : m <= 48 ? 512 : m <= 64 ? 256 : -1; }
 // Columns of the long side a workgroup takes: all of up to 384 (short sides of
 // up to 16) or 256, in turns of 256 by 16 wavefronts in one launch (256 x 8: 6.9 us,
 // 9.3 in two launches; 384 x 8: 8.3, 9.3; 768 x 8: 11.7, 9.7; 768 x 16: 15.3, 10.5; 32 x 192:
@@ -994,7 +1000,7 @@ constexpr int SM = 32;
 // 27 us, 331 by one workgroup).
 int small_chunk(int M, int N) {
     const int m = M < N ? M : N, n = M < N ? N : M;
-    if (n <= (m <= 16 ? 384 : 256)) return n;
+    if (m <= 32 && n <= (m <= 16 ? 384 : 256)) return n;
     return n <= 64 * 128 ? 128 : ((n + 63) / 64 + 127) / 128 * 128;
 }
 int small_chunks(int M, int N) {
@@ -1036,15 +1042,16 @@ __device__ __forceinline__ void target1(const Target& t, int64_t at, float v) {
         ((float*)t.out)[at] = v;
 }
 
-// Block index of (i, j), i >= j.
-__device__ __forceinline__ int low_block(int i, int j) { return i + j; }
+// Block index of (i, j), i >= j, and how many there are.
+__host__ __device__ constexpr int low_block(int i, int j) { return i * (i + 1) / 2 + j; }
+__host__ __device__ constexpr int low_blocks(int nb) { return low_block(nb, 0); }
 
 // This workgroup's sum of U U^T over columns lo .. hi - 1 of the long side, NB x NB
-// blocks of 16: blocks (0,0), (1,0), (1,1) of `sum` ([blocks][256], in LDS).
+// blocks of 16: blocks (0,0), (1,0), (1,1), .. of `sum` ([blocks][256], in LDS).
 // A wavefront takes 16 columns at a time.
 template <int NB, int NT>
 __device__ __forceinline__ void small_gram(const SmallArgs& a, int lo, int hi, double* sum) {
-    constexpr int BLOCKS = NB == 1 ? 1 : 3, WAVES = NT / 64;
+    constexpr int BLOCKS = low_blocks(NB), WAVES = NT / 64;
     __shared__ double part[WAVES][BLOCKS][256];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
     const bool tall = a.M > a.N;
@@ -1066,11 +1073,10 @@ __device__ __forceinline__ void small_gram(const SmallArgs& a, int lo, int hi, d
                               ? (double)source1(a.s, base + (tall ? (int64_t)l * m + p : (int64_t)p * n + l), true)
                               : 0.;
             }
-        acc[0] = mfma4(u[0], u[0], acc[0]);
-        if constexpr (NB == 2) {
-            acc[1] = mfma4(u[1], u[0], acc[1]);
-            acc[2] = mfma4(u[1], u[1], acc[2]);
-        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j <= i; ++j) acc[low_block(i, j)] = mfma4(u[i], u[j], acc[low_block(i, j)]);
     }
 #pragma unroll
     for (int k = 0; k < BLOCKS; ++k)
@@ -1086,10 +1092,14 @@ __device__ __forceinline__ void small_gram(const SmallArgs& a, int lo, int hi, d
     __syncthreads();
 }
 
-constexpr int kChunkThreads = 512, kOneThreads = 1024;
+constexpr int kOneThreads = 1024;
+// Four blocks a side: fewer wavefronts for the sums (their 10 blocks each go through
+// LDS), one for each of the 10 blocks in the steps.
+constexpr int gram_threads(int nb) { return nb == 4 ? 256 : 512; }
+constexpr int step_threads(int nb, bool one) { return one ? kOneThreads : nb == 4 ? 640 : 512; }
 template <int NB>
-__global__ __launch_bounds__(kChunkThreads) void ns_small_gram_kernel(const SmallArgs a) {
-    constexpr int BLOCKS = NB == 1 ? 1 : 3, NT = kChunkThreads;
+__global__ __launch_bounds__(gram_threads(NB)) void ns_small_gram_kernel(const SmallArgs a) {
+    constexpr int BLOCKS = low_blocks(NB), NT = gram_threads(NB);
     __shared__ double sum[BLOCKS * 256];
     const int n = a.M > a.N ? a.M : a.N, lo = blockIdx.x * a.chunk;
     small_gram<NB, NT>(a, lo, min(lo + a.chunk, n), sum);
@@ -1099,11 +1109,11 @@ __global__ __launch_bounds__(kChunkThreads) void ns_small_gram_kernel(const Smal
 
 // ONE: the whole matrix is this workgroup's chunk, and its sums are taken here.
 template <int NB, bool ONE>
-__global__ __launch_bounds__(ONE ? kOneThreads : kChunkThreads) void ns_small_kernel(const SmallArgs a) {
-    constexpr int BLOCKS = NB == 1 ? 1 : 3, NT = ONE ? kOneThreads : kChunkThreads;
+__global__ __launch_bounds__(step_threads(NB, ONE)) void ns_small_kernel(const SmallArgs a) {
+    constexpr int BLOCKS = low_blocks(NB), NT = step_threads(NB, ONE), NQ = NB > 2 ? 1 : 2;
     __shared__ double sum[BLOCKS * 256];
     // whole matrices, blocks [i][j] of 16 x 16 in result order: value v of a lane at 64 v + lane
-    __shared__ double A[NB][NB][256], P[NB][NB][256], U[NB][NB][256], Q[2][NB][NB][256];
+    __shared__ double A[NB][NB][256], P[NB][NB][256], U[NB][NB][256], Q[NQ][NB][NB][256];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
     const bool tall = a.M > a.N;
     const int m = tall ? a.N : a.M, n = tall ? a.M : a.N;
@@ -1122,7 +1132,7 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kChunkThreads) void ns_small_ke
     }
     double trace = lane < m ? sum[low_block(lane >> 4, lane >> 4) * 256 + (lane & 15) * 17] : 0.;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) trace += __shfl_xor(trace, o, 64);
+    for (int o = 32; o > 0; o >>= 1) trace += __shfl_xor(trace, o, 64);
     trace = __shfl(trace, 0, 64);
     const double inv = 1. / (sqrt(trace) + a.eps);
 
@@ -1177,9 +1187,12 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kChunkThreads) void ns_small_ke
         }
         __syncthreads();
     } else {
-        // ---- the steps: wavefront w < NB^2 owns block (bi, bj) of every matrix
-        const bool works = wave < NB * NB;
-        const int bi = wave >> 1 & 1, bj = wave & 1;
+        // ---- the steps: a wavefront owns block (bi, bj) of every matrix; from three
+        // blocks a side on only those on and below the diagonal, and writes their
+        // mirror images too
+        const bool works = wave < (NB > 2 ? BLOCKS : NB * NB);
+        const int bi = NB == 2 ? wave >> 1 & 1 : wave < 1 ? 0 : wave < 3 ? 1 : wave < 6 ? 2 : 3;
+        const int bj = NB == 2 ? wave & 1 : works ? wave - low_block(bi, 0) : 0;
         auto product = [&](double (*x)[NB][256], double (*y)[NB][256]) {
             f64x4_t acc = {0., 0., 0., 0.};
 #pragma unroll
@@ -1193,7 +1206,10 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kChunkThreads) void ns_small_ke
         };
         auto put = [&](double (*x)[NB][256], f64x4_t r) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) x[bi][bj][64 * v + lane] = r[v];
+            for (int v = 0; v < 4; ++v) {
+                x[bi][bj][64 * v + lane] = r[v];
+                if (NB > 2 && bi != bj) x[bj][bi][64 * (c >> 2) + 16 * (c & 3) + 4 * v + g] = r[v];
+            }
         };
         f64x4_t own;
 #pragma unroll
@@ -1217,11 +1233,17 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kChunkThreads) void ns_small_ke
                 if (k == 0) put(Q[0], r);
             }
             __syncthreads();
+            f64x4_t qn, un;
             if (works) {
-                if (k > 0) put(Q[q ^ 1], product(Q[q], P));
-                if (k + 1 < a.steps) put(U, product(A, P));
+                if (k > 0) qn = product(Q[q], P);
+                if (k + 1 < a.steps) un = product(A, P);
             }
-            if (k > 0) q ^= 1;
+            if (NQ == 1 && k > 0) __syncthreads();       // one Q: all have read it
+            if (NQ == 2 && k > 0) q ^= 1;
+            if (works) {
+                if (k > 0) put(Q[q], qn);
+                if (k + 1 < a.steps) put(U, un);
+            }
             __syncthreads();
             if (k + 1 < a.steps) {
                 if (works) {
@@ -1234,14 +1256,20 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kChunkThreads) void ns_small_ke
     }
 
     // ---- X = Q U / (|U| + eps) for columns lo .. hi - 1, 16 a wavefront at a time
-    if (NB == 2 && l0 < hi) load(l0);
-    f64x4_t qb[NB][NB];
+    if (NB > 1 && l0 < hi) load(l0);
+    f64x4_t qb[NB > 2 ? 1 : NB][NB];         // held in registers up to two blocks a side
+    auto fetch = [&](int i, int j) {
+        f64x4_t r;
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+        for (int v = 0; v < 4; ++v) r[v] = Q[q][i][j][64 * v + lane];
+        return r;
+    };
+    if constexpr (NB <= 2) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) qb[i][j][v] = Q[q][i][j][64 * v + lane];
+            for (int j = 0; j < NB; ++j) qb[i][j] = fetch(i, j);
+    }
 #pragma unroll 1
     for (; l0 < hi; l0 += NT / 4) {
         f64x4_t u[NB];
@@ -1250,11 +1278,14 @@ __global__ __launch_bounds__(ONE ? kOneThreads : kChunkThreads) void ns_small_ke
 #pragma unroll
             for (int v = 0; v < 4; ++v) u[k][v] = raw[k][v];
         if (l0 + NT / 4 < hi) load(l0 + NT / 4);
-#pragma unroll
+#pragma unroll (NB > 2 ? 1 : NB)
         for (int i = 0; i < NB; ++i) {
             f64x4_t r = {0., 0., 0., 0.};
 #pragma unroll
-            for (int k = 0; k < NB; ++k) r = tall ? mfma4(u[k], qb[k][i], r) : mfma4(qb[k][i], u[k], r);
+            for (int k = 0; k < NB; ++k) {
+                const f64x4_t x = NB > 2 ? fetch(k, i) : qb[NB > 2 ? 0 : k][i];
+                r = tall ? mfma4(u[k], x, r) : mfma4(x, u[k], r);
+            }
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 // the result's rows are columns of the long side when tall, of the short otherwise
@@ -1275,7 +1306,14 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 int pad64(int v) { return (v + 63) / 64 * 64; }
 
-bool is_small(int M, int N) { return (M < N ? M : N) <= SM; }
+bool is_small(int B, int M, int N) {
+    const int m = M < N ? M : N;
+    return (int64_t)B * small_chunks(M, N) <= small_most(m);
+}
+int small_blocks(int M, int N) {
+    const int m = M < N ? M : N;
+    return (m + 15) / 16;
+}
 
 struct Layout {
     size_t part, x, xt[2], sym[kSyms], total;
@@ -1289,9 +1327,9 @@ moe_status check_sizes(int B, int M, int N) {
 
 Layout layout_of(int B, int M, int N) {
     Layout L = {};
-    if (is_small(M, N)) {
-        const size_t chunks = small_chunks(M, N), blocks = (M < N ? M : N) <= 16 ? 1 : 3;
-        L.total = chunks > 1 ? (size_t)B * chunks * blocks * 256 * sizeof(double) : 0;
+    if (is_small(B, M, N)) {
+        const size_t chunks = small_chunks(M, N), blocks = low_blocks(small_blocks(M, N));
+        L.total = chunks > 1 || blocks > 3 ? (size_t)B * chunks * blocks * 256 * sizeof(double) : 0;
         return L;
     }
     const size_t m = pad64(M < N ? M : N), n = pad64(M < N ? N : M);
@@ -1448,23 +1486,28 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
         if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
         if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     }
-    if (is_small(M, N)) {
+    if (is_small(B, M, N)) {
         const int chunks = small_chunks(M, N);
         const SmallArgs s = {src, tgt, M, N, steps, small_chunk(M, N), a, b, c, eps, (double*)workspace};
         const dim3 grid(chunks, B);
         auto launch = [&](auto blocks) {
             constexpr int NB = decltype(blocks)::value;
-            if (chunks == 1) {
-                ns_small_kernel<NB, true><<<grid, kOneThreads, 0, stream>>>(s);
-                return ok();
+            if constexpr (NB <= 2) {
+                if (chunks == 1) {
+                    ns_small_kernel<NB, true><<<grid, kOneThreads, 0, stream>>>(s);
+                    return ok();
+                }
             }
-            ns_small_gram_kernel<NB><<<grid, kChunkThreads, 0, stream>>>(s);
+            ns_small_gram_kernel<NB><<<grid, gram_threads(NB), 0, stream>>>(s);
             if (!ok()) return false;
-            ns_small_kernel<NB, false><<<grid, kChunkThreads, 0, stream>>>(s);
+            ns_small_kernel<NB, false><<<grid, step_threads(NB, false), 0, stream>>>(s);
             return ok();
         };
-        const bool done = (M < N ? M : N) <= 16 ? launch(std::integral_constant<int, 1>{})
-                                                : launch(std::integral_constant<int, 2>{});
+        const int blocks = small_blocks(M, N);
+        const bool done = blocks == 1   ? launch(std::integral_constant<int, 1>{})
+                          : blocks == 2 ? launch(std::integral_constant<int, 2>{})
+                          : blocks == 3 ? launch(std::integral_constant<int, 3>{})
+                                        : launch(std::integral_constant<int, 4>{});
         return done ? MOE_OK : MOE_ERR_HIP;
     }
     char* ws = (char*)workspace;

@@ -595,8 +595,9 @@ moe_status moe_layer_norm_backward(const void *h, const float *mean, const float
 
 /* Workspace bytes moe_newton_schulz and moe_muon_step need (12 bytes an
  * element and 20 an entry of A, sizes padded to multiples of 64, and a
- * little; with a shorter side of at most 32 at most 384 KiB a matrix, and none when
- * the longer is at most 256); 0 if the sizes are invalid or unsupported. */
+ * little; few matrices with a shorter side of at most 64, or any number with one of at
+ * most 32: at most 1.25 MiB a matrix, and none when the shorter is at most 32 and the
+ * longer at most 256); 0 if the sizes are invalid or unsupported. */
 size_t moe_newton_schulz_workspace_size(int B, int M, int N);
 
 /*
@@ -605,7 +606,7 @@ size_t moe_newton_schulz_workspace_size(int B, int M, int N);
  *   workspace >= moe_newton_schulz_workspace_size() bytes, 256-byte aligned
  *
  * Results are those of fp32 arithmetic (fp16 pairs of 22 bits on the matrix
- * cores, fp32 sums; shorter sides of at most 32: fp64), rounded once to
+ * cores, fp32 sums; small matrices: fp64), rounded once to
  * dtype; the norm is summed in fp64, so gradients of any magnitude will do.
  * Summation orders are fixed: repeated calls give equal bits.  A zero
  * matrix gives zeros (eps > 0); one that holds an infinity or NaN gives NaN,
