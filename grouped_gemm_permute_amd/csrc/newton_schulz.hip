@@ -1191,7 +1191,7 @@ __global__ __launch_bounds__(step_threads(NB, ONE)) void ns_small_kernel(const S
         // blocks a side on only those on and below the diagonal, and writes their
         // mirror images too
         const bool works = wave < (NB > 2 ? BLOCKS : NB * NB);
-        const int bi = NB == 2 ? wave >> 1 & 1 : wave < 1 ? 0 : wave < 3 ? 1 : wave < 6 ? 2 : 3;
+        const int bi = NB == 2 ? wave >> 1 & 1 : !works || wave < 1 ? 0 : wave < 3 ? 1 : wave < 6 ? 2 : 3;
         const int bj = NB == 2 ? wave & 1 : works ? wave - low_block(bi, 0) : 0;
         auto product = [&](double (*x)[NB][256], double (*y)[NB][256]) {
             f64x4_t acc = {0., 0., 0., 0.};
