@@ -986,6 +986,7 @@ __global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulA
 // larger ones are 4, 6 or 10 blocks, one a wavefront, and go through LDS (1.5, 4 and 8 us a
 // step, bound by the fp64 instructions).
 typedef __attribute__((ext_vector_type(4))) double f64x4_t;
+constexpr int kMaxSteps = 64;
 
 // Short sides beyond 32 by the workgroups that would run, each of which takes the
 // steps by itself: up to 512 with short sides of up to 48 (512 of 48 x 48: 62 us, 107 in planes;
@@ -1013,8 +1014,16 @@ struct SmallArgs {
     Target t;
     int M, N, steps, chunk;      // chunk: columns of the long side a workgroup takes
     double a, b, c, eps;
-    double* part;                // [B][chunks][blocks][256] sums of A, blocks (0,0), (1,0), (1,1)
+    double* part;                // [B][chunks][blocks][256] sums of A's blocks on and below the diagonal
 };
+// What a long run adds to the diagonal of the A that step k starts with (see ns_small_kernel): a
+// kernel argument of its own, since 512 bytes more cost every launch 0.15 us.
+template <bool LONG>
+struct Shifts {
+    double of[kMaxSteps];
+};
+template <>
+struct Shifts<false> {};
 
 __device__ __forceinline__ f64x4_t mfma4(f64x4_t x, f64x4_t y, f64x4_t acc) {
 #pragma unroll
@@ -1108,8 +1117,22 @@ __global__ __launch_bounds__(gram_threads(NB)) void ns_small_gram_kernel(const S
 }
 
 // ONE: the whole matrix is this workgroup's chunk, and its sums are taken here.
-template <int NB, bool ONE>
-__global__ __launch_bounds__(step_threads(NB, ONE)) void ns_small_kernel(const SmallArgs a) {
+//
+// LONG: steps that would multiply A's rounding by more than it can bear.  Where U has no
+// component A = 0, and what rounding leaves there, n of either sign, grows by P^2 = a^2 a step as a
+// small singular value's square does; a negative one is no square of anything, meets no bound
+// and ends in infinity (rank 3 of 8, a = 3.44: 12 steps do, 20 are NaN).  Three measures keep
+// such a run an iteration of real singular values, those above fp32's resolution untouched:
+//  * shift_k = 2^-46 of the largest square is added to A's diagonal in every step, more than its
+//    rounding, so A stays positive, and X X^T <= A stays below the host's bound.  A direction of
+//    s |U| is off by 2^-47 / s^2, less than the 2^-24 / s of fp32 arithmetic from s = 2^-23 on.  It
+//    holds Q below 2^23 of the bound, so that Q U is off by 2^-30 at most.
+//  * A is made symmetric in every step: its skew part would grow alike.
+//  * Q <- P Q, the order of X <- P X: by then P and Q share their directions to rounding only, and
+//    Q P would multiply it by the large entries of Q.
+// Short runs (7 of the usual coefficients, see is_long) need none of it and keep what precision fp64 has.
+template <int NB, bool ONE, bool LONG>
+__global__ __launch_bounds__(step_threads(NB, ONE)) void ns_small_kernel(const SmallArgs a, const Shifts<LONG> shift) {
     constexpr int BLOCKS = low_blocks(NB), NT = step_threads(NB, ONE), NQ = NB > 2 ? 1 : 2;
     __shared__ double sum[BLOCKS * 256];
     // whole matrices, blocks [i][j] of 16 x 16 in result order: value v of a lane at 64 v + lane
@@ -1154,6 +1177,16 @@ __global__ __launch_bounds__(step_threads(NB, ONE)) void ns_small_kernel(const S
     int l0 = lo + 16 * wave;
     if (NB == 1 && l0 < hi) load(l0);
 
+    // LONG: a diagonal block's symmetric part (its transpose is its product with 1), the shift added
+    auto symmetric = [&](f64x4_t x, double more) {
+        f64x4_t one;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) one[v] = 4 * v + g == c ? 1. : 0.;
+        const f64x4_t t = mfma4(x, one, f64x4_t{0., 0., 0., 0.});
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[v] = 0.5 * (x[v] + t[v]) + more * one[v];
+        return x;
+    };
     int q = 0;
     if constexpr (NB == 1) {
         // ---- the steps, all in the registers of one wavefront.  Past m everything is
@@ -1172,6 +1205,7 @@ __global__ __launch_bounds__(step_threads(NB, ONE)) void ns_small_kernel(const S
             f64x4_t A1, Q1;
 #pragma unroll
             for (int v = 0; v < 4; ++v) A1[v] = sum[(4 * v + g) * 16 + c] * inv * inv;
+            if constexpr (LONG) A1 = symmetric(A1, shift.of[0]);
             for (int k = 0; k < a.steps; ++k) {
                 f64x4_t P1 = product(A1, A1);
 #pragma unroll
@@ -1179,44 +1213,55 @@ __global__ __launch_bounds__(step_threads(NB, ONE)) void ns_small_kernel(const S
                     const int i = 4 * v + g;
                     P1[v] = (i == c && i < m ? a.a : 0.) + a.b * A1[v] + a.c * P1[v];
                 }
-                Q1 = k == 0 ? P1 : product(Q1, P1);
+                Q1 = k == 0 ? P1 : LONG ? product(P1, Q1) : product(Q1, P1);
                 if (k + 1 < a.steps) A1 = product(product(A1, P1), P1);
+                if constexpr (LONG) {
+                    if (k + 1 < a.steps) A1 = symmetric(A1, shift.of[k + 1]);
+                }
             }
 #pragma unroll
-            for (int v = 0; v < 4; ++v) Q[0][0][0][64 * v + lane] = Q1[v];
+            for (int v = 0; v < 4; ++v) Q[0][0][0][LONG ? 16 * c + 4 * v + g : 64 * v + lane] = Q1[v];
         }
         __syncthreads();
     } else {
         // ---- the steps: a wavefront owns block (bi, bj) of every matrix; from three
-        // blocks a side on only those on and below the diagonal, and writes their
-        // mirror images too
-        const bool works = wave < (NB > 2 ? BLOCKS : NB * NB);
-        const int bi = NB == 2 ? wave >> 1 & 1 : !works || wave < 1 ? 0 : wave < 3 ? 1 : wave < 6 ? 2 : 3;
-        const int bj = NB == 2 ? wave & 1 : works ? wave - low_block(bi, 0) : 0;
-        auto product = [&](double (*x)[NB][256], double (*y)[NB][256]) {
+        // blocks a side on, and in long runs, only those on and below the diagonal, and
+        // writes their mirror images too
+        constexpr bool LOWER = NB > 2 || LONG;
+        const bool works = wave < (LOWER ? BLOCKS : NB * NB);
+        const int bi = !LOWER ? wave >> 1 & 1 : !works || wave < 1 ? 0 : wave < 3 ? 1 : wave < 6 ? 2 : 3;
+        const int bj = !LOWER ? wave & 1 : works ? wave - low_block(bi, 0) : 0;
+        auto block = [&](double (*x)[NB][256], double (*y)[NB][256], int i, int j) {
             f64x4_t acc = {0., 0., 0., 0.};
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 f64x4_t p, q;
 #pragma unroll
-                for (int v = 0; v < 4; ++v) p[v] = x[k][bi][64 * v + lane], q[v] = y[k][bj][64 * v + lane];
-                acc = mfma4(p, q, acc);          // block (k, bi)^T = block (bi, k)
+                for (int v = 0; v < 4; ++v) p[v] = x[k][i][64 * v + lane], q[v] = y[k][j][64 * v + lane];
+                acc = mfma4(p, q, acc);          // block (k, i)^T = block (i, k)
             }
             return acc;
         };
+        auto product = [&](double (*x)[NB][256], double (*y)[NB][256]) { return block(x, y, bi, bj); };
         auto put = [&](double (*x)[NB][256], f64x4_t r) {
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 x[bi][bj][64 * v + lane] = r[v];
-                if (NB > 2 && bi != bj) x[bj][bi][64 * (c >> 2) + 16 * (c & 3) + 4 * v + g] = r[v];
+                if (LOWER && bi != bj) x[bj][bi][64 * (c >> 2) + 16 * (c & 3) + 4 * v + g] = r[v];
             }
         };
+        // LONG: all blocks of Q, which is not symmetric there, by turns of the wavefronts; the
+        // last step leaves its transpose, from which X's product reads
+        constexpr int QS = LONG ? (NB * NB + NT / 64 - 1) / (NT / 64) : 1;
         f64x4_t own;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const int i = 4 * v + g;
             const double* blk = sum + low_block(max(bi, bj), min(bi, bj)) * 256;
             own[v] = (bi >= bj ? blk[i * 16 + c] : blk[c * 16 + i]) * inv * inv;
+        }
+        if constexpr (LONG) {
+            if (bi == bj) own = symmetric(own, shift.of[0]);
         }
         if (works) put(A, own);
         __syncthreads();
@@ -1233,21 +1278,40 @@ __global__ __launch_bounds__(step_threads(NB, ONE)) void ns_small_kernel(const S
                 if (k == 0) put(Q[0], r);
             }
             __syncthreads();
-            f64x4_t qn, un;
-            if (works) {
-                if (k > 0) qn = product(Q[q], P);
-                if (k + 1 < a.steps) un = product(A, P);
+            f64x4_t qn[QS], un;
+            if constexpr (LONG) {
+#pragma unroll
+                for (int t = 0; t < QS; ++t) {
+                    const int id = wave + t * (NT / 64);
+                    if (k > 0 && id < NB * NB) qn[t] = block(P, Q[q], id / NB, id % NB);
+                }
+            } else {
+                if (works && k > 0) qn[0] = product(Q[q], P);
             }
+            if (works && k + 1 < a.steps) un = product(A, P);
             if (NQ == 1 && k > 0) __syncthreads();       // one Q: all have read it
             if (NQ == 2 && k > 0) q ^= 1;
-            if (works) {
-                if (k > 0) put(Q[q], qn);
-                if (k + 1 < a.steps) put(U, un);
+            if constexpr (LONG) {
+#pragma unroll
+                for (int t = 0; t < QS; ++t) {
+                    const int id = wave + t * (NT / 64);
+                    if (k == 0 || id >= NB * NB) continue;
+                    const bool last = k + 1 == a.steps;
+                    double* to = last ? Q[q][id % NB][id / NB] : Q[q][id / NB][id % NB];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) to[last ? 16 * c + 4 * v + g : 64 * v + lane] = qn[t][v];
+                }
+            } else {
+                if (works && k > 0) put(Q[q], qn[0]);
             }
+            if (works && k + 1 < a.steps) put(U, un);
             __syncthreads();
             if (k + 1 < a.steps) {
                 if (works) {
                     own = product(U, P);
+                    if constexpr (LONG) {
+                        if (bi == bj) own = symmetric(own, shift.of[k + 1]);
+                    }
                     put(A, own);
                 }
                 __syncthreads();
@@ -1300,7 +1364,7 @@ __global__ __launch_bounds__(step_threads(NB, ONE)) void ns_small_kernel(const S
 // ---------------------------------------------------------------- host side
 
 constexpr size_t kAlign = 256;
-constexpr int kMaxSide = 32768, kMaxSteps = 64;
+constexpr int kMaxSide = 32768;
 constexpr int kSyms = 5;      // symmetric matrices of a call: A, A P and three of S and R
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -1464,6 +1528,14 @@ bool launch_product(MulArgs& g, int B, hipStream_t stream) {
     return hipGetLastError() == hipSuccess;
 }
 
+// Whether a run on the short side is a long one: what A's rounding, 2^-46 of the largest square and
+// less, has grown to by the last step's polynomial is beyond 2^-24.
+bool is_long(int steps, const double* whole) {
+    double grown = 0x1p-46;
+    for (int k = 0; k + 1 < steps; ++k) grown *= fmax(1., whole[k] * whole[k]);
+    return grown > 0x1p-24;
+}
+
 moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int steps, double a, double b,
                double c, double eps, void* workspace, size_t ws_bytes, hipStream_t stream) {
     if (steps < 1 || steps > kMaxSteps) return MOE_ERR_INVALID_ARG;
@@ -1490,24 +1562,32 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
         const int chunks = small_chunks(M, N);
         const SmallArgs s = {src, tgt, M, N, steps, small_chunk(M, N), a, b, c, eps, (double*)workspace};
         const dim3 grid(chunks, B);
-        auto launch = [&](auto blocks) {
+        auto launch = [&](auto blocks, auto long_run) {
             constexpr int NB = decltype(blocks)::value;
+            constexpr bool LONG = decltype(long_run)::value;
+            Shifts<LONG> shift;
+            if constexpr (LONG) {
+                for (int k = 0; k < kMaxSteps; ++k) shift.of[k] = k < steps ? 0x1p-46 * top[k] * top[k] : 0.;
+            }
             if constexpr (NB <= 2) {
                 if (chunks == 1) {
-                    ns_small_kernel<NB, true><<<grid, kOneThreads, 0, stream>>>(s);
+                    ns_small_kernel<NB, true, LONG><<<grid, kOneThreads, 0, stream>>>(s, shift);
                     return ok();
                 }
             }
             ns_small_gram_kernel<NB><<<grid, gram_threads(NB), 0, stream>>>(s);
             if (!ok()) return false;
-            ns_small_kernel<NB, false><<<grid, step_threads(NB, false), 0, stream>>>(s);
+            ns_small_kernel<NB, false, LONG><<<grid, step_threads(NB, false), 0, stream>>>(s, shift);
             return ok();
         };
-        const int blocks = small_blocks(M, N);
-        const bool done = blocks == 1   ? launch(std::integral_constant<int, 1>{})
-                          : blocks == 2 ? launch(std::integral_constant<int, 2>{})
-                          : blocks == 3 ? launch(std::integral_constant<int, 3>{})
-                                        : launch(std::integral_constant<int, 4>{});
+        auto of_blocks = [&](auto long_run) {
+            const int blocks = small_blocks(M, N);
+            return blocks == 1   ? launch(std::integral_constant<int, 1>{}, long_run)
+                   : blocks == 2 ? launch(std::integral_constant<int, 2>{}, long_run)
+                   : blocks == 3 ? launch(std::integral_constant<int, 3>{}, long_run)
+                                 : launch(std::integral_constant<int, 4>{}, long_run);
+        };
+        const bool done = is_long(steps, whole) ? of_blocks(std::true_type{}) : of_blocks(std::false_type{});
         return done ? MOE_OK : MOE_ERR_HIP;
     }
     char* ws = (char*)workspace;
