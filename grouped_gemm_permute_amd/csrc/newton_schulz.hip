@@ -18,7 +18,12 @@
 // with them.  s comes from a bound on the singular values: the host follows
 // the largest value of |x (a + b x^2 + c x^4)| from [0, 1] through the steps, an
 // entry is never larger than the largest singular value, and s puts the bound
-// at 2^15 at most (fp16 ends at 65504).
+// at 2^15 at most (fp16 ends at 65504).  That bound assumes |X_0| = 1; where eps holds X_0
+// down to rho = |U| / (|U| + eps) its planes would lose bits, and vanish below 2^-40.  So each matrix
+// has a power of two of its own, lift = log2(1 / rho) rounded down, found with its norm: its planes
+// hold 2^e X with e = max(0, lift + room_k) before step k, where 2^room_k is the bound of [0, 1] over
+// the largest product of polynomials so far, so that 2^e X stays below the bound.  X's products are
+// linear in X, so e enters as one factor of what a tile writes.
 //
 // Layout: a matrix of planes is cut into blocks of 32 rows by 32 columns of
 // 4 KiB, each in the order in which the matrix instruction's lanes take it (plane,
@@ -256,6 +261,7 @@ struct SplitArgs {
     int Mp, Np;             // padded
     double eps;
     float scale;
+    int* lift;              // [B], out
     char *rows, *cols;      // planes [B][Mp][Np] (U's rows) and [B][Np][Mp] (its columns)
 };
 constexpr int ST = 64;
@@ -273,7 +279,11 @@ __global__ __launch_bounds__(256) void ns_split_kernel(const SplitArgs a) {
         const int r = (tid >> 3) + 32 * k, left = a.N - (j0 + (tid & 7) * 8);
         if (i0 + r < a.M && left > 0) source8(a.s, base + (int64_t)(i0 + r) * a.N + j0 + (tid & 7) * 8, left, in[k]);
     }
-    const double inv = (double)a.scale / (sqrt(block_sum(mine, red, 4)) + a.eps);
+    const double norm = sqrt(block_sum(mine, red, 4)), more = (norm + a.eps) / norm;
+    // finite: neither a zero matrix nor one that holds an infinity or NaN
+    const int lift = more >= 2. && more < INFINITY ? ilogb(more) : 0;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) a.lift[b] = lift;
+    const double inv = ldexp((double)a.scale / (norm + a.eps), lift);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int r = (tid >> 3) + 32 * k, c = (tid & 7) * 8, left = i0 + r < a.M ? a.N - (j0 + c) : 0;
@@ -322,6 +332,8 @@ struct MulArgs {
     float so;                   // scale of the stored planes
     char *c, *ct;               // planes out, as computed and transposed
     int64_t c_stride;
+    const int* lift;            // [B]; room: before this product and after it
+    int room, room_after;
     int swap;                   // FINAL: the target is the transposed tile
     int M, N;                   // FINAL: the target's sizes
     Target t;
@@ -365,12 +377,20 @@ __device__ __forceinline__ void tile_of(const MulArgs& a, int id, int& b, int& t
     }
 }
 
+// What a matrix's own power of two comes to in what a product writes.
+template <int MODE>
+__device__ __forceinline__ float lift_factor(const MulArgs& a, int b) {
+    if constexpr (MODE == SYMM) return 1.f;
+    const int lift = a.lift[b], e = max(0, lift + a.room);
+    return ldexpf(1.f, MODE == GRAM ? -2 * e : MODE == APPLY ? max(0, lift + a.room_after) - e : -e);
+}
+
 // From the sums of a TS x TS tile (sum8: eight of a row) to what the mode
 // writes: eight values a thread along the rows, and, through the fp32 tile
 // `at` in LDS, along the columns for the transposed order.
 template <int MODE, int TS, int NT, typename Sum8, typename At>
-__device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0, bool both, Sum8 sum8,
-                                         At at) {
+__device__ __forceinline__ void epilogue(const MulArgs& a, float lift, int b, int i0, int j0, bool both,
+                                         Sum8 sum8, At at) {
     constexpr int SEGS = TS / 8, PASSES = (TS * SEGS + NT - 1) / NT;
     // consecutive lanes take consecutive rows (the planes' order), or, for the
     // target, the segments of a row
@@ -379,6 +399,7 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
         seg = 8 * (MODE == FINAL ? id % SEGS : id / TS);
     };
     if (MODE == FINAL) both = a.swap;
+    const float so = a.so * lift;
     auto here = [&](int r, int c) { return r < TS && c < TS && i0 + r < a.pr && j0 + c < a.qr; };
     // FINAL: where a piece of the target's row `row` begins
     auto target_at = [&](int row, int seg) {
@@ -430,10 +451,12 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
         if (MODE == SYMM && a.fq != 0.f) add_planes(qhi[k], qlo[k], a.fq, v);
         if constexpr (MODE != FINAL) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= a.so;
+            for (int e = 0; e < 8; ++e) v[e] *= so;
             store_planes(a.c + b * a.c_stride, plane_at(i0 + r, a.qr, j0 + c), v);
-        } else if (!a.swap) {
-            const int left = target_left(r, c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= lift;
+            const int left = a.swap ? 0 : target_left(r, c);
             if (left > 0) target8_store(a.t, target_at(r, c), left, v, w[k]);
         }
         if (both) {
@@ -470,8 +493,9 @@ __device__ __forceinline__ void epilogue(const MulArgs& a, int b, int i0, int j0
 // fp32 tile and two passes of 8 values a thread the same took about 7 us of a
 // 128-tile; this takes 2.
 template <int MODE, int NI, int NJ>
-__device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0, int jb0, bool both,
+__device__ __forceinline__ void epilogue_blocks(const MulArgs& a, float lift, int b, int ib0, int jb0, bool both,
                                                 const f32x16_t (&acc)[NI][NJ], char* lds) {
+    const float so = a.so * lift;
     const int lane = threadIdx.x & 63, rl = lane & 31, kh = lane >> 5;
     const int pb = a.pr >> 5, qb = a.qr >> 5;
     // piece q (rows 8 q .. + 7) of the transposed block; + LO for the low plane
@@ -511,7 +535,7 @@ __device__ __forceinline__ void epilogue_blocks(const MulArgs& a, int b, int ib0
             uint32_t oh[2], ol[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float x = v[2 * e] * a.so, y = v[2 * e + 1] * a.so;
+                const float x = v[2 * e] * so, y = v[2 * e + 1] * so;
                 const f16x2_t h = {(_Float16)x, (_Float16)y};
                 const f16x2_t l = {(_Float16)(x - (float)h[0]), (_Float16)(y - (float)h[1])};
                 oh[e] = __builtin_bit_cast(uint32_t, h);
@@ -593,6 +617,7 @@ __device__ __forceinline__ void product_tile(const MulArgs& a, int b, int i0, in
     constexpr int PIECE = 1024, ENTRY = 2 * KS * PIECE;      // a block's share of a stage: [plane][half]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const float lift = lift_factor<MODE>(a, b);
 
     // stage sources: wavefront w brings blocks w NB / 2 .. of the P then Q block
     // rows, 2 KS transfers of 1 KiB each.  Block rows past the padded end (tiles
@@ -695,7 +720,7 @@ __device__ __forceinline__ void product_tile(const MulArgs& a, int b, int i0, in
 
     if constexpr (MODE != FINAL) {
         char* mine = NS == 2 ? st0 + wave * BLOCK : wave == 0 ? st0 : wave == 1 ? st1 : wave == 2 ? st2 : st3;
-        epilogue_blocks<MODE>(a, b, (i0 >> 5) + NI * wi, (j0 >> 5) + NI * wj, both, acc, mine);
+        epilogue_blocks<MODE>(a, lift, b, (i0 >> 5) + NI * wi, (j0 >> 5) + NI * wj, both, acc, mine);
         return;
     }
     // ---- the target: the fp32 tile through LDS, T / NS rows a buffer
@@ -720,7 +745,7 @@ __device__ __forceinline__ void product_tile(const MulArgs& a, int b, int i0, in
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = at(r, c + e);
     };
-    epilogue<MODE, T, 256>(a, b, i0, j0, true, sum8, at);
+    epilogue<MODE, T, 256>(a, lift, b, i0, j0, true, sum8, at);
 }
 
 template <int MODE, int NI, int KS, int NS>
@@ -783,6 +808,7 @@ __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs 
     int b, ti, tj;
     tile_of<SYM>(a, xcd_remap(blockIdx.x, gridDim.x), b, ti, tj);
     const int i0 = ti * LT, j0 = tj * LT;
+    const float lift = lift_factor<MODE>(a, b);
     const int KT = a.K / KB;     // even
     const char* ps = a.p + b * a.p_stride + (int64_t)min((i0 >> 5) + wave, (a.pr >> 5) - 1) * KT * BLOCK;
     const char* qs = a.q + b * a.q_stride + (int64_t)min((j0 >> 5) + wave, (a.qr >> 5) - 1) * KT * BLOCK;
@@ -862,7 +888,7 @@ __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs 
     __syncthreads();
 
     if constexpr (MODE != FINAL) {
-        epilogue_blocks<MODE>(a, b, (i0 >> 5) + 4 * wi, (j0 >> 5) + 2 * wj, !SYM || ti != tj, acc, st0 + wave * BLOCK);
+        epilogue_blocks<MODE>(a, lift, b, (i0 >> 5) + 4 * wi, (j0 >> 5) + 2 * wj, !SYM || ti != tj, acc, st0 + wave * BLOCK);
         return;
     }
     // ---- the target by quadrants, a row of two at a time
@@ -890,7 +916,7 @@ __global__ __launch_bounds__(512, 2) void ns_product_large_kernel(const MulArgs 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = at(r, c + e);
             };
-            epilogue<MODE, BT, 512>(a, b, i0 + BT * qi, j0 + BT * qj, true, sum8, at);
+            epilogue<MODE, BT, 512>(a, lift, b, i0 + BT * qi, j0 + BT * qj, true, sum8, at);
         };
         quadrant(st0, st1, 0);
         quadrant(st2, st3, 1);
@@ -915,6 +941,7 @@ __global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulA
     int b, ti, tj;
     tile_of<SYM>(a, xcd_remap(blockIdx.x, gridDim.x), b, ti, tj);
     const int rl = lane & 31, kh = lane >> 5;
+    const float lift = lift_factor<MODE>(a, b);
     const int KT = a.K / KB;
     const char* pp = a.p + b * a.p_stride + (int64_t)ti * KT * BLOCK;
     const char* qp = a.q + b * a.q_stride + (int64_t)tj * KT * BLOCK;
@@ -962,7 +989,7 @@ __global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulA
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += part[w][r * LD + c + e];
     };
-    epilogue<MODE, DT, 64 * DW>(a, b, ti * DT, tj * DT, !SYM || ti != tj, sum8, at);
+    epilogue<MODE, DT, 64 * DW>(a, lift, b, ti * DT, tj * DT, !SYM || ti != tj, sum8, at);
 }
 
 // ------------------------------------------------- short sides of up to 64
@@ -1380,7 +1407,7 @@ int small_blocks(int M, int N) {
 }
 
 struct Layout {
-    size_t part, x, xt[2], sym[kSyms], total;
+    size_t part, lift, x, xt[2], sym[kSyms], total;
 };
 
 moe_status check_sizes(int B, int M, int N) {
@@ -1404,6 +1431,7 @@ Layout layout_of(int B, int M, int N) {
         return at;
     };
     L.part = take((size_t)B * norm_blocks((int64_t)M * N) * sizeof(double));
+    L.lift = take((size_t)B * sizeof(int));
     L.x = take((size_t)B * m * n * 4);
     L.xt[0] = take((size_t)B * m * n * 4);
     L.xt[1] = take((size_t)B * m * n * 4);
@@ -1541,7 +1569,8 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     if (steps < 1 || steps > kMaxSteps) return MOE_ERR_INVALID_ARG;
     if (!(eps >= 0.) || !isfinite(eps) || !isfinite(a) || !isfinite(b) || !isfinite(c))
         return MOE_ERR_INVALID_ARG;
-    double mid[kMaxSteps], whole[kMaxSteps], top[kMaxSteps + 1];
+    double mid[kMaxSteps], whole[kMaxSteps], top[kMaxSteps + 1], grown = 1.;
+    int room[kMaxSteps + 1] = {};
     top[0] = 1.;
     for (int k = 0; k < steps; ++k) {
         if (!step_bounds(a, b, c, top[k], &mid[k], &whole[k], &top[k + 1])) return MOE_ERR_UNSUPPORTED;
@@ -1549,6 +1578,9 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
         // zero coefficients are exact)
         if (top[k] != 0. && top[k] < 1e-9) return MOE_ERR_UNSUPPORTED;
         if (whole[k] != 0. && whole[k] < (1. + fabs(b) + fabs(c)) * 1e-12) return MOE_ERR_UNSUPPORTED;
+        // top is at most what the polynomials' product lets 1 grow to; all is zero with whole
+        grown *= whole[k];
+        if (grown > 0.) room[k + 1] = ilogb(top[k + 1] / grown);
     }
     if (B == 0) return MOE_OK;
     (void)hipGetLastError();
@@ -1611,7 +1643,8 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     char* xt[2] = {ws + L.xt[0], ws + L.xt[1]};
     double sx = scale_for(top[0]);
     const int Mp = pad64(M), Np = pad64(N);
-    const SplitArgs sp = {src, (const double*)(ws + L.part), nb, M, N, Mp, Np, eps, (float)sx,
+    int* lift = (int*)(ws + L.lift);
+    const SplitArgs sp = {src, (const double*)(ws + L.part), nb, M, N, Mp, Np, eps, (float)sx, lift,
                           tall ? xt[0] : x, tall ? x : xt[0]};
     ns_split_kernel<<<dim3(Np / ST, Mp / ST, B), 256, 0, stream>>>(sp);
     if (!ok()) return MOE_ERR_HIP;
@@ -1630,6 +1663,7 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     MulArgs y = {};      // a product on the short side
     y.p_stride = y.q_stride = y.add_stride = y.c_stride = as;
     y.pr = y.qr = y.K = m;
+    y.lift = lift;
     auto symm = [&](Plane P, Plane Q, double f, double fp, double fq, Plane out) {
         MulArgs g = y;
         g.p = g.add = P.p;
@@ -1666,6 +1700,7 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
         g.p = g.q = x;
         g.p_stride = g.q_stride = xs;
         g.K = n;
+        g.room = room[k];
         g.f = (float)(1. / (sx * sx));
         g.so = (float)A.scale;
         g.c = g.ct = A.p;
@@ -1692,8 +1727,10 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
                 A = next;
             }
         }
-        k += group;
         MulArgs z = y;
+        z.room = room[k];
+        k += group;
+        z.room_after = room[k];
         z.p = R.p;
         z.q = xt[turn];
         z.q_stride = z.add_stride = z.c_stride = xs;

@@ -607,7 +607,9 @@ size_t moe_newton_schulz_workspace_size(int B, int M, int N);
  *
  * Results are those of fp32 arithmetic (fp16 pairs of 22 bits on the matrix
  * cores, fp32 sums; small matrices: fp64), rounded once to
- * dtype; the norm is summed in fp64, so gradients of any magnitude will do.
+ * dtype; the norm is summed in fp64 and every matrix has a power of two of its
+ * own, so gradients of any magnitude will do, those with |U| far below eps
+ * included (with a = 0, whose X is then of |U / eps|^3, those lose precision or end as zeros).
  * Summation orders are fixed: repeated calls give equal bits.  A zero
  * matrix gives zeros (eps > 0); one that holds an infinity or NaN gives NaN,
  * the others of the batch are untouched by it.
