@@ -578,9 +578,10 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False, ou
     """moe_layer_norm_forward: y = (h - mean) rstd weight + bias over the rows
     of h = x (+ residual), x and residual [T,D], weight and bias [D] of x's
     dtype (None: 1, 0); with rms the mean is not taken off.  Returns y, h (x
-    itself without a residual, else the rounded sum), and the fp32 [T] mean
-    (None with rms) and rstd that layer_norm_backward takes (both None
-    with stats=False).  ``out`` may supply y and h."""
+    itself without a residual, None where y took its place; else the rounded
+    sum), and the fp32 [T] mean (None with rms) and rstd that
+    layer_norm_backward takes (both None with stats=False).  ``out`` may supply
+    y (x's buffer too) and h."""
     dt, shape, dev, dtype = x.dtype, x.shape, x.get_device(), _dtype_enum(x.dtype)
     if len(shape) != 2:
         raise ValueError("x must be [T,D]")
@@ -616,7 +617,7 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False, ou
     if st:
         raise MoeError(st, "moe_layer_norm_forward")
     if h is None:
-        o["h"] = x
+        o["h"] = None if T and o["y"].data_ptr() == x.data_ptr() else x
     o["mean"], o["rstd"] = mean, rstd
     return o
 
