@@ -392,6 +392,7 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_backward_kernel(cons
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 z[e] = (z[e] - mean) * rstd;
+                if (TAIL) z[e] = e < left(i) ? z[e] : 0.f;
                 g[e] = a.w ? g[e] * dy[e] : dy[e];
             }
         };
@@ -402,9 +403,11 @@ __global__ __launch_bounds__(threads_of<LANES>()) void norm_backward_kernel(cons
             constexpr int one = KEEP ? 1 : 0;
             float dy[VEC], *zi = z[i * one], *gi = g[i * one];
             values(i, dy, zi, gi);
+            // past the row's end nothing is added: dy is 0 there, but z, -mean rstd, may be
+            // infinite where no (h - mean) rstd is
+            if (left(i) <= 0) continue;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                // past the row's end dy is zero, and so is every sum's share
                 dw[i][e] = fmaf(dy[e], zi[e], dw[i][e]);
                 db[i][e] += dy[e];
                 sg += gi[e];
