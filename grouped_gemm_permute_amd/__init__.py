@@ -10,7 +10,8 @@ and streams, nothing else.
 """
 from ._lib import (MoeError, alloc_workspace, backward, backward_workspace_layout,  # noqa: F401
                    device_clock_sample, device_error, engine_clock_ghz, expert_permute, forward,
-                   forward_noalloc, forward_routed, forward_save_gu, layer_norm, layer_norm_backward, lib,
+                   forward_noalloc, forward_routed, forward_save_gu, layer_norm, layer_norm_backward,
+                   layer_norm_backward_workspace_size, lib,
                    muon_step, newton_schulz, newton_schulz_workspace_size, router_topk, status_string,
                    stream_read, tile_rows,
                    workspace_layout, workspace_size, EXPORTS, LIB_PATH, NOALLOC_SCRATCH_BYTES, NS_COEFFS)

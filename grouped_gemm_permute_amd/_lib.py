@@ -623,8 +623,10 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, rms=False, ou
 
 
 @functools.lru_cache(maxsize=1024)
-def _layer_norm_backward_bytes(T, D, dtype):
-    return lib().moe_layer_norm_backward_workspace_size(T, D, dtype)
+def layer_norm_backward_workspace_size(T, D, dtype) -> int:
+    """Bytes of layer_norm_backward's ``workspace`` for h [T,D] of a torch
+    dtype with dweight or dbias wanted (0: none is needed)."""
+    return lib().moe_layer_norm_backward_workspace_size(T, D, _dtype_enum(dtype))
 
 
 def layer_norm_backward(h, dy, rstd, mean=None, weight=None, dh=None, bias_grad=False, out=None,
@@ -633,7 +635,8 @@ def layer_norm_backward(h, dy, rstd, mean=None, weight=None, dh=None, bias_grad=
     [T,D], from its h, rstd and mean (None: rms).  Returns dx (x's and the
     residual's gradient, dh added when given), dweight (fp32 [D]; None
     without weight) and dbias (fp32 [D]; None without bias_grad).  ``out`` may
-    supply any of these."""
+    supply any of these, ``workspace`` the scratch bytes
+    (layer_norm_backward_workspace_size)."""
     dt, shape, dev, dtype = h.dtype, h.shape, h.get_device(), _dtype_enum(h.dtype)
     if len(shape) != 2:
         raise ValueError("h must be [T,D]")
@@ -665,7 +668,7 @@ def layer_norm_backward(h, dy, rstd, mean=None, weight=None, dh=None, bias_grad=
     for name in wanted:
         if name not in o:
             o[name] = _empty_like(h, stream) if name == "dx" else _empty(D, f32, h.device, stream)
-    n = _layer_norm_backward_bytes(T, D, dtype) if len(wanted) > 1 else 0
+    n = layer_norm_backward_workspace_size(T, D, dt) if len(wanted) > 1 else 0
     workspace = _workspace_for(h, dev, n, workspace, stream)
     dweight, dbias = o.setdefault("dweight", None), o.setdefault("dbias", None)
     st = lib().moe_layer_norm_backward(h.data_ptr(), _ptr(mean), rstd.data_ptr(), _ptr(weight), dy.data_ptr(),
@@ -692,6 +695,7 @@ def _check_matrices(name, x):
 
 @functools.lru_cache(maxsize=1024)
 def newton_schulz_workspace_size(B, M, N) -> int:
+    """Bytes of the ``workspace`` of newton_schulz and muon_step (0: none is needed)."""
     return lib().moe_newton_schulz_workspace_size(B, M, N)
 
 
