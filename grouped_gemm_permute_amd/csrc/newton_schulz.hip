@@ -1406,6 +1406,11 @@ int small_blocks(int M, int N) {
     return (m + 15) / 16;
 }
 
+// 128 x 128 tiles of a matrix's planes.
+int64_t tiles128(int M, int N) {
+    return (int64_t)((pad64(M) + BT - 1) / BT) * ((pad64(N) + BT - 1) / BT);
+}
+
 struct Layout {
     size_t part, lift, x, xt[2], sym[kSyms], total;
 };
@@ -1413,6 +1418,8 @@ struct Layout {
 moe_status check_sizes(int B, int M, int N) {
     if (B < 0 || M <= 0 || N <= 0) return MOE_ERR_INVALID_ARG;
     if (M > kMaxSide || N > kMaxSide || B > 65535) return MOE_ERR_UNSUPPORTED;
+    // a grid's threads are fewer than 2^32
+    if (!is_small(B, M, N) && B * tiles128(M, N) >= 1 << 24) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -1625,16 +1632,13 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     char* ws = (char*)workspace;
     const bool tall = M > N;
     const int m = pad64(tall ? N : M), n = pad64(tall ? M : N);
-    // a grid's threads are fewer than 2^32
-    if ((int64_t)B * ((m + BT - 1) / BT) * ((n + BT - 1) / BT) >= 1 << 24) return MOE_ERR_UNSUPPORTED;
     // Steps in groups trade 3 m^2 n products of a step for up to 4 m^3, and lose a
     // little (all steps 3.5x fp32's error, 1.1x one by one, so not for fp32
     // results), from long sides of 1.5 times the short on and enough tiles to
     // share out: eight 768 x 1024 417 us one by one, 419 in groups, 768 x 1152 439,
     // 432, 768 x 1536 537, 478; sixteen 1024 x 4096 3559, 2321; one 768 x 1536 (72
     // tiles) 163, 167, two 231, 219.
-    const bool grouped = (tgt.muon || tgt.out_bf16) && 2 * n >= 3 * m &&
-                         (int64_t)B * ((m + BT - 1) / BT) * ((n + BT - 1) / BT) >= 128;
+    const bool grouped = (tgt.muon || tgt.out_bf16) && 2 * n >= 3 * m && B * tiles128(M, N) >= 128;
     const int nb = norm_blocks((int64_t)M * N);
     ns_norm_kernel<<<dim3(nb, B), 256, 0, stream>>>(src, (int64_t)M * N, (double*)(ws + L.part));
     if (!ok()) return MOE_ERR_HIP;

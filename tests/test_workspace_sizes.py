@@ -15,12 +15,15 @@ def test_layer_norm_backward_workspace_size_is_the_entry_points(T, D):
         gg.layer_norm_backward_workspace_size(T, D, torch.float16)
 
 
-def test_layer_norm_backward_refuses_a_workspace_too_small():
-    x, s = torch.zeros(2000, 64), torch.zeros(2000)
-    need = gg.layer_norm_backward_workspace_size(2000, 64, torch.float32)
-    assert need > 0
+def test_newton_schulz_workspace_size_of_what_is_not_supported():
+    """0, as for sizes out of range, where the matrices' 128 x 128 tiles are 2^24 or more; one tile fewer has a size."""
+    size = gg.newton_schulz_workspace_size
+    assert size(65535, 4096, 4096) == 0 and size(16384, 4096, 4096) == 0
+    assert size(16383, 4096, 4096) > 16383 * 12 * 4096 * 4096
+    assert size(65535, 32768, 8) > 0                       # no tiles: short sides of up to 32 have none
+    assert size(1, 32769, 64) == 0 and size(65536, 64, 64) == 0
     with pytest.raises(ValueError, match="GPU"):
-        gg.layer_norm_backward(x, x, s, s, torch.zeros(64), workspace=torch.zeros(need, dtype=torch.uint8))
+        gg.newton_schulz(torch.empty(16384, 4096, 4096, device="meta"))
 
 
 @pytest.mark.gpu
