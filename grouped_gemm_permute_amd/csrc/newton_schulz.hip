@@ -1632,10 +1632,15 @@ moe_status run(const Source& src, const Target& tgt, int B, int M, int N, int st
     char* ws = (char*)workspace;
     const bool tall = M > N;
     const int m = pad64(tall ? N : M), n = pad64(tall ? M : N);
-    // Steps in groups trade 3 m^2 n products of a step for up to 4 m^3, and lose a
-    // little (all steps 3.5x fp32's error, 1.1x one by one, so not for fp32
-    // results), from long sides of 1.5 times the short on and enough tiles to
-    // share out: eight 768 x 1024 417 us one by one, 419 in groups, 768 x 1152 439,
+    // Steps in groups trade 3 m^2 n products of a step for up to 4 m^3, and lose
+    // precision: A's rounding grows by P^2 in each step that A takes by itself, where that of a
+    // new X X^T does not.  Five steps against 64 bits, in errors of the same iteration in fp32:
+    // eight 768 x 1536 1.9 (one by one 0.8), four 1024 x 4096 1.6 (0.75), sixteen 256 x 512 2.1 (0.9),
+    // 40 of 200 x 500 with strong directions 2.9 (0.8), 5e-6 to 7e-6 of |X|; the most 5.9, for three
+    // steps of 128 of 70 x 200.  So they are not for fp32 results, but for those that
+    // are rounded to bf16 (2^-8) or added to weights, W - rate X: at a rate of 0.02 that is 1e-7 of X, the
+    // half step of an fp32 weight of X's size.  They pay from long sides of 1.5 times the short on and
+    // enough tiles to share out: eight 768 x 1024 417 us one by one, 419 in groups, 768 x 1152 439,
     // 432, 768 x 1536 537, 478; sixteen 1024 x 4096 3559, 2321; one 768 x 1536 (72
     // tiles) 163, 167, two 231, 219.
     const bool grouped = (tgt.muon || tgt.out_bf16) && 2 * n >= 3 * m && B * tiles128(M, N) >= 128;

@@ -1,10 +1,11 @@
 """Newton-Schulz and the Muon step where eps holds X_0 = U / (|U| + eps) far below 1: a gradient, or the momentum
 of an expert without tokens that decays, down to 10^-30 beside the default eps of 10^-7.
 
-Tolerance: fp32 rounds a value by half a step, u = 2^-24.  The kernels round it to a pair of fp16 planes,
-u too, and leave out the products of two low parts, u of a product: two roundings for each of fp32's.  The errors
-of both are sums of such roundings, the kernels' at most twice as large for the same sums, and half as much
-again for another order: 3 times the error of the same iteration in fp32, from the same matrix, plus
+Tolerance, in norms, so roundings count by their root mean square.  A value's pair of fp16 planes (2^-11 of 2^-11) is off
+by 2^-24.6 of it, a product without that of its low parts by 2^-24.6, fp32's own rounding by 2^-25.3: a product of two pairs by
+2.8 times that.  Of a sum of K >= 64 products of either sign these leave 2.8 sqrt(K) of such roundings; the sum itself, in fp32 by
+16 partial sums (torch's on a CPU), leaves K / sqrt(32), in the kernels about as much: together less than sqrt(1 + 2.8^2 32 / K) + 1
+= 3.2 times fp32's error at K = 64, 2.3 at 300.  The shortest sums here have 66 to 100 products and the others in a step more: 3 times, plus
 16 u |X| where that happens to be nearly exact.
 """
 import pytest
