@@ -3,9 +3,9 @@ of an expert without tokens that decays, down to 10^-30 beside the default eps o
 
 Tolerance, in norms, so roundings count by their root mean square.  A value's pair of fp16 planes (2^-11 of 2^-11) is off
 by 2^-24.6 of it, a product without that of its low parts by 2^-24.6, fp32's own rounding by 2^-25.3: a product of two pairs by
-2.8 times that.  Of a sum of K >= 64 products of either sign these leave 2.8 sqrt(K) of such roundings; the sum itself, in fp32 by
-16 partial sums (torch's on a CPU), leaves K / sqrt(32), in the kernels about as much: together less than sqrt(1 + 2.8^2 32 / K) + 1
-= 3.2 times fp32's error at K = 64, 2.3 at 300.  The shortest sums here have 66 to 100 products and the others in a step more: 3 times, plus
+2.8 times that.  A sum of K products of either sign keeps sqrt(K) of theirs and adds K / sqrt(32) of its own (16 partial sums,
+as torch's on a CPU), in fp32 and in the kernels alike.  The kernels' error over fp32's on the same matrix is then
+sqrt((2.8^2 K + K^2 / 32) / (K + K^2 / 32)), 1.8 at K = 64 and less beyond; half as much again for chance: 3 times, plus
 16 u |X| where that happens to be nearly exact.
 """
 import pytest
