@@ -441,7 +441,8 @@ def block_step_record(workload, steps, warmup):
     """A pre-norm block's training step on one workload, its operators one
     after the other: residual sum and layer norm, router, layer (gate and up
     products kept), the layer's backward, the norm's backward, and a Muon step
-    on each expert matrix (fp32 weights beside the bf16 ones the layer reads).
+    on each expert matrix and each of the shared expert's (fp32 weights beside
+    the bf16 ones the layer reads; the gate's and the norm's weights stay).
     Each call is timed alone and the step as a whole (host clock between two
     synchronisations); one JSON line."""
     import torch
@@ -463,8 +464,9 @@ def block_step_record(workload, steps, warmup):
     W1, W3 = n(w.E, w.D, w.F, by=w.D ** -0.5), n(w.E, w.D, w.F, by=w.D ** -0.5)
     W2 = n(w.E, w.F, w.D, by=w.F ** -0.5)
     shared = (n(w.D, w.F, by=w.D ** -0.5), n(w.D, w.F, by=w.D ** -0.5), n(w.F, w.D, by=w.F ** -0.5)) if w.shared else None
+    names = ("dW1", "dW3", "dW2", "dWs1", "dWs3", "dWs2")
     state = {name: (t, t.float(), torch.zeros(t.shape, device="cuda"))
-             for name, t in (("dW1", W1), ("dW3", W3), ("dW2", W2))}
+             for name, t in zip(names, (W1, W3, W2, *(shared or ())))}
     log(f"block-step workload {w.name}")
     keep = {}
 
@@ -492,7 +494,7 @@ def block_step_record(workload, steps, warmup):
             gg.muon_step(master, keep["g"][name], mom, 1e-3, W_bf16=t)
 
     calls = {"layer_norm": norm, "router_topk": router, "forward_save_gu": forward, "backward_cached": backward,
-             "layer_norm_backward": norm_backward, "muon_step_x3": muon}
+             "layer_norm_backward": norm_backward, f"muon_step_x{len(state)}": muon}
     calls["step"] = lambda fs=tuple(calls.values()): [f() for f in fs]
     ms = {}
     for name, f in calls.items():
@@ -935,7 +937,8 @@ def main():
                          "recomputed by the backward or kept from the forward (bf16 workloads)")
     ap.add_argument("--block-step", action="store_true",
                     help="time a pre-norm block's training step: layer norm, router, layer, its "
-                         "backward, the norm's backward and a Muon step on the expert matrices")
+                         "backward, the norm's backward and a Muon step on the experts' and the shared "
+                         "expert's matrices")
     ap.add_argument("--routed", action="store_true",
                     help="time moe_ffn_forward_routed: the top-k router (x @ gate_w, top-k, softmax) "
                          "feeding the permute, then the same forward")
