@@ -742,7 +742,7 @@ def muon_step(W, dW, momentum, lr, beta=0.95, weight_decay=0.0, scale=None, nest
             _refuse(W, W_bf16=(W_bf16, W.shape, torch.bfloat16))
     _on_current_device(W, dev)
     if scale is None:
-        scale = max(1.0, N / M) ** 0.5
+        scale = max(1.0, N / max(1, M)) ** 0.5
     n = newton_schulz_workspace_size(B, M, N)
     workspace = _workspace_for(W, dev, n, workspace, stream)
     a, b, c = coeffs

@@ -40,3 +40,12 @@ def test_a_callers_workspace_of_just_that_size():
             assert all(torch.equal(got[k], want[k]) for k in ("dx", "dweight", "dbias"))
         with pytest.raises(ValueError, match="needs"):
             gg.layer_norm_backward(x, dy, f["rstd"], f["mean"], w, bias_grad=True, workspace=ws[:-1])
+
+
+@pytest.mark.gpu
+def test_matrices_without_rows_or_columns_are_refused_as_such():
+    for shape in ((2, 0, 5), (2, 5, 0), (0, 0)):
+        W, m = torch.empty(shape, device="cuda"), torch.empty(shape, device="cuda")
+        for call in (lambda: gg.newton_schulz(W), lambda: gg.muon_step(W, m, m, 0.1)):
+            with pytest.raises(gg.MoeError, match="INVALID_ARG"):
+                call()
