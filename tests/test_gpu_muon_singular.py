@@ -117,3 +117,37 @@ def test_a_matrix_by_itself_and_in_a_batch_over_long_runs():
         assert (out[1] == 0).all() and torch.isnan(out[2]).all() and torch.isnan(out[3]).all()
         for k in (0, 4):
             assert torch.equal(gg.newton_schulz(G[k].contiguous().cuda(), steps=40).cpu(), out[k])
+
+
+@pytest.mark.parametrize("kind", ["rank1", "rank3", "last", "repeated", "zeros", "integers"])
+@pytest.mark.parametrize("B,M,N", [c for c in SHAPES if min(c[1:]) <= 64])
+def test_lacking_matrices_against_64_bits(B, M, N, kind):
+    """Short runs, entry by entry, where each side still has fp64's rounding alone.  A, a sum of products of a side of up
+    to 64, is off by 64 2^-53 between the directions that U has and lacks, and a step multiplies that by a (P is a on
+    the one side, about 1 on the other).  The product of the polynomials, a^k in the directions that U lacks, takes it in by
+    b A: 64 2^-53 |b| a^(2 (steps - 1)) of the largest entry at most in the last step, most of the sum over the steps.
+    The rest is 2^-33 as for any matrix of such a side, and fp32's half step."""
+    G = lacking(kind, B, M, N, torch.Generator().manual_seed(M + N))
+    for steps in (1, 5, 7):
+        most = 2.0**-33 + 64 * 2.0**-53 * abs(MUON[1]) * MUON[0] ** (2 * (steps - 1))
+        say(f"newton_schulz {B}x{M}x{N} {kind} steps{steps}")
+        got = gg.newton_schulz(G.cuda(), steps=steps).double().cpu()
+        want = iterate(G, steps, MUON, 1e-7, torch.float64)
+        off = (got - want).abs() - U * want.abs() * 1.001
+        assert (off <= most * want.abs().amax((-1, -2), keepdim=True)).all(), float(off.max())
+
+
+@pytest.mark.parametrize("kind", ["rank1", "rank3", "last", "repeated", "zeros", "integers"])
+def test_steps_taken_together_stay_bounded(kind):
+    """Muon steps in groups (long sides of 1.5 times the short and 128 tiles and more), over long runs."""
+    for B, M, N in ((16, 256, 512), (40, 500, 200)):
+        dW = lacking(kind, B, M, N, torch.Generator().manual_seed(N)).cuda()
+        for coeffs in (MUON, QUINTIC, CUBIC, LOGISTIC):
+            top = tops(coeffs, 64)
+            for steps in (5, 12, 24, 64):
+                W, mom = torch.zeros_like(dW), torch.zeros_like(dW)
+                say(f"muon_step {B}x{M}x{N} {kind} {coeffs} steps{steps}")
+                gg.muon_step(W, dW, mom, 1.0, scale=1.0, steps=steps, coeffs=coeffs)
+                assert torch.isfinite(W).all(), (coeffs, steps)
+                s = float(torch.linalg.svdvals(W[:2].double().cpu()).max())
+                assert s <= top[steps], f"{coeffs} steps{steps}: singular value {s} over {top[steps]}"
