@@ -12,10 +12,10 @@
 // Both are bound by memory: a row is read once, held in registers as fp32
 // while its sums are formed (so the variance is the sum of squared
 // deviations, not a difference of large sums), and written once.  A row
-// belongs to LANES lanes, each holding NV vectors of 16 bytes: 8, 32 or 64
-// lanes of a wavefront with shuffle sums for rows of up to 32, 128 and 256
-// vectors, a whole workgroup of 256 or 1024 threads with sums through LDS for
-// longer ones.  16-byte accesses are taken at any element alignment (the
+// belongs to LANES lanes, each holding up to NV vectors of 16 bytes, 3 of bf16 or 4 of
+// fp32: 8, 32 or 64 lanes of a wavefront with shuffle sums for rows of up to 24, 96
+// and 192 vectors of bf16 (32, 128 and 256 of fp32), a whole workgroup of 256 or 1024
+// threads with sums through LDS for longer ones.  16-byte accesses are taken at any element alignment (the
 // global memory path splits those that straddle a line), so an odd D costs
 // only the element-wise tail of each row.
 //
@@ -517,7 +517,11 @@ struct Shape {
 };
 // Lanes per row and 16-byte vectors per lane: the fewest lanes that hold the
 // row in 24 bf16 or 16 fp32 elements each.  Their fp32 copies and, in the
-// backward, their gradient sums stay in registers; with a fourth bf16 vector
+// backward, their gradient sums stay in registers, but for the backward of more than
+// 8192 elements, whose 1024 threads have 128 registers each: it keeps the packed row and still
+// spills (10 registers a lane in bf16, 28 with tails; 20 to 109 in fp32), which with one workgroup
+// a unit leaves 2.8 TB/s (2048 x 16384 bf16 73 us without dh) where narrower rows have
+// 4.2 to 5.7.  With a fourth bf16 vector
 // the backward has one wavefront a SIMD (4096 x 777: 24 us instead of 16).
 Shape shape_of(int D, moe_dtype dt) {
     const int vec = dt == MOE_BF16 ? 8 : 4, most = dt == MOE_BF16 ? 3 : 4, nvec = (D + vec - 1) / vec;
@@ -530,8 +534,8 @@ int threads_for(int lanes) { return lanes > 256 ? lanes : 256; }
 
 constexpr int64_t kFwdMaxBlocks = 2048;
 // Partial rows of the backward: two workgroups a unit, one where it is 1024 threads
-// wide (8192 x 8191 fp32 178 -> 169 us, 2048 x 16384 bf16 131 -> 110; with 256 of the narrower
-// 8192 x 4096 bf16 would be 54 -> 74).
+// wide (with dh: 8192 x 8191 fp32 216 -> 207 us, 2048 x 16384 bf16 113 -> 92; with 256 of the narrower
+// 8192 x 4096 bf16 would be 56 -> 70, 32768 x 768 36 -> 42).
 int64_t bwd_blocks(int lanes) { return lanes == 1024 ? 256 : 512; }
 unsigned grid_of(int64_t T, int lanes, int64_t most) {
     const int64_t rows = threads_for(lanes) / lanes, need = (T + rows - 1) / rows;

@@ -12,7 +12,7 @@
 // An operand is held as two fp16 planes, hi = f16(v s) and lo = f16(v s - hi)
 // with a power of two s, 22 bits of v together, and a product takes the
 // three terms hi hi + hi lo + lo hi, summed in fp32: 3 of the fast fp16
-// instructions (16x the fp32 ones' rate) keep the iteration within 1.1x of
+// instructions (16x the fp32 ones' rate) keep the iteration at 0.3 to 1.3 of
 // fp32's own error, where one fp16 or bf16 plane leaves 2e-3 to 2e-2, since
 // small singular values grow by a factor a in each step and their rounding
 // with them.  s comes from a bound on the singular values: the host follows
@@ -999,7 +999,8 @@ __global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulA
 // the m x m side alone,
 //   A <- P A P,  Q <- Q P  with P = a I + b A + c A A,
 // in fp64 (whose rounding the growth of small singular values leaves far below
-// fp32's), and X = Q U / (|U| + eps), |U|^2 = trace(U U^T), takes U once more.
+// fp32's; for long runs see ns_small_kernel), and X = Q U / (|U| + eps), |U|^2 = trace(U U^T),
+// takes U once more.
 // One workgroup sums A for a chunk of the long side; each workgroup of the second
 // launch adds the chunks' sums, runs the steps by itself and multiplies its
 // own chunk.  A matrix of one chunk takes a single launch.
@@ -1015,7 +1016,10 @@ __global__ __launch_bounds__(64 * DW, 2) void ns_product_split_kernel(const MulA
 typedef __attribute__((ext_vector_type(4))) double f64x4_t;
 constexpr int kMaxSteps = 64;
 
-// Short sides beyond 32 by the workgroups that would run, each of which takes the
+// Which short sides go this way.  Up to 32 all: of 91 batches of 1 to 2048 matrices of 8, 16, 24 and 32 by 64
+// to 32768 the planes, padded to 64 rows, took 1.9 to 25 times as long (2048 of 8 x 64: 24 us, 258
+// in planes; one 32 x 4096 23, 111; 128 of them 305, 714; 512 1383, 2645, the nearest; 128 of
+// 32 x 32768 1461, 5756).  Beyond 32 by the workgroups that would run, each of which takes the
 // steps by itself: up to 512 with short sides of up to 48 (512 of 48 x 48: 62 us, 107 in planes;
 // 8 of 48 x 768 39, 67), 256 up to 64 (64 x 64: 51, 62; 64 x 4096 69, 108; 256 of 64 x 64 54, 71, 300
 // would be 102, 85).
@@ -1025,7 +1029,7 @@ constexpr int64_t small_most(int m) { return m <= 32 ? INT64_MAX : m <= 48 ? 512
 // 9.3 in two launches; 384 x 8: 8.3, 9.3; 768 x 8: 11.7, 9.7; 768 x 16: 15.3, 10.5; 32 x 192:
 // 16.6, 17.2; 32 x 256: 18.7, 17.7); otherwise 128, one turn of 8 wavefronts, or more
 // where that would be over 64 chunks, whose sums each workgroup adds (32 x 4096:
-// 27 us, 331 by one workgroup).
+// 23 us, 331 by one workgroup).
 int small_chunk(int M, int N) {
     const int m = M < N ? M : N, n = M < N ? N : M;
     if (m <= 32 && n <= (m <= 16 ? 384 : 256)) return n;

@@ -615,6 +615,8 @@ size_t moe_newton_schulz_workspace_size(int B, int M, int N);
  * on the short side alone: before the last rounding they are off by up to 8
  * times as much as fp32 arithmetic (measured 0.4 to 6; eight 768 x 1536 twice,
  * 7e-6 of |X|; one step at a time 0.3 to 1.3).
+ * Singular values below about 2^-23 |U|, which fp32 arithmetic does not tell from
+ * its rounding, may end between 0 and what exact steps make of them.
  * Summation orders are fixed: repeated calls give equal bits.  A zero
  * matrix gives zeros (eps > 0); one that holds an infinity or NaN gives NaN,
  * the others of the batch are untouched by it.
