@@ -613,8 +613,8 @@ size_t moe_newton_schulz_workspace_size(int B, int M, int N);
  * In bf16 results and in moe_muon_step, batches of 128 or more 128 x 128 tiles
  * with long sides from 1.5 times the short on take up to three steps at a time
  * on the short side alone: before the last rounding they are off by up to 8
- * times as much as fp32 arithmetic (measured 0.4 to 6; eight 768 x 1536 twice,
- * 7e-6 of |X|; one step at a time 0.3 to 1.3).
+ * times as much as fp32 arithmetic (2 to 7 steps of the usual coefficients: 0.4
+ * to 6 measured, eight 768 x 1536 twice, 7e-6 of |X|; one step at a time 0.3 to 1.3).
  * Singular values below about 2^-23 |U|, which fp32 arithmetic does not tell from
  * its rounding, may end between 0 and what exact steps make of them.
  * Summation orders are fixed: repeated calls give equal bits.  A zero
