@@ -32,6 +32,9 @@ EXPORTS = (
     "moe_ffn_backward_cached_timed", "moe_layer_norm_forward",
     "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward",
     "moe_newton_schulz_workspace_size", "moe_newton_schulz", "moe_muon_step",
+    "moe_embedding_forward", "moe_embedding_backward_workspace_size", "moe_embedding_backward",
+    "moe_cross_entropy_workspace_size", "moe_cross_entropy_forward", "moe_cross_entropy_backward",
+    "moe_distillation_workspace_size", "moe_distillation_forward", "moe_distillation_backward",
 )
 
 # Bytes of the per-device workspace array behind moe_ffn_forward_noalloc.
@@ -136,6 +139,24 @@ def lib():
         L.moe_newton_schulz.argtypes = [P, P, ci, ci, ci, ci, cd, cd, cd, cd, ci, P, sz, P]
         L.moe_muon_step.restype = ci
         L.moe_muon_step.argtypes = [P, P, P, P, ci, ci, ci, cf, cf, cf, cf, ci, ci, cd, cd, cd, cd, ci, P, sz, P]
+        L.moe_embedding_forward.restype = ci
+        L.moe_embedding_forward.argtypes = [P, P, P, i64, ci, ci, cf, ci, P]
+        L.moe_embedding_backward_workspace_size.restype = sz
+        L.moe_embedding_backward_workspace_size.argtypes = [i64, ci, ci]
+        L.moe_embedding_backward.restype = ci
+        L.moe_embedding_backward.argtypes = [P, P, P, i64, ci, ci, cf, ci, ci, ci, P, sz, P]
+        L.moe_cross_entropy_workspace_size.restype = sz
+        L.moe_cross_entropy_workspace_size.argtypes = [i64, ci, ci, ci, ci]
+        L.moe_cross_entropy_forward.restype = ci
+        L.moe_cross_entropy_forward.argtypes = [P] * 5 + [i64, ci, ci, ci, P, sz, P]
+        L.moe_cross_entropy_backward.restype = ci
+        L.moe_cross_entropy_backward.argtypes = [P] * 7 + [i64, ci, ci, ci, ci, P, sz, P]
+        L.moe_distillation_workspace_size.restype = sz
+        L.moe_distillation_workspace_size.argtypes = [i64, ci, ci, ci, ci, ci]
+        L.moe_distillation_forward.restype = ci
+        L.moe_distillation_forward.argtypes = [P] * 7 + [i64, ci, ci, ci, cf, ci, P, sz, P]
+        L.moe_distillation_backward.restype = ci
+        L.moe_distillation_backward.argtypes = [P] * 9 + [i64, ci, ci, ci, cf, ci, ci, P, sz, P]
         L.moe_ffn_get_device_error.restype = ci
         L.moe_ffn_get_device_error.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
         _lib = L
@@ -752,3 +773,248 @@ def muon_step(W, dW, momentum, lr, beta=0.95, weight_decay=0.0, scale=None, nest
     if st:
         raise MoeError(st, "moe_muon_step")
     return W
+
+
+def _check_table(name, table):
+    """(V, D) of a dense [V,D] table of a library dtype."""
+    _dtype_enum(table.dtype)
+    if table.dim() != 2:
+        raise ValueError(f"{name} must be [V,D]")
+    if not table.is_contiguous():
+        _refuse(table, **{name: (table, table.shape, table.dtype)})
+    _check_sizes(V=table.shape[0], D=table.shape[1])
+    return table.shape
+
+
+def _check_sizes(**sizes):
+    """Sizes that the C ABI takes as int."""
+    for name, n in sizes.items():
+        if not 0 < n < 1 << 31:
+            raise ValueError(f"{name} must be in [1, 2^31), got {n}")
+
+
+def embedding(ids, table, scale=1.0, out=None, stream=None):
+    """moe_embedding_forward: y [T,D] = scale table[ids] for ids int32 [T] and
+    table [V,D]; zeros where an id is outside [0, V)."""
+    V, D = _check_table("table", table)
+    dev, dt = table.get_device(), table.dtype
+    if ids.dim() != 1:
+        raise ValueError("ids must be [T]")
+    T = ids.shape[0]
+    if not _fits(ids, (T,), torch.int32, dev):
+        _refuse(table, ids=(ids, (T,), torch.int32))
+    if out is not None and not _fits(out, (T, D), dt, dev):
+        _refuse(table, out=(out, (T, D), dt))
+    _on_current_device(table, dev)
+    if out is None:
+        out = _empty((T, D), dt, table.device, stream)
+    st = lib().moe_embedding_forward(ids.data_ptr(), table.data_ptr(), out.data_ptr(), T, D, V, scale, _dtype_enum(dt),
+                                     _raw_stream(stream, dev))
+    if st:
+        raise MoeError(st, "moe_embedding_forward")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def embedding_backward_workspace_size(T, D, V) -> int:
+    """Bytes of embedding_backward's ``workspace`` for T tokens and a table [V,D]."""
+    return lib().moe_embedding_backward_workspace_size(T, D, V)
+
+
+def _grad_dtype(grad_dtype, out, dt, what):
+    """The type of a table's gradient: that of ``out``, else ``grad_dtype``, else the operands'."""
+    if grad_dtype is None:
+        grad_dtype = dt if out is None else out.dtype
+    if grad_dtype not in (torch.float32, dt):
+        raise TypeError(f"{what} must be torch.float32 or {dt}, got {grad_dtype}")
+    return grad_dtype
+
+
+def embedding_backward(ids, dy, V, scale=1.0, grad_dtype=None, accumulate=False, out=None, workspace=None, stream=None):
+    """moe_embedding_backward: the gradient [V,D] of embedding's table, scale
+    times the sum of dy [T,D] over each entry's tokens, in ``grad_dtype``
+    (dy's dtype by default, or torch.float32).  ``out`` may supply it;
+    ``accumulate`` adds to what ``out`` holds (a table shared with the loss)."""
+    dt, dev = dy.dtype, dy.get_device()
+    _dtype_enum(dt)
+    if dy.dim() != 2:
+        raise ValueError("dy must be [T,D]")
+    T, D = dy.shape
+    if not dy.is_contiguous():
+        _refuse(dy, dy=(dy, dy.shape, dt))
+    if not _fits(ids, (T,), torch.int32, dev):
+        _refuse(dy, ids=(ids, (T,), torch.int32))
+    _check_sizes(V=V, D=D)
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to out")
+    gdt = _grad_dtype(grad_dtype, out, dt, "the table's gradient")
+    if out is not None and not _fits(out, (V, D), gdt, dev):
+        _refuse(dy, out=(out, (V, D), gdt))
+    _on_current_device(dy, dev)
+    if out is None:
+        out = _empty((V, D), gdt, dy.device, stream)
+    n = embedding_backward_workspace_size(T, D, V)
+    workspace = _workspace_for(dy, dev, n, workspace, stream)
+    st = lib().moe_embedding_backward(ids.data_ptr(), dy.data_ptr(), out.data_ptr(), T, D, V, scale, int(accumulate),
+                                      _dtype_enum(dt), _dtype_enum(gdt), _ptr(workspace), n, _raw_stream(stream, dev))
+    if st:
+        raise MoeError(st, "moe_embedding_backward")
+    return out
+
+
+def _check_head(h, W, T_first):
+    """(T, D, V, dtype, device) of the rows h [T,D] and the table W [V,D];
+    T_first = {name: (tensor, dtype)}: tensors [T] beside them."""
+    V, D = _check_table("W", W)
+    dev, dt = W.get_device(), W.dtype
+    if h.dim() != 2:
+        raise ValueError("h must be [T,D]")
+    T = h.shape[0]
+    if not _fits(h, (T, D), dt, dev):
+        _refuse(W, h=(h, (T, D), dt))
+    for name, (t, d) in T_first.items():
+        if not _fits(t, (T,), d, dev):
+            _refuse(W, **{name: (t, (T,), d)})
+    return T, D, V, dt, dev
+
+
+def _check_teacher(W, ids, logits, T, dev, **more):
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T,K]")
+    K = ids.shape[1]
+    _check_sizes(K=K)
+    if not _fits(ids, (T, K), torch.int32, dev):
+        _refuse(W, ids=(ids, (T, K), torch.int32))
+    for name, t in dict(logits=logits, **more).items():
+        if not _fits(t, (T, K), torch.float32, dev):
+            _refuse(W, **{name: (t, (T, K), torch.float32)})
+    return K
+
+
+def _per_row(o, names, W, T, K, dev, stream):
+    """fp32 outputs [T] (z: [T,K]) in o, made where o has none."""
+    for name in names:
+        shape = (T, K) if name == "z" else (T,)
+        if name not in o:
+            o[name] = _empty(shape, torch.float32, W.device, stream)
+        elif not _fits(o[name], shape, torch.float32, dev):
+            _refuse(W, **{name: (o[name], shape, torch.float32)})
+
+
+def _head_gradients(o, wanted, W, T, D, V, dt, gdt, dev, stream):
+    for name in wanted:
+        shape, d = ((T, D), dt) if name == "dh" else ((V, D), gdt)
+        if name not in o:
+            o[name] = _empty(shape, d, W.device, stream)
+        elif not _fits(o[name], shape, d, dev):
+            _refuse(W, **{name: (o[name], shape, d)})
+    o.setdefault("dh", None)
+    o.setdefault("dW", None)
+
+
+def _wanted(wanted):
+    wanted = tuple(wanted)
+    if not wanted or any(name not in ("dh", "dW") for name in wanted):
+        raise ValueError("wanted must name dh, dW or both")
+    return wanted
+
+
+@functools.lru_cache(maxsize=1024)
+def cross_entropy_workspace_size(T, D, V, dtype, backward) -> int:
+    """Bytes of the ``workspace`` of cross_entropy (or of its backward) for h
+    [T,D] and W [V,D] of a torch dtype."""
+    return lib().moe_cross_entropy_workspace_size(T, D, V, _dtype_enum(dtype), int(backward))
+
+
+def cross_entropy(h, W, targets, out=None, workspace=None, stream=None) -> dict:
+    """moe_cross_entropy_forward: the softmax cross entropy of each row of
+    h W^T (h [T,D], W [V,D]) with targets (int32 [T]), the logits never in
+    memory.  Returns loss and lse (fp32 [T]); both 0 where the target is
+    outside [0, V).  ``out`` may supply them."""
+    T, D, V, dt, dev = _check_head(h, W, dict(targets=(targets, torch.int32)))
+    o = _outputs(out, ("loss", "lse"))
+    _on_current_device(W, dev)
+    _per_row(o, ("loss", "lse"), W, T, 0, dev, stream)
+    n = cross_entropy_workspace_size(T, D, V, dt, False)
+    workspace = _workspace_for(W, dev, n, workspace, stream)
+    st = lib().moe_cross_entropy_forward(h.data_ptr(), W.data_ptr(), targets.data_ptr(), o["loss"].data_ptr(),
+                                         o["lse"].data_ptr(), T, D, V, _dtype_enum(dt), _ptr(workspace), n,
+                                         _raw_stream(stream, dev))
+    if st:
+        raise MoeError(st, "moe_cross_entropy_forward")
+    return o
+
+
+def cross_entropy_backward(h, W, targets, lse, dloss, wanted=("dh", "dW"), grad_dtype=None, out=None, workspace=None,
+                           stream=None) -> dict:
+    """moe_cross_entropy_backward: dh [T,D] (h's dtype) and dW [V,D]
+    (``grad_dtype``: h's dtype by default, or torch.float32) from the
+    forward's lse and the losses' gradient dloss (fp32 [T]; 1/n of each for a
+    mean over n).  ``wanted`` names the gradients to make (the other is
+    None); ``out`` may supply them."""
+    f32 = torch.float32
+    T, D, V, dt, dev = _check_head(h, W, dict(targets=(targets, torch.int32), lse=(lse, f32), dloss=(dloss, f32)))
+    wanted = _wanted(wanted)
+    o = _outputs(out, wanted)
+    gdt = _grad_dtype(grad_dtype, o.get("dW"), dt, "dW")
+    _on_current_device(W, dev)
+    _head_gradients(o, wanted, W, T, D, V, dt, gdt, dev, stream)
+    n = cross_entropy_workspace_size(T, D, V, dt, True)
+    workspace = _workspace_for(W, dev, n, workspace, stream)
+    st = lib().moe_cross_entropy_backward(h.data_ptr(), W.data_ptr(), targets.data_ptr(), lse.data_ptr(),
+                                          dloss.data_ptr(), _ptr(o["dh"]), _ptr(o["dW"]), T, D, V, _dtype_enum(dt),
+                                          _dtype_enum(gdt), _ptr(workspace), n, _raw_stream(stream, dev))
+    if st:
+        raise MoeError(st, "moe_cross_entropy_backward")
+    return o
+
+
+@functools.lru_cache(maxsize=1024)
+def distillation_workspace_size(T, D, V, K, dtype, backward) -> int:
+    """Bytes of the ``workspace`` of distillation (or of its backward) for h
+    [T,D], W [V,D] of a torch dtype and K entries a row."""
+    return lib().moe_distillation_workspace_size(T, D, V, K, _dtype_enum(dtype), int(backward))
+
+
+def distillation(h, W, ids, logits, temperature=1.0, out=None, workspace=None, stream=None) -> dict:
+    """moe_distillation_forward: the divergence of softmax(h W^T / temperature)
+    from softmax(logits / temperature) of a teacher's K entries a row (ids int32
+    [T,K], logits fp32 [T,K]; ids outside [0, V) do not count).  Returns loss
+    and lse (fp32 [T]; 0 for rows without an entry) and z (fp32 [T,K]: h W^T at
+    ids), which the backward takes.  ``out`` may supply them."""
+    T, D, V, dt, dev = _check_head(h, W, {})
+    K = _check_teacher(W, ids, logits, T, dev)
+    o = _outputs(out, ("loss", "lse", "z"))
+    _on_current_device(W, dev)
+    _per_row(o, ("loss", "lse", "z"), W, T, K, dev, stream)
+    n = distillation_workspace_size(T, D, V, K, dt, False)
+    workspace = _workspace_for(W, dev, n, workspace, stream)
+    st = lib().moe_distillation_forward(h.data_ptr(), W.data_ptr(), ids.data_ptr(), logits.data_ptr(),
+                                        o["loss"].data_ptr(), o["lse"].data_ptr(), o["z"].data_ptr(), T, D, V, K,
+                                        temperature, _dtype_enum(dt), _ptr(workspace), n, _raw_stream(stream, dev))
+    if st:
+        raise MoeError(st, "moe_distillation_forward")
+    return o
+
+
+def distillation_backward(h, W, ids, logits, z, lse, dloss, temperature=1.0, wanted=("dh", "dW"), grad_dtype=None,
+                          out=None, workspace=None, stream=None) -> dict:
+    """moe_distillation_backward: dh and dW as cross_entropy_backward's, from
+    distillation's inputs, its z and lse, and the losses' gradient dloss."""
+    f32 = torch.float32
+    T, D, V, dt, dev = _check_head(h, W, dict(lse=(lse, f32), dloss=(dloss, f32)))
+    K = _check_teacher(W, ids, logits, T, dev, z=z)
+    wanted = _wanted(wanted)
+    o = _outputs(out, wanted)
+    gdt = _grad_dtype(grad_dtype, o.get("dW"), dt, "dW")
+    _on_current_device(W, dev)
+    _head_gradients(o, wanted, W, T, D, V, dt, gdt, dev, stream)
+    n = distillation_workspace_size(T, D, V, K, dt, True)
+    workspace = _workspace_for(W, dev, n, workspace, stream)
+    st = lib().moe_distillation_backward(h.data_ptr(), W.data_ptr(), ids.data_ptr(), logits.data_ptr(), z.data_ptr(),
+                                         lse.data_ptr(), dloss.data_ptr(), _ptr(o["dh"]), _ptr(o["dW"]), T, D, V, K,
+                                         temperature, _dtype_enum(dt), _dtype_enum(gdt), _ptr(workspace), n,
+                                         _raw_stream(stream, dev))
+    if st:
+        raise MoeError(st, "moe_distillation_backward")
+    return o

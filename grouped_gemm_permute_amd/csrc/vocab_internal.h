@@ -1,0 +1,89 @@
+// vocab_internal.h -- what the products of the vocabulary's losses
+// (vocab_gemm.hip) take from their entry points (vocab_loss.hip).  Internal
+// to libmoe_ffn.so.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// One operand of a product: bf16 rows, `planes` arrays of them `plane`
+// elements apart (an fp32 array is the sum of three such planes).
+struct VocabOperand {
+    const uint16_t* p;
+    int64_t pitch;            // elements between rows
+    int64_t plane;            // elements between planes
+};
+
+// Rows of tokens that count: `rows` lists them in order and `count` says how
+// many they are (both on the device); null: all T of them.
+struct VocabRows {
+    const int32_t* rows;
+    const int32_t* count;
+    int64_t T;
+};
+
+constexpr int kVocabTileRows = 128;   // rows of tokens of a logits tile
+constexpr int kVocabTileCols = 256;   // entries of the vocabulary of a logits tile
+
+// z = h W^T by tiles; per tile and row the largest z c and the sum of
+// 2^(z c - largest), to part[tile][row] (row pitch `part_pitch`); z of a
+// row's target to zt.  c = log2(e) / temperature.
+struct VocabStats {
+    VocabOperand h, W;
+    VocabRows rows;
+    bool gather;              // h's rows are found through rows.rows (else h is compact)
+    int64_t V;
+    int K;                    // a multiple of 32
+    int products;             // 1, or 6 products of three planes
+    float c;
+    float2* part;
+    int64_t part_pitch;
+    const int32_t* target;    // [T] or null
+    float* zt;                // [T]
+};
+hipError_t launch_vocab_stats(const VocabStats& a, hipStream_t s);
+
+// dz = g (exp(z inv_tau - lse) - [v = target]) for entries v0 .. v0 + len - 1,
+// to dz (bf16 [compact rows, pitch], or three planes of it), zeros up to the
+// next multiple of 256.  g and lse are of compact rows, g already divided by
+// the temperature; target (or null) is of token rows.
+struct VocabDz {
+    VocabOperand h, W;
+    VocabRows rows;
+    int64_t V, v0;
+    int len;
+    int K;
+    int products;
+    float inv_tau;
+    const float *g, *lse;
+    const int32_t* target;
+    uint16_t* dz;
+    int64_t dz_pitch, dz_plane;
+};
+hipError_t launch_vocab_dz(const VocabDz& a, hipStream_t s);
+
+// C[m][n] = sum over k of M and N operands, K split into `splits` parts.
+//   dh (dW = false): m = compact row, k = entry of the piece, n = column of D
+//   dW (dW = true):  m = entry of the piece, k = compact row, n = column of D
+// With partial, split s goes to partial + s split_stride (row pitch
+// part_pitch, added to what is there if `add`); else to out (rows mapped
+// through rows.rows for dh), fp32 or bf16, row pitch N.
+struct VocabGrad {
+    bool dW;
+    VocabOperand m, n;
+    VocabRows rows;
+    int len;                  // entries of the piece
+    int N;                    // columns of D
+    int splits;
+    int products;
+    float* partial;
+    int64_t split_stride, part_pitch;
+    bool add;
+    void* out;
+    bool out_bf16;
+};
+hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,790 @@
+// vocab_loss.hip -- cross entropy and distillation over a large vocabulary
+// from the rows h [T, D] in front of it and its table W [V, D], with their
+// gradients, without the logits z = h W^T in memory.
+//
+//   cross entropy   lse[t] = log sum_v exp z[t, v],  loss[t] = lse[t] - z[t, target[t]]
+//                   dz[t, v] = g[t] (exp(z[t, v] - lse[t]) - [v = target[t]])
+//   distillation    q[t] = softmax over the row's K entries of the teacher's logits / tau
+//                   lse[t] = log sum_v exp(z[t, v] / tau)
+//                   loss[t] = sum_k q[t, k] (log q[t, k] - z[t, ids[t, k]] / tau) + lse[t]
+//                   dz[t, v] = g[t] / tau (exp(z[t, v] / tau - lse[t]) - sum of q[t, k] over ids[t, k] = v)
+//   both            dh = dz W,  dW = dz^T h
+//
+// The forward is one pass of the tile kernel that keeps a largest value and a
+// sum for each row and 256 entries, and a small kernel that joins those.  The
+// backward makes the logits again, a piece of the vocabulary at a time, turns
+// them into dz (at most kDzBytes of it) and multiplies that with W and with h.
+// dz is rounded to the operands' precision: bf16 for bf16 operands (half a step,
+// 2^-9 of each entry, about what the rounding of dh itself is), three planes of
+// bf16 for fp32 ones.
+//
+// Rows that have no target (prompts, padding) take no part: from kListRows rows
+// on the rest are listed first and the products run on those alone; fewer are
+// not worth the launch, their dz is zero instead.
+#include "mfma_common.h"
+#include "vocab_internal.h"
+
+#include "../../include/moe_ffn.h"
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+namespace moe {
+namespace {
+
+using namespace mfma;
+
+constexpr size_t kAlign = 256;
+constexpr int kMaxD = 16384, kMaxTop = 256;
+constexpr int64_t kMaxV = 1 << 24, kMaxT = 1 << 28;
+constexpr int64_t kListRows = 1024;
+// dz of one piece of the vocabulary: the largest that ordinary steps take whole
+// or in a few pieces (32768 rows: 16384 entries), small beside 288 GB.
+constexpr int64_t kDzBytes = 1ll << 30;
+constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+size_t padded(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
+
+__device__ __forceinline__ float to_float(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ uint16_t to_bf16(float v) { return (uint16_t)pack_bf16(v, 0.f); }
+
+// Whether row t has a target (ids null), or an entry with some probability.
+__device__ __forceinline__ bool counts(int32_t id, float logit, int V) {
+    return id >= 0 && id < V && !(logit == -INFINITY);
+}
+
+struct Targets {
+    const int32_t* target;    // [T]; or
+    const int32_t* ids;       // [T, K]
+    const float* logits;      // [T, K]
+    int K, V;
+};
+
+__device__ __forceinline__ bool live_row(const Targets& a, int64_t t) {
+    if (a.target) return a.target[t] >= 0 && a.target[t] < a.V;
+    for (int k = 0; k < a.K; ++k)
+        if (counts(a.ids[t * a.K + k], a.logits[t * a.K + k], a.V)) return true;
+    return false;
+}
+
+// live[t] of a distillation's rows: a wavefront a row.
+__global__ __launch_bounds__(256) void vocab_live_kernel(const Targets a, int64_t T, int32_t* __restrict__ live) {
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (t >= T) return;
+    bool any = false;
+    for (int k = lane; k < a.K; k += 64) any |= counts(a.ids[t * a.K + k], a.logits[t * a.K + k], a.V);
+    const uint64_t m = __ballot(any);
+    if (lane == 0) live[t] = m != 0;
+}
+
+// The rows that count, in order: rows[0 .. *count), and pos[t], a row's place
+// among them or -1.  One workgroup; a thread takes 8 consecutive rows a turn.
+// zero0, zero1 (or null): set to 0 for the other rows.
+__global__ __launch_bounds__(1024) void vocab_list_kernel(const int32_t* __restrict__ target, const int32_t* __restrict__ live,
+                                                          int V, int64_t T, int32_t* __restrict__ rows,
+                                                          int32_t* __restrict__ pos, int32_t* __restrict__ count,
+                                                          float* zero0, float* zero1) {
+    __shared__ int32_t sums[16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int32_t n = 0;
+    for (int64_t base = 0; base < T; base += 8192) {
+        const int64_t t0 = base + 8 * tid;
+        int in = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t t = min(t0 + j, T - 1);
+            const bool l = target ? target[t] >= 0 && target[t] < V : live[t] != 0;
+            if (t0 + j < T && l) in |= 1 << j;
+        }
+        const int mine = __popc(in);
+        int incl = mine;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (lane == 63) sums[wave] = incl;
+        __syncthreads();
+        int place = n + incl - mine;
+        for (int w = 0; w < 16; ++w) {
+            if (w < wave) place += sums[w];
+            n += sums[w];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t t = t0 + j;
+            if (t >= T) break;
+            if (in >> j & 1) {
+                rows[place] = (int32_t)t;
+                pos[t] = place++;
+            } else {
+                pos[t] = -1;
+                if (zero0) zero0[t] = 0.f;
+                if (zero1) zero1[t] = 0.f;
+            }
+        }
+    }
+    if (tid == 0) *count = n;
+}
+
+// The backward's rows: row t of h to row pos[t] of the copy, as bf16 (one plane)
+// or as three bf16 planes whose sum it is, zeros behind its D columns; g / tau
+// and lse beside it.  Without pos every row is copied to its own place, those
+// that do not count as zeros with a dz of zero.  With pos those rows' dh is
+// written here, as zeros.
+struct CopyArgs {
+    const void* src;
+    int64_t T;
+    int D, Dp;
+    uint16_t* dst;
+    int64_t plane;
+    const int32_t* pos;
+    Targets targets;          // rows that count (pos null); target and ids null: all
+    const float *g, *lse;     // [T], or null
+    float inv_tau;
+    float *g_out, *lse_out;
+    void* dh;                 // or null
+};
+
+template <typename E>
+__global__ __launch_bounds__(256) void vocab_copy_kernel(const CopyArgs a) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.T; t += (int64_t)gridDim.x * 4) {
+        int64_t to = t;
+        bool live = true;
+        if (a.pos) {
+            to = a.pos[t];
+            live = to >= 0;
+            if (!live) {
+                if (a.dh)
+                    for (int c = lane; c < a.D; c += 64) ((E*)a.dh)[t * a.D + c] = E(0);
+                continue;
+            }
+        } else if (a.targets.target || a.targets.ids) {
+            if (a.targets.target) {
+                live = live_row(a.targets, t);
+            } else {
+                bool any = false;
+                for (int k = lane; k < a.targets.K; k += 64)
+                    any |= counts(a.targets.ids[t * a.targets.K + k], a.targets.logits[t * a.targets.K + k], a.targets.V);
+                live = __ballot(any) != 0;
+            }
+        }
+        if (a.g && lane == 0) {
+            a.g_out[to] = live ? a.g[t] * a.inv_tau : 0.f;
+            a.lse_out[to] = live ? a.lse[t] : INFINITY;
+        }
+        const E* src = (const E*)a.src + t * a.D;
+        uint16_t* dst = a.dst + to * a.Dp;
+        if (a.D % 8 == 0) {
+            for (int c = 8 * lane; c < a.Dp; c += 512) {
+                float x[8];
+                if (c < a.D && live) {
+                    if constexpr (sizeof(E) == 2) {
+                        *(u32x4_t*)(dst + c) = *(const u32x4_t*)(src + c);
+                        continue;
+                    } else {
+                        *(float4*)x = *(const float4*)(src + c);
+                        *(float4*)(x + 4) = *(const float4*)(src + c + 4);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                }
+#pragma unroll
+                for (int pl = 0; pl < (sizeof(E) == 2 ? 1 : 3); ++pl) {
+                    u32x4_t o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        o[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+                        x[2 * i] -= __uint_as_float(o[i] << 16);
+                        x[2 * i + 1] -= __uint_as_float(o[i] & 0xffff0000u);
+                    }
+                    *(u32x4_t*)(dst + pl * a.plane + c) = o;
+                }
+            }
+        } else {
+            for (int c = lane; c < a.Dp; c += 64) {
+                float x = c < a.D && live ? to_float(src[c]) : 0.f;
+#pragma unroll
+                for (int pl = 0; pl < (sizeof(E) == 2 ? 1 : 3); ++pl) {
+                    const uint16_t o = to_bf16(x);
+                    dst[pl * a.plane + c] = o;
+                    x -= to_float(o);
+                }
+            }
+        }
+    }
+}
+
+// Joins the tiles' largest values and sums of 16 rows: 16 threads a row, each
+// over every 16th tile, then over the 16.
+struct FinishArgs {
+    const float2* part;
+    int64_t pitch;
+    int n_tiles;
+    VocabRows rows;
+    Targets targets;
+    float c;
+    const float* zt;          // cross entropy: the targets' logits, or null
+    float *loss, *lse;        // [T]; loss null: lse alone
+};
+
+__global__ __launch_bounds__(256) void vocab_finish_kernel(const FinishArgs a) {
+    __shared__ float2 sums[16][17];
+    const int r = threadIdx.x & 15, sl = threadIdx.x >> 4;
+    const int64_t n = a.rows.count ? *a.rows.count : a.rows.T;
+    const int64_t i = (int64_t)blockIdx.x * 16 + r;
+    if ((int64_t)blockIdx.x * 16 >= n) return;
+    float top = -INFINITY, sum = 0.f;
+    if (i < n) {
+        for (int k = sl; k < a.n_tiles; k += 16) {
+            const float2 p = a.part[k * a.pitch + i];
+            const float m = fmaxf(top, p.x), off = m == -INFINITY ? 0.f : m;
+            sum = sum * __builtin_amdgcn_exp2f(top - off) + p.y * __builtin_amdgcn_exp2f(p.x - off);
+            top = m;
+        }
+    }
+    sums[sl][r] = make_float2(top, sum);
+    __syncthreads();
+    if (sl || i >= n) return;
+    float m = -INFINITY;
+    for (int k = 0; k < 16; ++k) m = fmaxf(m, sums[k][r].x);
+    const float off = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+    for (int k = 0; k < 16; ++k) s += sums[k][r].y * __builtin_amdgcn_exp2f(sums[k][r].x - off);
+    const int64_t t = a.rows.rows ? a.rows.rows[i] : i;
+    const bool live = a.rows.rows || live_row(a.targets, t);
+    const float l = __builtin_amdgcn_logf(s);       // log2
+    a.lse[t] = live ? (off + l) * kLn2 : 0.f;
+    // the two large terms first: their difference is exact where the target leads
+    if (a.loss) a.loss[t] = live ? (l + (off - a.zt[t] * a.c)) * kLn2 : 0.f;
+}
+
+// A teacher's row in LDS: q and log q of its K entries (0 for those that do not
+// count); true if any counts.  Called by the whole first wavefront.
+__device__ __forceinline__ bool teacher_row(const Targets& a, int64_t t, float inv_tau, float* q, float* logq, int32_t* id) {
+    const int lane = threadIdx.x & 63;
+    float top = -INFINITY;
+    bool any = false, nan = false;
+    for (int k = lane; k < a.K; k += 64) {
+        const int32_t v = a.ids[t * a.K + k];
+        const float x = a.logits[t * a.K + k];
+        const bool in = counts(v, x, a.V);
+        id[k] = in ? v : -1;
+        logq[k] = x;
+        if (in) {
+            any = true;
+            nan |= x != x;
+            top = fmaxf(top, x);
+        }
+    }
+    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    if (__ballot(nan)) top = NAN;
+    float sum = 0.f;
+    for (int k = lane; k < a.K; k += 64) {
+        // differences first: logits of the lowest value stay finite at any tau
+        const float x = (logq[k] - top) * inv_tau, e = id[k] >= 0 ? expf(x) : 0.f;
+        logq[k] = x;
+        q[k] = e;
+        sum += e;
+    }
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    const float l = logf(sum);
+    for (int k = lane; k < a.K; k += 64) {
+        const bool in = id[k] >= 0;
+        q[k] = in ? q[k] / sum : 0.f;
+        logq[k] = in ? logq[k] - l : 0.f;
+    }
+    return __ballot(any) != 0;
+}
+
+// z[t, k] = h[t] . W[ids[t, k]] and the row's loss: a workgroup a row, 16 lanes
+// an entry.  Gathers T K rows of the table, most of them from the last-level
+// cache.
+struct TopArgs {
+    const void *h, *W;
+    Targets targets;
+    int D;
+    float inv_tau;
+    const float* lse;
+    float *loss, *z;
+};
+
+template <typename E, bool VEC>
+__global__ __launch_bounds__(256) void vocab_top_kernel(const TopArgs a) {
+    __shared__ float q[kMaxTop], logq[kMaxTop], zs[kMaxTop];
+    __shared__ int32_t id[kMaxTop];
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x, K = a.targets.K;
+    const E* h = (const E*)a.h + t * a.D;
+    bool live = false;
+    if (tid < 64) live = teacher_row(a.targets, t, a.inv_tau, q, logq, id);
+    __syncthreads();
+    const int sub = tid & 15;
+    for (int k = tid >> 4; k < K; k += 16) {
+        const int32_t v = a.targets.ids[t * K + k];
+        float s = 0.f;
+        if (v >= 0 && v < a.targets.V) {
+            const E* w = (const E*)a.W + (int64_t)v * a.D;
+            if constexpr (VEC) {
+                constexpr int n = 16 / sizeof(E);
+#pragma unroll 4
+                for (int c = n * sub; c < a.D; c += 16 * n) {
+                    const u32x4_t x = *(const u32x4_t*)(w + c), y = *(const u32x4_t*)(h + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (sizeof(E) == 2) {
+                            s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+                            s = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), s);
+                        } else {
+                            s = fmaf(__uint_as_float(x[i]), __uint_as_float(y[i]), s);
+                        }
+                    }
+                }
+            } else {
+                for (int c = sub; c < a.D; c += 16) s = fmaf(to_float(w[c]), to_float(h[c]), s);
+            }
+        }
+        for (int d = 8; d; d >>= 1) s += __shfl_xor(s, d, 16);
+        if (sub == 0) {
+            zs[k] = s;
+            a.z[t * K + k] = s;
+        }
+    }
+    __syncthreads();
+    if (tid >= 64) return;
+    float sum = 0.f;
+    for (int k = tid; k < K; k += 64)
+        if (!(q[k] == 0.f)) sum += q[k] * (logq[k] - zs[k] * a.inv_tau);
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    if (tid == 0) a.loss[t] = live ? sum + a.lse[t] : 0.f;
+}
+
+// The teacher's share of dz: entries of the piece that a row's ids name are
+// written anew, g / tau (exp(z / tau - lse) - q) from the z of the forward, q
+// summed over ids that name the same one.  A wavefront a row.
+struct TeacherArgs {
+    Targets targets;
+    VocabRows rows;
+    const float *z;           // [T, K]
+    const float *g, *lse;     // of compact rows; g already divided by tau
+    float inv_tau;
+    int64_t v0;
+    int len;
+    uint16_t* dz;
+    int64_t pitch, plane;
+    int planes;
+};
+
+__global__ __launch_bounds__(64) void vocab_teacher_kernel(const TeacherArgs a) {
+    __shared__ float q[kMaxTop], logq[kMaxTop];
+    __shared__ int32_t id[kMaxTop];
+    const int64_t i = blockIdx.x;
+    if (a.rows.count && i >= *a.rows.count) return;
+    const int64_t t = a.rows.rows ? a.rows.rows[i] : i;
+    const int K = a.targets.K;
+    if (!teacher_row(a.targets, t, a.inv_tau, q, logq, id)) return;
+    __syncthreads();
+    const float g = a.g[i], lse = a.lse[i];
+    for (int k = threadIdx.x; k < K; k += 64) {
+        const int32_t v = id[k];
+        if (v < a.v0 || v >= a.v0 + a.len) continue;
+        float share = 0.f;
+        bool first = true;
+        for (int o = 0; o < K; ++o) {
+            if (id[o] != v) continue;
+            if (o < k) first = false;
+            share += q[o];
+        }
+        if (!first) continue;
+        float x = g * (__builtin_amdgcn_exp2f(fmaf(a.z[t * K + k], a.inv_tau, -lse) * kLog2E) - share);
+        uint16_t* p = a.dz + i * a.pitch + (v - a.v0);
+        for (int pl = 0; pl < a.planes; ++pl) {
+            const uint16_t o = to_bf16(x);
+            p[pl * a.plane] = o;
+            x -= to_float(o);
+        }
+    }
+}
+
+// out[map[i]][c] = sum over the buffers of part[s][i][c], in order.
+template <typename O>
+__global__ __launch_bounds__(256) void vocab_reduce_kernel(const float* __restrict__ part, int splits, int64_t stride,
+                                                           int64_t pitch, VocabRows rows, int N, O* __restrict__ out) {
+    const int64_t n = rows.count ? *rows.count : rows.T;
+    const int lane = threadIdx.x & 63;
+    for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < n; i += (int64_t)gridDim.x * 4) {
+        const int64_t t = rows.rows ? rows.rows[i] : i;
+        for (int c = 4 * lane; c < N; c += 256) {
+            float4 v = *(const float4*)(part + i * pitch + c);
+            for (int s = 1; s < splits; ++s) {
+                const float4 o = *(const float4*)(part + s * stride + i * pitch + c);
+                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+            }
+            O* p = out + t * N + c;
+            const float x[4] = {v.x, v.y, v.z, v.w};
+            if (c + 4 <= N && N % 4 == 0) {
+                if constexpr (sizeof(O) == 2) *(uint2*)p = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+                else *(float4*)p = v;
+            } else {
+                for (int q = 0; q < 4; ++q)
+                    if (c + q < N) {
+                        if constexpr (sizeof(O) == 2) p[q] = to_bf16(x[q]);
+                        else p[q] = x[q];
+                    }
+            }
+        }
+    }
+}
+
+template <typename O>
+__global__ __launch_bounds__(256) void vocab_zero_kernel(O* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = O(0);
+}
+
+// ---- plan and workspace
+
+struct Plan {
+    bool list;                // rows that count are listed first
+    bool copy_W, copy_h;      // operands as padded bf16 planes
+    int planes, products, Dp;
+    int64_t n_tiles;          // stats: column tiles
+    int64_t piece, pieces;    // entries of a piece (a multiple of 256), and how many
+    int dh_splits, dW_splits;
+    size_t rows, pos, count, live, hc, Wc, part, zt, g, lse, dz, dh_part, dW_part, total;
+};
+
+// Parts to split a product's K steps into: the fewest rounds of the 256 CUs,
+// each part costing about 6 steps more (its start and its end) and its fp32 tile,
+// written and read again, about 4.
+int splits_of(int64_t tiles, int64_t steps) {
+    int best = 1;
+    double least = 1e300;
+    for (int s = 1; s <= 64 && (s == 1 || (steps / s >= 4 && tiles * s <= 4096)); ++s) {
+        const double rounds = (double)((tiles * s + 255) / 256);
+        const double cost = rounds * (double)((steps + s - 1) / s + 6 + (s > 1 ? 4 : 0)) + (s > 1 ? 0.02 * tiles * s : 0);
+        if (cost < least * 0.98) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
+    Plan p = {};
+    p.list = T >= kListRows;
+    p.planes = dtype == MOE_BF16 ? 1 : 3;
+    p.products = dtype == MOE_BF16 ? 1 : 6;
+    p.Dp = (D + 31) / 32 * 32;
+    // bf16 rows of whole K steps are read where they are
+    p.copy_W = dtype != MOE_BF16 || p.Dp != D;
+    p.copy_h = p.copy_W || backward;
+    p.n_tiles = ((int64_t)V + kVocabTileCols - 1) / kVocabTileCols;
+    size_t at = 0;
+    auto take = [&](bool want, size_t bytes) {
+        const size_t o = at;
+        if (want) at += padded(bytes);
+        return o;
+    };
+    p.rows = take(p.list, (size_t)T * 4);
+    p.pos = take(p.list, (size_t)T * 4);
+    p.count = take(p.list, 4);
+    p.live = take(p.list && K > 0, (size_t)T * 4);
+    p.hc = take(p.copy_h, (size_t)p.planes * T * p.Dp * 2);
+    p.Wc = take(p.copy_W, (size_t)p.planes * V * p.Dp * 2);
+    if (!backward) {
+        p.part = take(true, (size_t)p.n_tiles * T * 8);
+        p.zt = take(K == 0, (size_t)T * 4);
+    } else {
+        const int64_t tile = kVocabTileCols;
+        const int64_t most = std::max<int64_t>(1, kDzBytes / (T * p.planes * 2) / tile);   // tiles of a piece
+        p.pieces = (p.n_tiles + most - 1) / most;
+        p.piece = (p.n_tiles + p.pieces - 1) / p.pieces * tile;
+        p.pieces = (p.n_tiles * tile + p.piece - 1) / p.piece;
+        const int64_t m_tiles = (T + 255) / 256, d_tiles = (D + 255) / 256;
+        p.dh_splits = splits_of(m_tiles * d_tiles, p.piece / 32 * p.products);
+        p.dW_splits = splits_of(p.piece / 256 * d_tiles, (T + 31) / 32 * p.products);
+        p.g = take(true, (size_t)T * 4);
+        p.lse = take(true, (size_t)T * 4);
+        p.dz = take(true, (size_t)p.planes * T * p.piece * 2);
+        p.dh_part = take(p.pieces * p.dh_splits > 1, (size_t)p.dh_splits * T * p.Dp * 4);
+        p.dW_part = take(p.dW_splits > 1, (size_t)p.dW_splits * p.piece * p.Dp * 4);
+    }
+    p.total = at;
+    return p;
+}
+
+struct Call {
+    const void *h, *W;
+    Targets targets;
+    int64_t T;
+    int D;
+    float tau;
+    moe_dtype dtype;
+};
+
+moe_status check(const Call& a) {
+    if (a.T < 0 || a.D <= 0 || a.targets.V <= 0 || (a.dtype != MOE_F32 && a.dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+    if (!(a.tau > 0.f) || a.tau > 3.4e38f || 1.f / a.tau > 3.4e38f) return MOE_ERR_INVALID_ARG;
+    if (a.D > kMaxD || a.targets.V > kMaxV || a.T > kMaxT || a.targets.K > kMaxTop) return MOE_ERR_UNSUPPORTED;
+    // workgroups of a grid
+    const int64_t t = (a.T + 127) / 128, v = (a.targets.V + 255) / 256, d = (a.D + 255) / 256;
+    if (t * v > (1 << 22) || t * d > (1 << 22) || v * d > (1 << 22)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+#define TRY(x)                                     \
+    do {                                           \
+        if ((x) != hipSuccess) return MOE_ERR_HIP; \
+    } while (0)
+
+hipError_t copy_rows(const CopyArgs& a, moe_dtype dtype, hipStream_t s) {
+    const unsigned grid = (unsigned)std::min<int64_t>((a.T + 3) / 4, 8192);
+    if (dtype == MOE_BF16) vocab_copy_kernel<uint16_t><<<grid, 256, 0, s>>>(a);
+    else vocab_copy_kernel<float><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+// The list of rows and the table's planes, where the plan has them.
+moe_status begin(const Call& a, const Plan& p, char* ws, VocabRows* rows, VocabOperand* W, float* zero0, float* zero1,
+                 hipStream_t s) {
+    *rows = {nullptr, nullptr, a.T};
+    if (p.list) {
+        int32_t* live = (int32_t*)(ws + p.live);
+        if (!a.targets.target) {
+            vocab_live_kernel<<<(unsigned)((a.T + 3) / 4), 256, 0, s>>>(a.targets, a.T, live);
+            TRY(hipGetLastError());
+        }
+        *rows = {(const int32_t*)(ws + p.rows), (const int32_t*)(ws + p.count), a.T};
+        vocab_list_kernel<<<1, 1024, 0, s>>>(a.targets.target, live, a.targets.V, a.T, (int32_t*)(ws + p.rows),
+                                            (int32_t*)(ws + p.pos), (int32_t*)(ws + p.count), zero0, zero1);
+        TRY(hipGetLastError());
+    }
+    *W = {(const uint16_t*)a.W, a.D, 0};
+    if (p.copy_W) {
+        uint16_t* to = (uint16_t*)(ws + p.Wc);
+        *W = {to, p.Dp, (int64_t)a.targets.V * p.Dp};
+        CopyArgs c = {a.W, a.targets.V, a.D, p.Dp, to, W->plane};
+        TRY(copy_rows(c, a.dtype, s));
+    }
+    return MOE_OK;
+}
+
+moe_status forward(const Call& a, float* loss, float* lse, float* z, void* workspace, size_t ws_bytes, hipStream_t s) {
+    if (a.T == 0) return MOE_OK;
+    const Plan p = plan_of(a.T, a.D, a.targets.V, a.targets.K, a.dtype, false);
+    if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
+    char* ws = (char*)workspace;
+    (void)hipGetLastError();
+    VocabRows rows;
+    VocabOperand W, h = {(const uint16_t*)a.h, a.D, 0};
+    if (const moe_status st = begin(a, p, ws, &rows, &W, lse, a.targets.target ? loss : nullptr, s)) return st;
+    if (p.copy_h) {
+        uint16_t* to = (uint16_t*)(ws + p.hc);
+        h = {to, p.Dp, a.T * p.Dp};
+        CopyArgs c = {a.h, a.T, a.D, p.Dp, to, h.plane};
+        c.pos = p.list ? (const int32_t*)(ws + p.pos) : nullptr;
+        TRY(copy_rows(c, a.dtype, s));
+    }
+    const float inv_tau = 1.f / a.tau;
+    VocabStats st = {h, W, rows, p.list && !p.copy_h, a.targets.V, p.Dp, p.products, kLog2E * inv_tau,
+                     (float2*)(ws + p.part), a.T, a.targets.target, (float*)(ws + p.zt)};
+    TRY(launch_vocab_stats(st, s));
+    FinishArgs f = {st.part, a.T, (int)p.n_tiles, rows, a.targets, st.c, st.zt, a.targets.target ? loss : nullptr, lse};
+    vocab_finish_kernel<<<(unsigned)((a.T + 15) / 16), 256, 0, s>>>(f);
+    TRY(hipGetLastError());
+    if (!a.targets.target) {
+        TopArgs t = {a.h, a.W, a.targets, a.D, inv_tau, lse, loss, z};
+        const unsigned grid = (unsigned)a.T;
+        if (a.dtype == MOE_BF16) {
+            if (a.D % 8 == 0) vocab_top_kernel<uint16_t, true><<<grid, 256, 0, s>>>(t);
+            else vocab_top_kernel<uint16_t, false><<<grid, 256, 0, s>>>(t);
+        } else {
+            if (a.D % 4 == 0) vocab_top_kernel<float, true><<<grid, 256, 0, s>>>(t);
+            else vocab_top_kernel<float, false><<<grid, 256, 0, s>>>(t);
+        }
+        TRY(hipGetLastError());
+    }
+    return MOE_OK;
+}
+
+moe_status backward(const Call& a, const float* z, const float* lse, const float* dloss, void* dh, void* dW,
+                    moe_dtype dW_dtype, void* workspace, size_t ws_bytes, hipStream_t s) {
+    const int V = a.targets.V;
+    if (a.T == 0) {
+        if (!dW) return MOE_OK;
+        const int64_t n = (int64_t)V * a.D;
+        const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, 65536);
+        (void)hipGetLastError();
+        if (dW_dtype == MOE_BF16) vocab_zero_kernel<<<grid, 256, 0, s>>>((uint16_t*)dW, n);
+        else vocab_zero_kernel<<<grid, 256, 0, s>>>((float*)dW, n);
+        TRY(hipGetLastError());
+        return MOE_OK;
+    }
+    const Plan p = plan_of(a.T, a.D, V, a.targets.K, a.dtype, true);
+    if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
+    char* ws = (char*)workspace;
+    (void)hipGetLastError();
+    VocabRows rows;
+    VocabOperand W;
+    if (const moe_status st = begin(a, p, ws, &rows, &W, nullptr, nullptr, s)) return st;
+    const float inv_tau = 1.f / a.tau;
+    float *g = (float*)(ws + p.g), *l = (float*)(ws + p.lse);
+    VocabOperand h = {(const uint16_t*)(ws + p.hc), p.Dp, a.T * p.Dp};
+    {
+        CopyArgs c = {a.h, a.T, a.D, p.Dp, (uint16_t*)(ws + p.hc), h.plane};
+        c.pos = p.list ? (const int32_t*)(ws + p.pos) : nullptr;
+        c.targets = a.targets;
+        c.g = dloss, c.lse = lse, c.inv_tau = inv_tau, c.g_out = g, c.lse_out = l;
+        c.dh = dh;
+        TRY(copy_rows(c, a.dtype, s));
+    }
+    uint16_t* dz = (uint16_t*)(ws + p.dz);
+    const int64_t dz_plane = a.T * p.piece;
+    const bool h16 = a.dtype == MOE_BF16;
+    for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
+        const int len = (int)std::min<int64_t>(p.piece, V - v0);
+        VocabDz d = {h, W, rows, V, v0, len, p.Dp, p.products, inv_tau, g, l, a.targets.target, dz, p.piece, dz_plane};
+        TRY(launch_vocab_dz(d, s));
+        if (!a.targets.target) {
+            TeacherArgs t = {a.targets, rows, z, g, l, inv_tau, v0, len, dz, p.piece, dz_plane, p.planes};
+            vocab_teacher_kernel<<<(unsigned)a.T, 64, 0, s>>>(t);
+            TRY(hipGetLastError());
+        }
+        VocabGrad q = {};
+        q.rows = rows;
+        q.len = len;
+        q.N = a.D;
+        q.products = p.products;
+        q.part_pitch = p.Dp;
+        if (dh) {
+            q.dW = false;
+            q.m = {dz, p.piece, dz_plane};
+            q.n = {W.p + v0 * W.pitch, W.pitch, W.plane};
+            q.splits = p.dh_splits;
+            q.partial = p.pieces * p.dh_splits > 1 ? (float*)(ws + p.dh_part) : nullptr;
+            q.split_stride = a.T * p.Dp;
+            q.add = v0 > 0;
+            q.out = dh;
+            q.out_bf16 = h16;
+            TRY(launch_vocab_grad(q, s));
+        }
+        if (dW) {
+            q.dW = true;
+            q.m = {dz, p.piece, dz_plane};
+            q.n = h;
+            q.splits = p.dW_splits;
+            q.partial = p.dW_splits > 1 ? (float*)(ws + p.dW_part) : nullptr;
+            q.split_stride = p.piece * p.Dp;
+            q.add = false;
+            q.out_bf16 = dW_dtype == MOE_BF16;
+            q.out = q.out_bf16 ? (void*)((uint16_t*)dW + v0 * a.D) : (void*)((float*)dW + v0 * a.D);
+            TRY(launch_vocab_grad(q, s));
+            if (q.partial) {
+                const VocabRows all = {nullptr, nullptr, len};
+                const unsigned grid = (unsigned)std::min<int64_t>((len + 3) / 4, 8192);
+                if (q.out_bf16)
+                    vocab_reduce_kernel<<<grid, 256, 0, s>>>(q.partial, q.splits, q.split_stride, q.part_pitch, all, a.D,
+                                                             (uint16_t*)q.out);
+                else
+                    vocab_reduce_kernel<<<grid, 256, 0, s>>>(q.partial, q.splits, q.split_stride, q.part_pitch, all, a.D,
+                                                             (float*)q.out);
+                TRY(hipGetLastError());
+            }
+        }
+    }
+    if (dh && p.pieces * p.dh_splits > 1) {
+        const unsigned grid = (unsigned)std::min<int64_t>((a.T + 3) / 4, 8192);
+        const float* part = (const float*)(ws + p.dh_part);
+        if (h16) vocab_reduce_kernel<<<grid, 256, 0, s>>>(part, p.dh_splits, a.T * p.Dp, p.Dp, rows, a.D, (uint16_t*)dh);
+        else vocab_reduce_kernel<<<grid, 256, 0, s>>>(part, p.dh_splits, a.T * p.Dp, p.Dp, rows, a.D, (float*)dh);
+        TRY(hipGetLastError());
+    }
+    return MOE_OK;
+}
+
+Call call_of(const void* h, const void* W, const int32_t* target, const int32_t* ids, const float* logits, int64_t T, int D,
+             int V, int K, float tau, moe_dtype dtype) {
+    return {h, W, {target, ids, logits, K, V}, T, D, tau, dtype};
+}
+
+// Pointers: 16 bytes for arrays of dtype, 4 for the others; null only where
+// there is nothing to read or write.
+bool bad(const void* p, size_t a, bool needed) { return (needed && !p) || !aligned(p, a); }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_cross_entropy_workspace_size(int64_t T, int D, int V, moe_dtype dtype, int backward) {
+    const Call a = call_of(nullptr, nullptr, nullptr, nullptr, nullptr, T, D, V, 0, 1.f, dtype);
+    return check(a) != MOE_OK || T == 0 ? 0 : plan_of(T, D, V, 0, dtype, backward != 0).total;
+}
+
+moe_status moe_cross_entropy_forward(const void* h, const void* W, const int32_t* targets, float* loss, float* lse,
+                                     int64_t T, int D, int V, moe_dtype dtype, void* workspace, size_t ws_bytes,
+                                     hipStream_t stream) {
+    const Call a = call_of(h, W, targets, nullptr, nullptr, T, D, V, 0, 1.f, dtype);
+    if (const moe_status st = check(a)) return st;
+    const bool any = T > 0;
+    if (bad(h, 16, any) || bad(W, 16, any) || bad(targets, 4, any) || bad(loss, 4, any) || bad(lse, 4, any))
+        return MOE_ERR_INVALID_ARG;
+    return forward(a, loss, lse, nullptr, workspace, ws_bytes, stream);
+}
+
+moe_status moe_cross_entropy_backward(const void* h, const void* W, const int32_t* targets, const float* lse,
+                                      const float* dloss, void* dh, void* dW, int64_t T, int D, int V, moe_dtype dtype,
+                                      moe_dtype dW_dtype, void* workspace, size_t ws_bytes, hipStream_t stream) {
+    const Call a = call_of(h, W, targets, nullptr, nullptr, T, D, V, 0, 1.f, dtype);
+    if (const moe_status st = check(a)) return st;
+    const bool any = T > 0;
+    if (bad(h, 16, any) || bad(W, 16, any) || bad(targets, 4, any) || bad(lse, 4, any) || bad(dloss, 4, any) ||
+        bad(dh, 16, any && !dW) || bad(dW, 16, false) || (dW_dtype != MOE_F32 && dW_dtype != dtype))
+        return MOE_ERR_INVALID_ARG;
+    return backward(a, nullptr, lse, dloss, dh, dW, dW_dtype, workspace, ws_bytes, stream);
+}
+
+size_t moe_distillation_workspace_size(int64_t T, int D, int V, int K, moe_dtype dtype, int backward) {
+    const Call a = call_of(nullptr, nullptr, nullptr, nullptr, nullptr, T, D, V, K, 1.f, dtype);
+    return K <= 0 || check(a) != MOE_OK || T == 0 ? 0 : plan_of(T, D, V, K, dtype, backward != 0).total;
+}
+
+moe_status moe_distillation_forward(const void* h, const void* W, const int32_t* ids, const float* logits, float* loss,
+                                    float* lse, float* z, int64_t T, int D, int V, int K, float temperature, moe_dtype dtype,
+                                    void* workspace, size_t ws_bytes, hipStream_t stream) {
+    const Call a = call_of(h, W, nullptr, ids, logits, T, D, V, K, temperature, dtype);
+    if (K <= 0) return MOE_ERR_INVALID_ARG;
+    if (const moe_status st = check(a)) return st;
+    const bool any = T > 0;
+    if (bad(h, 16, any) || bad(W, 16, any) || bad(ids, 4, any) || bad(logits, 4, any) || bad(loss, 4, any) ||
+        bad(lse, 4, any) || bad(z, 4, any))
+        return MOE_ERR_INVALID_ARG;
+    return forward(a, loss, lse, z, workspace, ws_bytes, stream);
+}
+
+moe_status moe_distillation_backward(const void* h, const void* W, const int32_t* ids, const float* logits, const float* z,
+                                     const float* lse, const float* dloss, void* dh, void* dW, int64_t T, int D, int V, int K,
+                                     float temperature, moe_dtype dtype, moe_dtype dW_dtype, void* workspace,
+                                     size_t ws_bytes, hipStream_t stream) {
+    const Call a = call_of(h, W, nullptr, ids, logits, T, D, V, K, temperature, dtype);
+    if (K <= 0) return MOE_ERR_INVALID_ARG;
+    if (const moe_status st = check(a)) return st;
+    const bool any = T > 0;
+    if (bad(h, 16, any) || bad(W, 16, any) || bad(ids, 4, any) || bad(logits, 4, any) || bad(z, 4, any) || bad(lse, 4, any) ||
+        bad(dloss, 4, any) || bad(dh, 16, any && !dW) || bad(dW, 16, false) || (dW_dtype != MOE_F32 && dW_dtype != dtype))
+        return MOE_ERR_INVALID_ARG;
+    return backward(a, z, lse, dloss, dh, dW, dW_dtype, workspace, ws_bytes, stream);
+}
+
+}  // extern "C"

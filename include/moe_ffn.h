@@ -658,6 +658,140 @@ moe_status moe_muon_step(void *W, void *W_bf16, const float *dW, float *momentum
                          int steps, double a, double b, double c, double eps, moe_dtype dtype,
                          void *workspace, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The two ends of a model around its blocks: the rows of a table [V, D]
+ * looked up by token, and the losses of the last rows h [T, D] over the
+ * vocabulary, z = h W^T with W [V, D] (the same table where a model shares it).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * y[t] = scale * table[ids[t]], rounded once; a row of zeros where ids[t] is
+ * outside [0, V).
+ *
+ *   ids    [T]     int32
+ *   table  [V, D]  dtype
+ *   y      [T, D]  dtype; out
+ *
+ * Any D up to 16384, V up to 2^24, T up to 2^29.  table and y are 16-byte
+ * aligned.  Returns MOE_OK; MOE_ERR_INVALID_ARG (null or misaligned pointer,
+ * T < 0, T >= 2^31, D or V < 1, scale not finite, unknown dtype);
+ * MOE_ERR_UNSUPPORTED; MOE_ERR_HIP.  T == 0 launches nothing.
+ */
+moe_status moe_embedding_forward(const int32_t *ids, const void *table, void *y, int64_t T, int D, int V,
+                                 float scale, moe_dtype dtype, hipStream_t stream);
+
+/* Workspace bytes of moe_embedding_backward; 0 if the sizes are invalid or unsupported. */
+size_t moe_embedding_backward_workspace_size(int64_t T, int D, int V);
+
+/*
+ * dtable[v] = scale * sum of dy[t] over the tokens with ids[t] = v, in fp32 in
+ * a fixed order (repeated calls give equal bits), rounded once; tokens
+ * outside [0, V) add nothing, and are not read.
+ *
+ *   dy      [T, D]  dtype
+ *   dtable  [V, D]  table_dtype: MOE_F32, or dtype; fully overwritten, or with
+ *           accumulate != 0 added to (entries without a token stay untouched):
+ *           a table that the losses below share has its gradient from both
+ *   workspace >= moe_embedding_backward_workspace_size() bytes, 256-byte aligned
+ *
+ * Sizes, alignment and errors as in the forward, and MOE_ERR_WORKSPACE.
+ */
+moe_status moe_embedding_backward(const int32_t *ids, const void *dy, void *dtable, int64_t T, int D, int V,
+                                  float scale, int accumulate, moe_dtype dtype, moe_dtype table_dtype,
+                                  void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of moe_cross_entropy_forward (backward == 0) or _backward; 0
+ * if the sizes are invalid or unsupported, or T == 0. */
+size_t moe_cross_entropy_workspace_size(int64_t T, int D, int V, moe_dtype dtype, int backward);
+
+/*
+ * Softmax cross entropy over the vocabulary, without the logits in memory:
+ *
+ *   lse[t] = log(sum over v of exp(z[t, v])),  loss[t] = lse[t] - z[t, targets[t]]
+ *
+ *   h        [T, D]  dtype
+ *   W        [V, D]  dtype
+ *   targets  [T]     int32; rows whose target is outside [0, V) take no part:
+ *            loss and lse are 0 there, whatever h holds
+ *   loss, lse [T]    fp32; out
+ *   workspace >= moe_cross_entropy_workspace_size(.., 0) bytes, 256-byte aligned
+ *
+ * bf16 products have fp32 sums; fp32 operands are multiplied as three bf16
+ * planes each, six products in all, off by about as much as fp32 products
+ * (magnitudes from 2^-100 to 2^127; an infinity gives NaN).  Sums have a
+ * fixed order: repeated calls give equal bits.  A row of h that holds an infinity
+ * or NaN touches its own outputs alone.
+ *
+ * Any D up to 16384, V up to 2^24, T up to 2^28, and fewer than 2^22 tiles of
+ * 128 rows x 256 entries.  h and W are 16-byte aligned, the others 4-byte.
+ * Returns MOE_OK; MOE_ERR_INVALID_ARG (null or misaligned pointer, T < 0, D or
+ * V < 1, unknown dtype); MOE_ERR_UNSUPPORTED; MOE_ERR_WORKSPACE; MOE_ERR_HIP.
+ * T == 0 launches nothing.
+ */
+moe_status moe_cross_entropy_forward(const void *h, const void *W, const int32_t *targets, float *loss,
+                                     float *lse, int64_t T, int D, int V, moe_dtype dtype, void *workspace,
+                                     size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Backward of moe_cross_entropy_forward:
+ *
+ *   dz[t, v] = dloss[t] (exp(z[t, v] - lse[t]) - [v = targets[t]])
+ *   dh = dz W,  dW = dz^T h
+ *
+ *   lse, dloss [T]   fp32; the forward's, and the gradient of each loss
+ *   dh       [T, D]  dtype; out, zeros for rows without a target; NULL: not wanted
+ *   dW       [V, D]  dW_dtype: MOE_F32, or dtype; out, fully overwritten (zeros
+ *            with T == 0); NULL: not wanted (not both)
+ *   workspace >= moe_cross_entropy_workspace_size(.., 1) bytes, 256-byte aligned
+ *
+ * The logits are made again, a piece of the vocabulary at a time; dz of a piece
+ * (at most 1 GiB, or 256 entries) stays in the workspace.  For bf16 operands dz is rounded to bf16 before the two
+ * products, also where dW is fp32.  Sizes and errors as in the forward.
+ */
+moe_status moe_cross_entropy_backward(const void *h, const void *W, const int32_t *targets, const float *lse,
+                                      const float *dloss, void *dh, void *dW, int64_t T, int D, int V,
+                                      moe_dtype dtype, moe_dtype dW_dtype, void *workspace, size_t ws_bytes,
+                                      hipStream_t stream);
+
+/* Workspace bytes of moe_distillation_forward (backward == 0) or _backward; 0
+ * if the sizes are invalid or unsupported, or T == 0. */
+size_t moe_distillation_workspace_size(int64_t T, int D, int V, int K, moe_dtype dtype, int backward);
+
+/*
+ * Distillation from the K largest logits of a teacher: the divergence of the
+ * softmax of h W^T / temperature from the teacher's over those K entries,
+ *
+ *   q[t] = softmax over k of logits[t, k] / temperature
+ *   lse[t] = log(sum over v of exp(z[t, v] / temperature))
+ *   loss[t] = sum over k of q[t, k] (log q[t, k] - z[t, ids[t, k]] / temperature) + lse[t]
+ *
+ *   ids      [T, K]  int32; an entry outside [0, V), or whose logit is -infinity,
+ *            does not count; a row without one that counts takes no part (loss
+ *            and lse 0).  The same id twice is two entries.
+ *   logits   [T, K]  fp32; +infinity or NaN gives NaN in its row
+ *   loss, lse [T]    fp32; out
+ *   z        [T, K]  fp32; out: z[t, ids[t, k]], 0 for ids outside [0, V); the
+ *            backward takes it
+ *
+ * K up to 256; temperature > 0 and finite.  Else as moe_cross_entropy_forward.
+ */
+moe_status moe_distillation_forward(const void *h, const void *W, const int32_t *ids, const float *logits,
+                                    float *loss, float *lse, float *z, int64_t T, int D, int V, int K,
+                                    float temperature, moe_dtype dtype, void *workspace, size_t ws_bytes,
+                                    hipStream_t stream);
+
+/*
+ * Backward of moe_distillation_forward, from its z and lse:
+ *
+ *   dz[t, v] = dloss[t] / temperature (exp(z[t, v] / temperature - lse[t]) - sum of q[t, k] over ids[t, k] = v)
+ *
+ * Else as moe_cross_entropy_backward.
+ */
+moe_status moe_distillation_backward(const void *h, const void *W, const int32_t *ids, const float *logits,
+                                     const float *z, const float *lse, const float *dloss, void *dh, void *dW,
+                                     int64_t T, int D, int V, int K, float temperature, moe_dtype dtype,
+                                     moe_dtype dW_dtype, void *workspace, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
