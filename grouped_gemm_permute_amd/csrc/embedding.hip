@@ -7,16 +7,17 @@
 // order of their tokens, so that repeated calls give equal bits and no atomics
 // meet.  Three launches:
 //
-//  sort:  workgroup b owns `span` entries of the table.  It reads all ids once
+//  sort:  workgroup b owns 32 to 512 entries of the table.  It reads all ids once
 //         to count those below its entries (where its first token goes) and
 //         those of each of its entries, a wavefront counting its own
 //         contiguous part of the tokens; then again to place its tokens, each
-//         wavefront in order behind the wavefronts before it.  No workgroup
+//         wavefront in order behind the wavefronts before it, the lanes of one
+//         entry found by a ballot a bit.  No workgroup
 //         waits for another: 512 workgroups reading 32768 ids are 64 MB from
 //         the L2s, less time than the second launch of a counting sort by
 //         blocks.
-//  sum:   a wavefront per entry adds its rows and writes the entry, zeros
-//         where it has no token.  Entries of more than kLong tokens (text has a
+//  sum:   adds each entry's rows and writes the entry, zeros where it has no
+//         token.  Entries of more than kLong tokens (text has a
 //         few that make up several percent of it) are left to further
 //         wavefronts, each of which adds the rows of kLong consecutive sorted
 //         tokens: at most two such entries have tokens there, and their two sums
@@ -37,9 +38,8 @@ namespace {
 
 using namespace mfma;
 
-constexpr int kSortThreads = 512;
+constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kMaxSpan = 512;          // entries of a sorting workgroup
 constexpr int kLong = 64;              // tokens of an entry that one wavefront adds
 constexpr int kMaxD = 16384;
 
@@ -106,26 +106,32 @@ __global__ __launch_bounds__(256) void embedding_forward_kernel(const FwdArgs a)
 
 // order: the tokens with ids in [0, V), sorted by id and then by token;
 // start[v]: where those of entry v begin, start[V] how many there are.
+// BITS: of an entry's place among the workgroup's.
+template <int BITS>
 __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const int32_t* __restrict__ ids, int64_t T, int V,
-                                                                      int span, int32_t* __restrict__ order,
+                                                                      int32_t* __restrict__ order,
                                                                       int32_t* __restrict__ start) {
-    __shared__ int32_t at[kSortWaves][kMaxSpan];   // counts, then places
+    constexpr int SPAN = 1 << BITS;
+    __shared__ int32_t at[kSortWaves][SPAN];   // counts, then places
     __shared__ int32_t below[kSortWaves], sums[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int lo = blockIdx.x * span, hi = min(lo + span, V);
-    for (int i = tid; i < kSortWaves * kMaxSpan; i += kSortThreads) (&at[0][0])[i] = 0;
+    const int lo = blockIdx.x * SPAN, hi = min(lo + SPAN, V);
+    for (int i = tid; i < kSortWaves * SPAN; i += kSortThreads) (&at[0][0])[i] = 0;
     __syncthreads();
-    // this wavefront's tokens
+    // this wavefront's tokens, 512 at a time: 64 consecutive ones a load
     const int64_t per = (T + kSortThreads - 1) / kSortThreads * 64;
     const int64_t t0 = min(per * wave, T), t1 = min(t0 + per, T);
-    int under = 0;
-    for (int64_t base = t0; base < t1; base += 512) {
-        int32_t id[8];
+    auto load = [&](int64_t base, int32_t (&id)[8]) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int64_t t = base + 64 * j + lane;
             id[j] = t < t1 ? ids[t] : -1;
         }
+    };
+    int under = 0;
+    for (int64_t base = t0; base < t1; base += 512) {
+        int32_t id[8];
+        load(base, id);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             under += id[j] >= 0 && id[j] < lo;
@@ -135,14 +141,11 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const int3
     for (int d = 32; d; d >>= 1) under += __shfl_xor(under, d);
     if (lane == 0) below[wave] = under;
     __syncthreads();
-    // exclusive prefix over (entry, wavefront)
+    // exclusive prefix over (entry, wavefront), an entry a thread
+    const bool entry = tid < SPAN;
     int mine = 0;
-    int32_t c[kSortWaves];
-#pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) {
-        c[w] = at[w][tid];
-        mine += c[w];
-    }
+    if (entry)
+        for (int w = 0; w < kSortWaves; ++w) mine += at[w][tid];
     int incl = mine;
     for (int d = 1; d < 64; d <<= 1) {
         const int o = __shfl_up(incl, d);
@@ -151,41 +154,43 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const int3
     if (lane == 63) sums[wave] = incl;
     __syncthreads();
     int place = incl - mine;
-#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
         place += below[w];
         if (w < wave) place += sums[w];
     }
-    if (lo + tid < hi) {
-        start[lo + tid] = place;
-        if (lo + tid == V - 1) start[V] = place + mine;
-    }
-#pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) {
-        at[w][tid] = place;
-        place += c[w];
+    if (entry) {
+        if (lo + tid < hi) {
+            start[lo + tid] = place;
+            if (lo + tid == V - 1) start[V] = place + mine;
+        }
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = at[w][tid];
+            at[w][tid] = place;
+            place += c;
+        }
     }
     __syncthreads();
     for (int64_t base = t0; base < t1; base += 512) {
         int32_t id[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t t = base + 64 * j + lane;
-            id[j] = t < t1 ? ids[t] : -1;
-        }
+        load(base, id);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const bool in = id[j] >= lo && id[j] < hi;
-            uint64_t todo = __ballot(in);
-            while (todo) {       // one entry at a time; every lane of the wavefront is here
-                const int first = __ffsll((unsigned long long)todo) - 1;
-                const int v = __shfl(id[j], first);
-                const uint64_t same = __ballot(in && id[j] == v);
-                const int p = at[wave][v - lo];
-                if (in && id[j] == v)
-                    order[p + __popcll(same & ((1ull << lane) - 1))] = (int32_t)(base + 64 * j + lane);
-                if (lane == first) at[wave][v - lo] = p + __popcll(same);
-                todo &= ~same;
+            uint64_t same = __ballot(in);
+            if (!same) continue;
+            // the lanes with this lane's entry: those that agree in every bit
+            const int e = in ? id[j] - lo : 0;
+#pragma unroll
+            for (int b = 0; b < BITS; ++b) {
+                const uint64_t set = __ballot(e >> b & 1);
+                same &= e >> b & 1 ? set : ~set;
+            }
+            const int before = __popcll(same & ((1ull << lane) - 1));
+            if (in) {
+                const int p = at[wave][e];
+                order[p + before] = (int32_t)(base + 64 * j + lane);
+                // one of them moves the place on, behind all their reads
+                if (before == 0) at[wave][e] = p + __popcll(same);
             }
         }
     }
@@ -200,71 +205,102 @@ struct SumArgs {
     int D, V;
     float scale;
     int add;
-    int64_t row_blocks;  // workgroups of 4 entries; those behind them take 4 chunks each
+    int rows;            // entries of a workgroup
+    int64_t row_blocks;  // workgroups of entries; those behind them take 4 chunks each
 };
 
-// Four columns, or one (VEC false), of a row.
-template <typename E, bool VEC>
-__device__ __forceinline__ float4 load_cols(const E* p) {
-    if constexpr (!VEC) {
-        return make_float4(to_float(*p), 0.f, 0.f, 0.f);
+// W consecutive columns (8 of bf16, 4 of fp32: 16 bytes; or 1) in fp32.
+template <int W>
+struct Cols {
+    float x[W];
+};
+template <typename E, int W>
+__device__ __forceinline__ Cols<W> load_cols(const E* p) {
+    Cols<W> o;
+    if constexpr (W == 1) {
+        o.x[0] = to_float(*p);
     } else if constexpr (sizeof(E) == 4) {
-        return *(const float4*)p;
-    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) *(float4*)(o.x + i) = *(const float4*)(p + i);
+    } else if constexpr (W == 4) {
         const uint2 v = *(const uint2*)p;
-        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                           __uint_as_float(v.y & 0xffff0000u));
+        o.x[0] = __uint_as_float(v.x << 16), o.x[1] = __uint_as_float(v.x & 0xffff0000u);
+        o.x[2] = __uint_as_float(v.y << 16), o.x[3] = __uint_as_float(v.y & 0xffff0000u);
+    } else {
+        const u32x4_t v = *(const u32x4_t*)p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o.x[2 * i] = __uint_as_float(v[i] << 16);
+            o.x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+        }
+    }
+    return o;
+}
+template <typename O, int W>
+__device__ __forceinline__ void store_cols(O* p, const Cols<W>& v) {
+    if constexpr (W == 1) {
+        put(p, v.x[0]);
+    } else if constexpr (sizeof(O) == 4) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) *(float4*)(p + i) = *(const float4*)(v.x + i);
+    } else if constexpr (W == 4) {
+        *(uint2*)p = make_uint2(pack_bf16(v.x[0], v.x[1]), pack_bf16(v.x[2], v.x[3]));
+    } else {
+        u32x4_t o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack_bf16(v.x[2 * i], v.x[2 * i + 1]);
+        *(u32x4_t*)p = o;
     }
 }
-template <typename O, bool VEC>
-__device__ __forceinline__ void store_cols(O* p, float4 v) {
-    if constexpr (!VEC) put(p, v.x);
-    else if constexpr (sizeof(O) == 4) *(float4*)p = v;
-    else *(uint2*)p = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+template <int W>
+__device__ __forceinline__ void add_to(Cols<W>& a, const Cols<W>& b) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) a.x[i] += b.x[i];
 }
-__device__ __forceinline__ float4 plus(float4 a, float4 b) {
-    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-}
-__device__ __forceinline__ float4 times(float4 a, float s) { return make_float4(a.x * s, a.y * s, a.z * s, a.w * s); }
 
 // The sum of columns c.. of the rows of sorted tokens p0 .. p1 - 1, in order.
-template <typename E, bool VEC>
-__device__ __forceinline__ float4 sum_rows(const SumArgs& a, int p0, int p1, int c) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+template <typename E, int W>
+__device__ __forceinline__ Cols<W> sum_rows(const SumArgs& a, int p0, int p1, int c) {
+    Cols<W> s = {};
     const E* dy = (const E*)a.dy + c;
     int p = p0;
     for (; p + 8 <= p1; p += 8) {
-        float4 v[8];
+        Cols<W> v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = load_cols<E, VEC>(dy + (int64_t)a.order[p + j] * a.D);
+        for (int j = 0; j < 8; ++j) v[j] = load_cols<E, W>(dy + (int64_t)a.order[p + j] * a.D);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = plus(s, v[j]);
+        for (int j = 0; j < 8; ++j) add_to(s, v[j]);
     }
-    for (; p < p1; ++p) s = plus(s, load_cols<E, VEC>(dy + (int64_t)a.order[p] * a.D));
+    for (; p < p1; ++p) add_to(s, load_cols<E, W>(dy + (int64_t)a.order[p] * a.D));
     return s;
 }
 
-template <typename O, bool VEC>
-__device__ __forceinline__ void write_cols(const SumArgs& a, int v, int c, float4 s) {
+template <typename O, int W>
+__device__ __forceinline__ void write_cols(const SumArgs& a, int v, int c, Cols<W> s) {
     O* p = (O*)a.out + (int64_t)v * a.D + c;
-    s = times(s, a.scale);
-    if (a.add) s = plus(s, load_cols<O, VEC>(p));
-    store_cols<O, VEC>(p, s);
+#pragma unroll
+    for (int i = 0; i < W; ++i) s.x[i] *= a.scale;
+    if (a.add) add_to(s, load_cols<O, W>(p));
+    store_cols<O, W>(p, s);
 }
 
-template <typename E, typename O, bool VEC>
+template <typename E, typename O, int W>
 __global__ __launch_bounds__(256) void embedding_sum_kernel(const SumArgs a) {
-    constexpr int W = VEC ? 4 : 1;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (blockIdx.x < a.row_blocks) {
-        const int64_t v = (int64_t)blockIdx.x * 4 + wave;
-        if (v >= a.V) return;
-        const int s = a.start[v], e = a.start[v + 1];
-        if (e - s > kLong || (a.add && e == s)) return;
-        for (int c = lane * W; c < a.D; c += 64 * W) write_cols<O, VEC>(a, (int)v, c, sum_rows<E, VEC>(a, s, e, c));
+        // W columns of an entry a thread
+        const int64_t v0 = (int64_t)blockIdx.x * a.rows;
+        const int rows = (int)min((int64_t)a.rows, a.V - v0), per_row = a.D / W;
+        for (int i = threadIdx.x; i < rows * per_row; i += 256) {
+            const int r = i / per_row, c = (i - r * per_row) * W;
+            const int v = (int)v0 + r;
+            const int s = a.start[v], e = a.start[v + 1];
+            if (e - s > kLong || (a.add && e == s)) continue;
+            write_cols<O, W>(a, v, c, sum_rows<E, W>(a, s, e, c));
+        }
         return;
     }
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t chunk = ((int64_t)blockIdx.x - a.row_blocks) * 4 + wave;
     const int all = a.start[a.V];
     if (chunk * kLong >= all) return;
@@ -275,17 +311,16 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const SumArgs a) {
     float* part = a.part + chunk * 2 * a.D;
     if (ae - a.start[va] > kLong)
         for (int c = lane * W; c < a.D; c += 64 * W)
-            store_cols<float, VEC>(part + c, sum_rows<E, VEC>(a, p0, min(ae, p1), c));
+            store_cols<float, W>(part + c, sum_rows<E, W>(a, p0, min(ae, p1), c));
     if (vb != va && a.start[vb + 1] - bs > kLong)
         for (int c = lane * W; c < a.D; c += 64 * W)
-            store_cols<float, VEC>(part + a.D + c, sum_rows<E, VEC>(a, bs, p1, c));
+            store_cols<float, W>(part + a.D + c, sum_rows<E, W>(a, bs, p1, c));
 }
 
 // Workgroup: the long entry that begins in this chunk, if one does (it then
 // holds the chunk's last token).
-template <typename O, bool VEC>
+template <typename O, int W>
 __global__ __launch_bounds__(256) void embedding_join_kernel(const SumArgs a) {
-    constexpr int W = VEC ? 4 : 1;
     const int64_t chunk = blockIdx.x;
     const int all = a.start[a.V];
     if (chunk * kLong >= all) return;
@@ -295,18 +330,19 @@ __global__ __launch_bounds__(256) void embedding_join_kernel(const SumArgs a) {
     if (e - s <= kLong || s < p0) return;
     // the first sum is the chunk's second where the entry begins behind another
     const int64_t last = (e - 1) / kLong;
+    const float* part = a.part + (a.ids[a.order[p0]] != v ? a.D : 0);
     for (int c = threadIdx.x * W; c < a.D; c += 256 * W) {
-        float4 sum = load_cols<float, VEC>(a.part + (chunk * 2 + (a.ids[a.order[p0]] != v)) * a.D + c);
+        Cols<W> sum = load_cols<float, W>(part + chunk * 2 * a.D + c);
         int64_t k = chunk + 1;
         for (; k + 8 <= last + 1; k += 8) {
-            float4 x[8];
+            Cols<W> x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = load_cols<float, VEC>(a.part + (k + j) * 2 * a.D + c);
+            for (int j = 0; j < 8; ++j) x[j] = load_cols<float, W>(a.part + (k + j) * 2 * a.D + c);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = plus(sum, x[j]);
+            for (int j = 0; j < 8; ++j) add_to(sum, x[j]);
         }
-        for (; k <= last; ++k) sum = plus(sum, load_cols<float, VEC>(a.part + k * 2 * a.D + c));
-        write_cols<O, VEC>(a, v, c, sum);
+        for (; k <= last; ++k) add_to(sum, load_cols<float, W>(a.part + k * 2 * a.D + c));
+        write_cols<O, W>(a, v, c, sum);
     }
 }
 
@@ -334,17 +370,32 @@ moe_status check(int64_t T, int D, int V, float scale, moe_dtype dtype) {
     return MOE_OK;
 }
 
-template <typename E, typename O>
-hipError_t launch_backward(SumArgs a, int64_t chunks, hipStream_t s) {
-    const unsigned grid = (unsigned)(a.row_blocks + (chunks + 3) / 4);
-    // rows of 4 columns a lane, where every row begins at a multiple of them
-    if (a.D % 4 == 0) embedding_sum_kernel<E, O, true><<<grid, 256, 0, s>>>(a);
-    else embedding_sum_kernel<E, O, false><<<grid, 256, 0, s>>>(a);
+template <typename E, typename O, int W>
+hipError_t launch_sums(SumArgs a, int64_t chunks, hipStream_t s) {
+    // about four column groups a thread
+    a.rows = std::max(1, 1024 / (a.D / W));
+    a.row_blocks = ((int64_t)a.V + a.rows - 1) / a.rows;
+    embedding_sum_kernel<E, O, W><<<(unsigned)(a.row_blocks + (chunks + 3) / 4), 256, 0, s>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
-    if (a.T > kLong) {
-        if (a.D % 4 == 0) embedding_join_kernel<O, true><<<(unsigned)chunks, 256, 0, s>>>(a);
-        else embedding_join_kernel<O, false><<<(unsigned)chunks, 256, 0, s>>>(a);
-    }
+    // 4 columns a thread: more loads in flight for the few rows there are
+    constexpr int J = W == 8 ? 4 : W;
+    if (a.T > kLong) embedding_join_kernel<O, J><<<(unsigned)chunks, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename E, typename O>
+hipError_t launch_backward(const SumArgs& a, int64_t chunks, hipStream_t s) {
+    // 16 bytes of dy a load where every row begins at a multiple of them
+    constexpr int W = Vec<E>::n;
+    if (a.D % W == 0) return launch_sums<E, O, W>(a, chunks, s);
+    return launch_sums<E, O, 1>(a, chunks, s);
+}
+
+hipError_t launch_sort(const int32_t* ids, int64_t T, int V, int32_t* order, int32_t* start, hipStream_t s) {
+    // about 512 workgroups, each with a power of two of entries
+    if (V <= 512 * 32) embedding_sort_kernel<5><<<(V + 31) / 32, kSortThreads, 0, s>>>(ids, T, V, order, start);
+    else if (V <= 512 * 128) embedding_sort_kernel<7><<<(V + 127) / 128, kSortThreads, 0, s>>>(ids, T, V, order, start);
+    else embedding_sort_kernel<9><<<(V + 511) / 512, kSortThreads, 0, s>>>(ids, T, V, order, start);
     return hipGetLastError();
 }
 
@@ -399,14 +450,9 @@ moe_status moe_embedding_backward(const int32_t* ids, const void* dy, void* dtab
     if (T == 0 && accumulate) return MOE_OK;
     char* ws = (char*)workspace;
     SumArgs a = {ids, (const int32_t*)(ws + l.order), (const int32_t*)(ws + l.start), dy, dtable, (float*)(ws + l.part),
-                 T, D, V, scale, accumulate ? 1 : 0, ((int64_t)V + 3) / 4};
-    // about 512 workgroups, each with a power of two of entries
-    int span = 16;
-    while (span < kMaxSpan && (int64_t)span * 512 < V) span *= 2;
+                 T, D, V, scale, accumulate ? 1 : 0, 1, 0};
     (void)hipGetLastError();
-    embedding_sort_kernel<<<(V + span - 1) / span, kSortThreads, 0, stream>>>(ids, T, V, span, (int32_t*)(ws + l.order),
-                                                                             (int32_t*)(ws + l.start));
-    if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
+    if (launch_sort(ids, T, V, (int32_t*)(ws + l.order), (int32_t*)(ws + l.start), stream) != hipSuccess) return MOE_ERR_HIP;
     const bool in16 = dtype == MOE_BF16, out16 = table_dtype == MOE_BF16;
     const hipError_t e = in16 && out16 ? launch_backward<uint16_t, uint16_t>(a, l.chunks, stream)
                          : in16        ? launch_backward<uint16_t, float>(a, l.chunks, stream)

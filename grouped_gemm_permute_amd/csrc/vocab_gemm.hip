@@ -76,8 +76,7 @@ struct Engine {
     int64_t m_pitch, n_pitch;         // bytes between k rows
     int k_m, k_n;                     // k rows that exist (not K-contiguous operands)
     int steps, kt_total;              // K steps of a product and of all
-    int ik = 0, ip = 0;               // the next stage: its step, its product
-    int k0;                           // first k row
+    int ik, ip;                       // the next stage: its step, its product
     int lane, wave, fw, rw;
     int m_off[NJ][2], n_off[2][2];    // fragment offsets in a stage
 
@@ -133,7 +132,7 @@ struct Engine {
             if constexpr (MC) {
                 p = m_src[j] + (om + (int64_t)ik * KC_ROW);
             } else {
-                const uint32_t k = min(k0 + ik * BK + ks_row(j, MJ), k_m - 1);
+                const uint32_t k = min(ik * BK + ks_row(j, MJ), k_m - 1);
                 p = m_src[j] + om + (uint64_t)k * (uint32_t)m_pitch;
             }
             load_lds16(p, st + (MJ * wave + j) * 1024);
@@ -144,7 +143,7 @@ struct Engine {
             if constexpr (NC) {
                 p = n_src[j] + (on + (int64_t)ik * KC_ROW);
             } else {
-                const int k = k0 + ik * BK + ks_row(j, WJ);
+                const int k = ik * BK + ks_row(j, WJ);
                 const char* row = n_src[j] + on + (uint64_t)(uint32_t)min(k, k_n - 1) * (uint32_t)n_pitch;
                 // opaque, so that the product does not move into a branch
                 asm volatile("" : "+v"(row));
@@ -323,6 +322,7 @@ __device__ __forceinline__ void logits_sources(Logits& e, const VocabOperand& h,
     e.n_plane = 2 * W.plane;
     e.steps = K / BK;
     e.ip = 6 - products;
+    e.ik = 0;
     e.kt_total = e.steps * products;
 }
 
@@ -415,24 +415,30 @@ __global__ __launch_bounds__(256, 2) void vocab_dz_kernel(const VocabDz a, int n
     Logits e;
     e.begin();
     logits_sources(e, a.h, a.W, a.products, a.K, row0, rows, nullptr, v0, a.V);
-    e.run(st0, st1, st2, nullptr);
-
     const int l = e.lane & 31, half = e.lane >> 5;
     const int left = (int)min((int64_t)a.len - c0, (int64_t)TN);
+    // the rows' values are on their way during the K loop
+    float lse[4], g[4];
+    int target[4];
 #pragma unroll
     for (int nj = 0; nj < 4; ++nj) {
         const int64_t row = min(row0 + 32 * nj + l, rows - 1);
-        const float lse = a.lse[row], g = a.g[row];
+        lse[nj] = a.lse[row], g[nj] = a.g[row];
+        target[nj] = a.target ? a.target[a.rows.rows ? a.rows.rows[row] : row] : -1;
+    }
+    e.run(st0, st1, st2, nullptr);
+
+#pragma unroll
+    for (int nj = 0; nj < 4; ++nj) {
 #pragma unroll
         for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
             for (int v = 0; v < 16; ++v)
-                e.acc[mi][nj][v] = __builtin_amdgcn_exp2f(fmaf(e.acc[mi][nj][v], a.inv_tau, -lse) * 1.4426950408889634f);
+                e.acc[mi][nj][v] = __builtin_amdgcn_exp2f(fmaf(e.acc[mi][nj][v], a.inv_tau, -lse[nj]) * 1.4426950408889634f);
         if (a.target) {
-            const int64_t target = a.target[a.rows.rows ? a.rows.rows[row] : row];
-            const bool mine = target >= v0 + 64 * e.fw && target < min(v0 + 64 * e.fw + 64, a.V);
+            const bool mine = target[nj] >= v0 + 64 * e.fw && target[nj] < min(v0 + 64 * e.fw + 64, a.V);
             if (__ballot(mine)) {
-                const int at = mine ? (int)(target - v0) - 64 * e.fw - 4 * half : -1;
+                const int at = mine ? (int)(target[nj] - v0) - 64 * e.fw - 4 * half : -1;
 #pragma unroll
                 for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
@@ -443,7 +449,7 @@ __global__ __launch_bounds__(256, 2) void vocab_dz_kernel(const VocabDz a, int n
 #pragma unroll
         for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) e.acc[mi][nj][v] *= g;
+            for (int v = 0; v < 16; ++v) e.acc[mi][nj][v] *= g[nj];
         if (left < TN) {
 #pragma unroll
             for (int mi = 0; mi < 2; ++mi)
@@ -488,118 +494,194 @@ __global__ __launch_bounds__(256, 2) void vocab_dz_kernel(const VocabDz a, int n
 #pragma unroll 4
         for (int r = threadIdx.x >> 5; r < 128; r += 8) {
             if (row0 + r >= rows) break;
-            *(u32x4_t*)(out + (row0 + r) * a.dz_pitch) = *(const u32x4_t*)(orow(r) + ((c ^ (r & 15)) << 4));
+            __builtin_nontemporal_store(*(const u32x4_t*)(orow(r) + ((c ^ (r & 15)) << 4)),
+                                        (u32x4_t*)(out + (row0 + r) * a.dz_pitch));
         }
     }
 }
 
+// The gradients' products run on one workgroup per CU.  A team of workgroups
+// takes the column tiles of the same 256 rows side by side, so that they read the
+// M operand once through their XCD's L2; the teams share out the K steps of all
+// row tiles evenly, each a contiguous range of them.  A tile whose steps one team
+// makes goes straight out; of any other each team writes its part (at most one
+// that it does not begin and one that it does not end) and a second kernel adds
+// them in order.
+constexpr int kGradUnits = 256;
+
+struct GradWork {
+    int m_tiles, n_tiles, teams;
+    int steps;                // K steps of one product
+    int virt;                 // of a tile: those of all products, at least 1
+    int per;                  // of a team
+};
+
+__device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64_t rows) {
+    GradWork w;
+    const int64_t M = a.dW ? a.len : rows;
+    const int K = a.dW ? (int)rows : a.len;
+    w.m_tiles = (int)((M + 255) / 256);
+    w.n_tiles = (a.N + TN - 1) / TN;
+    w.teams = kGradUnits / w.n_tiles;
+    w.steps = (K + BK - 1) / BK;
+    w.virt = max(w.steps * a.products, 1);
+    // parts cost what their write and their sum take, about 24 steps
+    const int even = (int)(((int64_t)w.m_tiles * w.virt + w.teams - 1) / w.teams);
+    const int whole = (w.m_tiles + w.teams - 1) / w.teams * w.virt;
+    w.per = max(even + 24 < whole ? max(even, 8) : whole, 1);
+    return w;
+}
+
+// Where a team's part of a tile goes: [256][256] fp32.
+__device__ __forceinline__ float* grad_part(const VocabGrad& a, const GradWork& w, int team, bool begun, int nt) {
+    return a.partial + (((int64_t)team * 2 + (begun ? 0 : 1)) * w.n_tiles + nt) * 65536;
+}
+
+// Four columns n0.. of row m on their way out.
+__device__ __forceinline__ void grad_out(const VocabGrad& a, int64_t m, int n0, float4 v) {
+    if (a.acc && n0 < a.acc_pitch) {
+        float4* p = (float4*)(a.acc + m * a.acc_pitch + n0);
+        if (a.add) {
+            const float4 o = *p;
+            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        }
+        if (!a.last) *p = v;
+    }
+    if (!a.last || n0 >= a.N) return;
+    const int64_t at = (!a.dW && a.rows.rows ? (int64_t)a.rows.rows[m] : m) * a.N + n0;
+    if (a.N % 4 == 0) {
+        if (a.out_bf16)
+            *(uint2*)((uint16_t*)a.out + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        else
+            *(float4*)((float*)a.out + at) = v;
+        return;
+    }
+    const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (n0 + q < a.N) {
+            if (a.out_bf16)
+                ((uint16_t*)a.out)[at + q] = (uint16_t)pack_bf16(x[q], 0.f);
+            else
+                ((float*)a.out)[at + q] = x[q];
+        }
+}
+
 // DW: both operands are k rows of columns; else M is K-contiguous.
 template <bool DW>
-__global__ __launch_bounds__(512, 1) void vocab_grad_kernel(const VocabGrad a, int m_tiles, int n_tiles) {
+__global__ __launch_bounds__(512, 1) void vocab_grad_kernel(const VocabGrad a) {
     using Eng = Engine<!DW, false, 256>;
     __shared__ __attribute__((aligned(1024))) char st0[Eng::SBYTES];
     __shared__ __attribute__((aligned(1024))) char st1[Eng::SBYTES];
     __shared__ __attribute__((aligned(1024))) char st2[Eng::SBYTES];
     __shared__ __attribute__((aligned(1024))) char st3[Eng::SBYTES];
     const int64_t rows = a.rows.count ? *a.rows.count : a.rows.T;
-    if (!DW) m_tiles = (int)((rows + 255) / 256);
-    // neighbouring tiles share the M operand's rows through an XCD's L2
-    const int id = xcd_remap_work(blockIdx.x, m_tiles * n_tiles * a.splits);
-    if (id < 0) return;
-    const int nt = id % n_tiles, rest = id / n_tiles;
-    const int mt = rest % m_tiles, split = rest / m_tiles;
-    const int64_t M = DW ? a.len : rows, m0 = (int64_t)mt * 256;
-    const int K = DW ? (int)rows : a.len;
-    const int all = (K + BK - 1) / BK, per = (all + a.splits - 1) / a.splits;
-    const int first = min(split * per, all), steps = min(per, all - first);
-
+    const GradWork w = grad_work(a, rows);
+    // 32 consecutive places on an XCD
+    const int place = (blockIdx.x & 7) * (kGradUnits / 8) + (blockIdx.x >> 3);
+    const int team = place / w.n_tiles, nt = place - team * w.n_tiles;
+    if (team >= w.teams) return;
+    const int64_t M = DW ? a.len : rows;
+    const int64_t total = (int64_t)w.m_tiles * w.virt;
+    const int64_t end = min((int64_t)(team + 1) * w.per, total);
     Eng e;
-    e.begin();
-    e.k0 = first * BK;
-    e.k_m = e.k_n = K;
-    e.steps = steps;
-    e.ip = 6 - a.products;
-    e.kt_total = steps * a.products;
-    e.m_plane = 2 * a.m.plane;
-    e.n_plane = 2 * a.n.plane;
-    e.m_pitch = 2 * a.m.pitch;
-    e.n_pitch = 2 * a.n.pitch;
-#pragma unroll
-    for (int j = 0; j < Eng::MJ; ++j) {
-        if constexpr (DW) {
-            const int c = e.ks_chunk(e.ks_row(j, Eng::MJ));
-            e.m_src[j] = (const char*)(a.m.p + m0 + 8 * c);   // dz's rows are whole tiles
-        } else {
-            const int row = e.kc_row(j, Eng::MJ);
-            e.m_src[j] = (const char*)(a.m.p + min(m0 + row, M - 1) * a.m.pitch + first * BK + 8 * e.kc_chunk(row));
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < Eng::WJ; ++j) {
-        int n = nt * TN + 8 * e.ks_chunk(e.ks_row(j, Eng::WJ));
-        if (n >= a.n.pitch) n = 0;       // an address that exists; its sums are never stored
-        e.n_src[j] = (const char*)(a.n.p + n);
-    }
-    e.run(st0, st1, st2, st3);
+    for (int64_t at = (int64_t)team * w.per; at < end;) {
+        const int mt = (int)(at / w.virt);
+        const int k0 = (int)(at - (int64_t)mt * w.virt), k1 = (int)min((int64_t)w.virt, k0 + (end - at));
+        at += k1 - k0;
+        const int64_t m0 = (int64_t)mt * 256;
 
-    // Through LDS in two passes of 128 rows (those of the wavefronts rw = pass),
-    // block nj in stage buffer nj as 32 rows of 1 KiB, 16-byte chunks
-    // XOR-swizzled by the row; then each wavefront stores 16 rows.
-    auto buf = [&](int q) -> char* { return q == 0 ? st0 : q == 1 ? st1 : q == 2 ? st2 : st3; };
-    const int l = e.lane & 31, n0 = nt * TN + 4 * e.lane;
+        e.begin();
+        e.k_m = e.k_n = DW ? (int)rows : a.len;
+        e.steps = w.steps;
+        e.ip = 6 - a.products + (w.steps ? k0 / w.steps : 0);
+        e.ik = w.steps ? k0 % w.steps : 0;
+        e.kt_total = w.steps ? k1 - k0 : 0;
+        e.m_plane = 2 * a.m.plane;
+        e.n_plane = 2 * a.n.plane;
+        e.m_pitch = 2 * a.m.pitch;
+        e.n_pitch = 2 * a.n.pitch;
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-        if (pass) __syncthreads();
-        if (e.rw == pass) {
-#pragma unroll
-            for (int nj = 0; nj < 4; ++nj)
-#pragma unroll
-                for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-                    for (int vg = 0; vg < 4; ++vg) {
-                        const int c = 16 * e.fw + 8 * mi + 2 * vg + (e.lane >> 5);
-                        const f32x16_t& v = e.acc[mi][nj];
-                        *(float4*)(buf(nj) + l * 1024 + ((c ^ l) << 4)) =
-                            make_float4(v[4 * vg], v[4 * vg + 1], v[4 * vg + 2], v[4 * vg + 3]);
-                    }
-        }
-        __syncthreads();
-        const char* sq = buf(e.wave >> 1);
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-            const int r = 16 * (e.wave & 1) + i;
-            const int64_t m = m0 + 128 * pass + 32 * (e.wave >> 1) + r;
-            if (m >= M) break;
-            float4 v = *(const float4*)(sq + r * 1024 + ((e.lane ^ r) << 4));
-            if (a.partial) {
-                if (n0 < a.part_pitch) {
-                    float4* p = (float4*)(a.partial + split * a.split_stride + m * a.part_pitch + n0);
-                    if (a.add) {
-                        const float4 o = *p;
-                        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-                    }
-                    *p = v;
-                }
-                continue;
-            }
-            const int64_t at = (!DW && a.rows.rows ? (int64_t)a.rows.rows[m] : m) * a.N + n0;
-            const float x[4] = {v.x, v.y, v.z, v.w};
-            if (n0 + 4 <= a.N && a.N % 4 == 0) {
-                if (a.out_bf16)
-                    *(uint2*)((uint16_t*)a.out + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-                else
-                    *(float4*)((float*)a.out + at) = v;
+        for (int j = 0; j < Eng::MJ; ++j) {
+            if constexpr (DW) {
+                e.m_src[j] = (const char*)(a.m.p + m0 + 8 * e.ks_chunk(e.ks_row(j, Eng::MJ)));   // dz's rows are whole tiles
             } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (n0 + q < a.N) {
-                        if (a.out_bf16)
-                            ((uint16_t*)a.out)[at + q] = (uint16_t)pack_bf16(x[q], 0.f);
-                        else
-                            ((float*)a.out)[at + q] = x[q];
-                    }
+                const int row = e.kc_row(j, Eng::MJ);
+                e.m_src[j] = (const char*)(a.m.p + min(m0 + row, M - 1) * a.m.pitch + 8 * e.kc_chunk(row));
             }
         }
+#pragma unroll
+        for (int j = 0; j < Eng::WJ; ++j) {
+            int n = nt * TN + 8 * e.ks_chunk(e.ks_row(j, Eng::WJ));
+            if (n >= a.n.pitch) n = 0;       // an address that exists; its sums are never stored
+            e.n_src[j] = (const char*)(a.n.p + n);
+        }
+        e.run(st0, st1, st2, st3);
+
+        // Through LDS in two passes of 128 rows (those of the wavefronts rw =
+        // pass), block nj in stage buffer nj as 32 rows of 1 KiB, 16-byte chunks
+        // XOR-swizzled by the row; then each wavefront stores 16 rows.
+        float* part = k1 - k0 < w.virt ? grad_part(a, w, team, k0 > 0, nt) : nullptr;
+        auto buf = [&](int q) -> char* { return q == 0 ? st0 : q == 1 ? st1 : q == 2 ? st2 : st3; };
+        const int l = e.lane & 31;
+#pragma unroll
+        for (int pass = 0; pass < 2; ++pass) {
+            if (pass) __syncthreads();
+            if (e.rw == pass) {
+#pragma unroll
+                for (int nj = 0; nj < 4; ++nj)
+#pragma unroll
+                    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                        for (int vg = 0; vg < 4; ++vg) {
+                            const int c = 16 * e.fw + 8 * mi + 2 * vg + (e.lane >> 5);
+                            const f32x16_t& v = e.acc[mi][nj];
+                            *(float4*)(buf(nj) + l * 1024 + ((c ^ l) << 4)) =
+                                make_float4(v[4 * vg], v[4 * vg + 1], v[4 * vg + 2], v[4 * vg + 3]);
+                        }
+            }
+            __syncthreads();
+            const char* sq = buf(e.wave >> 1);
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const int r = 16 * (e.wave & 1) + i, tr = 128 * pass + 32 * (e.wave >> 1) + r;
+                const int64_t m = m0 + tr;
+                if (m >= M) break;
+                const float4 v = *(const float4*)(sq + r * 1024 + ((e.lane ^ r) << 4));
+                if (part) *(float4*)(part + tr * 256 + 4 * e.lane) = v;
+                else grad_out(a, m, nt * TN + 4 * e.lane, v);
+            }
+        }
+        __syncthreads();       // the stages are read out before they are filled again
+    }
+}
+
+// The tiles that more than one team made: 32 rows of one a workgroup.
+__global__ __launch_bounds__(256) void vocab_grad_sum_kernel(const VocabGrad a) {
+    const int64_t rows = a.rows.count ? *a.rows.count : a.rows.T;
+    const GradWork w = grad_work(a, rows);
+    const int slab = blockIdx.x & 7, tile = blockIdx.x >> 3;
+    const int mt = tile / w.n_tiles, nt = tile - mt * w.n_tiles;
+    if (mt >= w.m_tiles) return;
+    const int64_t M = a.dW ? a.len : rows;
+    const int64_t s0 = (int64_t)mt * w.virt, s1 = s0 + w.virt;
+    const int t0 = (int)(s0 / w.per), t1 = (int)((s1 - 1) / w.per);
+    if (t0 == t1) return;
+    const int lane = threadIdx.x & 63, n0 = nt * TN + 4 * lane;
+    if (n0 >= a.N) return;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+        const int tr = 32 * slab + 4 * i + (threadIdx.x >> 6);
+        const int64_t m = (int64_t)mt * 256 + tr;
+        if (m >= M) break;
+        const int at = tr * 256 + 4 * lane;
+        float4 v = *(const float4*)(grad_part(a, w, t0, false, nt) + at);
+#pragma unroll 4
+        for (int t = t0 + 1; t <= t1; ++t) {
+            const float4 o = *(const float4*)(grad_part(a, w, t, true, nt) + at);
+            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        }
+        grad_out(a, m, n0, v);
     }
 }
 
@@ -625,16 +707,21 @@ hipError_t launch_vocab_dz(const VocabDz& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+size_t vocab_grad_partial_bytes(int N) {
+    const int n_tiles = (N + TN - 1) / TN;
+    return (size_t)(kGradUnits / n_tiles) * 2 * n_tiles * 65536 * 4;
+}
+
 hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s) {
-    if ((a.products != 1 && a.products != 6) || a.rows.T <= 0 || a.len <= 0 || a.N <= 0 || a.splits < 1 ||
-        a.n.pitch % BK || a.m.pitch % TN || a.n.pitch < a.N)
+    if ((a.products != 1 && a.products != 6) || a.rows.T <= 0 || a.len <= 0 || a.N <= 0 || a.N > kGradUnits * TN ||
+        a.n.pitch % BK || a.m.pitch % TN || a.n.pitch < a.N || !a.partial || ((a.add || !a.last) && !a.acc))
         return hipErrorInvalidValue;
-    const int64_t M = a.dW ? a.len : a.rows.T;
-    const int64_t m_tiles = (M + 255) / 256, n_tiles = (a.N + TN - 1) / TN;
-    if (m_tiles * n_tiles * a.splits > kMaxTiles) return hipErrorInvalidValue;
-    const unsigned grid = grid_for_work(m_tiles * n_tiles * a.splits);
-    if (a.dW) vocab_grad_kernel<true><<<grid, 512, 0, s>>>(a, (int)m_tiles, (int)n_tiles);
-    else vocab_grad_kernel<false><<<grid, 512, 0, s>>>(a, (int)m_tiles, (int)n_tiles);
+    const int64_t tiles = ((a.dW ? a.len : a.rows.T) + 255) / 256 * ((a.N + TN - 1) / TN);
+    if (tiles > kMaxTiles / 4) return hipErrorInvalidValue;
+    if (a.dW) vocab_grad_kernel<true><<<kGradUnits, 512, 0, s>>>(a);
+    else vocab_grad_kernel<false><<<kGradUnits, 512, 0, s>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+    vocab_grad_sum_kernel<<<(unsigned)(tiles * 8), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -64,26 +64,27 @@ struct VocabDz {
 };
 hipError_t launch_vocab_dz(const VocabDz& a, hipStream_t s);
 
-// C[m][n] = sum over k of M and N operands, K split into `splits` parts.
+// C[m][n] = sum over k of M and N operands:
 //   dh (dW = false): m = compact row, k = entry of the piece, n = column of D
 //   dW (dW = true):  m = entry of the piece, k = compact row, n = column of D
-// With partial, split s goes to partial + s split_stride (row pitch
-// part_pitch, added to what is there if `add`); else to out (rows mapped
-// through rows.rows for dh), fp32 or bf16, row pitch N.
+// added to acc's (fp32, row pitch acc_pitch) if `add`, and written to acc, or with
+// `last` to out (fp32 or bf16, row pitch N; dh's rows mapped through rows.rows).
+// Two launches: the tiles, and the sums of those that several workgroups made.
 struct VocabGrad {
     bool dW;
     VocabOperand m, n;
     VocabRows rows;
     int len;                  // entries of the piece
     int N;                    // columns of D
-    int splits;
     int products;
-    float* partial;
-    int64_t split_stride, part_pitch;
-    bool add;
+    float* partial;           // vocab_grad_partial_bytes()
+    float* acc;               // null where neither `add` nor !last
+    int64_t acc_pitch;
+    bool add, last;
     void* out;
     bool out_bf16;
 };
+size_t vocab_grad_partial_bytes(int N);
 hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s);
 
 }  // namespace moe

@@ -39,9 +39,9 @@ constexpr size_t kAlign = 256;
 constexpr int kMaxD = 16384, kMaxTop = 256;
 constexpr int64_t kMaxV = 1 << 24, kMaxT = 1 << 28;
 constexpr int64_t kListRows = 1024;
-// dz of one piece of the vocabulary: the largest that ordinary steps take whole
-// or in a few pieces (32768 rows: 16384 entries), small beside 288 GB.
-constexpr int64_t kDzBytes = 1ll << 30;
+// dz of one piece of the vocabulary: what ordinary steps take whole or in a few
+// pieces (32768 rows: 32768 entries), little of 288 GB.
+constexpr int64_t kDzBytes = 1ll << 31;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -82,53 +82,63 @@ __global__ __launch_bounds__(256) void vocab_live_kernel(const Targets a, int64_
 }
 
 // The rows that count, in order: rows[0 .. *count), and pos[t], a row's place
-// among them or -1.  One workgroup; a thread takes 8 consecutive rows a turn.
-// zero0, zero1 (or null): set to 0 for the other rows.
+// among them or -1.  A workgroup lists kListChunk rows and counts those before
+// them itself, so that none waits for another (32768 rows: 0.5 MB read by 8
+// workgroups).  zero0, zero1 (or null): set to 0 for the other rows.
+constexpr int kListChunk = 4096;
 __global__ __launch_bounds__(1024) void vocab_list_kernel(const int32_t* __restrict__ target, const int32_t* __restrict__ live,
                                                           int V, int64_t T, int32_t* __restrict__ rows,
                                                           int32_t* __restrict__ pos, int32_t* __restrict__ count,
                                                           float* zero0, float* zero1) {
-    __shared__ int32_t sums[16];
+    __shared__ int32_t sums[2][16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int32_t n = 0;
-    for (int64_t base = 0; base < T; base += 8192) {
-        const int64_t t0 = base + 8 * tid;
+    const int64_t base = (int64_t)blockIdx.x * kListChunk, t0 = base + 4 * tid;
+    auto four = [&](int64_t t) {       // which of rows t .. t + 3 (all there) count
+        int32_t x[4];
+        __builtin_memcpy(x, (target ? target : live) + t, 16);
         int in = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t t = min(t0 + j, T - 1);
-            const bool l = target ? target[t] >= 0 && target[t] < V : live[t] != 0;
-            if (t0 + j < T && l) in |= 1 << j;
-        }
-        const int mine = __popc(in);
-        int incl = mine;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(incl, d);
-            if (lane >= d) incl += o;
-        }
-        if (lane == 63) sums[wave] = incl;
-        __syncthreads();
-        int place = n + incl - mine;
-        for (int w = 0; w < 16; ++w) {
-            if (w < wave) place += sums[w];
-            n += sums[w];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t t = t0 + j;
-            if (t >= T) break;
-            if (in >> j & 1) {
-                rows[place] = (int32_t)t;
-                pos[t] = place++;
-            } else {
-                pos[t] = -1;
-                if (zero0) zero0[t] = 0.f;
-                if (zero1) zero1[t] = 0.f;
-            }
+        for (int j = 0; j < 4; ++j) in |= (target ? x[j] >= 0 && x[j] < V : x[j] != 0) << j;
+        return in;
+    };
+    int before = 0, in = 0;
+#pragma unroll 4
+    for (int64_t t = 4 * tid; t < base; t += 4096) before += __popc(four(t));
+    if (t0 + 4 <= T) {
+        in = four(t0);
+    } else {
+        for (int j = 0; t0 + j < T; ++j) {
+            const int32_t x = (target ? target : live)[t0 + j];
+            in |= (target ? x >= 0 && x < V : x != 0) << j;
         }
     }
-    if (tid == 0) *count = n;
+    const int mine = __popc(in);
+    int incl = mine;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(incl, d);
+        if (lane >= d) incl += o;
+    }
+    for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
+    if (lane == 63) sums[0][wave] = incl, sums[1][wave] = before;
+    __syncthreads();
+    int place = incl - mine, n = 0;
+    for (int w = 0; w < 16; ++w) {
+        if (w < wave) place += sums[0][w];
+        place += sums[1][w];
+        n += sums[0][w] + sums[1][w];
+    }
+    for (int j = 0; j < 4 && t0 + j < T; ++j) {
+        const int64_t t = t0 + j;
+        if (in >> j & 1) {
+            rows[place] = (int32_t)t;
+            pos[t] = place++;
+        } else {
+            pos[t] = -1;
+            if (zero0) zero0[t] = 0.f;
+            if (zero1) zero1[t] = 0.f;
+        }
+    }
+    if (tid == 0 && base + kListChunk >= T) *count = n;
 }
 
 // The backward's rows: row t of h to row pos[t] of the copy, as bf16 (one plane)
@@ -242,6 +252,7 @@ __global__ __launch_bounds__(256) void vocab_finish_kernel(const FinishArgs a) {
     if ((int64_t)blockIdx.x * 16 >= n) return;
     float top = -INFINITY, sum = 0.f;
     if (i < n) {
+#pragma unroll 4
         for (int k = sl; k < a.n_tiles; k += 16) {
             const float2 p = a.part[k * a.pitch + i];
             const float m = fmaxf(top, p.x), off = m == -INFINITY ? 0.f : m;
@@ -412,36 +423,6 @@ __global__ __launch_bounds__(64) void vocab_teacher_kernel(const TeacherArgs a) 
     }
 }
 
-// out[map[i]][c] = sum over the buffers of part[s][i][c], in order.
-template <typename O>
-__global__ __launch_bounds__(256) void vocab_reduce_kernel(const float* __restrict__ part, int splits, int64_t stride,
-                                                           int64_t pitch, VocabRows rows, int N, O* __restrict__ out) {
-    const int64_t n = rows.count ? *rows.count : rows.T;
-    const int lane = threadIdx.x & 63;
-    for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < n; i += (int64_t)gridDim.x * 4) {
-        const int64_t t = rows.rows ? rows.rows[i] : i;
-        for (int c = 4 * lane; c < N; c += 256) {
-            float4 v = *(const float4*)(part + i * pitch + c);
-            for (int s = 1; s < splits; ++s) {
-                const float4 o = *(const float4*)(part + s * stride + i * pitch + c);
-                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-            }
-            O* p = out + t * N + c;
-            const float x[4] = {v.x, v.y, v.z, v.w};
-            if (c + 4 <= N && N % 4 == 0) {
-                if constexpr (sizeof(O) == 2) *(uint2*)p = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-                else *(float4*)p = v;
-            } else {
-                for (int q = 0; q < 4; ++q)
-                    if (c + q < N) {
-                        if constexpr (sizeof(O) == 2) p[q] = to_bf16(x[q]);
-                        else p[q] = x[q];
-                    }
-            }
-        }
-    }
-}
-
 template <typename O>
 __global__ __launch_bounds__(256) void vocab_zero_kernel(O* p, int64_t n) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = O(0);
@@ -455,26 +436,8 @@ struct Plan {
     int planes, products, Dp;
     int64_t n_tiles;          // stats: column tiles
     int64_t piece, pieces;    // entries of a piece (a multiple of 256), and how many
-    int dh_splits, dW_splits;
-    size_t rows, pos, count, live, hc, Wc, part, zt, g, lse, dz, dh_part, dW_part, total;
+    size_t rows, pos, count, live, hc, Wc, part, zt, g, lse, dz, acc, total;
 };
-
-// Parts to split a product's K steps into: the fewest rounds of the 256 CUs,
-// each part costing about 6 steps more (its start and its end) and its fp32 tile,
-// written and read again, about 4.
-int splits_of(int64_t tiles, int64_t steps) {
-    int best = 1;
-    double least = 1e300;
-    for (int s = 1; s <= 64 && (s == 1 || (steps / s >= 4 && tiles * s <= 4096)); ++s) {
-        const double rounds = (double)((tiles * s + 255) / 256);
-        const double cost = rounds * (double)((steps + s - 1) / s + 6 + (s > 1 ? 4 : 0)) + (s > 1 ? 0.02 * tiles * s : 0);
-        if (cost < least * 0.98) {
-            least = cost;
-            best = s;
-        }
-    }
-    return best;
-}
 
 Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     Plan p = {};
@@ -507,14 +470,11 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
         p.pieces = (p.n_tiles + most - 1) / most;
         p.piece = (p.n_tiles + p.pieces - 1) / p.pieces * tile;
         p.pieces = (p.n_tiles * tile + p.piece - 1) / p.piece;
-        const int64_t m_tiles = (T + 255) / 256, d_tiles = (D + 255) / 256;
-        p.dh_splits = splits_of(m_tiles * d_tiles, p.piece / 32 * p.products);
-        p.dW_splits = splits_of(p.piece / 256 * d_tiles, (T + 31) / 32 * p.products);
         p.g = take(true, (size_t)T * 4);
         p.lse = take(true, (size_t)T * 4);
         p.dz = take(true, (size_t)p.planes * T * p.piece * 2);
-        p.dh_part = take(p.pieces * p.dh_splits > 1, (size_t)p.dh_splits * T * p.Dp * 4);
-        p.dW_part = take(p.dW_splits > 1, (size_t)p.dW_splits * p.piece * p.Dp * 4);
+        p.part = take(true, vocab_grad_partial_bytes(D));
+        p.acc = take(p.pieces > 1, (size_t)T * p.Dp * 4);
     }
     p.total = at;
     return p;
@@ -562,7 +522,8 @@ moe_status begin(const Call& a, const Plan& p, char* ws, VocabRows* rows, VocabO
             TRY(hipGetLastError());
         }
         *rows = {(const int32_t*)(ws + p.rows), (const int32_t*)(ws + p.count), a.T};
-        vocab_list_kernel<<<1, 1024, 0, s>>>(a.targets.target, live, a.targets.V, a.T, (int32_t*)(ws + p.rows),
+        const unsigned chunks = (unsigned)((a.T + kListChunk - 1) / kListChunk);
+        vocab_list_kernel<<<chunks, 1024, 0, s>>>(a.targets.target, live, a.targets.V, a.T, (int32_t*)(ws + p.rows),
                                             (int32_t*)(ws + p.pos), (int32_t*)(ws + p.count), zero0, zero1);
         TRY(hipGetLastError());
     }
@@ -660,53 +621,33 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
             TRY(hipGetLastError());
         }
         VocabGrad q = {};
+        q.m = {dz, p.piece, dz_plane};
         q.rows = rows;
         q.len = len;
         q.N = a.D;
         q.products = p.products;
-        q.part_pitch = p.Dp;
+        q.partial = (float*)(ws + p.part);
         if (dh) {
             q.dW = false;
-            q.m = {dz, p.piece, dz_plane};
             q.n = {W.p + v0 * W.pitch, W.pitch, W.plane};
-            q.splits = p.dh_splits;
-            q.partial = p.pieces * p.dh_splits > 1 ? (float*)(ws + p.dh_part) : nullptr;
-            q.split_stride = a.T * p.Dp;
+            q.acc = p.pieces > 1 ? (float*)(ws + p.acc) : nullptr;
+            q.acc_pitch = p.Dp;
             q.add = v0 > 0;
+            q.last = v0 + p.piece >= V;
             q.out = dh;
             q.out_bf16 = h16;
             TRY(launch_vocab_grad(q, s));
         }
         if (dW) {
             q.dW = true;
-            q.m = {dz, p.piece, dz_plane};
             q.n = h;
-            q.splits = p.dW_splits;
-            q.partial = p.dW_splits > 1 ? (float*)(ws + p.dW_part) : nullptr;
-            q.split_stride = p.piece * p.Dp;
+            q.acc = nullptr;
             q.add = false;
+            q.last = true;
             q.out_bf16 = dW_dtype == MOE_BF16;
             q.out = q.out_bf16 ? (void*)((uint16_t*)dW + v0 * a.D) : (void*)((float*)dW + v0 * a.D);
             TRY(launch_vocab_grad(q, s));
-            if (q.partial) {
-                const VocabRows all = {nullptr, nullptr, len};
-                const unsigned grid = (unsigned)std::min<int64_t>((len + 3) / 4, 8192);
-                if (q.out_bf16)
-                    vocab_reduce_kernel<<<grid, 256, 0, s>>>(q.partial, q.splits, q.split_stride, q.part_pitch, all, a.D,
-                                                             (uint16_t*)q.out);
-                else
-                    vocab_reduce_kernel<<<grid, 256, 0, s>>>(q.partial, q.splits, q.split_stride, q.part_pitch, all, a.D,
-                                                             (float*)q.out);
-                TRY(hipGetLastError());
-            }
         }
-    }
-    if (dh && p.pieces * p.dh_splits > 1) {
-        const unsigned grid = (unsigned)std::min<int64_t>((a.T + 3) / 4, 8192);
-        const float* part = (const float*)(ws + p.dh_part);
-        if (h16) vocab_reduce_kernel<<<grid, 256, 0, s>>>(part, p.dh_splits, a.T * p.Dp, p.Dp, rows, a.D, (uint16_t*)dh);
-        else vocab_reduce_kernel<<<grid, 256, 0, s>>>(part, p.dh_splits, a.T * p.Dp, p.Dp, rows, a.D, (float*)dh);
-        TRY(hipGetLastError());
     }
     return MOE_OK;
 }

@@ -745,7 +745,7 @@ moe_status moe_cross_entropy_forward(const void *h, const void *W, const int32_t
  *   workspace >= moe_cross_entropy_workspace_size(.., 1) bytes, 256-byte aligned
  *
  * The logits are made again, a piece of the vocabulary at a time; dz of a piece
- * (at most 1 GiB, or 256 entries) stays in the workspace.  For bf16 operands dz is rounded to bf16 before the two
+ * (at most 2 GiB, or 256 entries) stays in the workspace.  For bf16 operands dz is rounded to bf16 before the two
  * products, also where dW is fp32.  Sizes and errors as in the forward.
  */
 moe_status moe_cross_entropy_backward(const void *h, const void *W, const int32_t *targets, const float *lse,
