@@ -27,6 +27,8 @@
 #include "mfma_common.h"
 #include "vocab_internal.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -45,9 +47,6 @@ static_assert(kVocabTileCols == TN && kVocabTileRows == 128, "tile sizes");
 // 64-byte rows (4 chunks): 16 consecutive rows read at one logical chunk hit
 // 16 distinct bank groups.
 __device__ __forceinline__ int swz_kc(int row) { return (row >> 2) & 3; }
-
-// What an N operand's k rows past its last one are read as.
-__device__ __attribute__((aligned(16))) u32x4_t zero_chunk[1];
 
 // The products of planes, smallest first: (1,1) (2,0) (0,2) (1,0) (0,1) (0,0),
 // two bits each; one product alone is the last.
@@ -68,13 +67,15 @@ struct Engine {
     static constexpr int PER_STAGE = MJ + WJ;
     static_assert(MC || ROWS == 256, "k rows of 256 columns");
 
-    // What a lane's loads read: for a K-contiguous operand the addresses of its
-    // rows' chunks, else of its column chunk in k row 0.
-    const char* m_src[MJ];
-    const char* n_src[WJ];
+    // What the loads read: a base for the whole tile and a lane's offset from it,
+    // in bytes (one address register a load).  K-contiguous: the lane's row, its
+    // chunk of it; else its k row of a step, its chunk of columns.  A last step
+    // that ends inside has the largest offset that it may read; lanes past it
+    // read there.
+    const char *m_base, *n_base;
+    uint32_t m_at[MJ], n_at[WJ], m_most, n_most;
     int64_t m_plane, n_plane;         // bytes between planes
-    int64_t m_pitch, n_pitch;         // bytes between k rows
-    int k_m, k_n;                     // k rows that exist (not K-contiguous operands)
+    int64_t m_step, n_step;           // bytes between K steps
     int steps, kt_total;              // K steps of a product and of all
     int ik, ip;                       // the next stage: its step, its product
     int lane, wave, fw, rw;
@@ -86,16 +87,20 @@ struct Engine {
         bf16x8_t n[2][2], m[2][NJ];
     };
 
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+            for (int nj = 0; nj < NJ; ++nj) acc[mi][nj] = f32x16_t{};
+    }
+
     __device__ __forceinline__ void begin() {
         const int tid = threadIdx.x;
         lane = tid & 63;
         wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         fw = wave & 3;
         rw = wave >> 2;
-#pragma unroll
-        for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-            for (int nj = 0; nj < NJ; ++nj) acc[mi][nj] = f32x16_t{};
+        clear();
         const int G = lane >> 4, sl = lane & 15, xr = lane & 31;
         auto tr_off = [&](int R, int r) {
             const int k = 8 * (G >> 1) + 4 * r + (sl >> 2);
@@ -123,42 +128,63 @@ struct Engine {
     __device__ __forceinline__ int ks_row(int j, int per) const { return 2 * (per * wave + j) + (lane >> 5); }
     __device__ __forceinline__ int ks_chunk(int row) const { return (lane & 31) ^ swz_tr(row); }
 
-    __device__ __forceinline__ void issue(char* st) {
-        const int pm = (kPlaneM >> (2 * ip)) & 3, pn = (kPlaneN >> (2 * ip)) & 3;
-        const int64_t om = pm * m_plane, on = pn * n_plane;
+    // A lane's offsets in tiles of `rows` rows (at least 1) `pitch` bytes apart.
+    __device__ __forceinline__ void m_rows(int rows, int64_t pitch) {
 #pragma unroll
         for (int j = 0; j < MJ; ++j) {
-            const char* p;
-            if constexpr (MC) {
-                p = m_src[j] + (om + (int64_t)ik * KC_ROW);
-            } else {
-                const uint32_t k = min(ik * BK + ks_row(j, MJ), k_m - 1);
-                p = m_src[j] + om + (uint64_t)k * (uint32_t)m_pitch;
-            }
-            load_lds16(p, st + (MJ * wave + j) * 1024);
+            const int row = kc_row(j, MJ);
+            m_at[j] = (uint32_t)min(row, rows - 1) * (uint32_t)pitch + 16 * kc_chunk(row);
         }
+        m_step = KC_ROW;
+    }
+    __device__ __forceinline__ void n_rows(int rows, int64_t pitch) {
 #pragma unroll
         for (int j = 0; j < WJ; ++j) {
-            const char* p;
-            if constexpr (NC) {
-                p = n_src[j] + (on + (int64_t)ik * KC_ROW);
-            } else {
-                const int k = ik * BK + ks_row(j, WJ);
-                const char* row = n_src[j] + on + (uint64_t)(uint32_t)min(k, k_n - 1) * (uint32_t)n_pitch;
-                // opaque, so that the product does not move into a branch
-                asm volatile("" : "+v"(row));
-                p = k < k_n ? row : (const char*)zero_chunk;
-            }
-            load_lds16(p, st + M_BYTES + (WJ * wave + j) * 1024);
+            const int row = kc_row(j, WJ);
+            n_at[j] = (uint32_t)min(row, rows - 1) * (uint32_t)pitch + 16 * kc_chunk(row);
         }
+        n_step = KC_ROW;
+    }
+    // ... and of k rows, `last` of them (at least 1) in the last step; columns from
+    // `cols` on are read as the first ones, and their sums not stored.
+    static __device__ __forceinline__ uint32_t most(int last, int64_t pitch, int cols) {
+        return (uint32_t)(last - 1) * (uint32_t)pitch + 2 * min(cols, 256) - 16;
+    }
+    __device__ __forceinline__ void m_ks(int last, int64_t pitch) {
+#pragma unroll
+        for (int j = 0; j < MJ; ++j) {
+            const int k = ks_row(j, MJ);
+            m_at[j] = (uint32_t)k * (uint32_t)pitch + 16 * ks_chunk(k);
+        }
+        m_most = most(last, pitch, 256);
+        m_step = BK * pitch;
+    }
+    __device__ __forceinline__ void n_ks(int last, int64_t pitch, int cols) {
+#pragma unroll
+        for (int j = 0; j < WJ; ++j) {
+            const int k = ks_row(j, WJ);
+            n_at[j] = (uint32_t)k * (uint32_t)pitch + (8 * ks_chunk(k) < cols ? 16 * ks_chunk(k) : 0);
+        }
+        n_most = most(last, pitch, cols);
+        n_step = BK * pitch;
+    }
+
+    __device__ __forceinline__ void issue(char* st) {
+        const int pm = (kPlaneM >> (2 * ip)) & 3, pn = (kPlaneN >> (2 * ip)) & 3;
+        const char* m = m_base + pm * m_plane + ik * m_step;
+        const char* n = n_base + pn * n_plane + ik * n_step;
+        const bool end = ik + 1 == steps;
+#pragma unroll
+        for (int j = 0; j < MJ; ++j)
+            load_lds16(m + (MC ? m_at[j] : min(m_at[j], end ? m_most : ~0u)), st + (MJ * wave + j) * 1024);
+#pragma unroll
+        for (int j = 0; j < WJ; ++j)
+            load_lds16(n + (NC ? n_at[j] : min(n_at[j], end ? n_most : ~0u)), st + M_BYTES + (WJ * wave + j) * 1024);
         // the next stage; past the last one it is read again, into a buffer
         // that is never computed on, so that the loads in flight can be counted
-        if (ik + 1 < steps) {
-            ++ik;
-        } else if (ip < 5) {
-            ++ip;
-            ik = 0;
-        }
+        const bool turn = end && ip < 5;
+        ik = turn ? 0 : ik + (end ? 0 : 1);
+        ip += turn ? 1 : 0;
     }
 
     __device__ __forceinline__ void read_frags(const char* st, Frags& f) const {
@@ -203,6 +229,9 @@ struct Engine {
         __builtin_amdgcn_s_waitcnt(waitcnt_imm(NS == 4 ? PER_STAGE : 0, 0));
         __builtin_amdgcn_s_barrier();
         fence();
+        work(fc, fn, nxt, dma);
+    }
+    __device__ __forceinline__ void work(const Frags& fc, Frags& fn, const char* nxt, char* dma) {
         issue(dma);
         read_frags(nxt, fn);
         mfmas(fc);
@@ -298,32 +327,44 @@ __device__ __forceinline__ bool logits_tile(int m_tiles, int n_tiles, int& mt, i
 
 using Logits = Engine<true, true, 128>;
 
-// h's rows and W's rows of a logits tile.
-__device__ __forceinline__ void logits_sources(Logits& e, const VocabOperand& h, const VocabOperand& W, int products,
-                                               int K, int64_t row0, int64_t rows, const int32_t* gather, int64_t v0,
-                                               int64_t V) {
-    int64_t r[Logits::MJ];
-#pragma unroll
-    for (int j = 0; j < Logits::MJ; ++j) r[j] = min(row0 + e.kc_row(j, Logits::MJ), rows - 1);
-    if (gather) {
-#pragma unroll
-        for (int j = 0; j < Logits::MJ; ++j) r[j] = gather[r[j]];
-    }
-#pragma unroll
-    for (int j = 0; j < Logits::MJ; ++j)
-        e.m_src[j] = (const char*)(h.p + r[j] * h.pitch + 8 * e.kc_chunk(e.kc_row(j, Logits::MJ)));
-#pragma unroll
-    for (int j = 0; j < Logits::WJ; ++j) {
-        const int row = e.kc_row(j, Logits::WJ);
-        const int64_t v = min(v0 + row, V - 1);
-        e.n_src[j] = (const char*)(W.p + v * W.pitch + 8 * e.kc_chunk(row));
-    }
+// Rows row0.. of h (`rows` in all) and v0.. of W (V) of a logits tile.
+template <typename E>
+__device__ __forceinline__ void logits_sources(E& e, const VocabOperand& h, const VocabOperand& W, int products, int K,
+                                               int64_t row0, int64_t rows, int64_t v0, int64_t V) {
+    e.m_base = (const char*)(h.p + row0 * h.pitch);
+    e.n_base = (const char*)(W.p + v0 * W.pitch);
+    e.m_rows((int)min(rows - row0, (int64_t)256), 2 * h.pitch);
+    e.n_rows((int)min(V - v0, (int64_t)256), 2 * W.pitch);
     e.m_plane = 2 * h.plane;
     e.n_plane = 2 * W.plane;
     e.steps = K / BK;
     e.ip = 6 - products;
     e.ik = 0;
     e.kt_total = e.steps * products;
+}
+
+// Of the 64 logits of a row that lanes l and l + 32 hold: the largest times c,
+// and the sum of 2^(z c - that).
+__device__ __forceinline__ float2 row_stats(const f32x16_t& x, const f32x16_t& y, float c) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) top = fmaxf(top, fmaxf(x[v], y[v]));
+    top = fmaxf(top, __shfl_xor(top, 32)) * c;
+    const float off = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) sum += __builtin_amdgcn_exp2f(fmaf(x[v], c, -off));
+#pragma unroll
+    for (int v = 0; v < 16; ++v) sum += __builtin_amdgcn_exp2f(fmaf(y[v], c, -off));
+    return make_float2(top, sum + __shfl_xor(sum, 32));
+}
+__device__ __forceinline__ float2 join_stats(const float2 (&p)[4]) {
+    const float top = fmaxf(fmaxf(p[0].x, p[1].x), fmaxf(p[2].x, p[3].x));
+    const float off = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) sum += p[w].y * __builtin_amdgcn_exp2f(p[w].x - off);
+    return make_float2(top, sum);
 }
 
 // Element v of acc[mi][nj] on lane l: row 32 nj + l % 32 of the tile, column
@@ -338,7 +379,7 @@ __global__ __launch_bounds__(256, 2) void vocab_stats_kernel(const VocabStats a,
     const int64_t row0 = (int64_t)mt * 128, v0 = (int64_t)nt * TN;
     Logits e;
     e.begin();
-    logits_sources(e, a.h, a.W, a.products, a.K, row0, rows, a.gather ? a.rows.rows : nullptr, v0, a.V);
+    logits_sources(e, a.h, a.W, a.products, a.K, row0, rows, v0, a.V);
     e.run(st0, st1, st2, nullptr);
 
     const int l = e.lane & 31, half = e.lane >> 5;
@@ -349,8 +390,7 @@ __global__ __launch_bounds__(256, 2) void vocab_stats_kernel(const VocabStats a,
         const int64_t row = row0 + 32 * nj + l;
         // the target's logit, where it is among this wavefront's 64 columns
         if (a.target) {
-            const int64_t t = row < rows ? (a.rows.rows ? a.rows.rows[row] : row) : 0;
-            const int64_t target = row < rows ? a.target[t] : -1;
+            const int64_t target = row < rows ? a.target[a.rows.rows ? a.rows.rows[row] : row] : -1;
             const bool mine = target >= v0 + 64 * e.fw && target < min(v0 + 64 * e.fw + 64, a.V);
             if (__ballot(mine)) {
                 const int at = mine ? (int)(target - v0) - 64 * e.fw - 4 * half : -1;
@@ -358,7 +398,7 @@ __global__ __launch_bounds__(256, 2) void vocab_stats_kernel(const VocabStats a,
                 for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
                     for (int v = 0; v < 16; ++v)
-                        if (at == 32 * mi + 8 * (v / 4) + v % 4) a.zt[t] = e.acc[mi][nj][v];
+                        if (at == 32 * mi + 8 * (v / 4) + v % 4) a.zt[row] = e.acc[mi][nj][v];
             }
         }
         if (left < TN) {
@@ -368,37 +408,16 @@ __global__ __launch_bounds__(256, 2) void vocab_stats_kernel(const VocabStats a,
                 for (int v = 0; v < 16; ++v)
                     if (64 * e.fw + 32 * mi + 8 * (v / 4) + 4 * half + v % 4 >= left) e.acc[mi][nj][v] = -INFINITY;
         }
-        float top = -INFINITY;
-#pragma unroll
-        for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) top = fmaxf(top, e.acc[mi][nj][v]);
-        top = fmaxf(top, __shfl_xor(top, 32));
-        top *= a.c;
-        const float off = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-#pragma unroll
-        for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) sum += __builtin_amdgcn_exp2f(fmaf(e.acc[mi][nj][v], a.c, -off));
-        sum += __shfl_xor(sum, 32);
-        if (half == 0) tile[e.fw * 128 + 32 * nj + l] = make_float2(top, sum);
+        const float2 s = row_stats(e.acc[0][nj], e.acc[1][nj], a.c);
+        if (half == 0) tile[e.fw * 128 + 32 * nj + l] = s;
     }
     __syncthreads();
     const int r = threadIdx.x;
     if (r < 128 && row0 + r < rows) {
         float2 p[4];
-        float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            p[w] = tile[w * 128 + r];
-            top = fmaxf(top, p[w].x);
-        }
-        const float off = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) sum += p[w].y * __builtin_amdgcn_exp2f(p[w].x - off);
-        a.part[nt * a.part_pitch + row0 + r] = make_float2(top, sum);
+        for (int w = 0; w < 4; ++w) p[w] = tile[w * 128 + r];
+        a.part[nt * a.part_pitch + row0 + r] = join_stats(p);
     }
 }
 
@@ -414,7 +433,7 @@ __global__ __launch_bounds__(256, 2) void vocab_dz_kernel(const VocabDz a, int n
     const int64_t row0 = (int64_t)mt * 128, c0 = (int64_t)nt * TN, v0 = a.v0 + c0;
     Logits e;
     e.begin();
-    logits_sources(e, a.h, a.W, a.products, a.K, row0, rows, nullptr, v0, a.V);
+    logits_sources(e, a.h, a.W, a.products, a.K, row0, rows, v0, a.V);
     const int l = e.lane & 31, half = e.lane >> 5;
     const int left = (int)min((int64_t)a.len - c0, (int64_t)TN);
     // the rows' values are on their way during the K loop
@@ -497,6 +516,217 @@ __global__ __launch_bounds__(256, 2) void vocab_dz_kernel(const VocabDz a, int n
             __builtin_nontemporal_store(*(const u32x4_t*)(orow(r) + ((c ^ (r & 15)) << 4)),
                                         (u32x4_t*)(out + (row0 + r) * a.dz_pitch));
         }
+    }
+}
+
+// ---- many rows: stats and dz on 256 x 256 tiles, one workgroup a CU that goes
+// through its tiles without a pause: the last steps of a tile load the next
+// one's first stages, which land under the epilogue.  What the epilogue wants of
+// a row (its g, lse and target) comes into LDS with a stage's loads.  K is a
+// multiple of 128: a tile begins and ends with the same stage buffer.  Against the
+// 128-row tiles each byte loaded feeds a third more products.
+using Whole = Engine<true, true, 256>;
+constexpr int kWholeUnits = 256;
+
+// Where dz's rows behind the last one go, so that every wavefront issues the
+// same number of stores whatever the tile holds.
+__device__ __attribute__((aligned(16))) u32x4_t row_trash[1];
+
+struct WholeArgs {
+    VocabOperand h, W;
+    VocabRows rows;
+    const float4* info;       // of compact rows: g / tau, lse, target (as bits)
+    int64_t V, v0;
+    int len, K, products;
+    float scale;              // stats: log2(e) / tau; dz: 1 / tau
+    float2* part;             // stats
+    int64_t part_pitch;
+    float* zt;                // stats, of compact rows
+    uint16_t* dz;
+    int64_t dz_pitch, dz_plane;
+};
+
+template <bool DZ, int PLANES>
+__global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, int n_tiles) {
+    __shared__ __attribute__((aligned(1024))) char st0[Whole::SBYTES];
+    __shared__ __attribute__((aligned(1024))) char st1[Whole::SBYTES];
+    __shared__ __attribute__((aligned(1024))) char st2[Whole::SBYTES];
+    __shared__ __attribute__((aligned(1024))) char st3[Whole::SBYTES];
+    __shared__ __attribute__((aligned(1024))) float4 infos[256];
+    __shared__ float2 sums[DZ ? 1 : 4][256];
+    const int64_t rows = a.rows.count ? *a.rows.count : a.rows.T;
+    const int m_tiles = (int)((rows + 255) / 256);
+    // an XCD takes a contiguous range of tiles, its workgroups every 32nd of it;
+    // 8 row tiles walk over the columns together
+    constexpr int kRows = 8;
+    const int total = m_tiles * n_tiles, xcd = blockIdx.x & 7;
+    const int base = xcd * (total >> 3) + min(xcd, total & 7), count = (total >> 3) + (xcd < (total & 7) ? 1 : 0);
+    int i = blockIdx.x >> 3;
+    if (i >= count) return;
+
+    Whole e;
+    e.begin();
+    int64_t row0, c0;
+    auto place = [&](int i) {
+        const int id = base + i, g = id / (kRows * n_tiles);
+        const int in = min(kRows, m_tiles - g * kRows), r = id - g * kRows * n_tiles;
+        const int nt = r / in;
+        row0 = (int64_t)(g * kRows + (r - nt * in)) * 256;
+        c0 = (int64_t)nt * TN;
+    };
+    auto sources = [&] { logits_sources(e, a.h, a.W, a.products, a.K, row0, rows, a.v0 + c0, a.V); };
+    place(i);
+    sources();
+    const int groups = e.steps * a.products / 4;
+    // vector memory operations behind a stage's loads: the next stage's, and
+    // right behind a tile's epilogue its stores
+    constexpr int usual = Whole::PER_STAGE, after = Whole::PER_STAGE + (DZ ? 16 * PLANES : 0);
+    auto ready = [] {
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(usual, 0));
+        __builtin_amdgcn_s_barrier();
+        Whole::fence();
+    };
+    auto ready_early = [](bool early) {
+        if (early) __builtin_amdgcn_s_waitcnt(waitcnt_imm(after, 0));
+        else __builtin_amdgcn_s_waitcnt(waitcnt_imm(usual, 0));
+        __builtin_amdgcn_s_barrier();
+        Whole::fence();
+    };
+
+    Whole::Frags fa, fb;
+    e.issue(st0);
+    e.issue(st1);
+    e.issue(st2);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+    __builtin_amdgcn_s_barrier();
+    Whole::fence();
+    e.read_frags(st0, fa);
+    Whole::fence();
+    for (;;) {
+        const int64_t tile_row = row0, tile_col = c0;
+        const bool more = i + 32 < count;
+        i += 32;
+        for (int g = 0; g < groups; ++g) {
+            ready_early(g == 0);
+            if (g == 0) {
+                // 64 rows a wavefront (twice over)
+                int r = 64 * (e.wave & 3), in = e.lane;
+                asm volatile("" : "+v"(in));       // made here, not kept over the K loop
+                in = min(in, (int)min(rows - 1 - tile_row - r, (int64_t)63));
+                load_lds16(a.info + tile_row + r + in, (char*)infos + 16 * r);
+            }
+            e.work(fa, fb, st1, st3);
+            // the next tile's sources, once this one's last stage is on its way
+            if (g + 1 == groups && more) {
+                place(i);
+                sources();
+            }
+            ready_early(g == 0);
+            e.work(fb, fa, st2, st0);
+            ready();
+            e.work(fa, fb, st3, st1);
+            ready();
+            e.work(fb, fa, st0, st2);
+        }
+
+        // ---- epilogue.  Element v of acc[mi][nj] on lane l: row 128 rw + 32 nj +
+        // l % 32, column 64 fw + 32 mi + 8 (v / 4) + 4 (l / 32) + v % 4.
+        int lane = e.lane;
+        asm volatile("" : "+v"(lane));     // what follows from it is not kept over the K loop
+        const int l = lane & 31, half = lane >> 5;
+        const int64_t v0 = a.v0 + tile_col;
+        const int left = (int)min(a.v0 + a.len - v0, (int64_t)TN) - 64 * e.fw - 4 * half;
+#pragma unroll
+        for (int nj = 0; nj < 4; ++nj) {
+            const int r = 128 * e.rw + 32 * nj + l;
+            const float4 in = infos[r];
+            const int64_t row = tile_row + r;
+            const int target = (int)__float_as_uint(in.z) - (int)v0 - 64 * e.fw - 4 * half;   // its column here
+            const bool mine = __float_as_int(in.z) >= 0 && target >= -4 && target < 64;
+            const bool any = __ballot(mine);
+            if constexpr (DZ) {
+#pragma unroll
+                for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        e.acc[mi][nj][v] =
+                            __builtin_amdgcn_exp2f(fmaf(e.acc[mi][nj][v], a.scale, -in.y) * 1.4426950408889634f);
+                if (any) {
+#pragma unroll
+                    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v)
+                            if (mine && target == 32 * mi + 8 * (v / 4) + v % 4) e.acc[mi][nj][v] -= 1.f;
+                }
+#pragma unroll
+                for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) e.acc[mi][nj][v] *= in.x;
+                if (left < 64) {
+#pragma unroll
+                    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v)
+                            if (32 * mi + 8 * (v / 4) + v % 4 >= left) e.acc[mi][nj][v] = 0.f;
+                }
+                uint16_t* out = a.dz + row * a.dz_pitch + tile_col + 64 * e.fw + 8 * half;
+#pragma unroll
+                for (int pl = 0; pl < PLANES; ++pl) {
+#pragma unroll
+                    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            f32x16_t& x = e.acc[mi][nj];
+                            uint32_t p[4];
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) {
+                                const int v = 8 * q + 2 * d;
+                                p[d] = pack_bf16(x[v], x[v + 1]);
+                                if (pl + 1 < PLANES) {
+                                    x[v] -= __uint_as_float(p[d] << 16);
+                                    x[v + 1] -= __uint_as_float(p[d] & 0xffff0000u);
+                                }
+                            }
+                            // 4 columns each of two groups of 8, from both lane halves -> 8 of one group a lane
+                            const auto s0 = __builtin_amdgcn_permlane32_swap(p[0], p[2], false, false);
+                            const auto s1 = __builtin_amdgcn_permlane32_swap(p[1], p[3], false, false);
+                            const u32x4_t v = {s0[0], s1[0], s0[1], s1[1]};
+                            *(row < rows ? (u32x4_t*)(out + pl * a.dz_plane + 32 * mi + 16 * q) : row_trash) = v;
+                        }
+                }
+            } else {
+                if (any && row < rows) {
+#pragma unroll
+                    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v)
+                            if (mine && target == 32 * mi + 8 * (v / 4) + v % 4) a.zt[row] = e.acc[mi][nj][v];
+                }
+                if (left < 64) {
+#pragma unroll
+                    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v)
+                            if (32 * mi + 8 * (v / 4) + v % 4 >= left) e.acc[mi][nj][v] = -INFINITY;
+                }
+                const float2 s = row_stats(e.acc[0][nj], e.acc[1][nj], a.scale);
+                if (half == 0) sums[e.fw][r] = s;
+            }
+        }
+        if constexpr (!DZ) {
+            // LDS alone is waited for: the next tile's stages stay in flight
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+            __builtin_amdgcn_s_barrier();
+            const int r = threadIdx.x;
+            if (r < 256 && tile_row + r < rows) {
+                float2 p[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) p[w] = sums[w][r];
+                a.part[tile_col / TN * a.part_pitch + tile_row + r] = join_stats(p);
+            }
+        }
+        if (!more) return;
+        e.clear();
     }
 }
 
@@ -592,30 +822,24 @@ __global__ __launch_bounds__(512, 1) void vocab_grad_kernel(const VocabGrad a) {
         const int64_t m0 = (int64_t)mt * 256;
 
         e.begin();
-        e.k_m = e.k_n = DW ? (int)rows : a.len;
         e.steps = w.steps;
         e.ip = 6 - a.products + (w.steps ? k0 / w.steps : 0);
         e.ik = w.steps ? k0 % w.steps : 0;
         e.kt_total = w.steps ? k1 - k0 : 0;
         e.m_plane = 2 * a.m.plane;
         e.n_plane = 2 * a.n.plane;
-        e.m_pitch = 2 * a.m.pitch;
-        e.n_pitch = 2 * a.n.pitch;
-#pragma unroll
-        for (int j = 0; j < Eng::MJ; ++j) {
-            if constexpr (DW) {
-                e.m_src[j] = (const char*)(a.m.p + m0 + 8 * e.ks_chunk(e.ks_row(j, Eng::MJ)));   // dz's rows are whole tiles
-            } else {
-                const int row = e.kc_row(j, Eng::MJ);
-                e.m_src[j] = (const char*)(a.m.p + min(m0 + row, M - 1) * a.m.pitch + 8 * e.kc_chunk(row));
-            }
+        const int last = ((DW ? (int)rows : a.len) - 1) % BK + 1;
+        if constexpr (DW) {
+            e.m_base = (const char*)(a.m.p + m0);      // dz's rows are whole tiles
+            e.m_ks(last, 2 * a.m.pitch);
+        } else {
+            e.m_base = (const char*)(a.m.p + m0 * a.m.pitch);
+            e.m_rows((int)min(M - m0, (int64_t)256), 2 * a.m.pitch);
         }
-#pragma unroll
-        for (int j = 0; j < Eng::WJ; ++j) {
-            int n = nt * TN + 8 * e.ks_chunk(e.ks_row(j, Eng::WJ));
-            if (n >= a.n.pitch) n = 0;       // an address that exists; its sums are never stored
-            e.n_src[j] = (const char*)(a.n.p + n);
-        }
+        // k rows past the last: zeros behind h (dW), any of the table's against
+        // dz's zeros (dh)
+        e.n_base = (const char*)(a.n.p + nt * TN);
+        e.n_ks(DW ? BK : last, 2 * a.n.pitch, (int)a.n.pitch - nt * TN);
         e.run(st0, st1, st2, st3);
 
         // Through LDS in two passes of 128 rows (those of the wavefronts rw =
@@ -704,6 +928,25 @@ hipError_t launch_vocab_dz(const VocabDz& a, hipStream_t s) {
     if (tiles > kMaxTiles) return hipErrorInvalidValue;
     if (a.products == 1) vocab_dz_kernel<1><<<grid_for_work(tiles), 256, 0, s>>>(a, n_tiles);
     else vocab_dz_kernel<3><<<grid_for_work(tiles), 256, 0, s>>>(a, n_tiles);
+    return hipGetLastError();
+}
+
+hipError_t launch_vocab_stats_whole(const VocabStats& a, const float4* info, hipStream_t s) {
+    if (a.K <= 0 || a.K % (4 * BK) || (a.products != 1 && a.products != 6) || a.rows.T <= 0 || a.V <= 0 || !info) return hipErrorInvalidValue;
+    const int64_t n_tiles = (a.V + TN - 1) / TN;
+    if ((a.rows.T + 255) / 256 * n_tiles > kMaxTiles) return hipErrorInvalidValue;
+    const WholeArgs w = {a.h, a.W, a.rows, info, a.V, 0, (int)a.V, a.K, a.products, a.c, a.part, a.part_pitch, a.zt, nullptr, 0, 0};
+    vocab_whole_kernel<false, 1><<<kWholeUnits, 512, 0, s>>>(w, (int)n_tiles);
+    return hipGetLastError();
+}
+
+hipError_t launch_vocab_dz_whole(const VocabDz& a, const float4* info, hipStream_t s) {
+    if (a.K <= 0 || a.K % (4 * BK) || (a.products != 1 && a.products != 6) || a.rows.T <= 0 || a.len <= 0 || !info) return hipErrorInvalidValue;
+    const int64_t n_tiles = ((int64_t)a.len + TN - 1) / TN;
+    if (n_tiles * TN > a.dz_pitch || (a.rows.T + 255) / 256 * n_tiles > kMaxTiles) return hipErrorInvalidValue;
+    const WholeArgs w = {a.h, a.W, a.rows, info, a.V, a.v0, a.len, a.K, a.products, a.inv_tau, nullptr, 0, nullptr, a.dz, a.dz_pitch, a.dz_plane};
+    if (a.products == 1) vocab_whole_kernel<true, 1><<<kWholeUnits, 512, 0, s>>>(w, (int)n_tiles);
+    else vocab_whole_kernel<true, 3><<<kWholeUnits, 512, 0, s>>>(w, (int)n_tiles);
     return hipGetLastError();
 }
 

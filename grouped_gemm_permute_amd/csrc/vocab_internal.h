@@ -29,11 +29,10 @@ constexpr int kVocabTileCols = 256;   // entries of the vocabulary of a logits t
 
 // z = h W^T by tiles; per tile and row the largest z c and the sum of
 // 2^(z c - largest), to part[tile][row] (row pitch `part_pitch`); z of a
-// row's target to zt.  c = log2(e) / temperature.
+// row's target to zt.  Rows of h, part and zt are compact.  c = log2(e) / temperature.
 struct VocabStats {
     VocabOperand h, W;
     VocabRows rows;
-    bool gather;              // h's rows are found through rows.rows (else h is compact)
     int64_t V;
     int K;                    // a multiple of 32
     int products;             // 1, or 6 products of three planes
@@ -41,7 +40,7 @@ struct VocabStats {
     float2* part;
     int64_t part_pitch;
     const int32_t* target;    // [T] or null
-    float* zt;                // [T]
+    float* zt;
 };
 hipError_t launch_vocab_stats(const VocabStats& a, hipStream_t s);
 
@@ -64,6 +63,11 @@ struct VocabDz {
 };
 hipError_t launch_vocab_dz(const VocabDz& a, hipStream_t s);
 
+// The same for many rows; info: of compact rows g / tau, lse and the target's
+// bits (negative: none), instead of g, lse and target.  K a multiple of 128.
+hipError_t launch_vocab_stats_whole(const VocabStats& a, const float4* info, hipStream_t s);
+hipError_t launch_vocab_dz_whole(const VocabDz& a, const float4* info, hipStream_t s);
+
 // C[m][n] = sum over k of M and N operands:
 //   dh (dW = false): m = compact row, k = entry of the piece, n = column of D
 //   dW (dW = true):  m = entry of the piece, k = compact row, n = column of D
@@ -72,7 +76,7 @@ hipError_t launch_vocab_dz(const VocabDz& a, hipStream_t s);
 // Two launches: the tiles, and the sums of those that several workgroups made.
 struct VocabGrad {
     bool dW;
-    VocabOperand m, n;
+    VocabOperand m, n;        // dh: dz, the table; dW: dz, h with zeros up to the next 32nd row
     VocabRows rows;
     int len;                  // entries of the piece
     int N;                    // columns of D

@@ -154,19 +154,27 @@ struct CopyArgs {
     int64_t plane;
     const int32_t* pos;
     Targets targets;          // rows that count (pos null); target and ids null: all
+    const int32_t* count;     // rows in the copy (with pos)
     const float *g, *lse;     // [T], or null
     float inv_tau;
     float *g_out, *lse_out;
+    float4* info;             // g / tau, lse and the target's bits, or null
     void* dh;                 // or null
 };
 
 template <typename E>
 __global__ __launch_bounds__(256) void vocab_copy_kernel(const CopyArgs a) {
     const int lane = threadIdx.x & 63;
-    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.T; t += (int64_t)gridDim.x * 4) {
+    // behind the last row zeros up to the next multiple of 32
+    const int64_t n = a.count ? *a.count : a.T, end = (n + 31) / 32 * 32;
+    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.T + 32; t += (int64_t)gridDim.x * 4) {
         int64_t to = t;
         bool live = true;
-        if (a.pos) {
+        if (t >= a.T) {
+            to = n + (t - a.T);
+            live = false;
+            if (to >= end) break;
+        } else if (a.pos) {
             to = a.pos[t];
             live = to >= 0;
             if (!live) {
@@ -184,9 +192,16 @@ __global__ __launch_bounds__(256) void vocab_copy_kernel(const CopyArgs a) {
                 live = __ballot(any) != 0;
             }
         }
-        if (a.g && lane == 0) {
-            a.g_out[to] = live ? a.g[t] * a.inv_tau : 0.f;
-            a.lse_out[to] = live ? a.lse[t] : INFINITY;
+        if (lane == 0 && t < a.T && (a.g || a.info)) {
+            const float g = a.g && live ? a.g[t] * a.inv_tau : 0.f, lse = a.lse && live ? a.lse[t] : INFINITY;
+            if (a.info) {
+                const int target = a.targets.target && live ? a.targets.target[t] : -1;
+                a.info[to] = make_float4(g, lse, __int_as_float(target), 0.f);
+            }
+            if (a.g_out) {
+                a.g_out[to] = g;
+                a.lse_out[to] = lse;
+            }
         }
         const E* src = (const E*)a.src + t * a.D;
         uint16_t* dst = a.dst + to * a.Dp;
@@ -240,7 +255,7 @@ struct FinishArgs {
     VocabRows rows;
     Targets targets;
     float c;
-    const float* zt;          // cross entropy: the targets' logits, or null
+    const float* zt;          // cross entropy: the targets' logits
     float *loss, *lse;        // [T]; loss null: lse alone
 };
 
@@ -273,7 +288,7 @@ __global__ __launch_bounds__(256) void vocab_finish_kernel(const FinishArgs a) {
     const float l = __builtin_amdgcn_logf(s);       // log2
     a.lse[t] = live ? (off + l) * kLn2 : 0.f;
     // the two large terms first: their difference is exact where the target leads
-    if (a.loss) a.loss[t] = live ? (l + (off - a.zt[t] * a.c)) * kLn2 : 0.f;
+    if (a.loss) a.loss[t] = live ? (l + (off - a.zt[i] * a.c)) * kLn2 : 0.f;
 }
 
 // A teacher's row in LDS: q and log q of its K entries (0 for those that do not
@@ -432,11 +447,12 @@ __global__ __launch_bounds__(256) void vocab_zero_kernel(O* p, int64_t n) {
 
 struct Plan {
     bool list;                // rows that count are listed first
+    bool whole;               // logits by 256 x 256 tiles
     bool copy_W, copy_h;      // operands as padded bf16 planes
     int planes, products, Dp;
     int64_t n_tiles;          // stats: column tiles
     int64_t piece, pieces;    // entries of a piece (a multiple of 256), and how many
-    size_t rows, pos, count, live, hc, Wc, part, zt, g, lse, dz, acc, total;
+    size_t rows, pos, count, live, hc, info, Wc, part, zt, g, lse, dz, acc, total;
 };
 
 Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
@@ -444,10 +460,13 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     p.list = T >= kListRows;
     p.planes = dtype == MOE_BF16 ? 1 : 3;
     p.products = dtype == MOE_BF16 ? 1 : 6;
-    p.Dp = (D + 31) / 32 * 32;
     // bf16 rows of whole K steps are read where they are
-    p.copy_W = dtype != MOE_BF16 || p.Dp != D;
-    p.copy_h = p.copy_W || backward;
+    p.copy_W = dtype != MOE_BF16 || D % 32 != 0;
+    p.copy_h = p.copy_W || p.list || backward;
+    // what is copied is padded to what the tiles of many rows take
+    const int unit = p.copy_W && p.list ? 128 : 32;
+    p.Dp = (D + unit - 1) / unit * unit;
+    p.whole = p.list && p.Dp % 128 == 0;
     p.n_tiles = ((int64_t)V + kVocabTileCols - 1) / kVocabTileCols;
     size_t at = 0;
     auto take = [&](bool want, size_t bytes) {
@@ -459,8 +478,9 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     p.pos = take(p.list, (size_t)T * 4);
     p.count = take(p.list, 4);
     p.live = take(p.list && K > 0, (size_t)T * 4);
-    p.hc = take(p.copy_h, (size_t)p.planes * T * p.Dp * 2);
-    p.Wc = take(p.copy_W, (size_t)p.planes * V * p.Dp * 2);
+    p.hc = take(p.copy_h, (size_t)p.planes * (T + 32) * p.Dp * 2);
+    p.info = take(p.whole, (size_t)T * 16);
+    p.Wc = take(p.copy_W, (size_t)p.planes * (V + 32ll) * p.Dp * 2);
     if (!backward) {
         p.part = take(true, (size_t)p.n_tiles * T * 8);
         p.zt = take(K == 0, (size_t)T * 4);
@@ -505,7 +525,7 @@ moe_status check(const Call& a) {
     } while (0)
 
 hipError_t copy_rows(const CopyArgs& a, moe_dtype dtype, hipStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>((a.T + 3) / 4, 8192);
+    const unsigned grid = (unsigned)std::min<int64_t>((a.T + 32 + 3) / 4, 8192);
     if (dtype == MOE_BF16) vocab_copy_kernel<uint16_t><<<grid, 256, 0, s>>>(a);
     else vocab_copy_kernel<float><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
@@ -530,7 +550,7 @@ moe_status begin(const Call& a, const Plan& p, char* ws, VocabRows* rows, VocabO
     *W = {(const uint16_t*)a.W, a.D, 0};
     if (p.copy_W) {
         uint16_t* to = (uint16_t*)(ws + p.Wc);
-        *W = {to, p.Dp, (int64_t)a.targets.V * p.Dp};
+        *W = {to, p.Dp, (a.targets.V + 32ll) * p.Dp};
         CopyArgs c = {a.W, a.targets.V, a.D, p.Dp, to, W->plane};
         TRY(copy_rows(c, a.dtype, s));
     }
@@ -549,15 +569,16 @@ moe_status forward(const Call& a, float* loss, float* lse, float* z, void* works
     if (const moe_status st = begin(a, p, ws, &rows, &W, lse, a.targets.target ? loss : nullptr, s)) return st;
     if (p.copy_h) {
         uint16_t* to = (uint16_t*)(ws + p.hc);
-        h = {to, p.Dp, a.T * p.Dp};
+        h = {to, p.Dp, (a.T + 32) * p.Dp};
         CopyArgs c = {a.h, a.T, a.D, p.Dp, to, h.plane};
-        c.pos = p.list ? (const int32_t*)(ws + p.pos) : nullptr;
+        if (p.list) c.pos = (const int32_t*)(ws + p.pos), c.count = rows.count;
+        if (p.whole) c.targets = a.targets, c.info = (float4*)(ws + p.info);
         TRY(copy_rows(c, a.dtype, s));
     }
     const float inv_tau = 1.f / a.tau;
-    VocabStats st = {h, W, rows, p.list && !p.copy_h, a.targets.V, p.Dp, p.products, kLog2E * inv_tau,
+    VocabStats st = {h, W, rows, a.targets.V, p.Dp, p.products, kLog2E * inv_tau,
                      (float2*)(ws + p.part), a.T, a.targets.target, (float*)(ws + p.zt)};
-    TRY(launch_vocab_stats(st, s));
+    TRY(p.whole ? launch_vocab_stats_whole(st, (const float4*)(ws + p.info), s) : launch_vocab_stats(st, s));
     FinishArgs f = {st.part, a.T, (int)p.n_tiles, rows, a.targets, st.c, st.zt, a.targets.target ? loss : nullptr, lse};
     vocab_finish_kernel<<<(unsigned)((a.T + 15) / 16), 256, 0, s>>>(f);
     TRY(hipGetLastError());
@@ -599,10 +620,11 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
     if (const moe_status st = begin(a, p, ws, &rows, &W, nullptr, nullptr, s)) return st;
     const float inv_tau = 1.f / a.tau;
     float *g = (float*)(ws + p.g), *l = (float*)(ws + p.lse);
-    VocabOperand h = {(const uint16_t*)(ws + p.hc), p.Dp, a.T * p.Dp};
+    VocabOperand h = {(const uint16_t*)(ws + p.hc), p.Dp, (a.T + 32) * p.Dp};
     {
         CopyArgs c = {a.h, a.T, a.D, p.Dp, (uint16_t*)(ws + p.hc), h.plane};
-        c.pos = p.list ? (const int32_t*)(ws + p.pos) : nullptr;
+        if (p.list) c.pos = (const int32_t*)(ws + p.pos), c.count = rows.count;
+        if (p.whole) c.info = (float4*)(ws + p.info);
         c.targets = a.targets;
         c.g = dloss, c.lse = lse, c.inv_tau = inv_tau, c.g_out = g, c.lse_out = l;
         c.dh = dh;
@@ -614,7 +636,7 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
         const int len = (int)std::min<int64_t>(p.piece, V - v0);
         VocabDz d = {h, W, rows, V, v0, len, p.Dp, p.products, inv_tau, g, l, a.targets.target, dz, p.piece, dz_plane};
-        TRY(launch_vocab_dz(d, s));
+        TRY(p.whole ? launch_vocab_dz_whole(d, (const float4*)(ws + p.info), s) : launch_vocab_dz(d, s));
         if (!a.targets.target) {
             TeacherArgs t = {a.targets, rows, z, g, l, inv_tau, v0, len, dz, p.piece, dz_plane, p.planes};
             vocab_teacher_kernel<<<(unsigned)a.T, 64, 0, s>>>(t);
