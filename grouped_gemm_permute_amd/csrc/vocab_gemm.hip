@@ -53,6 +53,14 @@ __device__ __forceinline__ int swz_kc(int row) { return (row >> 2) & 3; }
 constexpr int kPlaneM = 1 | 2 << 2 | 0 << 4 | 1 << 6 | 0 << 8 | 0 << 10;
 constexpr int kPlaneN = 1 | 0 << 2 | 2 << 4 | 0 << 6 | 1 << 8 | 0 << 10;
 
+// The lane's number, made where it stands: kept in a register over a K loop it,
+// and what follows from it, would be one too many.
+__device__ __forceinline__ int fresh_lane() {
+    int z = 0;
+    asm volatile("" : "+v"(z));
+    return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, z));
+}
+
 // The K loop of one tile.  MC / NC: the M / N operand's rows are contiguous in
 // K; else its rows are k and the tile's 256 columns are contiguous.
 template <bool MC, bool NC, int ROWS>
@@ -574,7 +582,10 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
         row0 = (int64_t)(g * kRows + (r - nt * in)) * 256;
         c0 = (int64_t)nt * TN;
     };
-    auto sources = [&] { logits_sources(e, a.h, a.W, a.products, a.K, row0, rows, a.v0 + c0, a.V); };
+    auto sources = [&] {
+        e.lane = fresh_lane();
+        logits_sources(e, a.h, a.W, a.products, a.K, row0, rows, a.v0 + c0, a.V);
+    };
     place(i);
     sources();
     const int groups = e.steps * a.products / 4;
@@ -610,9 +621,8 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
             ready_early(g == 0);
             if (g == 0) {
                 // 64 rows a wavefront (twice over)
-                int r = 64 * (e.wave & 3), in = e.lane;
-                asm volatile("" : "+v"(in));       // made here, not kept over the K loop
-                in = min(in, (int)min(rows - 1 - tile_row - r, (int64_t)63));
+                const int r = 64 * (e.wave & 3);
+                const int in = min(fresh_lane(), (int)min(rows - 1 - tile_row - r, (int64_t)63));
                 load_lds16(a.info + tile_row + r + in, (char*)infos + 16 * r);
             }
             e.work(fa, fb, st1, st3);
@@ -631,8 +641,7 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
 
         // ---- epilogue.  Element v of acc[mi][nj] on lane l: row 128 rw + 32 nj +
         // l % 32, column 64 fw + 32 mi + 8 (v / 4) + 4 (l / 32) + v % 4.
-        int lane = e.lane;
-        asm volatile("" : "+v"(lane));     // what follows from it is not kept over the K loop
+        const int lane = fresh_lane();
         const int l = lane & 31, half = lane >> 5;
         const int64_t v0 = a.v0 + tile_col;
         const int left = (int)min(a.v0 + a.len - v0, (int64_t)TN) - 64 * e.fw - 4 * half;
@@ -669,30 +678,37 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
                         for (int v = 0; v < 16; ++v)
                             if (32 * mi + 8 * (v / 4) + v % 4 >= left) e.acc[mi][nj][v] = 0.f;
                 }
-                uint16_t* out = a.dz + row * a.dz_pitch + tile_col + 64 * e.fw + 8 * half;
+                // Through LDS, 32 rows of 128 bytes of the wavefront's own at a
+                // time (16-byte chunks XOR-swizzled by the row), so that a store
+                // writes whole lines; the buffer is free: its next stage comes
+                // behind the next barrier.
+                char* own = st3 + 4096 * e.wave;
+                const int sr = lane >> 3, sc = lane & 7;
+                uint16_t* out = a.dz + (tile_row + 128 * e.rw + 32 * nj + sr) * a.dz_pitch + tile_col + 64 * e.fw + 8 * sc;
+                const int64_t behind = rows - (tile_row + 128 * e.rw + 32 * nj + sr);
 #pragma unroll
                 for (int pl = 0; pl < PLANES; ++pl) {
 #pragma unroll
                     for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
+                        for (int vg = 0; vg < 4; ++vg) {
                             f32x16_t& x = e.acc[mi][nj];
-                            uint32_t p[4];
-#pragma unroll
-                            for (int d = 0; d < 4; ++d) {
-                                const int v = 8 * q + 2 * d;
-                                p[d] = pack_bf16(x[v], x[v + 1]);
-                                if (pl + 1 < PLANES) {
-                                    x[v] -= __uint_as_float(p[d] << 16);
-                                    x[v + 1] -= __uint_as_float(p[d] & 0xffff0000u);
-                                }
+                            const uint32_t lo = pack_bf16(x[4 * vg], x[4 * vg + 1]), hi = pack_bf16(x[4 * vg + 2], x[4 * vg + 3]);
+                            *(uint2*)(own + l * 128 + (((4 * mi + vg) ^ (l & 7)) << 4) + 8 * half) = make_uint2(lo, hi);
+                            if (pl + 1 < PLANES) {
+                                x[4 * vg] -= __uint_as_float(lo << 16);
+                                x[4 * vg + 1] -= __uint_as_float(lo & 0xffff0000u);
+                                x[4 * vg + 2] -= __uint_as_float(hi << 16);
+                                x[4 * vg + 3] -= __uint_as_float(hi & 0xffff0000u);
                             }
-                            // 4 columns each of two groups of 8, from both lane halves -> 8 of one group a lane
-                            const auto s0 = __builtin_amdgcn_permlane32_swap(p[0], p[2], false, false);
-                            const auto s1 = __builtin_amdgcn_permlane32_swap(p[1], p[3], false, false);
-                            const u32x4_t v = {s0[0], s1[0], s0[1], s1[1]};
-                            *(row < rows ? (u32x4_t*)(out + pl * a.dz_plane + 32 * mi + 16 * q) : row_trash) = v;
                         }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const u32x4_t v = *(const u32x4_t*)(own + (8 * q + sr) * 128 + ((sc ^ sr) << 4));
+                        // non-temporal: the tiles keep their L2 (1% of the whole backward)
+                        __builtin_nontemporal_store(
+                            v, 8 * q < behind ? (u32x4_t*)(out + pl * a.dz_plane + 8 * q * a.dz_pitch) : row_trash);
+                    }
                 }
             } else {
                 if (any && row < rows) {
@@ -717,7 +733,7 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
             // LDS alone is waited for: the next tile's stages stay in flight
             __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
             __builtin_amdgcn_s_barrier();
-            const int r = threadIdx.x;
+            const int r = 64 * e.wave + lane;
             if (r < 256 && tile_row + r < rows) {
                 float2 p[4];
 #pragma unroll
