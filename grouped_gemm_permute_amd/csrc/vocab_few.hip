@@ -1,0 +1,523 @@
+// vocab_few.hip -- the products of the losses over a vocabulary for few rows
+// (a decoding step's tokens, small chunks), where reading the table is all
+// the work:
+//
+//  logits:  z = h W^T for 128 entries and 32 or 64 rows a workgroup, and from it
+//           the tile's largest value and sum, or dz (as in vocab_gemm.hip)
+//  dh:      dz W for 256 columns and a part of the entries a workgroup, and the
+//           sum of the parts
+//  dW:      dz^T h, 64 entries x 256 columns a workgroup: a few steps of K, then
+//           the store, which is all of the time; several workgroups a CU
+//
+// The table is read once, in its own type: bf16 on the bf16 matrix
+// instructions, fp32 on the fp32 ones (a sixteenth of the rate, which 64 rows
+// still do not need), with no copy in planes.  Four wavefronts, each with its
+// own 32 entries (64 columns), a ring of 16 KiB stages of the table and the few
+// rows beside it, filled by 16-byte DMA; two workgroups a CU keep 64 to 96 KiB a CU
+// on their way.
+#include "mfma_common.h"
+#include "vocab_internal.h"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+using namespace mfma;
+
+constexpr int FN = kVocabFewCols;     // 128 entries of a logits tile
+constexpr int N_BYTES = 16384;        // of a stage, either product
+
+// What a row's bytes past its end are read as.
+__device__ __attribute__((aligned(16))) u32x4_t few_zeros[1];
+
+template <bool F32>
+struct Elem {
+    typedef uint16_t type;
+};
+template <>
+struct Elem<true> {
+    typedef float type;
+};
+
+// acc += the 32 x 32 product of 16 bytes a lane of each operand: lane l holds
+// row l % 32 and, of 8 (fp32) or 16 (bf16) k, those of its half.
+template <bool F32>
+__device__ __forceinline__ f32x16_t multiply(u32x4_t n, u32x4_t m, f32x16_t acc) {
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(n[i]), __uint_as_float(m[i]), acc, 0, 0, 0);
+        return acc;
+    } else {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, n), __builtin_bit_cast(bf16x8_t, m),
+                                                       acc, 0, 0, 0);
+    }
+}
+
+// Steps of a ring of NS stages: before step s its stage has landed, and the stage
+// NS - 1 on is issued into the buffer that step s - 1 read.  PER: a wavefront's
+// loads a stage.  `issue(s, buffer)` may be asked for stages past the last.
+template <int NS, int PER, typename I, typename W>
+__device__ __forceinline__ void ring(int steps, char* const (&st)[NS], I&& issue, W&& work) {
+    if (steps <= 0) return;
+#pragma unroll
+    for (int u = 0; u + 1 < NS; ++u) issue(u, st[u]);
+    for (int s = 0; s < steps; s += NS) {
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+            if (s + u >= steps) break;
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 2) * PER, 0));
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            issue(s + u + NS - 1, st[(u + NS - 1) % NS]);
+            work(st[u]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+    __syncthreads();
+}
+
+// RB: blocks of 32 rows.
+template <bool F32, int RB, bool DZ>
+__global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew a, int m_tiles) {
+    using E = typename Elem<F32>::type;
+    constexpr int NS = RB == 1 ? 4 : 3, PER = 4 + RB, SB = N_BYTES + RB * 4096;
+    __shared__ __attribute__((aligned(1024))) char st0[SB];
+    __shared__ __attribute__((aligned(1024))) char st1[SB];
+    __shared__ __attribute__((aligned(1024))) char st2[SB];
+    __shared__ __attribute__((aligned(1024))) char st3[NS == 4 ? SB : 16];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // row tiles of the same entries next to each other
+    const int64_t row0 = (int64_t)(blockIdx.x % m_tiles) * (32 * RB), v0 = (int64_t)(blockIdx.x / m_tiles) * FN;
+    const int64_t bytes = a.D * (int64_t)sizeof(E);          // of a row, a multiple of 16
+    const int steps = (int)((bytes + 127) / 128);
+
+    // DMA instruction: 8 rows of 128 bytes; lane -> row lane / 8, physical
+    // chunk lane % 8 holding logical chunk (lane % 8) ^ swz8(row)
+    const char* n_src[4];
+    const char* m_src[RB];
+    int n_c[4], m_c[RB];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = 32 * wave + 8 * j + (lane >> 3);
+        n_c[j] = 16 * ((lane & 7) ^ swz8(r));
+        n_src[j] = (const char*)a.W + min(v0 + r, (int64_t)a.V - 1) * bytes + n_c[j];
+    }
+#pragma unroll
+    for (int j = 0; j < RB; ++j) {
+        const int r = 8 * (RB * wave + j) + (lane >> 3);
+        m_c[j] = 16 * ((lane & 7) ^ swz8(r));
+        m_src[j] = (const char*)a.h + min(row0 + r, a.T - 1) * a.h_pitch * (int64_t)sizeof(E) + m_c[j];
+    }
+    auto issue = [&](int s, char* st) {
+        const int64_t k = (int64_t)min(s, steps - 1) * 128;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            load_lds16(k + n_c[j] < bytes ? n_src[j] + k : (const char*)few_zeros, st + (4 * wave + j) * 1024);
+#pragma unroll
+        for (int j = 0; j < RB; ++j)
+            load_lds16(k + m_c[j] < bytes ? m_src[j] + k : (const char*)few_zeros, st + N_BYTES + (RB * wave + j) * 1024);
+    };
+    const int l = lane & 31, half = lane >> 5;
+    f32x16_t acc[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) acc[rb] = f32x16_t{};
+    auto work = [&](const char* st) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const u32x4_t n = *(const u32x4_t*)(st + (32 * wave + l) * 128 + (((2 * i + half) ^ swz8(32 * wave + l)) << 4));
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+                const u32x4_t m = *(const u32x4_t*)(st + N_BYTES + (32 * rb + l) * 128 + (((2 * i + half) ^ swz8(32 * rb + l)) << 4));
+                acc[rb] = multiply<F32>(n, m, acc[rb]);
+            }
+        }
+    };
+    if constexpr (NS == 4) {
+        char* const st[4] = {st0, st1, st2, st3};
+        ring<4, PER>(steps, st, issue, work);
+    } else {
+        char* const st[3] = {st0, st1, st2};
+        ring<3, PER>(steps, st, issue, work);
+    }
+
+    // element v of acc on lane l: row l % 32, entry v0 + 32 w + 8 (v / 4) + 4 (l / 32) + v % 4
+    const int64_t c0 = v0 + 32 * wave + 4 * half;
+    const int left = (int)min((int64_t)a.V - c0, (int64_t)32);
+    float2* sums = (float2*)st0;                              // [4][32 RB]
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int64_t row = row0 + 32 * rb + l;
+        const bool there = row < a.T;
+        const int64_t target = there && a.target ? a.target[row] : -1;
+        const int at = target >= c0 && target < c0 + 32 && target < a.V ? (int)(target - c0) : -1;
+        if constexpr (!DZ) {
+            if (__ballot(at >= 0)) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    if (at == 8 * (v / 4) + v % 4) a.zt[row] = acc[rb][v];
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                if (8 * (v / 4) + v % 4 >= left) acc[rb][v] = -INFINITY;
+                top = fmaxf(top, acc[rb][v]);
+            }
+            top = fmaxf(top, __shfl_xor(top, 32)) * a.scale;
+            const float off = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) sum += __builtin_amdgcn_exp2f(fmaf(acc[rb][v], a.scale, -off));
+            sum += __shfl_xor(sum, 32);
+            if (half == 0) sums[wave * 32 * RB + 32 * rb + l] = make_float2(top, sum);
+        } else {
+            if (!there) continue;
+            const float lse = a.lse[row], g = a.g[row];
+#pragma unroll
+            for (int vg = 0; vg < 4; ++vg) {
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float p = __builtin_amdgcn_exp2f(fmaf(acc[rb][4 * vg + i], a.scale, -lse) * 1.4426950408889634f);
+                    if (at == 8 * vg + i) p -= 1.f;
+                    // a row that does not count has an infinite lse: zeros, whatever h holds
+                    x[i] = 8 * vg + i >= left || lse == INFINITY ? 0.f : p * g;
+                }
+                if constexpr (F32) *(float4*)(a.dz32 + row * a.dz_pitch + c0 + 8 * vg) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+                for (int pl = 0; pl < (F32 ? 3 : 1); ++pl) {
+                    const uint32_t lo = pack_bf16(x[0], x[1]), hi = pack_bf16(x[2], x[3]);
+                    *(uint2*)(a.dz + pl * a.dz_plane + row * a.dz_pitch + c0 + 8 * vg) = make_uint2(lo, hi);
+                    x[0] -= __uint_as_float(lo << 16);
+                    x[1] -= __uint_as_float(lo & 0xffff0000u);
+                    x[2] -= __uint_as_float(hi << 16);
+                    x[3] -= __uint_as_float(hi & 0xffff0000u);
+                }
+            }
+        }
+    }
+    if constexpr (!DZ) {
+        __syncthreads();
+        if (tid < 32 * RB && row0 + tid < a.T) {
+            float top = -INFINITY, sum = 0.f;
+            float2 p[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                p[w] = sums[w * 32 * RB + tid];
+                top = fmaxf(top, p[w].x);
+            }
+            const float off = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) sum += p[w].y * __builtin_amdgcn_exp2f(p[w].x - off);
+            a.part[v0 / FN * a.part_pitch + row0 + tid] = make_float2(top, sum);
+        }
+    }
+}
+
+// dh's parts: columns 256 of a tile, K: entries, 32 (bf16) or 16 (fp32) a step.
+template <bool F32, int RB>
+__global__ __launch_bounds__(256, 2) void vocab_few_dh_kernel(const VocabFew a, int n_tiles, int m_tiles, int splits) {
+    using E = typename Elem<F32>::type;
+    constexpr int NS = 4, PER = 5, KS = F32 ? 16 : 32, RPI = F32 ? 1 : 2;   // k rows of a DMA instruction
+    constexpr int ROW = 256 * sizeof(E), SB = N_BYTES + 4096;
+    __shared__ __attribute__((aligned(1024))) char st0[SB];
+    __shared__ __attribute__((aligned(1024))) char st1[SB];
+    __shared__ __attribute__((aligned(1024))) char st2[SB];
+    __shared__ __attribute__((aligned(1024))) char st3[SB];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int mt = blockIdx.x % m_tiles, rest = blockIdx.x / m_tiles;
+    const int nt = rest % n_tiles, split = rest / n_tiles;
+    const int64_t row0 = (int64_t)mt * (32 * RB);
+    const int all = (a.V + KS - 1) / KS, per = (all + splits - 1) / splits;
+    const int first = min(split * per, all), steps = min(per, all - first);
+
+    // the table: instruction j of wavefront w fills k rows RPI (4 w + j)..; 16-byte
+    // chunks swizzled so that neither the transposing reads (bf16) nor lanes l and
+    // l + 32, four k rows apart (fp32), meet in a bank
+    auto swz = [](int k) { return F32 ? 8 * ((k >> 2) & 1) : swz_tr(k); };
+    constexpr int CPR = ROW / 16;                            // chunks of a k row: 64 or 32
+    int n_k[4];
+    int64_t n_c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        n_k[j] = RPI * (4 * wave + j) + lane / CPR;
+        const int c = nt * 256 + ((lane % CPR) ^ swz(n_k[j])) * (16 / (int)sizeof(E));
+        n_c[j] = c < a.D ? c : 0;                            // a column that exists; its sums are not stored
+    }
+    // dz: 16 rows of 64 bytes an instruction, one a wavefront (with one block of
+    // rows twice over)
+    const int mr = 16 * (RB == 1 ? wave & 1 : wave) + (lane >> 2);
+    const int mc = (lane & 3) ^ ((mr >> 2) & 3);
+    const char* m_src = (F32 ? (const char*)a.dz32 : (const char*)a.dz) +
+                        (min(row0 + mr, a.T - 1) * a.dz_pitch * (int64_t)sizeof(E) + 16 * mc);
+    auto issue = [&](int s, char* st) {
+        const int64_t k = (int64_t)(first + min(s, steps - 1)) * KS;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            load_lds16((const E*)a.W + min(k + n_k[j], (int64_t)a.V - 1) * a.D + n_c[j], st + (4 * wave + j) * 1024);
+        load_lds16(m_src + k * (int64_t)sizeof(E), st + N_BYTES + (RB == 1 ? wave & 1 : wave) * 1024);
+    };
+    const int l = lane & 31, half = lane >> 5, G = lane >> 4, sl = lane & 15;
+    f32x16_t acc[2][RB];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) acc[b][rb] = f32x16_t{};
+    auto work = [&](const char* st) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            u32x4_t m[RB];
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb)
+                m[rb] = *(const u32x4_t*)(st + N_BYTES + (32 * rb + l) * 64 + (((2 * i + half) ^ ((l >> 2) & 3)) << 4));
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                u32x4_t n;
+                if constexpr (F32) {
+                    const int d = 64 * wave + 32 * b + l;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int k = 8 * i + 4 * half + q;
+                        n[q] = *(const uint32_t*)(st + k * ROW + (((d >> 2) ^ swz(k)) << 4) + 4 * (d & 3));
+                    }
+                } else {
+                    const int R = 64 * wave + 32 * b + 16 * (G & 1) + 4 * (sl & 3);
+                    s16x4_t h[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int k = 8 * (G >> 1) + 4 * r + (sl >> 2);
+                        h[r] = read_tr(st + (16 * i + k) * ROW + (((R >> 3) ^ swz_tr(k)) << 4) + 8 * ((R >> 2) & 1));
+                    }
+                    n = __builtin_bit_cast(u32x4_t, cat_bf16(h[0], h[1]));
+                }
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) acc[b][rb] = multiply<F32>(n, m[rb], acc[b][rb]);
+            }
+        }
+    };
+    char* const st[4] = {st0, st1, st2, st3};
+    ring<NS, PER>(steps, st, issue, work);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int64_t row = row0 + 32 * rb + l;
+        if (row >= a.T) continue;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int vg = 0; vg < 4; ++vg) {
+                const int c = nt * 256 + 64 * wave + 32 * b + 8 * vg + 4 * half;
+                const f32x16_t& x = acc[b][rb];
+                if (c < a.D)       // D is a multiple of 4
+                    *(float4*)(a.dh_part + ((int64_t)split * a.T + row) * a.D + c) =
+                        make_float4(x[4 * vg], x[4 * vg + 1], x[4 * vg + 2], x[4 * vg + 3]);
+            }
+    }
+}
+
+// dh = the sum of its parts: 16 groups of 4 columns a workgroup, 16 threads each
+// over every 16th part, then over the 16, in order.
+__global__ __launch_bounds__(256) void vocab_few_sum_kernel(const float* __restrict__ part, int splits, int64_t n4,
+                                                            bool bf16, void* __restrict__ dh) {
+    __shared__ float4 sums[16][16];
+    const int c = threadIdx.x & 15, sl = threadIdx.x >> 4;
+    const int64_t i = (int64_t)blockIdx.x * 16 + c;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n4) {
+#pragma unroll 8
+        for (int k = sl; k < splits; k += 16) {
+            const float4 v = *(const float4*)(part + (k * n4 + i) * 4);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+    }
+    sums[sl][c] = s;
+    __syncthreads();
+    if (sl || i >= n4) return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) {
+        const float4 v = sums[k][c];
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    if (bf16) *(uint2*)((uint16_t*)dh + i * 4) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    else *(float4*)((float*)dh + i * 4) = s;
+}
+
+// dW: K is the rows, 32 (bf16) or 16 (fp32) a step.
+template <bool F32, bool OUT16>
+__global__ __launch_bounds__(256, 4) void vocab_few_dw_kernel(const VocabFew a, int n_tiles, void* __restrict__ out) {
+    using E = typename Elem<F32>::type;
+    constexpr int KS = F32 ? 16 : 32;
+    constexpr int HROW = 256 * sizeof(E), ZROW = 64 * sizeof(E);   // bytes of a k row of h, of dz
+    __shared__ __attribute__((aligned(1024))) char lds[32768];     // h's rows, dz's rows; then the output's
+    constexpr int Z = 16384;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int nt = blockIdx.x % n_tiles;
+    const int64_t v0 = (int64_t)(blockIdx.x / n_tiles) * 64;
+    const int l = lane & 31, half = lane >> 5, G = lane >> 4, sl = lane & 15;
+    auto swz_z = [](int k) { return F32 ? 0 : 2 * (k & 3); };       // of dz's 128-byte rows
+
+    f32x16_t acc[2][2];                                             // [columns][entries]
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) acc[b][e] = f32x16_t{};
+    for (int64_t k0 = 0; k0 < a.T; k0 += KS) {
+        if (k0) __syncthreads();
+        constexpr int HC = HROW / 16, HR = 64 / HC, ZC = ZROW / 16, ZR = 64 / ZC;   // chunks of a row, rows of a DMA instruction
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = HR * (4 * wave + j) + lane / HC;
+            const int c = nt * 256 + ((lane % HC) ^ (F32 ? 0 : swz_tr(k))) * (16 / (int)sizeof(E));
+            // a row that does not count is read as zeros, whatever it holds
+            const bool there = k0 + k < a.T && (!F32 || a.lse[k0 + k] != INFINITY);
+            const E* p = (const E*)a.h + (k0 + k) * a.h_pitch + (c < a.D ? c : 0);
+            load_lds16(there ? (const void*)p : (const void*)few_zeros, lds + (4 * wave + j) * 1024);
+        }
+        {
+            const int k = ZR * wave + lane / ZC;
+            const E* p = (F32 ? (const E*)a.dz32 : (const E*)a.dz) + (k0 + k) * a.dz_pitch + v0 +
+                         ((lane % ZC) ^ swz_z(k)) * (16 / (int)sizeof(E));
+            load_lds16(k0 + k < a.T ? (const void*)p : (const void*)few_zeros, lds + Z + wave * 1024);
+        }
+        wait_vmem();
+        __syncthreads();
+        if constexpr (F32) {
+#pragma unroll
+            for (int i = 0; i < KS / 2; ++i) {
+                const int k = 2 * i + half;
+                float n[2], m[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    n[b] = *(const float*)(lds + k * HROW + 4 * (64 * wave + 32 * b + l));
+                    m[b] = *(const float*)(lds + Z + k * ZROW + 4 * (32 * b + l));
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) acc[b][e] = __builtin_amdgcn_mfma_f32_32x32x2f32(n[b], m[e], acc[b][e], 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                bf16x8_t n[2], m[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    s16x4_t x[2], y[2];
+                    const int R = 32 * b + 16 * (G & 1) + 4 * (sl & 3), C = 64 * wave + R;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int k = 8 * (G >> 1) + 4 * r + (sl >> 2);
+                        x[r] = read_tr(lds + (16 * i + k) * HROW + (((C >> 3) ^ swz_tr(k)) << 4) + 8 * ((C >> 2) & 1));
+                        y[r] = read_tr(lds + Z + (16 * i + k) * ZROW + (((R >> 3) ^ swz_z(k)) << 4) + 8 * ((R >> 2) & 1));
+                    }
+                    n[b] = cat_bf16(x[0], x[1]);
+                    m[b] = cat_bf16(y[0], y[1]);
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) acc[b][e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n[b], m[e], acc[b][e], 0, 0, 0);
+            }
+        }
+    }
+    __syncthreads();
+    // 32 entries x 64 columns of the wavefront's own at a time through LDS, so that
+    // a store writes whole rows of 128 or 256 bytes
+    using O = typename Elem<!OUT16>::type;
+    constexpr int OROW = 64 * sizeof(O), OC = OROW / 16, OR = 64 / OC;
+    char* own = lds + wave * 8192;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int vg = 0; vg < 4; ++vg) {
+                const f32x16_t& x = acc[b][e];
+                if constexpr (OUT16)
+                    *(uint2*)(own + l * OROW + (((4 * b + vg) ^ (l & 7)) << 4) + 8 * half) =
+                        make_uint2(pack_bf16(x[4 * vg], x[4 * vg + 1]), pack_bf16(x[4 * vg + 2], x[4 * vg + 3]));
+                else
+                    *(float4*)(own + l * OROW + (((8 * b + 2 * vg + half) ^ (l & 15)) << 4)) =
+                        make_float4(x[4 * vg], x[4 * vg + 1], x[4 * vg + 2], x[4 * vg + 3]);
+            }
+#pragma unroll
+        for (int q = 0; q < 32 / OR; ++q) {
+            const int r = OR * q + lane / OC, c = lane % OC;
+            const u32x4_t v = *(const u32x4_t*)(own + r * OROW + ((c ^ (r & (OC - 1))) << 4));
+            const int64_t row = v0 + 32 * e + r;
+            const int col = nt * 256 + 64 * wave + c * (16 / (int)sizeof(O));
+            if (row < a.V && col < a.D) *(u32x4_t*)((O*)out + row * a.D + col) = v;
+        }
+    }
+}
+
+bool fits(const VocabFew& a) {
+    return a.T > 0 && a.V > 0 && a.D > 0 && a.D % (a.f32 ? 4 : 8) == 0 && a.h_pitch >= a.D;
+}
+
+template <bool DZ>
+hipError_t launch_logits(const VocabFew& a, hipStream_t s) {
+    if (!fits(a)) return hipErrorInvalidValue;
+    const int rb = a.T <= 32 ? 1 : 2;
+    const int64_t m_tiles = (a.T + 32 * rb - 1) / (32 * rb), grid = m_tiles * ((a.V + FN - 1) / FN);
+    if (grid > 1 << 23) return hipErrorInvalidValue;
+    if (a.f32) {
+        if (rb == 1) vocab_few_logits_kernel<true, 1, DZ><<<(unsigned)grid, 256, 0, s>>>(a, (int)m_tiles);
+        else vocab_few_logits_kernel<true, 2, DZ><<<(unsigned)grid, 256, 0, s>>>(a, (int)m_tiles);
+    } else {
+        if (rb == 1) vocab_few_logits_kernel<false, 1, DZ><<<(unsigned)grid, 256, 0, s>>>(a, (int)m_tiles);
+        else vocab_few_logits_kernel<false, 2, DZ><<<(unsigned)grid, 256, 0, s>>>(a, (int)m_tiles);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int vocab_few_splits(int64_t T, int D, int V, bool f32) {
+    const int64_t m_tiles = (T + (T <= 32 ? 31 : 63)) / (T <= 32 ? 32 : 64), n_tiles = (D + 255) / 256;
+    const int64_t steps = (V + (f32 ? 15 : 31)) / (f32 ? 16 : 32);
+    // a workgroup a CU, of 4 steps at least
+    return (int)std::max<int64_t>(1, std::min<int64_t>(256 / (m_tiles * n_tiles), steps / 4));
+}
+
+hipError_t launch_vocab_few_stats(const VocabFew& a, hipStream_t s) { return launch_logits<false>(a, s); }
+hipError_t launch_vocab_few_dz(const VocabFew& a, hipStream_t s) {
+    if (a.dz_pitch % FN || a.dz_pitch < a.V) return hipErrorInvalidValue;
+    return launch_logits<true>(a, s);
+}
+
+hipError_t launch_vocab_few_dw(const VocabFew& a, void* dW, bool out16, hipStream_t s) {
+    if (!fits(a) || a.dz_pitch % FN || a.dz_pitch < a.V || (a.f32 && out16)) return hipErrorInvalidValue;
+    const int n_tiles = (a.D + 255) / 256;
+    const int64_t grid = ((int64_t)a.V + 63) / 64 * n_tiles;
+    if (grid > 1 << 23) return hipErrorInvalidValue;
+    if (a.f32) vocab_few_dw_kernel<true, false><<<(unsigned)grid, 256, 0, s>>>(a, n_tiles, dW);
+    else if (out16) vocab_few_dw_kernel<false, true><<<(unsigned)grid, 256, 0, s>>>(a, n_tiles, dW);
+    else vocab_few_dw_kernel<false, false><<<(unsigned)grid, 256, 0, s>>>(a, n_tiles, dW);
+    return hipGetLastError();
+}
+
+hipError_t launch_vocab_few_dh(const VocabFew& a, void* dh, hipStream_t s) {
+    if (!fits(a) || a.dz_pitch % FN || a.dz_pitch < a.V) return hipErrorInvalidValue;
+    const int rb = a.T <= 32 ? 1 : 2;
+    const int m_tiles = (int)((a.T + 32 * rb - 1) / (32 * rb)), n_tiles = (a.D + 255) / 256;
+    const int splits = vocab_few_splits(a.T, a.D, a.V, a.f32);
+    const unsigned grid = (unsigned)(m_tiles * n_tiles * splits);
+    if (a.f32) {
+        if (rb == 1) vocab_few_dh_kernel<true, 1><<<grid, 256, 0, s>>>(a, n_tiles, m_tiles, splits);
+        else vocab_few_dh_kernel<true, 2><<<grid, 256, 0, s>>>(a, n_tiles, m_tiles, splits);
+    } else {
+        if (rb == 1) vocab_few_dh_kernel<false, 1><<<grid, 256, 0, s>>>(a, n_tiles, m_tiles, splits);
+        else vocab_few_dh_kernel<false, 2><<<grid, 256, 0, s>>>(a, n_tiles, m_tiles, splits);
+    }
+    if (hipError_t e = hipGetLastError()) return e;
+    const int64_t n4 = a.T * a.D / 4;
+    vocab_few_sum_kernel<<<(unsigned)((n4 + 15) / 16), 256, 0, s>>>(a.dh_part, splits, n4, !a.f32, dh);
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -760,9 +760,10 @@ struct GradWork {
     int steps;                // K steps of one product
     int virt;                 // of a tile: those of all products, at least 1
     int per;                  // of a team
+    bool split;               // tiles are divided between teams
 };
 
-__device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64_t rows) {
+__host__ __device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64_t rows) {
     GradWork w;
     const int64_t M = a.dW ? a.len : rows;
     const int K = a.dW ? (int)rows : a.len;
@@ -770,11 +771,12 @@ __device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64_t rows) 
     w.n_tiles = (a.N + TN - 1) / TN;
     w.teams = kGradUnits / w.n_tiles;
     w.steps = (K + BK - 1) / BK;
-    w.virt = max(w.steps * a.products, 1);
+    w.virt = w.steps ? w.steps * a.products : 1;
     // parts cost what their write and their sum take, about 24 steps
     const int even = (int)(((int64_t)w.m_tiles * w.virt + w.teams - 1) / w.teams);
     const int whole = (w.m_tiles + w.teams - 1) / w.teams * w.virt;
-    w.per = max(even + 24 < whole ? max(even, 8) : whole, 1);
+    w.split = even + 24 < whole;
+    w.per = w.split ? (even > 8 ? even : 8) : whole > 1 ? whole : 1;
     return w;
 }
 
@@ -896,32 +898,49 @@ __global__ __launch_bounds__(512, 1) void vocab_grad_kernel(const VocabGrad a) {
     }
 }
 
-// The tiles that more than one team made: 32 rows of one a workgroup.
+// The tiles that more than one team made.  MANY (few row tiles, each of many
+// parts): a row a workgroup, its wavefronts over every fourth part and then over
+// the four; else 32 rows a workgroup, 8 a wavefront.
+template <bool MANY>
 __global__ __launch_bounds__(256) void vocab_grad_sum_kernel(const VocabGrad a) {
+    __shared__ float4 sums[MANY ? 4 : 1][64];
+    constexpr int PER = MANY ? 256 : 8;        // workgroups of a tile
     const int64_t rows = a.rows.count ? *a.rows.count : a.rows.T;
     const GradWork w = grad_work(a, rows);
-    const int slab = blockIdx.x & 7, tile = blockIdx.x >> 3;
+    const int slab = blockIdx.x % PER, tile = blockIdx.x / PER;
     const int mt = tile / w.n_tiles, nt = tile - mt * w.n_tiles;
     if (mt >= w.m_tiles) return;
     const int64_t M = a.dW ? a.len : rows;
     const int64_t s0 = (int64_t)mt * w.virt, s1 = s0 + w.virt;
     const int t0 = (int)(s0 / w.per), t1 = (int)((s1 - 1) / w.per);
     if (t0 == t1) return;
-    const int lane = threadIdx.x & 63, n0 = nt * TN + 4 * lane;
-    if (n0 >= a.N) return;
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-        const int tr = 32 * slab + 4 * i + (threadIdx.x >> 6);
-        const int64_t m = (int64_t)mt * 256 + tr;
-        if (m >= M) break;
-        const int at = tr * 256 + 4 * lane;
-        float4 v = *(const float4*)(grad_part(a, w, t0, false, nt) + at);
-#pragma unroll 4
-        for (int t = t0 + 1; t <= t1; ++t) {
-            const float4 o = *(const float4*)(grad_part(a, w, t, true, nt) + at);
-            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-        }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n0 = nt * TN + 4 * lane;
+    auto part = [&](int t, int tr) { return *(const float4*)(grad_part(a, w, t, t > t0, nt) + tr * 256 + 4 * lane); };
+    auto add = [](float4& v, float4 o) { v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w; };
+    if constexpr (MANY) {
+        const int64_t m = (int64_t)mt * 256 + slab;
+        if (m >= M) return;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int t = t0 + wave; t <= t1; t += 4) add(v, part(t, slab));
+        sums[wave][lane] = v;
+        __syncthreads();
+        if (wave || n0 >= a.N) return;
+#pragma unroll
+        for (int q = 1; q < 4; ++q) add(v, sums[q][lane]);
         grad_out(a, m, n0, v);
+    } else {
+        if (n0 >= a.N) return;
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+            const int tr = 32 * slab + 4 * i + wave;
+            const int64_t m = (int64_t)mt * 256 + tr;
+            if (m >= M) break;
+            float4 v = part(t0, tr);
+#pragma unroll 4
+            for (int t = t0 + 1; t <= t1; ++t) add(v, part(t, tr));
+            grad_out(a, m, n0, v);
+        }
     }
 }
 
@@ -980,7 +999,13 @@ hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s) {
     if (a.dW) vocab_grad_kernel<true><<<kGradUnits, 512, 0, s>>>(a);
     else vocab_grad_kernel<false><<<kGradUnits, 512, 0, s>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
-    vocab_grad_sum_kernel<<<(unsigned)(tiles * 8), 256, 0, s>>>(a);
+    // with the rows known here, or more of them than there can be (dW: fewer rows
+    // are fewer steps, which do not divide where more do not), tiles that are
+    // whole need no sum
+    const GradWork w = grad_work(a, a.rows.T);
+    if ((a.dW || !a.rows.count) && !w.split) return hipSuccess;
+    if (w.m_tiles * 8 <= w.teams) vocab_grad_sum_kernel<true><<<(unsigned)(tiles * 256), 256, 0, s>>>(a);
+    else vocab_grad_sum_kernel<false><<<(unsigned)(tiles * 8), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -91,4 +91,31 @@ struct VocabGrad {
 size_t vocab_grad_partial_bytes(int N);
 hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s);
 
+// Few rows (vocab_few.hip): the products that read the table once, in its own
+// type.  Rows of 16 bytes' multiples; every row is a row of its own, those that
+// do not count have an infinite lse (dz) and are left to the caller (stats).
+constexpr int kVocabFewCols = 128;    // entries of a logits tile
+struct VocabFew {
+    bool f32;
+    const void *h, *W;        // bf16, or fp32
+    int64_t h_pitch;          // elements
+    int64_t T;
+    int D, V;
+    float scale;              // stats: log2(e) / tau; dz: 1 / tau
+    const int32_t* target;    // [T] or null
+    float2* part;             // stats
+    int64_t part_pitch;
+    float* zt;                // stats
+    const float *g, *lse;     // dz: g / tau, lse
+    uint16_t* dz;             // bf16, or three planes: [T, pitch]
+    float* dz32;              // the same in fp32 (f32)
+    int64_t dz_pitch, dz_plane;
+    float* dh_part;           // [splits, T, D]
+};
+int vocab_few_splits(int64_t T, int D, int V, bool f32);
+hipError_t launch_vocab_few_stats(const VocabFew& a, hipStream_t s);
+hipError_t launch_vocab_few_dz(const VocabFew& a, hipStream_t s);
+hipError_t launch_vocab_few_dh(const VocabFew& a, void* dh, hipStream_t s);
+hipError_t launch_vocab_few_dw(const VocabFew& a, void* dW, bool out16, hipStream_t s);
+
 }  // namespace moe

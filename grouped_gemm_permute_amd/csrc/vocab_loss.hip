@@ -39,6 +39,8 @@ constexpr size_t kAlign = 256;
 constexpr int kMaxD = 16384, kMaxTop = 256;
 constexpr int64_t kMaxV = 1 << 24, kMaxT = 1 << 28;
 constexpr int64_t kListRows = 1024;
+// up to here the products of few rows, which read the table once
+constexpr int64_t kFewRows = 64, kFewRowsF32 = 256;
 // dz of one piece of the vocabulary: what ordinary steps take whole or in a few
 // pieces (32768 rows: 32768 entries), little of 288 GB.
 constexpr int64_t kDzBytes = 1ll << 31;
@@ -405,6 +407,7 @@ struct TeacherArgs {
     uint16_t* dz;
     int64_t pitch, plane;
     int planes;
+    float* dz32;              // the same in fp32, or null
 };
 
 __global__ __launch_bounds__(64) void vocab_teacher_kernel(const TeacherArgs a) {
@@ -430,6 +433,7 @@ __global__ __launch_bounds__(64) void vocab_teacher_kernel(const TeacherArgs a) 
         if (!first) continue;
         float x = g * (__builtin_amdgcn_exp2f(fmaf(a.z[t * K + k], a.inv_tau, -lse) * kLog2E) - share);
         uint16_t* p = a.dz + i * a.pitch + (v - a.v0);
+        if (a.dz32) a.dz32[i * a.pitch + (v - a.v0)] = x;
         for (int pl = 0; pl < a.planes; ++pl) {
             const uint16_t o = to_bf16(x);
             p[pl * a.plane] = o;
@@ -448,11 +452,12 @@ __global__ __launch_bounds__(256) void vocab_zero_kernel(O* p, int64_t n) {
 struct Plan {
     bool list;                // rows that count are listed first
     bool whole;               // logits by 256 x 256 tiles
+    bool few;                 // the products of few rows
     bool copy_W, copy_h;      // operands as padded bf16 planes
     int planes, products, Dp;
     int64_t n_tiles;          // stats: column tiles
     int64_t piece, pieces;    // entries of a piece (a multiple of 256), and how many
-    size_t rows, pos, count, live, hc, info, Wc, part, zt, g, lse, dz, acc, total;
+    size_t rows, pos, count, live, hc, info, Wc, part, zt, g, lse, dz, dz32, dh_part, acc, total;
 };
 
 Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
@@ -460,14 +465,17 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     p.list = T >= kListRows;
     p.planes = dtype == MOE_BF16 ? 1 : 3;
     p.products = dtype == MOE_BF16 ? 1 : 6;
+    const bool f32 = dtype != MOE_BF16;
+    p.few = T <= (f32 ? kFewRowsF32 : kFewRows) && D % (f32 ? 4 : 8) == 0 && T * V * p.planes * 2 <= kDzBytes;
     // bf16 rows of whole K steps are read where they are
-    p.copy_W = dtype != MOE_BF16 || D % 32 != 0;
+    p.copy_W = !p.few && (f32 || D % 32 != 0);
     p.copy_h = p.copy_W || p.list || backward;
     // what is copied is padded to what the tiles of many rows take
     const int unit = p.copy_W && p.list ? 128 : 32;
     p.Dp = (D + unit - 1) / unit * unit;
     p.whole = p.list && p.Dp % 128 == 0;
     p.n_tiles = ((int64_t)V + kVocabTileCols - 1) / kVocabTileCols;
+    if (p.few && !backward) p.n_tiles = ((int64_t)V + kVocabFewCols - 1) / kVocabFewCols;
     size_t at = 0;
     auto take = [&](bool want, size_t bytes) {
         const size_t o = at;
@@ -492,7 +500,10 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
         p.pieces = (p.n_tiles * tile + p.piece - 1) / p.piece;
         p.g = take(true, (size_t)T * 4);
         p.lse = take(true, (size_t)T * 4);
+        if (p.few) p.piece = p.n_tiles * tile, p.pieces = 1;
         p.dz = take(true, (size_t)p.planes * T * p.piece * 2);
+        p.dz32 = take(p.few && f32, (size_t)T * p.piece * 4);
+        p.dh_part = take(p.few, (size_t)(p.few ? vocab_few_splits(T, D, V, f32) : 0) * T * D * 4);
         p.part = take(true, vocab_grad_partial_bytes(D));
         p.acc = take(p.pieces > 1, (size_t)T * p.Dp * 4);
     }
@@ -578,7 +589,11 @@ moe_status forward(const Call& a, float* loss, float* lse, float* z, void* works
     const float inv_tau = 1.f / a.tau;
     VocabStats st = {h, W, rows, a.targets.V, p.Dp, p.products, kLog2E * inv_tau,
                      (float2*)(ws + p.part), a.T, a.targets.target, (float*)(ws + p.zt)};
-    TRY(p.whole ? launch_vocab_stats_whole(st, (const float4*)(ws + p.info), s) : launch_vocab_stats(st, s));
+    if (p.few) {
+        VocabFew w = {a.dtype != MOE_BF16, a.h, a.W, a.D, a.T, a.D, a.targets.V, st.c, a.targets.target, st.part, a.T, st.zt};
+        TRY(launch_vocab_few_stats(w, s));
+    } else
+        TRY(p.whole ? launch_vocab_stats_whole(st, (const float4*)(ws + p.info), s) : launch_vocab_stats(st, s));
     FinishArgs f = {st.part, a.T, (int)p.n_tiles, rows, a.targets, st.c, st.zt, a.targets.target ? loss : nullptr, lse};
     vocab_finish_kernel<<<(unsigned)((a.T + 15) / 16), 256, 0, s>>>(f);
     TRY(hipGetLastError());
@@ -635,10 +650,16 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
     const bool h16 = a.dtype == MOE_BF16;
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
         const int len = (int)std::min<int64_t>(p.piece, V - v0);
-        VocabDz d = {h, W, rows, V, v0, len, p.Dp, p.products, inv_tau, g, l, a.targets.target, dz, p.piece, dz_plane};
-        TRY(p.whole ? launch_vocab_dz_whole(d, (const float4*)(ws + p.info), s) : launch_vocab_dz(d, s));
+        const VocabDz d = {h, W, rows, V, v0, len, p.Dp, p.products, inv_tau, g, l, a.targets.target, dz, p.piece, dz_plane};
+        VocabFew w = {!h16, h16 ? (const void*)h.p : a.h, a.W, h16 ? h.pitch : a.D, a.T, a.D, V, inv_tau, a.targets.target};
+        w.g = g, w.lse = l;
+        w.dz = dz, w.dz32 = p.few && !h16 ? (float*)(ws + p.dz32) : nullptr;
+        w.dz_pitch = p.piece, w.dz_plane = dz_plane;
+        w.dh_part = (float*)(ws + p.dh_part);
+        if (p.few) TRY(launch_vocab_few_dz(w, s));
+        else TRY(p.whole ? launch_vocab_dz_whole(d, (const float4*)(ws + p.info), s) : launch_vocab_dz(d, s));
         if (!a.targets.target) {
-            TeacherArgs t = {a.targets, rows, z, g, l, inv_tau, v0, len, dz, p.piece, dz_plane, p.planes};
+            TeacherArgs t = {a.targets, rows, z, g, l, inv_tau, v0, len, dz, p.piece, dz_plane, p.planes, w.dz32};
             vocab_teacher_kernel<<<(unsigned)a.T, 64, 0, s>>>(t);
             TRY(hipGetLastError());
         }
@@ -649,7 +670,9 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
         q.N = a.D;
         q.products = p.products;
         q.partial = (float*)(ws + p.part);
-        if (dh) {
+        if (dh && p.few) {
+            TRY(launch_vocab_few_dh(w, dh, s));
+        } else if (dh) {
             q.dW = false;
             q.n = {W.p + v0 * W.pitch, W.pitch, W.plane};
             q.acc = p.pieces > 1 ? (float*)(ws + p.acc) : nullptr;
@@ -660,7 +683,9 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
             q.out_bf16 = h16;
             TRY(launch_vocab_grad(q, s));
         }
-        if (dW) {
+        if (dW && p.few && a.T <= kFewRows) {
+            TRY(launch_vocab_few_dw(w, dW, dW_dtype == MOE_BF16, s));
+        } else if (dW) {
             q.dW = true;
             q.n = h;
             q.acc = nullptr;
