@@ -39,8 +39,23 @@ constexpr size_t kAlign = 256;
 constexpr int kMaxD = 16384, kMaxTop = 256;
 constexpr int64_t kMaxV = 1 << 24, kMaxT = 1 << 28;
 constexpr int64_t kListRows = 1024;
-// up to here the products of few rows, which read the table once
-constexpr int64_t kFewRows = 64, kFewRowsF32 = 256;
+// Whether the products of few rows (vocab_few.hip) are the faster ones.  They read
+// the table once for 64 rows, the tiles of 128 x 256 once for 128, and those
+// leave compute units idle where they are few.  Measured, bf16: at 65536
+// entries x 768 and 65 rows 41 us against 28 (backward 108 against 118), at 20000
+// x 1024 and 192 rows 27 against 30 (80 against 104), at 256 rows 35 against 31 (96
+// against 113), at 8000 x 256 and 384 rows 11 against 16 (41 against 73).  fp32,
+// where the others begin with a copy of the table in planes: even at about 400
+// rows forward (65536 x 768: 356 us against 386 at 384) and 256 backward (793
+// against 795).
+bool few_rows(int64_t T, int D, int V, bool f32, bool backward) {
+    if (D % (f32 ? 4 : 8)) return false;
+    if (f32) return T <= (backward ? 256 : 384);
+    return T <= 64 || (T <= 512 && (T + 63) / 64 * V <= (backward ? 2 : 1) * 65536);
+}
+// fp32 dW of few rows on its own kernel: 94 us against 110 at 65 rows of 65536 x
+// 768, even at 256; bf16 always (22 against 48 at 64, 42 against 67 at 256).
+constexpr int64_t kFewDwRowsF32 = 192;
 // dz of one piece of the vocabulary: what ordinary steps take whole or in a few
 // pieces (32768 rows: 32768 entries), little of 288 GB.
 constexpr int64_t kDzBytes = 1ll << 31;
@@ -466,7 +481,7 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     p.planes = dtype == MOE_BF16 ? 1 : 3;
     p.products = dtype == MOE_BF16 ? 1 : 6;
     const bool f32 = dtype != MOE_BF16;
-    p.few = T <= (f32 ? kFewRowsF32 : kFewRows) && D % (f32 ? 4 : 8) == 0 && T * V * p.planes * 2 <= kDzBytes;
+    p.few = few_rows(T, D, V, f32, backward) && T * V * p.planes * 2 <= kDzBytes;
     // bf16 rows of whole K steps are read where they are
     p.copy_W = !p.few && (f32 || D % 32 != 0);
     p.copy_h = p.copy_W || p.list || backward;
@@ -683,7 +698,7 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
             q.out_bf16 = h16;
             TRY(launch_vocab_grad(q, s));
         }
-        if (dW && p.few && a.T <= kFewRows) {
+        if (dW && p.few && (h16 || a.T <= kFewDwRowsF32)) {
             TRY(launch_vocab_few_dw(w, dW, dW_dtype == MOE_BF16, s));
         } else if (dW) {
             q.dW = true;
