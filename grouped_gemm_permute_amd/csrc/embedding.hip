@@ -7,23 +7,22 @@
 // order of their tokens, so that repeated calls give equal bits and no atomics
 // meet.  Three launches:
 //
-//  sort:  workgroup b owns 32 to 512 entries of the table.  It reads all ids once
-//         to count those below its entries (where its first token goes) and
+//  sort:  workgroup b owns every 256th entry of the table.  It reads all ids once
+//         to count those of the workgroups before it (where its first token goes) and
 //         those of each of its entries, a wavefront counting its own
 //         contiguous part of the tokens; then again to place its tokens, each
 //         wavefront in order behind the wavefronts before it, the lanes of one
 //         entry found by a ballot a bit.  No workgroup
-//         waits for another: 512 workgroups reading 32768 ids are 64 MB from
-//         the L2s, less time than the second launch of a counting sort by
-//         blocks.
+//         waits for another: 256 workgroups reading 32768 ids twice are 64 MB
+//         from the L2s, against two more launches of a sort by digits.
 //  sum:   adds each entry's rows and writes the entry, zeros where it has no
 //         token.  Entries of more than kLong tokens (text has a
 //         few that make up several percent of it) are left to further
 //         wavefronts, each of which adds the rows of kLong consecutive sorted
 //         tokens: at most two such entries have tokens there, and their two sums
 //         are kept.
-//  join:  the sums of a long entry are added in order by the wavefronts of the
-//         workgroup at its start.
+//  join:  the sums of a long entry are added, in a fixed order, by the workgroup
+//         at its start.
 //
 // Bound by memory: T rows read, V rows written (or, added, T at most read and written).
 #include "mfma_common.h"
@@ -40,7 +39,7 @@ using namespace mfma;
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kLong = 64;              // tokens of an entry that one wavefront adds
+constexpr int kLong = 32;              // tokens of an entry that one wavefront adds
 constexpr int kMaxD = 16384;
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -104,40 +103,61 @@ __global__ __launch_bounds__(256) void embedding_forward_kernel(const FwdArgs a)
 
 // ---- backward
 
-// order: the tokens with ids in [0, V), sorted by id and then by token;
-// start[v]: where those of entry v begin, start[V] how many there are.
-// BITS: of an entry's place among the workgroup's.
+// order: the tokens with ids in [0, V), those of an entry together and in order;
+// first[v]: where those of entry v begin, count[v] how many they are; first[V] how
+// many there are in all.  Workgroup b owns entries b, b + 2^shift, b + 2 2^shift..,
+// at most 2^BITS of them, so that text's frequent entries, which are next to each
+// other, fall to different workgroups (32768 tokens, one in 11 / (v + 1) of them
+// entry v: 26 us with ranges of entries, 17 so).
 template <int BITS>
 __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const int32_t* __restrict__ ids, int64_t T, int V,
-                                                                      int32_t* __restrict__ order,
-                                                                      int32_t* __restrict__ start) {
+                                                                      int shift, int32_t* __restrict__ order,
+                                                                      int32_t* __restrict__ first,
+                                                                      int32_t* __restrict__ counts) {
     constexpr int SPAN = 1 << BITS;
     __shared__ int32_t at[kSortWaves][SPAN];   // counts, then places
     __shared__ int32_t below[kSortWaves], sums[kSortWaves];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int lo = blockIdx.x * SPAN, hi = min(lo + SPAN, V);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int mask = (1 << shift) - 1, own = blockIdx.x;
     for (int i = tid; i < kSortWaves * SPAN; i += kSortThreads) (&at[0][0])[i] = 0;
     __syncthreads();
-    // this wavefront's tokens, 512 at a time: 64 consecutive ones a load
-    const int64_t per = (T + kSortThreads - 1) / kSortThreads * 64;
-    const int64_t t0 = min(per * wave, T), t1 = min(t0 + per, T);
-    auto load = [&](int64_t base, int32_t (&id)[8]) {
+    // This wavefront's tokens, 64 consecutive ones a load.  Every workgroup looks at
+    // every token, and that is most of its time: a few instructions for 64.
+    const int per = (int)((T + kSortThreads - 1) / kSortThreads * 64);
+    const int t0 = (int)min((int64_t)per * wave, T), t1 = (int)min((int64_t)t0 + per, T);
+    auto each = [&](auto&& look) {
+        int base = t0;
+        if (base + 512 <= t1) {
+            int32_t id[8], next[8];
+            auto load = [&](const int32_t* p, int32_t (&to)[8]) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t t = base + 64 * j + lane;
-            id[j] = t < t1 ? ids[t] : -1;
+                for (int j = 0; j < 8; ++j) to[j] = p[64 * j + lane];
+            };
+            load(ids + base, id);
+            for (; base + 512 <= t1; base += 512) {
+                load(ids + (base + 1024 <= t1 ? base + 512 : base), next);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    look(id[j], base + 64 * j);
+                    id[j] = next[j];
+                }
+            }
         }
+        for (; base < t1; base += 64) look(base + lane < t1 ? ids[base + lane] : -1, base);
     };
     int under = 0;
-    for (int64_t base = t0; base < t1; base += 512) {
-        int32_t id[8];
-        load(base, id);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            under += id[j] >= 0 && id[j] < lo;
-            if (id[j] >= lo && id[j] < hi) atomicAdd(&at[wave][id[j] - lo], 1);
+    bool any = false;
+    each([&](int32_t id, int) {
+        // -1 for what is outside the table: no workgroup's number is above mask
+        id = (uint32_t)id < (uint32_t)V ? id : -1;
+        const int of = id & mask;
+        under += of < own;
+        const bool in = of == own && id >= 0;
+        if (__ballot(in)) {
+            any = true;
+            if (in) atomicAdd(&at[wave][id >> shift], 1);
         }
-    }
+    });
     for (int d = 32; d; d >>= 1) under += __shfl_xor(under, d);
     if (lane == 0) below[wave] = under;
     __syncthreads();
@@ -159,10 +179,12 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const int3
         if (w < wave) place += sums[w];
     }
     if (entry) {
-        if (lo + tid < hi) {
-            start[lo + tid] = place;
-            if (lo + tid == V - 1) start[V] = place + mine;
+        const int64_t v = ((int64_t)tid << shift) + own;
+        if (v < V) {
+            first[v] = place;
+            counts[v] = mine;
         }
+        if (own == mask && tid == SPAN - 1) first[V] = place + mine;
         for (int w = 0; w < kSortWaves; ++w) {
             const int c = at[w][tid];
             at[w][tid] = place;
@@ -170,34 +192,43 @@ __global__ __launch_bounds__(kSortThreads) void embedding_sort_kernel(const int3
         }
     }
     __syncthreads();
-    for (int64_t base = t0; base < t1; base += 512) {
-        int32_t id[8];
-        load(base, id);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bool in = id[j] >= lo && id[j] < hi;
-            uint64_t same = __ballot(in);
-            if (!same) continue;
-            // the lanes with this lane's entry: those that agree in every bit
-            const int e = in ? id[j] - lo : 0;
-#pragma unroll
-            for (int b = 0; b < BITS; ++b) {
-                const uint64_t set = __ballot(e >> b & 1);
-                same &= e >> b & 1 ? set : ~set;
-            }
-            const int before = __popcll(same & ((1ull << lane) - 1));
-            if (in) {
-                const int p = at[wave][e];
-                order[p + before] = (int32_t)(base + 64 * j + lane);
-                // one of them moves the place on, behind all their reads
-                if (before == 0) at[wave][e] = p + __popcll(same);
-            }
+    if (!any) return;
+    // in order
+    each([&](int32_t id, int base) {
+        const bool in = (id & mask) == own && (uint32_t)id < (uint32_t)V;
+        uint64_t todo = __ballot(in);
+        if (!todo) return;
+        const int e = in ? id >> shift : -1;
+        if (__popcll(todo) <= 8) {
+            // few lanes: one entry after the other
+            do {
+                const int v = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)todo) - 1);
+                const uint64_t same = __ballot(e == v);
+                const int p = at[wave][v];
+                if (e == v) order[p + __popcll(same & ((1ull << lane) - 1))] = base + lane;
+                if (lane == 0) at[wave][v] = p + __popcll(same);
+                todo &= ~same;
+            } while (todo);
+            return;
         }
-    }
+        // the lanes with this lane's entry: those that agree in every bit
+#pragma unroll
+        for (int b = 0; b < BITS; ++b) {
+            const uint64_t set = __ballot(e >> b & 1);
+            todo &= e >> b & 1 ? set : ~set;
+        }
+        const int before = __popcll(todo & ((1ull << lane) - 1));
+        if (in) {
+            const int p = at[wave][e];
+            order[p + before] = base + lane;
+            // one of them moves the place on, behind all their reads
+            if (before == 0) at[wave][e] = p + __popcll(todo);
+        }
+    });
 }
 
 struct SumArgs {
-    const int32_t *ids, *order, *start;
+    const int32_t *ids, *order, *first, *count;
     const void* dy;
     void* out;
     float* part;         // [chunks][2][D]
@@ -287,62 +318,78 @@ __device__ __forceinline__ void write_cols(const SumArgs& a, int v, int c, Cols<
 template <typename E, typename O, int W>
 __global__ __launch_bounds__(256) void embedding_sum_kernel(const SumArgs a) {
     if (blockIdx.x < a.row_blocks) {
-        // W columns of an entry a thread
-        const int64_t v0 = (int64_t)blockIdx.x * a.rows;
-        const int rows = (int)min((int64_t)a.rows, a.V - v0), per_row = a.D / W;
-        for (int i = threadIdx.x; i < rows * per_row; i += 256) {
-            const int r = i / per_row, c = (i - r * per_row) * W;
-            const int v = (int)v0 + r;
-            const int s = a.start[v], e = a.start[v + 1];
-            if (e - s > kLong || (a.add && e == s)) continue;
-            write_cols<O, W>(a, v, c, sum_rows<E, W>(a, s, e, c));
+        // W columns of an entry a thread; a workgroup's entries lie far apart,
+        // since text has its frequent ones next to each other
+        const int per_row = a.D / W;
+        for (int i0 = threadIdx.x; i0 < a.rows * per_row; i0 += 1024) {
+            int s[4], e[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = (i0 + 256 * j) / per_row;
+                const int64_t v = min(blockIdx.x + r * a.row_blocks, (int64_t)a.V - 1);
+                s[j] = a.first[v];
+                e[j] = s[j] + a.count[v];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + 256 * j, r = i / per_row, c = (i - r * per_row) * W;
+                const int64_t v = blockIdx.x + r * a.row_blocks;
+                if (r >= a.rows || v >= a.V || e[j] - s[j] > kLong || (a.add && e[j] == s[j])) continue;
+                write_cols<O, W>(a, (int)v, c, sum_rows<E, W>(a, s[j], e[j], c));
+            }
         }
         return;
     }
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t chunk = ((int64_t)blockIdx.x - a.row_blocks) * 4 + wave;
-    const int all = a.start[a.V];
+    const int all = a.first[a.V];
     if (chunk * kLong >= all) return;
     const int p0 = (int)(chunk * kLong), p1 = min(p0 + kLong, all);
     // the entry of the chunk's first token, and that of its last, if long
     const int va = a.ids[a.order[p0]], vb = a.ids[a.order[p1 - 1]];
-    const int ae = a.start[va + 1], bs = a.start[vb];
+    const int ae = a.first[va] + a.count[va], bs = a.first[vb];
     float* part = a.part + chunk * 2 * a.D;
-    if (ae - a.start[va] > kLong)
+    if (a.count[va] > kLong)
         for (int c = lane * W; c < a.D; c += 64 * W)
             store_cols<float, W>(part + c, sum_rows<E, W>(a, p0, min(ae, p1), c));
-    if (vb != va && a.start[vb + 1] - bs > kLong)
+    if (vb != va && a.count[vb] > kLong)
         for (int c = lane * W; c < a.D; c += 64 * W)
             store_cols<float, W>(part + a.D + c, sum_rows<E, W>(a, bs, p1, c));
 }
 
 // Workgroup: the long entry that begins in this chunk, if one does (it then
-// holds the chunk's last token).
+// holds the chunk's last token).  64 groups of columns at a time, 16 wavefronts
+// each over every 16th part, then over the 16.
 template <typename O, int W>
-__global__ __launch_bounds__(256) void embedding_join_kernel(const SumArgs a) {
+__global__ __launch_bounds__(1024) void embedding_join_kernel(const SumArgs a) {
+    __shared__ Cols<W> sums[16][64];
     const int64_t chunk = blockIdx.x;
-    const int all = a.start[a.V];
+    const int all = a.first[a.V];
     if (chunk * kLong >= all) return;
     const int p0 = (int)(chunk * kLong), p1 = min(p0 + kLong, all);
     const int v = a.ids[a.order[p1 - 1]];
-    const int s = a.start[v], e = a.start[v + 1];
+    const int s = a.first[v], e = s + a.count[v];
     if (e - s <= kLong || s < p0) return;
     // the first sum is the chunk's second where the entry begins behind another
     const int64_t last = (e - 1) / kLong;
-    const float* part = a.part + (a.ids[a.order[p0]] != v ? a.D : 0);
-    for (int c = threadIdx.x * W; c < a.D; c += 256 * W) {
-        Cols<W> sum = load_cols<float, W>(part + chunk * 2 * a.D + c);
-        int64_t k = chunk + 1;
-        for (; k + 8 <= last + 1; k += 8) {
-            Cols<W> x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = load_cols<float, W>(a.part + (k + j) * 2 * a.D + c);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) add_to(sum, x[j]);
+    const int64_t skip = a.ids[a.order[p0]] != v ? a.D : 0;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int c0 = 0; c0 < a.D; c0 += 64 * W) {
+        const int c = c0 + lane * W;
+        Cols<W> sum = {};
+        if (c < a.D) {
+#pragma unroll 4
+            for (int64_t k = chunk + wave; k <= last; k += 16)
+                add_to(sum, load_cols<float, W>(a.part + k * 2 * a.D + (k == chunk ? skip : 0) + c));
         }
-        for (; k <= last; ++k) add_to(sum, load_cols<float, W>(a.part + k * 2 * a.D + c));
-        write_cols<O, W>(a, v, c, sum);
+        sums[wave][lane] = sum;
+        __syncthreads();
+        if (wave == 0 && c < a.D) {
+            for (int w = 1; w < 16; ++w) add_to(sum, sums[w][lane]);
+            write_cols<O, W>(a, v, c, sum);
+        }
+        __syncthreads();
     }
 }
 
@@ -350,15 +397,16 @@ constexpr size_t kAlign = 256;
 size_t padded(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
 struct Layout {
-    size_t order, start, part, total;
+    size_t order, first, count, part, total;
     int64_t chunks;
 };
 Layout layout_of(int64_t T, int D, int V) {
     Layout l;
     l.chunks = (T + kLong - 1) / kLong;
     l.order = 0;
-    l.start = padded((size_t)T * 4);
-    l.part = l.start + padded(((size_t)V + 1) * 4);
+    l.first = padded((size_t)T * 4);
+    l.count = l.first + padded(((size_t)V + 1) * 4);
+    l.part = l.count + padded((size_t)V * 4);
     l.total = l.part + padded((size_t)l.chunks * 2 * D * 4);
     return l;
 }
@@ -366,20 +414,21 @@ Layout layout_of(int64_t T, int D, int V) {
 moe_status check(int64_t T, int D, int V, float scale, moe_dtype dtype) {
     if (T < 0 || T >= (1ll << 31) || D <= 0 || V <= 0 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
     if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
-    if (D > kMaxD || V > (1 << 24) || T > (1 << 29)) return MOE_ERR_UNSUPPORTED;
+    if (D > kMaxD || V > (1 << 24) || T > (1 << 26)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
 template <typename E, typename O, int W>
 hipError_t launch_sums(SumArgs a, int64_t chunks, hipStream_t s) {
-    // about four column groups a thread
-    a.rows = std::max(1, 1024 / (a.D / W));
+    // about eight column groups a thread (32768 entries x 768 in bf16: 14.8 us, with
+    // four 16.3, with two 19.1)
+    a.rows = std::max(1, 2048 / (a.D / W));
     a.row_blocks = ((int64_t)a.V + a.rows - 1) / a.rows;
     embedding_sum_kernel<E, O, W><<<(unsigned)(a.row_blocks + (chunks + 3) / 4), 256, 0, s>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
     // 4 columns a thread: more loads in flight for the few rows there are
     constexpr int J = W == 8 ? 4 : W;
-    if (a.T > kLong) embedding_join_kernel<O, J><<<(unsigned)chunks, 256, 0, s>>>(a);
+    if (a.T > kLong) embedding_join_kernel<O, J><<<(unsigned)chunks, 1024, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -391,11 +440,15 @@ hipError_t launch_backward(const SumArgs& a, int64_t chunks, hipStream_t s) {
     return launch_sums<E, O, 1>(a, chunks, s);
 }
 
-hipError_t launch_sort(const int32_t* ids, int64_t T, int V, int32_t* order, int32_t* start, hipStream_t s) {
-    // about 512 workgroups, each with a power of two of entries
-    if (V <= 512 * 32) embedding_sort_kernel<5><<<(V + 31) / 32, kSortThreads, 0, s>>>(ids, T, V, order, start);
-    else if (V <= 512 * 128) embedding_sort_kernel<7><<<(V + 127) / 128, kSortThreads, 0, s>>>(ids, T, V, order, start);
-    else embedding_sort_kernel<9><<<(V + 511) / 512, kSortThreads, 0, s>>>(ids, T, V, order, start);
+hipError_t launch_sort(const int32_t* ids, int64_t T, int V, int32_t* order, int32_t* first, int32_t* count, hipStream_t s) {
+    // Every workgroup reads every id, so there is one a CU, and more only for more
+    // than 1024 entries each.
+    int shift = 8;
+    while ((int64_t)V > 1024ll << shift) ++shift;
+    const unsigned grid = 1u << shift;
+    if (V <= 64 << shift) embedding_sort_kernel<6><<<grid, kSortThreads, 0, s>>>(ids, T, V, shift, order, first, count);
+    else if (V <= 256 << shift) embedding_sort_kernel<8><<<grid, kSortThreads, 0, s>>>(ids, T, V, shift, order, first, count);
+    else embedding_sort_kernel<10><<<grid, kSortThreads, 0, s>>>(ids, T, V, shift, order, first, count);
     return hipGetLastError();
 }
 
@@ -449,10 +502,11 @@ moe_status moe_embedding_backward(const int32_t* ids, const void* dy, void* dtab
     if (ws_bytes < l.total) return MOE_ERR_WORKSPACE;
     if (T == 0 && accumulate) return MOE_OK;
     char* ws = (char*)workspace;
-    SumArgs a = {ids, (const int32_t*)(ws + l.order), (const int32_t*)(ws + l.start), dy, dtable, (float*)(ws + l.part),
+    SumArgs a = {ids, (const int32_t*)(ws + l.order), (const int32_t*)(ws + l.first), (const int32_t*)(ws + l.count), dy, dtable, (float*)(ws + l.part),
                  T, D, V, scale, accumulate ? 1 : 0, 1, 0};
     (void)hipGetLastError();
-    if (launch_sort(ids, T, V, (int32_t*)(ws + l.order), (int32_t*)(ws + l.start), stream) != hipSuccess) return MOE_ERR_HIP;
+    if (launch_sort(ids, T, V, (int32_t*)(ws + l.order), (int32_t*)(ws + l.first),
+                    (int32_t*)(ws + l.count), stream) != hipSuccess) return MOE_ERR_HIP;
     const bool in16 = dtype == MOE_BF16, out16 = table_dtype == MOE_BF16;
     const hipError_t e = in16 && out16 ? launch_backward<uint16_t, uint16_t>(a, l.chunks, stream)
                          : in16        ? launch_backward<uint16_t, float>(a, l.chunks, stream)

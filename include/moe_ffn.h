@@ -672,7 +672,7 @@ moe_status moe_muon_step(void *W, void *W_bf16, const float *dW, float *momentum
  *   table  [V, D]  dtype
  *   y      [T, D]  dtype; out
  *
- * Any D up to 16384, V up to 2^24, T up to 2^29.  table and y are 16-byte
+ * Any D up to 16384, V up to 2^24, T up to 2^26.  table and y are 16-byte
  * aligned.  Returns MOE_OK; MOE_ERR_INVALID_ARG (null or misaligned pointer,
  * T < 0, T >= 2^31, D or V < 1, scale not finite, unknown dtype);
  * MOE_ERR_UNSUPPORTED; MOE_ERR_HIP.  T == 0 launches nothing.
