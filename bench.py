@@ -437,12 +437,15 @@ def run_train_step(args):
           flush=True)
 
 
-def block_step_record(workload, steps, warmup):
+def block_step_record(workload, steps, warmup, vocab=0):
     """A pre-norm block's training step on one workload, its operators one
     after the other: residual sum and layer norm, router, layer (gate and up
     products kept), the layer's backward, the norm's backward, and a Muon step
     on each expert matrix and each of the shared expert's (fp32 weights beside
     the bf16 ones the layer reads; the gate's and the norm's weights stay).
+    With ``vocab`` entries the block is a whole model: its rows are looked up
+    by token, its output goes through a last norm into the cross entropy over
+    the same table, and the table's gradient comes from both ends.
     Each call is timed alone and the step as a whole (host clock between two
     synchronisations); one JSON line."""
     import torch
@@ -495,6 +498,39 @@ def block_step_record(workload, steps, warmup):
 
     calls = {"layer_norm": norm, "router_topk": router, "forward_save_gu": forward, "backward_cached": backward,
              "layer_norm_backward": norm_backward, f"muon_step_x{len(state)}": muon}
+    if vocab:
+        # tokens as a text has them: entry v about 1 / (v + 1) of them
+        tokens = ((vocab + 1.0) ** torch.rand(w.T + 1, generator=gen, device="cuda")).int() - 1
+        tokens = tokens.clamp_(0, vocab - 1)
+        ids, targets = tokens[:-1].contiguous(), tokens[1:].contiguous()
+        table, mean = n(vocab, w.D, by=w.D ** -0.5), torch.full((w.T,), 1.0 / w.T, device="cuda")
+        keep["dtable"] = torch.empty((vocab, w.D), device="cuda")
+
+        def embedding():
+            gg.embedding(ids, table, scale=w.D ** 0.5, out=x)
+
+        def last_norm():
+            keep["last"] = gg.layer_norm(keep["y"], ln_w, ln_b, residual=keep["f"]["h"])
+
+        def loss():
+            keep["loss"] = gg.cross_entropy(keep["last"]["y"], table, targets)
+
+        def loss_backward():
+            keep["dh"] = gg.cross_entropy_backward(keep["last"]["y"], table, targets, keep["loss"]["lse"], mean,
+                                                   out={"dW": keep["dtable"]})["dh"]
+
+        def last_norm_backward():
+            f = keep["last"]
+            gg.layer_norm_backward(f["h"], keep["dh"], f["rstd"], f["mean"], ln_w, bias_grad=True, out={"dx": dout})
+
+        def embedding_backward():
+            gg.embedding_backward(ids, keep["b"]["dx"], vocab, scale=w.D ** 0.5, out=keep["dtable"], accumulate=True)
+
+        ends = {"embedding": embedding, "layer_norm": norm, "router_topk": router, "forward_save_gu": forward,
+                "last_layer_norm": last_norm, "cross_entropy": loss, "cross_entropy_backward": loss_backward,
+                "last_layer_norm_backward": last_norm_backward, "backward_cached": backward,
+                "layer_norm_backward": norm_backward, "embedding_backward": embedding_backward}
+        calls = {**ends, **{k: f for k, f in calls.items() if k not in ends}}
     calls["step"] = lambda fs=tuple(calls.values()): [f() for f in fs]
     ms = {}
     for name, f in calls.items():
@@ -508,10 +544,12 @@ def block_step_record(workload, steps, warmup):
         ms[name] = (time.perf_counter() - t0) * 1e3 / steps
         log(f"{name}: {ms[name]:.4f} ms per call")
     return {
-        "metric": "pre-norm MoE block training step ms (norm, router, layer, backward, Muon)", "unit": "ms",
+        "metric": "pre-norm MoE block training step ms (norm, router, layer, backward, Muon)" if not vocab else
+                  "one-block MoE model training step ms (embedding, norm, router, layer, loss, backward, Muon)", "unit": "ms",
         "value": round(ms["step"], 5), "higher_is_better": False, "n_gpus": 1, "steps": steps, "warmup": warmup,
         "dtype": w.dtype, "data": "synthetic",
-        "config": {"workload": w.name, "T": w.T, "D": w.D, "F": w.F, "E": w.E, "k": w.k, "shared_expert": w.shared},
+        "config": {"workload": w.name, "T": w.T, "D": w.D, "F": w.F, "E": w.E, "k": w.k, "shared_expert": w.shared,
+                   **({"vocab": vocab} if vocab else {})},
         "ms_per_call": {k: round(v, 5) for k, v in ms.items()},
     }
 
@@ -939,6 +977,9 @@ def main():
                     help="time a pre-norm block's training step: layer norm, router, layer, its "
                          "backward, the norm's backward and a Muon step on the experts' and the shared "
                          "expert's matrices")
+    ap.add_argument("--vocab", type=int, default=0,
+                    help="with --block-step: a vocabulary of this many entries at both ends of the block "
+                         "(embedding lookup, last norm, cross entropy, and their gradients)")
     ap.add_argument("--routed", action="store_true",
                     help="time moe_ffn_forward_routed: the top-k router (x @ gate_w, top-k, softmax) "
                          "feeding the permute, then the same forward")
@@ -969,7 +1010,7 @@ def main():
         run_train_step(args)
         return
     if args.block_step:
-        print(json.dumps(block_step_record(args.workload, args.steps, args.warmup)), flush=True)
+        print(json.dumps(block_step_record(args.workload, args.steps, args.warmup, args.vocab)), flush=True)
         return
     if args.sweep:
         run_sweep(args)

@@ -463,7 +463,9 @@ template <bool DZ>
 hipError_t launch_logits(const VocabFew& a, hipStream_t s) {
     if (!fits(a)) return hipErrorInvalidValue;
     const int rb = a.T <= 32 ? 1 : 2;
-    const int64_t m_tiles = (a.T + 32 * rb - 1) / (32 * rb), grid = m_tiles * ((a.V + FN - 1) / FN);
+    // dz is written to the end of its rows: what reads it takes whole tiles, and
+    // zeros times what the workspace held would be no zeros
+    const int64_t m_tiles = (a.T + 32 * rb - 1) / (32 * rb), grid = m_tiles * (DZ ? a.dz_pitch / FN : ((a.V + FN - 1) / FN));
     if (grid > 1 << 23) return hipErrorInvalidValue;
     if (a.f32) {
         if (rb == 1) vocab_few_logits_kernel<true, 1, DZ><<<(unsigned)grid, 256, 0, s>>>(a, (int)m_tiles);

@@ -467,7 +467,7 @@ __global__ __launch_bounds__(256) void vocab_zero_kernel(O* p, int64_t n) {
 struct Plan {
     bool list;                // rows that count are listed first
     bool whole;               // logits by 256 x 256 tiles
-    bool few;                 // the products of few rows
+    bool few, few_dw;         // the products of few rows, dW's among them
     bool copy_W, copy_h;      // operands as padded bf16 planes
     int planes, products, Dp;
     int64_t n_tiles;          // stats: column tiles
@@ -482,6 +482,7 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     p.products = dtype == MOE_BF16 ? 1 : 6;
     const bool f32 = dtype != MOE_BF16;
     p.few = few_rows(T, D, V, f32, backward) && T * V * p.planes * 2 <= kDzBytes;
+    p.few_dw = p.few && (!f32 || T <= kFewDwRowsF32);
     // bf16 rows of whole K steps are read where they are
     p.copy_W = !p.few && (f32 || D % 32 != 0);
     p.copy_h = p.copy_W || p.list || backward;
@@ -519,7 +520,7 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
         p.dz = take(true, (size_t)p.planes * T * p.piece * 2);
         p.dz32 = take(p.few && f32, (size_t)T * p.piece * 4);
         p.dh_part = take(p.few, (size_t)(p.few ? vocab_few_splits(T, D, V, f32) : 0) * T * D * 4);
-        p.part = take(true, vocab_grad_partial_bytes(D));
+        p.part = take(!p.few_dw, vocab_grad_partial_bytes(D));
         p.acc = take(p.pieces > 1, (size_t)T * p.Dp * 4);
     }
     p.total = at;
@@ -698,7 +699,7 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
             q.out_bf16 = h16;
             TRY(launch_vocab_grad(q, s));
         }
-        if (dW && p.few && (h16 || a.T <= kFewDwRowsF32)) {
+        if (dW && p.few_dw) {
             TRY(launch_vocab_few_dw(w, dW, dW_dtype == MOE_BF16, s));
         } else if (dW) {
             q.dW = true;

@@ -53,6 +53,8 @@ def teacher64(ids, logits, V, tau):
     count = (ids >= 0) & (ids < V) & (logits != -math.inf)
     a = torch.where(count, logits.double() / tau, torch.full_like(logits, -math.inf, dtype=torch.float64))
     some = count.any(1, keepdim=True)
+    # the largest off first: at -1e39 even 64 bits would lose the logarithm of the sum
+    a = torch.where(some, a - a.max(1, keepdim=True).values, a)
     logq = torch.where(some, a - torch.logsumexp(torch.where(some, a, torch.zeros_like(a)), 1, keepdim=True), torch.zeros_like(a))
     q = torch.where(count, logq.exp(), torch.zeros_like(a))
     return count, q, torch.where(count, logq, torch.zeros_like(a))
