@@ -9,6 +9,10 @@
 //  dW:      dz^T h, 64 entries x 256 columns a workgroup: a few steps of K, then
 //           the store, which is all of the time; several workgroups a CU
 //
+// dz of bf16 operands is two planes of bf16, 16 bits together: there are matrix
+// instructions to spare, and so the gradients' own rounding is the only one
+// that counts.
+//
 // The table is read once, in its own type: bf16 on the bf16 matrix
 // instructions, fp32 on the fp32 ones (a sixteenth of the rate, which 64 rows
 // still do not need), with no copy in planes.  Four wavefronts, each with its
@@ -122,9 +126,14 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
             load_lds16(k + m_c[j] < bytes ? m_src[j] + k : (const char*)few_zeros, st + N_BYTES + (RB * wave + j) * 1024);
     };
     const int l = lane & 31, half = lane >> 5;
-    f32x16_t acc[RB];
+    // fp32: D / 2 terms follow one another in a sum, so there are several sums (one
+    // of them was off by twice what a library's product is)
+    constexpr int CH = !F32 ? 1 : RB == 1 ? 4 : 2;
+    f32x16_t sum[CH][RB];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) acc[rb] = f32x16_t{};
+    for (int q = 0; q < CH; ++q)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) sum[q][rb] = f32x16_t{};
     auto work = [&](const char* st) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -132,7 +141,14 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
                 const u32x4_t m = *(const u32x4_t*)(st + N_BYTES + (32 * rb + l) * 128 + (((2 * i + half) ^ swz8(32 * rb + l)) << 4));
-                acc[rb] = multiply<F32>(n, m, acc[rb]);
+                if constexpr (F32) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        sum[q % CH][rb] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(n[q]), __uint_as_float(m[q]),
+                                                                               sum[q % CH][rb], 0, 0, 0);
+                } else {
+                    sum[0][rb] = multiply<false>(n, m, sum[0][rb]);
+                }
             }
         }
     };
@@ -142,6 +158,16 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
     } else {
         char* const st[3] = {st0, st1, st2};
         ring<3, PER>(steps, st, issue, work);
+    }
+
+    f32x16_t (&acc)[RB] = sum[0];
+    if constexpr (CH > 1) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            if constexpr (CH == 4) sum[2][rb] += sum[3][rb];
+            acc[rb] += sum[1][rb];
+            if constexpr (CH == 4) acc[rb] += sum[2][rb];
+        }
     }
 
     // element v of acc on lane l: row l % 32, entry v0 + 32 w + 8 (v / 4) + 4 (l / 32) + v % 4
@@ -181,14 +207,15 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
                 float x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float p = __builtin_amdgcn_exp2f(fmaf(acc[rb][4 * vg + i], a.scale, -lse) * 1.4426950408889634f);
+                    const float d = fmaf(acc[rb][4 * vg + i], a.scale, -lse);
+                    float p = F32 ? exp_fp32(d) : __builtin_amdgcn_exp2f(d * 1.4426950408889634f);
                     if (at == 8 * vg + i) p -= 1.f;
                     // a row that does not count has an infinite lse: zeros, whatever h holds
                     x[i] = 8 * vg + i >= left || lse == INFINITY ? 0.f : p * g;
                 }
                 if constexpr (F32) *(float4*)(a.dz32 + row * a.dz_pitch + c0 + 8 * vg) = make_float4(x[0], x[1], x[2], x[3]);
 #pragma unroll
-                for (int pl = 0; pl < (F32 ? 3 : 1); ++pl) {
+                for (int pl = 0; pl < (F32 ? 3 : 2); ++pl) {
                     const uint32_t lo = pack_bf16(x[0], x[1]), hi = pack_bf16(x[2], x[3]);
                     *(uint2*)(a.dz + pl * a.dz_plane + row * a.dz_pitch + c0 + 8 * vg) = make_uint2(lo, hi);
                     x[0] -= __uint_as_float(lo << 16);
@@ -221,12 +248,15 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
 template <bool F32, int RB>
 __global__ __launch_bounds__(256, 2) void vocab_few_dh_kernel(const VocabFew a, int n_tiles, int m_tiles, int splits) {
     using E = typename Elem<F32>::type;
-    constexpr int NS = 4, PER = 5, KS = F32 ? 16 : 32, RPI = F32 ? 1 : 2;   // k rows of a DMA instruction
-    constexpr int ROW = 256 * sizeof(E), SB = N_BYTES + 4096;
+    constexpr int KS = F32 ? 16 : 32, RPI = F32 ? 1 : 2;       // k rows of a DMA instruction
+    // dz: 16 rows of 64 bytes an instruction, of fp32 or of two planes of bf16
+    constexpr int PLANES = F32 ? 1 : 2, MI = 2 * RB * PLANES, MJ = MI / 4 ? MI / 4 : 1;
+    constexpr int NS = RB == 1 ? 4 : 3, PER = 4 + MJ;
+    constexpr int ROW = 256 * sizeof(E), SB = N_BYTES + MI * 1024;
     __shared__ __attribute__((aligned(1024))) char st0[SB];
     __shared__ __attribute__((aligned(1024))) char st1[SB];
     __shared__ __attribute__((aligned(1024))) char st2[SB];
-    __shared__ __attribute__((aligned(1024))) char st3[SB];
+    __shared__ __attribute__((aligned(1024))) char st3[NS == 4 ? SB : 16];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int mt = blockIdx.x % m_tiles, rest = blockIdx.x / m_tiles;
@@ -248,18 +278,24 @@ __global__ __launch_bounds__(256, 2) void vocab_few_dh_kernel(const VocabFew a, 
         const int c = nt * 256 + ((lane % CPR) ^ swz(n_k[j])) * (16 / (int)sizeof(E));
         n_c[j] = c < a.D ? c : 0;                            // a column that exists; its sums are not stored
     }
-    // dz: 16 rows of 64 bytes an instruction, one a wavefront (with one block of
-    // rows twice over)
-    const int mr = 16 * (RB == 1 ? wave & 1 : wave) + (lane >> 2);
-    const int mc = (lane & 3) ^ ((mr >> 2) & 3);
-    const char* m_src = (F32 ? (const char*)a.dz32 : (const char*)a.dz) +
-                        (min(row0 + mr, a.T - 1) * a.dz_pitch * (int64_t)sizeof(E) + 16 * mc);
+    // instruction m of a stage: plane m / (2 RB), rows 16 (m % (2 RB)).. (fp32 with one
+    // block of rows has two for four wavefronts: twice over)
+    const char* m_src[MJ];
+#pragma unroll
+    for (int j = 0; j < MJ; ++j) {
+        const int m = (MJ * wave + j) % MI, r = 16 * (m % (2 * RB)) + (lane >> 2);
+        const int c = (lane & 3) ^ ((r >> 2) & 3);
+        m_src[j] = (F32 ? (const char*)a.dz32 : (const char*)(a.dz + m / (2 * RB) * a.dz_plane)) +
+                   (min(row0 + r, a.T - 1) * a.dz_pitch * (int64_t)sizeof(E) + 16 * c);
+    }
     auto issue = [&](int s, char* st) {
         const int64_t k = (int64_t)(first + min(s, steps - 1)) * KS;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             load_lds16((const E*)a.W + min(k + n_k[j], (int64_t)a.V - 1) * a.D + n_c[j], st + (4 * wave + j) * 1024);
-        load_lds16(m_src + k * (int64_t)sizeof(E), st + N_BYTES + (RB == 1 ? wave & 1 : wave) * 1024);
+#pragma unroll
+        for (int j = 0; j < MJ; ++j)
+            load_lds16(m_src[j] + k * (int64_t)sizeof(E), st + N_BYTES + (MJ * wave + j) % MI * 1024);
     };
     const int l = lane & 31, half = lane >> 5, G = lane >> 4, sl = lane & 15;
     f32x16_t acc[2][RB];
@@ -270,10 +306,13 @@ __global__ __launch_bounds__(256, 2) void vocab_few_dh_kernel(const VocabFew a, 
     auto work = [&](const char* st) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            u32x4_t m[RB];
+            u32x4_t m[PLANES][RB];
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
-                m[rb] = *(const u32x4_t*)(st + N_BYTES + (32 * rb + l) * 64 + (((2 * i + half) ^ ((l >> 2) & 3)) << 4));
+            for (int pl = 0; pl < PLANES; ++pl)
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb)
+                    m[pl][rb] = *(const u32x4_t*)(st + N_BYTES + (32 * (RB * pl + rb) + l) * 64 +
+                                                  (((2 * i + half) ^ ((l >> 2) & 3)) << 4));
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 u32x4_t n;
@@ -295,12 +334,19 @@ __global__ __launch_bounds__(256, 2) void vocab_few_dh_kernel(const VocabFew a, 
                     n = __builtin_bit_cast(u32x4_t, cat_bf16(h[0], h[1]));
                 }
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb) acc[b][rb] = multiply<F32>(n, m[rb], acc[b][rb]);
+                for (int pl = PLANES - 1; pl >= 0; --pl)
+#pragma unroll
+                    for (int rb = 0; rb < RB; ++rb) acc[b][rb] = multiply<F32>(n, m[pl][rb], acc[b][rb]);
             }
         }
     };
-    char* const st[4] = {st0, st1, st2, st3};
-    ring<NS, PER>(steps, st, issue, work);
+    if constexpr (NS == 4) {
+        char* const st[4] = {st0, st1, st2, st3};
+        ring<4, PER>(steps, st, issue, work);
+    } else {
+        char* const st[3] = {st0, st1, st2};
+        ring<3, PER>(steps, st, issue, work);
+    }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         const int64_t row = row0 + 32 * rb + l;
@@ -349,7 +395,7 @@ __global__ __launch_bounds__(256) void vocab_few_sum_kernel(const float* __restr
 template <bool F32, bool OUT16>
 __global__ __launch_bounds__(256, 4) void vocab_few_dw_kernel(const VocabFew a, int n_tiles, void* __restrict__ out) {
     using E = typename Elem<F32>::type;
-    constexpr int KS = F32 ? 16 : 32;
+    constexpr int KS = F32 ? 16 : 32, PLANES = F32 ? 1 : 2;
     constexpr int HROW = 256 * sizeof(E), ZROW = 64 * sizeof(E);   // bytes of a k row of h, of dz
     __shared__ __attribute__((aligned(1024))) char lds[32768];     // h's rows, dz's rows; then the output's
     constexpr int Z = 16384;
@@ -377,11 +423,12 @@ __global__ __launch_bounds__(256, 4) void vocab_few_dw_kernel(const VocabFew a, 
             const E* p = (const E*)a.h + (k0 + k) * a.h_pitch + (c < a.D ? c : 0);
             load_lds16(there ? (const void*)p : (const void*)few_zeros, lds + (4 * wave + j) * 1024);
         }
-        {
+#pragma unroll
+        for (int pl = 0; pl < PLANES; ++pl) {
             const int k = ZR * wave + lane / ZC;
-            const E* p = (F32 ? (const E*)a.dz32 : (const E*)a.dz) + (k0 + k) * a.dz_pitch + v0 +
+            const E* p = (F32 ? (const E*)a.dz32 : (const E*)a.dz + pl * a.dz_plane) + (k0 + k) * a.dz_pitch + v0 +
                          ((lane % ZC) ^ swz_z(k)) * (16 / (int)sizeof(E));
-            load_lds16(k0 + k < a.T ? (const void*)p : (const void*)few_zeros, lds + Z + wave * 1024);
+            load_lds16(k0 + k < a.T ? (const void*)p : (const void*)few_zeros, lds + Z + (4 * pl + wave) * 1024);
         }
         wait_vmem();
         __syncthreads();
@@ -403,24 +450,28 @@ __global__ __launch_bounds__(256, 4) void vocab_few_dw_kernel(const VocabFew a, 
         } else {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                bf16x8_t n[2], m[2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    s16x4_t x[2], y[2];
-                    const int R = 32 * b + 16 * (G & 1) + 4 * (sl & 3), C = 64 * wave + R;
+                auto frag = [&](const char* at, int row, int R, int swz_of_k(int)) {
+                    s16x4_t x[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const int k = 8 * (G >> 1) + 4 * r + (sl >> 2);
-                        x[r] = read_tr(lds + (16 * i + k) * HROW + (((C >> 3) ^ swz_tr(k)) << 4) + 8 * ((C >> 2) & 1));
-                        y[r] = read_tr(lds + Z + (16 * i + k) * ZROW + (((R >> 3) ^ swz_z(k)) << 4) + 8 * ((R >> 2) & 1));
+                        x[r] = read_tr(at + (16 * i + k) * row + (((R >> 3) ^ swz_of_k(k)) << 4) + 8 * ((R >> 2) & 1));
                     }
-                    n[b] = cat_bf16(x[0], x[1]);
-                    m[b] = cat_bf16(y[0], y[1]);
-                }
+                    return cat_bf16(x[0], x[1]);
+                };
+                const int R = 16 * (G & 1) + 4 * (sl & 3);
+                bf16x8_t n[2];
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < 2; ++b) n[b] = frag(lds, HROW, 64 * wave + 32 * b + R, [](int k) { return swz_tr(k); });
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) acc[b][e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n[b], m[e], acc[b][e], 0, 0, 0);
+                for (int pl = PLANES - 1; pl >= 0; --pl)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const bf16x8_t m = frag(lds + Z + 4096 * pl, ZROW, 32 * e + R, [](int k) { return 2 * (k & 3); });
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+                            acc[b][e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n[b], m, acc[b][e], 0, 0, 0);
+                    }
             }
         }
     }

@@ -429,6 +429,12 @@ __global__ __launch_bounds__(256, 2) void vocab_stats_kernel(const VocabStats a,
     }
 }
 
+// e^d, by way of 2^x for bf16 results.
+template <int PLANES>
+__device__ __forceinline__ float softmax_of(float d) {
+    return PLANES == 1 ? __builtin_amdgcn_exp2f(d * 1.4426950408889634f) : exp_fp32(d);
+}
+
 // PLANES: 1 (bf16) or 3.
 template <int PLANES>
 __global__ __launch_bounds__(256, 2) void vocab_dz_kernel(const VocabDz a, int n_tiles) {
@@ -461,7 +467,7 @@ __global__ __launch_bounds__(256, 2) void vocab_dz_kernel(const VocabDz a, int n
         for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
             for (int v = 0; v < 16; ++v)
-                e.acc[mi][nj][v] = __builtin_amdgcn_exp2f(fmaf(e.acc[mi][nj][v], a.inv_tau, -lse[nj]) * 1.4426950408889634f);
+                e.acc[mi][nj][v] = softmax_of<PLANES>(fmaf(e.acc[mi][nj][v], a.inv_tau, -lse[nj]));
         if (a.target) {
             const bool mine = target[nj] >= v0 + 64 * e.fw && target[nj] < min(v0 + 64 * e.fw + 64, a.V);
             if (__ballot(mine)) {
@@ -658,8 +664,7 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
                 for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
                     for (int v = 0; v < 16; ++v)
-                        e.acc[mi][nj][v] =
-                            __builtin_amdgcn_exp2f(fmaf(e.acc[mi][nj][v], a.scale, -in.y) * 1.4426950408889634f);
+                        e.acc[mi][nj][v] = softmax_of<PLANES>(fmaf(e.acc[mi][nj][v], a.scale, -in.y));
                 if (any) {
 #pragma unroll
                     for (int mi = 0; mi < 2; ++mi)
@@ -772,10 +777,11 @@ __host__ __device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64
     w.teams = kGradUnits / w.n_tiles;
     w.steps = (K + BK - 1) / BK;
     w.virt = w.steps ? w.steps * a.products : 1;
-    // parts cost what their write and their sum take, about 24 steps
+    // parts cost what their write and their sum take, about 32 steps (measured from 4 to
+    // 40: 512 to 9000 rows, even between 20 and 40)
     const int even = (int)(((int64_t)w.m_tiles * w.virt + w.teams - 1) / w.teams);
     const int whole = (w.m_tiles + w.teams - 1) / w.teams * w.virt;
-    w.split = even + 24 < whole;
+    w.split = even + 32 < whole;
     w.per = w.split ? (even > 8 ? even : 8) : whole > 1 ? whole : 1;
     return w;
 }

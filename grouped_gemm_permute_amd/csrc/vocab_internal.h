@@ -8,6 +8,15 @@
 
 namespace moe {
 
+// e^d for fp32 results: d log2(e) is rounded by up to |d| 2^-24 of the result, and
+// that rounding is made good.
+__device__ __forceinline__ float exp_fp32(float d) {
+    const float t = d * 1.4426950408889634f;
+    const float r = fmaf(d, 1.4426950408889634f, -t) + d * 1.9259629911266175e-8f;   // log2(e) - its fp32 value
+    const float e = __builtin_amdgcn_exp2f(t);
+    return t > -126.f ? fmaf(e, r * 0.6931471805599453f, e) : e;
+}
+
 // One operand of a product: bf16 rows, `planes` arrays of them `plane`
 // elements apart (an fp32 array is the sum of three such planes).
 struct VocabOperand {
@@ -107,7 +116,7 @@ struct VocabFew {
     int64_t part_pitch;
     float* zt;                // stats
     const float *g, *lse;     // dz: g / tau, lse
-    uint16_t* dz;             // bf16, or three planes: [T, pitch]
+    uint16_t* dz;             // two planes of bf16 (bf16), three (f32): [T, pitch]
     float* dz32;              // the same in fp32 (f32)
     int64_t dz_pitch, dz_plane;
     float* dh_part;           // [splits, T, D]

@@ -38,7 +38,7 @@ using namespace mfma;
 constexpr size_t kAlign = 256;
 constexpr int kMaxD = 16384, kMaxTop = 256;
 constexpr int64_t kMaxV = 1 << 24, kMaxT = 1 << 28;
-constexpr int64_t kListRows = 1024;
+constexpr int64_t kListRows = 1024, kListRowsF32 = 512;
 // Whether the products of few rows (vocab_few.hip) are the faster ones.  They read
 // the table once for 64 rows, the tiles of 128 x 256 once for 128, and those
 // leave compute units idle where they are few.  Measured, bf16: at 65536
@@ -470,6 +470,7 @@ struct Plan {
     bool few, few_dw;         // the products of few rows, dW's among them
     bool copy_W, copy_h;      // operands as padded bf16 planes
     int planes, products, Dp;
+    int dz_planes;
     int64_t n_tiles;          // stats: column tiles
     int64_t piece, pieces;    // entries of a piece (a multiple of 256), and how many
     size_t rows, pos, count, live, hc, info, Wc, part, zt, g, lse, dz, dz32, dh_part, acc, total;
@@ -477,7 +478,7 @@ struct Plan {
 
 Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     Plan p = {};
-    p.list = T >= kListRows;
+    p.list = T >= (dtype == MOE_BF16 ? kListRows : kListRowsF32);
     p.planes = dtype == MOE_BF16 ? 1 : 3;
     p.products = dtype == MOE_BF16 ? 1 : 6;
     const bool f32 = dtype != MOE_BF16;
@@ -486,6 +487,7 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     // bf16 rows of whole K steps are read where they are
     p.copy_W = !p.few && (f32 || D % 32 != 0);
     p.copy_h = p.copy_W || p.list || backward;
+    p.dz_planes = p.few && !f32 ? 2 : p.planes;
     // what is copied is padded to what the tiles of many rows take
     const int unit = p.copy_W && p.list ? 128 : 32;
     p.Dp = (D + unit - 1) / unit * unit;
@@ -517,7 +519,7 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
         p.g = take(true, (size_t)T * 4);
         p.lse = take(true, (size_t)T * 4);
         if (p.few) p.piece = p.n_tiles * tile, p.pieces = 1;
-        p.dz = take(true, (size_t)p.planes * T * p.piece * 2);
+        p.dz = take(true, (size_t)p.dz_planes * T * p.piece * 2);
         p.dz32 = take(p.few && f32, (size_t)T * p.piece * 4);
         p.dh_part = take(p.few, (size_t)(p.few ? vocab_few_splits(T, D, V, f32) : 0) * T * D * 4);
         p.part = take(!p.few_dw, vocab_grad_partial_bytes(D));
@@ -675,7 +677,7 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
         if (p.few) TRY(launch_vocab_few_dz(w, s));
         else TRY(p.whole ? launch_vocab_dz_whole(d, (const float4*)(ws + p.info), s) : launch_vocab_dz(d, s));
         if (!a.targets.target) {
-            TeacherArgs t = {a.targets, rows, z, g, l, inv_tau, v0, len, dz, p.piece, dz_plane, p.planes, w.dz32};
+            TeacherArgs t = {a.targets, rows, z, g, l, inv_tau, v0, len, dz, p.piece, dz_plane, p.dz_planes, w.dz32};
             vocab_teacher_kernel<<<(unsigned)a.T, 64, 0, s>>>(t);
             TRY(hipGetLastError());
         }
