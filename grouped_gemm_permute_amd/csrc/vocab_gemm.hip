@@ -351,6 +351,21 @@ __device__ __forceinline__ void logits_sources(E& e, const VocabOperand& h, cons
     e.kt_total = e.steps * products;
 }
 
+// A lane's 32 values of a row stand for columns 32 (v / 16) + 8 (v / 4 % 4) + v % 4
+// of 64 (less 4 for the upper lanes): whether column `at` is among them, and it.
+__device__ __forceinline__ bool has_column(int at) { return at >= 0 && at < 64 && !(at & 4); }
+__device__ __forceinline__ float column(const f32x16_t& x, const f32x16_t& y, int at) {
+    float e = 0.f;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+        e = at == 8 * (v / 4) + v % 4 ? x[v] : e;
+        e = at == 32 + 8 * (v / 4) + v % 4 ? y[v] : e;
+    }
+    return e;
+}
+// What rounding to bf16 takes from a value.
+__device__ __forceinline__ float rounding_of(float e) { return e - __uint_as_float(pack_bf16(e, 0.f) << 16); }
+
 // Of the 64 logits of a row that lanes l and l + 32 hold: the largest times c,
 // and the sum of 2^(z c - that).
 __device__ __forceinline__ float2 row_stats(const f32x16_t& x, const f32x16_t& y, float c) {
@@ -402,11 +417,8 @@ __global__ __launch_bounds__(256, 2) void vocab_stats_kernel(const VocabStats a,
             const bool mine = target >= v0 + 64 * e.fw && target < min(v0 + 64 * e.fw + 64, a.V);
             if (__ballot(mine)) {
                 const int at = mine ? (int)(target - v0) - 64 * e.fw - 4 * half : -1;
-#pragma unroll
-                for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        if (at == 32 * mi + 8 * (v / 4) + v % 4) a.zt[row] = e.acc[mi][nj][v];
+                const float z = column(e.acc[0][nj], e.acc[1][nj], at);
+                if (has_column(at)) a.zt[row] = z;
             }
         }
         if (left < TN) {
@@ -483,6 +495,14 @@ __global__ __launch_bounds__(256, 2) void vocab_dz_kernel(const VocabDz a, int n
         for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
             for (int v = 0; v < 16; ++v) e.acc[mi][nj][v] *= g[nj];
+        if (PLANES == 1 && a.err) {
+            const bool mine = target[nj] >= v0 + 64 * e.fw && target[nj] < min(v0 + 64 * e.fw + 64, a.V);
+            if (__ballot(mine)) {
+                const int at = mine ? (int)(target[nj] - v0) - 64 * e.fw - 4 * half : -1;
+                const float x = column(e.acc[0][nj], e.acc[1][nj], at);
+                if (has_column(at)) a.err[min(row0 + 32 * nj + l, rows - 1)] = rounding_of(x);
+            }
+        }
         if (left < TN) {
 #pragma unroll
             for (int mi = 0; mi < 2; ++mi)
@@ -558,6 +578,7 @@ struct WholeArgs {
     float* zt;                // stats, of compact rows
     uint16_t* dz;
     int64_t dz_pitch, dz_plane;
+    float* err;
 };
 
 template <bool DZ, int PLANES>
@@ -676,6 +697,10 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
                 for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
                     for (int v = 0; v < 16; ++v) e.acc[mi][nj][v] *= in.x;
+                if (PLANES == 1 && any && a.err) {
+                    const float x = column(e.acc[0][nj], e.acc[1][nj], target);
+                    if (mine && has_column(target) && row < rows) a.err[row] = rounding_of(x);
+                }
                 if (left < 64) {
 #pragma unroll
                     for (int mi = 0; mi < 2; ++mi)
@@ -716,12 +741,9 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
                     }
                 }
             } else {
-                if (any && row < rows) {
-#pragma unroll
-                    for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-                        for (int v = 0; v < 16; ++v)
-                            if (mine && target == 32 * mi + 8 * (v / 4) + v % 4) a.zt[row] = e.acc[mi][nj][v];
+                if (any) {
+                    const float z = column(e.acc[0][nj], e.acc[1][nj], target);
+                    if (mine && has_column(target) && row < rows) a.zt[row] = z;
                 }
                 if (left < 64) {
 #pragma unroll
@@ -802,6 +824,15 @@ __device__ __forceinline__ void grad_out(const VocabGrad& a, int64_t m, int n0, 
         if (!a.last) *p = v;
     }
     if (!a.last || n0 >= a.N) return;
+    if (!a.dW && a.err) {
+        const int entry = a.entry[m];
+        if (entry >= 0) {
+            const float e = a.err[m];
+            const uint2 w = *(const uint2*)(a.table + (int64_t)entry * a.table_pitch + n0);
+            v.x = fmaf(e, __uint_as_float(w.x << 16), v.x), v.y = fmaf(e, __uint_as_float(w.x & 0xffff0000u), v.y);
+            v.z = fmaf(e, __uint_as_float(w.y << 16), v.z), v.w = fmaf(e, __uint_as_float(w.y & 0xffff0000u), v.w);
+        }
+    }
     const int64_t at = (!a.dW && a.rows.rows ? (int64_t)a.rows.rows[m] : m) * a.N + n0;
     if (a.N % 4 == 0) {
         if (a.out_bf16)
@@ -976,7 +1007,7 @@ hipError_t launch_vocab_stats_whole(const VocabStats& a, const float4* info, hip
     if (a.K <= 0 || a.K % (4 * BK) || (a.products != 1 && a.products != 6) || a.rows.T <= 0 || a.V <= 0 || !info) return hipErrorInvalidValue;
     const int64_t n_tiles = (a.V + TN - 1) / TN;
     if ((a.rows.T + 255) / 256 * n_tiles > kMaxTiles) return hipErrorInvalidValue;
-    const WholeArgs w = {a.h, a.W, a.rows, info, a.V, 0, (int)a.V, a.K, a.products, a.c, a.part, a.part_pitch, a.zt, nullptr, 0, 0};
+    const WholeArgs w = {a.h, a.W, a.rows, info, a.V, 0, (int)a.V, a.K, a.products, a.c, a.part, a.part_pitch, a.zt, nullptr, 0, 0, nullptr};
     vocab_whole_kernel<false, 1><<<kWholeUnits, 512, 0, s>>>(w, (int)n_tiles);
     return hipGetLastError();
 }
@@ -985,7 +1016,7 @@ hipError_t launch_vocab_dz_whole(const VocabDz& a, const float4* info, hipStream
     if (a.K <= 0 || a.K % (4 * BK) || (a.products != 1 && a.products != 6) || a.rows.T <= 0 || a.len <= 0 || !info) return hipErrorInvalidValue;
     const int64_t n_tiles = ((int64_t)a.len + TN - 1) / TN;
     if (n_tiles * TN > a.dz_pitch || (a.rows.T + 255) / 256 * n_tiles > kMaxTiles) return hipErrorInvalidValue;
-    const WholeArgs w = {a.h, a.W, a.rows, info, a.V, a.v0, a.len, a.K, a.products, a.inv_tau, nullptr, 0, nullptr, a.dz, a.dz_pitch, a.dz_plane};
+    const WholeArgs w = {a.h, a.W, a.rows, info, a.V, a.v0, a.len, a.K, a.products, a.inv_tau, nullptr, 0, nullptr, a.dz, a.dz_pitch, a.dz_plane, a.err};
     if (a.products == 1) vocab_whole_kernel<true, 1><<<kWholeUnits, 512, 0, s>>>(w, (int)n_tiles);
     else vocab_whole_kernel<true, 3><<<kWholeUnits, 512, 0, s>>>(w, (int)n_tiles);
     return hipGetLastError();

@@ -69,6 +69,7 @@ struct VocabDz {
     const int32_t* target;
     uint16_t* dz;
     int64_t dz_pitch, dz_plane;
+    float* err;               // or null; [compact rows], with target: see VocabGrad
 };
 hipError_t launch_vocab_dz(const VocabDz& a, hipStream_t s);
 
@@ -96,6 +97,12 @@ struct VocabGrad {
     bool add, last;
     void* out;
     bool out_bf16;
+    // dh, or null: what rounding dz to bf16 took from entry `entry[m]` of row m, which
+    // makes up most of the row (its target); it is given back with the sum
+    const float* err;
+    const int32_t* entry;     // negative: none
+    const uint16_t* table;    // bf16, all of it
+    int64_t table_pitch;
 };
 size_t vocab_grad_partial_bytes(int N);
 hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s);

@@ -14,9 +14,11 @@
 // sum for each row and 256 entries, and a small kernel that joins those.  The
 // backward makes the logits again, a piece of the vocabulary at a time, turns
 // them into dz (at most kDzBytes of it) and multiplies that with W and with h.
-// dz is rounded to the operands' precision: bf16 for bf16 operands (half a step,
-// 2^-9 of each entry, about what the rounding of dh itself is), three planes of
-// bf16 for fp32 ones.
+// dz is rounded to the operands' precision: three planes of bf16 for fp32
+// operands, one for bf16 ones, half a step or 2^-9 of each entry.  Most of a row
+// is its target's entry (the teacher's largest), and what the rounding took from
+// that one is given back in dh; so dh and dW are off by little more than their own
+// rounding (1.4 times as much without).
 //
 // Rows that have no target (prompts, padding) take no part: from kListRows rows
 // on the rest are listed first and the products run on those alone; fewer are
@@ -176,6 +178,7 @@ struct CopyArgs {
     float inv_tau;
     float *g_out, *lse_out;
     float4* info;             // g / tau, lse and the target's bits, or null
+    int32_t* entry;           // the target, or null
     void* dh;                 // or null
 };
 
@@ -211,8 +214,9 @@ __global__ __launch_bounds__(256) void vocab_copy_kernel(const CopyArgs a) {
         }
         if (lane == 0 && t < a.T && (a.g || a.info)) {
             const float g = a.g && live ? a.g[t] * a.inv_tau : 0.f, lse = a.lse && live ? a.lse[t] : INFINITY;
+            const int target = a.targets.target && live ? a.targets.target[t] : -1;
+            if (a.entry) a.entry[to] = target;
             if (a.info) {
-                const int target = a.targets.target && live ? a.targets.target[t] : -1;
                 a.info[to] = make_float4(g, lse, __int_as_float(target), 0.f);
             }
             if (a.g_out) {
@@ -423,21 +427,27 @@ struct TeacherArgs {
     int64_t pitch, plane;
     int planes;
     float* dz32;              // the same in fp32, or null
+    float* err;               // or null: what rounding takes from the largest of the
+    int32_t* entry;           // row's entries, and which it is (see VocabGrad)
 };
 
 __global__ __launch_bounds__(64) void vocab_teacher_kernel(const TeacherArgs a) {
     __shared__ float q[kMaxTop], logq[kMaxTop];
     __shared__ int32_t id[kMaxTop];
     const int64_t i = blockIdx.x;
-    if (a.rows.count && i >= *a.rows.count) return;
+    if (i >= (a.rows.count ? *a.rows.count : a.rows.T)) return;
     const int64_t t = a.rows.rows ? a.rows.rows[i] : i;
-    const int K = a.targets.K;
-    if (!teacher_row(a.targets, t, a.inv_tau, q, logq, id)) return;
+    const int K = a.targets.K, lane = threadIdx.x;
+    const bool some = teacher_row(a.targets, t, a.inv_tau, q, logq, id);
     __syncthreads();
     const float g = a.g[i], lse = a.lse[i];
-    for (int k = threadIdx.x; k < K; k += 64) {
+    const bool first_piece = a.err && a.v0 == 0;
+    float most = -1.f, rest = 0.f;
+    int which = -1;
+    for (int k = lane; some && k < K; k += 64) {
         const int32_t v = id[k];
-        if (v < a.v0 || v >= a.v0 + a.len) continue;
+        const bool here = v >= a.v0 && v < a.v0 + a.len;
+        if (v < 0 || !(here || first_piece)) continue;
         float share = 0.f;
         bool first = true;
         for (int o = 0; o < K; ++o) {
@@ -446,7 +456,13 @@ __global__ __launch_bounds__(64) void vocab_teacher_kernel(const TeacherArgs a) 
             share += q[o];
         }
         if (!first) continue;
-        float x = g * (__builtin_amdgcn_exp2f(fmaf(a.z[t * K + k], a.inv_tau, -lse) * kLog2E) - share);
+        float x = g * (exp_fp32(fmaf(a.z[t * K + k], a.inv_tau, -lse)) - share);
+        if (fabsf(x) > most) {
+            most = fabsf(x);
+            rest = x - to_float(to_bf16(x));
+            which = v;
+        }
+        if (!here) continue;
         uint16_t* p = a.dz + i * a.pitch + (v - a.v0);
         if (a.dz32) a.dz32[i * a.pitch + (v - a.v0)] = x;
         for (int pl = 0; pl < a.planes; ++pl) {
@@ -454,6 +470,17 @@ __global__ __launch_bounds__(64) void vocab_teacher_kernel(const TeacherArgs a) 
             p[pl * a.plane] = o;
             x -= to_float(o);
         }
+    }
+    if (!first_piece) return;
+    for (int d = 32; d; d >>= 1) {
+        const float m = __shfl_xor(most, d), r = __shfl_xor(rest, d);
+        const int w = __shfl_xor(which, d);
+        // the lower entry where two are alike, so that all lanes agree
+        if (m > most || (m == most && w < which)) most = m, rest = r, which = w;
+    }
+    if (lane == 0) {
+        a.err[i] = rest;
+        a.entry[i] = which;
     }
 }
 
@@ -471,9 +498,10 @@ struct Plan {
     bool copy_W, copy_h;      // operands as padded bf16 planes
     int planes, products, Dp;
     int dz_planes;
+    bool give_back;           // what rounding takes from a row's largest entry of dz
     int64_t n_tiles;          // stats: column tiles
     int64_t piece, pieces;    // entries of a piece (a multiple of 256), and how many
-    size_t rows, pos, count, live, hc, info, Wc, part, zt, g, lse, dz, dz32, dh_part, acc, total;
+    size_t rows, pos, count, live, hc, info, Wc, part, zt, g, lse, err, entry, dz, dz32, dh_part, acc, total;
 };
 
 Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
@@ -488,6 +516,7 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     p.copy_W = !p.few && (f32 || D % 32 != 0);
     p.copy_h = p.copy_W || p.list || backward;
     p.dz_planes = p.few && !f32 ? 2 : p.planes;
+    p.give_back = p.dz_planes == 1 && D % 4 == 0;
     // what is copied is padded to what the tiles of many rows take
     const int unit = p.copy_W && p.list ? 128 : 32;
     p.Dp = (D + unit - 1) / unit * unit;
@@ -518,6 +547,8 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
         p.pieces = (p.n_tiles * tile + p.piece - 1) / p.piece;
         p.g = take(true, (size_t)T * 4);
         p.lse = take(true, (size_t)T * 4);
+        p.err = take(p.give_back, (size_t)T * 4);
+        p.entry = take(p.give_back, (size_t)T * 4);
         if (p.few) p.piece = p.n_tiles * tile, p.pieces = 1;
         p.dz = take(true, (size_t)p.dz_planes * T * p.piece * 2);
         p.dz32 = take(p.few && f32, (size_t)T * p.piece * 4);
@@ -658,6 +689,7 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
         CopyArgs c = {a.h, a.T, a.D, p.Dp, (uint16_t*)(ws + p.hc), h.plane};
         if (p.list) c.pos = (const int32_t*)(ws + p.pos), c.count = rows.count;
         if (p.whole) c.info = (float4*)(ws + p.info);
+        if (p.give_back) c.entry = (int32_t*)(ws + p.entry);
         c.targets = a.targets;
         c.g = dloss, c.lse = lse, c.inv_tau = inv_tau, c.g_out = g, c.lse_out = l;
         c.dh = dh;
@@ -668,7 +700,8 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
     const bool h16 = a.dtype == MOE_BF16;
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
         const int len = (int)std::min<int64_t>(p.piece, V - v0);
-        const VocabDz d = {h, W, rows, V, v0, len, p.Dp, p.products, inv_tau, g, l, a.targets.target, dz, p.piece, dz_plane};
+        const VocabDz d = {h, W, rows, V, v0, len, p.Dp, p.products, inv_tau, g, l, a.targets.target, dz, p.piece, dz_plane,
+                           p.give_back ? (float*)(ws + p.err) : nullptr};
         VocabFew w = {!h16, h16 ? (const void*)h.p : a.h, a.W, h16 ? h.pitch : a.D, a.T, a.D, V, inv_tau, a.targets.target};
         w.g = g, w.lse = l;
         w.dz = dz, w.dz32 = p.few && !h16 ? (float*)(ws + p.dz32) : nullptr;
@@ -677,7 +710,8 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
         if (p.few) TRY(launch_vocab_few_dz(w, s));
         else TRY(p.whole ? launch_vocab_dz_whole(d, (const float4*)(ws + p.info), s) : launch_vocab_dz(d, s));
         if (!a.targets.target) {
-            TeacherArgs t = {a.targets, rows, z, g, l, inv_tau, v0, len, dz, p.piece, dz_plane, p.dz_planes, w.dz32};
+            TeacherArgs t = {a.targets, rows, z, g, l, inv_tau, v0, len, dz, p.piece, dz_plane, p.dz_planes, w.dz32,
+                             d.err, (int32_t*)(ws + p.entry)};
             vocab_teacher_kernel<<<(unsigned)a.T, 64, 0, s>>>(t);
             TRY(hipGetLastError());
         }
@@ -699,12 +733,16 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
             q.last = v0 + p.piece >= V;
             q.out = dh;
             q.out_bf16 = h16;
+            q.err = d.err;
+            q.entry = (const int32_t*)(ws + p.entry);
+            q.table = (const uint16_t*)a.W, q.table_pitch = a.D;
             TRY(launch_vocab_grad(q, s));
         }
         if (dW && p.few_dw) {
             TRY(launch_vocab_few_dw(w, dW, dW_dtype == MOE_BF16, s));
         } else if (dW) {
             q.dW = true;
+            q.err = nullptr;
             q.n = h;
             q.acc = nullptr;
             q.add = false;
