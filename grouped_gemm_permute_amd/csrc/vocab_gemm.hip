@@ -61,6 +61,14 @@ __device__ __forceinline__ int fresh_lane() {
     return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, z));
 }
 
+// Orders a wavefront's LDS accesses for the compiler (the hardware keeps their
+// order), where lanes read what other lanes wrote.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The K loop of one tile.  MC / NC: the M / N operand's rows are contiguous in
 // K; else its rows are k and the tile's 256 columns are contiguous.
 template <bool MC, bool NC, int ROWS>
@@ -557,10 +565,140 @@ __global__ __launch_bounds__(256, 2) void vocab_dz_kernel(const VocabDz a, int n
 // through its tiles without a pause: the last steps of a tile load the next
 // one's first stages, which land under the epilogue.  What the epilogue wants of
 // a row (its g, lse and target) comes into LDS with a stage's loads.  K is a
-// multiple of 128: a tile begins and ends with the same stage buffer.  Against the
-// 128-row tiles each byte loaded feeds a third more products.
-using Whole = Engine<true, true, 256>;
+// multiple of 128: a tile begins and ends with the same stage buffer.
 constexpr int kWholeUnits = 256;
+
+// The K loop of a tile, in steps of 64: rows of 128 bytes, whole lines, in two
+// stage buffers of 64 KiB, one barrier a step.  A step begins with the operands of
+// its first half in registers:
+//   read the second half's, run the first half's MFMAs;
+//   wait for those and for the next stage, barrier: nobody reads this stage any
+//   more;
+//   load the stage after the next into its buffer, read the next stage's first
+//   half, run the second half's MFMAs.
+struct Wide {
+    static constexpr int ROW = 128, BYTES = 256 * ROW, NJ = 4;
+    const char *m_base, *n_base;
+    uint32_t m_at[4], n_at[4];
+    int64_t m_plane, n_plane;
+    int steps, ik, ip;                // K steps of a product; the next stage
+    int wave, fw, rw;
+    int m_off[4], n_off[4];           // of a lane's chunks, by 16 k of a step; its rows are constants away
+    f32x16_t acc[2][NJ];
+
+    struct Frags {
+        bf16x8_t n[2][2], m[2][NJ];
+    };
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+            for (int nj = 0; nj < NJ; ++nj) acc[mi][nj] = f32x16_t{};
+    }
+    // chunk c of row r, bytes from the row's first
+    // (swizzled by the row's place among 32: the blocks of 32 rows are alike)
+    static __device__ __forceinline__ int chunk(int c, int r) { return (c ^ ((r ^ ((r & 31) >> 3)) & 7)) << 4; }
+
+    __device__ __forceinline__ void begin() {
+        const int lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        fw = wave & 3;
+        rw = wave >> 2;
+        clear();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at = (lane & 31) * ROW + chunk(2 * k + (lane >> 5), lane & 31);
+            m_off[k] = 128 * rw * ROW + at;
+            n_off[k] = 64 * fw * ROW + at;
+        }
+    }
+
+    // Rows row0.. of h (`rows` in all) and v0.. of W (V).  DMA instruction j of a
+    // wavefront: rows 8 (4 w + j)..; lane -> row lane / 8, physical chunk lane % 8.
+    __device__ __forceinline__ void sources(const VocabOperand& h, const VocabOperand& W, int products, int64_t row0,
+                                            int64_t rows, int64_t v0, int64_t V) {
+        const int lane = fresh_lane();
+        m_base = (const char*)(h.p + row0 * h.pitch);
+        n_base = (const char*)(W.p + v0 * W.pitch);
+        const int mr = (int)min(rows - row0, (int64_t)256), nr = (int)min(V - v0, (int64_t)256);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 8 * (4 * wave + j) + (lane >> 3), c = chunk(lane & 7, r);
+            m_at[j] = (uint32_t)min(r, mr - 1) * (uint32_t)(2 * h.pitch) + c;
+            n_at[j] = (uint32_t)min(r, nr - 1) * (uint32_t)(2 * W.pitch) + c;
+        }
+        ip = 6 - products;
+        ik = 0;
+    }
+
+    __device__ __forceinline__ void issue(char* ms, char* ns) {
+        const int pm = (kPlaneM >> (2 * ip)) & 3, pn = (kPlaneN >> (2 * ip)) & 3;
+        const char* m = m_base + pm * m_plane + (int64_t)ik * ROW;
+        const char* n = n_base + pn * n_plane + (int64_t)ik * ROW;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_lds16(m + m_at[j], ms + (4 * wave + j) * 1024);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_lds16(n + n_at[j], ns + (4 * wave + j) * 1024);
+        // past the last stage it is read again
+        const bool end = ik + 1 == steps, turn = end && ip < 5;
+        ik = turn ? 0 : ik + (end ? 0 : 1);
+        ip += turn ? 1 : 0;
+    }
+
+    // Operands of half `h` of a stage: k 32 h + 16 ks + 8 (lane / 32)..
+    __device__ __forceinline__ void read_frags(const char* ms, const char* ns, int h, Frags& f) const {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+            for (int mi = 0; mi < 2; ++mi)
+                f.n[ks][mi] = __builtin_bit_cast(bf16x8_t, *(const u32x4_t*)(ns + n_off[2 * h + ks] + 32 * mi * ROW));
+#pragma unroll
+            for (int nj = 0; nj < NJ; ++nj)
+                f.m[ks][nj] = __builtin_bit_cast(bf16x8_t, *(const u32x4_t*)(ms + m_off[2 * h + ks] + 32 * nj * ROW));
+        }
+    }
+
+    __device__ __forceinline__ void mfmas(const Frags& f) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int nj = 0; nj < NJ; ++nj)
+#pragma unroll
+                for (int mi = 0; mi < 2; ++mi)
+                    acc[mi][nj] =
+                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.n[ks][mi], f.m[ks][nj], acc[mi][nj], 0, 0, 0);
+    }
+    static __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+    // The halves of a step around its wait and barrier.
+    __device__ __forceinline__ void first(const Frags& fa, Frags& fb, const char* ms, const char* ns) {
+        fence();
+        read_frags(ms, ns, 1, fb);
+        mfmas(fa);
+#pragma unroll
+        for (int i = 0; i < 12; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+        }
+        fence();
+    }
+    __device__ __forceinline__ void second(Frags& fa, const Frags& fb, char* ms, char* ns, const char* mnext, const char* nnext) {
+        fence();
+        issue(ms, ns);
+        read_frags(mnext, nnext, 0, fa);
+        mfmas(fb);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // vector memory
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        fence();
+    }
+};
 
 // Where dz's rows behind the last one go, so that every wavefront issues the
 // same number of stores whatever the tile holds.
@@ -583,12 +721,12 @@ struct WholeArgs {
 
 template <bool DZ, int PLANES>
 __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, int n_tiles) {
-    __shared__ __attribute__((aligned(1024))) char st0[Whole::SBYTES];
-    __shared__ __attribute__((aligned(1024))) char st1[Whole::SBYTES];
-    __shared__ __attribute__((aligned(1024))) char st2[Whole::SBYTES];
-    __shared__ __attribute__((aligned(1024))) char st3[Whole::SBYTES];
+    __shared__ __attribute__((aligned(1024))) char m0[Wide::BYTES];
+    __shared__ __attribute__((aligned(1024))) char m1[Wide::BYTES];
+    __shared__ __attribute__((aligned(1024))) char n0[Wide::BYTES];
+    __shared__ __attribute__((aligned(1024))) char n1[Wide::BYTES];
     __shared__ __attribute__((aligned(1024))) float4 infos[256];
-    __shared__ float2 sums[DZ ? 1 : 4][256];
+    __shared__ __attribute__((aligned(1024))) char extra[DZ ? 8 * 2048 : 4 * 256 * 8];   // dz on its way out, or the wavefronts' sums
     const int64_t rows = a.rows.count ? *a.rows.count : a.rows.T;
     const int m_tiles = (int)((rows + 255) / 256);
     // an XCD takes a contiguous range of tiles, its workgroups every 32nd of it;
@@ -599,7 +737,7 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
     int i = blockIdx.x >> 3;
     if (i >= count) return;
 
-    Whole e;
+    Wide e;
     e.begin();
     int64_t row0, c0;
     auto place = [&](int i) {
@@ -609,61 +747,50 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
         row0 = (int64_t)(g * kRows + (r - nt * in)) * 256;
         c0 = (int64_t)nt * TN;
     };
-    auto sources = [&] {
-        e.lane = fresh_lane();
-        logits_sources(e, a.h, a.W, a.products, a.K, row0, rows, a.v0 + c0, a.V);
-    };
+    auto sources = [&] { e.sources(a.h, a.W, a.products, row0, rows, a.v0 + c0, a.V); };
+    e.m_plane = 2 * a.h.plane;
+    e.n_plane = 2 * a.W.plane;
+    e.steps = a.K / 64;
     place(i);
     sources();
-    const int groups = e.steps * a.products / 4;
-    // vector memory operations behind a stage's loads: the next stage's, and
-    // right behind a tile's epilogue its stores
-    constexpr int usual = Whole::PER_STAGE, after = Whole::PER_STAGE + (DZ ? 16 * PLANES : 0);
-    auto ready = [] {
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(usual, 0));
-        __builtin_amdgcn_s_barrier();
-        Whole::fence();
-    };
-    auto ready_early = [](bool early) {
+    const int pairs = e.steps * a.products / 2;      // of steps
+    // at a step's barrier the next stage has landed; right behind a tile's epilogue
+    // its stores may still be on their way
+    constexpr int after = DZ ? 16 * PLANES : 0;
+    auto ready = [](bool early) {
         if (early) __builtin_amdgcn_s_waitcnt(waitcnt_imm(after, 0));
-        else __builtin_amdgcn_s_waitcnt(waitcnt_imm(usual, 0));
+        else __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
         __builtin_amdgcn_s_barrier();
-        Whole::fence();
     };
 
-    Whole::Frags fa, fb;
-    e.issue(st0);
-    e.issue(st1);
-    e.issue(st2);
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
-    __builtin_amdgcn_s_barrier();
-    Whole::fence();
-    e.read_frags(st0, fa);
-    Whole::fence();
+    Wide::Frags fa, fb;
+    e.issue(m0, n0);
+    e.issue(m1, n1);
+    ready(false);
+    Wide::fence();
+    e.read_frags(m0, n0, 0, fa);
     for (;;) {
         const int64_t tile_row = row0, tile_col = c0;
         const bool more = i + 32 < count;
         i += 32;
-        for (int g = 0; g < groups; ++g) {
-            ready_early(g == 0);
+        for (int g = 0; g < pairs; ++g) {
+            e.first(fa, fb, m0, n0);
+            ready(g == 0);
             if (g == 0) {
                 // 64 rows a wavefront (twice over)
                 const int r = 64 * (e.wave & 3);
                 const int in = min(fresh_lane(), (int)min(rows - 1 - tile_row - r, (int64_t)63));
                 load_lds16(a.info + tile_row + r + in, (char*)infos + 16 * r);
             }
-            e.work(fa, fb, st1, st3);
             // the next tile's sources, once this one's last stage is on its way
-            if (g + 1 == groups && more) {
+            if (g + 1 == pairs && more) {
                 place(i);
                 sources();
             }
-            ready_early(g == 0);
-            e.work(fb, fa, st2, st0);
-            ready();
-            e.work(fa, fb, st3, st1);
-            ready();
-            e.work(fb, fa, st0, st2);
+            e.second(fa, fb, m0, n0, m1, n1);
+            e.first(fa, fb, m1, n1);
+            ready(false);
+            e.second(fa, fb, m1, n1, m0, n0);
         }
 
         // ---- epilogue.  Element v of acc[mi][nj] on lane l: row 128 rw + 32 nj +
@@ -708,23 +835,23 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
                         for (int v = 0; v < 16; ++v)
                             if (32 * mi + 8 * (v / 4) + v % 4 >= left) e.acc[mi][nj][v] = 0.f;
                 }
-                // Through LDS, 32 rows of 128 bytes of the wavefront's own at a
-                // time (16-byte chunks XOR-swizzled by the row), so that a store
-                // writes whole lines; the buffer is free: its next stage comes
-                // behind the next barrier.
-                char* own = st3 + 4096 * e.wave;
+                // Through LDS, 16 rows of 128 bytes of the wavefront's own at a time
+                // (16-byte chunks XOR-swizzled by the row), so that a store writes
+                // whole lines (half lines, 131072 bytes apart: 1415 us against 1150).
+                char* own = extra + 2048 * e.wave;
                 const int sr = lane >> 3, sc = lane & 7;
                 uint16_t* out = a.dz + (tile_row + 128 * e.rw + 32 * nj + sr) * a.dz_pitch + tile_col + 64 * e.fw + 8 * sc;
                 const int64_t behind = rows - (tile_row + 128 * e.rw + 32 * nj + sr);
 #pragma unroll
                 for (int pl = 0; pl < PLANES; ++pl) {
+                    uint2 p[2][4];
 #pragma unroll
                     for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
                         for (int vg = 0; vg < 4; ++vg) {
                             f32x16_t& x = e.acc[mi][nj];
                             const uint32_t lo = pack_bf16(x[4 * vg], x[4 * vg + 1]), hi = pack_bf16(x[4 * vg + 2], x[4 * vg + 3]);
-                            *(uint2*)(own + l * 128 + (((4 * mi + vg) ^ (l & 7)) << 4) + 8 * half) = make_uint2(lo, hi);
+                            p[mi][vg] = make_uint2(lo, hi);
                             if (pl + 1 < PLANES) {
                                 x[4 * vg] -= __uint_as_float(lo << 16);
                                 x[4 * vg + 1] -= __uint_as_float(lo & 0xffff0000u);
@@ -733,11 +860,24 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
                             }
                         }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const u32x4_t v = *(const u32x4_t*)(own + (8 * q + sr) * 128 + ((sc ^ sr) << 4));
-                        // non-temporal: the tiles keep their L2 (1% of the whole backward)
-                        __builtin_nontemporal_store(
-                            v, 8 * q < behind ? (u32x4_t*)(out + pl * a.dz_plane + 8 * q * a.dz_pitch) : row_trash);
+                    for (int part = 0; part < 2; ++part) {
+                        if (l >> 4 == part) {
+#pragma unroll
+                            for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                                for (int vg = 0; vg < 4; ++vg)
+                                    *(uint2*)(own + (l & 15) * 128 + (((4 * mi + vg) ^ (l & 7)) << 4) + 8 * half) = p[mi][vg];
+                        }
+                        wave_sync();       // half the lanes wrote what all of them read
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int r = 16 * part + 8 * q;
+                            const u32x4_t v = *(const u32x4_t*)(own + (8 * q + sr) * 128 + ((sc ^ sr) << 4));
+                            // non-temporal: the tiles keep their L2 (1% of the whole backward)
+                            __builtin_nontemporal_store(
+                                v, r < behind ? (u32x4_t*)(out + pl * a.dz_plane + r * a.dz_pitch) : row_trash);
+                        }
+                        wave_sync();
                     }
                 }
             } else {
@@ -753,7 +893,7 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
                             if (32 * mi + 8 * (v / 4) + v % 4 >= left) e.acc[mi][nj][v] = -INFINITY;
                 }
                 const float2 s = row_stats(e.acc[0][nj], e.acc[1][nj], a.scale);
-                if (half == 0) sums[e.fw][r] = s;
+                if (half == 0) ((float2*)extra)[256 * e.fw + r] = s;
             }
         }
         if constexpr (!DZ) {
@@ -764,7 +904,7 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
             if (r < 256 && tile_row + r < rows) {
                 float2 p[4];
 #pragma unroll
-                for (int w = 0; w < 4; ++w) p[w] = sums[w][r];
+                for (int w = 0; w < 4; ++w) p[w] = ((const float2*)extra)[256 * w + r];
                 a.part[tile_col / TN * a.part_pitch + tile_row + r] = join_stats(p);
             }
         }
