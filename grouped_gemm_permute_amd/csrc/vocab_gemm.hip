@@ -700,10 +700,6 @@ struct Wide {
     }
 };
 
-// Where dz's rows behind the last one go, so that every wavefront issues the
-// same number of stores whatever the tile holds.
-__device__ __attribute__((aligned(16))) u32x4_t row_trash[1];
-
 struct WholeArgs {
     VocabOperand h, W;
     VocabRows rows;
@@ -841,7 +837,8 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
                 char* own = extra + 2048 * e.wave;
                 const int sr = lane >> 3, sc = lane & 7;
                 uint16_t* out = a.dz + (tile_row + 128 * e.rw + 32 * nj + sr) * a.dz_pitch + tile_col + 64 * e.fw + 8 * sc;
-                const int64_t behind = rows - (tile_row + 128 * e.rw + 32 * nj + sr);
+                // rows behind the last are computed as the last, and stored as it
+                const int behind = (int)min(rows - 1 - (tile_row + 128 * e.rw + 32 * nj + sr), (int64_t)32);
 #pragma unroll
                 for (int pl = 0; pl < PLANES; ++pl) {
                     uint2 p[2][4];
@@ -875,7 +872,7 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
                             const u32x4_t v = *(const u32x4_t*)(own + (8 * q + sr) * 128 + ((sc ^ sr) << 4));
                             // non-temporal: the tiles keep their L2 (1% of the whole backward)
                             __builtin_nontemporal_store(
-                                v, r < behind ? (u32x4_t*)(out + pl * a.dz_plane + r * a.dz_pitch) : row_trash);
+                                v, (u32x4_t*)(out + pl * a.dz_plane + min(r, behind) * a.dz_pitch));
                         }
                         wave_sync();
                     }

@@ -505,6 +505,16 @@ struct Plan {
     size_t rows, pos, count, live, hc, info, Wc, part, zt, g, lse, err, entry, dz, dz32, dh_part, acc, total;
 };
 
+// Whether rows that are not listed take the tiles of 256 x 256 (one workgroup a CU)
+// rather than those of 128 x 256 (two): where there is one for every CU and the last
+// row tile is more than half full.  Measured, bf16, forward with the copy of h that
+// they need, and dz: 512 rows of 32768 x 768 36 us against 38 and 31 against 38, 768
+// of 65536 82 against 93 and 105 against 126; 640 of 50001 74 against 65 and 72
+// against 67 (half full), 1000 of 8000 x 1024 38 against 31 (half the CUs).
+bool whole_tiles(int64_t T, int V) {
+    return (T - 1) % 256 >= 128 && (T + 255) / 256 * ((V + kVocabTileCols - 1) / kVocabTileCols) >= 256;
+}
+
 Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     Plan p = {};
     p.list = T >= (dtype == MOE_BF16 ? kListRows : kListRowsF32);
@@ -515,13 +525,14 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     p.few_dw = p.few && (!f32 || T <= kFewDwRowsF32);
     // bf16 rows of whole K steps are read where they are
     p.copy_W = !p.few && (f32 || D % 32 != 0);
-    p.copy_h = p.copy_W || p.list || backward;
+    const bool many = p.list || (!p.few && whole_tiles(T, V));
+    p.copy_h = p.copy_W || many || backward;
     p.dz_planes = p.few && !f32 ? 2 : p.planes;
     p.give_back = p.dz_planes == 1 && D % 4 == 0;
     // what is copied is padded to what the tiles of many rows take
-    const int unit = p.copy_W && p.list ? 128 : 32;
+    const int unit = p.copy_W && many ? 128 : 32;
     p.Dp = (D + unit - 1) / unit * unit;
-    p.whole = p.list && p.Dp % 128 == 0;
+    p.whole = many && p.Dp % 128 == 0;
     p.n_tiles = ((int64_t)V + kVocabTileCols - 1) / kVocabTileCols;
     if (p.few && !backward) p.n_tiles = ((int64_t)V + kVocabFewCols - 1) / kVocabFewCols;
     size_t at = 0;
