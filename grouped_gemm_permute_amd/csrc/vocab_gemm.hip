@@ -92,7 +92,7 @@ struct Engine {
     uint32_t m_at[MJ], n_at[WJ], m_most, n_most;
     int64_t m_plane, n_plane;         // bytes between planes
     int64_t m_step, n_step;           // bytes between K steps
-    int steps, kt_total;              // K steps of a product and of all
+    int steps;                        // K steps of a product
     int ik, ip;                       // the next stage: its step, its product
     int lane, wave, fw, rw;
     int m_off[NJ][2], n_off[2][2];    // fragment offsets in a stage
@@ -276,21 +276,21 @@ struct Engine {
         fence();
     }
 
-    // All K steps; on return no load is in flight and every wavefront has read
-    // the stages.
-    __device__ __forceinline__ void run(char* st0, char* st1, char* st2, char* st3) {
-        if (kt_total <= 0) return;
+    // `KT` K steps (at least 1); on return no load is in flight and every wavefront
+    // has read the stages.  256 rows: the caller has issued the first three stages and
+    // seen them land.
+    __device__ __forceinline__ void run(const int KT, char* st0, char* st1, char* st2, char* st3) {
         Frags fa, fb;
-        issue(st0);
-        issue(st1);
-        if constexpr (NS == 4) issue(st2);
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 2) * PER_STAGE, 15));
-        __builtin_amdgcn_s_barrier();
+        if constexpr (NS == 3) {
+            issue(st0);
+            issue(st1);
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(PER_STAGE, 15));
+            __builtin_amdgcn_s_barrier();
+        }
         fence();
         read_frags(st0, fa);
         fence();
         int kt = 0;
-        const int KT = kt_total;
         if constexpr (NS == 4) {
             for (; kt + 4 <= KT; kt += 4) {
                 step(fa, fb, st1, st3);
@@ -356,7 +356,6 @@ __device__ __forceinline__ void logits_sources(E& e, const VocabOperand& h, cons
     e.steps = K / BK;
     e.ip = 6 - products;
     e.ik = 0;
-    e.kt_total = e.steps * products;
 }
 
 // A lane's 32 values of a row stand for columns 32 (v / 16) + 8 (v / 4 % 4) + v % 4
@@ -411,7 +410,7 @@ __global__ __launch_bounds__(256, 2) void vocab_stats_kernel(const VocabStats a,
     Logits e;
     e.begin();
     logits_sources(e, a.h, a.W, a.products, a.K, row0, rows, v0, a.V);
-    e.run(st0, st1, st2, nullptr);
+    e.run(e.steps * a.products, st0, st1, st2, nullptr);
 
     const int l = e.lane & 31, half = e.lane >> 5;
     const int left = (int)min(a.V - v0, (int64_t)TN);
@@ -479,7 +478,7 @@ __global__ __launch_bounds__(256, 2) void vocab_dz_kernel(const VocabDz a, int n
         lse[nj] = a.lse[row], g[nj] = a.g[row];
         target[nj] = a.target ? a.target[a.rows.rows ? a.rows.rows[row] : row] : -1;
     }
-    e.run(st0, st1, st2, nullptr);
+    e.run(e.steps * a.products, st0, st1, st2, nullptr);
 
 #pragma unroll
     for (int nj = 0; nj < 4; ++nj) {
@@ -910,13 +909,18 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
     }
 }
 
-// The gradients' products run on one workgroup per CU.  A team of workgroups
-// takes the column tiles of the same 256 rows side by side, so that they read the
-// M operand once through their XCD's L2; the teams share out the K steps of all
-// row tiles evenly, each a contiguous range of them.  A tile whose steps one team
-// makes goes straight out; of any other each team writes its part (at most one
-// that it does not begin and one that it does not end) and a second kernel adds
-// them in order.
+// The gradients' products run on one workgroup per CU.  Where the tiles of all
+// K steps fill the CUs well enough, each workgroup takes whole ones and they go
+// straight out.  Else the steps are shared out: a team of workgroups takes the
+// column tiles of the same 256 rows side by side, so that they read the M operand
+// once through their XCD's L2, and writes its parts of tiles, which a second kernel
+// adds in order.  Where the row tiles divide the teams well, each team has a range
+// of the steps of one, the teams of one range next to each other (they read the
+// same of the N operand); else the teams share out the steps of all row tiles
+// evenly, each a contiguous range of them: at most one part that it does not begin
+// and one that it does not end, and whole tiles between.  Against the even shares
+// alone, in teams for whole tiles too, of 768 columns: dh of 512 rows and 32768 entries
+// 47 -> 37 us, dW of 512 and 65536 100 -> 68.
 constexpr int kGradUnits = 256;
 
 struct GradWork {
@@ -925,6 +929,7 @@ struct GradWork {
     int virt;                 // of a tile: those of all products, at least 1
     int per;                  // of a team
     bool split;               // tiles are divided between teams
+    bool even;                // ... evenly, else range by range
 };
 
 __host__ __device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64_t rows) {
@@ -939,15 +944,60 @@ __host__ __device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64
     // parts cost what their write and their sum take, about 32 steps (measured from 4 to
     // 40: 512 to 9000 rows, even between 20 and 40)
     const int even = (int)(((int64_t)w.m_tiles * w.virt + w.teams - 1) / w.teams);
-    const int whole = (w.m_tiles + w.teams - 1) / w.teams * w.virt;
+    const int whole = (int)(((int64_t)w.m_tiles * w.n_tiles + kGradUnits - 1) / kGradUnits) * w.virt;
     w.split = even + 32 < whole;
-    w.per = w.split ? (even > 8 ? even : 8) : whole > 1 ? whole : 1;
+    // ranges, unless they leave more than an eighth of the teams without work
+    const int ranges = w.m_tiles && w.m_tiles <= w.teams ? w.teams / w.m_tiles : 1;
+    const int range = (w.virt + ranges - 1) / ranges;
+    w.even = w.m_tiles > w.teams || range > even + even / 8;
+    const int per = w.even ? even : range;
+    w.per = per > 8 ? per : 8;
     return w;
 }
 
-// Where a team's part of a tile goes: [256][256] fp32.
-__device__ __forceinline__ float* grad_part(const VocabGrad& a, const GradWork& w, int team, bool begun, int nt) {
-    return a.partial + (((int64_t)team * 2 + (begun ? 0 : 1)) * w.n_tiles + nt) * 65536;
+// A workgroup's part of the work: steps k0 to k1 of a tile.
+struct GradPart {
+    int mt, nt, k0, k1;
+    int at;                   // the tile (whole), or the first step of the next part
+};
+
+// The first (at < 0) or the next part of the workgroup at `place`; false: none.
+__device__ __forceinline__ bool grad_next(const GradWork& w, int place, GradPart& p) {
+    const bool first = p.at < 0;
+    if (!w.split) {
+        p.at = first ? place : p.at + kGradUnits;
+        if (p.at >= w.m_tiles * w.n_tiles) return false;
+        p.mt = p.at / w.n_tiles;
+        p.nt = p.at - p.mt * w.n_tiles;
+        p.k0 = 0;
+        p.k1 = w.virt;
+        return true;
+    }
+    const int team = place / w.n_tiles;
+    if (team >= w.teams) return false;
+    p.nt = place - team * w.n_tiles;
+    if (!w.even) {
+        const int range = team / w.m_tiles;
+        p.mt = team - range * w.m_tiles;
+        p.k0 = range * w.per;
+        p.k1 = min(w.virt, p.k0 + w.per);
+        p.at = 0;
+        return first && p.k0 < w.virt;
+    }
+    if (first) p.at = team * w.per;
+    const int end = min((team + 1) * w.per, w.m_tiles * w.virt);
+    if (p.at >= end) return false;
+    p.mt = p.at / w.virt;
+    p.k0 = p.at - p.mt * w.virt;
+    p.k1 = min(w.virt, p.k0 + (end - p.at));
+    p.at += p.k1 - p.k0;
+    return true;
+}
+
+// Where a team's part of a tile goes: [256][256] fp32; slot 1 if the team begins
+// a tile that it shares with the next.
+__device__ __forceinline__ float* grad_part(const VocabGrad& a, const GradWork& w, int team, int slot, int nt) {
+    return a.partial + (((int64_t)team * 2 + slot) * w.n_tiles + nt) * 65536;
 }
 
 // Four columns n0.. of row m on their way out.
@@ -989,7 +1039,8 @@ __device__ __forceinline__ void grad_out(const VocabGrad& a, int64_t m, int n0, 
         }
 }
 
-// DW: both operands are k rows of columns; else M is K-contiguous.
+// DW: both operands are k rows of columns; else M is K-contiguous.  A part's first
+// three stages are loaded under the epilogue of the one before.
 template <bool DW>
 __global__ __launch_bounds__(512, 1) void vocab_grad_kernel(const VocabGrad a) {
     using Eng = Engine<!DW, false, 256>;
@@ -997,78 +1048,108 @@ __global__ __launch_bounds__(512, 1) void vocab_grad_kernel(const VocabGrad a) {
     __shared__ __attribute__((aligned(1024))) char st1[Eng::SBYTES];
     __shared__ __attribute__((aligned(1024))) char st2[Eng::SBYTES];
     __shared__ __attribute__((aligned(1024))) char st3[Eng::SBYTES];
+    __shared__ __attribute__((aligned(1024))) char out_[8 * 4096];
     const int64_t rows = a.rows.count ? *a.rows.count : a.rows.T;
     const GradWork w = grad_work(a, rows);
     // 32 consecutive places on an XCD
     const int place = (blockIdx.x & 7) * (kGradUnits / 8) + (blockIdx.x >> 3);
-    const int team = place / w.n_tiles, nt = place - team * w.n_tiles;
-    if (team >= w.teams) return;
     const int64_t M = DW ? a.len : rows;
-    const int64_t total = (int64_t)w.m_tiles * w.virt;
-    const int64_t end = min((int64_t)(team + 1) * w.per, total);
-    Eng e;
-    for (int64_t at = (int64_t)team * w.per; at < end;) {
-        const int mt = (int)(at / w.virt);
-        const int k0 = (int)(at - (int64_t)mt * w.virt), k1 = (int)min((int64_t)w.virt, k0 + (end - at));
-        at += k1 - k0;
-        const int64_t m0 = (int64_t)mt * 256;
+    const int last = ((DW ? (int)rows : a.len) - 1) % BK + 1;
+    GradPart now;
+    now.at = -1;
+    if (!grad_next(w, place, now)) return;
 
-        e.begin();
-        e.steps = w.steps;
-        e.ip = 6 - a.products + (w.steps ? k0 / w.steps : 0);
-        e.ik = w.steps ? k0 % w.steps : 0;
-        e.kt_total = w.steps ? k1 - k0 : 0;
-        e.m_plane = 2 * a.m.plane;
-        e.n_plane = 2 * a.n.plane;
-        const int last = ((DW ? (int)rows : a.len) - 1) % BK + 1;
+    Eng e;
+    e.begin();
+    e.steps = w.steps;
+    e.m_plane = 2 * a.m.plane;
+    e.n_plane = 2 * a.n.plane;
+    auto start = [&] {
+        if (!w.steps) return;
+        const int64_t row0 = (int64_t)now.mt * 256;
+        e.ip = 6 - a.products + now.k0 / w.steps;
+        e.ik = now.k0 % w.steps;
         if constexpr (DW) {
-            e.m_base = (const char*)(a.m.p + m0);      // dz's rows are whole tiles
+            e.m_base = (const char*)(a.m.p + row0);      // dz's rows are whole tiles
             e.m_ks(last, 2 * a.m.pitch);
         } else {
-            e.m_base = (const char*)(a.m.p + m0 * a.m.pitch);
-            e.m_rows((int)min(M - m0, (int64_t)256), 2 * a.m.pitch);
+            e.m_base = (const char*)(a.m.p + row0 * a.m.pitch);
+            e.m_rows((int)min(M - row0, (int64_t)256), 2 * a.m.pitch);
         }
         // k rows past the last: zeros behind h (dW), any of the table's against
         // dz's zeros (dh)
-        e.n_base = (const char*)(a.n.p + nt * TN);
-        e.n_ks(DW ? BK : last, 2 * a.n.pitch, (int)a.n.pitch - nt * TN);
-        e.run(st0, st1, st2, st3);
+        e.n_base = (const char*)(a.n.p + now.nt * TN);
+        e.n_ks(DW ? BK : last, 2 * a.n.pitch, (int)a.n.pitch - now.nt * TN);
+        e.issue(st0);
+        e.issue(st1);
+        e.issue(st2);
+    };
+    start();
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+    for (;;) {
+        __builtin_amdgcn_s_barrier();
+        if (w.steps) e.run(now.k1 - now.k0, st0, st1, st2, st3);
+        const GradPart was = now;
+        const bool more = grad_next(w, place, now);
+        if (more) start();
 
-        // Through LDS in two passes of 128 rows (those of the wavefronts rw =
-        // pass), block nj in stage buffer nj as 32 rows of 1 KiB, 16-byte chunks
-        // XOR-swizzled by the row; then each wavefront stores 16 rows.
-        float* part = k1 - k0 < w.virt ? grad_part(a, w, team, k0 > 0, nt) : nullptr;
-        auto buf = [&](int q) -> char* { return q == 0 ? st0 : q == 1 ? st1 : q == 2 ? st2 : st3; };
-        const int l = e.lane & 31;
+        // Through LDS, 16 rows of the wavefront's 64 columns at a time (16-byte chunks
+        // XOR-swizzled by the row), so that stores write whole lines.
+        const int64_t row0 = (int64_t)was.mt * 256;
+        float* part = nullptr;
+        if (was.k1 - was.k0 < w.virt) part = grad_part(a, w, place / w.n_tiles, w.even && was.k0 == 0, was.nt);
+        const int lane = fresh_lane(), l = lane & 31, half = lane >> 5, sr = lane >> 4, sc = lane & 15;
+        char* own = out_ + 4096 * e.wave;
+        const int n0 = was.nt * TN + 64 * e.fw + 4 * sc;
+        const bool plain = DW && a.N % 4 == 0;
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-            if (pass) __syncthreads();
-            if (e.rw == pass) {
-#pragma unroll
-                for (int nj = 0; nj < 4; ++nj)
+        for (int nj = 0; nj < 4; ++nj)
+#pragma unroll 1
+            for (int p = 0; p < 2; ++p) {      // kept small: the instructions are fetched as they run
+                if (l >> 4 == p) {
 #pragma unroll
                     for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
                         for (int vg = 0; vg < 4; ++vg) {
-                            const int c = 16 * e.fw + 8 * mi + 2 * vg + (e.lane >> 5);
                             const f32x16_t& v = e.acc[mi][nj];
-                            *(float4*)(buf(nj) + l * 1024 + ((c ^ l) << 4)) =
+                            *(float4*)(own + (l & 15) * 256 + (((8 * mi + 2 * vg + half) ^ (l & 15)) << 4)) =
                                 make_float4(v[4 * vg], v[4 * vg + 1], v[4 * vg + 2], v[4 * vg + 3]);
                         }
+                }
+                wave_sync();       // half the lanes wrote what all of them read
+                // the next part's stages have landed, before more stores than can be counted
+                if (nj == 2) __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+                const int tr = 128 * e.rw + 32 * nj + 16 * p + sr;
+                auto sum = [&](int q) { return *(const float4*)(own + (4 * q + sr) * 256 + ((sc ^ (4 * q + sr)) << 4)); };
+                if (part) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) *(float4*)(part + (tr + 4 * q) * 256 + 64 * e.fw + 4 * sc) = sum(q);
+                } else if (plain) {
+                    const int64_t at = (row0 + tr) * a.N + n0;
+                    const int behind = n0 < a.N ? (int)min(M - row0 - tr, (int64_t)16) : 0;
+                    if (a.out_bf16) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float4 v = sum(q);
+                            if (4 * q < behind)
+                                *(uint2*)((uint16_t*)a.out + at + 4 * q * a.N) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float4 v = sum(q);
+                            if (4 * q < behind) *(float4*)((float*)a.out + at + 4 * q * a.N) = v;
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q)
+                        if (row0 + tr + 4 * q < M) grad_out(a, row0 + tr + 4 * q, n0, sum(q));
+                }
+                wave_sync();
             }
-            __syncthreads();
-            const char* sq = buf(e.wave >> 1);
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-                const int r = 16 * (e.wave & 1) + i, tr = 128 * pass + 32 * (e.wave >> 1) + r;
-                const int64_t m = m0 + tr;
-                if (m >= M) break;
-                const float4 v = *(const float4*)(sq + r * 1024 + ((e.lane ^ r) << 4));
-                if (part) *(float4*)(part + tr * 256 + 4 * e.lane) = v;
-                else grad_out(a, m, nt * TN + 4 * e.lane, v);
-            }
-        }
-        __syncthreads();       // the stages are read out before they are filled again
+        if (!more) return;
+        e.clear();
     }
 }
 
@@ -1085,18 +1166,23 @@ __global__ __launch_bounds__(256) void vocab_grad_sum_kernel(const VocabGrad a) 
     const int mt = tile / w.n_tiles, nt = tile - mt * w.n_tiles;
     if (mt >= w.m_tiles) return;
     const int64_t M = a.dW ? a.len : rows;
-    const int64_t s0 = (int64_t)mt * w.virt, s1 = s0 + w.virt;
-    const int t0 = (int)(s0 / w.per), t1 = (int)((s1 - 1) / w.per);
-    if (t0 == t1) return;
+    if (!w.split) return;
+    // the tile's parts
+    const int t0 = w.even ? mt * w.virt / w.per : 0;
+    const int parts = w.even ? ((mt + 1) * w.virt - 1) / w.per - t0 + 1 : (w.virt + w.per - 1) / w.per;
+    if (parts == 1) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n0 = nt * TN + 4 * lane;
-    auto part = [&](int t, int tr) { return *(const float4*)(grad_part(a, w, t, t > t0, nt) + tr * 256 + 4 * lane); };
+    auto part = [&](int t, int tr) {
+        const float* p = w.even ? grad_part(a, w, t0 + t, t == 0, nt) : grad_part(a, w, t * w.m_tiles + mt, 0, nt);
+        return *(const float4*)(p + tr * 256 + 4 * lane);
+    };
     auto add = [](float4& v, float4 o) { v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w; };
     if constexpr (MANY) {
         const int64_t m = (int64_t)mt * 256 + slab;
         if (m >= M) return;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int t = t0 + wave; t <= t1; t += 4) add(v, part(t, slab));
+        for (int t = wave; t < parts; t += 4) add(v, part(t, slab));
         sums[wave][lane] = v;
         __syncthreads();
         if (wave || n0 >= a.N) return;
@@ -1110,9 +1196,9 @@ __global__ __launch_bounds__(256) void vocab_grad_sum_kernel(const VocabGrad a) 
             const int tr = 32 * slab + 4 * i + wave;
             const int64_t m = (int64_t)mt * 256 + tr;
             if (m >= M) break;
-            float4 v = part(t0, tr);
+            float4 v = part(0, tr);
 #pragma unroll 4
-            for (int t = t0 + 1; t <= t1; ++t) add(v, part(t, tr));
+            for (int t = 1; t < parts; ++t) add(v, part(t, tr));
             grad_out(a, m, n0, v);
         }
     }
