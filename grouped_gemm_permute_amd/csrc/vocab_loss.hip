@@ -41,23 +41,30 @@ constexpr size_t kAlign = 256;
 constexpr int kMaxD = 16384, kMaxTop = 256;
 constexpr int64_t kMaxV = 1 << 24, kMaxT = 1 << 28;
 constexpr int64_t kListRows = 1024, kListRowsF32 = 512;
-// Whether the products of few rows (vocab_few.hip) are the faster ones.  They read
-// the table once for 64 rows, the tiles of 128 x 256 once for 128, and those
-// leave compute units idle where they are few.  Measured, bf16: at 65536
-// entries x 768 and 65 rows 41 us against 28 (backward 108 against 118), at 20000
-// x 1024 and 192 rows 27 against 30 (80 against 104), at 256 rows 35 against 31 (96
-// against 113), at 8000 x 256 and 384 rows 11 against 16 (41 against 73).  fp32,
-// where the others begin with a copy of the table in planes: even at about 400
-// rows forward (65536 x 768: 356 us against 386 at 384) and 256 backward (793
-// against 795).
+// Whether the products of few rows (vocab_few.hip) are the faster ones: they read the
+// table once for 64 rows, the tiles of 128 or 256 rows less often, but those leave
+// compute units idle where they are few, and in fp32 they begin with a copy of the
+// table in planes.  Measured in us, few rows against tiles, rows x entries x D:
+//   bf16 backward  65 x 20000 x 768 58/70, 192 x 20000 x 768 78/78, 256 x 16000 x 768 76/81, 65 x 40000 x 768 91/87,
+//                  320 x 16384 x 768 96/83, 192 x 40000 x 768 130/108, 512 x 8000 x 512 68/79, 512 x 20000 x 256 84/81
+//   bf16 forward   128 x 32768 x 768 23/26, 65 x 40000 x 768 31/26, 256 x 16000 x 512 18/18, 512 x 16000 x 256 22/15
+//   fp32 backward  100 x 65536 x 768 400/479, 150 x 65536 x 768 515/493, 300 x 16000 x 768 253/264, 384 x 20000 x 768 341/308
+//   fp32 forward   128 x 65536 x 768 126/220, 256 x 65536 x 768 236/233, 384 x 65536 x 768 345/380, 384 x 8000 x 512 45/76
 bool few_rows(int64_t T, int D, int V, bool f32, bool backward) {
     if (D % (f32 ? 4 : 8)) return false;
-    if (f32) return T <= (backward ? 256 : 384);
-    return T <= 64 || (T <= 512 && (T + 63) / 64 * V <= (backward ? 2 : 1) * 65536);
+    if (T <= 64) return true;
+    const int64_t work = (T + 63) / 64 * V * std::max(D, 512);
+    if (f32) return T <= 384 && (!backward || work <= (T <= 256 ? 1 << 27 : 1 << 26));
+    if (T > 512) return false;
+    return work <= (backward ? 7 << 23 : T <= 192 ? 3 << 24 : 1 << 25);
 }
-// fp32 dW of few rows on its own kernel: 94 us against 110 at 65 rows of 65536 x
-// 768, even at 256; bf16 always (22 against 48 at 64, 42 against 67 at 256).
-constexpr int64_t kFewDwRowsF32 = 192;
+// dW of few rows on its own kernel: bf16 always (22 against 48 at 64 rows of 65536 x
+// 768); fp32 to 64 rows and for small tables (150 x 8000 x 512 31 against 37, 100 x
+// 16000 x 768 36 against 32, 100 x 65536 x 768 126 against 88, 384 x 2000 x 256 63
+// against 27).
+bool few_dw(int64_t T, int D, int V, bool f32) {
+    return !f32 || T <= 64 || (T <= 192 && (T + 63) / 64 * V * D <= 1 << 24);
+}
 // dz of one piece of the vocabulary: what ordinary steps take whole or in a few
 // pieces (32768 rows: 32768 entries), little of 288 GB.
 constexpr int64_t kDzBytes = 1ll << 31;
@@ -522,7 +529,7 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     p.products = dtype == MOE_BF16 ? 1 : 6;
     const bool f32 = dtype != MOE_BF16;
     p.few = few_rows(T, D, V, f32, backward) && T * V * p.planes * 2 <= kDzBytes;
-    p.few_dw = p.few && (!f32 || T <= kFewDwRowsF32);
+    p.few_dw = p.few && few_dw(T, D, V, f32);
     // bf16 rows of whole K steps are read where they are
     p.copy_W = !p.few && (f32 || D % 32 != 0);
     const bool many = p.list || (!p.few && whole_tiles(T, V));
