@@ -14,16 +14,23 @@
 // an fp32 product's own rounding.  Matrix cores take fp32 operands directly at
 // a sixteenth of the bf16 rate, six bf16 products cost a sixth.
 //
-// Tile engine (that of gemm_bf16.hip, with either layout of each operand): K
-// steps of 32, operands global -> LDS with 16-byte DMA into a ring of stages,
-// the next step's fragments read from LDS under this step's MFMAs.  The MFMA's
-// A operand is 32 columns of N, its B operand 32 rows of M, so that a lane ends
-// with 4 consecutive columns of one row.
-//  * stats and dz: 128 rows x 256 entries, 4 wavefronts, 3 stages of 24 KiB, two
-//    workgroups a CU: the exponentials of one (quarter rate, 128 a lane) run
-//    under the other's MFMAs;
-//  * grad: 256 x 256, 8 wavefronts, 4 stages of 32 KiB; K is long, the epilogue
-//    small.
+// Tile engines (after that of gemm_bf16.hip, with either layout of each operand):
+// operands global -> LDS with 16-byte DMA into a ring of stages, the next
+// fragments read from LDS under this step's MFMAs.  The MFMA's A operand is 32
+// columns of N, its B operand 32 rows of M, so that a lane ends with 4 consecutive
+// columns of one row.
+//  * stats and dz, many rows: 256 x 256, 8 wavefronts, K steps of 64 in two stages of
+//    64 KiB, one workgroup a CU that goes from tile to tile and loads the next one
+//    under the epilogue's exponentials (stats of 32768 x 768 x 65536: 2.61 to 2.93 ms, 1130
+//    to 1260 TFLOP/s, MFMA 58% busy at 2.0 GHz; a library's product of that shape, the
+//    logits written: 1130.  dz of half of it: 1.68 ms, 980 with its 2 GiB written, 53%);
+//  * stats and dz, fewer rows, or a D that is no multiple of 128: 128 x 256, 4
+//    wavefronts, K steps of 32 in 3 stages of 24 KiB, two workgroups a CU: the
+//    exponentials of one run under the other's MFMAs;
+//  * grad: 256 x 256, 8 wavefronts, K steps of 32 in 4 stages of 32 KiB, a workgroup a
+//    CU that goes from part to part (dh and dW of 32768 x 768 x 32768: 1.26 and 1.28 ms, 1300
+//    TFLOP/s, MFMA 70 to 74% busy).  In steps of 64 as above the same products took 2%
+//    longer.
 #include "mfma_common.h"
 #include "vocab_internal.h"
 
@@ -376,9 +383,12 @@ __device__ __forceinline__ float rounding_of(float e) { return e - __uint_as_flo
 // Of the 64 logits of a row that lanes l and l + 32 hold: the largest times c,
 // and the sum of 2^(z c - that).
 __device__ __forceinline__ float2 row_stats(const f32x16_t& x, const f32x16_t& y, float c) {
-    float top = -INFINITY;
+    // the larger of two as the middle of them and infinity: fmaxf would first quieten
+    // what may be a signalling NaN, 58 instructions for these 32 values against 24
+    float top = -INFINITY, most = INFINITY;
+    asm volatile("" : "+s"(most));
 #pragma unroll
-    for (int v = 0; v < 16; ++v) top = fmaxf(top, fmaxf(x[v], y[v]));
+    for (int v = 0; v < 16; ++v) top = fmaxf(top, __builtin_amdgcn_fmed3f(x[v], y[v], most));
     top = fmaxf(top, __shfl_xor(top, 32)) * c;
     const float off = top == -INFINITY ? 0.f : top;
     float sum = 0.f;

@@ -223,9 +223,7 @@ __global__ __launch_bounds__(256) void vocab_copy_kernel(const CopyArgs a) {
             const float g = a.g && live ? a.g[t] * a.inv_tau : 0.f, lse = a.lse && live ? a.lse[t] : INFINITY;
             const int target = a.targets.target && live ? a.targets.target[t] : -1;
             if (a.entry) a.entry[to] = target;
-            if (a.info) {
-                a.info[to] = make_float4(g, lse, __int_as_float(target), 0.f);
-            }
+            if (a.info) a.info[to] = make_float4(g, lse, __int_as_float(target), 0.f);
             if (a.g_out) {
                 a.g_out[to] = g;
                 a.lse_out[to] = lse;
