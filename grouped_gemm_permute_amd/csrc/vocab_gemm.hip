@@ -924,13 +924,14 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
 // straight out.  Else the steps are shared out: a team of workgroups takes the
 // column tiles of the same 256 rows side by side, so that they read the M operand
 // once through their XCD's L2, and writes its parts of tiles, which a second kernel
-// adds in order.  Where the row tiles divide the teams well, each team has a range
-// of the steps of one, the teams of one range next to each other (they read the
-// same of the N operand); else the teams share out the steps of all row tiles
-// evenly, each a contiguous range of them: at most one part that it does not begin
-// and one that it does not end, and whole tiles between.  Against the even shares
-// alone, in teams for whole tiles too, of 768 columns: dh of 512 rows and 32768 entries
-// 47 -> 37 us, dW of 512 and 65536 100 -> 68.
+// adds in order.  For dW each team first takes as many whole tiles as there are for
+// all: the teams go through K together and read the same of h, which the L2s then
+// hold.  Of what remains, where its row tiles divide the teams well, each team has a
+// range of the steps of one, the teams of one range next to each other; else the
+// teams share out its steps evenly, each a contiguous range of them: at most one part
+// that it does not begin and one that it does not end, and whole tiles between.
+// Against the even shares alone, in teams for whole tiles too, of 768 columns: dh of
+// 512 rows and 32768 entries 47 -> 37 us, dW of 512 and 65536 100 -> 68.
 constexpr int kGradUnits = 256;
 
 struct GradWork {
@@ -938,8 +939,9 @@ struct GradWork {
     int steps;                // K steps of one product
     int virt;                 // of a tile: those of all products, at least 1
     int per;                  // of a team
-    bool split;               // tiles are divided between teams
+    bool split;               // tiles are divided between teams, from tile `shared` on
     bool even;                // ... evenly, else range by range
+    int rounds, shared;       // whole tiles of a team before, of all teams
 };
 
 __host__ __device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64_t rows) {
@@ -951,15 +953,20 @@ __host__ __device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64
     w.teams = kGradUnits / w.n_tiles;
     w.steps = (K + BK - 1) / BK;
     w.virt = w.steps ? w.steps * a.products : 1;
+    // (dh gains nothing from whole tiles first: 32768 x 768 x 65536 2640 us against
+    // 2553, dW 2520 against 2578)
+    w.rounds = a.dW ? w.m_tiles / w.teams : 0;
+    w.shared = w.rounds * w.teams;
+    const int rest = w.m_tiles - w.shared;
     // parts cost what their write and their sum take, about 32 steps (measured from 4 to
     // 40: 512 to 9000 rows, even between 20 and 40)
-    const int even = (int)(((int64_t)w.m_tiles * w.virt + w.teams - 1) / w.teams);
+    const int even = (int)(((int64_t)rest * w.virt + w.teams - 1) / w.teams);
     const int whole = (int)(((int64_t)w.m_tiles * w.n_tiles + kGradUnits - 1) / kGradUnits) * w.virt;
-    w.split = even + 32 < whole;
+    w.split = w.rounds * w.virt + even + 32 < whole;
     // ranges, unless they leave more than an eighth of the teams without work
-    const int ranges = w.m_tiles && w.m_tiles <= w.teams ? w.teams / w.m_tiles : 1;
+    const int ranges = rest && rest <= w.teams ? w.teams / rest : 1;
     const int range = (w.virt + ranges - 1) / ranges;
-    w.even = w.m_tiles > w.teams || range > even + even / 8;
+    w.even = rest > w.teams || range > even + even / 8;
     const int per = w.even ? even : range;
     w.per = per > 8 ? per : 8;
     return w;
@@ -968,39 +975,44 @@ __host__ __device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64
 // A workgroup's part of the work: steps k0 to k1 of a tile.
 struct GradPart {
     int mt, nt, k0, k1;
-    int at;                   // the tile (whole), or the first step of the next part
+    int round;                // those taken so far; below 0: none
+    int at;                   // the first step of the next part (even)
 };
 
-// The first (at < 0) or the next part of the workgroup at `place`; false: none.
+// The workgroup's first (round < 0) or next part; false: none.
 __device__ __forceinline__ bool grad_next(const GradWork& w, int place, GradPart& p) {
-    const bool first = p.at < 0;
+    ++p.round;
+    p.k0 = 0;
+    p.k1 = w.virt;
     if (!w.split) {
-        p.at = first ? place : p.at + kGradUnits;
-        if (p.at >= w.m_tiles * w.n_tiles) return false;
-        p.mt = p.at / w.n_tiles;
-        p.nt = p.at - p.mt * w.n_tiles;
-        p.k0 = 0;
-        p.k1 = w.virt;
-        return true;
+        const int tile = place + p.round * kGradUnits;
+        p.mt = tile / w.n_tiles;
+        p.nt = tile - p.mt * w.n_tiles;
+        return p.mt < w.m_tiles;
     }
     const int team = place / w.n_tiles;
     if (team >= w.teams) return false;
     p.nt = place - team * w.n_tiles;
+    if (p.round < w.rounds) {
+        p.mt = p.round * w.teams + team;
+        return true;
+    }
+    const int rest = w.m_tiles - w.shared;
     if (!w.even) {
-        const int range = team / w.m_tiles;
-        p.mt = team - range * w.m_tiles;
+        const int range = team / rest;
+        p.mt = w.shared + team - range * rest;
         p.k0 = range * w.per;
         p.k1 = min(w.virt, p.k0 + w.per);
-        p.at = 0;
-        return first && p.k0 < w.virt;
+        return p.round == w.rounds && p.k0 < w.virt;
     }
-    if (first) p.at = team * w.per;
-    const int end = min((team + 1) * w.per, w.m_tiles * w.virt);
+    if (p.round == w.rounds) p.at = team * w.per;
+    const int end = min((team + 1) * w.per, rest * w.virt);
     if (p.at >= end) return false;
     p.mt = p.at / w.virt;
     p.k0 = p.at - p.mt * w.virt;
     p.k1 = min(w.virt, p.k0 + (end - p.at));
     p.at += p.k1 - p.k0;
+    p.mt += w.shared;
     return true;
 }
 
@@ -1066,7 +1078,7 @@ __global__ __launch_bounds__(512, 1) void vocab_grad_kernel(const VocabGrad a) {
     const int64_t M = DW ? a.len : rows;
     const int last = ((DW ? (int)rows : a.len) - 1) % BK + 1;
     GradPart now;
-    now.at = -1;
+    now.round = -1;
     if (!grad_next(w, place, now)) return;
 
     Eng e;
@@ -1176,14 +1188,15 @@ __global__ __launch_bounds__(256) void vocab_grad_sum_kernel(const VocabGrad a) 
     const int mt = tile / w.n_tiles, nt = tile - mt * w.n_tiles;
     if (mt >= w.m_tiles) return;
     const int64_t M = a.dW ? a.len : rows;
-    if (!w.split) return;
+    if (!w.split || mt < w.shared) return;
     // the tile's parts
-    const int t0 = w.even ? mt * w.virt / w.per : 0;
-    const int parts = w.even ? ((mt + 1) * w.virt - 1) / w.per - t0 + 1 : (w.virt + w.per - 1) / w.per;
+    const int of = mt - w.shared, rest = w.m_tiles - w.shared;
+    const int t0 = w.even ? of * w.virt / w.per : 0;
+    const int parts = w.even ? ((of + 1) * w.virt - 1) / w.per - t0 + 1 : (w.virt + w.per - 1) / w.per;
     if (parts == 1) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n0 = nt * TN + 4 * lane;
     auto part = [&](int t, int tr) {
-        const float* p = w.even ? grad_part(a, w, t0 + t, t == 0, nt) : grad_part(a, w, t * w.m_tiles + mt, 0, nt);
+        const float* p = w.even ? grad_part(a, w, t0 + t, t == 0, nt) : grad_part(a, w, t * rest + of, 0, nt);
         return *(const float4*)(p + tr * 256 + 4 * lane);
     };
     auto add = [](float4& v, float4 o) { v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w; };
