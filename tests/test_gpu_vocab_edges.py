@@ -12,8 +12,8 @@ from vocab_util import HALF, U, distill64, gradients64, loss64, product, within
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
-# each way through the kernels: few rows, tiles of 128 and of 256, listed rows on tiles of 128 (D no multiple of 128) and of 256
-WAYS = [(40, 64, 700), (600, 160, 70000), (500, 128, 65601), (1400, 96, 900), (1300, 128, 900)]
+# each way through the kernels: few rows (fp32 dW by few rows, by tiles), tiles of 128 and of 256, listed rows on tiles of 128 (D no multiple of 128) and of 256
+WAYS = [(40, 64, 700), (150, 72, 700), (200, 64, 900), (600, 160, 70000), (500, 128, 65601), (1400, 96, 900), (1300, 128, 900)]
 
 
 def backward(h, W, target, seed=0, **more):
