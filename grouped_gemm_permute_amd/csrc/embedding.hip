@@ -24,6 +24,9 @@
 //  join:  the sums of a long entry are added, in a fixed order, by the workgroup
 //         at its start.
 //
+// Up to kFewTokens tokens one launch does all of it: each workgroup finds the
+// tokens of its own entries (512 of 32768 entries x 768: 21 -> 13 us).
+//
 // Bound by memory: T rows read, V rows written (or, added, T at most read and written).
 #include "mfma_common.h"
 
@@ -40,6 +43,8 @@ using namespace mfma;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kLong = 32;              // tokens of an entry that one wavefront adds
+constexpr int kFewTokens = 1024;       // in one launch
+constexpr int kFewEntries = 2048;      // of a workgroup, at most
 constexpr int kMaxD = 16384;
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -289,21 +294,26 @@ __device__ __forceinline__ void add_to(Cols<W>& a, const Cols<W>& b) {
     for (int i = 0; i < W; ++i) a.x[i] += b.x[i];
 }
 
-// The sum of columns c.. of the rows of sorted tokens p0 .. p1 - 1, in order.
-template <typename E, int W>
-__device__ __forceinline__ Cols<W> sum_rows(const SumArgs& a, int p0, int p1, int c) {
+// The sum of columns c.. of the rows of sorted tokens p0 .. p1 - 1, in order;
+// token(p): which they are.
+template <typename E, int W, typename F>
+__device__ __forceinline__ Cols<W> sum_rows(const SumArgs& a, int p0, int p1, int c, F&& token) {
     Cols<W> s = {};
     const E* dy = (const E*)a.dy + c;
     int p = p0;
     for (; p + 8 <= p1; p += 8) {
         Cols<W> v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = load_cols<E, W>(dy + (int64_t)a.order[p + j] * a.D);
+        for (int j = 0; j < 8; ++j) v[j] = load_cols<E, W>(dy + (int64_t)token(p + j) * a.D);
 #pragma unroll
         for (int j = 0; j < 8; ++j) add_to(s, v[j]);
     }
-    for (; p < p1; ++p) add_to(s, load_cols<E, W>(dy + (int64_t)a.order[p] * a.D));
+    for (; p < p1; ++p) add_to(s, load_cols<E, W>(dy + (int64_t)token(p) * a.D));
     return s;
+}
+template <typename E, int W>
+__device__ __forceinline__ Cols<W> sum_rows(const SumArgs& a, int p0, int p1, int c) {
+    return sum_rows<E, W>(a, p0, p1, c, [&](int p) { return a.order[p]; });
 }
 
 template <typename O, int W>
@@ -370,6 +380,101 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const SumArgs a) {
             store_cols<float, W>(part + a.D + c, sum_rows<E, W>(a, bs, p1, c));
 }
 
+// Few tokens, in one launch: each workgroup looks through all ids for those of its
+// entries (far apart, as above), sorts them by entry and token in LDS and sums; an
+// entry of more than kLong tokens has its wavefronts side by side, a quarter of the
+// tokens each.  Most workgroups find none and write zeros.
+template <typename E, typename O, int W>
+__global__ __launch_bounds__(256) void embedding_few_kernel(const SumArgs a) {
+    constexpr int J = kFewTokens / 256;
+    __shared__ uint64_t hits[4 * J];
+    __shared__ int list[kFewTokens], sorted[kFewTokens];       // entry << 10 | token
+    __shared__ uint16_t begin[kFewEntries], count[kFewEntries];
+    __shared__ Cols<W> sums[4][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const unsigned blocks = (unsigned)a.row_blocks;
+    const int per_row = a.D / W;
+    const float inv = 1.f / per_row;
+    // an item's entry and columns; entries past the table are V
+    auto item = [&](int i, int& r, int& c) {
+        r = (int)((i + 0.5f) * inv);       // i / per_row, as above
+        c = (i - r * per_row) * W;
+        return r < a.rows ? min((int)blockIdx.x + r * (int)blocks, a.V) : a.V;
+    };
+    int key[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int t = 256 * j + tid;
+        const int id = t < a.T ? a.ids[t] : -1;
+        const unsigned r = (unsigned)id / blocks;
+        key[j] = id >= 0 && id < a.V && (unsigned)id - r * blocks == blockIdx.x ? (int)(r << 10) | t : -1;
+        const uint64_t m = __ballot(key[j] >= 0);
+        if (lane == 0) hits[4 * j + wave] = m;
+    }
+    __syncthreads();
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint64_t m = hits[4 * j + w];
+            if (w == wave && key[j] >= 0) list[n + __popcll(m & ((1ull << lane) - 1))] = key[j];
+            n += __popcll(m);
+        }
+    if (n == 0) {
+        if (a.add) return;
+        for (int i = tid; i < a.rows * per_row; i += 256) {
+            int r, c;
+            const int v = item(i, r, c);
+            if (v < a.V) write_cols<O, W>(a, v, c, Cols<W>{});
+        }
+        return;
+    }
+    for (int r = tid; r < a.rows; r += 256) count[r] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += 256) {
+        int rank = 0;
+        for (int k = 0; k < n; ++k) rank += list[k] < list[i];
+        sorted[rank] = list[i];
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += 256) {
+        const int r = sorted[i] >> 10;
+        if (i && sorted[i - 1] >> 10 == r) continue;
+        int e = i + 1;
+        while (e < n && sorted[e] >> 10 == r) ++e;
+        begin[r] = (uint16_t)i;
+        count[r] = (uint16_t)(e - i);
+    }
+    __syncthreads();
+    auto token = [&](int p) { return sorted[p] & 1023; };
+    for (int i = tid; i < a.rows * per_row; i += 256) {
+        int r, c;
+        const int v = item(i, r, c);
+        if (v >= a.V || count[r] > kLong || (a.add && count[r] == 0)) continue;
+        const int p = begin[r];
+        write_cols<O, W>(a, v, c, count[r] ? sum_rows<E, W>(a, p, p + count[r], c, token) : Cols<W>{});
+    }
+    for (int p = 0; p < n;) {
+        const int r = sorted[p] >> 10, m = count[r];
+        if (m > kLong) {
+            for (int c0 = 0; c0 < a.D; c0 += 64 * W) {
+                const int c = c0 + lane * W;
+                Cols<W> s = {};
+                if (c < a.D) s = sum_rows<E, W>(a, p + m * wave / 4, p + m * (wave + 1) / 4, c, token);
+                sums[wave][lane] = s;
+                __syncthreads();
+                if (wave == 0 && c < a.D) {
+                    for (int w = 1; w < 4; ++w) add_to(s, sums[w][lane]);
+                    write_cols<O, W>(a, (int)(blockIdx.x + r * blocks), c, s);
+                }
+                __syncthreads();
+            }
+        }
+        p += m;
+    }
+}
+
 // Workgroup: the long entry that begins in this chunk, if one does (it then
 // holds the chunk's last token).  64 groups of columns at a time, 16 wavefronts
 // each over every 16th part, then over the 16.
@@ -430,12 +535,23 @@ moe_status check(int64_t T, int D, int V, float scale, moe_dtype dtype) {
     return MOE_OK;
 }
 
+// Each workgroup reads all ids: with 1024 of 32768 entries x 768 17 us against 23 of the
+// three launches, of 300 x 64, the smallest tables, 19 against 17.
+bool few_tokens(int64_t T) { return T <= kFewTokens; }
+
 template <typename E, typename O, int W>
 hipError_t launch_sums(SumArgs a, int64_t chunks, hipStream_t s) {
     // about eight column groups a thread (32768 entries x 768 in bf16: 14.8 us, with
     // four 16.3, with two 19.1)
-    a.rows = std::max(1, 2048 / (a.D / W));
+    a.rows = std::max(1, kFewEntries / (a.D / W));
     a.row_blocks = ((int64_t)a.V + a.rows - 1) / a.rows;
+    if (few_tokens(a.T)) {
+        // and at least 1024 workgroups, where a few have most of the tokens
+        a.rows = std::max(1, std::min(a.rows, a.V >> 10));
+        a.row_blocks = ((int64_t)a.V + a.rows - 1) / a.rows;
+        embedding_few_kernel<E, O, W><<<(unsigned)a.row_blocks, 256, 0, s>>>(a);
+        return hipGetLastError();
+    }
     embedding_sum_kernel<E, O, W><<<(unsigned)(a.row_blocks + (chunks + 3) / 4), 256, 0, s>>>(a);
     if (hipError_t e = hipGetLastError()) return e;
     // 4 columns a thread: more loads in flight for the few rows there are
@@ -446,8 +562,13 @@ hipError_t launch_sums(SumArgs a, int64_t chunks, hipStream_t s) {
 
 template <typename E, typename O>
 hipError_t launch_backward(const SumArgs& a, int64_t chunks, hipStream_t s) {
-    // 16 bytes of dy a load where every row begins at a multiple of them
+    // 16 bytes of dy a load where every row begins at a multiple of them; 16 bytes of a
+    // table that is written whole (two stores of 16 side by side write half lines: fp32
+    // of 65536 x 768 86 us against 51, but added to 30 against 32)
     constexpr int W = Vec<E>::n;
+    if constexpr (sizeof(E) < sizeof(O)) {
+        if (!a.add && a.D % 4 == 0) return launch_sums<E, O, 4>(a, chunks, s);
+    }
     if (a.D % W == 0) return launch_sums<E, O, W>(a, chunks, s);
     return launch_sums<E, O, 1>(a, chunks, s);
 }
@@ -517,7 +638,7 @@ moe_status moe_embedding_backward(const int32_t* ids, const void* dy, void* dtab
     SumArgs a = {ids, (const int32_t*)(ws + l.order), (const int32_t*)(ws + l.first), (const int32_t*)(ws + l.count), dy, dtable, (float*)(ws + l.part),
                  T, D, V, scale, accumulate ? 1 : 0, 1, 0};
     (void)hipGetLastError();
-    if (launch_sort(ids, T, V, (int32_t*)(ws + l.order), (int32_t*)(ws + l.first),
+    if (!few_tokens(T) && launch_sort(ids, T, V, (int32_t*)(ws + l.order), (int32_t*)(ws + l.first),
                     (int32_t*)(ws + l.count), stream) != hipSuccess) return MOE_ERR_HIP;
     const bool in16 = dtype == MOE_BF16, out16 = table_dtype == MOE_BF16;
     const hipError_t e = in16 && out16 ? launch_backward<uint16_t, uint16_t>(a, l.chunks, stream)

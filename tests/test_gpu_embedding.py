@@ -29,7 +29,10 @@ def tokens(T, V, seed, kind):
 
 
 SIZES = [(1, 1, 1), (1, 768, 50), (5, 3, 1), (64, 8, 17), (65, 20, 5), (128, 768, 2), (513, 33, 1000), (1000, 1024, 300),
-         (4097, 129, 5000), (9000, 96, 40), (300, 64, 20000)]
+         (4097, 129, 5000), (9000, 96, 40), (300, 64, 20000),
+         # beside the most tokens that take one launch
+         (1023, 8, 3000), (1024, 12, 5000), (1024, 33, 1000), (1025, 1, 1), (1025, 8, 17), (1100, 20, 5), (1500, 768, 50),
+         (2000, 1024, 300), (3000, 64, 20000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
