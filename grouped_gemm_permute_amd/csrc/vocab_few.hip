@@ -200,8 +200,10 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
             sum += __shfl_xor(sum, 32);
             if (half == 0) sums[wave * 32 * RB + 32 * rb + l] = make_float2(top, sum);
         } else {
-            if (!there) continue;
-            const float lse = a.lse[row], g = a.g[row];
+            // Through LDS, so that rows go out in whole lines: 32 of 128 entries in fp32,
+            // 16-byte chunks XOR-swizzled by the row.
+            const float lse = there ? a.lse[row] : INFINITY, g = there ? a.g[row] : 0.f;
+            if (rb) __syncthreads();
 #pragma unroll
             for (int vg = 0; vg < 4; ++vg) {
                 float x[4];
@@ -213,15 +215,28 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
                     // a row that does not count has an infinite lse: zeros, whatever h holds
                     x[i] = 8 * vg + i >= left || lse == INFINITY ? 0.f : p * g;
                 }
-                if constexpr (F32) *(float4*)(a.dz32 + row * a.dz_pitch + c0 + 8 * vg) = make_float4(x[0], x[1], x[2], x[3]);
+                *(float4*)(st0 + l * 512 + (((8 * wave + 2 * vg + half) ^ l) << 4)) = make_float4(x[0], x[1], x[2], x[3]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + (tid >> 5);
+                const int64_t m = row0 + 32 * rb + r;
+                if (m >= a.T) break;
+                float4 x = *(const float4*)(st0 + r * 512 + (((tid & 31) ^ r) << 4));
+                const int64_t to = m * a.dz_pitch + v0 + 4 * (tid & 31);
+                if constexpr (F32) {
+                    *(float4*)(a.dz32 + to) = x;
+                    if (!a.dz) continue;
+                }
 #pragma unroll
                 for (int pl = 0; pl < (F32 ? 3 : 2); ++pl) {
-                    const uint32_t lo = pack_bf16(x[0], x[1]), hi = pack_bf16(x[2], x[3]);
-                    *(uint2*)(a.dz + pl * a.dz_plane + row * a.dz_pitch + c0 + 8 * vg) = make_uint2(lo, hi);
-                    x[0] -= __uint_as_float(lo << 16);
-                    x[1] -= __uint_as_float(lo & 0xffff0000u);
-                    x[2] -= __uint_as_float(hi << 16);
-                    x[3] -= __uint_as_float(hi & 0xffff0000u);
+                    const uint32_t lo = pack_bf16(x.x, x.y), hi = pack_bf16(x.z, x.w);
+                    *(uint2*)(a.dz + pl * a.dz_plane + to) = make_uint2(lo, hi);
+                    x.x -= __uint_as_float(lo << 16);
+                    x.y -= __uint_as_float(lo & 0xffff0000u);
+                    x.z -= __uint_as_float(hi << 16);
+                    x.w -= __uint_as_float(hi & 0xffff0000u);
                 }
             }
         }

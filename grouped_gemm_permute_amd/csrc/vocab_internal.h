@@ -123,7 +123,7 @@ struct VocabFew {
     int64_t part_pitch;
     float* zt;                // stats
     const float *g, *lse;     // dz: g / tau, lse
-    uint16_t* dz;             // two planes of bf16 (bf16), three (f32): [T, pitch]
+    uint16_t* dz;             // two planes of bf16 (bf16), three (f32; or null): [T, pitch]
     float* dz32;              // the same in fp32 (f32)
     int64_t dz_pitch, dz_plane;
     float* dh_part;           // [splits, T, D]

@@ -570,7 +570,7 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
         // an odd number of 512 bytes: rows 2^n bytes apart meet in a few of the memory's
         // channels (131072 bytes: dz 1318 us, 131584: 1150)
         p.pitch = (p.piece / 256 | 1) * 256;
-        p.dz = take(true, (size_t)p.dz_planes * T * p.pitch * 2);
+        p.dz = take(!f32 || !p.few_dw, (size_t)p.dz_planes * T * p.pitch * 2);
         p.dz32 = take(p.few && f32, (size_t)T * p.pitch * 4);
         p.dh_part = take(p.few, (size_t)(p.few ? vocab_few_splits(T, D, V, f32) : 0) * T * D * 4);
         p.part = take(!p.few_dw, vocab_grad_partial_bytes(D));
@@ -724,13 +724,15 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
                            p.give_back ? (float*)(ws + p.err) : nullptr};
         VocabFew w = {!h16, h16 ? (const void*)h.p : a.h, a.W, h16 ? h.pitch : a.D, a.T, a.D, V, inv_tau, a.targets.target};
         w.g = g, w.lse = l;
-        w.dz = dz, w.dz32 = p.few && !h16 ? (float*)(ws + p.dz32) : nullptr;
+        // of fp32 operands, planes only for a dW by tiles
+        const bool planes = !p.few || h16 || (dW && !p.few_dw);
+        w.dz = planes ? dz : nullptr, w.dz32 = p.few && !h16 ? (float*)(ws + p.dz32) : nullptr;
         w.dz_pitch = p.pitch, w.dz_plane = dz_plane;
         w.dh_part = (float*)(ws + p.dh_part);
         if (p.few) TRY(launch_vocab_few_dz(w, s));
         else TRY(p.whole ? launch_vocab_dz_whole(d, (const float4*)(ws + p.info), s) : launch_vocab_dz(d, s));
         if (!a.targets.target) {
-            TeacherArgs t = {a.targets, rows, z, g, l, inv_tau, v0, len, dz, p.pitch, dz_plane, p.dz_planes, w.dz32,
+            TeacherArgs t = {a.targets, rows, z, g, l, inv_tau, v0, len, dz, p.pitch, dz_plane, planes ? p.dz_planes : 0, w.dz32,
                              d.err, (int32_t*)(ws + p.entry)};
             vocab_teacher_kernel<<<(unsigned)a.T, 64, 0, s>>>(t);
             TRY(hipGetLastError());
