@@ -116,8 +116,15 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
         m_c[j] = 16 * ((lane & 7) ^ swz8(r));
         m_src[j] = (const char*)a.h + min(row0 + r, a.T - 1) * a.h_pitch * (int64_t)sizeof(E) + m_c[j];
     }
+    // each tile begins elsewhere in K where rows are whole 2 KiB apart and the table's
+    // bytes are all there is to wait for: else all tiles read from the same few of the
+    // memory's channels (one row, fp32 32768 x 4096 145 -> 107 us, 131072 x 1024 128 ->
+    // 108, bf16 131072 x 4096 216 -> 177; 64 rows lose 5%)
+    const int turn = RB == 1 && bytes % 2048 == 0 ? blockIdx.x / m_tiles % steps : 0;
     auto issue = [&](int s, char* st) {
-        const int64_t k = (int64_t)min(s, steps - 1) * 128;
+        int at = min(s, steps - 1);
+        if (RB == 1) at = at + turn < steps ? at + turn : at + turn - steps;
+        const int64_t k = (int64_t)at * 128;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             load_lds16(k + n_c[j] < bytes ? n_src[j] + k : (const char*)few_zeros, st + (4 * wave + j) * 1024);
