@@ -134,8 +134,9 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
     };
     const int l = lane & 31, half = lane >> 5;
     // fp32: D / 2 terms follow one another in a sum, so there are several sums (one
-    // of them was off by twice what a library's product is)
-    constexpr int CH = !F32 ? 1 : RB == 1 ? 4 : 2;
+    // of them was off by twice what a library's product is), joined in 64 bits: a
+    // row's entry at its target is a small difference of large ones
+    constexpr int CH = !F32 ? 1 : RB == 1 ? 8 : 4;
     f32x16_t sum[CH][RB];
 #pragma unroll
     for (int q = 0; q < CH; ++q)
@@ -151,8 +152,8 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
                 if constexpr (F32) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        sum[q % CH][rb] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(n[q]), __uint_as_float(m[q]),
-                                                                               sum[q % CH][rb], 0, 0, 0);
+                        sum[(4 * i + q) % CH][rb] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                            __uint_as_float(n[q]), __uint_as_float(m[q]), sum[(4 * i + q) % CH][rb], 0, 0, 0);
                 } else {
                     sum[0][rb] = multiply<false>(n, m, sum[0][rb]);
                 }
@@ -168,13 +169,17 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
     }
 
     f32x16_t (&acc)[RB] = sum[0];
-    if constexpr (CH > 1) {
+    auto joined = [&](int rb, int v) {
+        double z = 0;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            if constexpr (CH == 4) sum[2][rb] += sum[3][rb];
-            acc[rb] += sum[1][rb];
-            if constexpr (CH == 4) acc[rb] += sum[2][rb];
-        }
+        for (int q = 0; q < CH; ++q) z += sum[q][rb][v];
+        return z;
+    };
+    if constexpr (F32 && !DZ) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[rb][v] = (float)joined(rb, v);
     }
 
     // element v of acc on lane l: row l % 32, entry v0 + 32 w + 8 (v / 4) + 4 (l / 32) + v % 4
@@ -216,8 +221,9 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
                 float x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float d = fmaf(acc[rb][4 * vg + i], a.scale, -lse);
-                    float p = F32 ? exp_fp32(d) : __builtin_amdgcn_exp2f(d * 1.4426950408889634f);
+                    float p;
+                    if constexpr (F32) p = exp_fp32((float)fma(joined(rb, 4 * vg + i), (double)a.scale, -(double)lse));
+                    else p = __builtin_amdgcn_exp2f(fmaf(acc[rb][4 * vg + i], a.scale, -lse) * 1.4426950408889634f);
                     if (at == 8 * vg + i) p -= 1.f;
                     // a row that does not count has an infinite lse: zeros, whatever h holds
                     x[i] = 8 * vg + i >= left || lse == INFINITY ? 0.f : p * g;
