@@ -283,6 +283,20 @@ struct Engine {
         fence();
     }
 
+    // The loads and barriers of run() for a wavefront without rows of its own.
+    __device__ __forceinline__ void idle(const int KT, char* st0, char* st1, char* st2, char* st3) {
+        static_assert(NS == 4, "stages");
+        for (int kt = 0; kt < KT; ++kt) {
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(PER_STAGE, 0));
+            __builtin_amdgcn_s_barrier();
+            fence();
+            const int to = (kt + 3) & 3;
+            issue(to == 0 ? st0 : to == 1 ? st1 : to == 2 ? st2 : st3);
+        }
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+        __syncthreads();
+    }
+
     // `KT` K steps (at least 1); on return no load is in flight and every wavefront
     // has read the stages.  256 rows: the caller has issued the first three stages and
     // seen them land.
@@ -920,8 +934,9 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
 }
 
 // The gradients' products run on one workgroup per CU.  Where the tiles of all
-// K steps fill the CUs well enough, each workgroup takes whole ones and they go
-// straight out.  Else the steps are shared out: a team of workgroups takes the
+// K steps fill the CUs well enough, each workgroup takes whole ones (of a last round
+// that is no more than half full, 128 of the rows each: dW of 1000 x 8000 x 1024 37 ->
+// 29 us, of 512 x 32768 x 768 45 -> 41) and they go straight out.  Else the steps are shared out: a team of workgroups takes the
 // column tiles of the same 256 rows side by side, so that they read the M operand
 // once through their XCD's L2, and writes its parts of tiles, which a second kernel
 // adds in order.  For dW each team first takes as many whole tiles as there are for
@@ -941,6 +956,8 @@ struct GradWork {
     int per;                  // of a team
     bool split;               // tiles are divided between teams, from tile `shared` on
     bool even;                // ... evenly, else range by range
+    bool halves;              // not split: those of the last round are, by rows
+    int gain;                 // steps that dividing saves
     int rounds, shared;       // whole tiles of a team before, of all teams
 };
 
@@ -961,8 +978,13 @@ __host__ __device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64
     // parts cost what their write and their sum take, about 32 steps (measured from 4 to
     // 40: 512 to 9000 rows, even between 20 and 40)
     const int even = (int)(((int64_t)rest * w.virt + w.teams - 1) / w.teams);
-    const int whole = (int)(((int64_t)w.m_tiles * w.n_tiles + kGradUnits - 1) / kGradUnits) * w.virt;
-    w.split = w.rounds * w.virt + even + 32 < whole;
+    // half a tile takes about three quarters of a whole one's time (fp32 dW of 1000 x
+    // 16001 x 512, 126 tiles: in halves 113 us, divided 107)
+    const int tiles = w.m_tiles * w.n_tiles, left = tiles % kGradUnits;
+    w.halves = a.halves && 0 < left && 2 * left <= kGradUnits;
+    const int whole = tiles / kGradUnits * w.virt + (w.halves ? (3 * w.virt + 3) / 4 : left ? w.virt : 0);
+    w.gain = whole - w.rounds * w.virt - even;
+    w.split = w.gain > 32;
     // ranges, unless they leave more than an eighth of the teams without work
     const int ranges = rest && rest <= w.teams ? w.teams / rest : 1;
     const int range = (w.virt + ranges - 1) / ranges;
@@ -975,6 +997,7 @@ __host__ __device__ __forceinline__ GradWork grad_work(const VocabGrad& a, int64
 // A workgroup's part of the work: steps k0 to k1 of a tile.
 struct GradPart {
     int mt, nt, k0, k1;
+    int half;                 // the 128 rows of the tile that are wanted; -1: all
     int round;                // those taken so far; below 0: none
     int at;                   // the first step of the next part (even)
 };
@@ -984,8 +1007,14 @@ __device__ __forceinline__ bool grad_next(const GradWork& w, int place, GradPart
     ++p.round;
     p.k0 = 0;
     p.k1 = w.virt;
+    p.half = -1;
     if (!w.split) {
-        const int tile = place + p.round * kGradUnits;
+        int tile = place + p.round * kGradUnits;
+        const int last = w.m_tiles * w.n_tiles / kGradUnits;
+        if (w.halves && p.round >= last) {
+            p.half = place & 1;
+            tile = p.round > last ? w.m_tiles * w.n_tiles : last * kGradUnits + (place >> 1);
+        }
         p.mt = tile / w.n_tiles;
         p.nt = tile - p.mt * w.n_tiles;
         return p.mt < w.m_tiles;
@@ -1063,7 +1092,8 @@ __device__ __forceinline__ void grad_out(const VocabGrad& a, int64_t m, int n0, 
 
 // DW: both operands are k rows of columns; else M is K-contiguous.  A part's first
 // three stages are loaded under the epilogue of the one before.
-template <bool DW>
+// HALVES: see GradWork; apart, since the large products lose 1% by it.
+template <bool DW, bool HALVES>
 __global__ __launch_bounds__(512, 1) void vocab_grad_kernel(const VocabGrad a) {
     using Eng = Engine<!DW, false, 256>;
     __shared__ __attribute__((aligned(1024))) char st0[Eng::SBYTES];
@@ -1110,10 +1140,19 @@ __global__ __launch_bounds__(512, 1) void vocab_grad_kernel(const VocabGrad a) {
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
     for (;;) {
         __builtin_amdgcn_s_barrier();
-        if (w.steps) e.run(now.k1 - now.k0, st0, st1, st2, st3);
+        const bool mine = !HALVES || now.half < 0 || now.half == e.rw;
+        if (w.steps) {
+            if (mine) e.run(now.k1 - now.k0, st0, st1, st2, st3);
+            else e.idle(now.k1 - now.k0, st0, st1, st2, st3);
+        }
         const GradPart was = now;
         const bool more = grad_next(w, place, now);
         if (more) start();
+        if (!mine) {
+            if (!more) return;
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+            continue;
+        }
 
         // Through LDS, 16 rows of the wavefront's 64 columns at a time (16-byte chunks
         // XOR-swizzled by the row), so that stores write whole lines.
@@ -1279,16 +1318,25 @@ hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s) {
         return hipErrorInvalidValue;
     const int64_t tiles = ((a.dW ? a.len : a.rows.T) + 255) / 256 * ((a.N + TN - 1) / TN);
     if (tiles > kMaxTiles / 4) return hipErrorInvalidValue;
-    if (a.dW) vocab_grad_kernel<true><<<kGradUnits, 512, 0, s>>>(a);
-    else vocab_grad_kernel<false><<<kGradUnits, 512, 0, s>>>(a);
+    VocabGrad b = a;
+    b.halves = a.dW || !a.rows.count;
+    GradWork w = grad_work(b, a.rows.T);
+    b.halves = w.halves && !w.split;
+    if (b.halves) {
+        if (a.dW) vocab_grad_kernel<true, true><<<kGradUnits, 512, 0, s>>>(b);
+        else vocab_grad_kernel<false, true><<<kGradUnits, 512, 0, s>>>(b);
+    } else {
+        if (a.dW) vocab_grad_kernel<true, false><<<kGradUnits, 512, 0, s>>>(b);
+        else vocab_grad_kernel<false, false><<<kGradUnits, 512, 0, s>>>(b);
+    }
     if (hipError_t e = hipGetLastError()) return e;
     // with the rows known here, or more of them than there can be (dW: fewer rows
-    // are fewer steps, which do not divide where more do not), tiles that are
-    // whole need no sum
-    const GradWork w = grad_work(a, a.rows.T);
-    if ((a.dW || !a.rows.count) && !w.split) return hipSuccess;
-    if (w.m_tiles * 8 <= w.teams) vocab_grad_sum_kernel<true><<<(unsigned)(tiles * 256), 256, 0, s>>>(a);
-    else vocab_grad_sum_kernel<false><<<(unsigned)(tiles * 8), 256, 0, s>>>(a);
+    // are fewer steps, which gain less by being divided, but for the rounding of two
+    // quotients), tiles that are whole need no sum
+    w = grad_work(b, a.rows.T);
+    if (!a.rows.count ? !w.split : a.dW && w.gain <= 30) return hipSuccess;
+    if (w.m_tiles * 8 <= w.teams) vocab_grad_sum_kernel<true><<<(unsigned)(tiles * 256), 256, 0, s>>>(b);
+    else vocab_grad_sum_kernel<false><<<(unsigned)(tiles * 8), 256, 0, s>>>(b);
     return hipGetLastError();
 }
 

@@ -103,6 +103,7 @@ struct VocabGrad {
     const int32_t* entry;     // negative: none
     const uint16_t* table;    // bf16, all of it
     int64_t table_pitch;
+    bool halves;              // of the launch: set by launch_vocab_grad
 };
 size_t vocab_grad_partial_bytes(int N);
 hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s);

@@ -18,7 +18,9 @@ SIZES = [(1, 64, 1), (1, 768, 1000), (3, 1, 5), (2, 8, 255), (127, 33, 256), (12
          # many rows on whole tiles, the last of one row, several tiles a workgroup
          (1025, 128, 2000), (3000, 256, 9000), (4353, 384, 300), (400, 256, 32769), (900, 128, 16400),
          # gradients: whole tiles and a rest shared out, steps shared out evenly (dW, dh)
-         (1400, 1100, 14000), (2600, 1001, 9400), (9400, 1000, 2600)]
+         (1400, 1100, 14000), (2600, 1001, 9400), (9400, 1000, 2600),
+         # and dW of a round of whole tiles and one of halves
+         (300, 600, 27000)]
 
 
 def inputs(T, D, V, dtype, masked, seed):
