@@ -933,20 +933,21 @@ __global__ __launch_bounds__(512, 1) void vocab_whole_kernel(const WholeArgs a, 
     }
 }
 
-// The gradients' products run on one workgroup per CU.  Where the tiles of all
-// K steps fill the CUs well enough, each workgroup takes whole ones (of a last round
-// that is no more than half full, 128 of the rows each: dW of 1000 x 8000 x 1024 37 ->
-// 29 us, of 512 x 32768 x 768 45 -> 41) and they go straight out.  Else the steps are shared out: a team of workgroups takes the
-// column tiles of the same 256 rows side by side, so that they read the M operand
-// once through their XCD's L2, and writes its parts of tiles, which a second kernel
-// adds in order.  For dW each team first takes as many whole tiles as there are for
-// all: the teams go through K together and read the same of h, which the L2s then
-// hold.  Of what remains, where its row tiles divide the teams well, each team has a
-// range of the steps of one, the teams of one range next to each other; else the
-// teams share out its steps evenly, each a contiguous range of them: at most one part
-// that it does not begin and one that it does not end, and whole tiles between.
-// Against the even shares alone, in teams for whole tiles too, of 768 columns: dh of
-// 512 rows and 32768 entries 47 -> 37 us, dW of 512 and 65536 100 -> 68.
+// The gradients' products run on one workgroup per CU.  Where the tiles of all K
+// steps fill the CUs well enough, each workgroup takes whole ones (of a last round
+// that is no more than half full, 128 of the rows each: dW of 1000 x 8000 x 1024 37
+// -> 29 us, of 512 x 32768 x 768 45 -> 41) and they go straight out.  Else the steps
+// are shared out: a team of workgroups takes the column tiles of the same 256 rows
+// side by side, so that they read the M operand once through their XCD's L2, and
+// writes its parts of tiles, which a second kernel adds in order.  For dW each team
+// first takes as many whole tiles as there are for all: the teams go through K
+// together and read the same of h, which the L2s then hold.  Of what remains, where
+// its row tiles divide the teams well, each team has a range of the steps of one, the
+// teams of one range next to each other; else the teams share out its steps evenly,
+// each a contiguous range of them: at most one part that it does not begin and one
+// that it does not end, and whole tiles between.  Against the even shares alone, in
+// teams for whole tiles too, of 768 columns: dh of 512 rows and 32768 entries 47 -> 37
+// us, dW of 512 and 65536 100 -> 68.
 constexpr int kGradUnits = 256;
 
 struct GradWork {
