@@ -334,20 +334,48 @@ __device__ __forceinline__ void write_cols(const SumArgs& a, int v, int c, Cols<
     }
 }
 
+// Zeros, past the caches too.
+template <typename O, int W>
+__device__ __forceinline__ void clear_cols(O* p) {
+    if constexpr (W % 4 == 0 && sizeof(O) * W % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(O) * W / 16); ++i) __builtin_nontemporal_store(u32x4_t{}, (u32x4_t*)p + i);
+    } else {
+        store_cols<O, W>(p, Cols<W>{});
+    }
+}
+
 template <typename E, typename O, int W>
 __global__ __launch_bounds__(256) void embedding_sum_kernel(const SumArgs a) {
     if (blockIdx.x < a.row_blocks) {
-        // W columns of an entry a thread; a workgroup's entries lie far apart,
-        // since text has its frequent ones next to each other
+        // W columns of an entry a thread.  The entries that a workgroup sums lie far
+        // apart, since text has its frequent ones next to each other; those that it
+        // clears follow one another, so that lines are written whole (rows of 632 fp32,
+        // 63069 of them: 41 -> 31 us).
         const int per_row = a.D / W;
         const float inv = 1.f / per_row;
+        // i / per_row: i is less than 2^15, so the product is off by less than 2^-8
+        // of one column group's share
+        auto row_of = [&](int i) { return (int)((i + 0.5f) * inv); };
+        if (!a.add) {
+            const int v0 = (int)blockIdx.x * a.rows;
+            for (int i0 = threadIdx.x; i0 < a.rows * per_row; i0 += 1024) {
+                bool none[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int v = v0 + row_of(i0 + 256 * j);
+                    none[j] = i0 + 256 * j < a.rows * per_row && v < a.V && a.count[min(v, a.V - 1)] == 0;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (none[j]) clear_cols<O, W>((O*)a.out + (int64_t)v0 * a.D + (int64_t)(i0 + 256 * j) * W);
+            }
+        }
         for (int i0 = threadIdx.x; i0 < a.rows * per_row; i0 += 1024) {
             int s[4], n[4], v[4], c[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                // i / per_row: i is less than 2^15, so the product is off by less than
-                // 2^-8 of one column group's share
-                const int i = i0 + 256 * j, r = (int)((i + 0.5f) * inv);
+                const int i = i0 + 256 * j, r = row_of(i);
                 c[j] = (i - r * per_row) * W;
                 v[j] = r < a.rows ? (int)blockIdx.x + r * (int)a.row_blocks : a.V;
                 const int at = min(v[j], a.V - 1);
@@ -356,7 +384,7 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const SumArgs a) {
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (v[j] >= a.V || n[j] > kLong || (a.add && n[j] == 0)) continue;
+                if (v[j] >= a.V || n[j] > kLong || n[j] == 0) continue;
                 write_cols<O, W>(a, v[j], c[j], sum_rows<E, W>(a, s[j], s[j] + n[j], c[j]));
             }
         }
@@ -380,16 +408,17 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const SumArgs a) {
             store_cols<float, W>(part + a.D + c, sum_rows<E, W>(a, bs, p1, c));
 }
 
-// Few tokens, in one launch: each workgroup looks through all ids for those of its
-// entries (far apart, as above), sorts them by entry and token in LDS and sums; an
-// entry of more than kLong tokens has its wavefronts side by side, a quarter of the
-// tokens each.  Most workgroups find none and write zeros.
+// Few tokens, in one launch: each workgroup looks through all ids for those of the
+// entries that it clears and of those that it sums (as above), sorts the latter by
+// entry and token in LDS and adds; an entry of more than kLong tokens has its
+// wavefronts side by side, a quarter of the tokens each.  Most workgroups find none.
 template <typename E, typename O, int W>
 __global__ __launch_bounds__(256) void embedding_few_kernel(const SumArgs a) {
     constexpr int J = kFewTokens / 256;
     __shared__ uint64_t hits[4 * J];
     __shared__ int list[kFewTokens], sorted[kFewTokens];       // entry << 10 | token
     __shared__ uint16_t begin[kFewEntries], count[kFewEntries];
+    __shared__ uint32_t taken[kFewEntries / 32];               // of the entries that it clears
     __shared__ Cols<W> sums[4][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const unsigned blocks = (unsigned)a.row_blocks;
@@ -401,12 +430,16 @@ __global__ __launch_bounds__(256) void embedding_few_kernel(const SumArgs a) {
         c = (i - r * per_row) * W;
         return r < a.rows ? min((int)blockIdx.x + r * (int)blocks, a.V) : a.V;
     };
+    const unsigned v0 = blockIdx.x * (unsigned)a.rows;
+    if (tid < kFewEntries / 32) taken[tid] = 0;
+    __syncthreads();
     int key[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int t = 256 * j + tid;
         const int id = t < a.T ? a.ids[t] : -1;
-        const unsigned r = (unsigned)id / blocks;
+        const unsigned r = (unsigned)id / blocks, own = (unsigned)id - v0;
+        if (id >= 0 && own < (unsigned)a.rows) atomicOr(taken + (own >> 5), 1u << (own & 31));
         key[j] = id >= 0 && id < a.V && (unsigned)id - r * blocks == blockIdx.x ? (int)(r << 10) | t : -1;
         const uint64_t m = __ballot(key[j] >= 0);
         if (lane == 0) hits[4 * j + wave] = m;
@@ -421,15 +454,15 @@ __global__ __launch_bounds__(256) void embedding_few_kernel(const SumArgs a) {
             if (w == wave && key[j] >= 0) list[n + __popcll(m & ((1ull << lane) - 1))] = key[j];
             n += __popcll(m);
         }
-    if (n == 0) {
-        if (a.add) return;
+    if (!a.add) {
+        O* out = (O*)a.out + (int64_t)v0 * a.D;
         for (int i = tid; i < a.rows * per_row; i += 256) {
             int r, c;
-            const int v = item(i, r, c);
-            if (v < a.V) write_cols<O, W>(a, v, c, Cols<W>{});
+            item(i, r, c);
+            if (v0 + r < (unsigned)a.V && !(taken[r >> 5] >> (r & 31) & 1)) clear_cols<O, W>(out + (int64_t)i * W);
         }
-        return;
     }
+    if (n == 0) return;
     for (int r = tid; r < a.rows; r += 256) count[r] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += 256) {
@@ -451,9 +484,9 @@ __global__ __launch_bounds__(256) void embedding_few_kernel(const SumArgs a) {
     for (int i = tid; i < a.rows * per_row; i += 256) {
         int r, c;
         const int v = item(i, r, c);
-        if (v >= a.V || count[r] > kLong || (a.add && count[r] == 0)) continue;
+        if (v >= a.V || count[r] > kLong || count[r] == 0) continue;
         const int p = begin[r];
-        write_cols<O, W>(a, v, c, count[r] ? sum_rows<E, W>(a, p, p + count[r], c, token) : Cols<W>{});
+        write_cols<O, W>(a, v, c, sum_rows<E, W>(a, p, p + count[r], c, token));
     }
     for (int p = 0; p < n;) {
         const int r = sorted[p] >> 10, m = count[r];
