@@ -2,8 +2,9 @@
 // (a decoding step's tokens, small chunks), where reading the table is all
 // the work:
 //
-//  logits:  z = h W^T for 128 entries and 32 or 64 rows a workgroup, and from it
-//           the tile's largest value and sum, or dz (as in vocab_gemm.hip)
+//  logits:  z = h W^T for 128 entries (of small tables 32, K divided over the
+//           wavefronts) and 32 or 64 rows a workgroup, and from it the tile's
+//           largest value and sum, or dz (as in vocab_gemm.hip)
 //  dh:      dz W for 256 columns and a part of the entries a workgroup, and the
 //           sum of the parts
 //  dW:      dz^T h, 64 entries x 256 columns a workgroup: a few steps of K, then
@@ -23,6 +24,7 @@
 #include "vocab_internal.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -268,6 +270,165 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
 #pragma unroll
             for (int w = 0; w < 4; ++w) sum += p[w].y * __builtin_amdgcn_exp2f(p[w].x - off);
             a.part[v0 / FN * a.part_pitch + row0 + tid] = make_float2(top, sum);
+        }
+    }
+}
+
+// The same for 32 entries a workgroup, its wavefronts each with a quarter of K: where
+// there are few tiles of 128 entries, a tile's steps are all of the time (four rows of
+// 2000 x 768 fp32 20 -> 9 us, 40 rows of 8000 x 1536 68 -> 25, bf16 16 -> 9).
+template <bool F32, int RB, bool DZ>
+__global__ __launch_bounds__(256, 2) void vocab_few_split_kernel(const VocabFew a, int m_tiles) {
+    using E = typename Elem<F32>::type;
+    constexpr int NS = RB == 1 ? 4 : 3, PER = 2 + 2 * RB, NB = 8192, SB = NB + RB * 8192;
+    __shared__ __attribute__((aligned(1024))) char st0[SB];
+    __shared__ __attribute__((aligned(1024))) char st1[SB];
+    __shared__ __attribute__((aligned(1024))) char st2[SB];
+    __shared__ __attribute__((aligned(1024))) char st3[NS == 4 ? SB : 16];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t row0 = (int64_t)(blockIdx.x % m_tiles) * (32 * RB), v0 = (int64_t)(blockIdx.x / m_tiles) * 32;
+    const int64_t bytes = a.D * (int64_t)sizeof(E);          // of a row, a multiple of 16
+    const int steps = (int)((bytes + 255) / 256);
+
+    // DMA instruction: 4 rows of 256 bytes; lane -> row lane / 16, physical chunk
+    // lane % 16 holding logical chunk (lane % 16) ^ (row % 16)
+    const char* n_src[2];
+    const char* m_src[2 * RB];
+    int n_c[2], m_c[2 * RB];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int r = 8 * wave + 4 * j + (lane >> 4);
+        n_c[j] = 16 * ((lane & 15) ^ (r & 15));
+        n_src[j] = (const char*)a.W + min(v0 + r, (int64_t)a.V - 1) * bytes + n_c[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 2 * RB; ++j) {
+        const int r = 8 * RB * wave + 4 * j + (lane >> 4);
+        m_c[j] = 16 * ((lane & 15) ^ (r & 15));
+        m_src[j] = (const char*)a.h + min(row0 + r, a.T - 1) * a.h_pitch * (int64_t)sizeof(E) + m_c[j];
+    }
+    auto issue = [&](int s, char* st) {
+        const int64_t k = (int64_t)min(s, steps - 1) * 256;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            load_lds16(k + n_c[j] < bytes ? n_src[j] + k : (const char*)few_zeros, st + (2 * wave + j) * 1024);
+#pragma unroll
+        for (int j = 0; j < 2 * RB; ++j)
+            load_lds16(k + m_c[j] < bytes ? m_src[j] + k : (const char*)few_zeros, st + NB + (2 * RB * wave + j) * 1024);
+    };
+    const int l = lane & 31, half = lane >> 5;
+    constexpr int CH = F32 ? 2 : 1;      // sums of a wavefront, as above
+    f32x16_t sum[CH][RB];
+#pragma unroll
+    for (int q = 0; q < CH; ++q)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) sum[q][rb] = f32x16_t{};
+    auto work = [&](const char* st) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = ((4 * wave + 2 * i + half) ^ (l & 15)) << 4;
+            const u32x4_t n = *(const u32x4_t*)(st + l * 256 + c);
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+                const u32x4_t m = *(const u32x4_t*)(st + NB + (32 * rb + l) * 256 + c);
+                if constexpr (F32) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        sum[q % CH][rb] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                            __uint_as_float(n[q]), __uint_as_float(m[q]), sum[q % CH][rb], 0, 0, 0);
+                } else {
+                    sum[0][rb] = multiply<false>(n, m, sum[0][rb]);
+                }
+            }
+        }
+    };
+    if constexpr (NS == 4) {
+        char* const st[4] = {st0, st1, st2, st3};
+        ring<4, PER>(steps, st, issue, work);
+    } else {
+        char* const st[3] = {st0, st1, st2};
+        ring<3, PER>(steps, st, issue, work);
+    }
+
+    // a block of rows a wavefront from here on
+    auto part = [&](int w) { return (float*)(w < 2 ? st0 : st1) + (w & 1) * RB * 1024; };
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            float x = sum[0][rb][v];
+            if constexpr (CH == 2) x += sum[1][rb][v];
+            part(wave)[(16 * rb + v) * 64 + lane] = x;
+        }
+    __syncthreads();
+    if (wave >= RB) return;
+    auto joined = [&](int v) {
+        using Z = typename std::conditional<F32, double, float>::type;
+        Z z = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) z += part(w)[(16 * wave + v) * 64 + lane];
+        return z;
+    };
+    // element v on lane l: row l % 32, entry v0 + 8 (v / 4) + 4 (l / 32) + v % 4
+    const int64_t c0 = v0 + 4 * half, row = row0 + 32 * wave + l;
+    const int left = (int)min((int64_t)a.V - c0, (int64_t)32);
+    const bool there = row < a.T;
+    const int64_t target = there && a.target ? a.target[row] : -1;
+    const int at = target >= c0 && target < c0 + 32 && target < a.V ? (int)(target - c0) : -1;
+    if constexpr (!DZ) {
+        float z[16], top = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            z[v] = (float)joined(v);
+            if (at == 8 * (v / 4) + v % 4) a.zt[row] = z[v];
+            if (8 * (v / 4) + v % 4 >= left) z[v] = -INFINITY;
+            top = fmaxf(top, z[v]);
+        }
+        top = fmaxf(top, __shfl_xor(top, 32)) * a.scale;
+        const float off = top == -INFINITY ? 0.f : top;
+        float s = 0.f;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s += __builtin_amdgcn_exp2f(fmaf(z[v], a.scale, -off));
+        s += __shfl_xor(s, 32);
+        if (half == 0 && there) a.part[v0 / 32 * a.part_pitch + row] = make_float2(top, s);
+    } else {
+        const float lse = there ? a.lse[row] : INFINITY, g = there ? a.g[row] : 0.f;
+        char* own = st2 + 4096 * wave;
+#pragma unroll
+        for (int vg = 0; vg < 4; ++vg) {
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float p;
+                if constexpr (F32) p = exp_fp32((float)fma(joined(4 * vg + i), (double)a.scale, -(double)lse));
+                else p = __builtin_amdgcn_exp2f(fmaf(joined(4 * vg + i), a.scale, -lse) * 1.4426950408889634f);
+                if (at == 8 * vg + i) p -= 1.f;
+                x[i] = 8 * vg + i >= left || lse == INFINITY ? 0.f : p * g;
+            }
+            *(float4*)(own + l * 128 + (((2 * vg + half) ^ (l & 7)) << 4)) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 3);
+            const int64_t m = row0 + 32 * wave + r;
+            if (m >= a.T) break;
+            float4 x = *(const float4*)(own + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            const int64_t to = m * a.dz_pitch + v0 + 4 * (lane & 7);
+            if constexpr (F32) {
+                *(float4*)(a.dz32 + to) = x;
+                if (!a.dz) continue;
+            }
+#pragma unroll
+            for (int pl = 0; pl < (F32 ? 3 : 2); ++pl) {
+                const uint32_t lo = pack_bf16(x.x, x.y), hi = pack_bf16(x.z, x.w);
+                *(uint2*)(a.dz + pl * a.dz_plane + to) = make_uint2(lo, hi);
+                x.x -= __uint_as_float(lo << 16);
+                x.y -= __uint_as_float(lo & 0xffff0000u);
+                x.z -= __uint_as_float(hi << 16);
+                x.w -= __uint_as_float(hi & 0xffff0000u);
+            }
         }
     }
 }
@@ -544,19 +705,29 @@ hipError_t launch_logits(const VocabFew& a, hipStream_t s) {
     const int rb = a.T <= 32 ? 1 : 2;
     // dz is written to the end of its rows: what reads it takes whole tiles, and
     // zeros times what the workspace held would be no zeros
-    const int64_t m_tiles = (a.T + 32 * rb - 1) / (32 * rb), grid = m_tiles * (DZ ? a.dz_pitch / FN : ((a.V + FN - 1) / FN));
+    const int cols = vocab_few_cols(a.T, a.V);
+    const int64_t m_tiles = (a.T + 32 * rb - 1) / (32 * rb), grid = m_tiles * (((DZ ? a.dz_pitch : (int64_t)a.V) + cols - 1) / cols);
     if (grid > 1 << 23) return hipErrorInvalidValue;
-    if (a.f32) {
-        if (rb == 1) vocab_few_logits_kernel<true, 1, DZ><<<(unsigned)grid, 256, 0, s>>>(a, (int)m_tiles);
-        else vocab_few_logits_kernel<true, 2, DZ><<<(unsigned)grid, 256, 0, s>>>(a, (int)m_tiles);
+    auto go = [&](auto* kernel) { kernel<<<(unsigned)grid, 256, 0, s>>>(a, (int)m_tiles); };
+    if (cols == FN) {
+        if (a.f32) go(rb == 1 ? vocab_few_logits_kernel<true, 1, DZ> : vocab_few_logits_kernel<true, 2, DZ>);
+        else go(rb == 1 ? vocab_few_logits_kernel<false, 1, DZ> : vocab_few_logits_kernel<false, 2, DZ>);
     } else {
-        if (rb == 1) vocab_few_logits_kernel<false, 1, DZ><<<(unsigned)grid, 256, 0, s>>>(a, (int)m_tiles);
-        else vocab_few_logits_kernel<false, 2, DZ><<<(unsigned)grid, 256, 0, s>>>(a, (int)m_tiles);
+        if (a.f32) go(rb == 1 ? vocab_few_split_kernel<true, 1, DZ> : vocab_few_split_kernel<true, 2, DZ>);
+        else go(rb == 1 ? vocab_few_split_kernel<false, 1, DZ> : vocab_few_split_kernel<false, 2, DZ>);
     }
     return hipGetLastError();
 }
 
 }  // namespace
+
+// With 125 tiles of 128 entries those of 32 take 15 us against 23 (4 rows of 16000 x 768
+// fp32), 22 against 38 (256 of 3900), 7 against 9 (bf16); with 235 26 against 25, bf16
+// 14 against 12.
+int vocab_few_cols(int64_t T, int V) {
+    const int rows = T <= 32 ? 32 : 64;
+    return ((int64_t)V + FN - 1) / FN * ((T + rows - 1) / rows) < 160 ? 32 : FN;
+}
 
 int vocab_few_splits(int64_t T, int D, int V, bool f32) {
     const int64_t m_tiles = (T + (T <= 32 ? 31 : 63)) / (T <= 32 ? 32 : 64), n_tiles = (D + 255) / 256;

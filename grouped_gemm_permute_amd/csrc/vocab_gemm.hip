@@ -68,14 +68,6 @@ __device__ __forceinline__ int fresh_lane() {
     return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, z));
 }
 
-// Orders a wavefront's LDS accesses for the compiler (the hardware keeps their
-// order), where lanes read what other lanes wrote.
-__device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // The K loop of one tile.  MC / NC: the M / N operand's rows are contiguous in
 // K; else its rows are k and the tile's 256 columns are contiguous.
 template <bool MC, bool NC, int ROWS>

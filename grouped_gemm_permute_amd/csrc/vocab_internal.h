@@ -17,6 +17,14 @@ __device__ __forceinline__ float exp_fp32(float d) {
     return t > -126.f ? fmaf(e, r * 0.6931471805599453f, e) : e;
 }
 
+// Orders a wavefront's LDS accesses for the compiler (the hardware keeps their
+// order), where lanes read what other lanes wrote.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // One operand of a product: bf16 rows, `planes` arrays of them `plane`
 // elements apart (an fp32 array is the sum of three such planes).
 struct VocabOperand {
@@ -111,7 +119,7 @@ hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s);
 // Few rows (vocab_few.hip): the products that read the table once, in its own
 // type.  Rows of 16 bytes' multiples; every row is a row of its own, those that
 // do not count have an infinite lse (dz) and are left to the caller (stats).
-constexpr int kVocabFewCols = 128;    // entries of a logits tile
+constexpr int kVocabFewCols = 128;    // entries of a logits tile, or, K divided over its wavefronts, 32
 struct VocabFew {
     bool f32;
     const void *h, *W;        // bf16, or fp32
@@ -129,6 +137,7 @@ struct VocabFew {
     int64_t dz_pitch, dz_plane;
     float* dh_part;           // [splits, T, D]
 };
+int vocab_few_cols(int64_t T, int V);          // entries of a logits tile
 int vocab_few_splits(int64_t T, int D, int V, bool f32);
 hipError_t launch_vocab_few_stats(const VocabFew& a, hipStream_t s);
 hipError_t launch_vocab_few_dz(const VocabFew& a, hipStream_t s);

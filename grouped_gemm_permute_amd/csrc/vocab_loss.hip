@@ -551,7 +551,7 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     p.Dp = (D + unit - 1) / unit * unit;
     p.whole = many && p.Dp % 128 == 0;
     p.n_tiles = ((int64_t)V + kVocabTileCols - 1) / kVocabTileCols;
-    if (p.few && !backward) p.n_tiles = ((int64_t)V + kVocabFewCols - 1) / kVocabFewCols;
+    if (p.few && !backward) p.n_tiles = ((int64_t)V + vocab_few_cols(T, V) - 1) / vocab_few_cols(T, V);
     size_t at = 0;
     auto take = [&](bool want, size_t bytes) {
         const size_t o = at;

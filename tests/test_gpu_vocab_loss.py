@@ -14,7 +14,7 @@ SIZES = [(1, 64, 1), (1, 768, 1000), (3, 1, 5), (2, 8, 255), (127, 33, 256), (12
          (700, 64, 5000), (1023, 40, 300), (1024, 64, 300), (1500, 96, 1025), (2500, 130, 70),
          # few rows: one and two blocks of 32, several tiles, columns past a tile, entries past a step
          (32, 136, 129), (33, 72, 1000), (64, 768, 3001), (65, 264, 40), (255, 516, 1100), (256, 40, 17), (257, 64, 500),
-         (3, 1024, 1500), (32, 2048, 700),
+         (3, 1024, 1500), (32, 2048, 700), (5, 72, 33000), (1, 1024, 32700), (40, 136, 33001), (65, 264, 16500), (200, 64, 9000),
          # many rows on whole tiles, the last of one row, several tiles a workgroup
          (1025, 128, 2000), (3000, 256, 9000), (4353, 384, 300), (400, 256, 32769), (900, 128, 16400),
          # gradients: whole tiles and a rest shared out, steps shared out evenly (dW, dh)
