@@ -24,7 +24,6 @@
 #include "vocab_internal.h"
 
 #include <algorithm>
-#include <type_traits>
 
 namespace moe {
 namespace {
@@ -85,6 +84,34 @@ __device__ __forceinline__ void ring(int steps, char* const (&st)[NS], I&& issue
     __syncthreads();
 }
 
+// dz of a lane's 16 entries from their logits z(v) in 64 bits, `at` of them (or none)
+// the target; those from `left` on are past the table.  fp32: at the target e^d - 1
+// by itself, without the rounding of an e^d near 1.
+template <bool F32, typename Z>
+__device__ __forceinline__ void few_dz(float (&x)[16], Z&& z, float scale, float lse, float g, int at, int left) {
+    float dt = 0.f;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+        const int e = 8 * (v / 4) + v % 4;
+        const float d = (float)fma(z(v), (double)scale, -(double)lse);
+        float p = F32 ? exp_fp32(d) : __builtin_amdgcn_exp2f(d * 1.4426950408889634f);
+        if (at == e) {
+            dt = d;
+            p -= 1.f;
+        }
+        // a row that does not count has an infinite lse: zeros, whatever h holds
+        x[v] = e >= left || lse == INFINITY ? 0.f : p * g;
+    }
+    if constexpr (F32) {
+        if (__ballot(at >= 0)) {
+            const float p = expm1f(dt) * g;
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                if (at == 8 * (v / 4) + v % 4 && lse != INFINITY) x[v] = p;
+        }
+    }
+}
+
 // RB: blocks of 32 rows.
 template <bool F32, int RB, bool DZ>
 __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew a, int m_tiles) {
@@ -135,10 +162,10 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
             load_lds16(k + m_c[j] < bytes ? m_src[j] + k : (const char*)few_zeros, st + N_BYTES + (RB * wave + j) * 1024);
     };
     const int l = lane & 31, half = lane >> 5;
-    // fp32: D / 2 terms follow one another in a sum, so there are several sums (one
-    // of them was off by twice what a library's product is), joined in 64 bits: a
-    // row's entry at its target is a small difference of large ones
-    constexpr int CH = !F32 ? 1 : RB == 1 ? 8 : 4;
+    // D / 2 (bf16: D / 16) terms follow one another in a sum, so there are several sums
+    // (one of them was off by twice what a library's product is), joined in 64 bits:
+    // a row's entry at its target is a small difference of large ones
+    constexpr int CH = F32 && RB == 1 ? 8 : 4;
     f32x16_t sum[CH][RB];
 #pragma unroll
     for (int q = 0; q < CH; ++q)
@@ -157,7 +184,7 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
                         sum[(4 * i + q) % CH][rb] = __builtin_amdgcn_mfma_f32_32x32x2f32(
                             __uint_as_float(n[q]), __uint_as_float(m[q]), sum[(4 * i + q) % CH][rb], 0, 0, 0);
                 } else {
-                    sum[0][rb] = multiply<false>(n, m, sum[0][rb]);
+                    sum[i][rb] = multiply<false>(n, m, sum[i][rb]);
                 }
             }
         }
@@ -177,7 +204,7 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
         for (int q = 0; q < CH; ++q) z += sum[q][rb][v];
         return z;
     };
-    if constexpr (F32 && !DZ) {
+    if constexpr (!DZ) {
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -218,20 +245,12 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
             // 16-byte chunks XOR-swizzled by the row.
             const float lse = there ? a.lse[row] : INFINITY, g = there ? a.g[row] : 0.f;
             if (rb) __syncthreads();
+            float x[16];
+            few_dz<F32>(x, [&](int v) { return joined(rb, v); }, a.scale, lse, g, at, left);
 #pragma unroll
-            for (int vg = 0; vg < 4; ++vg) {
-                float x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float p;
-                    if constexpr (F32) p = exp_fp32((float)fma(joined(rb, 4 * vg + i), (double)a.scale, -(double)lse));
-                    else p = __builtin_amdgcn_exp2f(fmaf(acc[rb][4 * vg + i], a.scale, -lse) * 1.4426950408889634f);
-                    if (at == 8 * vg + i) p -= 1.f;
-                    // a row that does not count has an infinite lse: zeros, whatever h holds
-                    x[i] = 8 * vg + i >= left || lse == INFINITY ? 0.f : p * g;
-                }
-                *(float4*)(st0 + l * 512 + (((8 * wave + 2 * vg + half) ^ l) << 4)) = make_float4(x[0], x[1], x[2], x[3]);
-            }
+            for (int vg = 0; vg < 4; ++vg)
+                *(float4*)(st0 + l * 512 + (((8 * wave + 2 * vg + half) ^ l) << 4)) =
+                    make_float4(x[4 * vg], x[4 * vg + 1], x[4 * vg + 2], x[4 * vg + 3]);
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -318,7 +337,7 @@ __global__ __launch_bounds__(256, 2) void vocab_few_split_kernel(const VocabFew 
             load_lds16(k + m_c[j] < bytes ? m_src[j] + k : (const char*)few_zeros, st + NB + (2 * RB * wave + j) * 1024);
     };
     const int l = lane & 31, half = lane >> 5;
-    constexpr int CH = F32 ? 2 : 1;      // sums of a wavefront, as above
+    constexpr int CH = 2;                // sums of a wavefront, as above
     f32x16_t sum[CH][RB];
 #pragma unroll
     for (int q = 0; q < CH; ++q)
@@ -338,7 +357,7 @@ __global__ __launch_bounds__(256, 2) void vocab_few_split_kernel(const VocabFew 
                         sum[q % CH][rb] = __builtin_amdgcn_mfma_f32_32x32x2f32(
                             __uint_as_float(n[q]), __uint_as_float(m[q]), sum[q % CH][rb], 0, 0, 0);
                 } else {
-                    sum[0][rb] = multiply<false>(n, m, sum[0][rb]);
+                    sum[i][rb] = multiply<false>(n, m, sum[i][rb]);
                 }
             }
         }
@@ -357,15 +376,12 @@ __global__ __launch_bounds__(256, 2) void vocab_few_split_kernel(const VocabFew 
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-            float x = sum[0][rb][v];
-            if constexpr (CH == 2) x += sum[1][rb][v];
-            part(wave)[(16 * rb + v) * 64 + lane] = x;
+            part(wave)[(16 * rb + v) * 64 + lane] = sum[0][rb][v] + sum[1][rb][v];
         }
     __syncthreads();
     if (wave >= RB) return;
     auto joined = [&](int v) {
-        using Z = typename std::conditional<F32, double, float>::type;
-        Z z = 0;
+        double z = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) z += part(w)[(16 * wave + v) * 64 + lane];
         return z;
@@ -395,19 +411,12 @@ __global__ __launch_bounds__(256, 2) void vocab_few_split_kernel(const VocabFew 
     } else {
         const float lse = there ? a.lse[row] : INFINITY, g = there ? a.g[row] : 0.f;
         char* own = st2 + 4096 * wave;
+        float x[16];
+        few_dz<F32>(x, joined, a.scale, lse, g, at, left);
 #pragma unroll
-        for (int vg = 0; vg < 4; ++vg) {
-            float x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float p;
-                if constexpr (F32) p = exp_fp32((float)fma(joined(4 * vg + i), (double)a.scale, -(double)lse));
-                else p = __builtin_amdgcn_exp2f(fmaf(joined(4 * vg + i), a.scale, -lse) * 1.4426950408889634f);
-                if (at == 8 * vg + i) p -= 1.f;
-                x[i] = 8 * vg + i >= left || lse == INFINITY ? 0.f : p * g;
-            }
-            *(float4*)(own + l * 128 + (((2 * vg + half) ^ (l & 7)) << 4)) = make_float4(x[0], x[1], x[2], x[3]);
-        }
+        for (int vg = 0; vg < 4; ++vg)
+            *(float4*)(own + l * 128 + (((2 * vg + half) ^ (l & 7)) << 4)) =
+                make_float4(x[4 * vg], x[4 * vg + 1], x[4 * vg + 2], x[4 * vg + 3]);
         wave_sync();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
