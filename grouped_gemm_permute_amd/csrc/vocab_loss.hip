@@ -70,6 +70,10 @@ bool few_dw(int64_t T, int D, int V, bool f32) {
 constexpr int64_t kDzBytes = 1ll << 31;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// Rows of one launch of a kernel with up to 256 threads a row: fewer than 2^32 threads
+// in a grid.
+constexpr int64_t kLaunchRows = 1 << 23;
+
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 size_t padded(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
@@ -96,9 +100,9 @@ __device__ __forceinline__ bool live_row(const Targets& a, int64_t t) {
     return false;
 }
 
-// live[t] of a distillation's rows: a wavefront a row.
-__global__ __launch_bounds__(256) void vocab_live_kernel(const Targets a, int64_t T, int32_t* __restrict__ live) {
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+// live[t] of a distillation's rows t0.. : a wavefront a row.
+__global__ __launch_bounds__(256) void vocab_live_kernel(const Targets a, int64_t t0, int64_t T, int32_t* __restrict__ live) {
+    const int64_t t = t0 + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     if (t >= T) return;
     bool any = false;
@@ -285,6 +289,7 @@ struct FinishArgs {
     float c;
     const float* zt;          // cross entropy: the targets' logits
     float *loss, *lse;        // [T]; loss null: lse alone
+    int64_t first;            // of the launch's (compact) rows
 };
 
 template <int LANES>
@@ -293,8 +298,8 @@ __global__ __launch_bounds__(256) void vocab_finish_kernel(const FinishArgs a) {
     __shared__ float2 sums[LANES][ROWS + 1];
     const int r = threadIdx.x % ROWS, sl = threadIdx.x / ROWS;
     const int64_t n = a.rows.count ? *a.rows.count : a.rows.T;
-    const int64_t i = (int64_t)blockIdx.x * ROWS + r;
-    if ((int64_t)blockIdx.x * ROWS >= n) return;
+    const int64_t i = a.first + (int64_t)blockIdx.x * ROWS + r;
+    if (i - r >= n) return;
     auto join = [](float2 x, float2 y) {
         const float m = fmaxf(x.x, y.x), off = m == -INFINITY ? 0.f : m;
         return make_float2(m, x.y * __builtin_amdgcn_exp2f(x.x - off) + y.y * __builtin_amdgcn_exp2f(y.x - off));
@@ -377,13 +382,14 @@ struct TopArgs {
     float inv_tau;
     const float* lse;
     float *loss, *z;
+    int64_t first;            // of the launch's rows
 };
 
 template <typename E, bool VEC>
 __global__ __launch_bounds__(256) void vocab_top_kernel(const TopArgs a) {
     __shared__ float q[kMaxTop], logq[kMaxTop], zs[kMaxTop];
     __shared__ int32_t id[kMaxTop];
-    const int64_t t = blockIdx.x;
+    const int64_t t = a.first + blockIdx.x;
     const int tid = threadIdx.x, K = a.targets.K;
     const E* h = (const E*)a.h + t * a.D;
     bool live = false;
@@ -446,12 +452,13 @@ struct TeacherArgs {
     float* dz32;              // the same in fp32, or null
     float* err;               // or null: what rounding takes from the largest of the
     int32_t* entry;           // row's entries, and which it is (see VocabGrad)
+    int64_t first;            // of the launch's (compact) rows
 };
 
 __global__ __launch_bounds__(64) void vocab_teacher_kernel(const TeacherArgs a) {
     __shared__ float q[kMaxTop], logq[kMaxTop];
     __shared__ int32_t id[kMaxTop];
-    const int64_t i = blockIdx.x;
+    const int64_t i = a.first + blockIdx.x;
     if (i >= (a.rows.count ? *a.rows.count : a.rows.T)) return;
     const int64_t t = a.rows.rows ? a.rows.rows[i] : i;
     const int K = a.targets.K, lane = threadIdx.x;
@@ -616,6 +623,16 @@ moe_status check(const Call& a) {
         if ((x) != hipSuccess) return MOE_ERR_HIP; \
     } while (0)
 
+// One launch after the other over T rows: launch(first row, rows).
+template <typename L>
+hipError_t by_rows(int64_t T, L&& launch) {
+    for (int64_t t = 0; t < T; t += kLaunchRows) {
+        launch(t, std::min(kLaunchRows, T - t));
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    return hipSuccess;
+}
+
 hipError_t copy_rows(const CopyArgs& a, moe_dtype dtype, hipStream_t s) {
     const unsigned grid = (unsigned)std::min<int64_t>((a.T + 32 + 3) / 4, 8192);
     if (dtype == MOE_BF16) vocab_copy_kernel<uint16_t><<<grid, 256, 0, s>>>(a);
@@ -630,8 +647,9 @@ moe_status begin(const Call& a, const Plan& p, char* ws, VocabRows* rows, VocabO
     if (p.list) {
         int32_t* live = (int32_t*)(ws + p.live);
         if (!a.targets.target) {
-            vocab_live_kernel<<<(unsigned)((a.T + 3) / 4), 256, 0, s>>>(a.targets, a.T, live);
-            TRY(hipGetLastError());
+            TRY(by_rows(a.T, [&](int64_t t, int64_t n) {
+                vocab_live_kernel<<<(unsigned)((n + 3) / 4), 256, 0, s>>>(a.targets, t, a.T, live);
+            }));
         }
         *rows = {(const int32_t*)(ws + p.rows), (const int32_t*)(ws + p.count), a.T};
         const unsigned chunks = (unsigned)((a.T + kListChunk - 1) / kListChunk);
@@ -676,21 +694,25 @@ moe_status forward(const Call& a, float* loss, float* lse, float* z, void* works
     } else
         TRY(p.whole ? launch_vocab_stats_whole(st, (const float4*)(ws + p.info), s) : launch_vocab_stats(st, s));
     FinishArgs f = {st.part, a.T, (int)p.n_tiles, rows, a.targets, st.c, st.zt, a.targets.target ? loss : nullptr, lse};
-    if (a.T <= 64 && f.n_tiles > 64) vocab_finish_kernel<256><<<(unsigned)a.T, 256, 0, s>>>(f);
-    else if (a.T <= 512 && f.n_tiles > 64) vocab_finish_kernel<64><<<(unsigned)((a.T + 3) / 4), 256, 0, s>>>(f);
-    else vocab_finish_kernel<16><<<(unsigned)((a.T + 15) / 16), 256, 0, s>>>(f);
-    TRY(hipGetLastError());
+    TRY(by_rows(a.T, [&](int64_t t, int64_t n) {
+        f.first = t;
+        if (a.T <= 64 && f.n_tiles > 64) vocab_finish_kernel<256><<<(unsigned)n, 256, 0, s>>>(f);
+        else if (a.T <= 512 && f.n_tiles > 64) vocab_finish_kernel<64><<<(unsigned)((n + 3) / 4), 256, 0, s>>>(f);
+        else vocab_finish_kernel<16><<<(unsigned)((n + 15) / 16), 256, 0, s>>>(f);
+    }));
     if (!a.targets.target) {
         TopArgs t = {a.h, a.W, a.targets, a.D, inv_tau, lse, loss, z};
-        const unsigned grid = (unsigned)a.T;
-        if (a.dtype == MOE_BF16) {
-            if (a.D % 8 == 0) vocab_top_kernel<uint16_t, true><<<grid, 256, 0, s>>>(t);
-            else vocab_top_kernel<uint16_t, false><<<grid, 256, 0, s>>>(t);
-        } else {
-            if (a.D % 4 == 0) vocab_top_kernel<float, true><<<grid, 256, 0, s>>>(t);
-            else vocab_top_kernel<float, false><<<grid, 256, 0, s>>>(t);
-        }
-        TRY(hipGetLastError());
+        TRY(by_rows(a.T, [&](int64_t first, int64_t n) {
+            t.first = first;
+            const unsigned grid = (unsigned)n;
+            if (a.dtype == MOE_BF16) {
+                if (a.D % 8 == 0) vocab_top_kernel<uint16_t, true><<<grid, 256, 0, s>>>(t);
+                else vocab_top_kernel<uint16_t, false><<<grid, 256, 0, s>>>(t);
+            } else {
+                if (a.D % 4 == 0) vocab_top_kernel<float, true><<<grid, 256, 0, s>>>(t);
+                else vocab_top_kernel<float, false><<<grid, 256, 0, s>>>(t);
+            }
+        }));
     }
     return MOE_OK;
 }
@@ -748,8 +770,10 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
         if (!a.targets.target) {
             TeacherArgs t = {a.targets, rows, z, g, l, inv_tau, v0, len, dz, p.pitch, dz_plane, planes ? p.dz_planes : 0, w.dz32,
                              d.err, (int32_t*)(ws + p.entry)};
-            vocab_teacher_kernel<<<(unsigned)a.T, 64, 0, s>>>(t);
-            TRY(hipGetLastError());
+            TRY(by_rows(a.T, [&](int64_t first, int64_t n) {
+                t.first = first;
+                vocab_teacher_kernel<<<(unsigned)n, 64, 0, s>>>(t);
+            }));
         }
         VocabGrad q = {};
         q.m = {dz, p.pitch, dz_plane};
