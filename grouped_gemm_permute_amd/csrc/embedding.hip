@@ -354,7 +354,7 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(const SumArgs a) {
         // 63069 of them: 41 -> 31 us).
         const int per_row = a.D / W;
         const float inv = 1.f / per_row;
-        // i / per_row: i is less than 2^15, so the product is off by less than 2^-8
+        // i / per_row: i is less than 2^16, so the product is off by less than 2^-7
         // of one column group's share
         auto row_of = [&](int i) { return (int)((i + 0.5f) * inv); };
         if (!a.add) {
@@ -576,11 +576,13 @@ template <typename E, typename O, int W>
 hipError_t launch_sums(SumArgs a, int64_t chunks, hipStream_t s) {
     // about eight column groups a thread (32768 entries x 768 in bf16: 14.8 us, with
     // four 16.3, with two 19.1)
-    a.rows = std::max(1, kFewEntries / (a.D / W));
+    // and fewer than 2^32 threads a grid
+    const int least = (a.V + (1 << 23) - 1) >> 23;
+    a.rows = std::max(least, kFewEntries / (a.D / W));
     a.row_blocks = ((int64_t)a.V + a.rows - 1) / a.rows;
     if (few_tokens(a.T)) {
         // and at least 1024 workgroups, where a few have most of the tokens
-        a.rows = std::max(1, std::min(a.rows, a.V >> 10));
+        a.rows = std::max(least, std::min(a.rows, a.V >> 10));
         a.row_blocks = ((int64_t)a.V + a.rows - 1) / a.rows;
         embedding_few_kernel<E, O, W><<<(unsigned)a.row_blocks, 256, 0, s>>>(a);
         return hipGetLastError();
