@@ -1309,8 +1309,8 @@ hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s) {
     if ((a.products != 1 && a.products != 6) || a.rows.T <= 0 || a.len <= 0 || a.N <= 0 || a.N > kGradUnits * TN ||
         a.n.pitch % BK || a.m.pitch % TN || a.n.pitch < a.N || !a.partial || ((a.add || !a.last) && !a.acc))
         return hipErrorInvalidValue;
-    const int64_t tiles = ((a.dW ? a.len : a.rows.T) + 255) / 256 * ((a.N + TN - 1) / TN);
-    if (tiles > kMaxTiles / 4) return hipErrorInvalidValue;
+    const int64_t tiles = vocab_grad_tiles(a.dW ? a.len : a.rows.T, a.N);
+    if (tiles > kVocabGradTiles) return hipErrorInvalidValue;
     VocabGrad b = a;
     b.halves = a.dW || !a.rows.count;
     GradWork w = grad_work(b, a.rows.T);

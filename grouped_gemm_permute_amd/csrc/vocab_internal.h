@@ -113,6 +113,10 @@ struct VocabGrad {
     int64_t table_pitch;
     bool halves;              // of the launch: set by launch_vocab_grad
 };
+// Tiles of 256 rows (entries of the piece) x 256 columns, at most: their sums are 8
+// workgroups of 256 threads each, fewer than 2^32 in a grid.
+constexpr int64_t kVocabGradTiles = 1 << 20;
+inline int64_t vocab_grad_tiles(int64_t M, int N) { return (M + 255) / 256 * ((N + 255) / 256); }
 size_t vocab_grad_partial_bytes(int N);
 hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s);
 

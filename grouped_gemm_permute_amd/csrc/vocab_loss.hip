@@ -577,7 +577,8 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
         p.zt = take(K == 0, (size_t)T * 4);
     } else {
         const int64_t tile = kVocabTileCols;
-        const int64_t most = std::max<int64_t>(1, kDzBytes / (T * p.planes * 2) / tile);   // tiles of a piece
+        // tiles of a piece
+        const int64_t most = std::min(std::max<int64_t>(1, kDzBytes / (T * p.planes * 2) / tile), kVocabGradTiles / ((D + 255) / 256));
         p.pieces = (p.n_tiles + most - 1) / most;
         p.piece = (p.n_tiles + p.pieces - 1) / p.pieces * tile;
         p.pieces = (p.n_tiles * tile + p.piece - 1) / p.piece;
@@ -731,6 +732,7 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
         return MOE_OK;
     }
     const Plan p = plan_of(a.T, a.D, V, a.targets.K, a.dtype, true);
+    if (dh && !p.few && vocab_grad_tiles(a.T, a.D) > kVocabGradTiles) return MOE_ERR_UNSUPPORTED;
     if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
     char* ws = (char*)workspace;
