@@ -111,37 +111,61 @@ __global__ __launch_bounds__(256) void vocab_live_kernel(const Targets a, int64_
     if (lane == 0) live[t] = m != 0;
 }
 
-// The rows that count, in order: rows[0 .. *count), and pos[t], a row's place
-// among them or -1.  A workgroup lists kListChunk rows and counts those before
-// them itself, so that none waits for another (32768 rows: 0.5 MB read by 8
-// workgroups).  zero0, zero1 (or null): set to 0 for the other rows.
+// Which of rows t .. t + 3 count, those that are there (less than T).
+__device__ __forceinline__ int four_rows(const int32_t* target, const int32_t* live, int V, int64_t t, int64_t T) {
+    const int32_t* p = (target ? target : live) + t;
+    int in = 0;
+    auto look = [&](int32_t x, int j) { in |= (target ? x >= 0 && x < V : x != 0) << j; };
+    if (t + 4 <= T) {
+        int32_t x[4];
+        __builtin_memcpy(x, p, 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) look(x[j], j);
+    } else {
+        for (int j = 0; t + j < T; ++j) look(p[j], j);
+    }
+    return in;
+}
+
+// How many rows of each chunk count.
 constexpr int kListChunk = 4096;
+__global__ __launch_bounds__(1024) void vocab_count_kernel(const int32_t* __restrict__ target, const int32_t* __restrict__ live,
+                                                           int V, int64_t T, int32_t* __restrict__ counts) {
+    __shared__ int32_t sums[16];
+    const int tid = threadIdx.x;
+    int n = __popc(four_rows(target, live, V, (int64_t)blockIdx.x * kListChunk + 4 * tid, T));
+    for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d);
+    if ((tid & 63) == 0) sums[tid >> 6] = n;
+    __syncthreads();
+    if (tid) return;
+    for (int w = 1; w < 16; ++w) n += sums[w];
+    counts[blockIdx.x] = n;
+}
+
+// The rows that count, in order: rows[0 .. *count), and pos[t], a row's place
+// among them or -1.  A workgroup lists kListChunk rows; of up to kListCounted it
+// counts those before them itself, in one launch (32768 rows: 0.5 MB read by 8
+// workgroups, 7.8 us against 6.0 and 2.6 for the counts), and of more it takes `counts`,
+// since that work grows with T^2 (65536 rows 11 us against 6.1 and 2.6, 131072 18 against
+// 5.9 and 4.1, 2^22 745 against 26 and 6).  zero0, zero1 (or null): set to 0 for the
+// other rows.
+constexpr int64_t kListCounted = 1 << 15;
 __global__ __launch_bounds__(1024) void vocab_list_kernel(const int32_t* __restrict__ target, const int32_t* __restrict__ live,
-                                                          int V, int64_t T, int32_t* __restrict__ rows,
-                                                          int32_t* __restrict__ pos, int32_t* __restrict__ count,
-                                                          float* zero0, float* zero1) {
+                                                          int V, int64_t T, const int32_t* __restrict__ counts,
+                                                          int32_t* __restrict__ rows, int32_t* __restrict__ pos,
+                                                          int32_t* __restrict__ count, float* zero0, float* zero1) {
     __shared__ int32_t sums[2][16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t base = (int64_t)blockIdx.x * kListChunk, t0 = base + 4 * tid;
-    auto four = [&](int64_t t) {       // which of rows t .. t + 3 (all there) count
-        int32_t x[4];
-        __builtin_memcpy(x, (target ? target : live) + t, 16);
-        int in = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) in |= (target ? x[j] >= 0 && x[j] < V : x[j] != 0) << j;
-        return in;
-    };
-    int before = 0, in = 0;
+    int before = 0;
+    if (counts) {
 #pragma unroll 4
-    for (int64_t t = 4 * tid; t < base; t += 4096) before += __popc(four(t));
-    if (t0 + 4 <= T) {
-        in = four(t0);
+        for (int c = tid; c < (int)blockIdx.x; c += 1024) before += counts[c];
     } else {
-        for (int j = 0; t0 + j < T; ++j) {
-            const int32_t x = (target ? target : live)[t0 + j];
-            in |= (target ? x >= 0 && x < V : x != 0) << j;
-        }
+#pragma unroll 4
+        for (int64_t t = 4 * tid; t < base; t += 4096) before += __popc(four_rows(target, live, V, t, base));
     }
+    const int in = four_rows(target, live, V, t0, T);
     const int mine = __popc(in);
     int incl = mine;
     for (int d = 1; d < 64; d <<= 1) {
@@ -526,7 +550,7 @@ struct Plan {
     int64_t n_tiles;          // stats: column tiles
     int64_t piece, pieces;    // entries of a piece (a multiple of 256), and how many
     int64_t pitch;            // elements between rows of its dz
-    size_t rows, pos, count, live, hc, info, Wc, part, zt, g, lse, err, entry, dz, dz32, dh_part, acc, total;
+    size_t rows, pos, count, counts, live, hc, info, Wc, part, zt, g, lse, err, entry, dz, dz32, dh_part, acc, total;
 };
 
 // Whether rows that are not listed take the tiles of 256 x 256 (one workgroup a CU)
@@ -568,6 +592,7 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     p.rows = take(p.list, (size_t)T * 4);
     p.pos = take(p.list, (size_t)T * 4);
     p.count = take(p.list, 4);
+    p.counts = take(p.list && T > kListCounted, (size_t)((T + kListChunk - 1) / kListChunk) * 4);
     p.live = take(p.list && K > 0, (size_t)T * 4);
     p.hc = take(p.copy_h, (size_t)p.planes * (T + 32) * p.Dp * 2);
     p.info = take(p.whole, (size_t)T * 16);
@@ -654,7 +679,12 @@ moe_status begin(const Call& a, const Plan& p, char* ws, VocabRows* rows, VocabO
         }
         *rows = {(const int32_t*)(ws + p.rows), (const int32_t*)(ws + p.count), a.T};
         const unsigned chunks = (unsigned)((a.T + kListChunk - 1) / kListChunk);
-        vocab_list_kernel<<<chunks, 1024, 0, s>>>(a.targets.target, live, a.targets.V, a.T, (int32_t*)(ws + p.rows),
+        int32_t* counts = a.T > kListCounted ? (int32_t*)(ws + p.counts) : nullptr;
+        if (counts) {
+            vocab_count_kernel<<<chunks, 1024, 0, s>>>(a.targets.target, live, a.targets.V, a.T, counts);
+            TRY(hipGetLastError());
+        }
+        vocab_list_kernel<<<chunks, 1024, 0, s>>>(a.targets.target, live, a.targets.V, a.T, counts, (int32_t*)(ws + p.rows),
                                             (int32_t*)(ws + p.pos), (int32_t*)(ws + p.count), zero0, zero1);
         TRY(hipGetLastError());
     }
