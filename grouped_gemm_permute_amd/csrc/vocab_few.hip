@@ -219,7 +219,7 @@ __global__ __launch_bounds__(256, 2) void vocab_few_logits_kernel(const VocabFew
     for (int rb = 0; rb < RB; ++rb) {
         const int64_t row = row0 + 32 * rb + l;
         const bool there = row < a.T;
-        const int64_t target = there && a.target ? a.target[row] : -1;
+        const int64_t target = there && a.target ? a.target[row] - a.v0 : -1;
         const int at = target >= c0 && target < c0 + 32 && target < a.V ? (int)(target - c0) : -1;
         if constexpr (!DZ) {
             if (__ballot(at >= 0)) {
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(256, 2) void vocab_few_split_kernel(const VocabFew 
     const int64_t c0 = v0 + 4 * half, row = row0 + 32 * wave + l;
     const int left = (int)min((int64_t)a.V - c0, (int64_t)32);
     const bool there = row < a.T;
-    const int64_t target = there && a.target ? a.target[row] : -1;
+    const int64_t target = there && a.target ? a.target[row] - a.v0 : -1;
     const int at = target >= c0 && target < c0 + 32 && target < a.V ? (int)(target - c0) : -1;
     if constexpr (!DZ) {
         float z[16], top = -INFINITY;
@@ -762,7 +762,7 @@ hipError_t launch_vocab_few_dw(const VocabFew& a, void* dW, bool out16, hipStrea
     return hipGetLastError();
 }
 
-hipError_t launch_vocab_few_dh(const VocabFew& a, void* dh, hipStream_t s) {
+hipError_t launch_vocab_few_dh(const VocabFew& a, hipStream_t s) {
     if (!fits(a) || a.dz_pitch % FN || a.dz_pitch < a.V) return hipErrorInvalidValue;
     const int rb = a.T <= 32 ? 1 : 2;
     const int m_tiles = (int)((a.T + 32 * rb - 1) / (32 * rb)), n_tiles = (a.D + 255) / 256;
@@ -775,9 +775,12 @@ hipError_t launch_vocab_few_dh(const VocabFew& a, void* dh, hipStream_t s) {
         if (rb == 1) vocab_few_dh_kernel<false, 1><<<grid, 256, 0, s>>>(a, n_tiles, m_tiles, splits);
         else vocab_few_dh_kernel<false, 2><<<grid, 256, 0, s>>>(a, n_tiles, m_tiles, splits);
     }
-    if (hipError_t e = hipGetLastError()) return e;
-    const int64_t n4 = a.T * a.D / 4;
-    vocab_few_sum_kernel<<<(unsigned)((n4 + 15) / 16), 256, 0, s>>>(a.dh_part, splits, n4, !a.f32, dh);
+    return hipGetLastError();
+}
+
+hipError_t launch_vocab_few_sum(const float* part, int parts, int64_t T, int D, bool bf16, void* dh, hipStream_t s) {
+    const int64_t n4 = T * D / 4;
+    vocab_few_sum_kernel<<<(unsigned)((n4 + 15) / 16), 256, 0, s>>>(part, parts, n4, bf16, dh);
     return hipGetLastError();
 }
 

@@ -126,10 +126,10 @@ hipError_t launch_vocab_grad(const VocabGrad& a, hipStream_t s);
 constexpr int kVocabFewCols = 128;    // entries of a logits tile, or, K divided over its wavefronts, 32
 struct VocabFew {
     bool f32;
-    const void *h, *W;        // bf16, or fp32
+    const void *h, *W;        // bf16, or fp32; W: of the piece's first entry
     int64_t h_pitch;          // elements
     int64_t T;
-    int D, V;
+    int D, V;                 // V: entries of the piece
     float scale;              // stats: log2(e) / tau; dz: 1 / tau
     const int32_t* target;    // [T] or null
     float2* part;             // stats
@@ -140,12 +140,15 @@ struct VocabFew {
     float* dz32;              // the same in fp32 (f32)
     int64_t dz_pitch, dz_plane;
     float* dh_part;           // [splits, T, D]
+    int64_t v0;               // dz: the piece's first entry
 };
 int vocab_few_cols(int64_t T, int V);          // entries of a logits tile
 int vocab_few_splits(int64_t T, int D, int V, bool f32);
 hipError_t launch_vocab_few_stats(const VocabFew& a, hipStream_t s);
 hipError_t launch_vocab_few_dz(const VocabFew& a, hipStream_t s);
-hipError_t launch_vocab_few_dh(const VocabFew& a, void* dh, hipStream_t s);
+hipError_t launch_vocab_few_dh(const VocabFew& a, hipStream_t s);     // vocab_few_splits() parts
+// dh = the sum of `parts` parts [T, D], in order.
+hipError_t launch_vocab_few_sum(const float* part, int parts, int64_t T, int D, bool bf16, void* dh, hipStream_t s);
 hipError_t launch_vocab_few_dw(const VocabFew& a, void* dW, bool out16, hipStream_t s);
 
 }  // namespace moe

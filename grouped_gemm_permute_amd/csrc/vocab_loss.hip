@@ -569,7 +569,7 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
     p.planes = dtype == MOE_BF16 ? 1 : 3;
     p.products = dtype == MOE_BF16 ? 1 : 6;
     const bool f32 = dtype != MOE_BF16;
-    p.few = few_rows(T, D, V, f32, backward) && T * V * p.planes * 2 <= kDzBytes;
+    p.few = few_rows(T, D, V, f32, backward);
     p.few_dw = p.few && few_dw(T, D, V, f32);
     // bf16 rows of whole K steps are read where they are
     p.copy_W = !p.few && (f32 || D % 32 != 0);
@@ -602,8 +602,10 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
         p.zt = take(K == 0, (size_t)T * 4);
     } else {
         const int64_t tile = kVocabTileCols;
+        // bytes of an entry of dz: its planes, or of few fp32 rows fp32 and what planes dW's tiles read
+        const int64_t each = !p.few || !f32 ? 2 * p.dz_planes : p.few_dw ? 4 : 4 + 2 * p.dz_planes;
         // tiles of a piece
-        const int64_t most = std::min(std::max<int64_t>(1, kDzBytes / (T * p.planes * 2) / tile), kVocabGradTiles / ((D + 255) / 256));
+        const int64_t most = std::min(std::max<int64_t>(1, kDzBytes / (T * each) / tile), kVocabGradTiles / ((D + 255) / 256));
         p.pieces = (p.n_tiles + most - 1) / most;
         p.piece = (p.n_tiles + p.pieces - 1) / p.pieces * tile;
         p.pieces = (p.n_tiles * tile + p.piece - 1) / p.piece;
@@ -611,15 +613,14 @@ Plan plan_of(int64_t T, int D, int V, int K, moe_dtype dtype, bool backward) {
         p.lse = take(true, (size_t)T * 4);
         p.err = take(p.give_back, (size_t)T * 4);
         p.entry = take(p.give_back, (size_t)T * 4);
-        if (p.few) p.piece = p.n_tiles * tile, p.pieces = 1;
         // an odd number of 512 bytes: rows 2^n bytes apart meet in a few of the memory's
         // channels (131072 bytes: dz 1318 us, 131584: 1150)
         p.pitch = (p.piece / 256 | 1) * 256;
         p.dz = take(!f32 || !p.few_dw, (size_t)p.dz_planes * T * p.pitch * 2);
         p.dz32 = take(p.few && f32, (size_t)T * p.pitch * 4);
-        p.dh_part = take(p.few, (size_t)(p.few ? vocab_few_splits(T, D, V, f32) : 0) * T * D * 4);
+        p.dh_part = take(p.few, (size_t)(p.few ? p.pieces * vocab_few_splits(T, D, p.pieces > 1 ? (int)p.piece : V, f32) : 0) * T * D * 4);
         p.part = take(!p.few_dw, vocab_grad_partial_bytes(D));
-        p.acc = take(p.pieces > 1, (size_t)T * p.Dp * 4);
+        p.acc = take(p.pieces > 1 && !p.few, (size_t)T * p.Dp * 4);
     }
     p.total = at;
     return p;
@@ -786,17 +787,20 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
     uint16_t* dz = (uint16_t*)(ws + p.dz);
     const int64_t dz_plane = a.T * p.pitch;
     const bool h16 = a.dtype == MOE_BF16;
+    int parts = 0;            // of few rows' dh
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
         const int len = (int)std::min<int64_t>(p.piece, V - v0);
         const VocabDz d = {h, W, rows, V, v0, len, p.Dp, p.products, inv_tau, g, l, a.targets.target, dz, p.pitch, dz_plane,
                            p.give_back ? (float*)(ws + p.err) : nullptr};
-        VocabFew w = {!h16, h16 ? (const void*)h.p : a.h, a.W, h16 ? h.pitch : a.D, a.T, a.D, V, inv_tau, a.targets.target};
+        VocabFew w = {!h16, h16 ? (const void*)h.p : a.h, (const char*)a.W + v0 * a.D * (h16 ? 2 : 4), h16 ? h.pitch : a.D,
+                      a.T, a.D, len, inv_tau, a.targets.target};
+        w.v0 = v0;
         w.g = g, w.lse = l;
         // of fp32 operands, planes only for a dW by tiles
         const bool planes = !p.few || h16 || (dW && !p.few_dw);
         w.dz = planes ? dz : nullptr, w.dz32 = p.few && !h16 ? (float*)(ws + p.dz32) : nullptr;
         w.dz_pitch = p.pitch, w.dz_plane = dz_plane;
-        w.dh_part = (float*)(ws + p.dh_part);
+        w.dh_part = (float*)(ws + p.dh_part) + (int64_t)parts * a.T * a.D;
         if (p.few) TRY(launch_vocab_few_dz(w, s));
         else TRY(p.whole ? launch_vocab_dz_whole(d, (const float4*)(ws + p.info), s) : launch_vocab_dz(d, s));
         if (!a.targets.target) {
@@ -815,7 +819,9 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
         q.products = p.products;
         q.partial = (float*)(ws + p.part);
         if (dh && p.few) {
-            TRY(launch_vocab_few_dh(w, dh, s));
+            TRY(launch_vocab_few_dh(w, s));
+            parts += vocab_few_splits(a.T, a.D, len, !h16);
+            if (v0 + p.piece >= V) TRY(launch_vocab_few_sum((const float*)(ws + p.dh_part), parts, a.T, a.D, h16, dh, s));
         } else if (dh) {
             q.dW = false;
             q.n = {W.p + v0 * W.pitch, W.pitch, W.plane};
@@ -831,7 +837,8 @@ moe_status backward(const Call& a, const float* z, const float* lse, const float
             TRY(launch_vocab_grad(q, s));
         }
         if (dW && p.few_dw) {
-            TRY(launch_vocab_few_dw(w, dW, dW_dtype == MOE_BF16, s));
+            const bool out16 = dW_dtype == MOE_BF16;
+            TRY(launch_vocab_few_dw(w, (char*)dW + v0 * a.D * (out16 ? 2 : 4), out16, s));
         } else if (dW) {
             q.dW = true;
             q.err = nullptr;

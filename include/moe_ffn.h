@@ -745,7 +745,7 @@ moe_status moe_cross_entropy_forward(const void *h, const void *W, const int32_t
  *   workspace >= moe_cross_entropy_workspace_size(.., 1) bytes, 256-byte aligned
  *
  * The logits are made again, a piece of the vocabulary at a time; dz of a piece
- * (at most 2 GiB, or 256 entries) stays in the workspace.  For bf16 operands dz is rounded to bf16 before the two
+ * stays in the workspace (2 GiB, or 256 entries, and up to 256 entries of padding a row).  For bf16 operands dz is rounded to bf16 before the two
  * products (with few rows to two bf16, 16 bits), also where dW is fp32.  Sizes and errors as in the forward;
  * dh has at most 2^20 tiles of 256 rows x 256 columns.
  */

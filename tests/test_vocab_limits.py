@@ -1,8 +1,9 @@
 """Cross entropy and distillation at the limits of their sizes, as far as the host decides (no GPU needed; no pointer here is
 dereferenced, and no call here has anything to launch)."""
 import pytest
+import torch
 
-from test_vocab_binding import DIST_BACK, LOSS_BACK, UNSUPPORTED, call
+from test_vocab_binding import DIST_BACK, LOSS_BACK, UNSUPPORTED, call, gg
 
 ROOM = dict(n=1 << 62)
 
@@ -12,3 +13,14 @@ ROOM = dict(n=1 << 62)
 def test_a_dh_of_too_many_tiles_is_refused_before_the_first_launch(name, defaults, over):
     assert call(name, defaults, dict(over, **ROOM)) == UNSUPPORTED
     assert call(name, defaults, dict(over, dW=None, **ROOM)) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,D,V", [(64, 8, 1 << 24), (64, 64, 1 << 23), (33, 8, 1 << 24), (128, 8, 1 << 24), (40000, 64, 1 << 20)])
+def test_dz_of_a_piece_is_two_gib_at_most(T, D, V, dtype):
+    """Beside it: its rows' padding, copies of h and (above 64 rows) of the table in planes, parts of dh."""
+    rows = T * 256 * (4 if dtype == torch.bfloat16 else 6)
+    copies = 6 * (T + 64) * (D + 128) + (6 * (V + 64) * (D + 128) if T > 64 else 0)
+    parts = 2 * 256 * 64 * D * 4 + 512 * 65536 * 4 + 64 * T + T * (D + 32) * 4
+    for need in (gg.cross_entropy_workspace_size(T, D, V, dtype, True), gg.distillation_workspace_size(T, D, V, 9, dtype, True)):
+        assert 1 << 29 < need <= (2 << 30) + rows + copies + parts
