@@ -637,7 +637,8 @@ struct Call {
 
 moe_status check(const Call& a) {
     if (a.T < 0 || a.D <= 0 || a.targets.V <= 0 || (a.dtype != MOE_F32 && a.dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
-    if (!(a.tau > 0.f) || a.tau > 3.4e38f || 1.f / a.tau > 3.4e38f) return MOE_ERR_INVALID_ARG;
+    // log2(e) / tau, the forward's factor, is finite
+    if (!(a.tau > 0.f) || a.tau > 3.4e38f || kLog2E / a.tau > 3.4e38f) return MOE_ERR_INVALID_ARG;
     if (a.D > kMaxD || a.targets.V > kMaxV || a.T > kMaxT || a.targets.K > kMaxTop) return MOE_ERR_UNSUPPORTED;
     // workgroups of a grid
     const int64_t t = (a.T + 127) / 128, v = (a.targets.V + 255) / 256, d = (a.D + 255) / 256;

@@ -3,7 +3,7 @@ dereferenced, and no call here has anything to launch)."""
 import pytest
 import torch
 
-from test_vocab_binding import DIST_BACK, LOSS_BACK, UNSUPPORTED, call, gg
+from test_vocab_binding import BAD, DIST, DIST_BACK, LOSS_BACK, OK, UNSUPPORTED, call, gg
 
 ROOM = dict(n=1 << 62)
 
@@ -24,3 +24,13 @@ def test_dz_of_a_piece_is_two_gib_at_most(T, D, V, dtype):
     parts = 2 * 256 * 64 * D * 4 + 512 * 65536 * 4 + 64 * T + T * (D + 32) * 4
     for need in (gg.cross_entropy_workspace_size(T, D, V, dtype, True), gg.distillation_workspace_size(T, D, V, 9, dtype, True)):
         assert 1 << 29 < need <= (2 << 30) + rows + copies + parts
+
+
+@pytest.mark.parametrize("name,defaults", [("moe_distillation_forward", DIST), ("moe_distillation_backward", DIST_BACK)])
+def test_temperatures_whose_log2_of_e_overflows_are_refused(name, defaults):
+    """1 / 4e-39 is an fp32 number, log2(e) / 4e-39 is none."""
+    none = dict(T=0, h=None, W=None, ids=None, q=None, lse=None, z=None, ws=None, **({"loss": None} if "loss" in defaults else {"g": None, "dh": None, "dW": None}))
+    for tau in (4e-39, 3e-39, 3.403e38):
+        assert call(name, defaults, dict(none, tau=tau)) == BAD
+    for tau in (4.4e-39, 1.0, 3.39e38):
+        assert call(name, defaults, dict(none, tau=tau)) == OK
