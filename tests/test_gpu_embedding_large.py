@@ -4,6 +4,7 @@ import torch
 
 import grouped_gemm_permute_amd as gg
 from gpu_util import say
+from test_gpu_embedding import tokens
 from vocab_util import HALF, U, within
 
 pytestmark = pytest.mark.gpu
@@ -29,3 +30,23 @@ def test_a_row_of_a_workgroups_own_for_each_of_the_most_entries(T):
     within(out[entries], want, far + HALF[torch.bfloat16] * (want.abs() + far), "dtable")
     rows = sum(int((out[v:v + (1 << 20)] != 0).any(1).sum()) for v in range(0, V, 1 << 20))
     assert rows == n, "entries without a token are zeros"
+
+
+# more entries than 256 for each of 256 sorting workgroups, than 1024 for each, for each of 512, of 1024
+@pytest.mark.parametrize("kind", ["even", "often", "one"])
+@pytest.mark.parametrize("T,V", [(1100, 65536), (1100, 65537), (40000, 100003), (5000, 262144), (5000, 262145), (30000, 600000), (3000, 1 << 24)])
+def test_gradient_of_large_tables(T, V, kind):
+    D = 24
+    say(f"embedding backward T{T} D{D} V{V} {kind}")
+    ids = tokens(T, V, T, kind)
+    dy = torch.randn(T, D, device="cuda").bfloat16()
+    got = gg.embedding_backward(ids, dy, V, scale=0.5, grad_dtype=torch.float32)
+    torch.cuda.synchronize()
+    inside = (ids >= 0) & (ids < V)
+    at, rows = ids.long().clamp(0, V - 1), dy.double() * inside[:, None]
+    sums = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, at, rows)
+    mags = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, at, rows.abs())
+    n = torch.bincount(at[inside], minlength=V)[:, None].double()
+    far = 0.5 * mags * (n + 2) * U
+    within(got, 0.5 * sums, far + HALF[torch.float32] * (0.5 * sums.abs() + far), "dtable")
+    assert torch.equal(got, gg.embedding_backward(ids, dy, V, scale=0.5, grad_dtype=torch.float32))

@@ -81,3 +81,12 @@ def check(T, D, V, dtype, grad, kind, each):
 @pytest.mark.parametrize("T,D,V", [(64, 8, 9_000_001), (40, 24, 1 << 24)])
 def test_few_rows_of_very_many_entries(T, D, V, dtype, grad, kind):
     check(T, D, V, dtype, grad, kind, 4)
+
+
+# tiles of 256 rows (listed; in three pieces), of 128 listed, of 128 not listed; of fp32 planes the same but for the second, whose rows are padded to whole tiles
+@pytest.mark.parametrize("kind", ["loss", "distill"])
+@pytest.mark.parametrize("T,D,V,dtype,grad", [(70000, 128, 20000, "bf16", "bf16"), (50000, 128, 50001, "bf16", "f32"), (60000, 96, 18433, "bf16", "bf16"),
+                                              (300, 36, 3_700_001, "bf16", "bf16"), (300, 33, 3_700_001, "bf16", "f32"),
+                                              (30000, 64, 20000, "f32", "f32"), (20000, 40, 40001, "f32", "f32"), (300, 33, 1_300_001, "f32", "f32")])
+def test_many_rows(T, D, V, dtype, grad, kind):
+    check(T, D, V, dtype, grad, kind, 2 if dtype == "bf16" else 6)
