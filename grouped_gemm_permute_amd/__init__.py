@@ -6,8 +6,8 @@ GEMMs over [W1|W3] with a fused silu(g)*u epilogue and over W2, and a
 deterministic unpermute/combine, and the layer's backward; and, around it,
 the layer norm with its backward and the Muon step on the weights'
 gradients; and a model's two ends: embedding lookup, and cross entropy and
-distillation over a vocabulary, each with its gradient.  This package is the Python binding: torch supplies device memory
-and streams, nothing else.
+distillation over a vocabulary, each with its gradient.  This package is the
+Python binding: torch supplies device memory and streams, nothing else.
 """
 from ._lib import (MoeError, alloc_workspace, backward, backward_workspace_layout,  # noqa: F401
                    cross_entropy, cross_entropy_backward, cross_entropy_workspace_size,

@@ -951,7 +951,9 @@ def cross_entropy_backward(h, W, targets, lse, dloss, wanted=("dh", "dW"), grad_
     (``grad_dtype``: h's dtype by default, or torch.float32) from the
     forward's lse and the losses' gradient dloss (fp32 [T]; 1/n of each for a
     mean over n).  ``wanted`` names the gradients to make (the other is
-    None); ``out`` may supply them."""
+    None); ``out`` may supply them.  Of bf16 operands the logits' gradient is
+    rounded to bf16 (few rows: 16 bits), also for an fp32 dW, whose sums and
+    whose own value are not."""
     f32 = torch.float32
     T, D, V, dt, dev = _check_head(h, W, dict(targets=(targets, torch.int32), lse=(lse, f32), dloss=(dloss, f32)))
     wanted = _wanted(wanted)

@@ -639,7 +639,7 @@ moe_status moe_embedding_forward(const int32_t* ids, const void* table, void* y,
     const bool vec = D * e % 16 == 0;
     // four 16-byte loads a thread
     a.rows = std::max(1, 1024 / (vec ? D * e / 16 : D));
-    // and fewer than 2^32 threads a grid (at most 64 rows of 16384 then)
+    // and fewer than 2^32 threads a grid (at most 8 rows then, T being 2^26 at most)
     a.rows = std::max(a.rows, (int)((T + (1 << 23) - 1) >> 23));
     const unsigned grid = (unsigned)((T + a.rows - 1) / a.rows);
     (void)hipGetLastError();

@@ -745,9 +745,13 @@ moe_status moe_cross_entropy_forward(const void *h, const void *W, const int32_t
  *   workspace >= moe_cross_entropy_workspace_size(.., 1) bytes, 256-byte aligned
  *
  * The logits are made again, a piece of the vocabulary at a time; dz of a piece
- * stays in the workspace (2 GiB, or 256 entries, and up to 256 entries of padding a row).  For bf16 operands dz is rounded to bf16 before the two
- * products (with few rows to two bf16, 16 bits), also where dW is fp32.  Sizes and errors as in the forward;
- * dh has at most 2^20 tiles of 256 rows x 256 columns.
+ * stays in the workspace (2 GiB, or 256 entries, and up to 256 entries of padding a row).
+ * For bf16 operands dz is rounded to bf16 before the two products (with few rows to two
+ * bf16, 16 bits), also where dW is fp32: such a dW has sums and a result that are not
+ * rounded (an embedding's gradient may be added to it), but terms that are off by up to
+ * 2^-8 each, 6e-4 to 1.6e-3 of dW in all (512 to 16384 rows).  What is rounded off a
+ * row's largest entry is given back in dh.
+ * Sizes and errors as in the forward; dh has at most 2^20 tiles of 256 rows x 256 columns.
  */
 moe_status moe_cross_entropy_backward(const void *h, const void *W, const int32_t *targets, const float *lse,
                                       const float *dloss, void *dh, void *dW, int64_t T, int D, int V,
