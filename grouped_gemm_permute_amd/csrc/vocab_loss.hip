@@ -52,12 +52,14 @@ constexpr int64_t kListRows = 1024, kListRowsF32 = 512;
 //                  320 x 16384 x 768 96/83, 192 x 40000 x 768 130/108, 512 x 8000 x 512 68/79, 512 x 20000 x 256 84/81
 //   bf16 forward   128 x 32768 x 768 23/26, 65 x 40000 x 768 31/26, 256 x 16000 x 512 18/18, 512 x 16000 x 256 22/15
 //   fp32 backward  100 x 65536 x 768 400/479, 150 x 65536 x 768 515/493, 300 x 16000 x 768 253/264, 384 x 20000 x 768 341/308
-//   fp32 forward   128 x 65536 x 768 126/220, 256 x 65536 x 768 236/233, 384 x 65536 x 768 345/380, 384 x 8000 x 512 45/76
+//   fp32 forward   128 x 65536 x 768 126/220, 256 x 65536 x 768 236/233, 384 x 65536 x 768 345/380, 384 x 8000 x 512 45/76,
+//                  40 x 10^7 x 64 1503/4108, 130 x 3 10^6 x 256 2980/3590, 256 x 2 10^6 x 256 2670/2480
 bool few_rows(int64_t T, int D, int V, bool f32, bool backward) {
     if (D % (f32 ? 4 : 8)) return false;
     if (T <= 64) return true;
     const int64_t work = (T + 63) / 64 * V * std::max(D, 512);
-    if (f32) return T <= 384 && (!backward || work <= (T <= 256 ? 1 << 27 : 1 << 26));
+    if (f32 && backward) return T <= 384 && work <= (T <= 256 ? 1 << 27 : 1 << 26);
+    if (f32) return T <= 192 || (T <= 384 && T * V <= (1ll << 31) / 6);
     if (T > 512) return false;
     return work <= (backward ? 7 << 23 : T <= 192 ? 3 << 24 : 1 << 25);
 }

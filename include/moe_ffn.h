@@ -722,8 +722,9 @@ size_t moe_cross_entropy_workspace_size(int64_t T, int D, int V, moe_dtype dtype
  * fixed order: repeated calls give equal bits.  A row of h that holds an infinity
  * or NaN touches its own outputs alone.
  *
- * Any D up to 16384, V up to 2^24, T up to 2^28, and fewer than 2^22 tiles of
- * 128 rows x 256 entries.  h and W are 16-byte aligned, the others 4-byte.
+ * Any D up to 16384, V up to 2^24, T up to 2^28, and at most 2^22 tiles of 128
+ * rows x 256 entries, 128 rows x 256 columns and 256 entries x 256 columns.  h and W
+ * are 16-byte aligned, the others 4-byte.
  * Returns MOE_OK; MOE_ERR_INVALID_ARG (null or misaligned pointer, T < 0, D or
  * V < 1, unknown dtype); MOE_ERR_UNSUPPORTED; MOE_ERR_WORKSPACE; MOE_ERR_HIP.
  * T == 0 launches nothing.
